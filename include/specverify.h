@@ -60,7 +60,7 @@ extern "C" {
 /* A cudaStream_t, declared without the CUDA headers. */
 typedef struct CUstream_st* sv_stream_t;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 /* paged cache entry points only */ } sv_dtype;
 typedef enum { SV_GREEDY = 0, SV_SAMPLE = 1 } sv_mode;
 
 typedef enum {
@@ -92,11 +92,13 @@ typedef enum {
     SV_FLAG_BAD_LENGTH = 64u,      /* a per-sequence draft length outside [0, K]   */
     SV_FLAG_BAD_TREE = 128u,       /* a tree node whose parent is not an earlier
                                       node                                         */
-    SV_FLAG_DEBUG_BOUNDS = 256u    /* debug builds only (libspecverify_debug.so,
+    SV_FLAG_DEBUG_BOUNDS = 256u,   /* debug builds only (libspecverify_debug.so,
                                       compiled with SPECVERIFY_DEBUG): the verify
                                       kernel was about to access global memory
                                       outside every buffer of the call; it skipped
                                       that access instead                          */
+    SV_FLAG_BAD_PAGE = 512u        /* a page table entry outside [0, n_pages) where
+                                      a token's page was needed                    */
 } sv_device_flag;
 
 /* Batched verify over logits already in device memory.
@@ -366,6 +368,165 @@ sv_status spec_verify_lmhead_noalloc(const void* hidden, const void* W,
  *   multiple of 64, V a positive multiple of 8; hidden and W 16-byte aligned. */
 sv_status spec_lmhead_logits(const void* hidden, const void* W, int M, int d, int V, float* out,
                              sv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged key/value cache of the target's forward pass.
+ *
+ * The verification rows come from one forward pass over each sequence's new
+ * tokens: the last committed token and its drafts, or a tree of candidates
+ * ("Inference-4", sections "Draft-model speculative decoding" and "Medusa"),
+ * or, before the first step, the prompt. These entry points do what that pass
+ * does with the cache: spec_kv_append writes the new tokens' keys and values
+ * with the rotary rotation applied, spec_paged_attention attends from the new
+ * tokens, and spec_kv_commit keeps what the verify step accepted.
+ *
+ * A chunk of a batch: sequence b has ctx_lens[b] tokens in the cache and
+ * cu_new[b+1] - cu_new[b] new ones (0 allowed), which are rows
+ * cu_new[b].. of the packed per-token arrays and cache slots ctx_lens[b]... .
+ * Slot j of sequence b is entry j % page_size of page page_table[b][j /
+ * page_size]. Rows of the packed arrays that no sequence claims are ignored.
+ *
+ * Strides are in elements. Rows of D elements are contiguous; every row
+ * starts on a multiple of 16 bytes (strides multiples of 8, 16-byte bases).
+ *
+ * Device-detected errors are flagged in the status word and never trap:
+ *   SV_FLAG_BAD_LENGTH  cu_new not ascending within [0, T], a negative
+ *     context, more tokens than the page table has room for, or more new
+ *     tokens than tree nodes: the sequence is left out (nothing appended;
+ *     its attention rows, if cu_new places them, are 0 with lse -inf; nothing
+ *     committed).
+ *   SV_FLAG_BAD_PAGE    a page outside [0, n_pages): the token is not stored
+ *     or moved; attention reads zeros there.
+ *   SV_FLAG_BAD_TREE    a node with a parent outside [0, node) in its chain:
+ *     it sees nothing (row 0, lse -inf) and takes the position ctx.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void* k;                     /* [n_pages, page_size, Hkv, D] dtype (device)   */
+    void* v;                     /* the same shape, strides of its own            */
+    sv_dtype dtype;              /* SV_BF16 or SV_F16                             */
+    int n_pages;                 /* >= 1                                          */
+    int page_size;               /* a multiple of 8, 8..65536                     */
+    int Hkv;                     /* kv heads, >= 1                                */
+    int D;                       /* head size: 64 or 128                          */
+    int B;                       /* sequences, >= 1                               */
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    const int32_t* page_table;   /* [B, max_pages] int32 (device); entries past a
+                                    sequence's last token are not read            */
+    int64_t page_table_stride;   /* between sequences, >= max_pages               */
+    int max_pages;               /* >= 1                                          */
+    const int32_t* ctx_lens;     /* [B] int32 (device): tokens in the cache before
+                                    the chunk                                     */
+} sv_kv_cache;
+
+/* Arguments of spec_kv_append. Zero-initialise, then fill what is used. */
+typedef struct {
+    sv_kv_cache cache;
+    const int32_t* cu_new;       /* [B+1] int32 (device): the chunk's packed rows */
+    int T;                       /* packed rows, >= 0                             */
+    const void* k;               /* [T, Hkv, D] (device)                          */
+    const void* v;               /* [T, Hkv, D] (device)                          */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int Hq;                      /* query heads, when q is given                  */
+    const void* q;               /* [T, Hq, D] (device), or NULL                  */
+    void* q_out;                 /* [T, Hq, D] (device): q rotated; may be q      */
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    const double* inv_freq;      /* HOST [rotary / 2]: angle per position of each
+                                    pair, in radians; NULL when rotary is 0. Read
+                                    before the call returns                       */
+    int rotary;                  /* elements that rotate: 0, or a multiple of 16
+                                    up to D                                       */
+    int interleaved;             /* 0: pairs (i, i + rotary/2); 1: (2i, 2i+1)     */
+    const int32_t* tree_parents; /* [B, N] int32 (device) or NULL: the chunk is a
+                                    tree as in spec_verify_tree, and a node's
+                                    position is ctx + its depth                   */
+    int N;                       /* 1..32 with tree_parents                       */
+    const int32_t* positions;    /* [T] int32 (device) or NULL: rotary positions
+                                    in place of the slot or depth                 */
+    uint32_t* status_word;       /* device uint32 or NULL                         */
+    sv_stream_t stream;
+} sv_kv_append_args;
+
+/* Appends the chunk: k and q rotated by their positions (a cos - b sin, b cos
+ * + a sin, in fp32, rounded once), v as it is. The angle is exact to 2^-24
+ * turns at any int32 position. Slots are not checked for sharing: sequences
+ * of the batch must not write the same entry. T == 0 enqueues nothing. */
+sv_status spec_kv_append(const sv_kv_append_args* args);
+
+/* CTAs (and so pieces of work) of one attention call at most. */
+#define SV_PAGED_MAX_CTAS 160
+
+/* Arguments of spec_paged_attention. Zero-initialise, then fill what is used. */
+typedef struct {
+    sv_kv_cache cache;
+    const int32_t* cu_new;       /* [B+1] int32 (device)                          */
+    int T;                       /* packed rows, >= 0                             */
+    int Hq;                      /* query heads: a multiple of Hkv, at most
+                                    128 * Hkv                                     */
+    const void* q;               /* [T, Hq, D] (device), the cache's dtype        */
+    void* out;                   /* [T, Hq, D] (device), the cache's dtype        */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    float* out_lse;              /* [T, Hq] float (device) or NULL: natural log of
+                                    the row's sum of exponentials                 */
+    float scale;                 /* of the scores: finite, > 0                    */
+    const int32_t* tree_parents; /* [B, N] int32 (device) or NULL: a token sees
+                                    the context and its ancestors, not the
+                                    chunk's earlier tokens                        */
+    int N;                       /* 1..32 with tree_parents                       */
+    void* workspace;             /* device, 256-byte aligned                      */
+    size_t workspace_bytes;
+    uint32_t* status_word;       /* device uint32 or NULL                         */
+    uint32_t flags;              /* SV_ARG_TEST_WAIT_TIMEOUT or 0                 */
+    sv_stream_t stream;
+} sv_paged_attention_args;
+
+/* Bytes of workspace of a call with T packed rows: SV_PAGED_WORKSPACE_HEAD
+ * bytes of counters, then room for the pieces of cut work. 0 for sizes the
+ * call would refuse. */
+size_t spec_paged_attention_workspace_bytes(int T, int Hq, int Hkv, int D);
+
+/* The workspace's counters, at its start: zero before its first use. A call
+ * leaves them zero (after SV_FLAG_TIMEOUT, zero them again). Nothing else in
+ * the workspace needs to start at any value. Calls that may overlap need
+ * workspaces of their own. */
+#define SV_PAGED_WORKSPACE_HEAD 1024
+
+/* Attention of the chunk's tokens, whose keys and values are in the cache
+ * already: out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h / G]) v[j, h /
+ * G], G = Hq / Hkv, over the slots j <= t's own (chain), or the context, t's
+ * ancestors and t itself (tree). Scores, the softmax's maximum and sum and the
+ * output accumulate in fp32; the weights are rounded to the cache's dtype
+ * before they meet v, and the output is rounded once. Entries past a
+ * sequence's last token may hold anything. A key or value that is not finite
+ * at a slot that some token of the chunk sees may reach other tokens of the
+ * chunk (weight 0 times infinity). Results do not depend on timing. T == 0
+ * enqueues nothing. */
+sv_status spec_paged_attention(const sv_paged_attention_args* args);
+
+/* Keeps what a verify step accepted. With a chain (tree_parents NULL) the
+ * entries lie where they belong and only lengths change: out_lens[b] =
+ * ctx_lens[b] + 1 + n_accepted[b]. With a tree the entries of the kept path
+ * (the root, then the n_accepted[b] nodes down to last_node[b], as
+ * spec_verify_tree reports them) move to slots ctx_lens[b] + 0 .. n; those
+ * were appended at ctx_lens[b] + node with the rotation of their depth, so
+ * they move unchanged. A negative n_accepted (an invalid verify result)
+ * commits nothing: out_lens[b] = ctx_lens[b].
+ *   n_accepted [B] int32 (device); tree_parents [B, N] int32 (device) or NULL,
+ *   1 <= N <= 32; last_node [B] int32 (device), with a tree;
+ *   out_lens [B] int32 (device); may be ctx_lens;
+ *   status_word: device uint32 or NULL. An n_accepted that does not fit the
+ *   tree or the page table (SV_FLAG_BAD_LENGTH) or a last_node whose chain is
+ *   not n_accepted long (SV_FLAG_BAD_TREE) commits nothing. */
+sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* n_accepted,
+                         const int32_t* tree_parents, int N,
+                         const int32_t* last_node, int32_t* out_lens,
+                         uint32_t* status_word, sv_stream_t stream);
+
+/* sizeof(sv_kv_cache), sizeof(sv_kv_append_args) and
+ * sizeof(sv_paged_attention_args) as compiled into the library. */
+size_t sv_kv_cache_size(void);
+size_t sv_kv_append_args_size(void);
+size_t sv_paged_attention_args_size(void);
 
 /* Static description of a status code (never NULL). */
 const char* sv_status_string(sv_status status);

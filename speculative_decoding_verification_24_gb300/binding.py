@@ -18,7 +18,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspecverify.so")
 DEBUG_LIB_PATH = os.path.join(_PKG, "libspecverify_debug.so")
 
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_GREEDY, SV_SAMPLE = 0, 1
 
 SV_FLAG_BAD_TOKEN = 1
@@ -30,11 +30,13 @@ SV_FLAG_TIMEOUT = 32
 SV_FLAG_BAD_LENGTH = 64
 SV_FLAG_BAD_TREE = 128
 SV_FLAG_DEBUG_BOUNDS = 256
+SV_FLAG_BAD_PAGE = 512
 SV_ARG_OVERLAP_PREVIOUS = 1
 SV_ARG_TEST_WAIT_TIMEOUT = 0x80000000
 SV_ARG_TEST_DEBUG_SHRINK = 0x40000000
 SV_ERR_SCRATCH_LIMIT = 12
 SV_LMHEAD_SCRATCH_BYTES = 32 << 20  # include/specverify.h
+SV_PAGED_WORKSPACE_HEAD = 1024  # include/specverify.h
 
 STATUS_NAMES = {
     0: "SV_OK", 1: "SV_ERR_NULL", 2: "SV_ERR_SHAPE", 3: "SV_ERR_DTYPE", 4: "SV_ERR_TEMPERATURE",
@@ -92,6 +94,85 @@ class sv_verify_plan(ctypes.Structure):
     ]
 
 
+class sv_kv_cache(ctypes.Structure):
+    """Mirror of sv_kv_cache in include/specverify.h."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("dtype", ctypes.c_int),
+        ("n_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("Hkv", ctypes.c_int),
+        ("D", ctypes.c_int),
+        ("B", ctypes.c_int),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p),
+        ("page_table_stride", ctypes.c_int64),
+        ("max_pages", ctypes.c_int),
+        ("ctx_lens", ctypes.c_void_p),
+    ]
+
+
+class sv_kv_append_args(ctypes.Structure):
+    """Mirror of sv_kv_append_args in include/specverify.h."""
+    _fields_ = [
+        ("cache", sv_kv_cache),
+        ("cu_new", ctypes.c_void_p),
+        ("T", ctypes.c_int),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("Hq", ctypes.c_int),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("q_out_token_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("inv_freq", ctypes.c_void_p),
+        ("rotary", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("tree_parents", ctypes.c_void_p),
+        ("N", ctypes.c_int),
+        ("positions", ctypes.c_void_p),
+        ("status_word", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class sv_paged_attention_args(ctypes.Structure):
+    """Mirror of sv_paged_attention_args in include/specverify.h."""
+    _fields_ = [
+        ("cache", sv_kv_cache),
+        ("cu_new", ctypes.c_void_p),
+        ("T", ctypes.c_int),
+        ("Hq", ctypes.c_int),
+        ("q", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("out_lse", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("tree_parents", ctypes.c_void_p),
+        ("N", ctypes.c_int),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("status_word", ctypes.c_void_p),
+        ("flags", ctypes.c_uint32),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -111,6 +192,13 @@ SIGNATURES = [
     ("spec_commit", I, [P, P, I, I, P, P, I, P, P]),
     ("spec_verify_lmhead_noalloc", I, [P, P, P, P, I, I, I, I, I, ctypes.c_float, I,
                                        ctypes.c_uint64, P, P, P]),
+    ("spec_kv_append", I, [ctypes.POINTER(sv_kv_append_args)]),
+    ("spec_paged_attention_workspace_bytes", ctypes.c_size_t, [I, I, I, I]),
+    ("spec_paged_attention", I, [ctypes.POINTER(sv_paged_attention_args)]),
+    ("spec_kv_commit", I, [ctypes.POINTER(sv_kv_cache), P, P, I, P, P, P, P]),
+    ("sv_kv_cache_size", ctypes.c_size_t, []),
+    ("sv_kv_append_args_size", ctypes.c_size_t, []),
+    ("sv_paged_attention_args_size", ctypes.c_size_t, []),
     ("sv_status_string", ctypes.c_char_p, [I]),
     ("sv_last_cuda_error", I, []),
     ("sv_version", I, []),
@@ -133,6 +221,9 @@ def load_library(path: str):
         fn.argtypes = args
     if lib.sv_verify_args_size() != ctypes.sizeof(sv_verify_args):
         raise ImportError("sv_verify_args layout differs between the binding and the library")
+    for struct in (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args):
+        if getattr(lib, struct.__name__ + "_size")() != ctypes.sizeof(struct):
+            raise ImportError(f"{struct.__name__} layout differs between the binding and the library")
     return lib
 
 
@@ -423,3 +514,218 @@ def spec_verify_lmhead_noalloc(hidden, W, draft_logits, draft_tokens, temperatur
             _ptr(out_tokens), _ptr(out_n_accepted), _stream(stream, dev))
     _check(st, "spec_verify_lmhead_noalloc")
     return out_tokens, out_n_accepted
+
+
+# ------------------------------------------------------ the paged cache
+
+
+_KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+
+
+def _rows(t, name, heads=None, width=None, like=None):
+    """A [rows, heads, width] tensor of any token and head strides: its data
+    pointer and those strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != width:
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {width}], got {list(t.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype} like the cache, got {t.dtype}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr(), st, sh
+
+
+def _int32(t, name, shape):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _fill_cache(c, k_cache, v_cache, page_table, ctx_lens):
+    """Fills the sv_kv_cache c from k_cache and v_cache [n_pages, page_size,
+    Hkv, D] (any strides but the last), page_table [B, max_pages] and ctx_lens
+    [B]."""
+    if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
+        raise ValueError("every tensor must live on a CUDA device")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be [n_pages, page_size, Hkv, D] and alike")
+    dtype = _KV_DTYPES.get(k_cache.dtype)
+    if dtype is None or v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"the cache must be bfloat16 or float16, got {k_cache.dtype} and {v_cache.dtype}")
+    kp, kt, kh, kd = k_cache.stride()
+    vp, vt, vh, vd = v_cache.stride()
+    if kd != 1 or vd != 1:
+        raise ValueError("the cache must be contiguous in its last dimension")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be int32 [B, max_pages], contiguous in its last dimension")
+    B, max_pages = page_table.shape
+    c.k, c.v, c.dtype = k_cache.data_ptr(), v_cache.data_ptr(), dtype
+    c.n_pages, c.page_size, c.Hkv, c.D = k_cache.shape
+    c.B, c.max_pages = B, max_pages
+    c.k_page_stride, c.k_token_stride, c.k_head_stride = kp, kt, kh
+    c.v_page_stride, c.v_token_stride, c.v_head_stride = vp, vt, vh
+    c.page_table = page_table.data_ptr()
+    c.page_table_stride = page_table.stride(0) if B > 1 else max_pages
+    c.ctx_lens = _int32(ctx_lens, "ctx_lens", (B,))
+    return B
+
+
+def _tree(tree_parents, B):
+    if tree_parents is None:
+        return None, 0
+    N = tree_parents.shape[-1]
+    return _int32(tree_parents, "tree_parents", (B, N)), N
+
+
+class _on:
+    """The tensors' device made current, at no cost when it already is."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None, inv_freq=None, interleaved=False,
+                   tree_parents=None, positions=None, q_out=None, status_word=None, stream=None):
+    """Appends a chunk's keys and values to the paged cache, rotated on the
+    way: k and v [T, Hkv, D] packed rows (any token and head strides), cu_new
+    [B+1] int32 the rows of each sequence, ctx_lens [B] int32 what the cache
+    holds before. With q [T, Hq, D] also rotates the queries, into q_out (or a
+    new tensor); q_out may be q. inv_freq: float64 CPU tensor [rotary / 2], the
+    angle per position of each rotating pair (rope_inv_freq makes the usual
+    one); None leaves keys and queries as they are. tree_parents [B, N]: the
+    chunk is a tree, a node's position its context plus its depth. positions
+    [T] int32: rotary positions of the caller's own. Returns q_out."""
+    a = sv_kv_append_args()
+    B = _fill_cache(a.cache, k_cache, v_cache, page_table, ctx_lens)
+    Hkv, D = a.cache.Hkv, a.cache.D
+    T = a.T = k.shape[0]
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("k, v and q must have the same number of rows")
+    a.cu_new = _int32(cu_new, "cu_new", (B + 1,))
+    a.k, a.k_token_stride, a.k_head_stride = _rows(k, "k", Hkv, D, k_cache)
+    a.v, a.v_token_stride, a.v_head_stride = _rows(v, "v", Hkv, D, k_cache)
+    if q is not None:
+        a.q, a.q_token_stride, a.q_head_stride = _rows(q, "q", None, D, k_cache)
+        a.Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(T, a.Hq, D, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError(f"q_out must be {list(q.shape)}, got {list(q_out.shape)}")
+        a.q_out, a.q_out_token_stride, a.q_out_head_stride = _rows(q_out, "q_out", a.Hq, D, k_cache)
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous 1-D float64 CPU tensor")
+        a.inv_freq, a.rotary = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    a.interleaved = 1 if interleaved else 0
+    a.tree_parents, a.N = _tree(tree_parents, B)
+    if positions is not None:
+        a.positions = _int32(positions, "positions", (T,))
+    a.status_word = _ptr(status_word)
+    dev = k_cache.device
+    a.stream = _stream(stream, dev)
+    with _on(dev):
+        st = _load().spec_kv_append(ctypes.byref(a))
+    _check(st, "spec_kv_append")
+    return q_out
+
+
+def rope_inv_freq(rotary, base=10000.0):
+    """base^(-2i / rotary) for i < rotary / 2, as spec_kv_append takes it."""
+    i = torch.arange(rotary // 2, dtype=torch.float64)
+    return torch.exp(i * (-2.0 / rotary) * torch.log(torch.tensor(float(base), dtype=torch.float64)))
+
+
+def spec_paged_attention_workspace_bytes(T, Hq, Hkv, D) -> int:
+    return int(_load().spec_paged_attention_workspace_bytes(T, Hq, Hkv, D))
+
+
+def spec_paged_attention_workspace(T, Hq, Hkv, D, device="cuda"):
+    """A workspace for calls of up to T packed rows, its counters zero. Calls
+    that may overlap (on different streams) need one each."""
+    need = spec_paged_attention_workspace_bytes(T, Hq, Hkv, D)
+    if need == 0:
+        raise ValueError(f"no workspace for T={T}, Hq={Hq}, Hkv={Hkv}, D={D}")
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws[:SV_PAGED_WORKSPACE_HEAD].zero_()
+    return ws
+
+
+def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scale=None, tree_parents=None, out=None,
+                         out_lse=None, workspace=None, status_word=None, stream=None, flags=0):
+    """Attention of a chunk's tokens (q [T, Hq, D], packed rows of any token
+    and head strides) over the paged cache, which holds their keys and values
+    already: each token sees its context, itself and the chunk's tokens before
+    it, or, with tree_parents [B, N], its ancestors. scale: D ** -0.5 by
+    default. out_lse [T, Hq] float32: the rows' log of the sum of exponentials.
+    workspace: spec_paged_attention_workspace; made anew when None. Returns
+    out."""
+    a = sv_paged_attention_args()
+    B = _fill_cache(a.cache, k_cache, v_cache, page_table, ctx_lens)
+    Hkv, D = a.cache.Hkv, a.cache.D
+    T = a.T = q.shape[0]
+    dev = k_cache.device
+    a.cu_new = _int32(cu_new, "cu_new", (B + 1,))
+    a.q, a.q_token_stride, a.q_head_stride = _rows(q, "q", None, D, k_cache)
+    Hq = a.Hq = q.shape[1]
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    a.out, a.out_token_stride, a.out_head_stride = _rows(out, "out", Hq, D, k_cache)
+    if out_lse is not None:
+        if out_lse.dtype != torch.float32 or tuple(out_lse.shape) != (T, Hq):
+            raise ValueError(f"out_lse must be float32 [{T}, {Hq}]")
+        a.out_lse = _ptr(out_lse)
+    a.scale = D ** -0.5 if scale is None else float(scale)
+    a.tree_parents, a.N = _tree(tree_parents, B)
+    with _on(dev):
+        a.stream = _stream(stream, dev)
+        if workspace is None and T > 0:
+            need = spec_paged_attention_workspace_bytes(T, Hq, Hkv, D)
+            if need:
+                with torch.cuda.stream(torch.cuda.ExternalStream(a.stream or 0, device=dev)):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                    workspace[:SV_PAGED_WORKSPACE_HEAD].zero_()
+        if workspace is not None:
+            a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+        a.status_word = _ptr(status_word)
+        a.flags = int(flags)
+        st = _load().spec_paged_attention(ctypes.byref(a))
+    _check(st, "spec_paged_attention")
+    return out
+
+
+def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_parents=None, last_node=None, out_lens=None,
+                   status_word=None, stream=None):
+    """Keeps what a verify step accepted in the paged cache: the new lengths
+    ctx_lens + 1 + n_accepted (into out_lens, which may be ctx_lens, or a new
+    tensor), and with tree_parents [B, N] and last_node [B] (as
+    spec_verify_tree takes and returns them) the kept path's entries moved
+    behind the context. Returns out_lens."""
+    c = sv_kv_cache()
+    B = _fill_cache(c, k_cache, v_cache, page_table, ctx_lens)
+    if out_lens is None:
+        out_lens = torch.empty_like(ctx_lens)
+    parents, N = _tree(tree_parents, B)
+    last = None if last_node is None else _int32(last_node, "last_node", (B,))
+    dev = k_cache.device
+    with _on(dev):
+        st = _load().spec_kv_commit(ctypes.byref(c), _int32(n_accepted, "n_accepted", (B,)), parents, N, last,
+                                    _int32(out_lens, "out_lens", (B,)), _ptr(status_word), _stream(stream, dev))
+    _check(st, "spec_kv_commit")
+    return out_lens

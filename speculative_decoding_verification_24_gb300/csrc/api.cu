@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "specverify.h"
+#include "paged.h"
 #include "sv_launch.h"
 
 namespace {
@@ -20,14 +21,17 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_state[kMaxDevices];
 std::atomic<int> g_dev_sms[kMaxDevices];
 
-sv_status fail_cuda(cudaError_t e) {
+}  // namespace
+
+// Shared with the paged cache's entry points (paged_api.cu).
+sv_status sv::fail_cuda(cudaError_t e) {
     g_last_cuda_error = (int)e;
     return SV_ERR_CUDA;
 }
 
 // The current device must be compute capability 10.3 (the library is built
 // for sm_103a only). Returns its SM count through *sms.
-sv_status check_device(int* sms) {
+sv_status sv::check_device(int* sms) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail_cuda(e);
@@ -47,6 +51,11 @@ sv_status check_device(int* sms) {
     *sms = g_dev_sms[dev].load(std::memory_order_relaxed);
     return SV_OK;
 }
+
+using sv::check_device;
+using sv::fail_cuda;
+
+namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

@@ -1,0 +1,315 @@
+// Writing and rearranging a paged key/value cache: appending a chunk's keys
+// and values with the rotary rotation applied on the way, and keeping the
+// path of a verified tree.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "paged_device.cuh"
+
+namespace sv {
+
+// ---------------------------------------------------------------------------
+// Append. For a token at position t and frequency f_i the pair (a, b) becomes
+//   (a cos(t f_i) - b sin(t f_i), b cos(t f_i) + a sin(t f_i)),
+// with (a, b) = (x_i, x_{i + R/2}) or (x_2i, x_2i+1); elements past R stay.
+// The angle is formed in turns as a 64-bit fixed-point fraction: position
+// times f_i / 2 pi modulo 2^64 drops whole turns exactly, so a position of
+// 2^20 has the same angle error (2^-25 turns, the fp32 argument of sincospif)
+// as position 1. A float product would lose 2^-4 turns there.
+//
+// Every input byte is read once and every output byte written once, so HBM
+// bounds it; a small call is bound by its chain of dependent loads (token ->
+// sequence -> page). A CTA takes a few tokens: one warp per token finds its
+// sequence and page, the angles of a token are formed once for all heads, and
+// then D/16 lanes move one head, each two 16-byte pieces that hold whole pairs
+// (pieces i and i + R/16, or neighbours), so that a rotation needs no exchange
+// between lanes.
+// ---------------------------------------------------------------------------
+constexpr int KA_THREADS = 256;
+constexpr int KA_MAX_TOKENS = 4;
+
+struct TokenPlace {
+    int64_t k_off, v_off;  // byte offsets of the slot in the caches, -1: not stored
+    int row;               // packed row, -1: no sequence claims it
+};
+
+template <bool F16>
+__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        } else {
+            x[2 * i] = bf16_lo(r[i]), x[2 * i + 1] = bf16_hi(r[i]);
+        }
+    }
+}
+
+// Rounded once, to nearest even: the cache's own type.
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F16) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The last sequence b with cu[b] <= t, by a warp that tests 32 places at once.
+// Whatever cu holds, the answer lies in [0, B).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, int lane) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const uint32_t le = __ballot_sync(0xFFFFFFFFu, at < hi && __ldg(cu + at) <= t);
+        const int k = le ? 31 - __clz(le) : 0;
+        const int nlo = lo + k * step;
+        hi = min(hi, nlo + step);
+        lo = nlo;
+    }
+    return lo;
+}
+
+// Read once, so not kept in L1; not the read-only path, since q_out may be q.
+__device__ __forceinline__ uint4 ld_once(const char* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(KA_THREADS) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+    __shared__ TokenPlace place[KA_MAX_TOKENS];
+    __shared__ int pos_s[KA_MAX_TOKENS];
+    __shared__ __align__(16) float2 cs[KA_MAX_TOKENS][KV_MAX_ROTARY / 2];  // (cos, sin)
+    const ChunkParams& ch = p.ch;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    launch_dependents();
+    grid_dependency_wait();
+    const int t0 = blockIdx.x * p.tokens_per_cta;
+    const int nt = min(p.tokens_per_cta, ch.T - t0);
+
+    if (warp < nt) {
+        const int t = t0 + warp;
+        const int b = find_sequence(ch.cu, ch.B, t, lane);
+        const Chunk s = load_chunk(ch, b);
+        const int i = t - s.q0;
+        const bool mine = s.rows_ok && i >= 0 && i < s.n;
+        int pos = s.ctx + i;
+        if (mine && s.ok && ch.parents) {
+            const uint32_t set = __shfl_sync(0xFFFFFFFFu, tree_sets(ch, b, s.n, lane), i);
+            pos = s.ctx + (set ? __popc(set) - 1 : 0);
+        }
+        if (lane == 0) {
+            TokenPlace pl{-1, -1, mine ? t : -1};
+            if (mine && !s.ok) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
+            if (mine && s.ok) {
+                const int slot = s.ctx + i;
+                const int page = page_of(ch, b, slot);
+                if (page >= 0) {
+                    const int at = slot % ch.page_size;
+                    pl.k_off = page * p.kc_ps + at * p.kc_ts;
+                    pl.v_off = page * p.vc_ps + at * p.vc_ts;
+                }
+            }
+            place[warp] = pl;
+            pos_s[warp] = p.positions && mine ? __ldg(p.positions + t) : pos;
+        }
+    }
+    __syncthreads();
+    const int half = p.rotary / 2;
+    for (int x = threadIdx.x; x < nt * (KV_MAX_ROTARY / 2); x += KA_THREADS) {
+        const int tk = x / (KV_MAX_ROTARY / 2), i = x % (KV_MAX_ROTARY / 2);
+        if (i < half) {
+            const uint64_t turns = (uint64_t)(int64_t)pos_s[tk] * p.turns[i];
+            float sn, cn;
+            sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31 half turns
+            cs[tk][i] = make_float2(cn, sn);
+        }
+    }
+    __syncthreads();
+
+    constexpr int L = D / 16;                  // lanes per head
+    const int heads = (p.q ? p.Hq : 0) + 2 * ch.Hkv;
+    const int per_token = heads * L;
+    const int rot_lanes = p.rotary / 16;       // lanes whose pieces rotate
+    for (int x = threadIdx.x; x < nt * per_token; x += KA_THREADS) {
+        const int tk = nt == 1 ? 0 : x / per_token;
+        const int y = x - tk * per_token;
+        int h = y / L;
+        const int c = y % L;
+        const TokenPlace pl = place[tk];
+        if (pl.row < 0) continue;
+        const char* src;
+        char* dst;
+        bool rotate = c < rot_lanes;
+        if (h < ch.Hkv) {
+            src = p.k + pl.row * p.k_ts + h * p.k_hs;
+            dst = pl.k_off >= 0 ? p.kc + pl.k_off + h * p.kc_hs : nullptr;
+        } else if (h < 2 * ch.Hkv) {
+            h -= ch.Hkv;
+            src = p.v + pl.row * p.v_ts + h * p.v_hs;
+            dst = pl.v_off >= 0 ? p.vc + pl.v_off + h * p.vc_hs : nullptr;
+            rotate = false;
+        } else {
+            h -= 2 * ch.Hkv;
+            src = p.q + pl.row * p.q_ts + h * p.q_hs;
+            dst = p.q_out + pl.row * p.qo_ts + h * p.qo_hs;
+        }
+        if (!dst) continue;
+        // this lane's two 16-byte pieces
+        int c0 = 2 * c, c1 = 2 * c + 1;
+        if (!p.interleaved && c < rot_lanes) c0 = c, c1 = c + rot_lanes;
+        const uint4 w0 = ld_once(src + 16 * c0);
+        const uint4 w1 = ld_once(src + 16 * c1);
+        uint4 o0 = w0, o1 = w1;
+        if (rotate) {
+            float a[8], b[8];
+            unpack8<F16>(w0, a);
+            unpack8<F16>(w1, b);
+            const float2* t = cs[tk] + 8 * c;
+            if (p.interleaved) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = t[i], g = t[4 + i];
+                    const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+                    a[2 * i] = a0 * f.x - a1 * f.y, a[2 * i + 1] = a1 * f.x + a0 * f.y;
+                    b[2 * i] = b0 * g.x - b1 * g.y, b[2 * i + 1] = b1 * g.x + b0 * g.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = t[i];
+                    const float a0 = a[i], b0 = b[i];
+                    a[i] = a0 * f.x - b0 * f.y;
+                    b[i] = b0 * f.x + a0 * f.y;
+                }
+            }
+            o0 = pack8<F16>(a);
+            o1 = pack8<F16>(b);
+        }
+        reinterpret_cast<uint4*>(dst)[c0] = o0;
+        reinterpret_cast<uint4*>(dst)[c1] = o1;
+    }
+}
+
+template <class K, class P>
+static cudaError_t launch_early(K kernel, int grid, int threads, const P& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+cudaError_t launch_kv_append(const KvAppendParams& in, int f16, int sms, cudaStream_t stream) {
+    KvAppendParams p = in;
+    p.tokens_per_cta = p.ch.T > 4 * sms ? KA_MAX_TOKENS : 1;
+    const int grid = (p.ch.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+    auto kernel = p.D == 128 ? (f16 ? kv_append_kernel<128, true> : kv_append_kernel<128, false>)
+                             : (f16 ? kv_append_kernel<64, true> : kv_append_kernel<64, false>);
+    return launch_early(kernel, grid, KA_THREADS, p, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Commit. A tree's nodes were appended at slots ctx + node; the kept path
+// 0 = p_0 < p_1 < ... < p_n moves to slots ctx + 1 .. ctx + n (keys carry the
+// rotation of ctx + depth already). Node p_j >= j, so a place j is never the
+// source of a later node: a thread that reads some nodes of its 16 bytes in
+// ascending order before it writes them, and then goes on to the next, moves
+// the path in place. One CTA per sequence; the bytes are few (2 n Hkv D per
+// cache) and the call is bound by its launch and its dependent loads.
+// ---------------------------------------------------------------------------
+constexpr int KC_THREADS = 256;
+constexpr int KC_BATCH = 8;  // 16-byte loads in flight per thread
+
+__global__ void __launch_bounds__(KC_THREADS) kv_commit_kernel(const __grid_constant__ KvCommitParams p) {
+    __shared__ int64_t k_from[KV_MAX_TREE], k_to[KV_MAX_TREE], v_from[KV_MAX_TREE], v_to[KV_MAX_TREE];
+    __shared__ int moves_s;
+    const ChunkParams& ch = p.ch;
+    const int lane = threadIdx.x & 31;
+    launch_dependents();
+    grid_dependency_wait();
+    const int b = blockIdx.x;
+    if (threadIdx.x < 32) {
+        const int ctx = ch.ctx[b], n = __ldg(p.n_accepted + b);  // out_lens may be ctx
+        const long long room = (long long)ch.max_pages * ch.page_size;
+        bool ok = ctx >= 0 && n >= 0 && (long long)ctx + 1 + n <= room && (!ch.parents || n < ch.N);
+        if (lane == 0 && n >= 0 && !ok) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
+        int moves = 0;
+        if (ok && ch.parents) {
+            const int last = __ldg(p.last_node + b);
+            const bool in_tree = last >= 0 && last < ch.N && (long long)ctx + last < room;
+            // nodes past the last one are not needed, and may be padding
+            const uint32_t set = __shfl_sync(0xFFFFFFFFu, tree_sets(ch, b, in_tree ? last + 1 : 0, lane), in_tree ? last : 0);
+            ok = in_tree && __popc(set) == n + 1;
+            if (lane == 0 && !ok) raise_flag(ch.status, SV_FLAG_BAD_TREE);
+            const int to = __popc(set & ((1u << lane) - 1u));
+            bool move = ok && ((set >> lane) & 1u) && to != lane;
+            int from_page = 0, to_page = 0;
+            if (move) {
+                from_page = page_of(ch, b, ctx + lane);
+                to_page = page_of(ch, b, ctx + to);
+                move = from_page >= 0 && to_page >= 0;
+            }
+            const uint32_t all = __ballot_sync(0xFFFFFFFFu, move);
+            moves = __popc(all);
+            if (move) {
+                const int at = __popc(all & ((1u << lane) - 1u));
+                const int f = (ctx + lane) % ch.page_size, d = (ctx + to) % ch.page_size;
+                k_from[at] = from_page * p.kc_ps + f * p.kc_ts;
+                k_to[at] = to_page * p.kc_ps + d * p.kc_ts;
+                v_from[at] = from_page * p.vc_ps + f * p.vc_ts;
+                v_to[at] = to_page * p.vc_ps + d * p.vc_ts;
+            }
+        }
+        if (lane == 0) {
+            moves_s = moves;
+            p.out_lens[b] = ok ? ctx + 1 + n : ctx;
+        }
+    }
+    __syncthreads();
+    const int moves = moves_s;
+    const int pieces = p.D / 8, per_cache = ch.Hkv * pieces;
+    for (int x = threadIdx.x; moves > 0 && x < 2 * per_cache; x += KC_THREADS) {
+        const bool is_v = x >= per_cache;
+        const int y = is_v ? x - per_cache : x;
+        const int h = y / pieces, c = y % pieces;
+        char* base = is_v ? p.vc + h * p.vc_hs + c * 16 : p.kc + h * p.kc_hs + c * 16;
+        const int64_t* from = is_v ? v_from : k_from;
+        const int64_t* to = is_v ? v_to : k_to;
+        for (int j0 = 0; j0 < moves; j0 += KC_BATCH) {
+            uint4 w[KC_BATCH];
+#pragma unroll
+            for (int j = 0; j < KC_BATCH; ++j)
+                if (j0 + j < moves) w[j] = *reinterpret_cast<const uint4*>(base + from[j0 + j]);
+#pragma unroll
+            for (int j = 0; j < KC_BATCH; ++j)
+                if (j0 + j < moves) *reinterpret_cast<uint4*>(base + to[j0 + j]) = w[j];
+        }
+    }
+}
+
+cudaError_t launch_kv_commit(const KvCommitParams& p, cudaStream_t stream) {
+    return launch_early(kv_commit_kernel, p.ch.B, KC_THREADS, p, stream);
+}
+
+}  // namespace sv

@@ -1,0 +1,1081 @@
+// Attention of each sequence's new tokens over its paged cache:
+//   o[t, h] = sum_j softmax_j(scale q[t, h] . k[j, h / G]) v[j, h / G]
+// over the slots j that token t sees (its context and itself; in a chain the
+// chunk's tokens before it, in a tree its ancestors).
+//
+// One kernel for one token, a few drafts, a tree and a prompt's chunk. The G
+// query heads of a kv head are packed with the tokens into rows (row = token
+// * G + head), so keys and values are read once for all of them. A tile is
+// 128 rows x 128 keys:
+//   S = Q K^T        tcgen05.mma, both operands in shared memory, S in TMEM;
+//   P = 2^(c S - m)  one thread per row: its 128 scores in registers, the
+//                    running maximum m and sum l of a one-pass softmax, P
+//                    rounded to the cache's type and written over S in TMEM;
+//   O += P V         tcgen05.mma, P from TMEM, V from shared memory, O in TMEM.
+// m is only raised (and O and l rescaled) when a score passes it by more than
+// 2^8: l and O share whatever m is used, so the result does not depend on it,
+// and most tiles touch no O at all.
+//
+// Two softmax warpgroups keep the tensor cores and the softmax busy at once:
+// while one computes P, the other's products run. A chunk of more than 128
+// rows gives each its own 128 rows and both use every key tile ("pair"); with
+// at most 128 rows both hold the same rows, take alternate key tiles and join
+// their (m, l, O) at the end ("split"), which for few rows halves the chain of
+// dependent steps per byte.
+//
+// Work is counted in key tiles over all (sequence, head, row tile) items in
+// that order, and every CTA takes an equal, contiguous share of the total,
+// cutting items where its share ends: one long context spreads over the whole
+// GPU, and so does a ragged batch, without the host knowing the lengths. A cut
+// item's pieces are written as (m, l, unscaled O) in fp32 and joined in order
+// by whichever CTA finishes last, so the result does not depend on timing.
+//
+// Warps: 0-3 and 4-7 softmax and output, 8 keys and values (TMA, one box per
+// page or 128 tokens), 9 the products, 10-11 queries (cp.async, any strides).
+// Every mbarrier wait is bounded; one that gives up sets SV_FLAG_TIMEOUT, the
+// others stop waiting, no further work is issued, what was issued is waited
+// for, TMEM is freed and the rows concerned are NaN.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "paged_device.cuh"
+
+namespace sv {
+
+constexpr int PA_THREADS = 384;
+constexpr int PA_SOFTMAX_THREADS = 256;
+constexpr uint32_t PA_WAIT_LIMIT = 1u << 22;
+constexpr float PA_RAISE = 8.0f;                 // log2 of how far a score may pass m
+constexpr int PA_TMEM_COLS = 512;                // S0, S1 (128 columns each), O0, O1 (D each)
+constexpr int PA_SLAB_BYTES = PA_TILE * 128;     // 128 rows of 64 elements: one 128-byte-swizzled operand block
+
+template <int D>
+struct PaShape {
+    static constexpr int SLABS = D / 64;
+    static constexpr int TILE_BYTES = SLABS * PA_SLAB_BYTES;  // 128 rows of Q, K or V
+    static constexpr int STAGES = 160 * 1024 / TILE_BYTES;    // K and V tiles in flight: 160 KB
+    static constexpr int TILES_BYTES = (2 + STAGES) * TILE_BYTES;
+};
+
+// ---------------------------------------------------------------------------
+// tcgen05 wrappers.
+// ---------------------------------------------------------------------------
+// Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
+// and stride byte offsets (all >> 4), descriptor version 1, layout code 2.
+__device__ __forceinline__ uint64_t pa_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Instruction descriptor of kind::f16: fp32 accumulator, A and B both f16 or
+// both bf16, 128 x n; b_mn: B is stored with n contiguous.
+__host__ __device__ constexpr uint32_t pa_idesc(bool f16, int n, bool b_mn) {
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(PA_TILE >> 4) << 24);
+}
+
+// S = Q K^T: A and B from shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// O += P V: A from TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A warp's 32 lanes x n columns, one row per lane. The wait is part of the
+// statement, so that no use of the registers can be scheduled before it.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int token, int head, int page,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Waits for a phase; once any wait of the CTA has given up, all return at once.
+__device__ __forceinline__ void pa_wait(uint64_t* bar, uint32_t parity, int* err) {
+    if (mbar_try_wait(bar, parity)) return;
+    for (uint32_t i = 0; i < PA_WAIT_LIMIT; ++i) {
+        if (mbar_try_wait(bar, parity) || *(volatile int*)err) return;
+    }
+    atomicExch(err, 1);
+}
+__device__ __forceinline__ bool pa_failed(const int* err) { return *(volatile const int*)err != 0; }
+
+// Named barrier 1: the 256 softmax threads (barrier 0 is __syncthreads).
+__device__ __forceinline__ void softmax_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(PA_SOFTMAX_THREADS) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Work: items in the order (sequence, kv head, row tile), each item its number
+// of key tiles long, laid end to end on one axis of W tiles.
+// ---------------------------------------------------------------------------
+// sum over i < n of floor((a i + b) / m)
+__device__ inline uint64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
+    uint64_t ans = 0;
+    while (n > 0) {
+        if (a >= m) {
+            ans += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            ans += n * (b / m);
+            b %= m;
+        }
+        const uint64_t y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const uint64_t t = m;
+        m = a;
+        a = t;
+    }
+    return ans;
+}
+
+__device__ __forceinline__ int tiles_of(int end) { return (int)(((long long)end + PA_TILE - 1) / PA_TILE); }
+
+// Row tiles pair up; row-tile pair p covers tokens [2 TT p, 2 TT (p + 1)).
+__device__ __forceinline__ int pairs_of(int n, int TT) { return n <= TT ? 1 : (n + 2 * TT - 1) / (2 * TT); }
+
+// Key tiles of one kv head's first p pairs (p < pairs: none of them the last).
+__device__ __forceinline__ long long tiles_before(int ctx, int TT, int p) {
+    return p == 0 ? 0 : (long long)floor_sum(p, PA_TILE, 2 * TT, (uint64_t)ctx + 2 * TT + PA_TILE - 1);
+}
+__device__ __forceinline__ long long tiles_per_head(int n, int ctx, int TT) {
+    return n == 0 ? 0 : tiles_before(ctx, TT, pairs_of(n, TT) - 1) + tiles_of(ctx + n);
+}
+
+// A walk over the items of a CTA's share, computed alike by every role.
+struct Cursor {
+    long long begin, end;   // this CTA's share
+    long long u0;           // where the current item begins
+    int b, h, p;            // sequence, kv head, row-tile pair
+    Chunk s;
+    int tok0, ntok, tiles;  // the item's tokens within the chunk, its key tiles
+
+    __device__ __forceinline__ void set_item(const PagedAttnParams& P) {
+        tok0 = 2 * P.TT * p;
+        ntok = min(s.n - tok0, 2 * P.TT);
+        tiles = tiles_of(s.ctx + tok0 + ntok);
+    }
+    __device__ __forceinline__ bool valid() const { return u0 < end; }
+    __device__ __forceinline__ void next(const PagedAttnParams& P) {
+        u0 += tiles;
+        if (u0 >= end) return;
+        if (++p == pairs_of(s.n, P.TT)) {
+            p = 0;
+            if (++h == P.ch.Hkv) {
+                h = 0;
+                // u0 < end <= W, so a later sequence has work
+                do {
+                    s = load_chunk(P.ch, ++b);
+                } while (b + 1 < P.ch.B && (!s.ok || s.n == 0));
+            }
+        }
+        set_item(P);
+    }
+    // the part of the item in this share
+    __device__ __forceinline__ int t0() const { return begin > u0 ? (int)(begin - u0) : 0; }
+    __device__ __forceinline__ int t1() const { return end - u0 < tiles ? (int)(end - u0) : tiles; }
+    __device__ __forceinline__ bool pair(const PagedAttnParams& P) const { return ntok > P.TT; }
+};
+
+// Share boundaries: u_c = floor(c W / A), moved to the item's edge when it
+// falls within `snap` tiles of one (a piece of a few tiles costs more in
+// joining than the uneven share does).
+struct Shares {
+    long long W;
+    int active;   // CTAs with work
+    int snap;
+};
+// A CTA gets at least this many tiles: below that, joining costs more than
+// another CTA saves.
+constexpr int PA_MIN_SHARE = 2;
+
+struct PaShared {
+    long long scan[PA_THREADS / 32];
+    long long W;
+    int found_b[2];
+    long long found_pre[2];
+    Cursor at[2];
+    uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2], mma_done, never;
+    float2 ml[2][PA_TILE];
+    uint32_t tmem;
+    int last;
+    int err;
+};
+template <int D>
+constexpr int PA_SMEM = PaShape<D>::TILES_BYTES + (int)sizeof(PaShared);
+static_assert(PA_SMEM<64> <= 227 * 1024 && PA_SMEM<128> <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += t;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < PA_THREADS / 32; ++w) {
+        const long long x = warp_sums[w];
+        before += w < warp ? x : 0;
+        total += x;
+    }
+    return before + v;
+}
+
+// Every thread: finds this CTA's share, and whether any sequence of the batch
+// is left out (bad). Returns false when there is no work here.
+__device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& sh, Shares& shares, Cursor& cur, bool& bad) {
+    const ChunkParams& ch = P.ch;
+    const int tid = threadIdx.x;
+    long long W = 0, first_incl = 0, first = 0;
+    bool my_bad = false;
+    for (int base = 0; base < ch.B; base += PA_THREADS) {
+        const int b = base + tid;
+        long long mine = 0;
+        if (b < ch.B) {
+            const Chunk s = load_chunk(ch, b);
+            if (s.ok) {
+                mine = tiles_per_head(s.n, s.ctx, P.TT) * ch.Hkv;
+            } else {
+                my_bad = true;
+                if (blockIdx.x == 0) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
+            }
+        }
+        long long total;
+        const long long incl = block_scan(mine, sh.scan, total);
+        if (base == 0) first_incl = incl, first = mine;
+        W += total;
+    }
+    bad = __syncthreads_or(my_bad);
+    shares.W = W;
+    const long long most = (W + PA_MIN_SHARE - 1) / PA_MIN_SHARE;
+    shares.active = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
+    if ((int)blockIdx.x >= shares.active) return false;
+    shares.snap = (int)(W / shares.active / 16);
+    const long long raw[2] = {(long long)blockIdx.x * W / shares.active, ((long long)blockIdx.x + 1) * W / shares.active};
+    long long run = 0;
+    for (int base = 0; base < ch.B; base += PA_THREADS) {
+        long long incl = first_incl, mine = first, total = 0;
+        const int b = base + tid;
+        if (ch.B > PA_THREADS) {
+            mine = 0;
+            if (b < ch.B) {
+                const Chunk s = load_chunk(ch, b);
+                if (s.ok) mine = tiles_per_head(s.n, s.ctx, P.TT) * ch.Hkv;
+            }
+            incl = block_scan(mine, sh.scan, total);
+        }
+        const long long excl = run + incl - mine;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (raw[k] >= excl && raw[k] < excl + mine) {
+                sh.found_b[k] = b;
+                sh.found_pre[k] = excl;
+            }
+        run += total;
+    }
+    __syncthreads();
+    if ((tid & 31) == 0 && tid < 64) {
+        const int k = tid >> 5;
+        Cursor c;
+        if (raw[k] < W) {
+            c.b = sh.found_b[k];
+            c.s = load_chunk(ch, c.b);
+            const long long per_head = tiles_per_head(c.s.n, c.s.ctx, P.TT);
+            const long long r = raw[k] - sh.found_pre[k];
+            c.h = (int)(r / per_head);
+            const long long in_head = r - c.h * per_head;
+            int lo = 0, hi = pairs_of(c.s.n, P.TT);
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (tiles_before(c.s.ctx, P.TT, mid) <= in_head) lo = mid;
+                else hi = mid;
+            }
+            c.p = lo;
+            c.u0 = sh.found_pre[k] + c.h * per_head + tiles_before(c.s.ctx, P.TT, lo);
+            c.set_item(P);
+            c.begin = raw[k];
+            if (raw[k] - c.u0 <= shares.snap) {
+                c.begin = c.u0;
+            } else if (c.u0 + c.tiles - raw[k] <= shares.snap) {
+                c.begin = c.u0 + c.tiles;
+                c.end = W;
+                c.next(P);
+            }
+        } else {
+            c.begin = c.u0 = W;
+        }
+        sh.at[k] = c;
+    }
+    __syncthreads();
+    cur = sh.at[0];
+    cur.end = sh.at[1].begin;
+    return cur.begin < cur.end;
+}
+
+// The pieces an item is cut into: the first boundary inside it (the item
+// begins in the CTA before) and how many pieces there are.
+__device__ __forceinline__ void pieces_of(const Shares& w, const Cursor& c, int& first_cta, int& pieces) {
+    const long long lo = c.u0 + w.snap + 1, hi = c.u0 + c.tiles - w.snap - 1;  // boundaries in [lo, hi] cut it
+    const long long c_lo = (lo * w.active + w.W - 1) / w.W;
+    const long long c_hi = ((hi + 1) * w.active + w.W - 1) / w.W - 1;
+    first_cta = (int)c_lo - 1;
+    pieces = (int)(c_hi - c_lo) + 2;
+}
+
+// Which ring entries (K and V tiles, in the order the products use them) tile
+// i of a piece of m tiles has. Pair: K0 V0 K1 V1 ...; split: K0 K1 V0 K2 V1
+// ... V(m-1).
+__device__ __forceinline__ int ring_k(bool pair, int i) { return pair ? 2 * i : (i == 0 ? 0 : 2 * i - 1); }
+__device__ __forceinline__ int ring_v(bool pair, int i, int m) { return pair ? 2 * i + 1 : (i == m - 1 ? 2 * m - 1 : 2 * i + 2); }
+
+// Which query buffer a split item uses: they alternate; a pair uses both.
+// uses[k] counts the fills of buffer k so far.
+struct QueryBuffers {
+    int uses[2] = {0, 0};
+    int turn = 0;
+    __device__ __forceinline__ int begin_split() {
+        const int k = turn;
+        turn ^= 1;
+        return k;
+    }
+};
+
+// A query buffer is free after two arrivals: one from each stream of a split
+// item, both from the one stream that uses it in a pair. A stream arrives when
+// its last scores have been formed; one that has no tiles here arrives only
+// after a barrier with the other, when the products have long taken the
+// buffer: an earlier arrival could let it be filled twice before they look.
+__device__ __forceinline__ void release_q(uint64_t* bar, bool pair) {
+    mbar_arrive(bar);
+    if (pair) mbar_arrive(bar);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+    uint32_t r;
+    if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// n values of one output row, scaled and rounded once, from column col on.
+template <bool F16, int N>
+__device__ __forceinline__ void store_row(char* row, int col, const float (&x)[N], float scale) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        uint4 w;
+        w.x = pack_pair<F16>(x[i] * scale, x[i + 1] * scale);
+        w.y = pack_pair<F16>(x[i + 2] * scale, x[i + 3] * scale);
+        w.z = pack_pair<F16>(x[i + 4] * scale, x[i + 5] * scale);
+        w.w = pack_pair<F16>(x[i + 6] * scale, x[i + 7] * scale);
+        *reinterpret_cast<uint4*>(row + (col + i) * 2) = w;
+    }
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Where row r of the item's row tile w lives in the batch.
+struct RowPlace {
+    int token, head;  // packed row of q and out, query head
+    bool valid;
+};
+__device__ __forceinline__ RowPlace place_row(const PagedAttnParams& P, const Cursor& c, int tile, int r) {
+    RowPlace x;
+    const int i = r / P.G, in_chunk = c.tok0 + tile * P.TT + i;
+    x.valid = i < P.TT && in_chunk < c.tok0 + c.ntok;
+    x.token = c.s.q0 + in_chunk;
+    x.head = c.h * P.G + r % P.G;
+    return x;
+}
+
+// Joins an item's pieces in their order, by the CTA that finished last: a warp
+// per row, a lane per piece for the weights and per D / 32 columns for O.
+template <int D, bool F16>
+__device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Cursor& c, int first_cta, int pieces) {
+    constexpr int C = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool pair = c.pair(P);
+    const int rows0 = (pair ? P.TT : c.ntok) * P.G, rows = c.ntok * P.G;
+    for (int r = warp; r < rows; r += PA_SOFTMAX_THREADS / 32) {
+        const int row = r < rows0 ? r : PA_TILE + r - rows0;
+        float M = -INFINITY, L = 0.0f, acc[C] = {};
+        for (int f0 = 0; f0 < pieces; f0 += 32) {
+            const int f = f0 + lane;
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (f < pieces) {
+                const int slot = f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f);
+                ml = __ldcg(P.part_ml + (size_t)slot * P.rows_cap + row);
+            }
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            m = fmaxf(m, M);
+            const float old = M == -INFINITY ? 0.0f : ex2(M - m);
+            const float w = ml.y == 0.0f ? 0.0f : ex2(ml.x - m);  // NaN stays NaN
+            float l = w * ml.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            L = L * old + l;
+            M = m;
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] *= old;
+            const int here = min(32, pieces - f0);
+#pragma unroll 4
+            for (int k = 0; k < here; ++k) {
+                const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+                const int slot = f0 + k == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f0 + k);
+                const float* src = P.part_o + ((size_t)slot * P.rows_cap + row) * D + lane * C;
+                float x[C];
+                if constexpr (C == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                    x[0] = v.x, x[1] = v.y;
+                }
+                // a piece that saw nothing of the row has weight 0 and no O
+#pragma unroll
+                for (int i = 0; i < C; ++i) acc[i] = wk == 0.0f ? acc[i] : fmaf(wk, x[i], acc[i]);
+            }
+        }
+        const RowPlace at = place_row(P, c, row / PA_TILE, row % PA_TILE);
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        char* dst = P.out + at.token * P.o_ts + at.head * P.o_hs + lane * C * 2;
+        if constexpr (C == 4) {
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_pair<F16>(acc[0] * inv, acc[1] * inv), pack_pair<F16>(acc[2] * inv, acc[3] * inv));
+        } else {
+            *reinterpret_cast<uint32_t*>(dst) = pack_pair<F16>(acc[0] * inv, acc[1] * inv);
+        }
+        if (P.lse && lane == 0) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M, L);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Roles.
+// ---------------------------------------------------------------------------
+// Warp 8: keys and values. A tile is 128 / box boxes of `box` tokens (the
+// largest power of two that divides the page, at most 128) per 64 columns; a
+// lane issues one. A box past the piece's last key is not loaded. A page the
+// table does not have reads as zeros (a page coordinate past the last one).
+template <int D>
+__device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t ring, const CUtensorMap* tm_k,
+                                        const CUtensorMap* tm_v, int lane) {
+    using S = PaShape<D>;
+    const ChunkParams& ch = P.ch;
+    const int box_shift = P.box_shift;
+    const int my_box = lane / S::SLABS, my_slab = lane % S::SLABS;
+    const bool has_box = my_box < (PA_TILE >> box_shift);
+    int it = 0;
+    bool stop = false;
+    for (; c.valid() && !stop; c.next(P)) {
+        const bool pair = c.pair(P);
+        const int t0 = c.t0(), m = c.t1() - t0, lead = pair ? 0 : 1;
+        const int key_end = c.s.ctx + c.tok0 + c.ntok;
+        const int32_t* table = ch.table + (int64_t)c.b * ch.table_stride;
+        // page of this lane's box of tile t, and its first entry there
+        auto page_at = [&](int t) -> int2 {
+            const int key = t * PA_TILE + (my_box << box_shift);
+            if (!has_box || key >= key_end) return make_int2(-1, 0);
+            const int page_no = key / ch.page_size;
+            int page = __ldg(table + page_no);
+            if (page < 0 || page >= ch.n_pages) {
+                raise_flag(ch.status, SV_FLAG_BAD_PAGE);
+                page = ch.n_pages;
+            }
+            return make_int2(page, key - page_no * ch.page_size);
+        };
+        // pages of tiles i and i + 1, looked up a step ahead
+        int2 p0 = page_at(t0), p1 = page_at(t0 + 1);
+        for (int i = -lead; i < m && !stop; ++i) {
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {  // K of tile i + lead, then V of tile i
+                const int t = kind == 0 ? i + lead : i;
+                if (t < 0 || t >= m || stop) continue;
+                const int2 pg = t > i && i >= 0 ? p1 : p0;
+                const int s = it % S::STAGES, n = it / S::STAGES;
+                if (n > 0) pa_wait(&sh.empty[s], (n - 1) & 1, &sh.err);
+                stop = __any_sync(0xFFFFFFFFu, pa_failed(&sh.err));
+                if (stop) continue;
+                ++it;
+                const int keys = min(key_end - (t0 + t) * PA_TILE, PA_TILE);
+                const int boxes = (keys + (1 << box_shift) - 1) >> box_shift;
+                if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * S::SLABS) << (box_shift + 7));
+                __syncwarp();
+                if (my_box < boxes)
+                    tma_load_4d(ring + s * S::TILE_BYTES + my_slab * PA_SLAB_BYTES + (my_box << (box_shift + 7)),
+                                kind == 0 ? tm_k : tm_v, my_slab * 64, pg.y, c.h, pg.x, &sh.full[s]);
+            }
+            if (i >= 0) {
+                p0 = p1;
+                if (i + 2 < m) p1 = page_at(t0 + i + 2);
+            }
+        }
+    }
+    // every load issued has landed before the CTA ends: the last ones are the
+    // latest phases of their stages
+    for (int q = it - S::STAGES > 0 ? it - S::STAGES : 0; q < it; ++q)
+        (void)mbar_wait(&sh.full[q % S::STAGES], (q / S::STAGES) & 1, PA_WAIT_LIMIT);
+}
+
+// Warps 10 and 11: the rows of Q, 16 bytes per lane, into the swizzled K-major
+// layout (rows of 64 elements, 16-byte piece x at x ^ (row & 7)).
+template <int D>
+__device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, Cursor c, char* q_smem, int x0, int lane) {
+    using S = PaShape<D>;
+    constexpr int PIECES = D / 8;
+    QueryBuffers qb;
+    for (; c.valid(); c.next(P)) {
+        const bool pair = c.pair(P);
+        const int split_buf = pair ? 0 : qb.begin_split();
+        for (int w = 0; w < (pair ? 2 : 1); ++w) {
+            const int buf = pair ? w : split_buf;
+            const int n = qb.uses[buf]++;
+            if (n > 0) pa_wait(&sh.q_empty[buf], (n - 1) & 1, &sh.err);
+            const int tok = c.tok0 + w * P.TT;
+            const int rows = min(P.TT, c.tok0 + c.ntok - tok) * P.G;
+            const uint32_t dst = smem_u32(q_smem + buf * S::TILE_BYTES);
+            const char* src = P.q + (int64_t)(c.s.q0 + tok) * P.q_ts + (int64_t)(c.h * P.G) * P.q_hs;
+            for (int x = x0; x < rows * PIECES; x += 64) {
+                const int r = x / PIECES, ch = x % PIECES;
+                const int i = r / P.G, g = r - i * P.G;
+                cp_async16(dst + (ch >> 3) * PA_SLAB_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                           src + i * P.q_ts + g * P.q_hs + ch * 16);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full[buf]);
+        }
+    }
+}
+
+// Warp 9, one thread: the products. Both warpgroups' streams alternate, and
+// the scores of a stream's next tile are issued right after its O += P V, so
+// that they run while the other warpgroup computes its P.
+template <int D, bool F16>
+__device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t q_smem, uint32_t ring,
+                                               uint32_t tmem) {
+    using S = PaShape<D>;
+    constexpr uint32_t ID_S = pa_idesc(F16, PA_TILE, false), ID_O = pa_idesc(F16, D, true);
+    QueryBuffers qb;
+    int ring0 = 0, p_count[2] = {0, 0};
+    for (; c.valid(); c.next(P)) {
+        const bool pair = c.pair(P);
+        const int t0 = c.t0(), m = c.t1() - t0;
+        int buf[2], last[2];  // each stream's buffer; the first tile index past its tiles
+        if (pair) {
+            buf[0] = 0, buf[1] = 1;
+            const int n0 = tiles_of(c.s.ctx + c.tok0 + P.TT) - t0;
+            last[0] = max(0, min(n0, m));
+            last[1] = m;
+            pa_wait(&sh.q_full[0], qb.uses[0]++ & 1, &sh.err);
+            pa_wait(&sh.q_full[1], qb.uses[1]++ & 1, &sh.err);
+        } else {
+            buf[0] = buf[1] = qb.begin_split();
+            last[0] = last[1] = m;
+            pa_wait(&sh.q_full[buf[0]], qb.uses[buf[0]]++ & 1, &sh.err);
+        }
+        const int step = pair ? 1 : 2;
+        // scores of stream w's tile i; `done`: nothing else will use K of tile i
+        auto scores = [&](int w, int i, bool done) {
+            const int e = ring0 + ring_k(pair, i), s = e % S::STAGES;
+            pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
+            if (pa_failed(&sh.err)) return;
+            tc_fence_after();
+            const uint32_t a = q_smem + buf[w] * S::TILE_BYTES, b = ring + s * S::TILE_BYTES;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k / 4) * PA_SLAB_BYTES + (k % 4) * 32;
+                mma_ss(tmem + w * PA_TILE, pa_desc(a + off, 16, 1024), pa_desc(b + off, 16, 1024), ID_S, k != 0);
+            }
+            mma_commit(&sh.s_full[w]);
+            if (done) mma_commit(&sh.empty[s]);
+        };
+        if (pair) {
+            if (last[0] > 0) scores(0, 0, false);
+            scores(1, 0, true);
+        } else {
+            scores(0, 0, true);
+            if (m > 1) scores(1, 1, true);
+        }
+        for (int i = 0; i < m; ++i) {
+            for (int w = pair ? 0 : i & 1; w < (pair ? 2 : (i & 1) + 1); ++w) {
+                if (i >= last[w]) continue;
+                const int e = ring0 + ring_v(pair, i, m), s = e % S::STAGES;
+                pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
+                pa_wait(&sh.p_full[w], p_count[w]++ & 1, &sh.err);
+                if (pa_failed(&sh.err)) return;
+                tc_fence_after();
+                const uint32_t b = ring + s * S::TILE_BYTES;
+                const bool first = i < step;
+#pragma unroll
+                for (int k = 0; k < PA_TILE / 16; ++k)
+                    mma_ts(tmem + 2 * PA_TILE + w * D, tmem + w * PA_TILE + k * 8, pa_desc(b + k * 2048, PA_SLAB_BYTES, 1024), ID_O,
+                           !first || k != 0);
+                if (!pair || w == 1) mma_commit(&sh.empty[s]);
+                if (i + step < last[w]) scores(w, i + step, !pair || w == 1);
+                else mma_commit(&sh.o_full[w]);
+            }
+        }
+        ring0 += 2 * m;
+    }
+}
+
+// Warps 0-3 (w = 0) and 4-7 (w = 1): softmax and output.
+template <int D, bool F16>
+__device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared& sh, const Shares& shares, Cursor c, int w,
+                                             char* q_smem, char* ring, uint32_t tmem_base) {
+    using S = PaShape<D>;
+    const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, warp = tid >> 5;
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const uint32_t tmem_s = tmem_base + lanes + w * PA_TILE, tmem_o = tmem_base + lanes + 2 * PA_TILE + w * D;
+    QueryBuffers qb;
+    int s_count = 0, o_count = 0, ring0 = 0;
+    const f32x2 cc = pack2(P.c, P.c);
+    for (; c.valid(); c.next(P)) {
+        const bool pair = c.pair(P);
+        const int t0 = c.t0(), t1 = c.t1(), m_tiles = t1 - t0;
+        const int key_end = c.s.ctx + c.tok0 + c.ntok;
+        const RowPlace at = place_row(P, c, pair ? w : 0, tid);
+        const int tok_first = c.tok0 + (pair ? w * P.TT : 0);
+        const int tile_rows = min(P.TT, c.tok0 + c.ntok - tok_first) * P.G;
+        const bool warp_on = 32 * warp < tile_rows;
+        // keys [0, seen) are visible, and in a tree the chunk's nodes in `set`
+        int seen = at.valid ? at.token - c.s.q0 + c.s.ctx + 1 : 0;
+        int seen_by_all = c.s.ctx + tok_first + 1;
+        uint32_t set = 0;
+        if (P.ch.parents) {
+            const uint32_t sets = tree_sets(P.ch, c.b, c.s.n, lane);
+            set = __shfl_sync(0xFFFFFFFFu, sets, at.valid ? at.token - c.s.q0 : 0);
+            if (!at.valid) set = 0;
+            // a node with a bad chain of parents sees nothing
+            seen = set ? c.s.ctx : 0;
+            seen_by_all = __all_sync(0xFFFFFFFFu, !at.valid || set) ? c.s.ctx : 0;
+        }
+        const int buf = pair ? w : qb.begin_split();
+        // this stream's tiles: first, first + step, ... below last
+        const int step = pair ? 1 : 2;
+        const int last0 = !pair ? m_tiles : max(0, min(m_tiles, tiles_of(c.s.ctx + c.tok0 + P.TT) - t0));
+        const int last = w == 0 ? last0 : m_tiles;
+        float m = -INFINITY;
+        f32x2 l2 = pack2(0.0f, 0.0f);
+        int done = 0;
+        for (int i = pair ? 0 : w; i < last; i += step, ++done) {
+            pa_wait(&sh.s_full[w], s_count & 1, &sh.err);
+            ++s_count;
+            tc_fence_after();
+            const int key0 = (t0 + i) * PA_TILE;
+            // this stream's last scores have been formed: it needs Q no more
+            if (i + step >= last && tid == 0) release_q(&sh.q_empty[buf], pair);
+            if (warp_on) {
+                uint32_t r[PA_TILE];
+                tmem_ld(tmem_s, r);
+                if (key0 + PA_TILE > seen_by_all) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = seen - key0 - 32 * q;
+                        uint32_t on = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+                        if (set) {  // node j is key ctx + j, bit ctx + j - key0 - 32 q
+                            const int at0 = c.s.ctx - key0 - 32 * q;
+                            if (at0 >= 0 && at0 < 32) on |= set << at0;
+                            else if (at0 < 0 && at0 > -32) on |= set >> -at0;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!((on >> k) & 1u)) r[32 * q + k] = 0xFF800000u;  // -inf, whatever stood there
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < PA_TILE; k += 8) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mx[j] = fmaxf(fmaxf(mx[j], __uint_as_float(r[k + 2 * j])), __uint_as_float(r[k + 2 * j + 1]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.c;
+                if (done == 0) {
+                    m = top;
+                } else {
+                    const bool raise = at.valid && top > m + PA_RAISE;
+                    if (__any_sync(0xFFFFFFFFu, raise)) {
+                        // O of the tiles before is complete: these scores were issued after it
+                        const float f = raise ? ex2(m - top) : 1.0f;
+                        if (raise) m = top;
+                        l2 = mul2(l2, pack2(f, f));
+#pragma unroll 1
+                        for (int col = 0; col < D; col += 16) {
+                            uint32_t o[16];
+                            tmem_ld(tmem_o + col, o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st(tmem_o + col, o);
+                        }
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.0f : -m;
+                const f32x2 mm = pack2(mu, mu);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int at2 = 32 * q + 2 * k;
+                        const f32x2 e = ex2x2(fma2(pack2(__uint_as_float(r[at2]), __uint_as_float(r[at2 + 1])), cc, mm));
+                        l2 = add2(l2, e);
+                        float a, b;
+                        unpack2(e, a, b);
+                        pk[k] = pack_pair<F16>(a, b);
+                    }
+                    tmem_st(tmem_s + 16 * q, pk);
+                }
+                tmem_wait_st();
+            }
+            // Entries past the last key are whatever the page holds, and weight
+            // 0 times infinity is not 0: they are cleared, by the stream whose
+            // product reads the tile first.
+            if (key0 + PA_TILE > key_end && (!pair || w == 0 || last0 < m_tiles)) {
+                const int e = ring0 + ring_v(pair, i, m_tiles), s = e % S::STAGES;
+                pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
+                const int r0 = key_end - key0, per_slab = (PA_TILE - r0) * 8;
+#pragma unroll
+                for (int slab = 0; slab < S::SLABS; ++slab)
+                    for (int x = tid; x < per_slab; x += 128)
+                        *reinterpret_cast<uint4*>(ring + s * S::TILE_BYTES + slab * PA_SLAB_BYTES + r0 * 128 + x * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[w]);
+        }
+        ring0 += 2 * m_tiles;
+        float l;
+        {
+            float a, b;
+            unpack2(l2, a, b);
+            l = a + b;
+        }
+        if (pa_failed(&sh.err)) l = __int_as_float(0x7fc00000);
+
+        // What this warpgroup writes: a pair's stream its own rows' columns, a
+        // split item's one half of the columns of both streams' O (a warp's
+        // TMEM lanes are the same rows in either).
+        bool has[2] = {pair ? w == 0 && done > 0 : true, pair ? w == 1 && done > 0 : m_tiles > 1};
+        if (done > 0) {
+            pa_wait(&sh.o_full[w], o_count & 1, &sh.err);
+            ++o_count;
+            tc_fence_after();
+        }
+        float mt = m, lt = l, f[2];
+        f[0] = f[1] = l == 0.0f ? 0.0f : 1.0f;
+        if (!pair) {
+            sh.ml[w][tid] = make_float2(m, l);
+            tc_fence_before();
+            softmax_barrier();  // both streams' O is complete
+            tc_fence_after();
+            if (done == 0 && tid == 0) release_q(&sh.q_empty[buf], false);
+            const float2 other = sh.ml[w ^ 1][tid];
+            mt = fmaxf(m, other.x);
+            const float mine = l == 0.0f ? 0.0f : ex2(m - mt), theirs = other.y == 0.0f ? 0.0f : ex2(other.x - mt);
+            lt = l * mine + other.y * theirs;
+            f[0] = w == 0 ? mine : theirs;
+            f[1] = w == 0 ? theirs : mine;
+        }
+
+        const bool whole = t0 == 0 && t1 == c.tiles;
+        const int slot = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
+        const int cap_row = (pair ? w * PA_TILE : 0) + tid;
+        const float scale = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
+        if (warp_on) {
+            const int col0 = pair ? 0 : w * (D / 2), cols = pair ? D : D / 2;
+#pragma unroll 1
+            for (int col = col0; col < col0 + cols; col += 32) {
+                float x[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (!has[q]) continue;
+                    uint32_t o[32];
+                    tmem_ld(tmem_base + lanes + 2 * PA_TILE + q * D + col, o);
+                    // a row that a stream saw nothing of has no O there
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = f[q] == 0.0f ? x[k] : fmaf(__uint_as_float(o[k]), f[q], x[k]);
+                }
+                if (!at.valid) continue;
+                if (whole) {
+                    store_row<F16, 32>(P.out + at.token * P.o_ts + at.head * P.o_hs, col, x, scale);
+                } else {
+                    float4* part = reinterpret_cast<float4*>(P.part_o + ((size_t)slot * P.rows_cap + cap_row) * D + col);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) __stcg(part + k, make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+                }
+            }
+        }
+        if (at.valid && (pair || w == 0)) {
+            if (!whole) __stcg(P.part_ml + (size_t)slot * P.rows_cap + cap_row, make_float2(mt, lt));
+            else if (P.lse) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(mt, lt);
+        }
+        // O has been read (by both warpgroups, if both read it): the next
+        // item's products may overwrite it
+        tc_fence_before();
+        if (!pair) softmax_barrier();
+        if (!whole) {
+            int first_cta, pieces;
+            pieces_of(shares, c, first_cta, pieces);
+            __threadfence();
+            softmax_barrier();
+            if (pair && done == 0 && tid == 0) release_q(&sh.q_empty[buf], true);
+            if (threadIdx.x == 0) {
+                const uint32_t before = atomicAdd(P.counters + first_cta, 1u);
+                sh.last = before == (uint32_t)(pieces - 1);
+                if (sh.last) atomicExch(P.counters + first_cta, 0u);
+                __threadfence();
+            }
+            softmax_barrier();
+            if (sh.last) {
+                __threadfence();
+                join_pieces<D, F16>(P, c, first_cta, pieces);
+            }
+            softmax_barrier();  // sh.last is read before the next item writes it
+        }
+    }
+}
+
+// Rows of sequences that cannot be attended (flagged): zeros, lse -inf.
+__device__ __forceinline__ void clear_bad_rows(const PagedAttnParams& P, int D) {
+    for (int b = blockIdx.x; b < P.ch.B; b += gridDim.x) {
+        const Chunk s = load_chunk(P.ch, b);
+        if (s.ok || !s.rows_ok) continue;
+        const int pieces = D / 8;
+        for (long long x = threadIdx.x; x < (long long)s.n * P.Hq * pieces; x += PA_THREADS) {
+            const long long row = x / pieces;
+            const int64_t t = s.q0 + row / P.Hq, h = row % P.Hq;
+            *reinterpret_cast<uint4*>(P.out + t * P.o_ts + h * P.o_hs + (x % pieces) * 16) = make_uint4(0, 0, 0, 0);
+            if (P.lse && x % pieces == 0) P.lse[t * P.Hq + h] = -INFINITY;
+        }
+    }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(PA_THREADS, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ PagedAttnParams P) {
+    using S = PaShape<D>;
+    // 1024-byte alignment for the 128-byte swizzle atoms; nothing is static, so
+    // that this begins at the CTA's first byte
+    extern __shared__ __align__(1024) char smem[];
+    char* q_smem = smem;
+    char* ring = smem + 2 * S::TILE_BYTES;
+    PaShared& sh = *reinterpret_cast<PaShared*>(smem + S::TILES_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&sh.s_full[w], 1);
+            mbar_init(&sh.p_full[w], 4);   // a warp each
+            mbar_init(&sh.o_full[w], 1);
+            mbar_init(&sh.q_full[w], 2);   // the two query warps
+            mbar_init(&sh.q_empty[w], 2);  // release_q
+        }
+        mbar_init(&sh.mma_done, 1);
+        mbar_init(&sh.never, 1);
+        sh.err = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8 && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tm_v : &tm_k)) : "memory");
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&sh.tmem)), "r"(PA_TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    grid_dependency_wait();
+
+    Shares shares;
+    Cursor cur;
+    bool bad = false;
+    const bool work = find_share(P, sh, shares, cur, bad);
+    if (bad) clear_bad_rows(P, D);
+    if (work) {
+        if (P.test_wait_timeout && threadIdx.x == 0) {
+            // the failure path, tested: a barrier that nothing completes
+            if (!mbar_wait(&sh.never, 0, 64)) atomicExch(&sh.err, 1);
+        }
+        if (warp < 8) {
+            softmax_rows<D, F16>(P, sh, shares, cur, warp >> 2, q_smem, ring, tmem);
+        } else if (warp == 8) {
+            load_kv<D>(P, sh, cur, smem_u32(ring), &tm_k, &tm_v, lane);
+        } else if (warp == 9) {
+            if (lane == 0) {
+                issue_products<D, F16>(P, sh, cur, smem_u32(q_smem), smem_u32(ring), tmem);
+                // every product issued has completed before TMEM is released
+                mma_commit(&sh.mma_done);
+                (void)mbar_wait(&sh.mma_done, 0, PA_WAIT_LIMIT);
+            }
+        } else {
+            load_q<D>(P, sh, cur, q_smem, threadIdx.x - 320, lane);
+        }
+    }
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(PA_TMEM_COLS) : "memory");
+    }
+    if (threadIdx.x == 0 && sh.err) raise_flag(P.ch.status, SV_FLAG_TIMEOUT);
+}
+
+template <int D, bool F16>
+static cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p, int grid,
+                          cudaStream_t stream) {
+    auto kernel = paged_attention_kernel<D, F16>;
+    static std::atomic<int> attr_done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_done[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM<D>);
+        if (e != cudaSuccess) return e;
+        attr_done[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(PA_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = PA_SMEM<D>;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, p);
+}
+
+cudaError_t launch_paged_attention(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p, int D,
+                                   int f16, int sms, cudaStream_t stream) {
+    const int grid = sms < PA_MAX_CTAS ? sms : PA_MAX_CTAS;
+    if (D == 128) return f16 ? launch<128, true>(tm_k, tm_v, p, grid, stream) : launch<128, false>(tm_k, tm_v, p, grid, stream);
+    return f16 ? launch<64, true>(tm_k, tm_v, p, grid, stream) : launch<64, false>(tm_k, tm_v, p, grid, stream);
+}
+
+}  // namespace sv
