@@ -182,6 +182,10 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     const sv_kv_cache& c = a->cache;
     if (!a->cu_new || (a->T > 0 && (!a->q || !a->out))) return SV_ERR_NULL;
     if (a->T < 0 || !heads_ok(a->Hq, c.Hkv)) return SV_ERR_SHAPE;
+    const int G = a->Hq / c.Hkv, TT = sv::PA_TILE / G;
+    // the kernel counts key tiles of (sequence, head, row tile) items in int32
+    const double items = (std::ceil(a->T / (2.0 * TT)) + c.B) * c.Hkv;
+    if (items * (std::ceil((double)c.max_pages * c.page_size / sv::PA_TILE) + 1.0) > 2147483647.0) return SV_ERR_SHAPE;
     if (!std::isfinite(a->scale) || !(a->scale > 0.0f) || !std::isfinite(a->scale * 1.4426950408889634f)) return SV_ERR_CONFIG;
     if (a->flags & ~SV_ARG_TEST_WAIT_TIMEOUT) return SV_ERR_CONFIG;
     if ((st = check_tree(a->tree_parents, a->N)) != SV_OK) return st;
@@ -206,11 +210,11 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     p.o_ts = a->out_token_stride * 2, p.o_hs = a->out_head_stride * 2;
     p.lse = a->out_lse;
     p.Hq = a->Hq;
-    p.G = a->Hq / c.Hkv;
-    p.TT = sv::PA_TILE / p.G;
+    p.G = G;
+    p.TT = TT;
     while (p.box_shift < 7 && c.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
     p.c = a->scale * 1.4426950408889634f;
-    p.rows_cap = piece_rows(a->T, p.G);
+    p.rows_cap = piece_rows(a->T, G);
     char* ws = static_cast<char*>(a->workspace);
     p.counters = reinterpret_cast<uint32_t*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + SV_PAGED_WORKSPACE_HEAD);

@@ -30,8 +30,8 @@
 // item's pieces are written as (m, l, unscaled O) in fp32 and joined in order
 // by whichever CTA finishes last, so the result does not depend on timing.
 //
-// Warps: 0-3 and 4-7 softmax and output, 8 keys and values (TMA, one box per
-// page or 128 tokens), 9 the products, 10-11 queries (cp.async, any strides).
+// Warps: 0-3 and 4-7 softmax and output, 8 keys and 10 values (TMA, one box per
+// page or 128 tokens), 9 the products, 11 queries (cp.async, any strides).
 // Every mbarrier wait is bounded; one that gives up sets SV_FLAG_TIMEOUT, the
 // others stop waiting, no further work is issued, what was issued is waited
 // for, TMEM is freed and the rows concerned are NaN.
@@ -46,7 +46,7 @@ namespace sv {
 
 constexpr int PA_THREADS = 384;
 constexpr int PA_SOFTMAX_THREADS = 256;
-constexpr uint32_t PA_WAIT_LIMIT = 1u << 22;
+constexpr long long PA_WAIT_CYCLES = 1ll << 31;  // a wait gives up after about a second
 constexpr float PA_RAISE = 8.0f;                 // log2 of how far a score may pass m
 constexpr int PA_TMEM_COLS = 512;                // S0, S1 (128 columns each), O0, O1 (D each)
 constexpr int PA_SLAB_BYTES = PA_TILE * 128;     // 128 rows of 64 elements: one 128-byte-swizzled operand block
@@ -100,6 +100,17 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  ::"r"(smem_u32(bar))
                  : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -187,13 +198,19 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Waits for a phase; once any wait of the CTA has given up, all return at once.
-__device__ __forceinline__ void pa_wait(uint64_t* bar, uint32_t parity, int* err) {
-    if (mbar_try_wait(bar, parity)) return;
-    for (uint32_t i = 0; i < PA_WAIT_LIMIT; ++i) {
-        if (mbar_try_wait(bar, parity) || *(volatile int*)err) return;
+// Waits for a phase; gives up after PA_WAIT_CYCLES, or at once when any wait of
+// the CTA has given up and `err` is passed.
+__device__ __forceinline__ bool pa_wait_until(uint64_t* bar, uint32_t parity, const int* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long start = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (err && *(volatile const int*)err) return false;
+        if (clock64() - start > PA_WAIT_CYCLES) return mbar_try_wait(bar, parity);
     }
-    atomicExch(err, 1);
+    return true;
+}
+__device__ __forceinline__ void pa_wait(uint64_t* bar, uint32_t parity, int* err) {
+    if (!pa_wait_until(bar, parity, err)) atomicExch(err, 1);
 }
 __device__ __forceinline__ bool pa_failed(const int* err) { return *(volatile const int*)err != 0; }
 
@@ -206,23 +223,24 @@ __device__ __forceinline__ void softmax_barrier() {
 // Work: items in the order (sequence, kv head, row tile), each item its number
 // of key tiles long, laid end to end on one axis of W tiles.
 // ---------------------------------------------------------------------------
-// sum over i < n of floor((a i + b) / m)
-__device__ inline uint64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
-    uint64_t ans = 0;
+// sum over i < n of floor((a i + b) / m), by Euclid's algorithm on (a, m).
+// With TT a power of two the first turn ends it, by shifts.
+__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+    uint32_t m = PA_TILE, ans = 0;
     while (n > 0) {
         if (a >= m) {
-            ans += n * (n - 1) / 2 * (a / m);
+            ans += (uint32_t)((uint64_t)n * (n - 1) / 2) * (a / m);
             a %= m;
         }
         if (b >= m) {
             ans += n * (b / m);
             b %= m;
         }
-        const uint64_t y = a * n + b;
+        const uint64_t y = (uint64_t)a * n + b;
         if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const uint64_t t = m;
+        n = (uint32_t)(y / m);
+        b = (uint32_t)(y - (uint64_t)n * m);
+        const uint32_t t = m;
         m = a;
         a = t;
     }
@@ -235,17 +253,19 @@ __device__ __forceinline__ int tiles_of(int end) { return (int)(((long long)end 
 __device__ __forceinline__ int pairs_of(int n, int TT) { return n <= TT ? 1 : (n + 2 * TT - 1) / (2 * TT); }
 
 // Key tiles of one kv head's first p pairs (p < pairs: none of them the last).
-__device__ __forceinline__ long long tiles_before(int ctx, int TT, int p) {
-    return p == 0 ? 0 : (long long)floor_sum(p, PA_TILE, 2 * TT, (uint64_t)ctx + 2 * TT + PA_TILE - 1);
+__device__ __forceinline__ int tiles_before(int ctx, int TT, int p) {
+    return p == 0 ? 0 : (int)floor_sum(p, 2 * TT, (uint32_t)ctx + 2 * TT + PA_TILE - 1);
 }
-__device__ __forceinline__ long long tiles_per_head(int n, int ctx, int TT) {
+__device__ __forceinline__ int tiles_per_head(int n, int ctx, int TT) {
     return n == 0 ? 0 : tiles_before(ctx, TT, pairs_of(n, TT) - 1) + tiles_of(ctx + n);
 }
 
-// A walk over the items of a CTA's share, computed alike by every role.
+// A walk over the items of a CTA's share, computed alike by every role. Places
+// on the axis of tiles are int32: the host refuses batches whose bound on the
+// total is larger.
 struct Cursor {
-    long long begin, end;   // this CTA's share
-    long long u0;           // where the current item begins
+    int begin, end;         // this CTA's share
+    int u0;                 // where the current item begins
     int b, h, p;            // sequence, kv head, row-tile pair
     Chunk s;
     int tok0, ntok, tiles;  // the item's tokens within the chunk, its key tiles
@@ -259,7 +279,7 @@ struct Cursor {
     __device__ __forceinline__ void next(const PagedAttnParams& P) {
         u0 += tiles;
         if (u0 >= end) return;
-        if (++p == pairs_of(s.n, P.TT)) {
+        if (tok0 + ntok == s.n) {
             p = 0;
             if (++h == P.ch.Hkv) {
                 h = 0;
@@ -268,35 +288,42 @@ struct Cursor {
                     s = load_chunk(P.ch, ++b);
                 } while (b + 1 < P.ch.B && (!s.ok || s.n == 0));
             }
+        } else {
+            ++p;
         }
         set_item(P);
     }
     // the part of the item in this share
-    __device__ __forceinline__ int t0() const { return begin > u0 ? (int)(begin - u0) : 0; }
-    __device__ __forceinline__ int t1() const { return end - u0 < tiles ? (int)(end - u0) : tiles; }
+    __device__ __forceinline__ int t0() const { return max(begin - u0, 0); }
+    __device__ __forceinline__ int t1() const { return min(end - u0, tiles); }
     __device__ __forceinline__ bool pair(const PagedAttnParams& P) const { return ntok > P.TT; }
 };
 
-// Share boundaries: u_c = floor(c W / A), moved to the item's edge when it
-// falls within `snap` tiles of one (a piece of a few tiles costs more in
-// joining than the uneven share does).
+// CTA c's share begins at u_c: W = active * size + extra, the first `extra`
+// shares one tile longer. A boundary moves to an item's edge when it falls
+// within `snap` tiles of one: a piece of a few tiles costs more in joining
+// than the uneven share does.
 struct Shares {
-    long long W;
-    int active;   // CTAs with work
-    int snap;
+    int W, active, size, extra, snap;
+
+    __device__ __forceinline__ int begin(int c) const { return c * size + min(c, extra); }
+    // the first boundary at or past x > 0
+    __device__ __forceinline__ int first_at(int x) const {
+        const int longer = extra * (size + 1);
+        return x <= longer ? (x + size) / (size + 1) : extra + (x - longer + size - 1) / size;
+    }
 };
 // A CTA gets at least this many tiles: below that, joining costs more than
 // another CTA saves.
 constexpr int PA_MIN_SHARE = 2;
 
 struct PaShared {
-    long long scan[PA_THREADS / 32];
-    long long W;
-    int found_b[2];
-    long long found_pre[2];
+    int scan[PA_THREADS / 32];
+    int found_b[2], found_pre[2];
     Cursor at[2];
     uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2], mma_done, never;
     float2 ml[2][PA_TILE];
+    int loads[2][10];       // by producer and stage: phases of `full` up to its latest load
     uint32_t tmem;
     int last;
     int err;
@@ -305,25 +332,26 @@ template <int D>
 constexpr int PA_SMEM = PaShape<D>::TILES_BYTES + (int)sizeof(PaShared);
 static_assert(PA_SMEM<64> <= 227 * 1024 && PA_SMEM<128> <= 227 * 1024, "shared memory of one CTA");
 
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
+// Inclusive sums over the CTA's threads.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        const int t = __shfl_up_sync(0xFFFFFFFFu, v, o);
         if (lane >= o) v += t;
     }
-    __syncthreads();
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < PA_THREADS / 32; ++w) {
-        const long long x = warp_sums[w];
-        before += w < warp ? x : 0;
-        total += x;
-    }
-    return before + v;
+    const int mine = lane < PA_THREADS / 32 ? warp_sums[lane] : 0;
+    total = __reduce_add_sync(0xFFFFFFFFu, mine);
+    return v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? mine : 0);
+}
+
+__device__ __forceinline__ int sequence_tiles(const PagedAttnParams& P, int b, bool& bad) {
+    if (b >= P.ch.B) return 0;
+    const Chunk s = load_chunk(P.ch, b);
+    bad |= !s.ok;
+    return s.ok ? tiles_per_head(s.n, s.ctx, P.TT) * P.ch.Hkv : 0;
 }
 
 // Every thread: finds this CTA's share, and whether any sequence of the batch
@@ -331,72 +359,70 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& sh, Shares& shares, Cursor& cur, bool& bad) {
     const ChunkParams& ch = P.ch;
     const int tid = threadIdx.x;
-    long long W = 0, first_incl = 0, first = 0;
-    bool my_bad = false;
-    for (int base = 0; base < ch.B; base += PA_THREADS) {
-        const int b = base + tid;
-        long long mine = 0;
-        if (b < ch.B) {
-            const Chunk s = load_chunk(ch, b);
-            if (s.ok) {
-                mine = tiles_per_head(s.n, s.ctx, P.TT) * ch.Hkv;
-            } else {
-                my_bad = true;
-                if (blockIdx.x == 0) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
-            }
+    const bool one_turn = ch.B <= PA_THREADS;
+    int mine = sequence_tiles(P, tid, bad), W;
+    int incl = block_scan(mine, sh.scan, W);
+    if (!one_turn) {
+        for (int base = PA_THREADS; base < ch.B; base += PA_THREADS) {
+            int total;
+            __syncthreads();
+            block_scan(sequence_tiles(P, base + tid, bad), sh.scan, total);
+            W += total;
         }
-        long long total;
-        const long long incl = block_scan(mine, sh.scan, total);
-        if (base == 0) first_incl = incl, first = mine;
-        W += total;
     }
-    bad = __syncthreads_or(my_bad);
     shares.W = W;
-    const long long most = (W + PA_MIN_SHARE - 1) / PA_MIN_SHARE;
-    shares.active = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
-    if ((int)blockIdx.x >= shares.active) return false;
-    shares.snap = (int)(W / shares.active / 16);
-    const long long raw[2] = {(long long)blockIdx.x * W / shares.active, ((long long)blockIdx.x + 1) * W / shares.active};
-    long long run = 0;
+    shares.active = min((W + PA_MIN_SHARE - 1) / PA_MIN_SHARE, (int)gridDim.x);
+    const bool here = (int)blockIdx.x < shares.active;
+    int raw[2] = {0, 0};
+    if (here) {
+        shares.size = W / shares.active;
+        shares.extra = W - shares.size * shares.active;
+        shares.snap = shares.size / 16;
+        raw[0] = shares.begin(blockIdx.x);
+        raw[1] = shares.begin(blockIdx.x + 1);
+    }
+    int run = 0;
     for (int base = 0; base < ch.B; base += PA_THREADS) {
-        long long incl = first_incl, mine = first, total = 0;
-        const int b = base + tid;
-        if (ch.B > PA_THREADS) {
-            mine = 0;
-            if (b < ch.B) {
-                const Chunk s = load_chunk(ch, b);
-                if (s.ok) mine = tiles_per_head(s.n, s.ctx, P.TT) * ch.Hkv;
-            }
+        int total = 0;
+        if (!one_turn) {
+            bool again = false;
+            __syncthreads();
+            mine = sequence_tiles(P, base + tid, again);
             incl = block_scan(mine, sh.scan, total);
         }
-        const long long excl = run + incl - mine;
+        const int excl = run + incl - mine;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (raw[k] >= excl && raw[k] < excl + mine) {
-                sh.found_b[k] = b;
+                sh.found_b[k] = base + tid;
                 sh.found_pre[k] = excl;
             }
         run += total;
     }
-    __syncthreads();
+    bad = __syncthreads_or(bad);
+    if (bad && blockIdx.x == 0 && tid == 0) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
+    if (!here) return false;
     if ((tid & 31) == 0 && tid < 64) {
         const int k = tid >> 5;
         Cursor c;
+        c.begin = c.u0 = W;
         if (raw[k] < W) {
             c.b = sh.found_b[k];
             c.s = load_chunk(ch, c.b);
-            const long long per_head = tiles_per_head(c.s.n, c.s.ctx, P.TT);
-            const long long r = raw[k] - sh.found_pre[k];
-            c.h = (int)(r / per_head);
-            const long long in_head = r - c.h * per_head;
-            int lo = 0, hi = pairs_of(c.s.n, P.TT);
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (tiles_before(c.s.ctx, P.TT, mid) <= in_head) lo = mid;
-                else hi = mid;
+            const int pairs = pairs_of(c.s.n, P.TT);
+            const int per_head = tiles_per_head(c.s.n, c.s.ctx, P.TT), r = raw[k] - sh.found_pre[k];
+            c.h = r / per_head;
+            const int in_head = r - c.h * per_head;
+            // tiles_before(p) is close to p (ctx + TT + TT p) / 128: start
+            // from its root and step to the pair that holds in_head
+            c.p = 0;
+            if (pairs > 1) {
+                const float A = (float)P.TT, half = 0.5f * ((float)c.s.ctx + A);
+                c.p = min(pairs - 1, max(0, (int)((sqrtf(half * half + A * (float)in_head * PA_TILE) - half) / A)));
+                while (c.p > 0 && tiles_before(c.s.ctx, P.TT, c.p) > in_head) --c.p;
+                while (c.p + 1 < pairs && tiles_before(c.s.ctx, P.TT, c.p + 1) <= in_head) ++c.p;
             }
-            c.p = lo;
-            c.u0 = sh.found_pre[k] + c.h * per_head + tiles_before(c.s.ctx, P.TT, lo);
+            c.u0 = sh.found_pre[k] + c.h * per_head + tiles_before(c.s.ctx, P.TT, c.p);
             c.set_item(P);
             c.begin = raw[k];
             if (raw[k] - c.u0 <= shares.snap) {
@@ -406,8 +432,6 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
                 c.end = W;
                 c.next(P);
             }
-        } else {
-            c.begin = c.u0 = W;
         }
         sh.at[k] = c;
     }
@@ -420,11 +444,10 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
 // The pieces an item is cut into: the first boundary inside it (the item
 // begins in the CTA before) and how many pieces there are.
 __device__ __forceinline__ void pieces_of(const Shares& w, const Cursor& c, int& first_cta, int& pieces) {
-    const long long lo = c.u0 + w.snap + 1, hi = c.u0 + c.tiles - w.snap - 1;  // boundaries in [lo, hi] cut it
-    const long long c_lo = (lo * w.active + w.W - 1) / w.W;
-    const long long c_hi = ((hi + 1) * w.active + w.W - 1) / w.W - 1;
-    first_cta = (int)c_lo - 1;
-    pieces = (int)(c_hi - c_lo) + 2;
+    // boundaries from u0 + snap + 1 up to u0 + tiles - snap - 1 cut it
+    const int c_lo = w.first_at(c.u0 + w.snap + 1), c_end = w.first_at(c.u0 + c.tiles - w.snap);
+    first_cta = c_lo - 1;
+    pieces = c_end - c_lo + 1;
 }
 
 // Which ring entries (K and V tiles, in the order the products use them) tile
@@ -495,89 +518,79 @@ __device__ __forceinline__ RowPlace place_row(const PagedAttnParams& P, const Cu
     return x;
 }
 
-// Joins an item's pieces in their order, by the CTA that finished last: a warp
-// per row, a lane per piece for the weights and per D / 32 columns for O.
+// Joins an item's pieces in their order, by the CTA that finished last: 8
+// lanes per row, so that 32 rows' loads are in flight at once (a warp per row
+// spent 2 us on each: its loads waited for one another).
 template <int D, bool F16>
 __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Cursor& c, int first_cta, int pieces) {
-    constexpr int C = D / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int C = D / 32;  // float4s per lane
+    const int sub = threadIdx.x & 7;
     const bool pair = c.pair(P);
     const int rows0 = (pair ? P.TT : c.ntok) * P.G, rows = c.ntok * P.G;
-    for (int r = warp; r < rows; r += PA_SOFTMAX_THREADS / 32) {
+    const auto slot_of = [&](int f) { return (size_t)(f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f)); };
+    for (int r = threadIdx.x >> 3; r < rows; r += PA_SOFTMAX_THREADS / 8) {
         const int row = r < rows0 ? r : PA_TILE + r - rows0;
-        float M = -INFINITY, L = 0.0f, acc[C] = {};
-        for (int f0 = 0; f0 < pieces; f0 += 32) {
-            const int f = f0 + lane;
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (f < pieces) {
-                const int slot = f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f);
-                ml = __ldcg(P.part_ml + (size_t)slot * P.rows_cap + row);
-            }
-            float m = ml.x;
+        float M = -INFINITY;
+#pragma unroll 8
+        for (int f = 0; f < pieces; ++f) M = fmaxf(M, __ldcg(&P.part_ml[slot_of(f) * P.rows_cap + row].x));
+        float L = 0.0f;
+        float4 acc[C];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            m = fmaxf(m, M);
-            const float old = M == -INFINITY ? 0.0f : ex2(M - m);
-            const float w = ml.y == 0.0f ? 0.0f : ex2(ml.x - m);  // NaN stays NaN
-            float l = w * ml.y;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-            L = L * old + l;
-            M = m;
-#pragma unroll
-            for (int i = 0; i < C; ++i) acc[i] *= old;
-            const int here = min(32, pieces - f0);
+        for (int k = 0; k < C; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-            for (int k = 0; k < here; ++k) {
-                const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-                const int slot = f0 + k == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f0 + k);
-                const float* src = P.part_o + ((size_t)slot * P.rows_cap + row) * D + lane * C;
-                float x[C];
-                if constexpr (C == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-                    x[0] = v.x, x[1] = v.y;
-                }
-                // a piece that saw nothing of the row has weight 0 and no O
+        for (int f = 0; f < pieces; ++f) {
+            const size_t at = slot_of(f) * P.rows_cap + row;
+            const float2 ml = __ldcg(P.part_ml + at);
+            const float4* src = reinterpret_cast<const float4*>(P.part_o + at * D) + sub;
+            float4 x[C];
 #pragma unroll
-                for (int i = 0; i < C; ++i) acc[i] = wk == 0.0f ? acc[i] : fmaf(wk, x[i], acc[i]);
+            for (int k = 0; k < C; ++k) x[k] = __ldcg(src + 8 * k);
+            // a piece that saw nothing of the row has weight 0 and no O; NaN stays NaN
+            const float w = ml.y == 0.0f ? 0.0f : ex2(ml.x - M);
+            L = fmaf(w, ml.y, L);
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                acc[k].x = w == 0.0f ? acc[k].x : fmaf(w, x[k].x, acc[k].x);
+                acc[k].y = w == 0.0f ? acc[k].y : fmaf(w, x[k].y, acc[k].y);
+                acc[k].z = w == 0.0f ? acc[k].z : fmaf(w, x[k].z, acc[k].z);
+                acc[k].w = w == 0.0f ? acc[k].w : fmaf(w, x[k].w, acc[k].w);
             }
         }
         const RowPlace at = place_row(P, c, row / PA_TILE, row % PA_TILE);
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        char* dst = P.out + at.token * P.o_ts + at.head * P.o_hs + lane * C * 2;
-        if constexpr (C == 4) {
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_pair<F16>(acc[0] * inv, acc[1] * inv), pack_pair<F16>(acc[2] * inv, acc[3] * inv));
-        } else {
-            *reinterpret_cast<uint32_t*>(dst) = pack_pair<F16>(acc[0] * inv, acc[1] * inv);
-        }
-        if (P.lse && lane == 0) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M, L);
+        uint2* dst = reinterpret_cast<uint2*>(P.out + at.token * P.o_ts + at.head * P.o_hs) + sub;
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+            dst[8 * k] = make_uint2(pack_pair<F16>(acc[k].x * inv, acc[k].y * inv), pack_pair<F16>(acc[k].z * inv, acc[k].w * inv));
+        if (P.lse && sub == 0) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M, L);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Roles.
 // ---------------------------------------------------------------------------
-// Warp 8: keys and values. A tile is 128 / box boxes of `box` tokens (the
-// largest power of two that divides the page, at most 128) per 64 columns; a
-// lane issues one. A box past the piece's last key is not loaded. A page the
-// table does not have reads as zeros (a page coordinate past the last one).
-template <int D>
-__device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t ring, const CUtensorMap* tm_k,
-                                        const CUtensorMap* tm_v, int lane) {
+// Warps 8 and 10: keys and values. A tile is 128 / box boxes of `box` tokens
+// (the largest power of two that divides the page, at most 128) per 64
+// columns; a lane issues one. Issuing takes about 64 cycles a box, one lane
+// after another, so keys and values have a warp each: with pages of 16 one warp
+// for both issued a tile in 1.1 us of the 1.4 us that HBM takes to bring it
+// and held the kernel to 68 % of the copy rate. A box past the piece's last
+// key is not loaded. A page the table does not have reads as zeros (a page
+// coordinate past the last one).
+template <int D, bool IS_V>
+__device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t ring, const CUtensorMap* map,
+                                        int lane) {
     using S = PaShape<D>;
     const ChunkParams& ch = P.ch;
     const int box_shift = P.box_shift;
     const int my_box = lane / S::SLABS, my_slab = lane % S::SLABS;
     const bool has_box = my_box < (PA_TILE >> box_shift);
-    int it = 0;
+    const uint32_t my_dst = ring + my_slab * PA_SLAB_BYTES + (my_box << (box_shift + 7));
+    int ring0 = 0;
     bool stop = false;
     for (; c.valid() && !stop; c.next(P)) {
         const bool pair = c.pair(P);
-        const int t0 = c.t0(), m = c.t1() - t0, lead = pair ? 0 : 1;
+        const int t0 = c.t0(), m = c.t1() - t0;
         const int key_end = c.s.ctx + c.tok0 + c.ntok;
         const int32_t* table = ch.table + (int64_t)c.b * ch.table_stride;
         // page of this lane's box of tile t, and its first entry there
@@ -592,43 +605,31 @@ __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, 
             }
             return make_int2(page, key - page_no * ch.page_size);
         };
-        // pages of tiles i and i + 1, looked up a step ahead
-        int2 p0 = page_at(t0), p1 = page_at(t0 + 1);
-        for (int i = -lead; i < m && !stop; ++i) {
-#pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {  // K of tile i + lead, then V of tile i
-                const int t = kind == 0 ? i + lead : i;
-                if (t < 0 || t >= m || stop) continue;
-                const int2 pg = t > i && i >= 0 ? p1 : p0;
-                const int s = it % S::STAGES, n = it / S::STAGES;
-                if (n > 0) pa_wait(&sh.empty[s], (n - 1) & 1, &sh.err);
-                stop = __any_sync(0xFFFFFFFFu, pa_failed(&sh.err));
-                if (stop) continue;
-                ++it;
-                const int keys = min(key_end - (t0 + t) * PA_TILE, PA_TILE);
-                const int boxes = (keys + (1 << box_shift) - 1) >> box_shift;
-                if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * S::SLABS) << (box_shift + 7));
-                __syncwarp();
-                if (my_box < boxes)
-                    tma_load_4d(ring + s * S::TILE_BYTES + my_slab * PA_SLAB_BYTES + (my_box << (box_shift + 7)),
-                                kind == 0 ? tm_k : tm_v, my_slab * 64, pg.y, c.h, pg.x, &sh.full[s]);
+        int2 page = page_at(t0);
+        for (int i = 0; i < m && !stop; ++i) {
+            const int2 here = page;
+            if (i + 1 < m) page = page_at(t0 + i + 1);  // looked up a tile ahead
+            const int e = ring0 + (IS_V ? ring_v(pair, i, m) : ring_k(pair, i)), s = e % S::STAGES, n = e / S::STAGES;
+            if (n > 0) pa_wait(&sh.empty[s], (n - 1) & 1, &sh.err);
+            stop = __any_sync(0xFFFFFFFFu, pa_failed(&sh.err));
+            if (stop) continue;
+            const int keys = min(key_end - (t0 + i) * PA_TILE, PA_TILE);
+            const int boxes = (keys + (1 << box_shift) - 1) >> box_shift;
+            if (lane == 0) {
+                sh.loads[IS_V][s] = n + 1;
+                mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * S::SLABS) << (box_shift + 7));
             }
-            if (i >= 0) {
-                p0 = p1;
-                if (i + 2 < m) p1 = page_at(t0 + i + 2);
-            }
+            __syncwarp();
+            if (my_box < boxes) tma_load_4d(my_dst + s * S::TILE_BYTES, map, my_slab * 64, here.y, c.h, here.x, &sh.full[s]);
         }
+        ring0 += 2 * m;
     }
-    // every load issued has landed before the CTA ends: the last ones are the
-    // latest phases of their stages
-    for (int q = it - S::STAGES > 0 ? it - S::STAGES : 0; q < it; ++q)
-        (void)mbar_wait(&sh.full[q % S::STAGES], (q / S::STAGES) & 1, PA_WAIT_LIMIT);
 }
 
-// Warps 10 and 11: the rows of Q, 16 bytes per lane, into the swizzled K-major
-// layout (rows of 64 elements, 16-byte piece x at x ^ (row & 7)).
+// Warp 11: the rows of Q, 16 bytes per lane, into the swizzled K-major layout
+// (rows of 64 elements, 16-byte piece x at x ^ (row & 7)).
 template <int D>
-__device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, Cursor c, char* q_smem, int x0, int lane) {
+__device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, Cursor c, char* q_smem, int lane) {
     using S = PaShape<D>;
     constexpr int PIECES = D / 8;
     QueryBuffers qb;
@@ -643,7 +644,7 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, C
             const int rows = min(P.TT, c.tok0 + c.ntok - tok) * P.G;
             const uint32_t dst = smem_u32(q_smem + buf * S::TILE_BYTES);
             const char* src = P.q + (int64_t)(c.s.q0 + tok) * P.q_ts + (int64_t)(c.h * P.G) * P.q_hs;
-            for (int x = x0; x < rows * PIECES; x += 64) {
+            for (int x = lane; x < rows * PIECES; x += 32) {
                 const int r = x / PIECES, ch = x % PIECES;
                 const int i = r / P.G, g = r - i * P.G;
                 cp_async16(dst + (ch >> 3) * PA_SLAB_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
@@ -657,24 +658,28 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, C
     }
 }
 
-// Warp 9, one thread: the products. Both warpgroups' streams alternate, and
-// the scores of a stream's next tile are issued right after its O += P V, so
-// that they run while the other warpgroup computes its P.
+// Warp 9: the products. Both warpgroups' streams alternate, and the scores of
+// a stream's next tile are issued right after its O += P V, so that they run
+// while the other warpgroup computes its P. The whole warp walks the items and
+// one elected lane issues, with each operand's descriptor formed once per tile
+// and stepped by constants: what the instruction takes lives in uniform
+// registers, and forming every descriptor anew in one lane's branch took
+// longer (about 1000 cycles for 16 instructions) than the products themselves.
 template <int D, bool F16>
 __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t q_smem, uint32_t ring,
                                                uint32_t tmem) {
     using S = PaShape<D>;
     constexpr uint32_t ID_S = pa_idesc(F16, PA_TILE, false), ID_O = pa_idesc(F16, D, true);
+    const uint64_t q_desc = pa_desc(q_smem, 16, 1024), k_desc = pa_desc(ring, 16, 1024), v_desc = pa_desc(ring, PA_SLAB_BYTES, 1024);
     QueryBuffers qb;
     int ring0 = 0, p_count[2] = {0, 0};
     for (; c.valid(); c.next(P)) {
         const bool pair = c.pair(P);
         const int t0 = c.t0(), m = c.t1() - t0;
-        int buf[2], last[2];  // each stream's buffer; the first tile index past its tiles
+        int buf[2], last[2];  // each stream's query buffer; the first tile past its own
         if (pair) {
             buf[0] = 0, buf[1] = 1;
-            const int n0 = tiles_of(c.s.ctx + c.tok0 + P.TT) - t0;
-            last[0] = max(0, min(n0, m));
+            last[0] = max(0, min(tiles_of(c.s.ctx + c.tok0 + P.TT) - t0, m));
             last[1] = m;
             pa_wait(&sh.q_full[0], qb.uses[0]++ & 1, &sh.err);
             pa_wait(&sh.q_full[1], qb.uses[1]++ & 1, &sh.err);
@@ -688,16 +693,20 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
         auto scores = [&](int w, int i, bool done) {
             const int e = ring0 + ring_k(pair, i), s = e % S::STAGES;
             pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
-            if (pa_failed(&sh.err)) return;
+            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
             tc_fence_after();
-            const uint32_t a = q_smem + buf[w] * S::TILE_BYTES, b = ring + s * S::TILE_BYTES;
+            const uint64_t a = q_desc + (uint32_t)(buf[w] * (S::TILE_BYTES >> 4)), b = k_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
+            const uint32_t d = tmem + w * PA_TILE;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k / 4) * PA_SLAB_BYTES + (k % 4) * 32;
-                mma_ss(tmem + w * PA_TILE, pa_desc(a + off, 16, 1024), pa_desc(b + off, 16, 1024), ID_S, k != 0);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k / 4) * PA_SLAB_BYTES + (k % 4) * 32) >> 4;
+                    mma_ss(d, a + off, b + off, ID_S, k != 0);
+                }
+                mma_commit(&sh.s_full[w]);
+                if (done) mma_commit(&sh.empty[s]);
             }
-            mma_commit(&sh.s_full[w]);
-            if (done) mma_commit(&sh.empty[s]);
+            __syncwarp();
         };
         if (pair) {
             if (last[0] > 0) scores(0, 0, false);
@@ -712,17 +721,20 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
                 const int e = ring0 + ring_v(pair, i, m), s = e % S::STAGES;
                 pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
                 pa_wait(&sh.p_full[w], p_count[w]++ & 1, &sh.err);
-                if (pa_failed(&sh.err)) return;
+                if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
                 tc_fence_after();
-                const uint32_t b = ring + s * S::TILE_BYTES;
-                const bool first = i < step;
+                const uint64_t b = v_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
+                const uint32_t d = tmem + 2 * PA_TILE + w * D, a = tmem + w * PA_TILE;
+                const uint32_t add = i >= step;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < PA_TILE / 16; ++k)
-                    mma_ts(tmem + 2 * PA_TILE + w * D, tmem + w * PA_TILE + k * 8, pa_desc(b + k * 2048, PA_SLAB_BYTES, 1024), ID_O,
-                           !first || k != 0);
-                if (!pair || w == 1) mma_commit(&sh.empty[s]);
+                    for (int k = 0; k < PA_TILE / 16; ++k)
+                        mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, k != 0 ? 1 : add);
+                    if (!pair || w == 1) mma_commit(&sh.empty[s]);
+                    if (i + step >= last[w]) mma_commit(&sh.o_full[w]);
+                }
+                __syncwarp();
                 if (i + step < last[w]) scores(w, i + step, !pair || w == 1);
-                else mma_commit(&sh.o_full[w]);
             }
         }
         ring0 += 2 * m;
@@ -988,11 +1000,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             mbar_init(&sh.s_full[w], 1);
             mbar_init(&sh.p_full[w], 4);   // a warp each
             mbar_init(&sh.o_full[w], 1);
-            mbar_init(&sh.q_full[w], 2);   // the two query warps
+            mbar_init(&sh.q_full[w], 1);
             mbar_init(&sh.q_empty[w], 2);  // release_q
         }
         mbar_init(&sh.mma_done, 1);
         mbar_init(&sh.never, 1);
+        for (int s = 0; s < 10; ++s) sh.loads[0][s] = sh.loads[1][s] = 0;
         sh.err = 0;
         fence_barrier_init();
     }
@@ -1023,24 +1036,31 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (warp < 8) {
             softmax_rows<D, F16>(P, sh, shares, cur, warp >> 2, q_smem, ring, tmem);
         } else if (warp == 8) {
-            load_kv<D>(P, sh, cur, smem_u32(ring), &tm_k, &tm_v, lane);
+            load_kv<D, false>(P, sh, cur, smem_u32(ring), &tm_k, lane);
         } else if (warp == 9) {
-            if (lane == 0) {
-                issue_products<D, F16>(P, sh, cur, smem_u32(q_smem), smem_u32(ring), tmem);
-                // every product issued has completed before TMEM is released
-                mma_commit(&sh.mma_done);
-                (void)mbar_wait(&sh.mma_done, 0, PA_WAIT_LIMIT);
-            }
+            issue_products<D, F16>(P, sh, cur, smem_u32(q_smem), smem_u32(ring), tmem);
+            // every product issued has completed before TMEM is released
+            if (elect_one()) mma_commit(&sh.mma_done);
+            (void)pa_wait_until(&sh.mma_done, 0, nullptr);
+        } else if (warp == 10) {
+            load_kv<D, true>(P, sh, cur, smem_u32(ring), &tm_v, lane);
         } else {
-            load_q<D>(P, sh, cur, q_smem, threadIdx.x - 320, lane);
+            load_q<D>(P, sh, cur, q_smem, lane);
         }
     }
     __syncthreads();
+    // Every load issued has landed before the CTA ends: the products have used
+    // them all, unless a wait gave up.
+    if (work && sh.err && threadIdx.x < S::STAGES) {
+        const int n = max(sh.loads[0][threadIdx.x], sh.loads[1][threadIdx.x]);
+        if (n > 0) (void)pa_wait_until(&sh.full[threadIdx.x], (n - 1) & 1, nullptr);
+    }
     if (warp == 9) {
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(PA_TMEM_COLS) : "memory");
     }
+    __syncthreads();
     if (threadIdx.x == 0 && sh.err) raise_flag(P.ch.status, SV_FLAG_TIMEOUT);
 }
 

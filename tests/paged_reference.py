@@ -38,9 +38,9 @@ def make_table(need, n_pages, rng, max_pages=None):
 
 def entries(cache, table, b, slots, page):
     """[len(slots), Hkv, D] float64 of sequence b's entries."""
-    c = cache.detach().cpu().double()
     slots = np.asarray(slots, np.int64)
-    return c[torch.from_numpy(table[b, slots // page].astype(np.int64)), torch.from_numpy(slots % page)]
+    at = (torch.from_numpy(table[b, slots // page].astype(np.int64)), torch.from_numpy(slots % page))
+    return cache.detach()[tuple(x.to(cache.device) for x in at)].cpu().double()
 
 
 def path_to(parents, node):

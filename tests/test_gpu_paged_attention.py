@@ -119,6 +119,15 @@ def test_one_long_context_over_all_ctas():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("Hq,D,new", [(2, 64, 2), (3, 128, 1), (1, 128, 200)])
+def test_long_shares(Hq, D, new):
+    # a score of tiles per CTA: every stage of the pipeline is used many times
+    rng = np.random.default_rng(21)
+    seqs = [(int(rng.integers(6000, 12000)), new) for _ in range(45 if new < 10 else 6)]
+    c = Case(seqs, Hq=Hq, Hkv=1, D=D, page=16, seed=21, dirty=False)
+    c.check(c.run())
+
+
 def test_long_chunk_cut_into_pieces():
     c = Case([(5000, 70)], Hq=4, Hkv=1, D=64, seed=7)
     c.check(c.run())
