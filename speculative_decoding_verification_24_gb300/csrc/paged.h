@@ -53,12 +53,11 @@ struct KvCommitParams {
 
 struct PagedAttnParams {
     ChunkParams ch;
-    const char* q;
-    int64_t q_ts, q_hs;      // bytes
     char* out;
-    int64_t o_ts, o_hs;
+    int64_t o_ts, o_hs;      // bytes
     float* lse;              // [T, Hq] or nullptr
     int Hq, G, TT;           // G = Hq / Hkv; TT = tokens per 128-row tile
+    int q_box;               // tokens of one copy of queries, a divisor of TT
     int box_shift;           // log2 of the rows of one copy (page_size's power of two, at most 128)
     float c;                 // scale * log2(e)
     int rows_cap;            // rows of one partial in the workspace
@@ -70,8 +69,8 @@ struct PagedAttnParams {
 
 cudaError_t launch_kv_append(const KvAppendParams& p, int f16, int sms, cudaStream_t stream);
 cudaError_t launch_kv_commit(const KvCommitParams& p, cudaStream_t stream);
-cudaError_t launch_paged_attention(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p, int D,
-                                   int f16, int sms, cudaStream_t stream);
+cudaError_t launch_paged_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                   const PagedAttnParams& p, int D, int f16, int sms, cudaStream_t stream);
 
 // The library's record of a failed CUDA call on this host thread, and the
 // check that the current device is one it was built for (api.cu).

@@ -84,21 +84,39 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-// Map over one half of the cache, (D, entry of the page, head, page); a box is
-// 64 columns of `box` entries of one head, 128-byte swizzled.
-bool encode_cache(CUtensorMap* map, const sv_kv_cache& c, const void* base, int64_t page, int64_t token, int64_t head, int box) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
-    if (!encode) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.n_pages};
-    // a stride of an extent of 1 is never used, but has to be a valid one
-    const auto bytes = [](int64_t s, int extent) { return (cuuint64_t)(extent == 1 && s == 0 ? 16 : s * 2); };
-    const cuuint64_t strides[3] = {bytes(token, c.page_size), bytes(head, c.Hkv), bytes(page, c.n_pages)};
-    const cuuint32_t box_dims[4] = {64, (cuuint32_t)box, 1, 1};
+// A tensor map of the cache's type, 128-byte swizzled, in boxes of 64 columns.
+// A stride of an extent of 1 is never used, but has to be a valid one.
+bool encode(CUtensorMap* map, sv_dtype dtype, const void* base, int rank, const int64_t* extents, const int64_t* strides,
+            const int* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = get_encode();
+    if (!fn) return false;
+    cuuint64_t dims[4], bytes[3];
+    cuuint32_t boxes[4];
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return encode(map, c.dtype == SV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                  const_cast<void*>(base), dims, strides, box_dims, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    for (int i = 0; i < rank; ++i) {
+        dims[i] = (cuuint64_t)extents[i];
+        boxes[i] = (cuuint32_t)box[i];
+        if (i > 0) bytes[i - 1] = extents[i] == 1 && strides[i] == 0 ? 16 : (cuuint64_t)strides[i] * 2;
+    }
+    return fn(map, dtype == SV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+              const_cast<void*>(base), dims, bytes, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One half of the cache as (D, entry of the page, head, page); a box is `box`
+// entries of one head.
+bool encode_cache(CUtensorMap* map, const sv_kv_cache& c, const void* base, int64_t page, int64_t token, int64_t head, int box) {
+    const int64_t extents[4] = {c.D, c.page_size, c.Hkv, c.n_pages}, strides[4] = {1, token, head, page};
+    const int boxes[4] = {64, box, 1, 1};
+    return encode(map, c.dtype, base, 4, extents, strides, boxes);
+}
+
+// The queries as (D, head, token); a box is `tokens` tokens of one kv head's
+// `group` query heads, in the order of a tile's rows.
+bool encode_queries(CUtensorMap* map, const sv_paged_attention_args& a, int tokens, int group) {
+    const int64_t extents[3] = {a.cache.D, a.Hq, a.T}, strides[3] = {1, a.q_head_stride, a.q_token_stride};
+    const int boxes[3] = {64, group, tokens};
+    return encode(map, a.cache.dtype, a.q, 3, extents, strides, boxes);
 }
 
 // 2^64 times the fraction of a turn that w radians are.
@@ -195,6 +213,7 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     if (!stride_ok(a->q_token_stride) || !stride_ok(a->q_head_stride) || !stride_ok(a->out_token_stride) ||
         !stride_ok(a->out_head_stride))
         return SV_ERR_ALIGN;
+    if ((a->T > 1 && a->q_token_stride == 0) || (a->Hq > 1 && a->q_head_stride == 0)) return SV_ERR_SHAPE;
     if (a->T > 0 &&
         (!a->workspace || a->workspace_bytes < spec_paged_attention_workspace_bytes(a->T, a->Hq, c.Hkv, c.D)))
         return SV_ERR_WORKSPACE;
@@ -204,8 +223,6 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
 
     sv::PagedAttnParams p = {};
     p.ch = chunk_of(c, a->cu_new, a->T, a->tree_parents, a->N, a->status_word);
-    p.q = static_cast<const char*>(a->q);
-    p.q_ts = a->q_token_stride * 2, p.q_hs = a->q_head_stride * 2;
     p.out = static_cast<char*>(a->out);
     p.o_ts = a->out_token_stride * 2, p.o_hs = a->out_head_stride * 2;
     p.lse = a->out_lse;
@@ -220,11 +237,15 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     p.part_ml = reinterpret_cast<float2*>(ws + SV_PAGED_WORKSPACE_HEAD);
     p.part_o = reinterpret_cast<float*>(ws + SV_PAGED_WORKSPACE_HEAD + stats_bytes(p.rows_cap));
     p.test_wait_timeout = (a->flags & SV_ARG_TEST_WAIT_TIMEOUT) != 0;
-    CUtensorMap tm_k, tm_v;
-    if (!encode_cache(&tm_k, c, c.k, c.k_page_stride, c.k_token_stride, c.k_head_stride, 1 << p.box_shift) ||
+    // queries come in boxes of about as many tokens as a sequence has: one box
+    // for a token or a tile, and few rows of other sequences with them
+    const int mean = (int)(((int64_t)a->T + c.B - 1) / c.B);
+    for (p.q_box = mean < TT ? mean : TT; TT % p.q_box != 0;) --p.q_box;
+    CUtensorMap tm_q, tm_k, tm_v;
+    if (!encode_queries(&tm_q, *a, p.q_box, G) || !encode_cache(&tm_k, c, c.k, c.k_page_stride, c.k_token_stride, c.k_head_stride, 1 << p.box_shift) ||
         !encode_cache(&tm_v, c, c.v, c.v_page_stride, c.v_token_stride, c.v_head_stride, 1 << p.box_shift))
         return fail_cuda(cudaErrorInvalidValue);
-    const cudaError_t e = sv::launch_paged_attention(tm_k, tm_v, p, c.D, c.dtype == SV_F16, sms, (cudaStream_t)a->stream);
+    const cudaError_t e = sv::launch_paged_attention(tm_q, tm_k, tm_v, p, c.D, c.dtype == SV_F16, sms, (cudaStream_t)a->stream);
     return e == cudaSuccess ? SV_OK : fail_cuda(e);
 }
 

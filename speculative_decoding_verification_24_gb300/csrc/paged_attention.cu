@@ -31,7 +31,7 @@
 // by whichever CTA finishes last, so the result does not depend on timing.
 //
 // Warps: 0-3 and 4-7 softmax and output, 8 keys and 10 values (TMA, one box per
-// page or 128 tokens), 9 the products, 11 queries (cp.async, any strides).
+// page or 128 tokens), 9 the products, 11 queries (TMA).
 // Every mbarrier wait is bounded; one that gives up sets SV_FLAG_TIMEOUT, the
 // others stop waiting, no further work is issued, what was issued is waited
 // for, TMEM is freed and the rows concerned are NaN.
@@ -76,41 +76,48 @@ __host__ __device__ constexpr uint32_t pa_idesc(bool f16, int n, bool b_mn) {
            ((uint32_t)(PA_TILE >> 4) << 24);
 }
 
+// The products and commits are predicated, not branched to: `issue` is set in
+// one lane of a converged warp.
 // S = Q K^T: A and B from shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t issue) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(issue)
         : "memory");
 }
 
 // O += P V: A from TMEM.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t issue) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(issue)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t issue) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar)), "r"(issue)
+        : "memory");
 }
 
 // True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "elect.sync _|p, 0xFFFFFFFF;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(one));
-    return one != 0;
+    return one;
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -194,8 +201,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int head, int token, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // Waits for a phase; gives up after PA_WAIT_CYCLES, or at once when any wait of
@@ -319,11 +330,11 @@ constexpr int PA_MIN_SHARE = 2;
 
 struct PaShared {
     int scan[PA_THREADS / 32];
-    int found_b[2], found_pre[2];
     Cursor at[2];
-    uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2], mma_done, never;
+    uint64_t full[10], empty[10], s_full[2], p_half[2], p_full[2], o_full[2], q_full[2], q_empty[2], mma_done, never;
     float2 ml[2][PA_TILE];
     int loads[2][10];       // by producer and stage: phases of `full` up to its latest load
+    int q_loads[2];         // the same of q_full
     uint32_t tmem;
     int last;
     int err;
@@ -352,6 +363,45 @@ __device__ __forceinline__ int sequence_tiles(const PagedAttnParams& P, int b, b
     const Chunk s = load_chunk(P.ch, b);
     bad |= !s.ok;
     return s.ok ? tiles_per_head(s.n, s.ctx, P.TT) * P.ch.Hkv : 0;
+}
+
+// The item that holds place `raw`, in sequence b, whose items begin at `first`;
+// c.begin: raw, or the item's edge if that is near.
+__device__ __forceinline__ void place_boundary(const PagedAttnParams& P, const Shares& shares, int raw, int b, int first, Cursor& out) {
+    Cursor c;
+    c.b = b;
+    c.s = load_chunk(P.ch, b);
+    const int pairs = pairs_of(c.s.n, P.TT);
+    const int per_head = tiles_per_head(c.s.n, c.s.ctx, P.TT), r = raw - first;
+    c.h = r / per_head;
+    const int in_head = r - c.h * per_head;
+    c.p = 0;
+    int before = 0;
+    if (pairs > 1) {
+        // tiles_before(p) is close to p (ctx + TT + TT p) / 128: start from its
+        // root and step to the pair that holds in_head
+        const float A = (float)P.TT, half = 0.5f * ((float)c.s.ctx + A);
+        c.p = min(pairs - 1, max(0, (int)((sqrtf(half * half + A * (float)in_head * PA_TILE) - half) / A)));
+        before = tiles_before(c.s.ctx, P.TT, c.p);
+        while (before > in_head) before = tiles_before(c.s.ctx, P.TT, --c.p);
+        while (c.p + 1 < pairs) {
+            const int next = tiles_before(c.s.ctx, P.TT, c.p + 1);
+            if (next > in_head) break;
+            before = next;
+            ++c.p;
+        }
+    }
+    c.u0 = first + c.h * per_head + before;
+    c.set_item(P);
+    c.begin = raw;
+    c.end = shares.W;
+    if (raw - c.u0 <= shares.snap) {
+        c.begin = c.u0;
+    } else if (c.u0 + c.tiles - raw <= shares.snap) {
+        c.begin = c.u0 + c.tiles;
+        c.next(P);
+    }
+    out = c;
 }
 
 // Every thread: finds this CTA's share, and whether any sequence of the batch
@@ -391,51 +441,15 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
             incl = block_scan(mine, sh.scan, total);
         }
         const int excl = run + incl - mine;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 2; ++k)
-            if (raw[k] >= excl && raw[k] < excl + mine) {
-                sh.found_b[k] = base + tid;
-                sh.found_pre[k] = excl;
-            }
+            if (here && raw[k] >= excl && raw[k] < excl + mine) place_boundary(P, shares, raw[k], base + tid, excl, sh.at[k]);
         run += total;
     }
+    if (here && raw[1] == W && tid == 0) sh.at[1].begin = W;
     bad = __syncthreads_or(bad);
     if (bad && blockIdx.x == 0 && tid == 0) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
     if (!here) return false;
-    if ((tid & 31) == 0 && tid < 64) {
-        const int k = tid >> 5;
-        Cursor c;
-        c.begin = c.u0 = W;
-        if (raw[k] < W) {
-            c.b = sh.found_b[k];
-            c.s = load_chunk(ch, c.b);
-            const int pairs = pairs_of(c.s.n, P.TT);
-            const int per_head = tiles_per_head(c.s.n, c.s.ctx, P.TT), r = raw[k] - sh.found_pre[k];
-            c.h = r / per_head;
-            const int in_head = r - c.h * per_head;
-            // tiles_before(p) is close to p (ctx + TT + TT p) / 128: start
-            // from its root and step to the pair that holds in_head
-            c.p = 0;
-            if (pairs > 1) {
-                const float A = (float)P.TT, half = 0.5f * ((float)c.s.ctx + A);
-                c.p = min(pairs - 1, max(0, (int)((sqrtf(half * half + A * (float)in_head * PA_TILE) - half) / A)));
-                while (c.p > 0 && tiles_before(c.s.ctx, P.TT, c.p) > in_head) --c.p;
-                while (c.p + 1 < pairs && tiles_before(c.s.ctx, P.TT, c.p + 1) <= in_head) ++c.p;
-            }
-            c.u0 = sh.found_pre[k] + c.h * per_head + tiles_before(c.s.ctx, P.TT, c.p);
-            c.set_item(P);
-            c.begin = raw[k];
-            if (raw[k] - c.u0 <= shares.snap) {
-                c.begin = c.u0;
-            } else if (c.u0 + c.tiles - raw[k] <= shares.snap) {
-                c.begin = c.u0 + c.tiles;
-                c.end = W;
-                c.next(P);
-            }
-        }
-        sh.at[k] = c;
-    }
-    __syncthreads();
     cur = sh.at[0];
     cur.end = sh.at[1].begin;
     return cur.begin < cur.end;
@@ -476,6 +490,12 @@ struct QueryBuffers {
 __device__ __forceinline__ void release_q(uint64_t* bar, bool pair) {
     mbar_arrive(bar);
     if (pair) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {  // drops NaN, as fmaxf does
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 template <bool F16>
@@ -626,12 +646,16 @@ __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, 
     }
 }
 
-// Warp 11: the rows of Q, 16 bytes per lane, into the swizzled K-major layout
-// (rows of 64 elements, 16-byte piece x at x ^ (row & 7)).
+// Warp 11: the rows of Q, by boxes of q_box tokens x G heads x 64 columns,
+// which lie in shared memory as the rows of a tile do. q_box divides TT, so
+// no box passes the tile; rows past the item's are other tokens' or zeros,
+// and nothing is read from theirs. (A warp that copied the rows by 16 bytes
+// took 11 us for a pair's 64 KB, exposed at every item.)
 template <int D>
-__device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, Cursor c, char* q_smem, int lane) {
+__device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t q_smem, const CUtensorMap* map,
+                                       int lane) {
     using S = PaShape<D>;
-    constexpr int PIECES = D / 8;
+    const uint32_t box_bytes = (uint32_t)(P.q_box * P.G) * 128u;
     QueryBuffers qb;
     for (; c.valid(); c.next(P)) {
         const bool pair = c.pair(P);
@@ -640,102 +664,110 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, C
             const int buf = pair ? w : split_buf;
             const int n = qb.uses[buf]++;
             if (n > 0) pa_wait(&sh.q_empty[buf], (n - 1) & 1, &sh.err);
-            const int tok = c.tok0 + w * P.TT;
-            const int rows = min(P.TT, c.tok0 + c.ntok - tok) * P.G;
-            const uint32_t dst = smem_u32(q_smem + buf * S::TILE_BYTES);
-            const char* src = P.q + (int64_t)(c.s.q0 + tok) * P.q_ts + (int64_t)(c.h * P.G) * P.q_hs;
-            for (int x = lane; x < rows * PIECES; x += 32) {
-                const int r = x / PIECES, ch = x % PIECES;
-                const int i = r / P.G, g = r - i * P.G;
-                cp_async16(dst + (ch >> 3) * PA_SLAB_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                           src + i * P.q_ts + g * P.q_hs + ch * 16);
+            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
+            const int tok = c.tok0 + w * P.TT, boxes = (min(P.TT, c.tok0 + c.ntok - tok) + P.q_box - 1) / P.q_box;
+            if (lane == 0) {
+                sh.q_loads[buf] = n + 1;
+                mbar_arrive_expect_tx(&sh.q_full[buf], (uint32_t)(boxes * S::SLABS) * box_bytes);
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full[buf]);
+            const uint32_t dst = q_smem + buf * S::TILE_BYTES;
+            for (int x = lane; x < boxes * S::SLABS; x += 32) {
+                const int box = x / S::SLABS, slab = x % S::SLABS;
+                tma_load_3d(dst + slab * PA_SLAB_BYTES + box * box_bytes, map, slab * 64, c.h * P.G, c.s.q0 + tok + box * P.q_box,
+                            &sh.q_full[buf]);
+            }
         }
     }
 }
 
 // Warp 9: the products. Both warpgroups' streams alternate, and the scores of
 // a stream's next tile are issued right after its O += P V, so that they run
-// while the other warpgroup computes its P. The whole warp walks the items and
-// one elected lane issues, with each operand's descriptor formed once per tile
-// and stepped by constants: what the instruction takes lives in uniform
-// registers, and forming every descriptor anew in one lane's branch took
-// longer (about 1000 cycles for 16 instructions) than the products themselves.
+// while the other warpgroup computes its P. O += P V begins with the first
+// half of P. The instructions take their operands from uniform registers, so
+// the whole warp walks the items, one elected lane's predicate issues, and
+// what descriptors and branches come from passes through a warp reduction,
+// whose result is known to be uniform: with operands from a lane's registers
+// the 16 instructions of a tile took 1950 cycles to issue, twice what they
+// take to run.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xFFFFFFFFu, x); }
+
 template <int D, bool F16>
 __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t q_smem, uint32_t ring,
-                                               uint32_t tmem) {
+                                               uint32_t tmem_any, uint32_t issue) {
     using S = PaShape<D>;
     constexpr uint32_t ID_S = pa_idesc(F16, PA_TILE, false), ID_O = pa_idesc(F16, D, true);
+    constexpr int KS = PA_TILE / 16;
+    const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
     const uint64_t q_desc = pa_desc(q_smem, 16, 1024), k_desc = pa_desc(ring, 16, 1024), v_desc = pa_desc(ring, PA_SLAB_BYTES, 1024);
-    QueryBuffers qb;
-    int ring0 = 0, p_count[2] = {0, 0};
-    for (; c.valid(); c.next(P)) {
-        const bool pair = c.pair(P);
-        const int t0 = c.t0(), m = c.t1() - t0;
-        int buf[2], last[2];  // each stream's query buffer; the first tile past its own
-        if (pair) {
-            buf[0] = 0, buf[1] = 1;
-            last[0] = max(0, min(tiles_of(c.s.ctx + c.tok0 + P.TT) - t0, m));
-            last[1] = m;
-            pa_wait(&sh.q_full[0], qb.uses[0]++ & 1, &sh.err);
-            pa_wait(&sh.q_full[1], qb.uses[1]++ & 1, &sh.err);
-        } else {
-            buf[0] = buf[1] = qb.begin_split();
-            last[0] = last[1] = m;
-            pa_wait(&sh.q_full[buf[0]], qb.uses[buf[0]]++ & 1, &sh.err);
-        }
+    int ring0 = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0}, turn = 0;
+    for (; __any_sync(0xFFFFFFFFu, c.valid()); c.next(P)) {
+        const bool pair = __any_sync(0xFFFFFFFFu, c.pair(P));
+        const int m = uniform(c.t1() - c.t0());
+        // the first tile past each stream's own
+        const int last0 = pair ? max(0, min(uniform(tiles_of(c.s.ctx + c.tok0 + P.TT) - c.t0()), m)) : m;
         const int step = pair ? 1 : 2;
+        if (pair || turn == 0) {
+            pa_wait(&sh.q_full[0], q_phase[0], &sh.err);
+            q_phase[0] ^= 1;
+        }
+        if (pair || turn == 1) {
+            pa_wait(&sh.q_full[1], q_phase[1], &sh.err);
+            q_phase[1] ^= 1;
+        }
+        const int buf0 = pair ? 0 : turn, buf1 = pair ? 1 : turn;
+        if (!pair) turn ^= 1;
         // scores of stream w's tile i; `done`: nothing else will use K of tile i
         auto scores = [&](int w, int i, bool done) {
             const int e = ring0 + ring_k(pair, i), s = e % S::STAGES;
             pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
             if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
             tc_fence_after();
-            const uint64_t a = q_desc + (uint32_t)(buf[w] * (S::TILE_BYTES >> 4)), b = k_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
+            const uint64_t a = q_desc + (uint32_t)((w == 0 ? buf0 : buf1) * (S::TILE_BYTES >> 4));
+            const uint64_t b = k_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
             const uint32_t d = tmem + w * PA_TILE;
-            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k / 4) * PA_SLAB_BYTES + (k % 4) * 32) >> 4;
-                    mma_ss(d, a + off, b + off, ID_S, k != 0);
-                }
-                mma_commit(&sh.s_full[w]);
-                if (done) mma_commit(&sh.empty[s]);
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k / 4) * PA_SLAB_BYTES + (k % 4) * 32) >> 4;
+                mma_ss(d, a + off, b + off, ID_S, k != 0, issue);
             }
-            __syncwarp();
+            mma_commit(&sh.s_full[w], issue);
+            if (done) mma_commit(&sh.empty[s], issue);
         };
         if (pair) {
-            if (last[0] > 0) scores(0, 0, false);
+            if (last0 > 0) scores(0, 0, false);
             scores(1, 0, true);
         } else {
             scores(0, 0, true);
             if (m > 1) scores(1, 1, true);
         }
-        for (int i = 0; i < m; ++i) {
-            for (int w = pair ? 0 : i & 1; w < (pair ? 2 : (i & 1) + 1); ++w) {
-                if (i >= last[w]) continue;
-                const int e = ring0 + ring_v(pair, i, m), s = e % S::STAGES;
-                pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
-                pa_wait(&sh.p_full[w], p_count[w]++ & 1, &sh.err);
-                if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
-                tc_fence_after();
-                const uint64_t b = v_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
-                const uint32_t d = tmem + 2 * PA_TILE + w * D, a = tmem + w * PA_TILE;
-                const uint32_t add = i >= step;
-                if (elect_one()) {
+        // O += P V of stream w's tile i, then the scores of its next one
+        auto step_stream = [&](int w, int i, int last) {
+            const int e = ring0 + ring_v(pair, i, m), s = e % S::STAGES;
+            const int phase = p_phase[w];
+            p_phase[w] ^= 1;
+            pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
+            pa_wait(&sh.p_half[w], phase, &sh.err);
+            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
+            tc_fence_after();
+            const uint64_t b = v_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
+            const uint32_t d = tmem + 2 * PA_TILE + w * D, a = tmem + w * PA_TILE;
+            const uint32_t add = i >= step;
 #pragma unroll
-                    for (int k = 0; k < PA_TILE / 16; ++k)
-                        mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, k != 0 ? 1 : add);
-                    if (!pair || w == 1) mma_commit(&sh.empty[s]);
-                    if (i + step >= last[w]) mma_commit(&sh.o_full[w]);
-                }
-                __syncwarp();
-                if (i + step < last[w]) scores(w, i + step, !pair || w == 1);
-            }
+            for (int k = 0; k < KS / 2; ++k) mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, k != 0 ? 1 : add, issue);
+            pa_wait(&sh.p_full[w], phase, &sh.err);
+            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
+            tc_fence_after();
+#pragma unroll
+            for (int k = KS / 2; k < KS; ++k) mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, 1, issue);
+            if (!pair || w == 1) mma_commit(&sh.empty[s], issue);
+            if (i + step < last) scores(w, i + step, !pair || w == 1);
+            else mma_commit(&sh.o_full[w], issue);
+        };
+        for (int i = 0; i < m; ++i) {
+            if (pair ? i < last0 : (i & 1) == 0) step_stream(0, i, last0);
+            if (pair || (i & 1) == 1) step_stream(1, i, m);
+            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
         }
         ring0 += 2 * m;
     }
@@ -787,6 +819,20 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             const int key0 = (t0 + i) * PA_TILE;
             // this stream's last scores have been formed: it needs Q no more
             if (i + step >= last && tid == 0) release_q(&sh.q_empty[buf], pair);
+            // Entries past the last key are whatever the page holds, and weight
+            // 0 times infinity is not 0: they are cleared, by the stream whose
+            // product reads the tile first.
+            if (key0 + PA_TILE > key_end && (!pair || w == 0 || last0 < m_tiles)) {
+                const int e = ring0 + ring_v(pair, i, m_tiles), s = e % S::STAGES;
+                pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
+                const int r0 = key_end - key0, per_slab = (PA_TILE - r0) * 8;
+#pragma unroll
+                for (int slab = 0; slab < S::SLABS; ++slab)
+                    for (int x = tid; x < per_slab; x += 128)
+                        *reinterpret_cast<uint4*>(ring + s * S::TILE_BYTES + slab * PA_SLAB_BYTES + r0 * 128 + x * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
             if (warp_on) {
                 uint32_t r[PA_TILE];
                 tmem_ld(tmem_s, r);
@@ -809,8 +855,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
 #pragma unroll
                 for (int k = 0; k < PA_TILE; k += 8) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mx[j] = fmaxf(fmaxf(mx[j], __uint_as_float(r[k + 2 * j])), __uint_as_float(r[k + 2 * j + 1]));
+                    for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(r[k + 2 * j]), __uint_as_float(r[k + 2 * j + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.c;
                 if (done == 0) {
@@ -847,22 +892,16 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                         pk[k] = pack_pair<F16>(a, b);
                     }
                     tmem_st(tmem_s + 16 * q, pk);
+                    if (q == 1) {  // the product may begin with the first 64 keys
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.p_half[w]);
+                    }
                 }
                 tmem_wait_st();
-            }
-            // Entries past the last key are whatever the page holds, and weight
-            // 0 times infinity is not 0: they are cleared, by the stream whose
-            // product reads the tile first.
-            if (key0 + PA_TILE > key_end && (!pair || w == 0 || last0 < m_tiles)) {
-                const int e = ring0 + ring_v(pair, i, m_tiles), s = e % S::STAGES;
-                pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
-                const int r0 = key_end - key0, per_slab = (PA_TILE - r0) * 8;
-#pragma unroll
-                for (int slab = 0; slab < S::SLABS; ++slab)
-                    for (int x = tid; x < per_slab; x += 128)
-                        *reinterpret_cast<uint4*>(ring + s * S::TILE_BYTES + slab * PA_SLAB_BYTES + r0 * 128 + x * 16) =
-                            make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
+            } else if (lane == 0) {
+                mbar_arrive(&sh.p_half[w]);
             }
             tc_fence_before();
             __syncwarp();
@@ -979,8 +1018,8 @@ __device__ __forceinline__ void clear_bad_rows(const PagedAttnParams& P, int D) 
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(PA_THREADS, 1)
-    paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                           const __grid_constant__ PagedAttnParams P) {
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams P) {
     using S = PaShape<D>;
     // 1024-byte alignment for the 128-byte swizzle atoms; nothing is static, so
     // that this begins at the CTA's first byte
@@ -998,7 +1037,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&sh.s_full[w], 1);
-            mbar_init(&sh.p_full[w], 4);   // a warp each
+            mbar_init(&sh.p_half[w], 4);   // a warp each
+            mbar_init(&sh.p_full[w], 4);
             mbar_init(&sh.o_full[w], 1);
             mbar_init(&sh.q_full[w], 1);
             mbar_init(&sh.q_empty[w], 2);  // release_q
@@ -1006,11 +1046,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         mbar_init(&sh.mma_done, 1);
         mbar_init(&sh.never, 1);
         for (int s = 0; s < 10; ++s) sh.loads[0][s] = sh.loads[1][s] = 0;
+        sh.q_loads[0] = sh.q_loads[1] = 0;
         sh.err = 0;
         fence_barrier_init();
     }
-    if (warp == 8 && lane < 2)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tm_v : &tm_k)) : "memory");
+    if (warp == 8 && lane < 3)
+        asm volatile("prefetch.tensormap [%0];"
+                     ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &tm_k : lane == 1 ? &tm_v : &tm_q))
+                     : "memory");
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&sh.tmem)), "r"(PA_TMEM_COLS)
@@ -1038,14 +1081,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         } else if (warp == 8) {
             load_kv<D, false>(P, sh, cur, smem_u32(ring), &tm_k, lane);
         } else if (warp == 9) {
-            issue_products<D, F16>(P, sh, cur, smem_u32(q_smem), smem_u32(ring), tmem);
+            const uint32_t issue = elect_one();
+            issue_products<D, F16>(P, sh, cur, smem_u32(q_smem), smem_u32(ring), tmem, issue);
             // every product issued has completed before TMEM is released
-            if (elect_one()) mma_commit(&sh.mma_done);
+            mma_commit(&sh.mma_done, issue);
             (void)pa_wait_until(&sh.mma_done, 0, nullptr);
         } else if (warp == 10) {
             load_kv<D, true>(P, sh, cur, smem_u32(ring), &tm_v, lane);
         } else {
-            load_q<D>(P, sh, cur, q_smem, lane);
+            load_q<D>(P, sh, cur, smem_u32(q_smem), &tm_q, lane);
         }
     }
     __syncthreads();
@@ -1054,6 +1098,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     if (work && sh.err && threadIdx.x < S::STAGES) {
         const int n = max(sh.loads[0][threadIdx.x], sh.loads[1][threadIdx.x]);
         if (n > 0) (void)pa_wait_until(&sh.full[threadIdx.x], (n - 1) & 1, nullptr);
+        const int q = threadIdx.x < 2 ? sh.q_loads[threadIdx.x] : 0;
+        if (q > 0) (void)pa_wait_until(&sh.q_full[threadIdx.x], (q - 1) & 1, nullptr);
     }
     if (warp == 9) {
         __syncwarp();
@@ -1065,8 +1111,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 }
 
 template <int D, bool F16>
-static cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p, int grid,
-                          cudaStream_t stream) {
+static cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p,
+                          int grid, cudaStream_t stream) {
     auto kernel = paged_attention_kernel<D, F16>;
     static std::atomic<int> attr_done[64];
     int dev = 0;
@@ -1088,14 +1134,15 @@ static cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, p);
+    return cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_k, tm_v, p);
 }
 
-cudaError_t launch_paged_attention(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p, int D,
-                                   int f16, int sms, cudaStream_t stream) {
+cudaError_t launch_paged_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                   const PagedAttnParams& p, int D, int f16, int sms, cudaStream_t stream) {
     const int grid = sms < PA_MAX_CTAS ? sms : PA_MAX_CTAS;
-    if (D == 128) return f16 ? launch<128, true>(tm_k, tm_v, p, grid, stream) : launch<128, false>(tm_k, tm_v, p, grid, stream);
-    return f16 ? launch<64, true>(tm_k, tm_v, p, grid, stream) : launch<64, false>(tm_k, tm_v, p, grid, stream);
+    if (D == 128)
+        return f16 ? launch<128, true>(tm_q, tm_k, tm_v, p, grid, stream) : launch<128, false>(tm_q, tm_k, tm_v, p, grid, stream);
+    return f16 ? launch<64, true>(tm_q, tm_k, tm_v, p, grid, stream) : launch<64, false>(tm_q, tm_k, tm_v, p, grid, stream);
 }
 
 }  // namespace sv
