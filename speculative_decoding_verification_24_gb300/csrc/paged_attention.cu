@@ -717,12 +717,11 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
         }
         const int buf0 = pair ? 0 : turn, buf1 = pair ? 1 : turn;
         if (!pair) turn ^= 1;
-        // scores of stream w's tile i; `done`: nothing else will use K of tile i
+        auto wait_full = [&](int e) { pa_wait(&sh.full[e % S::STAGES], (e / S::STAGES) & 1, &sh.err); };
+        // scores of stream w's tile i, whose K is there; `done`: nothing else
+        // will use it
         auto scores = [&](int w, int i, bool done) {
-            const int e = ring0 + ring_k(pair, i), s = e % S::STAGES;
-            pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
-            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
-            tc_fence_after();
+            const int s = (ring0 + ring_k(pair, i)) % S::STAGES;
             const uint64_t a = q_desc + (uint32_t)((w == 0 ? buf0 : buf1) * (S::TILE_BYTES >> 4));
             const uint64_t b = k_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
             const uint32_t d = tmem + w * PA_TILE;
@@ -734,39 +733,44 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
             mma_commit(&sh.s_full[w], issue);
             if (done) mma_commit(&sh.empty[s], issue);
         };
-        if (pair) {
-            if (last0 > 0) scores(0, 0, false);
-            scores(1, 0, true);
-        } else {
-            scores(0, 0, true);
-            if (m > 1) scores(1, 1, true);
-        }
-        // O += P V of stream w's tile i, then the scores of its next one
+        // O += P V of stream w's tile i, then the scores of its next one. A wait
+        // takes about 100 cycles even for what is there: each is made once, and
+        // between products that keep the tensor cores busy meanwhile.
         auto step_stream = [&](int w, int i, int last) {
+            const bool alone = !pair || w == 1, first_of_pair = !pair || w == 0 || i >= last0;
             const int e = ring0 + ring_v(pair, i, m), s = e % S::STAGES;
             const int phase = p_phase[w];
             p_phase[w] ^= 1;
-            pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
+            if (first_of_pair) wait_full(e);
             pa_wait(&sh.p_half[w], phase, &sh.err);
-            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
             tc_fence_after();
             const uint64_t b = v_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
             const uint32_t d = tmem + 2 * PA_TILE + w * D, a = tmem + w * PA_TILE;
             const uint32_t add = i >= step;
 #pragma unroll
             for (int k = 0; k < KS / 2; ++k) mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, k != 0 ? 1 : add, issue);
+            if (i + step < last && (!pair || w == 0 || i + step >= last0)) wait_full(ring0 + ring_k(pair, i + step));
             pa_wait(&sh.p_full[w], phase, &sh.err);
-            if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
             tc_fence_after();
 #pragma unroll
             for (int k = KS / 2; k < KS; ++k) mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, 1, issue);
-            if (!pair || w == 1) mma_commit(&sh.empty[s], issue);
-            if (i + step < last) scores(w, i + step, !pair || w == 1);
+            if (alone) mma_commit(&sh.empty[s], issue);
+            if (i + step < last) scores(w, i + step, alone);
             else mma_commit(&sh.o_full[w], issue);
         };
+        wait_full(ring0);
+        tc_fence_after();
+        if (last0 > 0) scores(0, 0, !pair);
+        if (pair) {
+            scores(1, 0, true);
+        } else if (m > 1) {
+            wait_full(ring0 + ring_k(pair, 1));
+            scores(1, 1, true);
+        }
         for (int i = 0; i < m; ++i) {
             if (pair ? i < last0 : (i & 1) == 0) step_stream(0, i, last0);
             if (pair || (i & 1) == 1) step_stream(1, i, m);
+            // after a wait that gave up: what was issued read whatever was there
             if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
         }
         ring0 += 2 * m;
