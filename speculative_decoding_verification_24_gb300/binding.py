@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct as _struct
 import threading
 
 import torch
@@ -192,10 +193,10 @@ SIGNATURES = [
     ("spec_commit", I, [P, P, I, I, P, P, I, P, P]),
     ("spec_verify_lmhead_noalloc", I, [P, P, P, P, I, I, I, I, I, ctypes.c_float, I,
                                        ctypes.c_uint64, P, P, P]),
-    ("spec_kv_append", I, [ctypes.POINTER(sv_kv_append_args)]),
+    ("spec_kv_append", I, [P]),  # sv_kv_append_args*
     ("spec_paged_attention_workspace_bytes", ctypes.c_size_t, [I, I, I, I]),
-    ("spec_paged_attention", I, [ctypes.POINTER(sv_paged_attention_args)]),
-    ("spec_kv_commit", I, [ctypes.POINTER(sv_kv_cache), P, P, I, P, P, P, P]),
+    ("spec_paged_attention", I, [P]),  # sv_paged_attention_args*
+    ("spec_kv_commit", I, [P, P, P, I, P, P, P, P]),
     ("sv_kv_cache_size", ctypes.c_size_t, []),
     ("sv_kv_append_args_size", ctypes.c_size_t, []),
     ("sv_paged_attention_args_size", ctypes.c_size_t, []),
@@ -517,86 +518,101 @@ def spec_verify_lmhead_noalloc(hidden, W, draft_logits, draft_tokens, temperatur
 
 
 # ------------------------------------------------------ the paged cache
+#
+# These calls are short (a few microseconds on the GPU), so their arguments
+# are packed in one step instead of field by field.
 
 
+def _packer(struct):
+    """A struct.Struct of the native layout of a ctypes structure, whose
+    fields (nested ones in their place) are its arguments in order."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_uint32: "I", ctypes.c_float: "f",
+             ctypes.c_size_t: "N"}
+
+    def fields(st):
+        return "".join(fields(t) if issubclass(t, ctypes.Structure) else codes[t] for _, t in st._fields_)
+
+    packer = _struct.Struct("@" + fields(struct) + "0q")
+    assert packer.size == ctypes.sizeof(struct)
+    return packer.pack
+
+
+_pack_cache, _pack_append, _pack_attention = map(_packer, (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args))
 _KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+_I32 = torch.int32
 
 
-def _rows(t, name, heads=None, width=None, like=None):
-    """A [rows, heads, width] tensor of any token and head strides: its data
-    pointer and those strides."""
+def _rows(t, name, heads, width, dtype):
+    """Data pointer, token stride and head stride of a [rows, heads, width]
+    tensor (any number of heads when None) of any strides but the last."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != width or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {width}], got {list(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} like the cache, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != width:
-        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {width}], got {list(t.shape)}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype} like the cache, got {t.dtype}")
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     return t.data_ptr(), st, sh
 
 
-def _int32(t, name, shape):
+def _int32(t, name, *shape):
+    if t.dtype is not _I32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
 
-def _fill_cache(c, k_cache, v_cache, page_table, ctx_lens):
-    """Fills the sv_kv_cache c from k_cache and v_cache [n_pages, page_size,
+def _cache_fields(k_cache, v_cache, page_table, ctx_lens):
+    """The fields of sv_kv_cache from k_cache and v_cache [n_pages, page_size,
     Hkv, D] (any strides but the last), page_table [B, max_pages] and ctx_lens
     [B]."""
     if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
         raise ValueError("every tensor must live on a CUDA device")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, Hkv, D] and alike")
+    n_pages, page_size, Hkv, D = shape
     dtype = _KV_DTYPES.get(k_cache.dtype)
-    if dtype is None or v_cache.dtype != k_cache.dtype:
+    if dtype is None or v_cache.dtype is not k_cache.dtype:
         raise TypeError(f"the cache must be bfloat16 or float16, got {k_cache.dtype} and {v_cache.dtype}")
     kp, kt, kh, kd = k_cache.stride()
     vp, vt, vh, vd = v_cache.stride()
     if kd != 1 or vd != 1:
         raise ValueError("the cache must be contiguous in its last dimension")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
-        raise ValueError("page_table must be int32 [B, max_pages], contiguous in its last dimension")
+    if page_table.dtype is not _I32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
     B, max_pages = page_table.shape
-    c.k, c.v, c.dtype = k_cache.data_ptr(), v_cache.data_ptr(), dtype
-    c.n_pages, c.page_size, c.Hkv, c.D = k_cache.shape
-    c.B, c.max_pages = B, max_pages
-    c.k_page_stride, c.k_token_stride, c.k_head_stride = kp, kt, kh
-    c.v_page_stride, c.v_token_stride, c.v_head_stride = vp, vt, vh
-    c.page_table = page_table.data_ptr()
-    c.page_table_stride = page_table.stride(0) if B > 1 else max_pages
-    c.ctx_lens = _int32(ctx_lens, "ctx_lens", (B,))
-    return B
+    row, entry = page_table.stride()
+    if entry != 1 and max_pages > 1:
+        raise ValueError("page_table must be contiguous in its last dimension")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), dtype, n_pages, page_size, Hkv, D, B, kp, kt, kh, vp, vt, vh,
+            page_table.data_ptr(), row if B > 1 else max_pages, max_pages, _int32(ctx_lens, "ctx_lens", B))
 
 
 def _tree(tree_parents, B):
     if tree_parents is None:
-        return None, 0
+        return 0, 0
     N = tree_parents.shape[-1]
-    return _int32(tree_parents, "tree_parents", (B, N)), N
+    return _int32(tree_parents, "tree_parents", B, N), N
 
 
-class _on:
-    """The tensors' device made current, at no cost when it already is."""
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _call(name, device, stream, fn):
+    """fn(raw stream) with `device` current; raises on a status."""
+    index = device.index
+    current = torch.cuda.current_device()
+    if current == index:
+        st = fn(torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(_stream(stream, device))
+    if st:
+        _check(st, name)
 
 
 def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None, inv_freq=None, interleaved=False,
@@ -610,37 +626,35 @@ def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None,
     one); None leaves keys and queries as they are. tree_parents [B, N]: the
     chunk is a tree, a node's position its context plus its depth. positions
     [T] int32: rotary positions of the caller's own. Returns q_out."""
-    a = sv_kv_append_args()
-    B = _fill_cache(a.cache, k_cache, v_cache, page_table, ctx_lens)
-    Hkv, D = a.cache.Hkv, a.cache.D
-    T = a.T = k.shape[0]
+    cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
+    Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
+    T = k.shape[0]
     if v.shape[0] != T or (q is not None and q.shape[0] != T):
         raise ValueError("k, v and q must have the same number of rows")
-    a.cu_new = _int32(cu_new, "cu_new", (B + 1,))
-    a.k, a.k_token_stride, a.k_head_stride = _rows(k, "k", Hkv, D, k_cache)
-    a.v, a.v_token_stride, a.v_head_stride = _rows(v, "v", Hkv, D, k_cache)
+    kp, kt, kh = _rows(k, "k", Hkv, D, dtype)
+    vp, vt, vh = _rows(v, "v", Hkv, D, dtype)
+    Hq = qp = qt = qh = op = ot = oh = 0
     if q is not None:
-        a.q, a.q_token_stride, a.q_head_stride = _rows(q, "q", None, D, k_cache)
-        a.Hq = q.shape[1]
+        qp, qt, qh = _rows(q, "q", None, D, dtype)
+        Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(T, a.Hq, D, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
+            q_out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
+        elif q_out.shape[0] != T:
             raise ValueError(f"q_out must be {list(q.shape)}, got {list(q_out.shape)}")
-        a.q_out, a.q_out_token_stride, a.q_out_head_stride = _rows(q_out, "q_out", a.Hq, D, k_cache)
+        op, ot, oh = _rows(q_out, "q_out", Hq, D, dtype)
+    freq = rotary = 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous 1-D float64 CPU tensor")
-        a.inv_freq, a.rotary = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
-    a.interleaved = 1 if interleaved else 0
-    a.tree_parents, a.N = _tree(tree_parents, B)
-    if positions is not None:
-        a.positions = _int32(positions, "positions", (T,))
-    a.status_word = _ptr(status_word)
-    dev = k_cache.device
-    a.stream = _stream(stream, dev)
-    with _on(dev):
-        st = _load().spec_kv_append(ctypes.byref(a))
-    _check(st, "spec_kv_append")
+        freq, rotary = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    parents, N = _tree(tree_parents, B)
+    pos = 0 if positions is None else _int32(positions, "positions", T)
+    status = 0 if status_word is None else _ptr(status_word)
+    cu = _int32(cu_new, "cu_new", B + 1)
+    lib = _lib or _load()
+    _call("spec_kv_append", k_cache.device, stream, lambda raw: lib.spec_kv_append(_pack_append(
+        *cache, cu, T, kp, vp, kt, kh, vt, vh, Hq, qp, op, qt, qh, ot, oh, freq, rotary, 1 if interleaved else 0, parents, N,
+        pos, status, raw)))
     return q_out
 
 
@@ -665,6 +679,19 @@ def spec_paged_attention_workspace(T, Hq, Hkv, D, device="cuda"):
     return ws
 
 
+def _own_workspace(T, Hq, Hkv, D, device, stream):
+    """A workspace of this call alone, on its stream; None where there is none
+    (the call itself says why)."""
+    if T == 0 or spec_paged_attention_workspace_bytes(T, Hq, Hkv, D) == 0:
+        return None
+    if stream is None:
+        return spec_paged_attention_workspace(T, Hq, Hkv, D, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return spec_paged_attention_workspace(T, Hq, Hkv, D, device)
+
+
 def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scale=None, tree_parents=None, out=None,
                          out_lse=None, workspace=None, status_word=None, stream=None, flags=0):
     """Attention of a chunk's tokens (q [T, Hq, D], packed rows of any token
@@ -674,39 +701,30 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     default. out_lse [T, Hq] float32: the rows' log of the sum of exponentials.
     workspace: spec_paged_attention_workspace; made anew when None. Returns
     out."""
-    a = sv_paged_attention_args()
-    B = _fill_cache(a.cache, k_cache, v_cache, page_table, ctx_lens)
-    Hkv, D = a.cache.Hkv, a.cache.D
-    T = a.T = q.shape[0]
-    dev = k_cache.device
-    a.cu_new = _int32(cu_new, "cu_new", (B + 1,))
-    a.q, a.q_token_stride, a.q_head_stride = _rows(q, "q", None, D, k_cache)
-    Hq = a.Hq = q.shape[1]
+    cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
+    Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
+    qp, qt, qh = _rows(q, "q", None, D, dtype)
+    T, Hq = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
-    elif out.shape != q.shape:
+        out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
+    elif out.shape[0] != T:
         raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
-    a.out, a.out_token_stride, a.out_head_stride = _rows(out, "out", Hq, D, k_cache)
+    op, ot, oh = _rows(out, "out", Hq, D, dtype)
+    lse = 0
     if out_lse is not None:
-        if out_lse.dtype != torch.float32 or tuple(out_lse.shape) != (T, Hq):
+        if out_lse.dtype is not torch.float32 or out_lse.shape != (T, Hq):
             raise ValueError(f"out_lse must be float32 [{T}, {Hq}]")
-        a.out_lse = _ptr(out_lse)
-    a.scale = D ** -0.5 if scale is None else float(scale)
-    a.tree_parents, a.N = _tree(tree_parents, B)
-    with _on(dev):
-        a.stream = _stream(stream, dev)
-        if workspace is None and T > 0:
-            need = spec_paged_attention_workspace_bytes(T, Hq, Hkv, D)
-            if need:
-                with torch.cuda.stream(torch.cuda.ExternalStream(a.stream or 0, device=dev)):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-                    workspace[:SV_PAGED_WORKSPACE_HEAD].zero_()
-        if workspace is not None:
-            a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-        a.status_word = _ptr(status_word)
-        a.flags = int(flags)
-        st = _load().spec_paged_attention(ctypes.byref(a))
-    _check(st, "spec_paged_attention")
+        lse = _ptr(out_lse)
+    parents, N = _tree(tree_parents, B)
+    if workspace is None:
+        workspace = _own_workspace(T, Hq, Hkv, D, k_cache.device, stream)
+    ws, ws_bytes = (0, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+    status = 0 if status_word is None else _ptr(status_word)
+    cu = _int32(cu_new, "cu_new", B + 1)
+    scale = D ** -0.5 if scale is None else scale
+    lib = _lib or _load()
+    _call("spec_paged_attention", k_cache.device, stream, lambda raw: lib.spec_paged_attention(_pack_attention(
+        *cache, cu, T, Hq, qp, op, qt, qh, ot, oh, lse, scale, parents, N, ws, ws_bytes, status, int(flags), raw)))
     return out
 
 
@@ -717,15 +735,15 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     tensor), and with tree_parents [B, N] and last_node [B] (as
     spec_verify_tree takes and returns them) the kept path's entries moved
     behind the context. Returns out_lens."""
-    c = sv_kv_cache()
-    B = _fill_cache(c, k_cache, v_cache, page_table, ctx_lens)
+    cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
+    B = cache[7]
     if out_lens is None:
         out_lens = torch.empty_like(ctx_lens)
     parents, N = _tree(tree_parents, B)
-    last = None if last_node is None else _int32(last_node, "last_node", (B,))
-    dev = k_cache.device
-    with _on(dev):
-        st = _load().spec_kv_commit(ctypes.byref(c), _int32(n_accepted, "n_accepted", (B,)), parents, N, last,
-                                    _int32(out_lens, "out_lens", (B,)), _ptr(status_word), _stream(stream, dev))
-    _check(st, "spec_kv_commit")
+    last = None if last_node is None else _int32(last_node, "last_node", B)
+    n, lens = _int32(n_accepted, "n_accepted", B), _int32(out_lens, "out_lens", B)
+    status = None if status_word is None else _ptr(status_word)
+    lib = _lib or _load()
+    _call("spec_kv_commit", k_cache.device, stream, lambda raw: lib.spec_kv_commit(
+        _pack_cache(*cache), n, parents, N, last, lens, status, raw))
     return out_lens

@@ -55,6 +55,7 @@ struct PagedAttnParams {
     ChunkParams ch;
     char* out;
     int64_t o_ts, o_hs;      // bytes
+    bool wide_out;           // every output row starts on a multiple of 32 bytes
     float* lse;              // [T, Hq] or nullptr
     int Hq, G, TT;           // G = Hq / Hkv; TT = tokens per 128-row tile
     int q_box;               // tokens of one copy of queries, a divisor of TT
@@ -63,7 +64,7 @@ struct PagedAttnParams {
     int rows_cap;            // rows of one partial in the workspace
     uint32_t* counters;      // [PA_MAX_CTAS], zero between calls
     float2* part_ml;         // [2 * PA_MAX_CTAS, rows_cap]
-    float* part_o;           // [2 * PA_MAX_CTAS, rows_cap, D]
+    float* part_o;           // [2 * PA_MAX_CTAS, D / 4, rows_cap, 4]
     int test_wait_timeout;
 };
 

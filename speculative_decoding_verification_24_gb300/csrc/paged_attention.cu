@@ -137,17 +137,58 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+// Two such blocks at once.
+__device__ __forceinline__ void tmem_ld2(uint32_t ta, uint32_t tb, uint32_t (&a)[32], uint32_t (&b)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
         "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+          "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+          "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
+          "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]),
+          "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+          "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]),
+          "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]),
+          "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
+        : "r"(ta), "r"(tb)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld2(uint32_t ta, uint32_t tb, uint32_t (&a)[64], uint32_t (&b)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+          "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+          "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
+          "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]),
+          "=r"(a[32]), "=r"(a[33]), "=r"(a[34]), "=r"(a[35]), "=r"(a[36]), "=r"(a[37]), "=r"(a[38]), "=r"(a[39]),
+          "=r"(a[40]), "=r"(a[41]), "=r"(a[42]), "=r"(a[43]), "=r"(a[44]), "=r"(a[45]), "=r"(a[46]), "=r"(a[47]),
+          "=r"(a[48]), "=r"(a[49]), "=r"(a[50]), "=r"(a[51]), "=r"(a[52]), "=r"(a[53]), "=r"(a[54]), "=r"(a[55]),
+          "=r"(a[56]), "=r"(a[57]), "=r"(a[58]), "=r"(a[59]), "=r"(a[60]), "=r"(a[61]), "=r"(a[62]), "=r"(a[63]),
+          "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+          "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]),
+          "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]),
+          "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31]),
+          "=r"(b[32]), "=r"(b[33]), "=r"(b[34]), "=r"(b[35]), "=r"(b[36]), "=r"(b[37]), "=r"(b[38]), "=r"(b[39]),
+          "=r"(b[40]), "=r"(b[41]), "=r"(b[42]), "=r"(b[43]), "=r"(b[44]), "=r"(b[45]), "=r"(b[46]), "=r"(b[47]),
+          "=r"(b[48]), "=r"(b[49]), "=r"(b[50]), "=r"(b[51]), "=r"(b[52]), "=r"(b[53]), "=r"(b[54]), "=r"(b[55]),
+          "=r"(b[56]), "=r"(b[57]), "=r"(b[58]), "=r"(b[59]), "=r"(b[60]), "=r"(b[61]), "=r"(b[62]), "=r"(b[63])
+        : "r"(ta), "r"(tb)
         : "memory");
 }
 
@@ -234,28 +275,35 @@ __device__ __forceinline__ void softmax_barrier() {
 // Work: items in the order (sequence, kv head, row tile), each item its number
 // of key tiles long, laid end to end on one axis of W tiles.
 // ---------------------------------------------------------------------------
-// sum over i < n of floor((a i + b) / m), by Euclid's algorithm on (a, m).
-// With TT a power of two the first turn ends it, by shifts.
+// sum over i < n of floor((a i + b) / 128). With a = 2^k (TT a power of two)
+// the terms are floor((i + b / a) / q), q = 128 / a: runs of q equal ones.
+// Otherwise Euclid's algorithm on (a, m).
 __device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
-    uint32_t m = PA_TILE, ans = 0;
-    while (n > 0) {
-        if (a >= m) {
-            ans += (uint32_t)((uint64_t)n * (n - 1) / 2) * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            ans += n * (b / m);
-            b %= m;
-        }
+    const auto pairs_below = [](uint32_t x) { return (uint32_t)((uint64_t)x * (x - 1) / 2); };
+    uint32_t m = PA_TILE, ans = n * (b / m) + pairs_below(n) * (a / m);
+    a %= m;
+    b %= m;
+    if (a == 0 || n == 0) return ans;
+    if ((a & (a - 1)) == 0) {
+        const int k = 31 - __clz(a), q_shift = 7 - k;
+        const auto below = [&](uint32_t x) {  // sum over i < x of floor(i / q)
+            const uint32_t t = x >> q_shift;
+            return (pairs_below(t) << q_shift) + t * (x - (t << q_shift));
+        };
+        return ans + below(n + (b >> k)) - below(b >> k);
+    }
+    while (true) {
         const uint64_t y = (uint64_t)a * n + b;
-        if (y < m) break;
+        if (y < m) return ans;
         n = (uint32_t)(y / m);
         b = (uint32_t)(y - (uint64_t)n * m);
         const uint32_t t = m;
         m = a;
         a = t;
+        ans += n * (b / m) + pairs_below(n) * (a / m);
+        a %= m;
+        b %= m;
     }
-    return ans;
 }
 
 __device__ __forceinline__ int tiles_of(int end) { return (int)(((long long)end + PA_TILE - 1) / PA_TILE); }
@@ -314,6 +362,7 @@ struct Cursor {
 // shares one tile longer. A boundary moves to an item's edge when it falls
 // within `snap` tiles of one: a piece of a few tiles costs more in joining
 // than the uneven share does.
+constexpr int PA_SNAP = 3;
 struct Shares {
     int W, active, size, extra, snap;
 
@@ -331,6 +380,7 @@ constexpr int PA_MIN_SHARE = 2;
 struct PaShared {
     int scan[PA_THREADS / 32];
     Cursor at[2];
+    Shares shares;
     uint64_t full[10], empty[10], s_full[2], p_half[2], p_full[2], o_full[2], q_full[2], q_empty[2], mma_done, never;
     float2 ml[2][PA_TILE];
     int loads[2][10];       // by producer and stage: phases of `full` up to its latest load
@@ -358,22 +408,23 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     return v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? mine : 0);
 }
 
-__device__ __forceinline__ int sequence_tiles(const PagedAttnParams& P, int b, bool& bad) {
+__device__ __forceinline__ int sequence_tiles(const PagedAttnParams& P, int b, Chunk& s, bool& bad) {
     if (b >= P.ch.B) return 0;
-    const Chunk s = load_chunk(P.ch, b);
+    s = load_chunk(P.ch, b);
     bad |= !s.ok;
     return s.ok ? tiles_per_head(s.n, s.ctx, P.TT) * P.ch.Hkv : 0;
 }
 
 // The item that holds place `raw`, in sequence b, whose items begin at `first`;
 // c.begin: raw, or the item's edge if that is near.
-__device__ __forceinline__ void place_boundary(const PagedAttnParams& P, const Shares& shares, int raw, int b, int first, Cursor& out) {
+__device__ __forceinline__ void place_boundary(const PagedAttnParams& P, const Shares& shares, int raw, int b, const Chunk& s, int first,
+                                               int tiles, Cursor& out) {
     Cursor c;
     c.b = b;
-    c.s = load_chunk(P.ch, b);
-    const int pairs = pairs_of(c.s.n, P.TT);
-    const int per_head = tiles_per_head(c.s.n, c.s.ctx, P.TT), r = raw - first;
-    c.h = r / per_head;
+    c.s = s;
+    const int pairs = pairs_of(s.n, P.TT);
+    const int per_head = (int)((uint32_t)tiles / (uint32_t)P.ch.Hkv), r = raw - first;
+    c.h = (int)((uint32_t)r / (uint32_t)per_head);
     const int in_head = r - c.h * per_head;
     c.p = 0;
     int before = 0;
@@ -406,28 +457,30 @@ __device__ __forceinline__ void place_boundary(const PagedAttnParams& P, const S
 
 // Every thread: finds this CTA's share, and whether any sequence of the batch
 // is left out (bad). Returns false when there is no work here.
-__device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& sh, Shares& shares, Cursor& cur, bool& bad) {
+__device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& sh, bool& bad) {
     const ChunkParams& ch = P.ch;
     const int tid = threadIdx.x;
     const bool one_turn = ch.B <= PA_THREADS;
-    int mine = sequence_tiles(P, tid, bad), W;
+    Chunk s = {};
+    int mine = sequence_tiles(P, tid, s, bad), W;
     int incl = block_scan(mine, sh.scan, W);
     if (!one_turn) {
         for (int base = PA_THREADS; base < ch.B; base += PA_THREADS) {
             int total;
             __syncthreads();
-            block_scan(sequence_tiles(P, base + tid, bad), sh.scan, total);
+            block_scan(sequence_tiles(P, base + tid, s, bad), sh.scan, total);
             W += total;
         }
     }
+    Shares shares = {};
     shares.W = W;
     shares.active = min((W + PA_MIN_SHARE - 1) / PA_MIN_SHARE, (int)gridDim.x);
     const bool here = (int)blockIdx.x < shares.active;
     int raw[2] = {0, 0};
     if (here) {
-        shares.size = W / shares.active;
+        shares.size = (int)((uint32_t)W / (uint32_t)shares.active);
         shares.extra = W - shares.size * shares.active;
-        shares.snap = shares.size / 16;
+        shares.snap = max(shares.size / 16, PA_SNAP);
         raw[0] = shares.begin(blockIdx.x);
         raw[1] = shares.begin(blockIdx.x + 1);
     }
@@ -437,22 +490,31 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
         if (!one_turn) {
             bool again = false;
             __syncthreads();
-            mine = sequence_tiles(P, base + tid, again);
+            mine = sequence_tiles(P, base + tid, s, again);
             incl = block_scan(mine, sh.scan, total);
         }
         const int excl = run + incl - mine;
 #pragma unroll 1
         for (int k = 0; k < 2; ++k)
-            if (here && raw[k] >= excl && raw[k] < excl + mine) place_boundary(P, shares, raw[k], base + tid, excl, sh.at[k]);
+            if (here && raw[k] >= excl && raw[k] < excl + mine) place_boundary(P, shares, raw[k], base + tid, s, excl, mine, sh.at[k]);
         run += total;
     }
-    if (here && raw[1] == W && tid == 0) sh.at[1].begin = W;
+    if (tid == 0) {
+        if (here && raw[1] == W) sh.at[1].begin = W;
+        sh.shares = shares;
+    }
     bad = __syncthreads_or(bad);
     if (bad && blockIdx.x == 0 && tid == 0) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
     if (!here) return false;
-    cur = sh.at[0];
-    cur.end = sh.at[1].begin;
-    return cur.begin < cur.end;
+    return sh.at[0].begin < sh.at[1].begin;
+}
+
+// This CTA's share, as each role starts on it. Every role reads it for itself:
+// kept in registers across the branch, it cost the softmax threads spills.
+__device__ __forceinline__ Cursor share_of(const PaShared& sh) {
+    Cursor c = sh.at[0];
+    c.end = sh.at[1].begin;
+    return c;
 }
 
 // The pieces an item is cut into: the first boundary inside it (the item
@@ -498,6 +560,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {  // drops NaN
     return r;
 }
 
+__device__ __forceinline__ uint32_t add_release_acquire(uint32_t* p) {
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p) : "memory");
+    return before;
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     uint32_t r;
@@ -506,17 +574,25 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     return r;
 }
 
-// n values of one output row, scaled and rounded once, from column col on.
+// n values of one output row, scaled and rounded once, from column col on. A
+// lane's row is a line of its own, and a store costs the memory pipe a cycle
+// per line: 32 bytes at a time where rows allow it (`wide`).
 template <bool F16, int N>
-__device__ __forceinline__ void store_row(char* row, int col, const float (&x)[N], float scale) {
+__device__ __forceinline__ void store_row(char* row, int col, const float (&x)[N], float scale, bool wide) {
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int i = 0; i < N; i += 8) {
-        uint4 w;
-        w.x = pack_pair<F16>(x[i] * scale, x[i + 1] * scale);
-        w.y = pack_pair<F16>(x[i + 2] * scale, x[i + 3] * scale);
-        w.z = pack_pair<F16>(x[i + 4] * scale, x[i + 5] * scale);
-        w.w = pack_pair<F16>(x[i + 6] * scale, x[i + 7] * scale);
-        *reinterpret_cast<uint4*>(row + (col + i) * 2) = w;
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_pair<F16>(x[2 * i] * scale, x[2 * i + 1] * scale);
+    char* to = row + col * 2;
+    if (N >= 16 && wide) {
+#pragma unroll
+        for (int i = 0; i + 8 <= N / 2; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                         ::"l"(to + i * 4), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]),
+                           "r"(w[i + 6]), "r"(w[i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 4) *reinterpret_cast<uint4*>(to + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
 }
 
@@ -524,65 +600,107 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Where row r of the item's row tile w lives in the batch.
+// Where row (i, g) of a row tile, token i and head g of its group, lives in
+// the batch. Rows past TT * G are nobody's.
 struct RowPlace {
     int token, head;  // packed row of q and out, query head
     bool valid;
 };
-__device__ __forceinline__ RowPlace place_row(const PagedAttnParams& P, const Cursor& c, int tile, int r) {
+__device__ __forceinline__ RowPlace place_row(const PagedAttnParams& P, const Cursor& c, int tile, int i, int g) {
     RowPlace x;
-    const int i = r / P.G, in_chunk = c.tok0 + tile * P.TT + i;
+    const int in_chunk = c.tok0 + tile * P.TT + i;
     x.valid = i < P.TT && in_chunk < c.tok0 + c.ntok;
     x.token = c.s.q0 + in_chunk;
-    x.head = c.h * P.G + r % P.G;
+    x.head = c.h * P.G + g;
     return x;
 }
 
-// Joins an item's pieces in their order, by the CTA that finished last: 8
-// lanes per row, so that 32 rows' loads are in flight at once (a warp per row
-// spent 2 us on each: its loads waited for one another).
+// One piece's O is kept as [D / 4][rows] groups of 4 columns, so that lanes
+// that hold rows write and read neighbouring 16 bytes.
+__device__ __forceinline__ size_t part_at(const PagedAttnParams& P, int D, int slot, int row, int group) {
+    return ((size_t)slot * (D / 4) + group) * P.rows_cap + row;
+}
+
+// Joins an item's pieces in their order, by the CTA that finished last. A
+// thread takes 8 columns of a row over all pieces; with few rows several
+// lanes share them, each a contiguous run of the pieces, joined at the end.
+// One online pass: the loads of 4 pieces of 2 such units are in flight together.
 template <int D, bool F16>
 __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Cursor& c, int first_cta, int pieces) {
-    constexpr int C = D / 32;  // float4s per lane
-    const int sub = threadIdx.x & 7;
     const bool pair = c.pair(P);
-    const int rows0 = (pair ? P.TT : c.ntok) * P.G, rows = c.ntok * P.G;
-    const auto slot_of = [&](int f) { return (size_t)(f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f)); };
-    for (int r = threadIdx.x >> 3; r < rows; r += PA_SOFTMAX_THREADS / 8) {
-        const int row = r < rows0 ? r : PA_TILE + r - rows0;
-        float M = -INFINITY;
-#pragma unroll 8
-        for (int f = 0; f < pieces; ++f) M = fmaxf(M, __ldcg(&P.part_ml[slot_of(f) * P.rows_cap + row].x));
-        float L = 0.0f;
-        float4 acc[C];
+    const int rows0 = (pair ? P.TT : c.ntok) * P.G, rows = c.ntok * P.G, units = rows * (D / 8);
+    int share = 0;  // log2 of the lanes per unit
+    while (share < 5 && (units << share) < PA_SOFTMAX_THREADS && (2 << share) <= pieces) ++share;
+    const int per_lane = (pieces + (1 << share) - 1) >> share;
+    const int lane_of = threadIdx.x & ((1 << share) - 1);
+    const int f0 = lane_of * per_lane, f1 = min(f0 + per_lane, pieces);
+    constexpr int U = 2, F = 4;  // units and pieces whose loads are in flight together
+    const int stride = PA_SOFTMAX_THREADS >> share;
+    for (int base = 0; base < units; base += U * stride) {
+        int group[U], row[U];
+        bool on[U];
+        float M[U], L[U], acc[U][8];
 #pragma unroll
-        for (int k = 0; k < C; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int f = 0; f < pieces; ++f) {
-            const size_t at = slot_of(f) * P.rows_cap + row;
-            const float2 ml = __ldcg(P.part_ml + at);
-            const float4* src = reinterpret_cast<const float4*>(P.part_o + at * D) + sub;
-            float4 x[C];
+        for (int j = 0; j < U; ++j) {
+            const int u = base + j * stride + ((int)threadIdx.x >> share);
+            on[j] = u < units;
+            group[j] = on[j] ? u / rows : 0;
+            const int r = on[j] ? u - group[j] * rows : 0;
+            row[j] = r < rows0 ? r : PA_TILE + r - rows0;
+            M[j] = -INFINITY, L[j] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < C; ++k) x[k] = __ldcg(src + 8 * k);
-            // a piece that saw nothing of the row has weight 0 and no O; NaN stays NaN
-            const float w = ml.y == 0.0f ? 0.0f : ex2(ml.x - M);
-            L = fmaf(w, ml.y, L);
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-                acc[k].x = w == 0.0f ? acc[k].x : fmaf(w, x[k].x, acc[k].x);
-                acc[k].y = w == 0.0f ? acc[k].y : fmaf(w, x[k].y, acc[k].y);
-                acc[k].z = w == 0.0f ? acc[k].z : fmaf(w, x[k].z, acc[k].z);
-                acc[k].w = w == 0.0f ? acc[k].w : fmaf(w, x[k].w, acc[k].w);
-            }
+            for (int k = 0; k < 8; ++k) acc[j][k] = 0.0f;
         }
-        const RowPlace at = place_row(P, c, row / PA_TILE, row % PA_TILE);
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        uint2* dst = reinterpret_cast<uint2*>(P.out + at.token * P.o_ts + at.head * P.o_hs) + sub;
+#pragma unroll 1
+        for (int fb = f0; fb < f1; fb += F) {
+            float2 ml[U][F];
+            float4 a[U][F], b[U][F];
 #pragma unroll
-        for (int k = 0; k < C; ++k)
-            dst[8 * k] = make_uint2(pack_pair<F16>(acc[k].x * inv, acc[k].y * inv), pack_pair<F16>(acc[k].z * inv, acc[k].w * inv));
-        if (P.lse && sub == 0) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M, L);
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int k = 0; k < F; ++k) {
+                    const int f = fb + k, slot = f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f);
+                    ml[j][k] = make_float2(-INFINITY, 0.0f);
+                    a[j][k] = b[j][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (f < f1 && on[j]) {
+                        const float4* src = reinterpret_cast<const float4*>(P.part_o) + part_at(P, D, slot, row[j], 2 * group[j]);
+                        ml[j][k] = __ldcg(P.part_ml + (size_t)slot * P.rows_cap + row[j]);
+                        a[j][k] = __ldcg(src);
+                        b[j][k] = __ldcg(src + P.rows_cap);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int k = 0; k < F; ++k) {
+                    // a piece that saw nothing of the row has weight 0 and no O; NaN stays NaN
+                    const float m = fmaxf(M[j], ml[j][k].x);
+                    const float old = L[j] == 0.0f ? 0.0f : ex2(M[j] - m), w = ml[j][k].y == 0.0f ? 0.0f : ex2(ml[j][k].x - m);
+                    M[j] = m;
+                    L[j] = fmaf(w, ml[j][k].y, L[j] * old);
+                    const float x[8] = {a[j][k].x, a[j][k].y, a[j][k].z, a[j][k].w, b[j][k].x, b[j][k].y, b[j][k].z, b[j][k].w};
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) acc[j][q] = fmaf(w, w == 0.0f ? 0.0f : x[q], acc[j][q] * old);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            for (int o = 1; o < (1 << share); o <<= 1) {
+                const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M[j], o), l2 = __shfl_xor_sync(0xFFFFFFFFu, L[j], o);
+                const float m = fmaxf(M[j], m2);
+                const float w1 = L[j] == 0.0f ? 0.0f : ex2(M[j] - m), w2 = l2 == 0.0f ? 0.0f : ex2(m2 - m);
+                M[j] = m;
+                L[j] = L[j] * w1 + l2 * w2;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[j][k] = acc[j][k] * w1 + __shfl_xor_sync(0xFFFFFFFFu, acc[j][k], o) * w2;
+            }
+            if (!on[j] || lane_of != 0) continue;
+            const int r = row[j] % PA_TILE, i = r / P.G;
+            const RowPlace at = place_row(P, c, row[j] / PA_TILE, i, r - i * P.G);
+            store_row<F16, 8>(P.out + at.token * P.o_ts + at.head * P.o_hs, 8 * group[j], acc[j], L[j] == 0.0f ? 0.0f : 1.0f / L[j],
+                              false);
+            if (P.lse && group[j] == 0) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M[j], L[j]);
+        }
     }
 }
 
@@ -598,7 +716,7 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
 // key is not loaded. A page the table does not have reads as zeros (a page
 // coordinate past the last one).
 template <int D, bool IS_V>
-__device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t ring, const CUtensorMap* map,
+__device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, uint32_t ring, const CUtensorMap* map,
                                         int lane) {
     using S = PaShape<D>;
     const ChunkParams& ch = P.ch;
@@ -608,7 +726,7 @@ __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, 
     const uint32_t my_dst = ring + my_slab * PA_SLAB_BYTES + (my_box << (box_shift + 7));
     int ring0 = 0;
     bool stop = false;
-    for (; c.valid() && !stop; c.next(P)) {
+    for (Cursor c = share_of(sh); c.valid() && !stop; c.next(P)) {
         const bool pair = c.pair(P);
         const int t0 = c.t0(), m = c.t1() - t0;
         const int key_end = c.s.ctx + c.tok0 + c.ntok;
@@ -652,12 +770,12 @@ __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, 
 // and nothing is read from theirs. (A warp that copied the rows by 16 bytes
 // took 11 us for a pair's 64 KB, exposed at every item.)
 template <int D>
-__device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t q_smem, const CUtensorMap* map,
+__device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, uint32_t q_smem, const CUtensorMap* map,
                                        int lane) {
     using S = PaShape<D>;
     const uint32_t box_bytes = (uint32_t)(P.q_box * P.G) * 128u;
     QueryBuffers qb;
-    for (; c.valid(); c.next(P)) {
+    for (Cursor c = share_of(sh); c.valid(); c.next(P)) {
         const bool pair = c.pair(P);
         const int split_buf = pair ? 0 : qb.begin_split();
         for (int w = 0; w < (pair ? 2 : 1); ++w) {
@@ -693,7 +811,7 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, C
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xFFFFFFFFu, x); }
 
 template <int D, bool F16>
-__device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShared& sh, Cursor c, uint32_t q_smem, uint32_t ring,
+__device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShared& sh, uint32_t q_smem, uint32_t ring,
                                                uint32_t tmem_any, uint32_t issue) {
     using S = PaShape<D>;
     constexpr uint32_t ID_S = pa_idesc(F16, PA_TILE, false), ID_O = pa_idesc(F16, D, true);
@@ -701,7 +819,7 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
     const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
     const uint64_t q_desc = pa_desc(q_smem, 16, 1024), k_desc = pa_desc(ring, 16, 1024), v_desc = pa_desc(ring, PA_SLAB_BYTES, 1024);
     int ring0 = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0}, turn = 0;
-    for (; __any_sync(0xFFFFFFFFu, c.valid()); c.next(P)) {
+    for (Cursor c = share_of(sh); __any_sync(0xFFFFFFFFu, c.valid()); c.next(P)) {
         const bool pair = __any_sync(0xFFFFFFFFu, c.pair(P));
         const int m = uniform(c.t1() - c.t0());
         // the first tile past each stream's own
@@ -777,22 +895,38 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
     }
 }
 
+// Half of a row's columns, to the output or, of a cut item, to this CTA's piece.
+template <int D, bool F16>
+__device__ __forceinline__ void put_columns(const PagedAttnParams& P, const RowPlace& at, bool whole, int slot, int row, int col,
+                                            const float (&x)[D / 2]) {
+    if (!at.valid) return;
+    if (whole) {
+        store_row<F16, D / 2>(P.out + at.token * P.o_ts + at.head * P.o_hs, col, x, 1.0f, P.wide_out);
+    } else {
+        float4* part = reinterpret_cast<float4*>(P.part_o) + part_at(P, D, slot, row, col / 4);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+            __stcg(part + k * P.rows_cap, make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+    }
+}
+
 // Warps 0-3 (w = 0) and 4-7 (w = 1): softmax and output.
 template <int D, bool F16>
-__device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared& sh, const Shares& shares, Cursor c, int w,
+__device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared& sh, int w,
                                              char* q_smem, char* ring, uint32_t tmem_base) {
     using S = PaShape<D>;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, warp = tid >> 5;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t tmem_s = tmem_base + lanes + w * PA_TILE, tmem_o = tmem_base + lanes + 2 * PA_TILE + w * D;
+    const int row_token = tid / P.G, row_head = tid - row_token * P.G;
     QueryBuffers qb;
     int s_count = 0, o_count = 0, ring0 = 0;
     const f32x2 cc = pack2(P.c, P.c);
-    for (; c.valid(); c.next(P)) {
+    for (Cursor c = share_of(sh); c.valid(); c.next(P)) {
         const bool pair = c.pair(P);
         const int t0 = c.t0(), t1 = c.t1(), m_tiles = t1 - t0;
         const int key_end = c.s.ctx + c.tok0 + c.ntok;
-        const RowPlace at = place_row(P, c, pair ? w : 0, tid);
+        const RowPlace at = place_row(P, c, pair ? w : 0, row_token, row_head);
         const int tok_first = c.tok0 + (pair ? w * P.TT : 0);
         const int tile_rows = min(P.TT, c.tok0 + c.ntok - tok_first) * P.G;
         const bool warp_on = 32 * warp < tile_rows;
@@ -920,10 +1054,9 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         }
         if (pa_failed(&sh.err)) l = __int_as_float(0x7fc00000);
 
-        // What this warpgroup writes: a pair's stream its own rows' columns, a
+        // What this warpgroup writes: a pair's stream its own rows' columns, of a
         // split item's one half of the columns of both streams' O (a warp's
         // TMEM lanes are the same rows in either).
-        bool has[2] = {pair ? w == 0 && done > 0 : true, pair ? w == 1 && done > 0 : m_tiles > 1};
         if (done > 0) {
             pa_wait(&sh.o_full[w], o_count & 1, &sh.err);
             ++o_count;
@@ -950,29 +1083,23 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         const int cap_row = (pair ? w * PA_TILE : 0) + tid;
         const float scale = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
         if (warp_on) {
-            const int col0 = pair ? 0 : w * (D / 2), cols = pair ? D : D / 2;
-#pragma unroll 1
-            for (int col = col0; col < col0 + cols; col += 32) {
-                float x[32];
+            constexpr int C = D / 2;
+            const uint32_t o_base = tmem_base + lanes + 2 * PA_TILE;
+            uint32_t a[C], b[C];
+            tmem_ld2(pair ? tmem_o : o_base + w * C, pair ? tmem_o + C : o_base + D + w * C, a, b);
+            const float sa = f[0] * scale, sb = f[1] * scale;
+            float x[C];
+            // what a stream saw nothing of has no O there
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+            for (int k = 0; k < C; ++k) {
+                const float y = sa == 0.0f ? 0.0f : __uint_as_float(a[k]) * sa;
+                x[k] = pair || sb == 0.0f ? y : fmaf(__uint_as_float(b[k]), sb, y);
+            }
+            put_columns<D, F16>(P, at, whole, slot, cap_row, pair ? 0 : w * C, x);
+            if (pair) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (!has[q]) continue;
-                    uint32_t o[32];
-                    tmem_ld(tmem_base + lanes + 2 * PA_TILE + q * D + col, o);
-                    // a row that a stream saw nothing of has no O there
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = f[q] == 0.0f ? x[k] : fmaf(__uint_as_float(o[k]), f[q], x[k]);
-                }
-                if (!at.valid) continue;
-                if (whole) {
-                    store_row<F16, 32>(P.out + at.token * P.o_ts + at.head * P.o_hs, col, x, scale);
-                } else {
-                    float4* part = reinterpret_cast<float4*>(P.part_o + ((size_t)slot * P.rows_cap + cap_row) * D + col);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) __stcg(part + k, make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
-                }
+                for (int k = 0; k < C; ++k) x[k] = sb == 0.0f ? 0.0f : __uint_as_float(b[k]) * sb;
+                put_columns<D, F16>(P, at, whole, slot, cap_row, C, x);
             }
         }
         if (at.valid && (pair || w == 0)) {
@@ -985,21 +1112,18 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         if (!pair) softmax_barrier();
         if (!whole) {
             int first_cta, pieces;
-            pieces_of(shares, c, first_cta, pieces);
-            __threadfence();
-            softmax_barrier();
+            pieces_of(sh.shares, c, first_cta, pieces);
+            softmax_barrier();  // both warpgroups' rows are written
             if (pair && done == 0 && tid == 0) release_q(&sh.q_empty[buf], true);
             if (threadIdx.x == 0) {
-                const uint32_t before = atomicAdd(P.counters + first_cta, 1u);
+                // the barrier has brought every thread's rows to this one; its
+                // release passes them on, its acquire brings the others'
+                const uint32_t before = add_release_acquire(P.counters + first_cta);
                 sh.last = before == (uint32_t)(pieces - 1);
-                if (sh.last) atomicExch(P.counters + first_cta, 0u);
-                __threadfence();
+                if (sh.last) P.counters[first_cta] = 0;
             }
             softmax_barrier();
-            if (sh.last) {
-                __threadfence();
-                join_pieces<D, F16>(P, c, first_cta, pieces);
-            }
+            if (sh.last) join_pieces<D, F16>(P, c, first_cta, pieces);
             softmax_barrier();  // sh.last is read before the next item writes it
         }
     }
@@ -1070,30 +1194,34 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     const uint32_t tmem = sh.tmem;
     grid_dependency_wait();
 
-    Shares shares;
-    Cursor cur;
     bool bad = false;
-    const bool work = find_share(P, sh, shares, cur, bad);
+    const bool work = find_share(P, sh, bad);
     if (bad) clear_bad_rows(P, D);
     if (work) {
         if (P.test_wait_timeout && threadIdx.x == 0) {
             // the failure path, tested: a barrier that nothing completes
             if (!mbar_wait(&sh.never, 0, 64)) atomicExch(&sh.err, 1);
         }
+        // The CTA's registers, 384 x 168 at launch, move to the softmax threads:
+        // 256 x 208 + 128 x 88 is the same sum.
         if (warp < 8) {
-            softmax_rows<D, F16>(P, sh, shares, cur, warp >> 2, q_smem, ring, tmem);
-        } else if (warp == 8) {
-            load_kv<D, false>(P, sh, cur, smem_u32(ring), &tm_k, lane);
-        } else if (warp == 9) {
-            const uint32_t issue = elect_one();
-            issue_products<D, F16>(P, sh, cur, smem_u32(q_smem), smem_u32(ring), tmem, issue);
-            // every product issued has completed before TMEM is released
-            mma_commit(&sh.mma_done, issue);
-            (void)pa_wait_until(&sh.mma_done, 0, nullptr);
-        } else if (warp == 10) {
-            load_kv<D, true>(P, sh, cur, smem_u32(ring), &tm_v, lane);
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+            softmax_rows<D, F16>(P, sh, warp >> 2, q_smem, ring, tmem);
         } else {
-            load_q<D>(P, sh, cur, smem_u32(q_smem), &tm_q, lane);
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+            if (warp == 8) {
+                load_kv<D, false>(P, sh, smem_u32(ring), &tm_k, lane);
+            } else if (warp == 9) {
+                const uint32_t issue = elect_one();
+                issue_products<D, F16>(P, sh, smem_u32(q_smem), smem_u32(ring), tmem, issue);
+                // every product issued has completed before TMEM is released
+                mma_commit(&sh.mma_done, issue);
+                (void)pa_wait_until(&sh.mma_done, 0, nullptr);
+            } else if (warp == 10) {
+                load_kv<D, true>(P, sh, smem_u32(ring), &tm_v, lane);
+            } else {
+                load_q<D>(P, sh, smem_u32(q_smem), &tm_q, lane);
+            }
         }
     }
     __syncthreads();
