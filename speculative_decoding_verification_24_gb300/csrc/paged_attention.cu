@@ -233,12 +233,21 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
         : "memory");
 }
 
+// A split item's keys and values are read once: marked to be evicted first,
+// they do not push the kernel's own code out of L2. A pair's are read again by
+// the CTAs of the chunk's other rows.
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int token, int head, int page,
-                                            uint64_t* bar) {
+                                            uint64_t* bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 
@@ -278,7 +287,7 @@ __device__ __forceinline__ void softmax_barrier() {
 // sum over i < n of floor((a i + b) / 128). With a = 2^k (TT a power of two)
 // the terms are floor((i + b / a) / q), q = 128 / a: runs of q equal ones.
 // Otherwise Euclid's algorithm on (a, m).
-__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+__device__ __noinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
     const auto pairs_below = [](uint32_t x) { return (uint32_t)((uint64_t)x * (x - 1) / 2); };
     uint32_t m = PA_TILE, ans = n * (b / m) + pairs_below(n) * (a / m);
     a %= m;
@@ -319,6 +328,17 @@ __device__ __forceinline__ int tiles_per_head(int n, int ctx, int TT) {
     return n == 0 ? 0 : tiles_before(ctx, TT, pairs_of(n, TT) - 1) + tiles_of(ctx + n);
 }
 
+// The next sequence after b that has work; b becomes its number.
+__device__ __forceinline__ Chunk next_chunk(const ChunkParams& ch, int& b) {
+    Chunk s;
+    int at = b;
+    do {
+        s = load_chunk(ch, ++at);
+    } while (at + 1 < ch.B && (!s.ok || s.n == 0));
+    b = at;
+    return s;
+}
+
 // A walk over the items of a CTA's share, computed alike by every role. Places
 // on the axis of tiles are int32: the host refuses batches whose bound on the
 // total is larger.
@@ -343,9 +363,7 @@ struct Cursor {
             if (++h == P.ch.Hkv) {
                 h = 0;
                 // u0 < end <= W, so a later sequence has work
-                do {
-                    s = load_chunk(P.ch, ++b);
-                } while (b + 1 < P.ch.B && (!s.ok || s.n == 0));
+                s = next_chunk(P.ch, b);
             }
         } else {
             ++p;
@@ -715,15 +733,16 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
 // and held the kernel to 68 % of the copy rate. A box past the piece's last
 // key is not loaded. A page the table does not have reads as zeros (a page
 // coordinate past the last one).
-template <int D, bool IS_V>
+template <int D>
 __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, uint32_t ring, const CUtensorMap* map,
-                                        int lane) {
+                                        bool is_v, int lane) {
     using S = PaShape<D>;
     const ChunkParams& ch = P.ch;
     const int box_shift = P.box_shift;
     const int my_box = lane / S::SLABS, my_slab = lane % S::SLABS;
     const bool has_box = my_box < (PA_TILE >> box_shift);
     const uint32_t my_dst = ring + my_slab * PA_SLAB_BYTES + (my_box << (box_shift + 7));
+    const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
     int ring0 = 0;
     bool stop = false;
     for (Cursor c = share_of(sh); c.valid() && !stop; c.next(P)) {
@@ -747,18 +766,19 @@ __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, 
         for (int i = 0; i < m && !stop; ++i) {
             const int2 here = page;
             if (i + 1 < m) page = page_at(t0 + i + 1);  // looked up a tile ahead
-            const int e = ring0 + (IS_V ? ring_v(pair, i, m) : ring_k(pair, i)), s = e % S::STAGES, n = e / S::STAGES;
+            const int e = ring0 + (is_v ? ring_v(pair, i, m) : ring_k(pair, i)), s = e % S::STAGES, n = e / S::STAGES;
             if (n > 0) pa_wait(&sh.empty[s], (n - 1) & 1, &sh.err);
             stop = __any_sync(0xFFFFFFFFu, pa_failed(&sh.err));
             if (stop) continue;
             const int keys = min(key_end - (t0 + i) * PA_TILE, PA_TILE);
             const int boxes = (keys + (1 << box_shift) - 1) >> box_shift;
             if (lane == 0) {
-                sh.loads[IS_V][s] = n + 1;
+                sh.loads[is_v][s] = n + 1;
                 mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * S::SLABS) << (box_shift + 7));
             }
             __syncwarp();
-            if (my_box < boxes) tma_load_4d(my_dst + s * S::TILE_BYTES, map, my_slab * 64, here.y, c.h, here.x, &sh.full[s]);
+            if (my_box < boxes)
+                tma_load_4d(my_dst + s * S::TILE_BYTES, map, my_slab * 64, here.y, c.h, here.x, &sh.full[s], pair ? again : once);
         }
         ring0 += 2 * m;
     }
@@ -818,7 +838,7 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
     constexpr int KS = PA_TILE / 16;
     const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
     const uint64_t q_desc = pa_desc(q_smem, 16, 1024), k_desc = pa_desc(ring, 16, 1024), v_desc = pa_desc(ring, PA_SLAB_BYTES, 1024);
-    int ring0 = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0}, turn = 0;
+    int ring0 = 0, p_phase = 0, q_phase[2] = {0, 0}, turn = 0;
     for (Cursor c = share_of(sh); __any_sync(0xFFFFFFFFu, c.valid()); c.next(P)) {
         const bool pair = __any_sync(0xFFFFFFFFu, c.pair(P));
         const int m = uniform(c.t1() - c.t0());
@@ -836,58 +856,54 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
         const int buf0 = pair ? 0 : turn, buf1 = pair ? 1 : turn;
         if (!pair) turn ^= 1;
         auto wait_full = [&](int e) { pa_wait(&sh.full[e % S::STAGES], (e / S::STAGES) & 1, &sh.err); };
-        // scores of stream w's tile i, whose K is there; `done`: nothing else
-        // will use it
-        auto scores = [&](int w, int i, bool done) {
-            const int s = (ring0 + ring_k(pair, i)) % S::STAGES;
-            const uint64_t a = q_desc + (uint32_t)((w == 0 ? buf0 : buf1) * (S::TILE_BYTES >> 4));
-            const uint64_t b = k_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
-            const uint32_t d = tmem + w * PA_TILE;
+        // Stream w's step i: O += P V of its tile i, then the scores of its
+        // next one; the first steps have only the latter. A wait takes about
+        // 100 cycles even for what is there: each is made once, and between
+        // products that keep the tensor cores busy meanwhile.
+        for (int i = -step; i < m; ++i) {
+            const int w0 = pair ? 0 : i & 1, w1 = pair ? 1 : i & 1;
+#pragma unroll 1
+            for (int w = w0; w <= w1; ++w) {
+                const int last = w == 0 ? last0 : m, next = i + step;
+                const bool values = i >= 0 && i < last, keys = next < last;
+                // the last use of a tile's keys or values by any stream, and the first
+                const bool alone = !pair || w == 1;
+                const int ev = ring0 + ring_v(pair, i, m), sv = ev % S::STAGES;
+                const int ek = ring0 + ring_k(pair, next), sk = ek % S::STAGES;
+                const uint64_t b = v_desc + (uint32_t)(sv * (S::TILE_BYTES >> 4));
+                const uint32_t o = tmem + 2 * PA_TILE + w * D, p = tmem + w * PA_TILE;
+                const int phase = (p_phase >> w) & 1;
+                if (values) {
+                    p_phase ^= 1 << w;
+                    if (!pair || w == 0 || i >= last0) wait_full(ev);
+                    pa_wait(&sh.p_half[w], phase, &sh.err);
+                    tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = ((k / 4) * PA_SLAB_BYTES + (k % 4) * 32) >> 4;
-                mma_ss(d, a + off, b + off, ID_S, k != 0, issue);
+                    for (int k = 0; k < KS / 2; ++k)
+                        mma_ts(o, p + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, k != 0 ? 1 : i >= step, issue);
+                }
+                if (keys && (!pair || w == 0 || next >= last0)) wait_full(ek);
+                if (values) {
+                    pa_wait(&sh.p_full[w], phase, &sh.err);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = KS / 2; k < KS; ++k) mma_ts(o, p + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, 1, issue);
+                    if (alone) mma_commit(&sh.empty[sv], issue);
+                    if (!keys) mma_commit(&sh.o_full[w], issue);
+                }
+                if (keys) {
+                    tc_fence_after();
+                    const uint64_t qa = q_desc + (uint32_t)((w == 0 ? buf0 : buf1) * (S::TILE_BYTES >> 4));
+                    const uint64_t kb = k_desc + (uint32_t)(sk * (S::TILE_BYTES >> 4));
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * PA_SLAB_BYTES + (k % 4) * 32) >> 4;
+                        mma_ss(p, qa + off, kb + off, ID_S, k != 0, issue);
+                    }
+                    mma_commit(&sh.s_full[w], issue);
+                    if (alone) mma_commit(&sh.empty[sk], issue);
+                }
             }
-            mma_commit(&sh.s_full[w], issue);
-            if (done) mma_commit(&sh.empty[s], issue);
-        };
-        // O += P V of stream w's tile i, then the scores of its next one. A wait
-        // takes about 100 cycles even for what is there: each is made once, and
-        // between products that keep the tensor cores busy meanwhile.
-        auto step_stream = [&](int w, int i, int last) {
-            const bool alone = !pair || w == 1, first_of_pair = !pair || w == 0 || i >= last0;
-            const int e = ring0 + ring_v(pair, i, m), s = e % S::STAGES;
-            const int phase = p_phase[w];
-            p_phase[w] ^= 1;
-            if (first_of_pair) wait_full(e);
-            pa_wait(&sh.p_half[w], phase, &sh.err);
-            tc_fence_after();
-            const uint64_t b = v_desc + (uint32_t)(s * (S::TILE_BYTES >> 4));
-            const uint32_t d = tmem + 2 * PA_TILE + w * D, a = tmem + w * PA_TILE;
-            const uint32_t add = i >= step;
-#pragma unroll
-            for (int k = 0; k < KS / 2; ++k) mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, k != 0 ? 1 : add, issue);
-            if (i + step < last && (!pair || w == 0 || i + step >= last0)) wait_full(ring0 + ring_k(pair, i + step));
-            pa_wait(&sh.p_full[w], phase, &sh.err);
-            tc_fence_after();
-#pragma unroll
-            for (int k = KS / 2; k < KS; ++k) mma_ts(d, a + k * 8, b + (uint32_t)(k * 2048 >> 4), ID_O, 1, issue);
-            if (alone) mma_commit(&sh.empty[s], issue);
-            if (i + step < last) scores(w, i + step, alone);
-            else mma_commit(&sh.o_full[w], issue);
-        };
-        wait_full(ring0);
-        tc_fence_after();
-        if (last0 > 0) scores(0, 0, !pair);
-        if (pair) {
-            scores(1, 0, true);
-        } else if (m > 1) {
-            wait_full(ring0 + ring_k(pair, 1));
-            scores(1, 1, true);
-        }
-        for (int i = 0; i < m; ++i) {
-            if (pair ? i < last0 : (i & 1) == 0) step_stream(0, i, last0);
-            if (pair || (i & 1) == 1) step_stream(1, i, m);
             // after a wait that gave up: what was issued read whatever was there
             if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
         }
@@ -1085,21 +1101,19 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         if (warp_on) {
             constexpr int C = D / 2;
             const uint32_t o_base = tmem_base + lanes + 2 * PA_TILE;
-            uint32_t a[C], b[C];
-            tmem_ld2(pair ? tmem_o : o_base + w * C, pair ? tmem_o + C : o_base + D + w * C, a, b);
-            const float sa = f[0] * scale, sb = f[1] * scale;
-            float x[C];
-            // what a stream saw nothing of has no O there
+            const float sa = f[0] * scale, sb = pair ? 0.0f : f[1] * scale;
+#pragma unroll 1
+            for (int half = pair ? 0 : w; half <= (pair ? 1 : w); ++half) {
+                uint32_t a[C], b[C];
+                tmem_ld2((pair ? tmem_o : o_base) + half * C, o_base + D + half * C, a, b);
+                float x[C];
+                // what a stream saw nothing of has no O there
 #pragma unroll
-            for (int k = 0; k < C; ++k) {
-                const float y = sa == 0.0f ? 0.0f : __uint_as_float(a[k]) * sa;
-                x[k] = pair || sb == 0.0f ? y : fmaf(__uint_as_float(b[k]), sb, y);
-            }
-            put_columns<D, F16>(P, at, whole, slot, cap_row, pair ? 0 : w * C, x);
-            if (pair) {
-#pragma unroll
-                for (int k = 0; k < C; ++k) x[k] = sb == 0.0f ? 0.0f : __uint_as_float(b[k]) * sb;
-                put_columns<D, F16>(P, at, whole, slot, cap_row, C, x);
+                for (int k = 0; k < C; ++k) {
+                    const float y = sa == 0.0f ? 0.0f : __uint_as_float(a[k]) * sa;
+                    x[k] = sb == 0.0f ? y : fmaf(__uint_as_float(b[k]), sb, y);
+                }
+                put_columns<D, F16>(P, at, whole, slot, cap_row, half * C, x);
             }
         }
         if (at.valid && (pair || w == 0)) {
@@ -1209,16 +1223,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             softmax_rows<D, F16>(P, sh, warp >> 2, q_smem, ring, tmem);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
-            if (warp == 8) {
-                load_kv<D, false>(P, sh, smem_u32(ring), &tm_k, lane);
+            if (warp == 8 || warp == 10) {
+                load_kv<D>(P, sh, smem_u32(ring), warp == 10 ? &tm_v : &tm_k, warp == 10, lane);
             } else if (warp == 9) {
                 const uint32_t issue = elect_one();
                 issue_products<D, F16>(P, sh, smem_u32(q_smem), smem_u32(ring), tmem, issue);
                 // every product issued has completed before TMEM is released
                 mma_commit(&sh.mma_done, issue);
                 (void)pa_wait_until(&sh.mma_done, 0, nullptr);
-            } else if (warp == 10) {
-                load_kv<D, true>(P, sh, smem_u32(ring), &tm_v, lane);
             } else {
                 load_q<D>(P, sh, smem_u32(q_smem), &tm_q, lane);
             }
