@@ -542,12 +542,14 @@ _KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 _I32 = torch.int32
 
 
-def _rows(t, name, heads, width, dtype):
-    """Data pointer, token stride and head stride of a [rows, heads, width]
-    tensor (any number of heads when None) of any strides but the last."""
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != width or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {width}], got {list(shape)}")
+def _rows(t, name, rows, heads, width, dtype):
+    """Data pointer, strides of the first two dimensions and sizes of them of a
+    [rows, heads, width] tensor (any number where None) of any strides but the
+    last."""
+    n, h, w = t.shape if t.dim() == 3 else (-1, -1, -1)
+    if w != width or (heads is not None and h != heads) or (rows is not None and n != rows):
+        raise ValueError(f"{name} must be [{'T' if rows is None else rows}, {'heads' if heads is None else heads}, {width}], "
+                         f"got {list(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like the cache, got {t.dtype}")
     if not t.is_cuda:
@@ -555,7 +557,7 @@ def _rows(t, name, heads, width, dtype):
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t.data_ptr(), st, sh
+    return t.data_ptr(), st, sh, n, h
 
 
 def _int32(t, name, *shape):
@@ -574,13 +576,13 @@ def _cache_fields(k_cache, v_cache, page_table, ctx_lens):
     [B]."""
     if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
         raise ValueError("every tensor must live on a CUDA device")
-    shape = k_cache.shape
+    shape, torch_dtype = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, Hkv, D] and alike")
     n_pages, page_size, Hkv, D = shape
-    dtype = _KV_DTYPES.get(k_cache.dtype)
-    if dtype is None or v_cache.dtype is not k_cache.dtype:
-        raise TypeError(f"the cache must be bfloat16 or float16, got {k_cache.dtype} and {v_cache.dtype}")
+    dtype = _KV_DTYPES.get(torch_dtype)
+    if dtype is None or v_cache.dtype is not torch_dtype:
+        raise TypeError(f"the cache must be bfloat16 or float16, got {torch_dtype} and {v_cache.dtype}")
     kp, kt, kh, kd = k_cache.stride()
     vp, vt, vh, vd = v_cache.stride()
     if kd != 1 or vd != 1:
@@ -602,15 +604,21 @@ def _tree(tree_parents, B):
     return _int32(tree_parents, "tree_parents", B, N), N
 
 
-def _call(name, device, stream, fn):
-    """fn(raw stream) with `device` current; raises on a status."""
-    index = device.index
-    current = torch.cuda.current_device()
-    if current == index:
-        st = fn(torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device))
+def _stream_of(tensor, stream):
+    """The tensor's device, where it is not the current one (else None), and
+    the raw stream to launch on."""
+    index = tensor.get_device()
+    if index != torch.cuda.current_device():
+        return tensor.device, _stream(stream, tensor.device)
+    return None, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, tensor.device)
+
+
+def _call(name, device, fn, *args):
+    if device is None:
+        st = fn(*args)
     else:
         with torch.cuda.device(device):
-            st = fn(_stream(stream, device))
+            st = fn(*args)
     if st:
         _check(st, name)
 
@@ -628,33 +636,27 @@ def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None,
     [T] int32: rotary positions of the caller's own. Returns q_out."""
     cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
-    T = k.shape[0]
-    if v.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise ValueError("k, v and q must have the same number of rows")
-    kp, kt, kh = _rows(k, "k", Hkv, D, dtype)
-    vp, vt, vh = _rows(v, "v", Hkv, D, dtype)
+    kp, kt, kh, T, _ = _rows(k, "k", None, Hkv, D, dtype)
+    vp, vt, vh, _, _ = _rows(v, "v", T, Hkv, D, dtype)
     Hq = qp = qt = qh = op = ot = oh = 0
     if q is not None:
-        qp, qt, qh = _rows(q, "q", None, D, dtype)
-        Hq = q.shape[1]
+        qp, qt, qh, _, Hq = _rows(q, "q", T, None, D, dtype)
         if q_out is None:
             q_out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
-        elif q_out.shape[0] != T:
-            raise ValueError(f"q_out must be {list(q.shape)}, got {list(q_out.shape)}")
-        op, ot, oh = _rows(q_out, "q_out", Hq, D, dtype)
+        op, ot, oh, _, _ = _rows(q_out, "q_out", T, Hq, D, dtype)
     freq = rotary = 0
     if inv_freq is not None:
         if inv_freq.dtype is not torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous 1-D float64 CPU tensor")
-        freq, rotary = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+        freq, rotary = inv_freq.data_ptr(), 2 * len(inv_freq)
     parents, N = _tree(tree_parents, B)
     pos = 0 if positions is None else _int32(positions, "positions", T)
     status = 0 if status_word is None else _ptr(status_word)
     cu = _int32(cu_new, "cu_new", B + 1)
-    lib = _lib or _load()
-    _call("spec_kv_append", k_cache.device, stream, lambda raw: lib.spec_kv_append(_pack_append(
+    device, raw = _stream_of(k_cache, stream)
+    _call("spec_kv_append", device, (_lib or _load()).spec_kv_append, _pack_append(
         *cache, cu, T, kp, vp, kt, kh, vt, vh, Hq, qp, op, qt, qh, ot, oh, freq, rotary, 1 if interleaved else 0, parents, N,
-        pos, status, raw)))
+        pos, status, raw))
     return q_out
 
 
@@ -703,13 +705,10 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     out."""
     cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
-    qp, qt, qh = _rows(q, "q", None, D, dtype)
-    T, Hq = q.shape[0], q.shape[1]
+    qp, qt, qh, T, Hq = _rows(q, "q", None, None, D, dtype)
     if out is None:
         out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
-    elif out.shape[0] != T:
-        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
-    op, ot, oh = _rows(out, "out", Hq, D, dtype)
+    op, ot, oh, _, _ = _rows(out, "out", T, Hq, D, dtype)
     lse = 0
     if out_lse is not None:
         if out_lse.dtype is not torch.float32 or out_lse.shape != (T, Hq):
@@ -722,9 +721,9 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     status = 0 if status_word is None else _ptr(status_word)
     cu = _int32(cu_new, "cu_new", B + 1)
     scale = D ** -0.5 if scale is None else scale
-    lib = _lib or _load()
-    _call("spec_paged_attention", k_cache.device, stream, lambda raw: lib.spec_paged_attention(_pack_attention(
-        *cache, cu, T, Hq, qp, op, qt, qh, ot, oh, lse, scale, parents, N, ws, ws_bytes, status, int(flags), raw)))
+    device, raw = _stream_of(k_cache, stream)
+    _call("spec_paged_attention", device, (_lib or _load()).spec_paged_attention, _pack_attention(
+        *cache, cu, T, Hq, qp, op, qt, qh, ot, oh, lse, scale, parents, N, ws, ws_bytes, status, int(flags), raw))
     return out
 
 
@@ -743,7 +742,6 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     last = None if last_node is None else _int32(last_node, "last_node", B)
     n, lens = _int32(n_accepted, "n_accepted", B), _int32(out_lens, "out_lens", B)
     status = None if status_word is None else _ptr(status_word)
-    lib = _lib or _load()
-    _call("spec_kv_commit", k_cache.device, stream, lambda raw: lib.spec_kv_commit(
-        _pack_cache(*cache), n, parents, N, last, lens, status, raw))
+    device, raw = _stream_of(k_cache, stream)
+    _call("spec_kv_commit", device, (_lib or _load()).spec_kv_commit, _pack_cache(*cache), n, parents, N, last, lens, status, raw)
     return out_lens

@@ -55,7 +55,6 @@ struct PagedAttnParams {
     ChunkParams ch;
     char* out;
     int64_t o_ts, o_hs;      // bytes
-    bool wide_out;           // every output row starts on a multiple of 32 bytes
     float* lse;              // [T, Hq] or nullptr
     int Hq, G, TT;           // G = Hq / Hkv; TT = tokens per 128-row tile
     int q_box;               // tokens of one copy of queries, a divisor of TT

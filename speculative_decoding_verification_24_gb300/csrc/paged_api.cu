@@ -123,7 +123,7 @@ bool encode_queries(CUtensorMap* map, const sv_paged_attention_args& a, int toke
 uint64_t turn_fraction(double w) {
     double t = w * 0.15915494309189535;  // 1 / 2 pi
     t -= std::floor(t);
-    const double x = std::ldexp(t, 64);
+    const double x = t * 18446744073709551616.0;  // 2^64: exact
     return x >= 18446744073709551616.0 ? 0 : (uint64_t)x;
 }
 
@@ -225,7 +225,6 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     p.ch = chunk_of(c, a->cu_new, a->T, a->tree_parents, a->N, a->status_word);
     p.out = static_cast<char*>(a->out);
     p.o_ts = a->out_token_stride * 2, p.o_hs = a->out_head_stride * 2;
-    p.wide_out = aligned(a->out, 32) && p.o_ts % 32 == 0 && p.o_hs % 32 == 0;
     p.lse = a->out_lse;
     p.Hq = a->Hq;
     p.G = G;

@@ -592,25 +592,46 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     return r;
 }
 
-// n values of one output row, scaled and rounded once, from column col on. A
-// lane's row is a line of its own, and a store costs the memory pipe a cycle
-// per line: 32 bytes at a time where rows allow it (`wide`).
+// N values of each lane's output row, rounded once. A lane's row is a line of
+// its own, and a store costs the memory pipe about 2.5 cycles per line (2600
+// cycles for a tile's half of the columns), so with many rows (`dense`) groups
+// of N / 8 lanes first exchange 16-byte pieces, each lane's row for one piece
+// of each row of the group, and a store then writes whole rows. A few rows are
+// stored as they lie: the exchange took longer (256 contexts of at most 400
+// tokens, 4 rows: 112 us with it, 94 without; 64 trees of 128 rows: 72 and 74).
 template <bool F16, int N>
-__device__ __forceinline__ void store_row(char* row, int col, const float (&x)[N], float scale, bool wide) {
-    uint32_t w[N / 2];
+__device__ __forceinline__ void store_rows(char* row, bool valid, bool dense, const float (&x)[N], int lane) {
+    constexpr int NP = N / 8;
+    uint32_t w[NP][4];
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = pack_pair<F16>(x[2 * i] * scale, x[2 * i + 1] * scale);
-    char* to = row + col * 2;
-    if (N >= 16 && wide) {
+    for (int i = 0; i < N / 2; ++i) w[i / 4][i % 4] = pack_pair<F16>(x[2 * i], x[2 * i + 1]);
+    if (!dense) {
+        if (valid) {
 #pragma unroll
-        for (int i = 0; i + 8 <= N / 2; i += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                         ::"l"(to + i * 4), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]),
-                           "r"(w[i + 6]), "r"(w[i + 7])
-                         : "memory");
-    } else {
+            for (int c = 0; c < NP; ++c) reinterpret_cast<uint4*>(row)[c] = make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
+        }
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < N / 2; i += 4) *reinterpret_cast<uint4*>(to + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    for (int s = 1; s < NP; s <<= 1) {
+        const bool high = (lane & s) != 0;
+#pragma unroll
+        for (int c = 0; c < NP; ++c) {
+            if (c & s) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, high ? w[c][q] : w[c | s][q], s);
+                w[c][q] = high ? got : w[c][q];
+                w[c | s][q] = high ? w[c | s][q] : got;
+            }
+        }
+    }
+    const unsigned long long mine = valid ? reinterpret_cast<unsigned long long>(row) : 0ull;
+    const int piece = lane % NP;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        char* to = reinterpret_cast<char*>(__shfl_sync(0xFFFFFFFFu, mine, lane - piece + i));
+        if (to) *reinterpret_cast<uint4*>(to + piece * 16) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
     }
 }
 
@@ -715,8 +736,13 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
             if (!on[j] || lane_of != 0) continue;
             const int r = row[j] % PA_TILE, i = r / P.G;
             const RowPlace at = place_row(P, c, row[j] / PA_TILE, i, r - i * P.G);
-            store_row<F16, 8>(P.out + at.token * P.o_ts + at.head * P.o_hs, 8 * group[j], acc[j], L[j] == 0.0f ? 0.0f : 1.0f / L[j],
-                              false);
+            const float inv = L[j] == 0.0f ? 0.0f : 1.0f / L[j];
+            uint4 w;
+            w.x = pack_pair<F16>(acc[j][0] * inv, acc[j][1] * inv);
+            w.y = pack_pair<F16>(acc[j][2] * inv, acc[j][3] * inv);
+            w.z = pack_pair<F16>(acc[j][4] * inv, acc[j][5] * inv);
+            w.w = pack_pair<F16>(acc[j][6] * inv, acc[j][7] * inv);
+            *reinterpret_cast<uint4*>(P.out + at.token * P.o_ts + at.head * P.o_hs + group[j] * 16) = w;
             if (P.lse && group[j] == 0) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M[j], L[j]);
         }
     }
@@ -914,11 +940,10 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
 // Half of a row's columns, to the output or, of a cut item, to this CTA's piece.
 template <int D, bool F16>
 __device__ __forceinline__ void put_columns(const PagedAttnParams& P, const RowPlace& at, bool whole, int slot, int row, int col,
-                                            const float (&x)[D / 2]) {
-    if (!at.valid) return;
+                                            const float (&x)[D / 2], bool dense, int lane) {
     if (whole) {
-        store_row<F16, D / 2>(P.out + at.token * P.o_ts + at.head * P.o_hs, col, x, 1.0f, P.wide_out);
-    } else {
+        store_rows<F16, D / 2>(P.out + at.token * P.o_ts + at.head * P.o_hs + col * 2, at.valid, dense, x, lane);
+    } else if (at.valid) {
         float4* part = reinterpret_cast<float4*>(P.part_o) + part_at(P, D, slot, row, col / 4);
 #pragma unroll
         for (int k = 0; k < D / 8; ++k)
@@ -975,7 +1000,8 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             if (i + step >= last && tid == 0) release_q(&sh.q_empty[buf], pair);
             // Entries past the last key are whatever the page holds, and weight
             // 0 times infinity is not 0: they are cleared, by the stream whose
-            // product reads the tile first.
+            // product reads the tile first. (Here and not between the two halves
+            // of P: with the scores in registers it cost the loop 5 %.)
             if (key0 + PA_TILE > key_end && (!pair || w == 0 || last0 < m_tiles)) {
                 const int e = ring0 + ring_v(pair, i, m_tiles), s = e % S::STAGES;
                 pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
@@ -1000,6 +1026,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                             if (at0 >= 0 && at0 < 32) on |= set << at0;
                             else if (at0 < 0 && at0 > -32) on |= set >> -at0;
                         }
+                        // most blocks are seen whole by every row of the warp
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (!((on >> k) & 1u)) r[32 * q + k] = 0xFF800000u;  // -inf, whatever stood there
@@ -1101,19 +1128,20 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         if (warp_on) {
             constexpr int C = D / 2;
             const uint32_t o_base = tmem_base + lanes + 2 * PA_TILE;
-            const float sa = f[0] * scale, sb = pair ? 0.0f : f[1] * scale;
+            const float sa = f[0] * scale, sb = f[1] * scale;
+            const bool both = !pair && m_tiles > 1;
+            const int done0 = pair ? done : 1;
 #pragma unroll 1
             for (int half = pair ? 0 : w; half <= (pair ? 1 : w); ++half) {
                 uint32_t a[C], b[C];
                 tmem_ld2((pair ? tmem_o : o_base) + half * C, o_base + D + half * C, a, b);
                 float x[C];
-                // what a stream saw nothing of has no O there
 #pragma unroll
                 for (int k = 0; k < C; ++k) {
-                    const float y = sa == 0.0f ? 0.0f : __uint_as_float(a[k]) * sa;
-                    x[k] = sb == 0.0f ? y : fmaf(__uint_as_float(b[k]), sb, y);
+                    const float y = done0 == 0 ? 0.0f : __uint_as_float(a[k]) * sa;
+                    x[k] = both ? fmaf(__uint_as_float(b[k]), sb, y) : y;
                 }
-                put_columns<D, F16>(P, at, whole, slot, cap_row, half * C, x);
+                put_columns<D, F16>(P, at, whole, slot, cap_row, half * C, x, tile_rows > 32, lane);
             }
         }
         if (at.valid && (pair || w == 0)) {
