@@ -14,6 +14,7 @@ constexpr int KV_MAX_TREE = 32;       // nodes of a tree: one warp lane, one mas
 constexpr int KV_MAX_ROTARY = 128;    // rotary size: 64 frequencies in the kernel's parameters
 constexpr int PA_TILE = 128;          // keys per tile (MMA N), rows per tile (MMA M)
 constexpr int PA_MAX_CTAS = SV_PAGED_MAX_CTAS;
+constexpr int PA_ITEM_COST = 2;       // units of work of an item besides its key tiles
 
 // The chunk of a batch: which packed rows belong to which sequence, and where
 // its tokens lie in the cache.

@@ -203,7 +203,7 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     const int G = a->Hq / c.Hkv, TT = sv::PA_TILE / G;
     // the kernel counts key tiles of (sequence, head, row tile) items in int32
     const double items = (std::ceil(a->T / (2.0 * TT)) + c.B) * c.Hkv;
-    if (items * (std::ceil((double)c.max_pages * c.page_size / sv::PA_TILE) + 1.0) > 2147483647.0) return SV_ERR_SHAPE;
+    if (items * (std::ceil((double)c.max_pages * c.page_size / sv::PA_TILE) + sv::PA_ITEM_COST) > 2147483647.0) return SV_ERR_SHAPE;
     if (!std::isfinite(a->scale) || !(a->scale > 0.0f) || !std::isfinite(a->scale * 1.4426950408889634f)) return SV_ERR_CONFIG;
     if (a->flags & ~SV_ARG_TEST_WAIT_TIMEOUT) return SV_ERR_CONFIG;
     if ((st = check_tree(a->tree_parents, a->N)) != SV_OK) return st;

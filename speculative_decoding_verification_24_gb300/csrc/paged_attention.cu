@@ -281,8 +281,10 @@ __device__ __forceinline__ void softmax_barrier() {
 }
 
 // ---------------------------------------------------------------------------
-// Work: items in the order (sequence, kv head, row tile), each item its number
-// of key tiles long, laid end to end on one axis of W tiles.
+// Work: items in the order (sequence, kv head, row tile), laid end to end on
+// one axis of W units. A unit is a key tile; an item begins with PA_ITEM_COST
+// units for what it takes besides its tiles (first scores, output, and joining
+// both streams: about 5000 cycles, a tile takes 1400 to 3000).
 // ---------------------------------------------------------------------------
 // sum over i < n of floor((a i + b) / 128). With a = 2^k (TT a power of two)
 // the terms are floor((i + b / a) / q), q = 128 / a: runs of q equal ones.
@@ -320,12 +322,12 @@ __device__ __forceinline__ int tiles_of(int end) { return (int)(((long long)end 
 // Row tiles pair up; row-tile pair p covers tokens [2 TT p, 2 TT (p + 1)).
 __device__ __forceinline__ int pairs_of(int n, int TT) { return n <= TT ? 1 : (n + 2 * TT - 1) / (2 * TT); }
 
-// Key tiles of one kv head's first p pairs (p < pairs: none of them the last).
-__device__ __forceinline__ int tiles_before(int ctx, int TT, int p) {
-    return p == 0 ? 0 : (int)floor_sum(p, 2 * TT, (uint32_t)ctx + 2 * TT + PA_TILE - 1);
+// Units of one kv head's first p pairs (p < pairs: none of them the last).
+__device__ __forceinline__ int units_before(int ctx, int TT, int p) {
+    return p == 0 ? 0 : (int)floor_sum(p, 2 * TT, (uint32_t)ctx + 2 * TT + PA_TILE - 1) + p * PA_ITEM_COST;
 }
-__device__ __forceinline__ int tiles_per_head(int n, int ctx, int TT) {
-    return n == 0 ? 0 : tiles_before(ctx, TT, pairs_of(n, TT) - 1) + tiles_of(ctx + n);
+__device__ __forceinline__ int units_per_head(int n, int ctx, int TT) {
+    return n == 0 ? 0 : units_before(ctx, TT, pairs_of(n, TT) - 1) + tiles_of(ctx + n) + PA_ITEM_COST;
 }
 
 // The next sequence after b that has work; b becomes its number.
@@ -340,7 +342,7 @@ __device__ __forceinline__ Chunk next_chunk(const ChunkParams& ch, int& b) {
 }
 
 // A walk over the items of a CTA's share, computed alike by every role. Places
-// on the axis of tiles are int32: the host refuses batches whose bound on the
+// on the axis are int32: the host refuses batches whose bound on the
 // total is larger.
 struct Cursor {
     int begin, end;         // this CTA's share
@@ -356,7 +358,7 @@ struct Cursor {
     }
     __device__ __forceinline__ bool valid() const { return u0 < end; }
     __device__ __forceinline__ void next(const PagedAttnParams& P) {
-        u0 += tiles;
+        u0 += PA_ITEM_COST + tiles;
         if (u0 >= end) return;
         if (tok0 + ntok == s.n) {
             p = 0;
@@ -371,18 +373,18 @@ struct Cursor {
         set_item(P);
     }
     // the part of the item in this share
-    __device__ __forceinline__ int t0() const { return max(begin - u0, 0); }
-    __device__ __forceinline__ int t1() const { return min(end - u0, tiles); }
+    __device__ __forceinline__ int t0() const { return max(begin - u0 - PA_ITEM_COST, 0); }
+    __device__ __forceinline__ int t1() const { return min(end - u0 - PA_ITEM_COST, tiles); }
     __device__ __forceinline__ bool pair(const PagedAttnParams& P) const { return ntok > P.TT; }
 };
 
 // CTA c's share begins at u_c: W = active * size + extra, the first `extra`
-// shares one tile longer. A boundary moves to an item's edge when it falls
-// within `snap` tiles of one: a piece of a few tiles costs more in joining
+// shares one unit longer. A boundary moves to an item's edge when it falls
+// within PA_SNAP tiles of one: a piece of a few tiles costs more in joining
 // than the uneven share does.
 constexpr int PA_SNAP = 3;
 struct Shares {
-    int W, active, size, extra, snap;
+    int W, active, size, extra;
 
     __device__ __forceinline__ int begin(int c) const { return c * size + min(c, extra); }
     // the first boundary at or past x > 0
@@ -391,9 +393,9 @@ struct Shares {
         return x <= longer ? (x + size) / (size + 1) : extra + (x - longer + size - 1) / size;
     }
 };
-// A CTA gets at least this many tiles: below that, joining costs more than
+// A CTA gets at least this many units: below that, joining costs more than
 // another CTA saves.
-constexpr int PA_MIN_SHARE = 2;
+constexpr int PA_MIN_SHARE = 4;
 
 struct PaShared {
     int scan[PA_THREADS / 32];
@@ -426,11 +428,11 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     return v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? mine : 0);
 }
 
-__device__ __forceinline__ int sequence_tiles(const PagedAttnParams& P, int b, Chunk& s, bool& bad) {
+__device__ __forceinline__ int sequence_units(const PagedAttnParams& P, int b, Chunk& s, bool& bad) {
     if (b >= P.ch.B) return 0;
     s = load_chunk(P.ch, b);
     bad |= !s.ok;
-    return s.ok ? tiles_per_head(s.n, s.ctx, P.TT) * P.ch.Hkv : 0;
+    return s.ok ? units_per_head(s.n, s.ctx, P.TT) * P.ch.Hkv : 0;
 }
 
 // The item that holds place `raw`, in sequence b, whose items begin at `first`;
@@ -447,14 +449,14 @@ __device__ __forceinline__ void place_boundary(const PagedAttnParams& P, const S
     c.p = 0;
     int before = 0;
     if (pairs > 1) {
-        // tiles_before(p) is close to p (ctx + TT + TT p) / 128: start from its
-        // root and step to the pair that holds in_head
-        const float A = (float)P.TT, half = 0.5f * ((float)c.s.ctx + A);
+        // units_before(p) is close to p (ctx + TT + TT p) / 128 + p PA_ITEM_COST:
+        // start from its root and step to the pair that holds in_head
+        const float A = (float)P.TT, half = 0.5f * ((float)c.s.ctx + A + PA_TILE * PA_ITEM_COST);
         c.p = min(pairs - 1, max(0, (int)((sqrtf(half * half + A * (float)in_head * PA_TILE) - half) / A)));
-        before = tiles_before(c.s.ctx, P.TT, c.p);
-        while (before > in_head) before = tiles_before(c.s.ctx, P.TT, --c.p);
+        before = units_before(c.s.ctx, P.TT, c.p);
+        while (before > in_head) before = units_before(c.s.ctx, P.TT, --c.p);
         while (c.p + 1 < pairs) {
-            const int next = tiles_before(c.s.ctx, P.TT, c.p + 1);
+            const int next = units_before(c.s.ctx, P.TT, c.p + 1);
             if (next > in_head) break;
             before = next;
             ++c.p;
@@ -464,10 +466,11 @@ __device__ __forceinline__ void place_boundary(const PagedAttnParams& P, const S
     c.set_item(P);
     c.begin = raw;
     c.end = shares.W;
-    if (raw - c.u0 <= shares.snap) {
+    const int item_end = c.u0 + PA_ITEM_COST + c.tiles;
+    if (raw - c.u0 <= PA_ITEM_COST + PA_SNAP) {
         c.begin = c.u0;
-    } else if (c.u0 + c.tiles - raw <= shares.snap) {
-        c.begin = c.u0 + c.tiles;
+    } else if (item_end - raw <= PA_SNAP) {
+        c.begin = item_end;
         c.next(P);
     }
     out = c;
@@ -480,13 +483,13 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
     const int tid = threadIdx.x;
     const bool one_turn = ch.B <= PA_THREADS;
     Chunk s = {};
-    int mine = sequence_tiles(P, tid, s, bad), W;
+    int mine = sequence_units(P, tid, s, bad), W;
     int incl = block_scan(mine, sh.scan, W);
     if (!one_turn) {
         for (int base = PA_THREADS; base < ch.B; base += PA_THREADS) {
             int total;
             __syncthreads();
-            block_scan(sequence_tiles(P, base + tid, s, bad), sh.scan, total);
+            block_scan(sequence_units(P, base + tid, s, bad), sh.scan, total);
             W += total;
         }
     }
@@ -498,7 +501,6 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
     if (here) {
         shares.size = (int)((uint32_t)W / (uint32_t)shares.active);
         shares.extra = W - shares.size * shares.active;
-        shares.snap = max(shares.size / 16, PA_SNAP);
         raw[0] = shares.begin(blockIdx.x);
         raw[1] = shares.begin(blockIdx.x + 1);
     }
@@ -508,7 +510,7 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
         if (!one_turn) {
             bool again = false;
             __syncthreads();
-            mine = sequence_tiles(P, base + tid, s, again);
+            mine = sequence_units(P, base + tid, s, again);
             incl = block_scan(mine, sh.scan, total);
         }
         const int excl = run + incl - mine;
@@ -538,8 +540,9 @@ __device__ __forceinline__ Cursor share_of(const PaShared& sh) {
 // The pieces an item is cut into: the first boundary inside it (the item
 // begins in the CTA before) and how many pieces there are.
 __device__ __forceinline__ void pieces_of(const Shares& w, const Cursor& c, int& first_cta, int& pieces) {
-    // boundaries from u0 + snap + 1 up to u0 + tiles - snap - 1 cut it
-    const int c_lo = w.first_at(c.u0 + w.snap + 1), c_end = w.first_at(c.u0 + c.tiles - w.snap);
+    // boundaries more than PA_SNAP tiles from both its edges cut it
+    const int first = c.u0 + PA_ITEM_COST;
+    const int c_lo = w.first_at(first + PA_SNAP + 1), c_end = w.first_at(first + c.tiles - PA_SNAP);
     first_cta = c_lo - 1;
     pieces = c_end - c_lo + 1;
 }
@@ -678,7 +681,8 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
     for (int base = 0; base < units; base += U * stride) {
         int group[U], row[U];
         bool on[U];
-        float M[U], L[U], acc[U][8];
+        float M[U], L[U];
+        f32x2 acc[U][4];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int u = base + j * stride + ((int)threadIdx.x >> share);
@@ -688,7 +692,7 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
             row[j] = r < rows0 ? r : PA_TILE + r - rows0;
             M[j] = -INFINITY, L[j] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[j][k] = 0.0f;
+            for (int k = 0; k < 4; ++k) acc[j][k] = 0ull;
         }
 #pragma unroll 1
         for (int fb = f0; fb < f1; fb += F) {
@@ -709,18 +713,29 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
                     }
                 }
 #pragma unroll
-            for (int j = 0; j < U; ++j)
+            for (int j = 0; j < U; ++j) {
+                // one weight per piece and one for what was joined before; a
+                // piece that saw nothing of the row has weight 0 and zeros for
+                // O, and NaN stays NaN
+                float m = M[j];
+#pragma unroll
+                for (int k = 0; k < F; ++k) m = fmaxf(m, ml[j][k].x);
+                const float old = L[j] == 0.0f ? 0.0f : ex2(M[j] - m);
+                M[j] = m;
+                L[j] *= old;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[j][q] = mul2(acc[j][q], pack2(old, old));
 #pragma unroll
                 for (int k = 0; k < F; ++k) {
-                    // a piece that saw nothing of the row has weight 0 and no O; NaN stays NaN
-                    const float m = fmaxf(M[j], ml[j][k].x);
-                    const float old = L[j] == 0.0f ? 0.0f : ex2(M[j] - m), w = ml[j][k].y == 0.0f ? 0.0f : ex2(ml[j][k].x - m);
-                    M[j] = m;
-                    L[j] = fmaf(w, ml[j][k].y, L[j] * old);
-                    const float x[8] = {a[j][k].x, a[j][k].y, a[j][k].z, a[j][k].w, b[j][k].x, b[j][k].y, b[j][k].z, b[j][k].w};
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) acc[j][q] = fmaf(w, w == 0.0f ? 0.0f : x[q], acc[j][q] * old);
+                    const float w = ml[j][k].y == 0.0f ? 0.0f : ex2(ml[j][k].x - m);
+                    const f32x2 ww = pack2(w, w);
+                    L[j] = fmaf(w, ml[j][k].y, L[j]);
+                    acc[j][0] = fma2(pack2(a[j][k].x, a[j][k].y), ww, acc[j][0]);
+                    acc[j][1] = fma2(pack2(a[j][k].z, a[j][k].w), ww, acc[j][1]);
+                    acc[j][2] = fma2(pack2(b[j][k].x, b[j][k].y), ww, acc[j][2]);
+                    acc[j][3] = fma2(pack2(b[j][k].z, b[j][k].w), ww, acc[j][3]);
                 }
+            }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
@@ -731,18 +746,21 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
                 M[j] = m;
                 L[j] = L[j] * w1 + l2 * w2;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) acc[j][k] = acc[j][k] * w1 + __shfl_xor_sync(0xFFFFFFFFu, acc[j][k], o) * w2;
+                for (int k = 0; k < 4; ++k)
+                    acc[j][k] = fma2(__shfl_xor_sync(0xFFFFFFFFu, acc[j][k], o), pack2(w2, w2), mul2(acc[j][k], pack2(w1, w1)));
             }
             if (!on[j] || lane_of != 0) continue;
             const int r = row[j] % PA_TILE, i = r / P.G;
             const RowPlace at = place_row(P, c, row[j] / PA_TILE, i, r - i * P.G);
             const float inv = L[j] == 0.0f ? 0.0f : 1.0f / L[j];
-            uint4 w;
-            w.x = pack_pair<F16>(acc[j][0] * inv, acc[j][1] * inv);
-            w.y = pack_pair<F16>(acc[j][2] * inv, acc[j][3] * inv);
-            w.z = pack_pair<F16>(acc[j][4] * inv, acc[j][5] * inv);
-            w.w = pack_pair<F16>(acc[j][6] * inv, acc[j][7] * inv);
-            *reinterpret_cast<uint4*>(P.out + at.token * P.o_ts + at.head * P.o_hs + group[j] * 16) = w;
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;
+                unpack2(acc[j][k], lo, hi);
+                w[k] = pack_pair<F16>(lo * inv, hi * inv);
+            }
+            *reinterpret_cast<uint4*>(P.out + at.token * P.o_ts + at.head * P.o_hs + group[j] * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             if (P.lse && group[j] == 0) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M[j], L[j]);
         }
     }
