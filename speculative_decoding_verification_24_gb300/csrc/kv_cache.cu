@@ -26,7 +26,9 @@ namespace sv {
 // between lanes.
 // ---------------------------------------------------------------------------
 constexpr int KA_THREADS = 256;
-constexpr int KA_MAX_TOKENS = 4;
+constexpr int KA_MAX_TOKENS = 8;    // a warp each
+constexpr int KA_MANY = 16;         // tokens per SM from which on there are many
+constexpr int KA_BATCH = 3;         // pairs of pieces per thread whose loads are in flight together
 
 struct TokenPlace {
     int64_t k_off, v_off;  // byte offsets of the slot in the caches, -1: not stored
@@ -90,8 +92,41 @@ __device__ __forceinline__ uint4 ld_once(const char* p) {
     return v;
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(KA_THREADS) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+// What a lane moves: two pieces of one head of one of the CTA's tokens.
+// Heads count keys first, then values, then queries.
+template <int D>
+struct Pieces {
+    int token, head, c;  // c: which pair of pieces
+    __device__ __forceinline__ Pieces(int x, int heads) {
+        constexpr int L = D / 16;  // lanes per head
+        const int y = x / L;
+        c = x % L;
+        token = y / heads;
+        head = y - token * heads;
+    }
+    __device__ __forceinline__ bool apart(const KvAppendParams& p) const { return !p.interleaved && c < p.rotary / 16; }
+    __device__ __forceinline__ int first(const KvAppendParams& p) const { return apart(p) ? c : 2 * c; }
+    __device__ __forceinline__ int second(const KvAppendParams& p) const { return apart(p) ? c + p.rotary / 16 : 2 * c + 1; }
+    __device__ __forceinline__ const char* from(const KvAppendParams& p, int row) const {
+        const int Hkv = p.ch.Hkv;
+        if (head < Hkv) return p.k + row * p.k_ts + head * p.k_hs;
+        if (head < 2 * Hkv) return p.v + row * p.v_ts + (head - Hkv) * p.v_hs;
+        return p.q + row * p.q_ts + (head - 2 * Hkv) * p.q_hs;
+    }
+    // nullptr: not stored
+    __device__ __forceinline__ char* to(const KvAppendParams& p, const TokenPlace& pl) const {
+        const int Hkv = p.ch.Hkv;
+        if (head < Hkv) return pl.k_off < 0 ? nullptr : p.kc + pl.k_off + head * p.kc_hs;
+        if (head < 2 * Hkv) return pl.v_off < 0 ? nullptr : p.vc + pl.v_off + (head - Hkv) * p.vc_hs;
+        return pl.row < 0 ? nullptr : p.q_out + pl.row * p.qo_ts + (head - 2 * Hkv) * p.qo_hs;
+    }
+    __device__ __forceinline__ bool rotates(const KvAppendParams& p) const {
+        return c < p.rotary / 16 && (head < p.ch.Hkv || head >= 2 * p.ch.Hkv);
+    }
+};
+
+template <int D, bool F16, int BATCH>
+__global__ void __launch_bounds__(KA_THREADS, BATCH > 1 ? 4 : 6) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
     __shared__ TokenPlace place[KA_MAX_TOKENS];
     __shared__ int pos_s[KA_MAX_TOKENS];
     __shared__ __align__(16) float2 cs[KA_MAX_TOKENS][KV_MAX_ROTARY / 2];  // (cos, sin)
@@ -101,6 +136,24 @@ __global__ void __launch_bounds__(KA_THREADS) kv_append_kernel(const __grid_cons
     grid_dependency_wait();
     const int t0 = blockIdx.x * p.tokens_per_cta;
     const int nt = min(p.tokens_per_cta, ch.T - t0);
+    const int heads = (p.q ? p.Hq : 0) + 2 * ch.Hkv, all = nt * heads * (D / 16);
+
+    uint4 w0[BATCH], w1[BATCH];
+    const auto load = [&](int x0) {
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int x = x0 + u * KA_THREADS;
+            if (x >= all) continue;
+            const Pieces<D> m(x, heads);
+            const char* src = m.from(p, t0 + m.token);
+            w0[u] = ld_once(src + 16 * m.first(p));
+            w1[u] = ld_once(src + 16 * m.second(p));
+        }
+    };
+    // The rows are known before their places are: with few tokens the first
+    // loads fly while the places are found.
+    constexpr bool EARLY = BATCH > 1;
+    if (EARLY) load(threadIdx.x);
 
     if (warp < nt) {
         const int t = t0 + warp;
@@ -142,67 +195,44 @@ __global__ void __launch_bounds__(KA_THREADS) kv_append_kernel(const __grid_cons
     }
     __syncthreads();
 
-    constexpr int L = D / 16;                  // lanes per head
-    const int heads = (p.q ? p.Hq : 0) + 2 * ch.Hkv;
-    const int per_token = heads * L;
-    const int rot_lanes = p.rotary / 16;       // lanes whose pieces rotate
-    for (int x = threadIdx.x; x < nt * per_token; x += KA_THREADS) {
-        const int tk = nt == 1 ? 0 : x / per_token;
-        const int y = x - tk * per_token;
-        int h = y / L;
-        const int c = y % L;
-        const TokenPlace pl = place[tk];
-        if (pl.row < 0) continue;
-        const char* src;
-        char* dst;
-        bool rotate = c < rot_lanes;
-        if (h < ch.Hkv) {
-            src = p.k + pl.row * p.k_ts + h * p.k_hs;
-            dst = pl.k_off >= 0 ? p.kc + pl.k_off + h * p.kc_hs : nullptr;
-        } else if (h < 2 * ch.Hkv) {
-            h -= ch.Hkv;
-            src = p.v + pl.row * p.v_ts + h * p.v_hs;
-            dst = pl.v_off >= 0 ? p.vc + pl.v_off + h * p.vc_hs : nullptr;
-            rotate = false;
-        } else {
-            h -= 2 * ch.Hkv;
-            src = p.q + pl.row * p.q_ts + h * p.q_hs;
-            dst = p.q_out + pl.row * p.qo_ts + h * p.qo_hs;
-        }
-        if (!dst) continue;
-        // this lane's two 16-byte pieces
-        int c0 = 2 * c, c1 = 2 * c + 1;
-        if (!p.interleaved && c < rot_lanes) c0 = c, c1 = c + rot_lanes;
-        const uint4 w0 = ld_once(src + 16 * c0);
-        const uint4 w1 = ld_once(src + 16 * c1);
-        uint4 o0 = w0, o1 = w1;
-        if (rotate) {
-            float a[8], b[8];
-            unpack8<F16>(w0, a);
-            unpack8<F16>(w1, b);
-            const float2* t = cs[tk] + 8 * c;
-            if (p.interleaved) {
+    for (int x0 = threadIdx.x; x0 < all; x0 += BATCH * KA_THREADS) {
+        if (!EARLY || x0 != threadIdx.x) load(x0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = t[i], g = t[4 + i];
-                    const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-                    a[2 * i] = a0 * f.x - a1 * f.y, a[2 * i + 1] = a1 * f.x + a0 * f.y;
-                    b[2 * i] = b0 * g.x - b1 * g.y, b[2 * i + 1] = b1 * g.x + b0 * g.y;
-                }
-            } else {
+        for (int u = 0; u < BATCH; ++u) {
+            const int x = x0 + u * KA_THREADS;
+            if (x >= all) continue;
+            const Pieces<D> m(x, heads);
+            char* dst = m.to(p, place[m.token]);
+            if (!dst) continue;
+            uint4 o0 = w0[u], o1 = w1[u];
+            if (m.rotates(p)) {
+                float a[8], b[8];
+                unpack8<F16>(o0, a);
+                unpack8<F16>(o1, b);
+                const float2* t = cs[m.token] + 8 * m.c;
+                if (p.interleaved) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = t[i];
-                    const float a0 = a[i], b0 = b[i];
-                    a[i] = a0 * f.x - b0 * f.y;
-                    b[i] = b0 * f.x + a0 * f.y;
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = t[i], g = t[4 + i];
+                        const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+                        a[2 * i] = a0 * f.x - a1 * f.y, a[2 * i + 1] = a1 * f.x + a0 * f.y;
+                        b[2 * i] = b0 * g.x - b1 * g.y, b[2 * i + 1] = b1 * g.x + b0 * g.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 f = t[i];
+                        const float a0 = a[i], b0 = b[i];
+                        a[i] = a0 * f.x - b0 * f.y;
+                        b[i] = b0 * f.x + a0 * f.y;
+                    }
                 }
+                o0 = pack8<F16>(a);
+                o1 = pack8<F16>(b);
             }
-            o0 = pack8<F16>(a);
-            o1 = pack8<F16>(b);
+            reinterpret_cast<uint4*>(dst)[m.first(p)] = o0;
+            reinterpret_cast<uint4*>(dst)[m.second(p)] = o1;
         }
-        reinterpret_cast<uint4*>(dst)[c0] = o0;
-        reinterpret_cast<uint4*>(dst)[c1] = o1;
     }
 }
 
@@ -220,13 +250,30 @@ static cudaError_t launch_early(K kernel, int grid, int threads, const P& p, cud
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int BATCH>
+static cudaError_t launch_append(const KvAppendParams& p, int f16, cudaStream_t stream) {
+    const int grid = (p.ch.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+    auto kernel = p.D == 128 ? (f16 ? kv_append_kernel<128, true, BATCH> : kv_append_kernel<128, false, BATCH>)
+                             : (f16 ? kv_append_kernel<64, true, BATCH> : kv_append_kernel<64, false, BATCH>);
+    return launch_early(kernel, grid, KA_THREADS, p, stream);
+}
+
+// Many tokens: several per CTA and one pair of loads per thread at a time, in
+// few registers, so that 6 CTAs per SM cover one another's searches. Fewer: as
+// many tokens as one batch of loads holds, which then fly while the places are
+// found. Measured with 48 heads of 128, the first and the second way, in us:
+// 512 tokens 6.5 and 5.4, 1024 11.5 and 7.5, 2560 16.7 and 16.8, 6400 32.3 and
+// 35.1, 32000 131 and 140 (6.0 and 5.6 TB/s).
 cudaError_t launch_kv_append(const KvAppendParams& in, int f16, int sms, cudaStream_t stream) {
     KvAppendParams p = in;
-    p.tokens_per_cta = p.ch.T > 4 * sms ? KA_MAX_TOKENS : 1;
-    const int grid = (p.ch.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
-    auto kernel = p.D == 128 ? (f16 ? kv_append_kernel<128, true> : kv_append_kernel<128, false>)
-                             : (f16 ? kv_append_kernel<64, true> : kv_append_kernel<64, false>);
-    return launch_early(kernel, grid, KA_THREADS, p, stream);
+    const int per_token = ((p.q ? p.Hq : 0) + 2 * p.ch.Hkv) * (p.D / 16);
+    const int fit = KA_BATCH * KA_THREADS / per_token;
+    if (p.ch.T > KA_MANY * sms) {
+        p.tokens_per_cta = KA_MAX_TOKENS / 2;
+        return launch_append<1>(p, f16, stream);
+    }
+    p.tokens_per_cta = p.ch.T <= 4 * sms || fit < 1 ? 1 : fit > KA_MAX_TOKENS ? KA_MAX_TOKENS : fit;
+    return launch_append<KA_BATCH>(p, f16, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -681,6 +681,8 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
     for (int base = 0; base < units; base += U * stride) {
         int group[U], row[U];
         bool on[U];
+        const float4* o_of[U];
+        const float2* ml_of[U];
         float M[U], L[U];
         f32x2 acc[U][4];
 #pragma unroll
@@ -690,6 +692,8 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
             group[j] = on[j] ? u / rows : 0;
             const int r = on[j] ? u - group[j] * rows : 0;
             row[j] = r < rows0 ? r : PA_TILE + r - rows0;
+            o_of[j] = reinterpret_cast<const float4*>(P.part_o) + part_at(P, D, 0, row[j], 2 * group[j]);
+            ml_of[j] = P.part_ml + row[j];
             M[j] = -INFINITY, L[j] = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[j][k] = 0ull;
@@ -702,15 +706,14 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
             for (int j = 0; j < U; ++j)
 #pragma unroll
                 for (int k = 0; k < F; ++k) {
-                    const int f = fb + k, slot = f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f);
-                    ml[j][k] = make_float2(-INFINITY, 0.0f);
-                    a[j][k] = b[j][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (f < f1 && on[j]) {
-                        const float4* src = reinterpret_cast<const float4*>(P.part_o) + part_at(P, D, slot, row[j], 2 * group[j]);
-                        ml[j][k] = __ldcg(P.part_ml + (size_t)slot * P.rows_cap + row[j]);
-                        a[j][k] = __ldcg(src);
-                        b[j][k] = __ldcg(src + P.rows_cap);
-                    }
+                    // past the last piece, or the last unit, a load repeats one
+                    // and its weight is 0: no branch parts the loads
+                    const int f = min(fb + k, f1 - 1), slot = f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f);
+                    const float4* src = o_of[j] + (size_t)(uint32_t)slot * ((D / 4) * P.rows_cap);
+                    ml[j][k] = __ldcg(ml_of[j] + (uint32_t)(slot * P.rows_cap));
+                    a[j][k] = __ldcg(src);
+                    b[j][k] = __ldcg(src + P.rows_cap);
+                    if (fb + k >= f1) ml[j][k].y = 0.0f;
                 }
 #pragma unroll
             for (int j = 0; j < U; ++j) {
