@@ -666,7 +666,7 @@ __device__ __forceinline__ size_t part_at(const PagedAttnParams& P, int D, int s
 // Joins an item's pieces in their order, by the CTA that finished last. A
 // thread takes 8 columns of a row over all pieces; with few rows several
 // lanes share them, each a contiguous run of the pieces, joined at the end.
-// One online pass: the loads of 4 pieces of 2 such units are in flight together.
+// One online pass: the loads of 4 pieces of 3 such units are in flight together.
 template <int D, bool F16>
 __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Cursor& c, int first_cta, int pieces) {
     const bool pair = c.pair(P);
@@ -676,7 +676,7 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
     const int per_lane = (pieces + (1 << share) - 1) >> share;
     const int lane_of = threadIdx.x & ((1 << share) - 1);
     const int f0 = lane_of * per_lane, f1 = min(f0 + per_lane, pieces);
-    constexpr int U = 2, F = 4;  // units and pieces whose loads are in flight together
+    constexpr int U = 3, F = 4;  // units and pieces whose loads are in flight together
     const int stride = PA_SOFTMAX_THREADS >> share;
     for (int base = 0; base < units; base += U * stride) {
         int group[U], row[U];
@@ -972,6 +972,72 @@ __device__ __forceinline__ void put_columns(const PagedAttnParams& P, const RowP
     }
 }
 
+// Joins an item of few pieces by the CTA that finished last, whose own piece is
+// still in TMEM: a thread keeps to its row, takes 32 columns at a time and adds
+// the pieces in their order, its own from TMEM (the values it stored, formed
+// again) and the others' from memory. Two pieces of 128 rows: 1.6 us, where
+// join_pieces takes 6.5. cols: [col, col_end) of this thread's row; a, b and
+// sa, sb: the addresses and weights of its own O.
+constexpr int PA_FEW_PIECES = 3;
+template <int D, bool F16>
+__device__ __forceinline__ void join_few(const PagedAttnParams& P, const RowPlace& at, int first_cta, int pieces, int row, float m,
+                                         float l, int col, int col_end, uint32_t a_at, uint32_t b_at, float sa, float sb, bool both,
+                                         bool none, bool dense, int lane) {
+    const int own = (int)blockIdx.x - first_cta;
+    const auto slot_of = [&](int f) { return f == 0 ? 2 * first_cta + 1 : 2 * (first_cta + f); };
+    float2 ml[PA_FEW_PIECES];
+    float M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int f = 0; f < PA_FEW_PIECES; ++f) {
+        ml[f] = make_float2(m, l);
+        if (f < pieces && f != own) ml[f] = __ldcg(P.part_ml + (size_t)slot_of(f) * P.rows_cap + row);
+        if (f < pieces) M = fmaxf(M, ml[f].x);
+    }
+#pragma unroll
+    for (int f = 0; f < PA_FEW_PIECES; ++f) {
+        ml[f].x = f >= pieces || ml[f].y == 0.0f ? 0.0f : ex2(ml[f].x - M);
+        if (f < pieces) L = fmaf(ml[f].x, ml[f].y, L);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll 1
+    for (; col < col_end; col += 32) {
+        float acc[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] = 0.0f;
+#pragma unroll
+        for (int f = 0; f < PA_FEW_PIECES; ++f) {
+            if (f >= pieces) break;
+            const float w = ml[f].x;
+            if (f == own) {
+                uint32_t x[32], y[32];
+                tmem_ld2(a_at + col, b_at + col, x, y);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float v = none ? 0.0f : __uint_as_float(x[k]) * sa;
+                    v = both ? fmaf(__uint_as_float(y[k]), sb, v) : v;
+                    acc[k] = fmaf(w, v, acc[k]);
+                }
+            } else {
+                const float4* src = reinterpret_cast<const float4*>(P.part_o) + part_at(P, D, slot_of(f), row, col / 4);
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + k * P.rows_cap);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    acc[4 * k] = fmaf(w, v[k].x, acc[4 * k]);
+                    acc[4 * k + 1] = fmaf(w, v[k].y, acc[4 * k + 1]);
+                    acc[4 * k + 2] = fmaf(w, v[k].z, acc[4 * k + 2]);
+                    acc[4 * k + 3] = fmaf(w, v[k].w, acc[4 * k + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] *= inv;
+        store_rows<F16, 32>(P.out + at.token * P.o_ts + at.head * P.o_hs + col * 2, at.valid, dense, acc, lane);
+    }
+    if (P.lse && at.valid) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M, L);
+}
+
 // Warps 0-3 (w = 0) and 4-7 (w = 1): softmax and output.
 template <int D, bool F16>
 __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared& sh, int w,
@@ -1186,7 +1252,16 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                 if (sh.last) P.counters[first_cta] = 0;
             }
             softmax_barrier();
-            if (sh.last) join_pieces<D, F16>(P, c, first_cta, pieces);
+            if (sh.last) {
+                if (pieces > PA_FEW_PIECES) {
+                    join_pieces<D, F16>(P, c, first_cta, pieces);
+                } else if (warp_on) {
+                    const uint32_t o_base = tmem_base + lanes + 2 * PA_TILE;
+                    join_few<D, F16>(P, at, first_cta, pieces, cap_row, mt, lt, pair ? 0 : w * (D / 2), pair ? D : (w + 1) * (D / 2),
+                                     pair ? tmem_o : o_base, o_base + D, f[0] * scale, f[1] * scale, !pair && m_tiles > 1,
+                                     pair && done == 0, tile_rows > 32, lane);
+                }
+            }
             softmax_barrier();  // sh.last is read before the next item writes it
         }
     }
