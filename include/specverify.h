@@ -390,11 +390,11 @@ sv_status spec_lmhead_logits(const void* hidden, const void* W, int M, int d, in
  * starts on a multiple of 16 bytes (strides multiples of 8, 16-byte bases).
  *
  * Device-detected errors are flagged in the status word and never trap:
- *   SV_FLAG_BAD_LENGTH  cu_new not ascending within [0, T], a negative
- *     context, more tokens than the page table has room for, or more new
- *     tokens than tree nodes: the sequence is left out (nothing appended;
- *     its attention rows, if cu_new places them, are 0 with lse -inf; nothing
- *     committed).
+ *   SV_FLAG_BAD_LENGTH  a negative context, more tokens than the page table
+ *     has room for, or more new tokens than tree nodes: the sequence is left
+ *     out (nothing appended; its attention rows are 0 with lse -inf; nothing
+ *     committed). Or cu_new does not ascend within [0, T]: rows that are not
+ *     one sequence's are not appended, and no row of the call is attended.
  *   SV_FLAG_BAD_PAGE    a page outside [0, n_pages): the token is not stored
  *     or moved; attention reads zeros there.
  *   SV_FLAG_BAD_TREE    a node with a parent outside [0, node) in its chain:

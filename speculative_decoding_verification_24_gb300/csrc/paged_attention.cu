@@ -428,10 +428,12 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     return v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? mine : 0);
 }
 
-__device__ __forceinline__ int sequence_units(const PagedAttnParams& P, int b, Chunk& s, bool& bad) {
+// bad: a sequence that is left out; torn: its rows are not where rows can be.
+__device__ __forceinline__ int sequence_units(const PagedAttnParams& P, int b, Chunk& s, bool& bad, bool& torn) {
     if (b >= P.ch.B) return 0;
     s = load_chunk(P.ch, b);
     bad |= !s.ok;
+    torn |= !s.rows_ok;
     return s.ok ? units_per_head(s.n, s.ctx, P.TT) * P.ch.Hkv : 0;
 }
 
@@ -483,15 +485,23 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
     const int tid = threadIdx.x;
     const bool one_turn = ch.B <= PA_THREADS;
     Chunk s = {};
-    int mine = sequence_units(P, tid, s, bad), W;
+    bool torn = false;
+    int mine = sequence_units(P, tid, s, bad, torn), W;
     int incl = block_scan(mine, sh.scan, W);
     if (!one_turn) {
         for (int base = PA_THREADS; base < ch.B; base += PA_THREADS) {
             int total;
             __syncthreads();
-            block_scan(sequence_units(P, base + tid, s, bad), sh.scan, total);
+            block_scan(sequence_units(P, base + tid, s, bad, torn), sh.scan, total);
             W += total;
         }
+    }
+    // Where cu_new descends, sequences may overlap, and their work may be more
+    // than the host's bound on it: nothing is done.
+    if (__syncthreads_or(torn)) {
+        if (blockIdx.x == 0 && tid == 0) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
+        bad = false;
+        return false;
     }
     Shares shares = {};
     shares.W = W;
@@ -510,7 +520,7 @@ __device__ __forceinline__ bool find_share(const PagedAttnParams& P, PaShared& s
         if (!one_turn) {
             bool again = false;
             __syncthreads();
-            mine = sequence_units(P, base + tid, s, again);
+            mine = sequence_units(P, base + tid, s, again, again);
             incl = block_scan(mine, sh.scan, total);
         }
         const int excl = run + incl - mine;
@@ -1341,12 +1351,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             if (!mbar_wait(&sh.never, 0, 64)) atomicExch(&sh.err, 1);
         }
         // The CTA's registers, 384 x 168 at launch, move to the softmax threads:
-        // 256 x 208 + 128 x 88 is the same sum.
+        // 256 x 216 + 128 x 72 is the same sum.
         if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
             softmax_rows<D, F16>(P, sh, warp >> 2, q_smem, ring, tmem);
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
             if (warp == 8 || warp == 10) {
                 load_kv<D>(P, sh, smem_u32(ring), warp == 10 ? &tm_v : &tm_k, warp == 10, lane);
             } else if (warp == 9) {

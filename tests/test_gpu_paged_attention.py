@@ -240,8 +240,8 @@ def test_bad_lengths_and_pages_are_flagged():
     cu = c.args[2].clone()
     cu[1], cu[2] = 10, 3
     c.args[2], keep = cu, c.args[2]
-    c.run(out=torch.zeros_like(c.q))
-    assert int(c.status) == binding.SV_FLAG_BAD_LENGTH
+    out = c.run(out=torch.full_like(c.q, 2.0))
+    assert int(c.status) == binding.SV_FLAG_BAD_LENGTH and (out == 2).all()
     c.args[2] = keep
     # a page that is not there reads as zeros: scores 0, values 0
     table = c.args[0].clone()
@@ -256,6 +256,38 @@ def test_bad_lengths_and_pages_are_flagged():
         zeroed.k[int(kept[b, j])] = 0
         zeroed.v[int(kept[b, j])] = 0
     assert torch.equal(out, zeroed.run())
+
+
+def test_overlapping_sequences_are_refused():
+    # every other sequence claims all rows: more work than any valid call has
+    T, B = 3000, 1000
+    c = Case([(5, 1)], Hq=2, Hkv=1, D=64, seed=23)
+    q = torch.randn(T, 2, 64, device="cuda").to(BF16)
+    cu = torch.tensor([T * (b % 2) for b in range(B + 1)], dtype=torch.int32, device="cuda")
+    table = torch.zeros(B, 4000, dtype=torch.int32, device="cuda")
+    out, status = torch.full_like(q, 2.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+    spec_paged_attention(q, c.k, c.v, table, torch.full((B,), 50000, dtype=torch.int32, device="cuda"), cu, out=out,
+                         status_word=status)
+    torch.cuda.synchronize()
+    assert int(status) == binding.SV_FLAG_BAD_LENGTH and (out == 2).all()
+
+
+def test_what_is_not_finite_stays_with_the_rows_that_see_it():
+    c = Case([(200, 6), (30, 4)], Hq=4, Hkv=2, seed=24)
+    want = c.run()
+    q = c.q.clone()
+    q[2, 1], q[7, 3] = float("nan"), float("inf")
+    out = c.run(q=q)
+    lost = torch.zeros(10, 4, dtype=torch.bool, device="cuda")
+    lost[2, 1] = lost[7, 3] = True
+    assert torch.equal(torch.isnan(out).any(-1), lost) and torch.equal(out[~lost], want[~lost])
+    # a key of the chunk: the tokens before it do not see it
+    slot = 203
+    c.k[int(c.table[0, slot // 16]), slot % 16, 1] = float("nan")
+    out = c.run()
+    lost[:] = False
+    lost[3:6, 2:] = True
+    assert torch.equal(torch.isnan(out).any(-1), lost) and torch.equal(out[~lost], want[~lost])
 
 
 def test_calls_repeat_bit_for_bit_and_leave_the_workspace_ready():
