@@ -23,12 +23,25 @@
 // their (m, l, O) at the end ("split"), which for few rows halves the chain of
 // dependent steps per byte.
 //
-// Work is counted in key tiles over all (sequence, head, row tile) items in
-// that order, and every CTA takes an equal, contiguous share of the total,
-// cutting items where its share ends: one long context spreads over the whole
-// GPU, and so does a ragged batch, without the host knowing the lengths. A cut
-// item's pieces are written as (m, l, unscaled O) in fp32 and joined in order
-// by whichever CTA finishes last, so the result does not depend on timing.
+// Work is counted in key tiles (and some units per item) over all (sequence,
+// head, row tile) items in that order, and every CTA takes an equal, contiguous
+// share of the total, cutting items where its share ends: one long context
+// spreads over the whole GPU, and so does a ragged batch, without the host
+// knowing the lengths. A cut item's pieces are written as (m, l, unscaled O) in
+// fp32 and joined in order by whichever CTA finishes last, so the result does
+// not depend on timing.
+//
+// What bounds it, with 32 query and 8 kv heads of 128 in bf16 (copy rate 6789
+// GB/s, cuBLAS 1909 TFLOP/s):
+//   many rows per key: the softmax's chain. A tile's products take 1024 cycles
+//     of the tensor cores per stream, its softmax about 1650 from scores to P;
+//     two streams overlap them, at about 2900 cycles for both streams' tiles.
+//     4096 tokens over 12288: 575-595 us, 1.62-1.67 PFLOP/s, 85-88 %.
+//   few rows: HBM. 256 single tokens over up to 8192 keys each: 629-648 us,
+//     6.7-6.9 TB/s, 99-101 % of the copy rate.
+//   little work: latency. One token over 500 keys: 11 us, of which 2 find the
+//     share, 2.4 bring the first scores, and the rest is two tiles per stream,
+//     the join of the streams and the output.
 //
 // Warps: 0-3 and 4-7 softmax and output, 8 keys and 10 values (TMA, one box per
 // page or 128 tokens), 9 the products, 11 queries (TMA).
@@ -563,18 +576,8 @@ __device__ __forceinline__ void pieces_of(const Shares& w, const Cursor& c, int&
 __device__ __forceinline__ int ring_k(bool pair, int i) { return pair ? 2 * i : (i == 0 ? 0 : 2 * i - 1); }
 __device__ __forceinline__ int ring_v(bool pair, int i, int m) { return pair ? 2 * i + 1 : (i == m - 1 ? 2 * m - 1 : 2 * i + 2); }
 
-// Which query buffer a split item uses: they alternate; a pair uses both.
-// uses[k] counts the fills of buffer k so far.
-struct QueryBuffers {
-    int uses[2] = {0, 0};
-    int turn = 0;
-    __device__ __forceinline__ int begin_split() {
-        const int k = turn;
-        turn ^= 1;
-        return k;
-    }
-};
-
+// Query buffers: a pair's stream w uses buffer w; split items use one each, in
+// turn, so that the next item's queries load while this one runs.
 // A query buffer is free after two arrivals: one from each stream of a split
 // item, both from the one stream that uses it in a pair. A stream arrives when
 // its last scores have been formed; one that has no tiles here arrives only
@@ -784,12 +787,12 @@ __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Curs
 // ---------------------------------------------------------------------------
 // Warps 8 and 10: keys and values. A tile is 128 / box boxes of `box` tokens
 // (the largest power of two that divides the page, at most 128) per 64
-// columns; a lane issues one. Issuing takes about 64 cycles a box, one lane
-// after another, so keys and values have a warp each: with pages of 16 one warp
-// for both issued a tile in 1.1 us of the 1.4 us that HBM takes to bring it
-// and held the kernel to 68 % of the copy rate. A box past the piece's last
-// key is not loaded. A page the table does not have reads as zeros (a page
-// coordinate past the last one).
+// columns; a lane issues one. A warp issues its boxes one lane after another,
+// so keys and values have a warp each: 256 contexts in pages of 16 (32 boxes of
+// 2 KB for a tile's keys and values) took 936 us with one warp for both, at 68
+// % of the copy rate, and 693 with two. A box past the piece's last key is not
+// loaded. A page the table does not have reads as zeros (a page coordinate past
+// the last one).
 template <int D>
 __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, uint32_t ring, const CUtensorMap* map,
                                         bool is_v, int lane) {
@@ -851,13 +854,14 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, u
                                        int lane) {
     using S = PaShape<D>;
     const uint32_t box_bytes = (uint32_t)(P.q_box * P.G) * 128u;
-    QueryBuffers qb;
+    int fills[2] = {0, 0}, turn = 0;
     for (Cursor c = share_of(sh); c.valid(); c.next(P)) {
         const bool pair = c.pair(P);
-        const int split_buf = pair ? 0 : qb.begin_split();
+        const int split_buf = turn;
+        if (!pair) turn ^= 1;
         for (int w = 0; w < (pair ? 2 : 1); ++w) {
             const int buf = pair ? w : split_buf;
-            const int n = qb.uses[buf]++;
+            const int n = fills[buf]++;
             if (n > 0) pa_wait(&sh.q_empty[buf], (n - 1) & 1, &sh.err);
             if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
             const int tok = c.tok0 + w * P.TT, boxes = (min(P.TT, c.tok0 + c.ntok - tok) + P.q_box - 1) / P.q_box;
@@ -1057,8 +1061,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t tmem_s = tmem_base + lanes + w * PA_TILE, tmem_o = tmem_base + lanes + 2 * PA_TILE + w * D;
     const int row_token = tid / P.G, row_head = tid - row_token * P.G;
-    QueryBuffers qb;
-    int s_count = 0, o_count = 0, ring0 = 0;
+    int s_count = 0, o_count = 0, ring0 = 0, turn = 0;
     const f32x2 cc = pack2(P.c, P.c);
     for (Cursor c = share_of(sh); c.valid(); c.next(P)) {
         const bool pair = c.pair(P);
@@ -1080,7 +1083,8 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             seen = set ? c.s.ctx : 0;
             seen_by_all = __all_sync(0xFFFFFFFFu, !at.valid || set) ? c.s.ctx : 0;
         }
-        const int buf = pair ? w : qb.begin_split();
+        const int buf = pair ? w : turn;
+        if (!pair) turn ^= 1;
         // this stream's tiles: first, first + step, ... below last
         const int step = pair ? 1 : 2;
         const int last0 = !pair ? m_tiles : max(0, min(m_tiles, tiles_of(c.s.ctx + c.tok0 + P.TT) - t0));
@@ -1123,7 +1127,6 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                             if (at0 >= 0 && at0 < 32) on |= set << at0;
                             else if (at0 < 0 && at0 > -32) on |= set >> -at0;
                         }
-                        // most blocks are seen whole by every row of the warp
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (!((on >> k) & 1u)) r[32 * q + k] = 0xFF800000u;  // -inf, whatever stood there
