@@ -542,40 +542,46 @@ _KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 _I32 = torch.int32
 
 
-def _rows(t, name, rows, heads, width, dtype):
+def _rows(t, name, rows, heads, width, dtype, index):
     """Data pointer, strides of the first two dimensions and sizes of them of a
     [rows, heads, width] tensor (any number where None) of any strides but the
-    last."""
-    n, h, w = t.shape if t.dim() == 3 else (-1, -1, -1)
+    last, on CUDA device `index`."""
+    try:
+        n, h, w = t.shape
+    except ValueError:
+        n = h = w = -1
     if w != width or (heads is not None and h != heads) or (rows is not None and n != rows):
         raise ValueError(f"{name} must be [{'T' if rows is None else rows}, {'heads' if heads is None else heads}, {width}], "
                          f"got {list(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like the cache, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on the cache's CUDA device")
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     return t.data_ptr(), st, sh, n, h
 
 
-def _int32(t, name, *shape):
+def _int32(t, name, index, *shape):
+    """Data pointer of a contiguous int32 tensor of that shape on CUDA device
+    `index`."""
     if t.dtype is not _I32:
         raise TypeError(f"{name} must be int32, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on the cache's CUDA device")
     return t.data_ptr()
 
 
 def _cache_fields(k_cache, v_cache, page_table, ctx_lens):
     """The fields of sv_kv_cache from k_cache and v_cache [n_pages, page_size,
     Hkv, D] (any strides but the last), page_table [B, max_pages] and ctx_lens
-    [B]."""
-    if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
-        raise ValueError("every tensor must live on a CUDA device")
+    [B], and the CUDA device they are on."""
+    index = k_cache.get_device()
+    if index < 0 or v_cache.get_device() != index or page_table.get_device() != index:
+        raise ValueError("k_cache, v_cache and page_table must live on one CUDA device")
     shape, torch_dtype = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, Hkv, D] and alike")
@@ -594,30 +600,26 @@ def _cache_fields(k_cache, v_cache, page_table, ctx_lens):
     if entry != 1 and max_pages > 1:
         raise ValueError("page_table must be contiguous in its last dimension")
     return (k_cache.data_ptr(), v_cache.data_ptr(), dtype, n_pages, page_size, Hkv, D, B, kp, kt, kh, vp, vt, vh,
-            page_table.data_ptr(), row if B > 1 else max_pages, max_pages, _int32(ctx_lens, "ctx_lens", B))
+            page_table.data_ptr(), row if B > 1 else max_pages, max_pages, _int32(ctx_lens, "ctx_lens", index, B)), index
 
 
-def _tree(tree_parents, B):
+def _tree(tree_parents, index, B):
     if tree_parents is None:
         return 0, 0
     N = tree_parents.shape[-1]
-    return _int32(tree_parents, "tree_parents", B, N), N
+    return _int32(tree_parents, "tree_parents", index, B, N), N
 
 
-def _stream_of(tensor, stream):
-    """The tensor's device, where it is not the current one (else None), and
-    the raw stream to launch on."""
-    index = tensor.get_device()
-    if index != torch.cuda.current_device():
-        return tensor.device, _stream(stream, tensor.device)
-    return None, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, tensor.device)
+def _raw_stream(index, stream):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, index)
 
 
-def _call(name, device, fn, *args):
-    if device is None:
+def _call(name, index, fn, *args):
+    """fn(*args) with CUDA device `index` current; raises on a status."""
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args)
     if st:
         _check(st, name)
@@ -634,29 +636,28 @@ def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None,
     one); None leaves keys and queries as they are. tree_parents [B, N]: the
     chunk is a tree, a node's position its context plus its depth. positions
     [T] int32: rotary positions of the caller's own. Returns q_out."""
-    cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
+    cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
-    kp, kt, kh, T, _ = _rows(k, "k", None, Hkv, D, dtype)
-    vp, vt, vh, _, _ = _rows(v, "v", T, Hkv, D, dtype)
+    kp, kt, kh, T, _ = _rows(k, "k", None, Hkv, D, dtype, index)
+    vp, vt, vh, _, _ = _rows(v, "v", T, Hkv, D, dtype, index)
     Hq = qp = qt = qh = op = ot = oh = 0
     if q is not None:
-        qp, qt, qh, _, Hq = _rows(q, "q", T, None, D, dtype)
+        qp, qt, qh, _, Hq = _rows(q, "q", T, None, D, dtype, index)
         if q_out is None:
             q_out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
-        op, ot, oh, _, _ = _rows(q_out, "q_out", T, Hq, D, dtype)
+        op, ot, oh, _, _ = _rows(q_out, "q_out", T, Hq, D, dtype, index)
     freq = rotary = 0
     if inv_freq is not None:
         if inv_freq.dtype is not torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous 1-D float64 CPU tensor")
-        freq, rotary = inv_freq.data_ptr(), 2 * len(inv_freq)
-    parents, N = _tree(tree_parents, B)
-    pos = 0 if positions is None else _int32(positions, "positions", T)
+        freq, rotary = inv_freq.data_ptr(), 2 * inv_freq.numel()
+    parents, N = _tree(tree_parents, index, B)
+    pos = 0 if positions is None else _int32(positions, "positions", index, T)
     status = 0 if status_word is None else _ptr(status_word)
-    cu = _int32(cu_new, "cu_new", B + 1)
-    device, raw = _stream_of(k_cache, stream)
-    _call("spec_kv_append", device, (_lib or _load()).spec_kv_append, _pack_append(
+    cu = _int32(cu_new, "cu_new", index, B + 1)
+    _call("spec_kv_append", index, (_lib or _load()).spec_kv_append, _pack_append(
         *cache, cu, T, kp, vp, kt, kh, vt, vh, Hq, qp, op, qt, qh, ot, oh, freq, rotary, 1 if interleaved else 0, parents, N,
-        pos, status, raw))
+        pos, status, _raw_stream(index, stream)))
     return q_out
 
 
@@ -703,27 +704,27 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     default. out_lse [T, Hq] float32: the rows' log of the sum of exponentials.
     workspace: spec_paged_attention_workspace; made anew when None. Returns
     out."""
-    cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
+    cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
-    qp, qt, qh, T, Hq = _rows(q, "q", None, None, D, dtype)
+    qp, qt, qh, T, Hq = _rows(q, "q", None, None, D, dtype, index)
     if out is None:
         out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
-    op, ot, oh, _, _ = _rows(out, "out", T, Hq, D, dtype)
+    op, ot, oh, _, _ = _rows(out, "out", T, Hq, D, dtype, index)
     lse = 0
     if out_lse is not None:
         if out_lse.dtype is not torch.float32 or out_lse.shape != (T, Hq):
             raise ValueError(f"out_lse must be float32 [{T}, {Hq}]")
         lse = _ptr(out_lse)
-    parents, N = _tree(tree_parents, B)
+    parents, N = _tree(tree_parents, index, B)
     if workspace is None:
         workspace = _own_workspace(T, Hq, Hkv, D, k_cache.device, stream)
     ws, ws_bytes = (0, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
     status = 0 if status_word is None else _ptr(status_word)
-    cu = _int32(cu_new, "cu_new", B + 1)
+    cu = _int32(cu_new, "cu_new", index, B + 1)
     scale = D ** -0.5 if scale is None else scale
-    device, raw = _stream_of(k_cache, stream)
-    _call("spec_paged_attention", device, (_lib or _load()).spec_paged_attention, _pack_attention(
-        *cache, cu, T, Hq, qp, op, qt, qh, ot, oh, lse, scale, parents, N, ws, ws_bytes, status, int(flags), raw))
+    _call("spec_paged_attention", index, (_lib or _load()).spec_paged_attention, _pack_attention(
+        *cache, cu, T, Hq, qp, op, qt, qh, ot, oh, lse, scale, parents, N, ws, ws_bytes, status, int(flags),
+        _raw_stream(index, stream)))
     return out
 
 
@@ -734,14 +735,14 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     tensor), and with tree_parents [B, N] and last_node [B] (as
     spec_verify_tree takes and returns them) the kept path's entries moved
     behind the context. Returns out_lens."""
-    cache = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
+    cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     B = cache[7]
     if out_lens is None:
         out_lens = torch.empty_like(ctx_lens)
-    parents, N = _tree(tree_parents, B)
-    last = None if last_node is None else _int32(last_node, "last_node", B)
-    n, lens = _int32(n_accepted, "n_accepted", B), _int32(out_lens, "out_lens", B)
+    parents, N = _tree(tree_parents, index, B)
+    last = None if last_node is None else _int32(last_node, "last_node", index, B)
+    n, lens = _int32(n_accepted, "n_accepted", index, B), _int32(out_lens, "out_lens", index, B)
     status = None if status_word is None else _ptr(status_word)
-    device, raw = _stream_of(k_cache, stream)
-    _call("spec_kv_commit", device, (_lib or _load()).spec_kv_commit, _pack_cache(*cache), n, parents, N, last, lens, status, raw)
+    _call("spec_kv_commit", index, (_lib or _load()).spec_kv_commit, _pack_cache(*cache), n, parents, N, last, lens, status,
+          _raw_stream(index, stream))
     return out_lens
