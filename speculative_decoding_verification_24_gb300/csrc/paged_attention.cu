@@ -36,7 +36,7 @@
 //   many rows per key: the softmax's chain. A tile's products take 1024 cycles
 //     of the tensor cores per stream, its softmax about 1650 from scores to P;
 //     two streams overlap them, at about 2900 cycles for both streams' tiles.
-//     4096 tokens over 12288: 575-595 us, 1.62-1.67 PFLOP/s, 85-88 %.
+//     4096 tokens over 12288: 552-595 us, 1.62-1.74 PFLOP/s, 85-91 %.
 //   few rows: HBM. 256 single tokens over up to 8192 keys each: 629-648 us,
 //     6.7-6.9 TB/s, 99-101 % of the copy rate.
 //   little work: latency. One token over 500 keys: 11 us, of which 2 find the
