@@ -73,7 +73,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t, in
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int at = lo + lane * step;
-        const uint32_t le = __ballot_sync(0xFFFFFFFFu, at < hi && __ldg(cu + at) <= t);
+        const uint32_t le = __ballot_sync(0xFFFFFFFFu, at < hi && cu[at] <= t);
         const int k = le ? 31 - __clz(le) : 0;
         const int nlo = lo + k * step;
         hi = min(hi, nlo + step);
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(KA_THREADS, BATCH > 1 ? 4 : 6) kv_append_kerne
                 }
             }
             place[warp] = pl;
-            pos_s[warp] = p.positions && mine ? __ldg(p.positions + t) : pos;
+            pos_s[warp] = p.positions && mine ? p.positions[t] : pos;
         }
     }
     __syncthreads();
@@ -297,13 +297,13 @@ __global__ void __launch_bounds__(KC_THREADS) kv_commit_kernel(const __grid_cons
     grid_dependency_wait();
     const int b = blockIdx.x;
     if (threadIdx.x < 32) {
-        const int ctx = ch.ctx[b], n = __ldg(p.n_accepted + b);  // out_lens may be ctx
+        const int ctx = ch.ctx[b], n = p.n_accepted[b];
         const long long room = (long long)ch.max_pages * ch.page_size;
         bool ok = ctx >= 0 && n >= 0 && (long long)ctx + 1 + n <= room && (!ch.parents || n < ch.N);
         if (lane == 0 && n >= 0 && !ok) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
         int moves = 0;
         if (ok && ch.parents) {
-            const int last = __ldg(p.last_node + b);
+            const int last = p.last_node[b];
             const bool in_tree = last >= 0 && last < ch.N && (long long)ctx + last < room;
             // nodes past the last one are not needed, and may be padding
             const uint32_t set = __shfl_sync(0xFFFFFFFFu, tree_sets(ch, b, in_tree ? last + 1 : 0, lane), in_tree ? last : 0);

@@ -815,7 +815,7 @@ __device__ __forceinline__ void load_kv(const PagedAttnParams& P, PaShared& sh, 
             const int key = t * PA_TILE + (my_box << box_shift);
             if (!has_box || key >= key_end) return make_int2(-1, 0);
             const int page_no = key / ch.page_size;
-            int page = __ldg(table + page_no);
+            int page = table[page_no];
             if (page < 0 || page >= ch.n_pages) {
                 raise_flag(ch.status, SV_FLAG_BAD_PAGE);
                 page = ch.n_pages;

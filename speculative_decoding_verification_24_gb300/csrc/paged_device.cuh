@@ -10,6 +10,12 @@ __device__ __forceinline__ void raise_flag(uint32_t* status, uint32_t bits) {
     if (status) atomicOr(status, bits);
 }
 
+// Lengths, tables, parents and results come from the kernels before, which may
+// still run when this one starts: they are read after the grid's wait, and by
+// plain loads, since a read-only load may use a line that was cached before.
+// (A step's commit writes the lengths that the next step's append, started
+// beside it, reads.)
+
 // One sequence's chunk: n new tokens at packed rows q0.., ctx tokens before
 // them in the cache. rows_ok: the packed rows themselves lie inside [0, T).
 // ok also asks that the tokens fit the page table and, in a tree, that there
@@ -21,8 +27,8 @@ struct Chunk {
 
 __device__ __forceinline__ Chunk load_chunk(const ChunkParams& p, int b) {
     Chunk s;
-    const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
-    s.ctx = __ldg(p.ctx + b);
+    const int lo = p.cu[b], hi = p.cu[b + 1];
+    s.ctx = p.ctx[b];
     s.q0 = lo;
     s.rows_ok = lo >= 0 && lo <= hi && hi <= p.T;
     s.n = s.rows_ok ? hi - lo : 0;
@@ -34,7 +40,7 @@ __device__ __forceinline__ Chunk load_chunk(const ChunkParams& p, int b) {
 // The page that holds slot `slot` of sequence b, or -1 (and its flag) where
 // the table has none.
 __device__ __forceinline__ int page_of(const ChunkParams& p, int b, int slot) {
-    const int page = __ldg(p.table + (int64_t)b * p.table_stride + slot / p.page_size);
+    const int page = p.table[(int64_t)b * p.table_stride + slot / p.page_size];
     if (page >= 0 && page < p.n_pages) return page;
     raise_flag(p.status, SV_FLAG_BAD_PAGE);
     return -1;
@@ -46,7 +52,7 @@ __device__ __forceinline__ int page_of(const ChunkParams& p, int b, int slot) {
 // the root; a node whose chain of parents has one outside [0, node) gets the
 // empty set, and its lane raises the flag.
 __device__ __forceinline__ uint32_t tree_sets(const ChunkParams& p, int b, int n, int lane) {
-    int up = lane > 0 && lane < n ? __ldg(p.parents + (int64_t)b * p.N + lane) : 0;
+    int up = lane > 0 && lane < n ? p.parents[(int64_t)b * p.N + lane] : 0;
     bool good = lane == 0 || lane >= n || (up >= 0 && up < lane);
     if (!good) {
         raise_flag(p.status, SV_FLAG_BAD_TREE);

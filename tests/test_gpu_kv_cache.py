@@ -220,3 +220,39 @@ def test_commit_refuses_what_does_not_fit():
     room = torch.full((4,), 400, dtype=torch.int32, device="cuda")
     assert spec_kv_commit(b.k_cache, b.v_cache, b.args[0], b.args[1], room, status_word=b.status).tolist() == [10] * 4
     assert int(b.status) == binding.SV_FLAG_BAD_LENGTH
+
+
+@pytest.mark.parametrize("B", [1, 40, 700])
+def test_steps_back_to_back_read_the_lengths_of_the_step_before(B):
+    # a graph's kernels start beside one another: append waits for the commit
+    # before it, and then has to read what that wrote
+    steps, page, Hkv, D = 40, 8, 1, 64
+    rng = np.random.default_rng(B)
+    n = rng.integers(0, 4, B).astype(np.int32)
+    need = [-(-(int(x) + 1) * steps // page) + 1 for x in n]
+    table = torch.from_numpy(make_table(need, sum(need) + 1, rng)).cuda()
+    kc, vc = (torch.zeros(sum(need) + 1, page, Hkv, D, dtype=BF16, device="cuda") for _ in range(2))
+    k, v = (torch.randn(steps, B, Hkv, D, device="cuda", generator=torch.Generator("cuda").manual_seed(B)).to(BF16) for _ in range(2))
+    ctx = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    took, status = torch.from_numpy(n).cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run():
+        for i in range(steps):
+            spec_kv_append(k[i], v[i], kc, vc, table, ctx, cu, status_word=status)
+            spec_kv_commit(kc, vc, table, ctx, took, out_lens=ctx, status_word=status)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    at = torch.arange(steps)[:, None] * (torch.from_numpy(n) + 1)[None]  # slot of each step's token
+    pages, rows = table.cpu().gather(1, (at // page).T).T.long(), at % page
+    for _ in range(5):
+        kc.zero_(), vc.zero_(), ctx.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(status) == 0 and torch.equal(ctx.cpu(), torch.from_numpy((n + 1) * steps))
+        for cache, x in ((kc, k), (vc, v)):
+            got = cache.cpu()
+            assert torch.equal(got[pages, rows], x.cpu())
+            got[pages, rows] = 0
+            assert (got == 0).all()
