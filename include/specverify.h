@@ -497,10 +497,9 @@ size_t spec_paged_attention_workspace_bytes(int T, int Hq, int Hkv, int D);
  * ancestors and t itself (tree). Scores, the softmax's maximum and sum and the
  * output accumulate in fp32; the weights are rounded to the cache's dtype
  * before they meet v, and the output is rounded once. Entries past a
- * sequence's last token may hold anything. A key or value that is not finite
- * at a slot that some token of the chunk sees may reach other tokens of the
- * chunk (weight 0 times infinity). Results do not depend on timing. T == 0
- * enqueues nothing. */
+ * sequence's last token may hold anything, and a key or value that is not
+ * finite reaches the tokens that see its slot and no others. Results do not
+ * depend on timing. T == 0 enqueues nothing. */
 sv_status spec_paged_attention(const sv_paged_attention_args* args);
 
 /* Keeps what a verify step accepted. With a chain (tree_parents NULL) the

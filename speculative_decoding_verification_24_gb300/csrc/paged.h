@@ -57,6 +57,8 @@ struct PagedAttnParams {
     char* out;
     int64_t o_ts, o_hs;      // bytes
     float* lse;              // [T, Hq] or nullptr
+    const char* vc;          // the values, for the few read by address (add_not_finite)
+    int64_t vc_ps, vc_ts, vc_hs;  // bytes
     int Hq, G, TT;           // G = Hq / Hkv; TT = tokens per 128-row tile
     int q_box;               // tokens of one copy of queries, a divisor of TT
     int box_shift;           // log2 of the rows of one copy (page_size's power of two, at most 128)

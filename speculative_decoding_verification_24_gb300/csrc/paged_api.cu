@@ -226,6 +226,8 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     p.out = static_cast<char*>(a->out);
     p.o_ts = a->out_token_stride * 2, p.o_hs = a->out_head_stride * 2;
     p.lse = a->out_lse;
+    p.vc = static_cast<const char*>(c.v);
+    p.vc_ps = c.v_page_stride * 2, p.vc_ts = c.v_token_stride * 2, p.vc_hs = c.v_head_stride * 2;
     p.Hq = a->Hq;
     p.G = G;
     p.TT = TT;

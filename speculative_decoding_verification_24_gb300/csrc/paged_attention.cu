@@ -419,7 +419,8 @@ struct PaShared {
     int loads[2][10];       // by producer and stage: phases of `full` up to its latest load
     int q_loads[2];         // the same of q_full
     uint32_t tmem;
-    int last;
+    int last;               // this CTA finished an item last (1), and add_not_finite is due (2)
+    int not_finite;         // a value that was cleared was not finite; stays set
     int err;
 };
 template <int D>
@@ -594,9 +595,58 @@ __device__ __forceinline__ float max3(float a, float b, float c) {  // drops NaN
     return r;
 }
 
-__device__ __forceinline__ uint32_t add_release_acquire(uint32_t* p) {
+// Bit 15 (31) is set where the low (high) half of a pair is not finite: an
+// exponent of all ones and one more carries into the sign's place.
+template <bool F16>
+__device__ __forceinline__ uint32_t not_finite_pair(uint32_t w) {
+    constexpr uint32_t EXP = F16 ? 0x7C007C00u : 0x7F807F80u, ONE = F16 ? 0x04000400u : 0x00800080u;
+    return ((w & EXP) + ONE) & 0x80008000u;
+}
+
+// A tile of values, by `threads` threads of a stream: rows from r0 on lie past
+// the last key and hold whatever the page does, and weight 0 times infinity is
+// not 0, so they become 0; rows from r1 on are not seen by every row of the
+// item, and what is not finite there becomes 0 (see add_not_finite).
+template <int D, bool F16>
+__device__ __forceinline__ void clean_values(uint4* tile, int r1, int r0, int* not_finite, int thread, int threads) {
+    constexpr int SLABS = D / 64, SLAB = PA_SLAB_BYTES / 16;
+#pragma unroll 1
+    for (int x = r1 * 8 + thread; x < r0 * 8; x += threads) {
+        uint4 v[SLABS];
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < SLABS; ++j) v[j] = tile[j * SLAB + x];
+#pragma unroll
+        for (int j = 0; j < SLABS; ++j)
+            bad |= (not_finite_pair<F16>(v[j].x) | not_finite_pair<F16>(v[j].y) | not_finite_pair<F16>(v[j].z) | not_finite_pair<F16>(v[j].w)) != 0;
+        if (!bad) continue;
+        *(volatile int*)not_finite = 1;
+#pragma unroll 1
+        for (int k = 0; k < SLABS * 4; ++k) {
+            uint32_t* u = reinterpret_cast<uint32_t*>(tile + (k / 4) * SLAB + x) + k % 4;
+            const uint32_t n = not_finite_pair<F16>(*u);
+            *u &= ((n & 0x8000u) ? 0u : 0xFFFFu) | ((n >> 31) ? 0u : 0xFFFF0000u);
+        }
+    }
+#pragma unroll 1
+    for (int x = r0 * 8 + thread; x < PA_TILE * 8; x += threads)
+#pragma unroll
+        for (int j = 0; j < SLABS; ++j) tile[j * SLAB + x] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+}
+
+// From which token of the chunk on a key may be one that a row of the item that
+// begins with token tok0 does not see.
+// (The tiles that hold such keys, and the last one, are cleaned by the warps
+// that have no rows, if there are any, while the others go on: one token over
+// 500 keys 11.05 us, 11.35 when all clean first. Where all have rows their scan
+// costs 3 % of a prompt of 4096 tokens, which has many short items, and nothing
+// measurable of the same over 12288.)
+__device__ __forceinline__ int mixed_from(const ChunkParams& ch, int tok0) { return ch.parents ? 1 : tok0 + 1; }
+
+__device__ __forceinline__ uint32_t add_release_acquire(uint32_t* p, uint32_t x) {
     uint32_t before;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p) : "memory");
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before) : "l"(p), "r"(x) : "memory");
     return before;
 }
 
@@ -606,6 +656,11 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ float to_float(uint16_t x) {
+    return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
 }
 
 // N values of each lane's output row, rounded once. A lane's row is a line of
@@ -972,6 +1027,57 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
     }
 }
 
+// A value of the chunk that is not finite is no business of the rows that do
+// not see it, but in the product their weight 0 makes NaN of it. So it is
+// cleared in the tile, where rows exist that do not see it, and added here to
+// the rows that do: as their weight is positive, out + value is what the sum
+// with it gives. A rare path, which a CTA takes for all its items from the
+// first such value on: everything is found again from the item, and nothing of
+// the usual path is kept for it. A node of a broken tree sees nothing, but
+// the product had its weight 0 meet the whole context: its row becomes 0. A warp's lanes take their rows; of a split
+// item warpgroup w takes half of the columns, as it wrote them.
+template <int D, bool F16>
+__device__ __noinline__ void add_not_finite(const PagedAttnParams& P, int b, int h, int q0, int n, int ctx, int tok0, int ntok, int w) {
+    const ChunkParams& ch = P.ch;
+    const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const bool pair = ntok > P.TT;
+    const int i = tid / P.G, g = tid - i * P.G, node = tok0 + (pair ? w * P.TT : 0) + i;
+    const bool valid = i < P.TT && node < tok0 + ntok;
+    uint32_t set = 0;
+    if (ch.parents) set = __shfl_sync(0xFFFFFFFFu, tree_sets(ch, b, n, lane), valid ? node : 0);
+    if (!valid) return;
+    const int key_end = ctx + tok0 + ntok;
+    const bool broken = ch.parents && set == 0;
+    char* out = P.out + (int64_t)(q0 + node) * P.o_ts + (h * P.G + g) * P.o_hs;
+    for (int col = pair ? 0 : w * (D / 2); col < (pair ? D : (w + 1) * (D / 2)); col += 8) {
+        if (broken) {
+            *reinterpret_cast<uint4*>(out + col * 2) = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        float sum[8] = {};
+        uint32_t hit = 0;
+        for (int j = ctx + mixed_from(ch, tok0); j < key_end; ++j) {
+            if (ch.parents ? !(set >> (j - ctx) & 1u) : j > ctx + node) continue;
+            const int page = ch.table[(int64_t)b * ch.table_stride + j / ch.page_size];
+            if (page < 0 || page >= ch.n_pages) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(P.vc + page * P.vc_ps + (j % ch.page_size) * P.vc_ts + h * P.vc_hs + col * 2);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (!(not_finite_pair<F16>(u[k / 2]) >> (k % 2 ? 31 : 15) & 1u)) continue;
+                sum[k] += to_float<F16>((uint16_t)(u[k / 2] >> (k % 2 ? 16 : 0)));
+                hit |= 1u << k;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (!(hit >> k & 1u)) continue;
+            uint16_t* o = reinterpret_cast<uint16_t*>(out) + col + k;
+            *o = (uint16_t)pack_pair<F16>(to_float<F16>(*o) + sum[k], 0.0f);
+        }
+    }
+}
+
 // Half of a row's columns, to the output or, of a cut item, to this CTA's piece.
 template <int D, bool F16>
 __device__ __forceinline__ void put_columns(const PagedAttnParams& P, const RowPlace& at, bool whole, int slot, int row, int col,
@@ -1092,6 +1198,11 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         float m = -INFINITY;
         f32x2 l2 = pack2(0.0f, 0.0f);
         int done = 0;
+        // From this tile on there are values that no row, or not every row, sees;
+        // the stream whose product reads a tile first cleans it: the warps that
+        // have no rows, while the others go on, or all of them.
+        const int clean_from = max(pair && w == 1 ? last0 : 0, (c.s.ctx + mixed_from(P.ch, c.tok0)) / PA_TILE - t0);
+        const int cleaner = tile_rows > PA_TILE - 32 ? 0 : (tile_rows + 31) / 32;  // the first warp that does
         for (int i = pair ? 0 : w; i < last; i += step, ++done) {
             pa_wait(&sh.s_full[w], s_count & 1, &sh.err);
             ++s_count;
@@ -1099,20 +1210,13 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             const int key0 = (t0 + i) * PA_TILE;
             // this stream's last scores have been formed: it needs Q no more
             if (i + step >= last && tid == 0) release_q(&sh.q_empty[buf], pair);
-            // Entries past the last key are whatever the page holds, and weight
-            // 0 times infinity is not 0: they are cleared, by the stream whose
-            // product reads the tile first. (Here and not between the two halves
-            // of P: with the scores in registers it cost the loop 5 %.)
-            if (key0 + PA_TILE > key_end && (!pair || w == 0 || last0 < m_tiles)) {
+            if (i >= clean_from && warp >= cleaner) {
                 const int e = ring0 + ring_v(pair, i, m_tiles), s = e % S::STAGES;
                 pa_wait(&sh.full[s], (e / S::STAGES) & 1, &sh.err);
-                const int r0 = key_end - key0, per_slab = (PA_TILE - r0) * 8;
-#pragma unroll
-                for (int slab = 0; slab < S::SLABS; ++slab)
-                    for (int x = tid; x < per_slab; x += 128)
-                        *reinterpret_cast<uint4*>(ring + s * S::TILE_BYTES + slab * PA_SLAB_BYTES + r0 * 128 + x * 16) =
-                            make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
+                clean_values<D, F16>(reinterpret_cast<uint4*>(ring + s * S::TILE_BYTES),
+                                     max(c.s.ctx + mixed_from(P.ch, c.tok0) - key0, 0), min(key_end - key0, PA_TILE), &sh.not_finite,
+                                     tid - 32 * cleaner, 128 - 32 * cleaner);
+                __syncwarp();
             }
             if (warp_on) {
                 uint32_t r[PA_TILE];
@@ -1187,6 +1291,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[w]);
+            
         }
         ring0 += 2 * m_tiles;
         float l;
@@ -1252,6 +1357,8 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         // item's products may overwrite it
         tc_fence_before();
         if (!pair) softmax_barrier();
+        // whether the rows written here miss what add_not_finite adds
+        bool written = whole, rest = whole && *(volatile int*)&sh.not_finite;
         if (!whole) {
             int first_cta, pieces;
             pieces_of(sh.shares, c, first_cta, pieces);
@@ -1260,12 +1367,15 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             if (threadIdx.x == 0) {
                 // the barrier has brought every thread's rows to this one; its
                 // release passes them on, its acquire brings the others'
-                const uint32_t before = add_release_acquire(P.counters + first_cta);
-                sh.last = before == (uint32_t)(pieces - 1);
+                // (one piece more, and above them how many found values to add)
+                const uint32_t found = *(volatile int*)&sh.not_finite ? 1u << 16 : 0u;
+                const uint32_t before = add_release_acquire(P.counters + first_cta, 1u + found);
+                sh.last = (before & 0xFFFFu) != (uint32_t)(pieces - 1) ? 0 : (before + found) >> 16 ? 3 : 1;
                 if (sh.last) P.counters[first_cta] = 0;
             }
             softmax_barrier();
-            if (sh.last) {
+            const int joins = sh.last;
+            if (joins) {
                 if (pieces > PA_FEW_PIECES) {
                     join_pieces<D, F16>(P, c, first_cta, pieces);
                 } else if (warp_on) {
@@ -1275,8 +1385,13 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                                      pair && done == 0, tile_rows > 32, lane);
                 }
             }
-            softmax_barrier();  // sh.last is read before the next item writes it
+            softmax_barrier();  // sh.last is read before the next item writes it, and the rows are written
+            written = joins != 0;
+            rest = (joins & 2) != 0;
         }
+        // (seen_by_all < ctx: a node of a broken tree, which is no warp's usual row)
+        if (__any_sync(0xFFFFFFFFu, rest || (written && seen_by_all < c.s.ctx)))
+            add_not_finite<D, F16>(P, c.b, c.h, c.s.q0, c.s.n, c.s.ctx, c.tok0, c.ntok, w);
     }
 }
 
@@ -1326,7 +1441,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         mbar_init(&sh.never, 1);
         for (int s = 0; s < 10; ++s) sh.loads[0][s] = sh.loads[1][s] = 0;
         sh.q_loads[0] = sh.q_loads[1] = 0;
-        sh.err = 0;
+        sh.err = sh.not_finite = 0;
         fence_barrier_init();
     }
     if (warp == 8 && lane < 3)

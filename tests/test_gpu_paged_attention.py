@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from paged_reference import attention, make_cache, make_table
+from paged_reference import attention, make_cache, make_table, path_to
 from speculative_decoding_verification_24_gb300 import binding, spec_paged_attention, spec_paged_attention_workspace
 from speculative_decoding_verification_24_gb300.build import build
 
@@ -337,3 +337,54 @@ def test_a_wait_that_gives_up_is_flagged():
     ws[:binding.SV_PAGED_WORKSPACE_HEAD].zero_()
     assert torch.equal(c.run(workspace=ws), want)
     assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,dtype,tree", [
+    ([(200, 6), (30, 4), (125, 9)], 4, 2, 128, BF16, False),     # one tile of rows, tiles that the chunk straddles
+    ([(0, 9), (119, 9), (40, 1)], 8, 2, 64, FP16, False),
+    ([(60000, 9)], 8, 1, 128, BF16, False),                      # many pieces
+    ([(900, 20), (2000, 30)], 8, 2, 64, BF16, False),            # few
+    ([(0, 700), (3, 130), (1000, 300)], 8, 2, 128, BF16, False),   # two tiles of rows
+    ([(250, 1000)], 32, 1, 128, FP16, False),                    # row tiles of 4 tokens, cut
+    ([(100, 32), (30, 32), (0, 17)], 8, 2, 128, BF16, True),
+    ([(5000, 32), (96, 32)], 16, 2, 64, FP16, True),
+])
+def test_a_value_that_is_not_finite_stays_with_the_rows_that_see_it(seqs, Hq, Hkv, D, dtype, tree):
+    rng = np.random.default_rng(5)
+    parents = None
+    if tree:
+        parents = np.array([[int(rng.integers(max(0, i - 6), i)) if i else 0 for i in range(32)] for _ in seqs], np.int32)
+    c = Case(seqs, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, parents=parents, seed=31)
+    ref, bound, lse, lse_bound = attention(c.q, c.k, c.v, c.table, c.ctx, c.cu, c.page, c.scale, c.parents)
+    G = Hq // Hkv
+    extra = torch.zeros_like(ref)  # what the planted values add to the rows that see them
+    bad = [float("inf"), -float("inf"), float("nan"), float("inf")]
+    for b, (ctx, n) in enumerate(seqs):
+        for x in range(min(n, 4)):
+            node, h = int(rng.integers(0, n)), int(rng.integers(0, Hkv))
+            slot = ctx + node
+            at = (int(c.table[b, slot // 16]), slot % 16, h)
+            for col in rng.permutation(D)[:3].tolist():
+                if not np.isfinite(float(c.v[at][col])):
+                    continue
+                c.v[at][col] = bad[x]
+                for i in range(node, n):
+                    if not tree or node in path_to(parents[b], i):
+                        extra[int(c.cu[b]) + i, h * G:(h + 1) * G, col] += bad[x]
+    got = c.run().double().cpu()
+    assert int(c.status) == 0
+    clean = extra == 0
+    assert clean.any() and not clean.all()
+    assert ((got - ref).abs() <= bound)[clean].all()
+    assert torch.equal(got[~clean].nan_to_num(7.0, 8.0, 9.0), extra[~clean].nan_to_num(7.0, 8.0, 9.0))
+    assert ((c.lse.double().cpu() - lse).abs() <= lse_bound).all()
+
+
+def test_nodes_of_a_broken_tree_see_nothing_whatever_the_context_holds():
+    parents = np.array([[0, 0, 5, 2, 1, 0]], np.int32)  # nodes 2 and 3 hang on nothing
+    c = Case([(300, 6)], parents=parents, seed=32)
+    c.v[int(c.table[0, 1]), 3] = float("nan")
+    out = c.run()
+    assert int(c.status) == binding.SV_FLAG_BAD_TREE
+    assert (out[2:4] == 0).all() and torch.isneginf(c.lse[2:4]).all()
+    assert torch.isnan(out[[0, 1, 4, 5]]).all()
