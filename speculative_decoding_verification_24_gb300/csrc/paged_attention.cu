@@ -402,8 +402,9 @@ struct Shares {
     __device__ __forceinline__ int begin(int c) const { return c * size + min(c, extra); }
     // the first boundary at or past x > 0
     __device__ __forceinline__ int first_at(int x) const {
-        const int longer = extra * (size + 1);
-        return x <= longer ? (x + size) / (size + 1) : extra + (x - longer + size - 1) / size;
+        // unsigned: x + size may pass 2^31
+        const uint32_t n = (uint32_t)size, longer = (uint32_t)extra * (n + 1), u = (uint32_t)x;
+        return (int)(u <= longer ? (u + n) / (n + 1) : (uint32_t)extra + (u - longer + n - 1) / n);
     }
 };
 // A CTA gets at least this many units: below that, joining costs more than
