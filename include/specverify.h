@@ -184,8 +184,12 @@ typedef struct {
 
 /* sv_verify_args.flags: the inputs of this call are not written by the work
  * enqueued just before it on `stream`, so the call may start reading them
- * while that work (typically the previous verify call) is still running. Its
- * outputs are still written only after that work has completed. Without the
+ * while that work (typically the previous verify call) is still running. A
+ * verify call lets the next one start as soon as it has started itself: where
+ * the work just before is a verify call, the same has to hold for the work
+ * before that, and so on. Any other call of this library lets the next one
+ * start only when all work before it has completed. The call's outputs are
+ * still written only after the work before it has completed. Without the
  * flag a call starts after everything before it on the stream. Such a call
  * runs one CTA per sequence (unless cluster_size asks otherwise), two per SM,
  * so that consecutive calls share the GPU; a lone call without the flag

@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(KA_THREADS, BATCH > 1 ? 4 : 6) kv_append_kerne
     __shared__ __align__(16) float2 cs[KA_MAX_TOKENS][KV_MAX_ROTARY / 2];  // (cos, sin)
     const ChunkParams& ch = p.ch;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    launch_dependents();
     grid_dependency_wait();
+    launch_dependents();
     const int t0 = blockIdx.x * p.tokens_per_cta;
     const int nt = min(p.tokens_per_cta, ch.T - t0);
     const int heads = (p.q ? p.Hq : 0) + 2 * ch.Hkv, all = nt * heads * (D / 16);
@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(KC_THREADS) kv_commit_kernel(const __grid_cons
     __shared__ int moves_s;
     const ChunkParams& ch = p.ch;
     const int lane = threadIdx.x & 31;
-    launch_dependents();
     grid_dependency_wait();
+    launch_dependents();
     const int b = blockIdx.x;
     if (threadIdx.x < 32) {
         const int ctx = ch.ctx[b], n = p.n_accepted[b];

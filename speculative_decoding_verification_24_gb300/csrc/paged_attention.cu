@@ -1424,7 +1424,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     PaShared& sh = *reinterpret_cast<PaShared*>(smem + S::TILES_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
             mbar_init(&sh.full[s], 1);
@@ -1460,6 +1459,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     grid_dependency_wait();
+    launch_dependents();
 
     bool bad = false;
     const bool work = find_share(P, sh, bad);

@@ -215,15 +215,15 @@ __global__ void __launch_bounds__(PL_THREADS) prompt_lookup_whole_kernel(const i
     // the host), so every copy below is a whole number of 16-byte units
     // inside the sequence's row.
     const int n0 = min(PLW_TILE, L_max);
-    // The next call may launch now; this one reads its inputs only once the
-    // work ahead of it has completed (the commit step writes the contexts).
-    launch_dependents();
     if (tid == 0) {
         for (int t = 0; t < PLW_MAX_TILES; ++t) mbar_init(&bar[t], 1);
         s_err = 0;
         fence_barrier_init();
     }
+    // This call reads its inputs only once the work ahead of it has completed
+    // (the commit step writes the contexts); then the next one may launch.
     grid_dependency_wait();
+    launch_dependents();
     if (tid == 0) {
         mbar_arrive_expect_tx(&bar[0], (uint32_t)n0 * 4u);
         bulk_g2s(ctx, seq, (uint32_t)n0 * 4u, &bar[0]);
@@ -391,10 +391,10 @@ namespace sv {
 // advances its length, up to L_max. One warp per sequence (K + 1 <= 32).
 __global__ void commit_kernel(int32_t* tokens, int32_t* lengths, int B, int L_max, const int32_t* out_tokens,
                               const int32_t* n_accepted, int K, int32_t* out_n_committed) {
-    // launched early: the next call may launch now, and this one reads the
-    // verify step's outputs only once the work ahead of it has completed
-    launch_dependents();
+    // launched early: reads the verify step's outputs only once the work ahead
+    // of it has completed; then the next call may launch
     grid_dependency_wait();
+    launch_dependents();
     const int b = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (b >= B) return;
