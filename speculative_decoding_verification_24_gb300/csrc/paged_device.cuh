@@ -10,6 +10,10 @@ __device__ __forceinline__ void raise_flag(uint32_t* status, uint32_t bits) {
     if (status) atomicOr(status, bits);
 }
 
+// A kernel that waits for all work before it lets the next one start only after
+// that wait: a verify call with SV_ARG_OVERLAP_PREVIOUS reads its inputs before
+// its own wait, and the work before this kernel may have written them.
+
 // Lengths, tables, parents and results come from the kernels before, which may
 // still run when this one starts: they are read after the grid's wait, and by
 // plain loads, since a read-only load may use a line that was cached before.

@@ -82,11 +82,6 @@ __device__ __forceinline__ void cluster_wait_started() { asm volatile("barrier.c
 // Programmatic dependent launch: wait until the grids this one depends on
 // have completed and their memory is visible (returns at once when the
 // launch had no such dependency); let the next grid on the stream launch.
-// A kernel that waits for all of its work lets the next one launch only after
-// that wait: a verify call with SV_ARG_OVERLAP_PREVIOUS reads its inputs
-// before its own wait, and they may have been written by the work before this
-// kernel. (Verify kernels let it launch at their start, which the flag's
-// description says.)
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
