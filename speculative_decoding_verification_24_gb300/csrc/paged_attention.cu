@@ -14,7 +14,11 @@
 //   O += P V         tcgen05.mma, P from TMEM, V from shared memory, O in TMEM.
 // m is only raised (and O and l rescaled) when a score passes it by more than
 // 2^8: l and O share whatever m is used, so the result does not depend on it,
-// and most tiles touch no O at all.
+// and most tiles touch no O at all. In fp16 m lies 7 below the maximum: P is
+// then at most 2^15 (65504 is the largest), and a weight is off by half a step
+// of its own or 2^-32 of the row's largest (half the step of the subnormals,
+// 2^-25, over 2^7). At the maximum itself that would be 2^-25, and 131,000 keys
+// of 2^-25.2 beside one of 1 lost all of their 0.3 %, 7 half steps of the output.
 //
 // Two softmax warpgroups keep the tensor cores and the softmax busy at once:
 // while one computes P, the other's products run. A chunk of more than 128
@@ -60,7 +64,8 @@ namespace sv {
 constexpr int PA_THREADS = 384;
 constexpr int PA_SOFTMAX_THREADS = 256;
 constexpr long long PA_WAIT_CYCLES = 1ll << 31;  // a wait gives up after about a second
-constexpr float PA_RAISE = 8.0f;                 // log2 of how far a score may pass m
+constexpr float PA_RAISE = 8.0f;                 // log2 of how far the maximum may pass m (with PA_F16_BELOW)
+constexpr float PA_F16_BELOW = 7.0f;             // how far m lies below the maximum in fp16, log2
 constexpr int PA_TMEM_COLS = 512;                // S0, S1 (128 columns each), O0, O1 (D each)
 constexpr int PA_SLAB_BYTES = PA_TILE * 128;     // 128 rows of 64 elements: one 128-byte-swizzled operand block
 
@@ -1243,7 +1248,8 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
 #pragma unroll
                     for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(r[k + 2 * j]), __uint_as_float(r[k + 2 * j + 1]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.c;
+                const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const float top = F16 ? fmaf(most, P.c, -PA_F16_BELOW) : most * P.c;
                 if (done == 0) {
                     m = top;
                 } else {
@@ -1265,6 +1271,9 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                 }
                 const float mu = m == -INFINITY ? 0.0f : -m;
                 const f32x2 mm = pack2(mu, mu);
+                // a tile's weights are added up before l takes them: one by one a
+                // long context's small weights would be rounded away
+                f32x2 sum = pack2(0.0f, 0.0f);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
@@ -1272,7 +1281,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                     for (int k = 0; k < 16; ++k) {
                         const int at2 = 32 * q + 2 * k;
                         const f32x2 e = ex2x2(fma2(pack2(__uint_as_float(r[at2]), __uint_as_float(r[at2 + 1])), cc, mm));
-                        l2 = add2(l2, e);
+                        sum = at2 == 0 ? e : add2(sum, e);
                         float a, b;
                         unpack2(e, a, b);
                         pk[k] = pack_pair<F16>(a, b);
@@ -1285,6 +1294,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                         if (lane == 0) mbar_arrive(&sh.p_half[w]);
                     }
                 }
+                l2 = add2(l2, sum);
                 tmem_wait_st();
             } else if (lane == 0) {
                 mbar_arrive(&sh.p_half[w]);
