@@ -397,8 +397,10 @@ sv_status spec_lmhead_logits(const void* hidden, const void* W, int M, int d, in
  *   SV_FLAG_BAD_LENGTH  a negative context, more tokens than the page table
  *     has room for, or more new tokens than tree nodes: the sequence is left
  *     out (nothing appended; its attention rows are 0 with lse -inf; nothing
- *     committed). Or cu_new does not ascend within [0, T]: rows that are not
- *     one sequence's are not appended, and no row of the call is attended.
+ *     committed). Or cu_new does not ascend within [0, T]: sequences whose own
+ *     two offsets do not are left out by the append (their rows of q_out are
+ *     not written, and a row that two others claim is stored for one of them
+ *     at most), and no row of the call is attended.
  *   SV_FLAG_BAD_PAGE    a page outside [0, n_pages): the token is not stored
  *     or moved; attention reads zeros there.
  *   SV_FLAG_BAD_TREE    a node with a parent outside [0, node) in its chain:

@@ -182,6 +182,11 @@ __global__ void __launch_bounds__(KA_THREADS, BATCH > 1 ? 4 : 6) kv_append_kerne
             pos_s[warp] = p.positions && mine ? p.positions[t] : pos;
         }
     }
+    // A sequence whose rows are not where rows can be is flagged, whether or not
+    // a token has led to it: the grid's threads look at one each, the last first,
+    // whose warps find no places when tokens are few.
+    for (int64_t b = (int64_t)blockIdx.x * KA_THREADS + (KA_THREADS - 1 - threadIdx.x); b < ch.B; b += (int64_t)gridDim.x * KA_THREADS)
+        if (!load_chunk(ch, (int)b).rows_ok) raise_flag(ch.status, SV_FLAG_BAD_LENGTH);
     __syncthreads();
     const int half = p.rotary / 2;
     for (int x = threadIdx.x; x < nt * (KV_MAX_ROTARY / 2); x += KA_THREADS) {

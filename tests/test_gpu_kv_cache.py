@@ -256,3 +256,28 @@ def test_steps_back_to_back_read_the_lengths_of_the_step_before(B):
             assert torch.equal(got[pages, rows], x.cpu())
             got[pages, rows] = 0
             assert (got == 0).all()
+
+
+@pytest.mark.parametrize("seqs,cu,whole", [
+    ([(10, 3), (20, 4), (5, 2)], [0, 40, 7, 9], [2]),   # ends past T, then descends
+    ([(10, 3), (20, 4), (5, 2)], [-1, 3, 7, 9], [1, 2]),
+    ([(10, 3), (20, 4), (5, 2)], [0, 3, 7, 10], [0, 1]),
+    ([(0, 9), (20, 0), (5, 0)], [0, 9, 9, 4], [0]),     # no row lies in the one that descends
+    ([(0, 9)] + [(20, 0)] * 599, [0] + [9] * 599 + [8], [0]),
+])
+def test_append_flags_sequences_that_are_not_rows(seqs, cu, whole):
+    b = Batch(seqs, seed=10)
+    want_k, want_v = b.k_cache.clone(), b.v_cache.clone()
+    args = [b.args[0], b.args[1], torch.tensor(cu, dtype=torch.int32, device="cuda")]
+    q_out = torch.full_like(b.q, 7.0)
+    spec_kv_append(b.k, b.v, b.k_cache, b.v_cache, *args, q=b.q, q_out=q_out, status_word=b.status)
+    torch.cuda.synchronize()
+    assert int(b.status) == binding.SV_FLAG_BAD_LENGTH
+    rows = torch.zeros(b.q.shape[0], dtype=torch.bool, device="cuda")
+    for s in whole:
+        for i in range(cu[s + 1] - cu[s]):
+            at = int(b.table[s, (seqs[s][0] + i) // b.page]), (seqs[s][0] + i) % b.page
+            want_k[at], want_v[at] = b.k[cu[s] + i], b.v[cu[s] + i]
+            rows[cu[s] + i] = True
+    assert torch.equal(b.k_cache, want_k) and torch.equal(b.v_cache, want_v)
+    assert torch.equal(q_out[rows], b.q[rows]) and (q_out[~rows] == 7).all()
