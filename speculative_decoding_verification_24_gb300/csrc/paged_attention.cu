@@ -1040,8 +1040,9 @@ __device__ __forceinline__ void issue_products(const PagedAttnParams& P, PaShare
 // with it gives. A rare path, which a CTA takes for all its items from the
 // first such value on: everything is found again from the item, and nothing of
 // the usual path is kept for it. A node of a broken tree sees nothing, but
-// the product had its weight 0 meet the whole context: its row becomes 0. A warp's lanes take their rows; of a split
-// item warpgroup w takes half of the columns, as it wrote them.
+// the product had its weight 0 meet the whole context and the root: its row
+// becomes 0. A warp's lanes take their rows; of a split item warpgroup w takes
+// half of the columns, as it wrote them.
 template <int D, bool F16>
 __device__ __noinline__ void add_not_finite(const PagedAttnParams& P, int b, int h, int q0, int n, int ctx, int tok0, int ntok, int w) {
     const ChunkParams& ch = P.ch;
@@ -1193,7 +1194,8 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             if (!at.valid) set = 0;
             // a node with a bad chain of parents sees nothing
             seen = set ? c.s.ctx : 0;
-            seen_by_all = __all_sync(0xFFFFFFFFu, !at.valid || set) ? c.s.ctx : 0;
+            // (-1: add_not_finite is due, also where there is no context)
+            seen_by_all = __all_sync(0xFFFFFFFFu, !at.valid || set) ? c.s.ctx : -1;
         }
         const int buf = pair ? w : turn;
         if (!pair) turn ^= 1;

@@ -388,3 +388,14 @@ def test_nodes_of_a_broken_tree_see_nothing_whatever_the_context_holds():
     assert int(c.status) == binding.SV_FLAG_BAD_TREE
     assert (out[2:4] == 0).all() and torch.isneginf(c.lse[2:4]).all()
     assert torch.isnan(out[[0, 1, 4, 5]]).all()
+
+
+@pytest.mark.parametrize("Hq,value", [(8, float("nan")), (64, float("inf"))])
+def test_nodes_of_a_broken_tree_see_nothing_of_a_root_without_context(Hq, value):
+    parents = np.array([[0, 0, 5, 2, 1, 0]], np.int32)
+    c = Case([(0, 6)], Hq=Hq, parents=parents, seed=33)
+    c.v[int(c.table[0, 0]), 0] = value
+    out = c.run()
+    assert int(c.status) == binding.SV_FLAG_BAD_TREE
+    assert (out[2:4] == 0).all() and torch.isneginf(c.lse[2:4]).all()
+    assert (out[[0, 1, 4, 5]].isfinite() == 0).all()
