@@ -4,7 +4,10 @@ Every function takes torch tensors that already live on the current CUDA
 device, passes their data pointers and the current torch stream to the C ABI
 declared in include/specverify.h, and raises SpecVerifyError on a non-OK
 status. All of the verify arithmetic runs in the library's CUDA kernels; this
-module computes nothing. Missing outputs are allocated with torch.empty.
+module computes nothing. Missing outputs are allocated with torch.empty, under
+the stream of the call. Where that is not the current stream (stream=), the
+caller orders it after the work that makes the inputs, and what reads the
+outputs after it.
 """
 from __future__ import annotations
 
@@ -288,6 +291,26 @@ def _stream(stream, device):
     return int(stream)
 
 
+def _as_stream(stream, device):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _empty(shape, dtype, device, stream, zero=False):
+    """A tensor that a call on `stream` writes. It is allocated under that
+    stream: memory of the current one may still be in use by work that is
+    enqueued there, and would be handed out again there while this call writes
+    it. The current stream, which the caller goes on with, holds it too."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    stream, current = _as_stream(stream, device), torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if stream != current:
+        t.record_stream(current)
+    return t
+
+
 def spec_verify(target_logits, draft_logits, draft_tokens, temperature=1.0, mode="sample", seed=0,
                 out_tokens=None, out_n_accepted=None, stream=None):
     """Verify a batch: returns (out_tokens [B, K+1] int32, out_n_accepted [B] int32)."""
@@ -295,9 +318,9 @@ def spec_verify(target_logits, draft_logits, draft_tokens, temperature=1.0, mode
     K = K1 - 1
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty(B, K1, dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, K1), torch.int32, dev, stream)
     if out_n_accepted is None:
-        out_n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_n_accepted = _empty((B,), torch.int32, dev, stream)
     with torch.cuda.device(dev):
         st = _load().spec_verify(
             _ptr(target_logits), _ptr(draft_logits), _ptr(draft_tokens), B, K, V,
@@ -332,20 +355,20 @@ def spec_verify_ex(target_logits, draft_logits, draft_tokens, temperature=1.0, m
     dev = target_logits.device
     a = sv_verify_args()
     if out_tokens is None:
-        out_tokens = torch.empty(B, K1, dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, K1), torch.int32, dev, stream)
     if out_n_accepted is None:
-        out_n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_n_accepted = _empty((B,), torch.int32, dev, stream)
     if debug:
         if out_p_target is None:
-            out_p_target = torch.empty(B, K, dtype=torch.float32, device=dev)
+            out_p_target = _empty((B, K), torch.float32, dev, stream)
         if out_p_draft is None:
-            out_p_draft = torch.empty(B, K, dtype=torch.float32, device=dev)
+            out_p_draft = _empty((B, K), torch.float32, dev, stream)
         if out_residual_mass is None:
-            out_residual_mass = torch.empty(B, dtype=torch.float32, device=dev)
+            out_residual_mass = _empty((B,), torch.float32, dev, stream)
         if status_word is None:
-            status_word = torch.zeros(1, dtype=torch.int32, device=dev)
+            status_word = _empty((1,), torch.int32, dev, stream, zero=True)
         if out_draw_edges is None:
-            out_draw_edges = torch.empty(B, 2, dtype=torch.float32, device=dev)
+            out_draw_edges = _empty((B, 2), torch.float32, dev, stream)
     a.target_logits = _ptr(target_logits)
     a.draft_logits = _ptr(draft_logits)
     a.draft_tokens = _ptr(draft_tokens)
@@ -400,11 +423,11 @@ def spec_verify_tree(target_logits, tree_tokens, tree_parents, out_tokens=None, 
     B, N, V = target_logits.shape
     dev = target_logits.device
     if out_tokens is None:
-        out_tokens = torch.empty(B, N, dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, N), torch.int32, dev, stream)
     if out_n_accepted is None:
-        out_n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_n_accepted = _empty((B,), torch.int32, dev, stream)
     if out_last_node is None:
-        out_last_node = torch.empty(B, dtype=torch.int32, device=dev)
+        out_last_node = _empty((B,), torch.int32, dev, stream)
     with torch.cuda.device(dev):
         st = _load().spec_verify_tree(_ptr(target_logits), _dtype_code(target_logits), _ptr(tree_tokens),
                                       _ptr(tree_parents), B, N, V, _ptr(out_tokens), _ptr(out_n_accepted),
@@ -420,9 +443,9 @@ def spec_prompt_lookup(tokens, lengths, max_ngram=3, n_drafts=5, out_drafts=None
     B, L_max = tokens.shape
     dev = tokens.device
     if out_drafts is None:
-        out_drafts = torch.empty(B, n_drafts, dtype=torch.int32, device=dev)
+        out_drafts = _empty((B, n_drafts), torch.int32, dev, stream)
     if out_n_drafts is None:
-        out_n_drafts = torch.empty(B, dtype=torch.int32, device=dev)
+        out_n_drafts = _empty((B,), torch.int32, dev, stream)
     with torch.cuda.device(dev):
         st = _load().spec_prompt_lookup(_ptr(tokens), _ptr(lengths), B, L_max, int(max_ngram),
                                         int(n_drafts), _ptr(out_drafts), _ptr(out_n_drafts),
@@ -439,7 +462,7 @@ def spec_commit(tokens, lengths, out_tokens, n_accepted, out_n_committed=None, s
     K = out_tokens.shape[1] - 1
     dev = tokens.device
     if out_n_committed is None:
-        out_n_committed = torch.empty(B, dtype=torch.int32, device=dev)
+        out_n_committed = _empty((B,), torch.int32, dev, stream)
     with torch.cuda.device(dev):
         st = _load().spec_commit(_ptr(tokens), _ptr(lengths), B, L_max, _ptr(out_tokens), _ptr(n_accepted), K,
                                  _ptr(out_n_committed), _stream(stream, dev))
@@ -454,7 +477,7 @@ def spec_lmhead_logits(hidden, W, out=None, stream=None):
     V = W.shape[1]
     dev = hidden.device
     if out is None:
-        out = torch.empty(M, V, dtype=torch.float32, device=dev)
+        out = _empty((M, V), torch.float32, dev, stream)
     with torch.cuda.device(dev):
         st = _load().spec_lmhead_logits(_ptr(hidden), _ptr(W), M, d, V, _ptr(out), _stream(stream, dev))
     _check(st, "spec_lmhead_logits")
@@ -476,11 +499,11 @@ def spec_verify_lmhead(hidden, W, draft_logits, draft_tokens, temperature=1.0, m
     dev = hidden.device
     need = spec_verify_lmhead_workspace_bytes(B, K, d, V)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
     if out_tokens is None:
-        out_tokens = torch.empty(B, K1, dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, K1), torch.int32, dev, stream)
     if out_n_accepted is None:
-        out_n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_n_accepted = _empty((B,), torch.int32, dev, stream)
     ddt = _dtype_code(draft_logits) if draft_logits is not None else SV_BF16
     with torch.cuda.device(dev):
         st = (lib or _load()).spec_verify_lmhead(
@@ -504,9 +527,9 @@ def spec_verify_lmhead_noalloc(hidden, W, draft_logits, draft_tokens, temperatur
     V = W.shape[1]
     dev = hidden.device
     if out_tokens is None:
-        out_tokens = torch.empty(B, K1, dtype=torch.int32, device=dev)
+        out_tokens = _empty((B, K1), torch.int32, dev, stream)
     if out_n_accepted is None:
-        out_n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        out_n_accepted = _empty((B,), torch.int32, dev, stream)
     ddt = _dtype_code(draft_logits) if draft_logits is not None else SV_BF16
     with torch.cuda.device(dev):
         st = _load().spec_verify_lmhead_noalloc(
@@ -644,7 +667,7 @@ def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None,
     if q is not None:
         qp, qt, qh, _, Hq = _rows(q, "q", T, None, D, dtype, index)
         if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
+            q_out = _empty((T, Hq, D), dtype, q.device, stream)
         op, ot, oh, _, _ = _rows(q_out, "q_out", T, Hq, D, dtype, index)
     freq = rotary = 0
     if inv_freq is not None:
@@ -689,9 +712,7 @@ def _own_workspace(T, Hq, Hkv, D, device, stream):
         return None
     if stream is None:
         return spec_paged_attention_workspace(T, Hq, Hkv, D, device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_as_stream(stream, device)):
         return spec_paged_attention_workspace(T, Hq, Hkv, D, device)
 
 
@@ -708,7 +729,7 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
     qp, qt, qh, T, Hq = _rows(q, "q", None, None, D, dtype, index)
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
+        out = _empty((T, Hq, D), dtype, q.device, stream)
     op, ot, oh, _, _ = _rows(out, "out", T, Hq, D, dtype, index)
     lse = 0
     if out_lse is not None:
@@ -738,7 +759,7 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     B = cache[7]
     if out_lens is None:
-        out_lens = torch.empty_like(ctx_lens)
+        out_lens = _empty((B,), _I32, ctx_lens.device, stream)
     parents, N = _tree(tree_parents, index, B)
     last = None if last_node is None else _int32(last_node, "last_node", index, B)
     n, lens = _int32(n_accepted, "n_accepted", index, B), _int32(out_lens, "out_lens", index, B)
