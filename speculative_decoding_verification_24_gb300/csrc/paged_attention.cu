@@ -1048,6 +1048,7 @@ __device__ __noinline__ void add_not_finite(const PagedAttnParams& P, int b, int
     const ChunkParams& ch = P.ch;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
     const bool pair = ntok > P.TT;
+    __syncwarp();  // store_rows may have had other lanes write this lane's row
     const int i = tid / P.G, g = tid - i * P.G, node = tok0 + (pair ? w * P.TT : 0) + i;
     const bool valid = i < P.TT && node < tok0 + ntok;
     uint32_t set = 0;

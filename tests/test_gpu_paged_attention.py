@@ -399,3 +399,19 @@ def test_nodes_of_a_broken_tree_see_nothing_of_a_root_without_context(Hq, value)
     assert int(c.status) == binding.SV_FLAG_BAD_TREE
     assert (out[2:4] == 0).all() and torch.isneginf(c.lse[2:4]).all()
     assert (out[[0, 1, 4, 5]].isfinite() == 0).all()
+
+
+def test_rows_written_by_other_lanes_take_what_is_not_finite():
+    # two row tiles, whole, full: a row's pieces are stored by the lanes of its
+    # group and read back by its own
+    c = Case([(0, 64)] * 200, Hq=4, Hkv=1, D=128, seed=34, dirty=False)
+    want = c.run().clone()
+    col = torch.arange(0, 128, 9, device="cuda")
+    at = torch.from_numpy(c.table[:, 2]).cuda().long()  # slot 40 of each sequence
+    c.v[at[:, None], 8, 0, col] = float("inf")
+    out = c.run().view(200, 64, 4, 128)
+    seen = torch.zeros_like(out, dtype=torch.bool)
+    seen[:, 40:, :, col] = True
+    assert (out[seen] == float("inf")).all()
+    assert torch.equal(out[:, :40], want.view(200, 64, 4, 128)[:, :40])
+    assert torch.isfinite(out[~seen]).all()
