@@ -598,6 +598,25 @@ def _int32(t, name, index, *shape):
     return t.data_ptr()
 
 
+def _plain(t, name, index):
+    """Data pointer of a contiguous tensor on CUDA device `index`."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on the cache's CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _status(t, index):
+    if t is None:
+        return 0
+    if t.dtype is not _I32 and t.dtype is not torch.uint32:
+        raise TypeError(f"status_word must be int32 or uint32, got {t.dtype}")
+    if t.numel() == 0:
+        raise ValueError("status_word has no element")
+    return _plain(t, "status_word", index)
+
+
 def _cache_fields(k_cache, v_cache, page_table, ctx_lens):
     """The fields of sv_kv_cache from k_cache and v_cache [n_pages, page_size,
     Hkv, D] (any strides but the last), page_table [B, max_pages] and ctx_lens
@@ -676,7 +695,7 @@ def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None,
         freq, rotary = inv_freq.data_ptr(), 2 * inv_freq.numel()
     parents, N = _tree(tree_parents, index, B)
     pos = 0 if positions is None else _int32(positions, "positions", index, T)
-    status = 0 if status_word is None else _ptr(status_word)
+    status = _status(status_word, index)
     cu = _int32(cu_new, "cu_new", index, B + 1)
     _call("spec_kv_append", index, (_lib or _load()).spec_kv_append, _pack_append(
         *cache, cu, T, kp, vp, kt, kh, vt, vh, Hq, qp, op, qt, qh, ot, oh, freq, rotary, 1 if interleaved else 0, parents, N,
@@ -735,12 +754,12 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     if out_lse is not None:
         if out_lse.dtype is not torch.float32 or out_lse.shape != (T, Hq):
             raise ValueError(f"out_lse must be float32 [{T}, {Hq}]")
-        lse = _ptr(out_lse)
+        lse = _plain(out_lse, "out_lse", index)
     parents, N = _tree(tree_parents, index, B)
     if workspace is None:
         workspace = _own_workspace(T, Hq, Hkv, D, k_cache.device, stream)
-    ws, ws_bytes = (0, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
-    status = 0 if status_word is None else _ptr(status_word)
+    ws, ws_bytes = (0, 0) if workspace is None else (_plain(workspace, "workspace", index), workspace.numel() * workspace.element_size())
+    status = _status(status_word, index)
     cu = _int32(cu_new, "cu_new", index, B + 1)
     scale = D ** -0.5 if scale is None else scale
     _call("spec_paged_attention", index, (_lib or _load()).spec_paged_attention, _pack_attention(
@@ -763,7 +782,7 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     parents, N = _tree(tree_parents, index, B)
     last = None if last_node is None else _int32(last_node, "last_node", index, B)
     n, lens = _int32(n_accepted, "n_accepted", index, B), _int32(out_lens, "out_lens", index, B)
-    status = None if status_word is None else _ptr(status_word)
+    status = _status(status_word, index)
     _call("spec_kv_commit", index, (_lib or _load()).spec_kv_commit, _pack_cache(*cache), n, parents, N, last, lens, status,
           _raw_stream(index, stream))
     return out_lens

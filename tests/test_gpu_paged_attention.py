@@ -415,3 +415,16 @@ def test_rows_written_by_other_lanes_take_what_is_not_finite():
     assert (out[seen] == float("inf")).all()
     assert torch.equal(out[:, :40], want.view(200, 64, 4, 128)[:, :40])
     assert torch.isfinite(out[~seen]).all()
+
+
+@pytest.mark.parametrize("kw,error", [
+    (dict(workspace=torch.zeros(1 << 24, dtype=torch.uint8)), "workspace must live"),
+    (dict(out_lse=torch.zeros(3, 8)), "out_lse must live"),
+    (dict(status_word=torch.zeros(1, dtype=torch.int32)), "status_word must live"),
+    (dict(status_word=torch.zeros(0, dtype=torch.int32)), "no element"),
+    (dict(status_word=torch.zeros(1)), "int32"),
+])
+def test_tensors_that_do_not_belong_are_refused(kw, error):
+    c = Case([(20, 3)], seed=35)
+    with pytest.raises((ValueError, TypeError), match=error):
+        spec_paged_attention(c.q, c.k, c.v, *c.args, **kw)

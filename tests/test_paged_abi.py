@@ -150,3 +150,23 @@ def test_binding_checks_its_tensors(lib):
                  lambda: spec_kv_commit(cache, cache, ints.view(1, 3), ints[:1], ints[:1])):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_binding_checks_status_and_plain_tensors():
+    one = torch.zeros(1, dtype=torch.int32)
+    assert binding._status(None, 0) == 0
+    for bad in (one.float(), one.long(), one.to(torch.uint8)):
+        with pytest.raises(TypeError, match="status_word"):
+            binding._status(bad, 0)
+    with pytest.raises(ValueError, match="no element"):
+        binding._status(one[:0], 0)
+    for good in (one, one.view(torch.uint32), one.view(()), torch.zeros(4, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="CUDA device"):  # of a device that is not the cache's
+            binding._status(good, 0)
+        assert binding._status(good, -1) == good.data_ptr()
+    x = torch.zeros(4, 6)
+    with pytest.raises(ValueError, match="workspace must live"):
+        binding._plain(x, "workspace", 0)
+    with pytest.raises(ValueError, match="out_lse must be contiguous"):
+        binding._plain(x.t(), "out_lse", -1)
+    assert binding._plain(x, "workspace", -1) == x.data_ptr()
