@@ -678,6 +678,8 @@ def spec_kv_append(k, v, k_cache, v_cache, page_table, ctx_lens, cu_new, q=None,
     one); None leaves keys and queries as they are. tree_parents [B, N]: the
     chunk is a tree, a node's position its context plus its depth. positions
     [T] int32: rotary positions of the caller's own. Returns q_out."""
+    if q is None and q_out is not None:
+        raise ValueError("q_out is given without q")
     cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     Hkv, D, B, dtype = cache[5], cache[6], cache[7], k_cache.dtype
     kp, kt, kh, T, _ = _rows(k, "k", None, Hkv, D, dtype, index)

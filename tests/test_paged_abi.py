@@ -152,6 +152,14 @@ def test_binding_checks_its_tensors(lib):
             call()
 
 
+def test_binding_refuses_an_output_of_queries_that_are_not_given():
+    from speculative_decoding_verification_24_gb300 import spec_kv_append
+    cache, ints = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    k = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q_out is given without q"):
+        spec_kv_append(k, k, cache, cache, ints.view(1, 3), ints[:1], ints[:2], q_out=k)
+
+
 def test_binding_checks_status_and_plain_tensors():
     one = torch.zeros(1, dtype=torch.int32)
     assert binding._status(None, 0) == 0
