@@ -392,6 +392,8 @@ sv_status spec_lmhead_logits(const void* hidden, const void* W, int M, int d, in
  *
  * Strides are in elements. Rows of D elements are contiguous; every row
  * starts on a multiple of 16 bytes (strides multiples of 8, 16-byte bases).
+ * A stride of 0 over more than one token, head or page is taken for the
+ * append's inputs only.
  *
  * Device-detected errors are flagged in the status word and never trap:
  *   SV_FLAG_BAD_LENGTH  a negative context, more tokens than the page table

@@ -19,6 +19,9 @@ using sv::fail_cuda;
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < (int64_t(1) << 38); }
 
+// Entries of their own: what is broadcast cannot be written.
+bool apart(int64_t stride, int extent) { return stride > 0 || extent <= 1; }
+
 sv_status check_cache(const sv_kv_cache& c) {
     if (!c.k || !c.v || !c.page_table || !c.ctx_lens) return SV_ERR_NULL;
     if (c.dtype != SV_BF16 && c.dtype != SV_F16) return SV_ERR_DTYPE;
@@ -31,8 +34,6 @@ sv_status check_cache(const sv_kv_cache& c) {
     if (!stride_ok(c.k_page_stride) || !stride_ok(c.k_token_stride) || !stride_ok(c.k_head_stride) ||
         !stride_ok(c.v_page_stride) || !stride_ok(c.v_token_stride) || !stride_ok(c.v_head_stride))
         return SV_ERR_ALIGN;
-    // entries of their own: a broadcast cache cannot be written
-    const auto apart = [](int64_t stride, int extent) { return stride > 0 || extent == 1; };
     if (!apart(c.k_page_stride, c.n_pages) || !apart(c.k_token_stride, c.page_size) || !apart(c.k_head_stride, c.Hkv) ||
         !apart(c.v_page_stride, c.n_pages) || !apart(c.v_token_stride, c.page_size) || !apart(c.v_head_stride, c.Hkv))
         return SV_ERR_SHAPE;
@@ -160,6 +161,7 @@ extern "C" sv_status spec_kv_append(const sv_kv_append_args* a) {
         (a->q && (!stride_ok(a->q_token_stride) || !stride_ok(a->q_head_stride) || !stride_ok(a->q_out_token_stride) ||
                   !stride_ok(a->q_out_head_stride))))
         return SV_ERR_ALIGN;
+    if (a->q && (!apart(a->q_out_token_stride, a->T) || !apart(a->q_out_head_stride, a->Hq))) return SV_ERR_SHAPE;
     for (int i = 0; i < a->rotary / 2; ++i)
         if (!std::isfinite(a->inv_freq[i])) return SV_ERR_CONFIG;
     int sms = 0;
@@ -213,7 +215,10 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     if (!stride_ok(a->q_token_stride) || !stride_ok(a->q_head_stride) || !stride_ok(a->out_token_stride) ||
         !stride_ok(a->out_head_stride))
         return SV_ERR_ALIGN;
-    if ((a->T > 1 && a->q_token_stride == 0) || (a->Hq > 1 && a->q_head_stride == 0)) return SV_ERR_SHAPE;
+    // (queries: a tensor map has no stride of 0)
+    if (!apart(a->q_token_stride, a->T) || !apart(a->q_head_stride, a->Hq) || !apart(a->out_token_stride, a->T) ||
+        !apart(a->out_head_stride, a->Hq))
+        return SV_ERR_SHAPE;
     if (a->T > 0 &&
         (!a->workspace || a->workspace_bytes < spec_paged_attention_workspace_bytes(a->T, a->Hq, c.Hkv, c.D)))
         return SV_ERR_WORKSPACE;

@@ -178,3 +178,22 @@ def test_binding_checks_status_and_plain_tensors():
     with pytest.raises(ValueError, match="out_lse must be contiguous"):
         binding._plain(x.t(), "out_lse", -1)
     assert binding._plain(x, "workspace", -1) == x.data_ptr()
+
+
+@pytest.mark.parametrize("name", ["out_token_stride", "out_head_stride", "q_token_stride", "q_head_stride"])
+def test_attention_refuses_rows_without_places_of_their_own(lib, name):
+    assert lib.spec_paged_attention(ctypes.byref(attention_args(**{name: 0}))) == SHAPE
+    # one token or head has no next one (no workspace: the next check)
+    one = dict(T=1) if "token" in name else dict(Hq=1)
+    cache_changes = {} if "token" in name else dict(Hkv=1)
+    assert lib.spec_paged_attention(ctypes.byref(attention_args(cache_changes, workspace=None, **one, **{name: 0}))) == WORKSPACE
+
+
+@pytest.mark.parametrize("name", ["q_out_token_stride", "q_out_head_stride"])
+def test_append_refuses_rows_without_places_of_their_own(lib, name):
+    assert lib.spec_kv_append(ctypes.byref(append_args(**{name: 0}))) == SHAPE
+    one = dict(T=1) if "token" in name else dict(Hq=1)
+    bad = (ctypes.c_double * 64)(*([float("nan")] * 64))  # the next check
+    assert lib.spec_kv_append(ctypes.byref(append_args(**one, **{name: 0}, inv_freq=ctypes.addressof(bad)))) == CONFIG
+    for read in ("k_token_stride", "v_head_stride", "q_token_stride"):
+        assert lib.spec_kv_append(ctypes.byref(append_args(**{read: 0}, inv_freq=ctypes.addressof(bad)))) == CONFIG
