@@ -457,8 +457,9 @@ typedef struct {
 
 /* Appends the chunk: k and q rotated by their positions (a cos - b sin, b cos
  * + a sin, in fp32, rounded once), v as it is. The angle is exact to 2^-24
- * turns at any int32 position. Slots are not checked for sharing: sequences
- * of the batch must not write the same entry. T == 0 enqueues nothing. */
+ * turns at any int32 position and any frequency up to 2^40. Slots are not
+ * checked for sharing: sequences of the batch must not write the same entry.
+ * T == 0 enqueues nothing. */
 sv_status spec_kv_append(const sv_kv_append_args* args);
 
 /* CTAs (and so pieces of work) of one attention call at most. */

@@ -120,12 +120,21 @@ bool encode_queries(CUtensorMap* map, const sv_paged_attention_args& a, int toke
     return encode(map, a.cache.dtype, a.q, 3, extents, strides, boxes);
 }
 
-// 2^64 times the fraction of a turn that w radians are.
+// 2^64 times the fraction of a turn that t turns are, modulo 2^64.
+uint64_t fixed_turns(double t) {
+    const double whole = std::fabs(t), x = (whole - std::floor(whole)) * 18446744073709551616.0;  // below 2^64, exact
+    return t < 0.0 ? 0 - (uint64_t)x : (uint64_t)x;
+}
+
+// The same of w radians. A position multiplies the error by up to 2^31, so 1 /
+// 2 pi is taken in two parts and the product with what its rounding dropped:
+// with one double each, 2^31 positions were off by 2^-24 turns at w = 1 and by
+// 2^-18 at w = 100.
 uint64_t turn_fraction(double w) {
-    double t = w * 0.15915494309189535;  // 1 / 2 pi
-    t -= std::floor(t);
-    const double x = t * 18446744073709551616.0;  // 2^64: exact
-    return x >= 18446744073709551616.0 ? 0 : (uint64_t)x;
+    constexpr double high = 0x1.45f306dc9c883p-3, low = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    const volatile double rounded = w * high;  // volatile: not contracted with what follows
+    const double t = rounded;
+    return fixed_turns(t) + fixed_turns(std::fma(w, high, -t) + w * low);
 }
 
 // Rows of one piece: a tile of 128 or, when a sequence may have more rows, a

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from paged_reference import make_cache, make_table, path_to, rotate, rotate_bound
+from paged_reference import angle_far, make_cache, make_table, path_to, rotate, rotate_bound
 from speculative_decoding_verification_24_gb300 import binding, rope_inv_freq, spec_kv_append, spec_kv_commit
 from speculative_decoding_verification_24_gb300.build import build
 
@@ -281,3 +281,25 @@ def test_append_flags_sequences_that_are_not_rows(seqs, cu, whole):
             rows[cu[s] + i] = True
     assert torch.equal(b.k_cache, want_k) and torch.equal(b.v_cache, want_v)
     assert torch.equal(q_out[rows], b.q[rows]) and (q_out[~rows] == 7).all()
+
+
+def test_append_angles_at_far_positions_of_any_frequency():
+    # x = (1, 0) gives (cos, sin); near a multiple of pi the sine shows the
+    # angle's own error, 2^-24 turns at most (2 pi 2^-24 < 2^-21)
+    rng = np.random.default_rng(12)
+    f = np.concatenate([rng.uniform(0, 1, 24), 10.0 ** rng.uniform(0, 6, 24), -10.0 ** rng.uniform(-8, 6, 16)])
+    T = 400
+    pos = rng.integers(2 ** 20, 2 ** 31, T) * rng.choice([-1, 1], T)
+    b = Batch([(0, T)], Hq=1, Hkv=1, dtype=FP16, seed=12)
+    b.k.zero_(), b.q.zero_()
+    b.k[..., :64] = b.q[..., :64] = 1.0
+    q_out = b.append(q=b.q, inv_freq=torch.from_numpy(f), positions=torch.from_numpy(pos.astype(np.int32)).cuda())
+    angle = np.array([[angle_far(int(p), float(w)) for w in f] for p in pos])
+    slots = np.arange(T)
+    k = b.k_cache[torch.from_numpy(b.table[0, slots // 16].astype(np.int64)).cuda(), torch.from_numpy(slots % 16).cuda(), 0]
+    assert (np.abs(np.sin(angle)) < 2.0 ** -9).sum() > 20
+    for x in (q_out[:, 0], k):
+        x = x.double().cpu().numpy()
+        for got, want in ((x[:, :64], np.cos(angle)), (x[:, 64:], np.sin(angle))):
+            bound = 2.0 ** -11 * np.abs(want) + 1.01 * (2.0 ** -21 + 2.0 ** -22) + 2.0 ** -25
+            assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
