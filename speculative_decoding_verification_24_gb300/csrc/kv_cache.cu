@@ -257,7 +257,7 @@ static cudaError_t launch_early(K kernel, int grid, int threads, const P& p, cud
 
 template <int BATCH>
 static cudaError_t launch_append(const KvAppendParams& p, int f16, cudaStream_t stream) {
-    const int grid = (p.ch.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+    const int grid = (p.ch.T - 1) / p.tokens_per_cta + 1;  // T >= 1, and may be near 2^31
     auto kernel = p.D == 128 ? (f16 ? kv_append_kernel<128, true, BATCH> : kv_append_kernel<128, false, BATCH>)
                              : (f16 ? kv_append_kernel<64, true, BATCH> : kv_append_kernel<64, false, BATCH>);
     return launch_early(kernel, grid, KA_THREADS, p, stream);

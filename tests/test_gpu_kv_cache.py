@@ -303,3 +303,23 @@ def test_append_angles_at_far_positions_of_any_frequency():
         for got, want in ((x[:, :64], np.cos(angle)), (x[:, 64:], np.sin(angle))):
             bound = 2.0 ** -11 * np.abs(want) + 1.01 * (2.0 ** -21 + 2.0 ** -22) + 2.0 ** -25
             assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
+
+
+def test_append_of_the_most_rows_there_can_be():
+    # 2^31 - 1 rows, all of them one row's memory; sequences claim the last three and two others
+    T = 2 ** 31 - 1
+    b = Batch([(3, 2), (0, 3)], Hkv=1, Hq=1, D=64, seed=13)
+    want_k, want_v = b.k_cache.clone(), b.v_cache.clone()
+    k, v = b.k[:1].expand(T, -1, -1), b.v[:1].expand(T, -1, -1)
+    for s, ctx, n in ((0, 3, 2), (2, 0, 3)):
+        for i in range(n):
+            at = int(b.table[s // 2, (ctx + i) // 16]), (ctx + i) % 16
+            want_k[at], want_v[at] = b.k[0], b.v[0]
+    # a sequence between them, of all other rows, has no room: nothing is stored for it
+    table = torch.cat([b.args[0][:1], b.args[0][:1], b.args[0][1:]])
+    lens = torch.tensor([3, 0, 0], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 2, T - 3, T], dtype=torch.int32, device="cuda")
+    spec_kv_append(k, v, b.k_cache, b.v_cache, table, lens, cu, status_word=b.status)
+    torch.cuda.synchronize()
+    assert int(b.status) == binding.SV_FLAG_BAD_LENGTH
+    assert torch.equal(b.k_cache, want_k) and torch.equal(b.v_cache, want_v)
