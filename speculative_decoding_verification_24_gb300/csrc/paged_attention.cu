@@ -49,7 +49,8 @@
 //
 // Warps: 0-3 and 4-7 softmax and output, 8 keys and 10 values (TMA, one box per
 // page or 128 tokens), 9 the products, 11 queries (TMA).
-// Every mbarrier wait is bounded; one that gives up sets SV_FLAG_TIMEOUT, the
+// Every mbarrier wait is bounded (about a second; that for a buffer of queries
+// by the share's length as well); one that gives up sets SV_FLAG_TIMEOUT, the
 // others stop waiting, no further work is issued, what was issued is waited
 // for, TMEM is freed and the rows concerned are NaN.
 #include <cuda_bf16.h>
@@ -64,6 +65,7 @@ namespace sv {
 constexpr int PA_THREADS = 384;
 constexpr int PA_SOFTMAX_THREADS = 256;
 constexpr long long PA_WAIT_CYCLES = 1ll << 31;  // a wait gives up after about a second
+constexpr long long PA_UNIT_CYCLES = 1ll << 13;  // more than a tile takes (3000); for waits that last as long as an item
 constexpr float PA_RAISE = 8.0f;                 // log2 of how far the maximum may pass m (with PA_F16_BELOW)
 constexpr float PA_F16_BELOW = 7.0f;             // how far m lies below the maximum in fp16, log2
 constexpr int PA_TMEM_COLS = 512;                // S0, S1 (128 columns each), O0, O1 (D each)
@@ -277,19 +279,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Waits for a phase; gives up after PA_WAIT_CYCLES, or at once when any wait of
-// the CTA has given up and `err` is passed.
-__device__ __forceinline__ bool pa_wait_until(uint64_t* bar, uint32_t parity, const int* err) {
+// Waits for a phase; gives up after `cycles`, or at once when any wait of the
+// CTA has given up and `err` is passed.
+__device__ __forceinline__ bool pa_wait_until(uint64_t* bar, uint32_t parity, const int* err, long long cycles = PA_WAIT_CYCLES) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long start = clock64();
     while (!mbar_try_wait(bar, parity)) {
         if (err && *(volatile const int*)err) return false;
-        if (clock64() - start > PA_WAIT_CYCLES) return mbar_try_wait(bar, parity);
+        if (clock64() - start > cycles) return mbar_try_wait(bar, parity);
     }
     return true;
 }
-__device__ __forceinline__ void pa_wait(uint64_t* bar, uint32_t parity, int* err) {
-    if (!pa_wait_until(bar, parity, err)) atomicExch(err, 1);
+__device__ __forceinline__ void pa_wait(uint64_t* bar, uint32_t parity, int* err, long long cycles = PA_WAIT_CYCLES) {
+    if (!pa_wait_until(bar, parity, err, cycles)) atomicExch(err, 1);
 }
 __device__ __forceinline__ bool pa_failed(const int* err) { return *(volatile const int*)err != 0; }
 
@@ -916,6 +918,9 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, u
     using S = PaShape<D>;
     const uint32_t box_bytes = (uint32_t)(P.q_box * P.G) * 128u;
     int fills[2] = {0, 0}, turn = 0;
+    // a buffer is free when the item's last scores have been formed: the wait
+    // lasts as long as the item, which is part of the share
+    const long long patience = PA_WAIT_CYCLES + (sh.at[1].begin - sh.at[0].begin) * PA_UNIT_CYCLES;
     for (Cursor c = share_of(sh); c.valid(); c.next(P)) {
         const bool pair = c.pair(P);
         const int split_buf = turn;
@@ -923,7 +928,7 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& P, PaShared& sh, u
         for (int w = 0; w < (pair ? 2 : 1); ++w) {
             const int buf = pair ? w : split_buf;
             const int n = fills[buf]++;
-            if (n > 0) pa_wait(&sh.q_empty[buf], (n - 1) & 1, &sh.err);
+            if (n > 0) pa_wait(&sh.q_empty[buf], (n - 1) & 1, &sh.err, patience);
             if (__any_sync(0xFFFFFFFFu, pa_failed(&sh.err))) return;
             const int tok = c.tok0 + w * P.TT, boxes = (min(P.TT, c.tok0 + c.ntok - tok) + P.q_box - 1) / P.q_box;
             if (lane == 0) {

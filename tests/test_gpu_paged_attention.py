@@ -428,3 +428,20 @@ def test_tensors_that_do_not_belong_are_refused(kw, error):
     c = Case([(20, 3)], seed=35)
     with pytest.raises((ValueError, TypeError), match=error):
         spec_paged_attention(c.q, c.k, c.v, *c.args, **kw)
+
+
+def test_an_item_that_takes_over_a_second():
+    # little more than an item of 190 million keys per CTA (one page, read again
+    # and again): the next item's queries wait for as long as the first one runs,
+    # about 3 * 10^9 cycles
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    page, pages, T, D = 65536, 2900, 2 * (sms + 8), 64
+    g = torch.Generator("cuda").manual_seed(36)
+    k, v = (torch.randn(1, page, 1, D, generator=g, device="cuda").to(BF16) for _ in range(2))
+    q = torch.randn(T, 128, D, generator=g, device="cuda").to(BF16)
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([(pages - 1) * page], dtype=torch.int32, device="cuda")
+    cu, status = torch.tensor([0, T], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = spec_paged_attention(q, k, v, table, lens, cu, status_word=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and torch.isfinite(out).all()
