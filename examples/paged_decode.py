@@ -27,6 +27,7 @@ from speculative_decoding_verification_24_gb300 import (  # noqa: E402
     spec_verify_tree)
 
 BF16 = torch.bfloat16
+CHUNK = 32  # tokens of a step's chunk at most
 
 
 class Decoder:
@@ -41,7 +42,9 @@ class Decoder:
         self.head = w(d, V) * 4
         self.layers = [dict(qkv=w(d, (Hq + 2 * Hkv) * D), out=w(Hq * D, d), up=w(d, 4 * d), down=w(4 * d, d))
                        for _ in range(layers)]
-        per_seq = -(-L_max // page)
+        # the last steps' drafts lie past the text's last place; a chunk without
+        # room for all of its tokens would be left out as a whole
+        per_seq = -(-(L_max + CHUNK) // page)
         self.caches = [tuple(torch.empty(B * per_seq, page, Hkv, D, dtype=BF16, device=device) for _ in range(2))
                        for _ in range(layers)]
         self.table = torch.randperm(B * per_seq, generator=g, device=device).to(torch.int32).view(B, per_seq)
@@ -76,6 +79,13 @@ class Decoder:
             spec_kv_commit(kc, vc, self.table, self.ctx, n_accepted, tree_parents=parents, last_node=last_node, out_lens=lens)
         self.ctx = lens
 
+    def commit(self, text, lens, tokens, n_accepted, parents=None, last_node=None):
+        """What was accepted, in the cache and in the text. A text that is full
+        takes no more, and the cache stays with it."""
+        self.keep(n_accepted, parents, last_node)
+        spec_commit(text, lens, tokens, n_accepted)
+        torch.minimum(self.ctx, lens - 1, out=self.ctx)
+
 
 def start(model, prompts, L_max):
     """Texts and lengths on the GPU, and the cache filled with all but each
@@ -100,8 +110,7 @@ def step_plain(model, text, lens):
     cu = torch.arange(model.B + 1, dtype=torch.int32, device=model.device)
     logits = spec_lmhead_logits(model.forward(last_tokens(text, lens).view(-1), cu), model.head)
     none = torch.zeros_like(lens)
-    model.keep(none)
-    spec_commit(text, lens, logits.argmax(1, keepdim=True).to(torch.int32), none)
+    model.commit(text, lens, logits.argmax(1, keepdim=True).to(torch.int32), none)
     return none, logits
 
 
@@ -113,8 +122,7 @@ def step_chain(model, text, lens, K=4):
     need = spec_verify_lmhead_workspace_bytes(model.B, K, model.d, model.V)
     tokens, n = spec_verify_lmhead(hidden.view(model.B, K + 1, -1), model.head, None, drafts, mode="greedy",
                                    workspace=torch.empty(need, dtype=torch.uint8, device=model.device))
-    model.keep(n)
-    spec_commit(text, lens, tokens, n)
+    model.commit(text, lens, tokens, n)
     return n, None
 
 
@@ -131,8 +139,7 @@ def step_tree(model, text, lens, K=4):
     cu = torch.arange(B + 1, dtype=torch.int32, device=dev) * N
     logits = spec_lmhead_logits(model.forward(nodes.view(-1), cu, parents), model.head)
     tokens, n, last = spec_verify_tree(logits.view(B, N, -1), nodes, parents)
-    model.keep(n, parents, last)
-    spec_commit(text, lens, tokens, n)
+    model.commit(text, lens, tokens, n, parents, last)
     return n, None
 
 

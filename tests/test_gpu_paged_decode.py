@@ -55,3 +55,35 @@ def test_drafted_decoding_equals_plain_decoding(plain, mode):
             # rounded to bf16 (2^-8) in either way of batching
             assert float(gaps[int(differ[0]) - len(p), b]) < 2.0 ** -6, (b, int(differ[0]))
     assert whole >= B // 2
+
+
+@pytest.mark.parametrize("mode", ["chain", "tree"])
+def test_drafted_decoding_up_to_the_end_of_the_text(mode):
+    # the drafts of the last steps lie past the text's last place, and a full
+    # text's steps change nothing
+    import paged_decode as ex
+    build()
+    L, steps = 128, 124  # whole pages
+    texts, gaps = {}, []
+    for way in ("plain", mode):
+        model = ex.Decoder(B, L)
+        prompts = ex.example_prompts(B, model.V)
+        text, lens = ex.start(model, prompts, L)
+        for _ in range(steps):
+            full = (lens == L).tolist()
+            before = text[lens == L]
+            _, logits = ex.STEPS[way](model, text, lens)
+            assert torch.equal(text[torch.tensor(full, device="cuda")], before)
+            assert torch.equal(model.ctx, lens - 1)
+            if way == "plain":
+                top = logits.topk(2, dim=1).values
+                gaps.append((top[:, 0] - top[:, 1]) / logits.abs().amax(1))
+        assert (lens == L).all()
+        texts[way] = text.cpu()
+    gaps, whole = torch.stack(gaps).cpu(), 0
+    for b, p in enumerate(prompts):
+        differ = (texts["plain"][b] != texts[mode][b]).nonzero()
+        whole += len(differ) == 0
+        if len(differ):  # only where two tokens are as good as equal, as above
+            assert float(gaps[int(differ[0]) - len(p), b]) < 2.0 ** -6, (b, int(differ[0]))
+    assert whole >= B // 2
