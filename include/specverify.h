@@ -521,7 +521,9 @@ sv_status spec_paged_attention(const sv_paged_attention_args* args);
  * commits nothing: out_lens[b] = ctx_lens[b].
  *   n_accepted [B] int32 (device); tree_parents [B, N] int32 (device) or NULL,
  *   1 <= N <= 32; last_node [B] int32 (device), with a tree;
- *   out_lens [B] int32 (device); may be ctx_lens;
+ *   out_lens [B] int32 (device); may be ctx_lens. The layers of a model share
+ *   their lengths, and every layer's call takes those from before the step:
+ *   only the last one's out_lens may then be ctx_lens;
  *   status_word: device uint32 or NULL. An n_accepted that does not fit the
  *   tree or the page table (SV_FLAG_BAD_LENGTH) or a last_node whose chain is
  *   not n_accepted long (SV_FLAG_BAD_TREE) commits nothing. */

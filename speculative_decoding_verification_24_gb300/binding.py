@@ -744,6 +744,8 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     already: each token sees its context, itself and the chunk's tokens before
     it, or, with tree_parents [B, N], its ancestors. scale: D ** -0.5 by
     default. out_lse [T, Hq] float32: the rows' log of the sum of exponentials.
+    The softmax's weights are rounded to the cache's type before they meet the
+    values; scores, sums and the output's sum are fp32.
     workspace: spec_paged_attention_workspace; made anew when None. Returns
     out."""
     cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
@@ -776,7 +778,9 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     ctx_lens + 1 + n_accepted (into out_lens, which may be ctx_lens, or a new
     tensor), and with tree_parents [B, N] and last_node [B] (as
     spec_verify_tree takes and returns them) the kept path's entries moved
-    behind the context. Returns out_lens."""
+    behind the context. A model's layers share their lengths: each layer's call
+    takes those from before the step, so out_lens may be ctx_lens in the last
+    one only. Returns out_lens."""
     cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
     B = cache[7]
     if out_lens is None:

@@ -323,3 +323,19 @@ def test_append_of_the_most_rows_there_can_be():
     torch.cuda.synchronize()
     assert int(b.status) == binding.SV_FLAG_BAD_LENGTH
     assert torch.equal(b.k_cache, want_k) and torch.equal(b.v_cache, want_v)
+
+
+def test_commit_of_several_layers_that_share_their_lengths():
+    layers = [Batch([(10, 6), (33, 6), (0, 6)], seed=20 + i) for i in range(3)]
+    parents = np.tile(np.array([-1, 0, 0, 2, 2, 4], np.int32), (3, 1))
+    n, last = np.array([3, 2, 1], np.int32), np.array([5, 3, 2], np.int32)
+    dev = [torch.from_numpy(x).cuda() for x in (n, parents, last)]
+    ctx = layers[0].args[1]
+    want = [commit_reference(b, parents, n, last, None) for b in layers]
+    for i, b in enumerate(layers):  # the last layer's call may advance the lengths in place
+        spec_kv_commit(b.k_cache, b.v_cache, b.args[0], ctx, dev[0], tree_parents=dev[1], last_node=dev[2],
+                       out_lens=ctx if i == 2 else torch.empty_like(ctx), status_word=b.status)
+    torch.cuda.synchronize()
+    for b, (k, v, lens) in zip(layers, want):
+        assert int(b.status) == 0 and torch.equal(b.k_cache, k) and torch.equal(b.v_cache, v)
+    assert np.array_equal(ctx.cpu().numpy(), want[0][2])
