@@ -83,3 +83,32 @@ def test_outputs_that_were_dropped_are_not_handed_out_while_the_call_writes_them
         side.synchronize()
         torch.cuda.synchronize()
         assert all((t == 7).all() for t in fresh)
+
+
+def test_threads_with_streams_and_workspaces_of_their_own():
+    import threading
+    from test_gpu_paged_attention import Case
+    from speculative_decoding_verification_24_gb300 import spec_paged_attention_workspace
+    build()
+    cases = [Case([(700, 5), (0, 200), (3000, 1)], seed=50 + i) for i in range(4)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, ref):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                ws = spec_paged_attention_workspace(c.q.shape[0], 8, 2, 128)
+                outs = [spec_paged_attention(c.q, c.k, c.v, *c.args, workspace=ws) for _ in range(50)]
+            stream.synchronize()
+            bad.extend(i for i, out in enumerate(outs) if not torch.equal(out, ref))
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == []
