@@ -1340,9 +1340,11 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             const float2 other = sh.ml[w ^ 1][tid];
             mt = fmaxf(m, other.x);
             const float mine = l == 0.0f ? 0.0f : ex2(m - mt), theirs = other.y == 0.0f ? 0.0f : ex2(other.x - mt);
-            lt = l * mine + other.y * theirs;
             f[0] = w == 0 ? mine : theirs;
             f[1] = w == 0 ? theirs : mine;
+            // in the same order in both warpgroups: a joined item's weights are
+            // those that either has formed, whichever CTA ends last
+            lt = fmaf(w == 0 ? other.y : l, f[1], __fmul_rn(w == 0 ? l : other.y, f[0]));
         }
 
         const bool whole = t0 == 0 && t1 == c.tiles;
