@@ -197,3 +197,27 @@ def test_append_refuses_rows_without_places_of_their_own(lib, name):
     assert lib.spec_kv_append(ctypes.byref(append_args(**one, **{name: 0}, inv_freq=ctypes.addressof(bad)))) == CONFIG
     for read in ("k_token_stride", "v_head_stride", "q_token_stride"):
         assert lib.spec_kv_append(ctypes.byref(append_args(**{read: 0}, inv_freq=ctypes.addressof(bad)))) == CONFIG
+
+
+def test_a_call_on_another_device_makes_it_current(monkeypatch):
+    current = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    seen = []
+    binding._call("f", 1, lambda x: seen.append((x, current[0])) or 0, 5)
+    binding._call("f", 0, lambda x: seen.append((x, current[0])) or 0, 6)
+    assert seen == [(5, 1), (6, 0)] and current == [0]
+    with pytest.raises(binding.SpecVerifyError, match="f"):
+        binding._call("f", 1, lambda: SHAPE)
+    assert current == [0]
