@@ -132,9 +132,9 @@ uint64_t fixed_turns(double t) {
 // 2^-18 at w = 100.
 uint64_t turn_fraction(double w) {
     constexpr double high = 0x1.45f306dc9c883p-3, low = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
-    const volatile double rounded = w * high;  // volatile: not contracted with what follows
-    const double t = rounded;
-    return fixed_turns(t) + fixed_turns(std::fma(w, high, -t) + w * low);
+    const double t = std::fma(w, high, 0.0);  // the product, rounded, and not contracted with what follows
+    const double rest = std::fma(w, high, -t) + w * low;
+    return fixed_turns(t) + (std::fabs(rest) < 0.25 ? (uint64_t)(int64_t)(rest * 18446744073709551616.0) : fixed_turns(rest));
 }
 
 // Rows of one piece: a tile of 128 or, when a sequence may have more rows, a
