@@ -9,12 +9,13 @@
 // 128 rows x 128 keys:
 //   S = Q K^T        tcgen05.mma, both operands in shared memory, S in TMEM;
 //   P = 2^(c S - m)  one thread per row: its 128 scores in registers, the
-//                    running maximum m and sum l of a one-pass softmax, P
-//                    rounded to the cache's type and written over S in TMEM;
+//                    running maximum m and sum l of a one-pass softmax (Milakov
+//                    and Gimelshein, 2018), P rounded to the cache's type, as
+//                    the product takes it, and written over S in TMEM;
 //   O += P V         tcgen05.mma, P from TMEM, V from shared memory, O in TMEM.
 // m is only raised (and O and l rescaled) when a score passes it by more than
-// 2^8: l and O share whatever m is used, so the result does not depend on it,
-// and most tiles touch no O at all. In fp16 m lies 7 below the maximum: P is
+// 2^8, as later work on attention has it: l and O share whatever m is used, so
+// the result does not depend on it, and most tiles touch no O at all. In fp16 m lies 7 below the maximum: P is
 // then at most 2^15 (65504 is the largest), and a weight is off by half a step
 // of its own or 2^-32 of the row's largest (half the step of the subnormals,
 // 2^-25, over 2^7). At the maximum itself that would be 2^-25, and 131,000 keys
@@ -37,14 +38,17 @@
 //
 // What bounds it, with 32 query and 8 kv heads of 128 in bf16 (copy rate 6789
 // GB/s, cuBLAS 1909 TFLOP/s):
-//   many rows per key: the softmax's chain. A tile's products take 1024 cycles
-//     of the tensor cores per stream, its softmax about 1650 from scores to P;
-//     two streams overlap them, at about 2900 cycles for both streams' tiles.
-//     4096 tokens over 12288: 552-595 us, 1.62-1.74 PFLOP/s, 85-91 %.
+//   many rows per key: a stream's chain. A tile's products take 1024 cycles of
+//     the tensor cores per stream, its softmax about 1650 from scores to P, and
+//     the next scores wait for O += P V, since P lies over S; two streams
+//     overlap them, at about 2900 cycles for both streams' tiles. 4096 tokens
+//     over 12288: 547-606 us replayed from a graph, 1.59-1.76 PFLOP/s, 83-92 %;
+//     called one after another, at the power limit, 611-617 us, 82 %. With D =
+//     64 the products halve and the chain stays: 434 us, 58 %.
 //   few rows: HBM. 256 single tokens over up to 8192 keys each: 629-648 us,
 //     6.7-6.9 TB/s, 99-101 % of the copy rate.
-//   little work: latency. One token over 500 keys: 11 us, of which 2 find the
-//     share, 2.4 bring the first scores, and the rest is two tiles per stream,
+//   little work: latency. One token over 500 keys: 11 us, of which 2.3 find the
+//     share, 2 bring the first scores, 3.4 are two tiles per stream, and 2.2
 //     the join of the streams and the output.
 //
 // Warps: 0-3 and 4-7 softmax and output, 8 keys and 10 values (TMA, one box per
@@ -308,7 +312,9 @@ __device__ __forceinline__ void softmax_barrier() {
 // ---------------------------------------------------------------------------
 // sum over i < n of floor((a i + b) / 128). With a = 2^k (TT a power of two)
 // the terms are floor((i + b / a) / q), q = 128 / a: runs of q equal ones.
-// Otherwise Euclid's algorithm on (a, m).
+// Otherwise the points below a line are counted by Euclid's algorithm on (a, m),
+// the axes changing places at each step, the usual way for such sums (Graham,
+// Knuth and Patashnik, Concrete Mathematics, section 3.5, treats them).
 __device__ __noinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
     const auto pairs_below = [](uint32_t x) { return (uint32_t)((uint64_t)x * (x - 1) / 2); };
     uint32_t m = PA_TILE, ans = n * (b / m) + pairs_below(n) * (a / m);
@@ -743,6 +749,7 @@ __device__ __forceinline__ size_t part_at(const PagedAttnParams& P, int D, int s
 // thread takes 8 columns of a row over all pieces; with few rows several
 // lanes share them, each a contiguous run of the pieces, joined at the end.
 // One online pass: the loads of 4 pieces of 3 such units are in flight together.
+// 19 pieces of 36 rows of 128 columns: 8 us, 22 bytes a cycle.
 template <int D, bool F16>
 __device__ __forceinline__ void join_pieces(const PagedAttnParams& P, const Cursor& c, int first_cta, int pieces) {
     const bool pair = c.pair(P);
