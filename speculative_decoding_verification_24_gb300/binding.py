@@ -292,7 +292,11 @@ def _stream(stream, device):
 
 
 def _as_stream(stream, device):
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    """The torch stream of a stream or a raw handle. 0 and 1 (cudaStreamLegacy)
+    are the default stream, for which ExternalStream would give a new one."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1 else torch.cuda.default_stream(device)
 
 
 def _empty(shape, dtype, device, stream, zero=False):

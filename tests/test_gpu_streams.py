@@ -112,3 +112,19 @@ def test_threads_with_streams_and_workspaces_of_their_own():
     for t in threads:
         t.join()
     assert bad == []
+
+
+@pytest.mark.parametrize("raw", [0, 1])
+def test_the_default_streams_handle(raw):
+    from test_gpu_paged_attention import Case
+    from speculative_decoding_verification_24_gb300 import binding
+    build()
+    assert binding._as_stream(raw, "cuda:0") == torch.cuda.default_stream()
+    c = Case([(3000, 5), (100, 70)], seed=51)
+    want = c.run()
+    size = binding.spec_paged_attention_workspace_bytes(c.q.shape[0], 8, 2, 128)
+    for _ in range(5):
+        junk = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(DELAY // 10)
+        del junk  # the call's own workspace is this memory, its counters zeroed on the same stream
+        assert torch.equal(c.run(stream=raw), want)
