@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from paged_reference import angle_far, make_cache, make_table, path_to, rotate, rotate_bound
+from paged_reference import make_cache, make_table, path_to, rotate, rotate_bound
 from speculative_decoding_verification_24_gb300 import binding, rope_inv_freq, spec_kv_append, spec_kv_commit
 from speculative_decoding_verification_24_gb300.build import build
 
@@ -284,6 +284,7 @@ def test_append_flags_sequences_that_are_not_rows(seqs, cu, whole):
 
 
 def test_append_angles_at_far_positions_of_any_frequency():
+    from paged_reference import angle_far
     # x = (1, 0) gives (cos, sin); near a multiple of pi the sine shows the
     # angle's own error, 2^-24 turns at most (2 pi 2^-24 < 2^-21)
     rng = np.random.default_rng(12)
