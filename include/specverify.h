@@ -97,8 +97,11 @@ typedef enum {
                                       kernel was about to access global memory
                                       outside every buffer of the call; it skipped
                                       that access instead                          */
-    SV_FLAG_BAD_PAGE = 512u        /* a page table entry outside [0, n_pages) where
+    SV_FLAG_BAD_PAGE = 512u,       /* a page table entry outside [0, n_pages) where
                                       a token's page was needed                    */
+    SV_FLAG_BAD_SETTING = 1024u,   /* a row's temperature, top_k, top_p or min_p is
+                                      out of range                                 */
+    SV_FLAG_NO_PAGES = 2048u       /* too few free pages for every sequence's tokens */
 } sv_device_flag;
 
 /* Batched verify over logits already in device memory.
@@ -537,6 +540,70 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* n_accepted,
 size_t sv_kv_cache_size(void);
 size_t sv_kv_append_args_size(void);
 size_t sv_paged_attention_args_size(void);
+
+/* ---------------------------------------------------------------------------
+ * Rows of logits cut by temperature, top-k, top-p and min-p.
+ *
+ * A serving loop rarely samples from a model's whole distribution: drafts are
+ * drawn from rows that are cut to their likely tokens, and the verify step then
+ * needs the draft's and the target's rows cut in the same way, since it accepts
+ * by the distributions that the tokens come from. spec_sample draws from cut
+ * rows; spec_truncate_logits writes them, with -inf for what is cut, as
+ * spec_verify takes them.
+ *
+ * With a row's logits z in descending order (equal ones in ascending order of
+ * index) and w_j = exp((z_j - max z) / T):
+ *   top_k  keeps the first top_k (0: all);
+ *   top_p  keeps of those the fewest whose w add up to at least top_p times
+ *          their sum, at least one (1: all);
+ *   min_p  keeps those with w_j >= min_p, that is at least min_p times as likely
+ *          as the first (0: all).
+ * A row keeps what all three keep, always its first. T = 0 keeps the first
+ * alone. w and their sums are held to about 2^-33 of each w in integers of 64
+ * bits; results do not depend on timing.
+ *
+ * Rows with a NaN, with +inf or without a finite logit (SV_FLAG_BAD_ROW) and
+ * rows with a setting that is out of range (SV_FLAG_BAD_SETTING) give token -1
+ * and log-probability NaN; spec_truncate_logits copies them as they are, with
+ * n_kept -1. -inf logits have probability 0.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void* logits;          /* [B, R, V] dtype (device): R rows per sequence */
+    sv_dtype dtype;              /* SV_F32 or SV_BF16                             */
+    int B, R, V;                 /* B, R >= 1, 2 <= V <= 262144, B * R <= 2^28    */
+    int64_t seq_stride, row_stride; /* in elements, >= 0; a row's V are contiguous */
+    float temperature;           /* 0, or from 2^-64 to 2^64                      */
+    int top_k;                   /* >= 0                                          */
+    float top_p, min_p;          /* 0..1                                          */
+    const float* temperatures;   /* [B] (device) a sequence's own, or NULL        */
+    const int32_t* top_ks;       /* likewise; the numbers above are not looked at */
+    const float* top_ps;
+    const float* min_ps;
+    uint32_t* status_word;       /* device uint32 or NULL                         */
+    sv_stream_t stream;
+} sv_logits_cut;
+
+/* Draws one token per row: the smallest index whose cumulative w over what is
+ * kept, in the order of indices, exceeds u times their sum.
+ *   uniforms [B, R] float (device): the u, in [0, 1); others are taken as the
+ *     nearest one, NaN as 0.
+ *   out_tokens [B, R] int32 (device).
+ *   out_logprobs [B, R] float (device) or NULL: natural log of the token's
+ *     probability among what is kept.
+ * An u within about 1e-11 of the edge between two tokens may give the other. */
+sv_status spec_sample(const sv_logits_cut* cut, const float* uniforms, int32_t* out_tokens, float* out_logprobs);
+
+/* Writes the rows with -inf in the place of what is cut; what is kept is copied
+ * (the temperature is not applied to it).
+ *   out [B, R, V] of the logits' dtype (device), strides in elements >= 0; may be
+ *     the logits (same address and strides), else must not overlap them.
+ *   out_n_kept [B, R] int32 (device) or NULL: how many are kept, -inf logits
+ *     among them where no cut leaves them out. */
+sv_status spec_truncate_logits(const sv_logits_cut* cut, void* out, int64_t out_seq_stride, int64_t out_row_stride,
+                               int32_t* out_n_kept);
+
+/* sizeof(sv_logits_cut) as compiled into the library. */
+size_t sv_logits_cut_size(void);
 
 /* Static description of a status code (never NULL). */
 const char* sv_status_string(sv_status status);

@@ -35,6 +35,8 @@ SV_FLAG_BAD_LENGTH = 64
 SV_FLAG_BAD_TREE = 128
 SV_FLAG_DEBUG_BOUNDS = 256
 SV_FLAG_BAD_PAGE = 512
+SV_FLAG_BAD_SETTING = 1024
+SV_FLAG_NO_PAGES = 2048
 SV_ARG_OVERLAP_PREVIOUS = 1
 SV_ARG_TEST_WAIT_TIMEOUT = 0x80000000
 SV_ARG_TEST_DEBUG_SHRINK = 0x40000000
@@ -177,6 +179,29 @@ class sv_paged_attention_args(ctypes.Structure):
     ]
 
 
+class sv_logits_cut(ctypes.Structure):
+    """Mirror of sv_logits_cut in include/specverify.h."""
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("dtype", ctypes.c_int),
+        ("B", ctypes.c_int),
+        ("R", ctypes.c_int),
+        ("V", ctypes.c_int),
+        ("seq_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("temperature", ctypes.c_float),
+        ("top_k", ctypes.c_int),
+        ("top_p", ctypes.c_float),
+        ("min_p", ctypes.c_float),
+        ("temperatures", ctypes.c_void_p),
+        ("top_ks", ctypes.c_void_p),
+        ("top_ps", ctypes.c_void_p),
+        ("min_ps", ctypes.c_void_p),
+        ("status_word", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -200,6 +225,9 @@ SIGNATURES = [
     ("spec_paged_attention_workspace_bytes", ctypes.c_size_t, [I, I, I, I]),
     ("spec_paged_attention", I, [P]),  # sv_paged_attention_args*
     ("spec_kv_commit", I, [P, P, P, I, P, P, P, P]),
+    ("spec_sample", I, [P, P, P, P]),  # sv_logits_cut*, ...
+    ("spec_truncate_logits", I, [P, P, ctypes.c_int64, ctypes.c_int64, P]),
+    ("sv_logits_cut_size", ctypes.c_size_t, []),
     ("sv_kv_cache_size", ctypes.c_size_t, []),
     ("sv_kv_append_args_size", ctypes.c_size_t, []),
     ("sv_paged_attention_args_size", ctypes.c_size_t, []),
@@ -225,7 +253,7 @@ def load_library(path: str):
         fn.argtypes = args
     if lib.sv_verify_args_size() != ctypes.sizeof(sv_verify_args):
         raise ImportError("sv_verify_args layout differs between the binding and the library")
-    for struct in (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args):
+    for struct in (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args, sv_logits_cut):
         if getattr(lib, struct.__name__ + "_size")() != ctypes.sizeof(struct):
             raise ImportError(f"{struct.__name__} layout differs between the binding and the library")
     return lib
@@ -564,7 +592,7 @@ def _packer(struct):
     return packer.pack
 
 
-_pack_cache, _pack_append, _pack_attention = map(_packer, (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args))
+_pack_cache, _pack_append, _pack_attention, _pack_cut = map(_packer, (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args, sv_logits_cut))
 _KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 _I32 = torch.int32
 
@@ -796,3 +824,102 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     _call("spec_kv_commit", index, (_lib or _load()).spec_kv_commit, _pack_cache(*cache), n, parents, N, last, lens, status,
           _raw_stream(index, stream))
     return out_lens
+
+
+# ------------------------------------------------------ rows of logits, cut
+
+
+def _setting(x, name, dtype, index, B):
+    """A setting as (number, pointer): one of them is not used."""
+    if not isinstance(x, torch.Tensor):
+        return x, 0
+    if x.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.shape != (B,):
+        raise ValueError(f"{name} must be a number or [{B}], one per sequence, got {list(x.shape)}")
+    if x.get_device() != index:
+        raise ValueError(f"{name} must live on the logits' CUDA device")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return 0, x.data_ptr()
+
+
+def _logits_rows(t, name):
+    """Sizes and strides of [B, V] or [B, R, V] rows of any strides but the
+    last."""
+    if t.dim() == 2:
+        (B, V), R = t.shape, 1
+        seq, last = t.stride()
+        row = 0
+    elif t.dim() == 3:
+        B, R, V = t.shape
+        seq, row, last = t.stride()
+    else:
+        raise ValueError(f"{name} must be [B, V] or [B, R, V], got {list(t.shape)}")
+    if last != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return B, R, V, seq, row
+
+
+def _per_row(t, name, dtype, logits):
+    """Data pointer of a contiguous tensor of one number per row of logits."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != logits.shape[:-1] or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(logits.shape[:-1])}, got {list(t.shape)}")
+    if t.get_device() != logits.get_device():
+        raise ValueError(f"{name} must live on the logits' CUDA device")
+    return t.data_ptr()
+
+
+def _cut_fields(logits, temperature, top_k, top_p, min_p, status_word, stream):
+    """The fields of sv_logits_cut, and the CUDA device of the logits."""
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError("logits must live on a CUDA device")
+    dtype = _dtype_code(logits)
+    B, R, V, seq, row = _logits_rows(logits, "logits")
+    T, Ts = _setting(temperature, "temperature", torch.float32, index, B)
+    k, ks = _setting(0 if top_k is None else top_k, "top_k", _I32, index, B)
+    p, ps = _setting(1.0 if top_p is None else top_p, "top_p", torch.float32, index, B)
+    m, ms = _setting(0.0 if min_p is None else min_p, "min_p", torch.float32, index, B)
+    return (logits.data_ptr(), dtype, B, R, V, seq, row, T, min(k, 2**31 - 1), p, m, Ts, ks, ps, ms, _status(status_word, index),
+            _raw_stream(index, stream)), index
+
+
+def spec_sample(logits, uniforms, temperature=1.0, top_k=None, top_p=None, min_p=None, out_tokens=None, out_logprobs=None,
+                status_word=None, stream=None):
+    """Draws a token per row of logits ([B, V] or [B, R, V], float32 or
+    bfloat16, any strides but the last) by the given uniforms in [0, 1) (float32,
+    one per row), from the row cut to its top_k first, to the fewest that hold
+    top_p of those, and to what is at least min_p times as likely as the first.
+    temperature 0 takes the first. Each setting is a number or one per sequence
+    ([B], float32; top_k int32). out_logprobs: the tokens' log-probabilities
+    among what is kept. Returns out_tokens, int32, one per row; -1 (and a flag)
+    where a row or its settings cannot be used."""
+    fields, index = _cut_fields(logits, temperature, top_k, top_p, min_p, status_word, stream)
+    if out_tokens is None:
+        out_tokens = _empty(logits.shape[:-1], _I32, logits.device, stream)
+    u, tokens = _per_row(uniforms, "uniforms", torch.float32, logits), _per_row(out_tokens, "out_tokens", _I32, logits)
+    logprobs = None if out_logprobs is None else _per_row(out_logprobs, "out_logprobs", torch.float32, logits)
+    _call("spec_sample", index, (_lib or _load()).spec_sample, _pack_cut(*fields), u, tokens, logprobs)
+    return out_tokens
+
+
+def spec_truncate_logits(logits, temperature=1.0, top_k=None, top_p=None, min_p=None, out=None, out_n_kept=None,
+                         status_word=None, stream=None):
+    """The rows of logits ([B, V] or [B, R, V], as spec_sample takes them) with
+    -inf in the place of what spec_sample would not draw from: the rows that
+    spec_verify takes when drafts and targets are cut. out may be the logits.
+    out_n_kept: how many are kept, int32, one per row. Returns out."""
+    fields, index = _cut_fields(logits, temperature, top_k, top_p, min_p, status_word, stream)
+    if out is None:
+        out = _empty(logits.shape, logits.dtype, logits.device, stream)
+    if out.dtype is not logits.dtype:
+        raise TypeError(f"out must be {logits.dtype} like the logits, got {out.dtype}")
+    if out.shape != logits.shape or out.get_device() != index:
+        raise ValueError(f"out must be {list(logits.shape)} on the logits' CUDA device, got {list(out.shape)}")
+    *_, seq, row = _logits_rows(out, "out")
+    n = None if out_n_kept is None else _per_row(out_n_kept, "out_n_kept", _I32, logits)
+    _call("spec_truncate_logits", index, (_lib or _load()).spec_truncate_logits, _pack_cut(*fields), out.data_ptr(), seq, row, n)
+    return out

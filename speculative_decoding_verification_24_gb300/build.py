@@ -28,7 +28,7 @@ LIB_DEBUG = os.path.join(PKG, "libspecverify_debug.so")
 VARIANTS = [(LIB, BUILD_DIR, []), (LIB_DEBUG, os.path.join(BUILD_DIR, "debug"), ["-DSPECVERIFY_DEBUG"])]
 
 SOURCES = ["verify_logits.cu", "verify_grouped.cu", "lmhead.cu", "paged_attention.cu", "prompt_lookup.cu", "kv_cache.cu",
-           "api.cu", "paged_api.cu"]
+           "cut_logits.cu", "api.cu", "paged_api.cu", "cut_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
