@@ -490,6 +490,12 @@ typedef struct {
     uint32_t* status_word;       /* device uint32 or NULL                         */
     uint32_t flags;              /* SV_ARG_TEST_WAIT_TIMEOUT or 0                 */
     sv_stream_t stream;
+    float score_cap;             /* 0: none; else 2^-10..4096: scores become cap *
+                                    tanh(scale q . k / cap)                       */
+    const float* bias_slopes;    /* [Hq] float (device), finite, or NULL: slope_h *
+                                    (the key's position - the token's) is added to
+                                    the score, after the cap. A slot's position is
+                                    its number, a tree node's ctx + its depth     */
 } sv_paged_attention_args;
 
 /* Bytes of workspace of a call with T packed rows: SV_PAGED_WORKSPACE_HEAD
@@ -506,7 +512,8 @@ size_t spec_paged_attention_workspace_bytes(int T, int Hq, int Hkv, int D);
 /* Attention of the chunk's tokens, whose keys and values are in the cache
  * already: out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h / G]) v[j, h /
  * G], G = Hq / Hkv, over the slots j <= t's own (chain), or the context, t's
- * ancestors and t itself (tree). Scores, the softmax's maximum and sum and the
+ * ancestors and t itself (tree). score_cap and bias_slopes change the scores
+ * first; a capped score is off by about 2^-21 of the cap at most. Scores, the softmax's maximum and sum and the
  * output accumulate in fp32; the weights are rounded to the cache's dtype
  * before they meet v, and the output is rounded once. Entries past a
  * sequence's last token may hold anything, and a key or value that is not
@@ -534,6 +541,53 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* n_accepted,
                          const int32_t* tree_parents, int N,
                          const int32_t* last_node, int32_t* out_lens,
                          uint32_t* status_word, sv_stream_t stream);
+
+/* Arguments of spec_kv_pages. Zero-initialise, then fill what is used. */
+typedef struct {
+    int32_t* page_table;         /* [B, max_pages] int32 (device), in place       */
+    int64_t page_table_stride;   /* between sequences, >= max_pages               */
+    int max_pages;               /* >= 1                                          */
+    int32_t* held;               /* [B] int32 (device), in place: how many entries
+                                    of its table, from the first, are sequence b's */
+    int32_t* free_pages;         /* [n_pages] int32 (device), in place: the stack
+                                    of free pages                                 */
+    int32_t* n_free;             /* [1] int32 (device), in place: its height      */
+    int n_pages;                 /* >= 1: pages of the cache                      */
+    int page_size;               /* a multiple of 8, 8..65536                     */
+    int B;                       /* sequences, 1..8192                            */
+    const int32_t* ctx_lens;     /* [B] int32 (device): tokens in the cache       */
+    const int32_t* cu_new;       /* [B+1] int32 (device): the new tokens' rows    */
+    int T;                       /* packed rows, >= 0                             */
+    int64_t* slots;              /* [T] int64 (device) or NULL: where each row's
+                                    token belongs, page * page_size + entry; -1
+                                    where it has no place or no sequence          */
+    int32_t* positions;          /* [T] int32 (device) or NULL: ctx + its place in
+                                    the chunk; -1 without a sequence              */
+    uint32_t* status_word;       /* device uint32 or NULL                         */
+    sv_stream_t stream;
+} sv_kv_pages_args;
+
+/* Hands out the cache's pages before a chunk is appended: afterwards sequence b
+ * holds exactly the ceil((ctx_lens[b] + new tokens) / page_size) pages that its
+ * tokens need. First what the sequences hold beyond that goes on the stack, by
+ * sequence and place (those entries become -1): pages of drafts that were not
+ * kept, and all of a sequence whose lengths are 0. Then each sequence's missing
+ * pages are taken from the stack's top, in the order of sequences and places.
+ * Where too few are left, the first sequence that asks for more than there are
+ * and all later ones that ask get none (SV_FLAG_NO_PAGES): they keep what they
+ * have, held says so, and their tokens beyond it have slot -1.
+ * What lies in the stack from n_free on has no meaning.
+ *   SV_FLAG_BAD_LENGTH: a sequence with a negative context, more tokens than its
+ *     table has room for or a held outside [0, max_pages] is left out (it keeps
+ *     its pages; its rows' slots and positions are -1). Where cu_new does not
+ *     ascend within [0, T], n_free is not in [0, n_pages] or more pages come back
+ *     than there are, nothing changes and every slot and position is -1.
+ *   SV_FLAG_BAD_PAGE: a page outside [0, n_pages) in an entry that was given
+ *     back, taken or looked up; it moves as it is, a slot on it is -1. */
+sv_status spec_kv_pages(const sv_kv_pages_args* args);
+
+/* sizeof(sv_kv_pages_args) as compiled into the library. */
+size_t sv_kv_pages_args_size(void);
 
 /* sizeof(sv_kv_cache), sizeof(sv_kv_append_args) and
  * sizeof(sv_paged_attention_args) as compiled into the library. */

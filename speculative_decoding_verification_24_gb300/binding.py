@@ -176,6 +176,30 @@ class sv_paged_attention_args(ctypes.Structure):
         ("status_word", ctypes.c_void_p),
         ("flags", ctypes.c_uint32),
         ("stream", ctypes.c_void_p),
+        ("score_cap", ctypes.c_float),
+        ("bias_slopes", ctypes.c_void_p),
+    ]
+
+
+class sv_kv_pages_args(ctypes.Structure):
+    """Mirror of sv_kv_pages_args in include/specverify.h."""
+    _fields_ = [
+        ("page_table", ctypes.c_void_p),
+        ("page_table_stride", ctypes.c_int64),
+        ("max_pages", ctypes.c_int),
+        ("held", ctypes.c_void_p),
+        ("free_pages", ctypes.c_void_p),
+        ("n_free", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("B", ctypes.c_int),
+        ("ctx_lens", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p),
+        ("T", ctypes.c_int),
+        ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("status_word", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
     ]
 
 
@@ -225,6 +249,8 @@ SIGNATURES = [
     ("spec_paged_attention_workspace_bytes", ctypes.c_size_t, [I, I, I, I]),
     ("spec_paged_attention", I, [P]),  # sv_paged_attention_args*
     ("spec_kv_commit", I, [P, P, P, I, P, P, P, P]),
+    ("spec_kv_pages", I, [P]),  # sv_kv_pages_args*
+    ("sv_kv_pages_args_size", ctypes.c_size_t, []),
     ("spec_sample", I, [P, P, P, P]),  # sv_logits_cut*, ...
     ("spec_truncate_logits", I, [P, P, ctypes.c_int64, ctypes.c_int64, P]),
     ("sv_logits_cut_size", ctypes.c_size_t, []),
@@ -253,7 +279,7 @@ def load_library(path: str):
         fn.argtypes = args
     if lib.sv_verify_args_size() != ctypes.sizeof(sv_verify_args):
         raise ImportError("sv_verify_args layout differs between the binding and the library")
-    for struct in (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args, sv_logits_cut):
+    for struct in (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args, sv_kv_pages_args, sv_logits_cut):
         if getattr(lib, struct.__name__ + "_size")() != ctypes.sizeof(struct):
             raise ImportError(f"{struct.__name__} layout differs between the binding and the library")
     return lib
@@ -592,7 +618,8 @@ def _packer(struct):
     return packer.pack
 
 
-_pack_cache, _pack_append, _pack_attention, _pack_cut = map(_packer, (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args, sv_logits_cut))
+_pack_cache, _pack_append, _pack_attention, _pack_pages, _pack_cut = map(
+    _packer, (sv_kv_cache, sv_kv_append_args, sv_paged_attention_args, sv_kv_pages_args, sv_logits_cut))
 _KV_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 _I32 = torch.int32
 
@@ -770,7 +797,7 @@ def _own_workspace(T, Hq, Hkv, D, device, stream):
 
 
 def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scale=None, tree_parents=None, out=None,
-                         out_lse=None, workspace=None, status_word=None, stream=None, flags=0):
+                         out_lse=None, workspace=None, status_word=None, stream=None, flags=0, score_cap=None, bias_slopes=None):
     """Attention of a chunk's tokens (q [T, Hq, D], packed rows of any token
     and head strides) over the paged cache, which holds their keys and values
     already: each token sees its context, itself and the chunk's tokens before
@@ -778,6 +805,9 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     default. out_lse [T, Hq] float32: the rows' log of the sum of exponentials.
     The softmax's weights are rounded to the cache's type before they meet the
     values; scores, sums and the output's sum are fp32.
+    score_cap: scores become cap * tanh(score / cap). bias_slopes [Hq] float32:
+    slope * (the key's position - the token's) is added to them, a tree node's
+    position being its context plus its depth.
     workspace: spec_paged_attention_workspace; made anew when None. Returns
     out."""
     cache, index = _cache_fields(k_cache, v_cache, page_table, ctx_lens)
@@ -798,9 +828,14 @@ def spec_paged_attention(q, k_cache, v_cache, page_table, ctx_lens, cu_new, scal
     status = _status(status_word, index)
     cu = _int32(cu_new, "cu_new", index, B + 1)
     scale = D ** -0.5 if scale is None else scale
+    slopes = 0
+    if bias_slopes is not None:
+        if bias_slopes.dtype is not torch.float32 or bias_slopes.shape != (Hq,):
+            raise ValueError(f"bias_slopes must be float32 [{Hq}]")
+        slopes = _plain(bias_slopes, "bias_slopes", index)
     _call("spec_paged_attention", index, (_lib or _load()).spec_paged_attention, _pack_attention(
         *cache, cu, T, Hq, qp, op, qt, qh, ot, oh, lse, scale, parents, N, ws, ws_bytes, status, int(flags),
-        _raw_stream(index, stream)))
+        _raw_stream(index, stream), score_cap or 0.0, slopes))
     return out
 
 
@@ -824,6 +859,40 @@ def spec_kv_commit(k_cache, v_cache, page_table, ctx_lens, n_accepted, tree_pare
     _call("spec_kv_commit", index, (_lib or _load()).spec_kv_commit, _pack_cache(*cache), n, parents, N, last, lens, status,
           _raw_stream(index, stream))
     return out_lens
+
+
+def spec_kv_pages(page_table, held, free_pages, n_free, ctx_lens, cu_new, page_size, slots=None, positions=None, status_word=None,
+                  stream=None):
+    """Hands out the cache's pages for a chunk of new tokens (cu_new [B+1],
+    behind ctx_lens [B]), all in place: page_table [B, max_pages], held [B] (how
+    many of its table's entries each sequence has), free_pages [n_pages] (a
+    stack) and n_free [1] (its height), all int32. What a sequence has too many
+    goes back, what its tokens need is taken from the stack's top. slots [T]
+    int64: page * page_size + entry of every packed row; positions [T] int32:
+    its place in its sequence. Returns slots."""
+    index = page_table.get_device()
+    if index < 0 or page_table.dtype is not _I32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages] on a CUDA device")
+    B, max_pages = page_table.shape
+    row, entry = page_table.stride()
+    if entry != 1 and max_pages > 1:
+        raise ValueError("page_table must be contiguous in its last dimension")
+    n_pages, T = free_pages.numel(), 2**31 - 1  # (where no row is written any number will do)
+    slots_at = positions_at = 0
+    if slots is not None:
+        if slots.dtype is not torch.int64 or slots.dim() != 1:
+            raise TypeError(f"slots must be int64 [T], got {slots.dtype} {list(slots.shape)}")
+        T, slots_at = slots.numel(), _plain(slots, "slots", index)
+    if positions is not None:
+        T = positions.numel() if slots is None else T
+        positions_at = _int32(positions, "positions", index, T)
+    held_at, ctx = _int32(held, "held", index, B), _int32(ctx_lens, "ctx_lens", index, B)
+    free_at, n_free_at = _int32(free_pages, "free_pages", index, n_pages), _int32(n_free, "n_free", index, 1)
+    cu = _int32(cu_new, "cu_new", index, B + 1)
+    _call("spec_kv_pages", index, (_lib or _load()).spec_kv_pages, _pack_pages(
+        page_table.data_ptr(), row if B > 1 else max_pages, max_pages, held_at, free_at, n_free_at, n_pages, page_size, B, ctx, cu, T,
+        slots_at, positions_at, _status(status_word, index), _raw_stream(index, stream)))
+    return slots
 
 
 # ------------------------------------------------------ rows of logits, cut

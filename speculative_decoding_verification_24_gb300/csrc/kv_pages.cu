@@ -1,0 +1,233 @@
+// The pages of a paged key/value cache, handed out on the GPU: every sequence
+// holds as many as its context and new tokens need, what it has too many goes
+// back on the stack of free pages, and the new tokens' slots follow.
+//
+// With need_b = ceil((ctx_b + new_b) / page_size): the pages of b's table from
+// need_b on go on the stack, by sequence and place; then the missing ones are
+// taken from its top in the same order, sequence b's i-th from below those of
+// the sequences before it. Both places are prefix sums over the sequences
+// (a scan), so the result is one that a loop over them would give.
+//
+// A step's call moves a few kilobytes and is all latency: lengths, scan, pushes,
+// pops and rows depend on one another. One cluster of CTAs does it: each scans
+// all sequences for itself (a few coalesced loads, no exchange), pushes its
+// share, and after one cluster barrier, when the stack is whole, pops and writes
+// its share of the tables and rows. Old lengths are kept in shared memory, so
+// that the ones in place can be replaced meanwhile.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "paged_device.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace sv {
+
+constexpr int KP_THREADS = 512;
+constexpr int KP_WARPS = KP_THREADS / 32;
+constexpr int KP_CTAS = 8;
+
+struct KpSequence {
+    int lo, held;  // first row; pages held before, -1: left out
+    int push, pop; // pages given back and wanted by the sequences before
+};
+
+__device__ __forceinline__ int2 warp_scan2(int2 v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, v.x, o), y = __shfl_up_sync(0xFFFFFFFFu, v.y, o);
+        if (lane >= o) v.x += x, v.y += y;
+    }
+    return v;
+}
+
+__global__ void __launch_bounds__(KP_THREADS, 1) kv_pages_kernel(const __grid_constant__ KvPagesParams P) {
+    cluster_arrive_started();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), CS = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    extern __shared__ __align__(16) KpSequence seq[];  // [B + 1]
+    __shared__ int2 warp_sums[KP_WARPS];
+    __shared__ int taken;
+    if (tid == 0) taken = 0;
+    grid_dependency_wait();
+    launch_dependents();
+
+    // lengths and both prefix sums; every CTA for itself
+    const int n_free = *P.n_free;
+    int2 run = make_int2(0, 0);
+    bool torn = n_free < 0 || n_free > P.n_pages, bad = false;
+    for (int base = 0; base < P.B; base += KP_THREADS) {
+        const int b = base + tid;
+        int lo = 0, held = -1;
+        int2 mine = make_int2(0, 0);
+        if (b < P.B) {
+            lo = P.cu[b];
+            const int hi = P.cu[b + 1], ctx = P.ctx[b], has = P.held[b];
+            const bool rows_ok = lo >= 0 && lo <= hi && hi <= P.T;
+            torn |= !rows_ok;
+            const bool ok = rows_ok && ctx >= 0 && has >= 0 && has <= P.max_pages &&
+                            (long long)ctx + (hi - lo) <= (long long)P.max_pages * P.page_size;
+            if (ok) {
+                held = has;
+                const int need = (int)(((long long)ctx + (hi - lo) + P.page_size - 1) / P.page_size);
+                mine = make_int2(max(has - need, 0), max(need - has, 0));
+            } else {
+                bad = true;
+            }
+        }
+        const int2 incl = warp_scan2(mine, lane);
+        __syncthreads();
+        if (lane == 31) warp_sums[warp] = incl;
+        __syncthreads();
+        int2 before = run;
+        for (int w = 0; w < KP_WARPS; ++w) {
+            const int2 t = warp_sums[w];
+            if (w < warp) before.x += t.x, before.y += t.y;
+            run.x += t.x, run.y += t.y;
+        }
+        if (b < P.B) seq[b] = KpSequence{lo, held, before.x + incl.x - mine.x, before.y + incl.y - mine.y};
+    }
+    if (tid == 0) seq[P.B] = KpSequence{P.cu[P.B], -1, run.x, run.y};
+    // (more pages than there are: the sequences hold some twice)
+    torn |= (long long)n_free + run.x > P.n_pages;
+    torn = __syncthreads_or(torn);
+    bad = __syncthreads_or(bad);
+    const int top = torn ? 0 : n_free + run.x;
+    if ((bad || torn) && rank == 0 && tid == 0) raise_flag(P.status, SV_FLAG_BAD_LENGTH);
+
+    // Sequences go round the cluster's CTAs, a warp looks at 32 of one CTA's.
+    const auto each = [&](auto&& f) {
+        for (int first = warp * 32; first * CS < P.B; first += KP_THREADS) {
+            const int b = (first + lane) * CS + rank;
+            KpSequence s = {0, -1, 0, 0};
+            int give = 0, want = 0;
+            if (b < P.B) {
+                s = seq[b];
+                give = seq[b + 1].push - s.push;
+                want = seq[b + 1].pop - s.pop;
+            }
+            f(b, s, give, want);
+        }
+    };
+    if (!torn) {
+        each([&](int b, const KpSequence& s, int give, int) {
+            for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, give > 0); todo; todo &= todo - 1) {
+                const int l = __ffs(todo) - 1;
+                const int n = __shfl_sync(0xFFFFFFFFu, give, l), at = n_free + __shfl_sync(0xFFFFFFFFu, s.push, l);
+                const int from = __shfl_sync(0xFFFFFFFFu, s.held, l) - n;
+                int32_t* row = P.table + (int64_t)__shfl_sync(0xFFFFFFFFu, b, l) * P.table_stride + from;
+                for (int i = lane; i < n; i += 32) {
+                    const int page = row[i];
+                    if (page < 0 || page >= P.n_pages) raise_flag(P.status, SV_FLAG_BAD_PAGE);
+                    P.free_pages[at + i] = page;
+                    row[i] = -1;
+                }
+            }
+        });
+    }
+    cluster_wait_started();
+    cluster.sync();
+    // the stack is whole, and every CTA has read the lengths
+
+    // Page `i` from the stack's top.
+    const auto popped = [&](int i) {
+        const int page = P.free_pages[top - 1 - i];
+        if (page < 0 || page >= P.n_pages) raise_flag(P.status, SV_FLAG_BAD_PAGE);
+        return page;
+    };
+    if (!torn) {
+        int most = 0;
+        bool none = false;
+        each([&](int b, const KpSequence& s, int give, int want) {
+            const bool granted = want > 0 && want <= top - s.pop;
+            none |= want > 0 && !granted;
+            if (granted) most = max(most, s.pop + want);
+            if (give > 0 || granted) P.held[b] = s.held - give + want;
+            for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, granted); todo; todo &= todo - 1) {
+                const int l = __ffs(todo) - 1;
+                const int n = __shfl_sync(0xFFFFFFFFu, want, l), at = __shfl_sync(0xFFFFFFFFu, s.pop, l);
+                int32_t* row = P.table + (int64_t)__shfl_sync(0xFFFFFFFFu, b, l) * P.table_stride + __shfl_sync(0xFFFFFFFFu, s.held, l);
+                for (int i = lane; i < n; i += 32) row[i] = popped(at + i);
+            }
+        });
+        if (none) raise_flag(P.status, SV_FLAG_NO_PAGES);
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        if (lane == 0 && most > 0) atomicMax(cluster.map_shared_rank(&taken, 0), most);
+    }
+    if (P.slots || P.positions) {
+        // a warp has a run of rows; a lane searches its first row's sequence and
+        // steps on from there
+        const int warps = CS * KP_WARPS;
+        const long long per = ((P.T + (long long)warps - 1) / warps + 31) / 32 * 32;
+        const int t0 = (int)min((rank * KP_WARPS + warp) * per, (long long)P.T), t1 = (int)min(t0 + per, (long long)P.T);
+        int b = -1;
+        for (long long tt = t0 + lane; tt < t1; tt += 32) {
+            const int t = (int)tt;
+            int64_t slot = -1;
+            int pos = -1;
+            if (!torn && t >= seq[0].lo && t < seq[P.B].lo) {
+                if (b < 0) {
+                    int hi = P.B;  // seq[b].lo <= t < seq[hi].lo
+                    b = 0;
+                    while (hi - b > 1) {
+                        const int mid = (b + hi) >> 1;
+                        if (seq[mid].lo <= t) b = mid;
+                        else hi = mid;
+                    }
+                }
+                while (seq[b + 1].lo <= t) ++b;
+                const KpSequence s = seq[b];
+                if (s.held >= 0) {
+                    pos = P.ctx[b] + (t - s.lo);
+                    const int j = (int)((uint32_t)pos / (uint32_t)P.page_size), in_page = pos - j * P.page_size;
+                    int page = -1;
+                    if (j < s.held) {
+                        page = P.table[(int64_t)b * P.table_stride + j];
+                        if (page < 0 || page >= P.n_pages) raise_flag(P.status, SV_FLAG_BAD_PAGE);
+                    } else if (seq[b + 1].pop - s.pop <= top - s.pop) {
+                        page = popped(s.pop + j - s.held);
+                    }
+                    if (page >= 0 && page < P.n_pages) slot = (int64_t)page * P.page_size + in_page;
+                }
+            }
+            if (P.slots) P.slots[t] = slot;
+            if (P.positions) P.positions[t] = pos;
+        }
+    }
+    cluster.sync();  // `taken` is complete
+    if (rank == 0 && tid == 0 && !torn) *P.n_free = top - taken;
+}
+
+cudaError_t launch_kv_pages(const KvPagesParams& p, cudaStream_t stream) {
+    const int smem = (p.B + 1) * (int)sizeof(KpSequence);
+    static std::atomic<int> attr_done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_done[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kv_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (KP_MAX_SEQUENCES + 1) * (int)sizeof(KpSequence));
+        if (e != cudaSuccess) return e;
+        attr_done[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(KP_CTAS, 1, 1);
+    cfg.blockDim = dim3(KP_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = KP_CTAS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kv_pages_kernel, p);
+}
+
+}  // namespace sv

@@ -1,5 +1,5 @@
 // Internal interface between the paged cache's C-ABI layer (paged_api.cu) and
-// its kernels (kv_cache.cu, paged_attention.cu).
+// its kernels (kv_cache.cu, kv_pages.cu, paged_attention.cu).
 #pragma once
 
 #include <cstdint>
@@ -52,6 +52,19 @@ struct KvCommitParams {
     int32_t* out_lens;
 };
 
+// Handing out pages (kv_pages.cu).
+constexpr int KP_MAX_SEQUENCES = 8192;  // their lengths lie in shared memory
+struct KvPagesParams {
+    int32_t* table;          // [B, max_pages], rows table_stride apart
+    int64_t table_stride;
+    int32_t *held, *free_pages, *n_free;  // [B], [n_pages], [1]
+    const int32_t *ctx, *cu;  // [B], [B+1]
+    int max_pages, page_size, n_pages, B, T;
+    int64_t* slots;          // [T] or nullptr
+    int32_t* positions;      // [T] or nullptr
+    uint32_t* status;        // or nullptr
+};
+
 struct PagedAttnParams {
     ChunkParams ch;
     char* out;
@@ -63,6 +76,8 @@ struct PagedAttnParams {
     int q_box;               // tokens of one copy of queries, a divisor of TT
     int box_shift;           // log2 of the rows of one copy (page_size's power of two, at most 128)
     float c;                 // scale * log2(e)
+    float cap_c, cap_two;    // cap * log2(e), or 0 without a cap; 2 scale * log2(e) / cap
+    const float* slopes;     // [Hq] or nullptr
     int rows_cap;            // rows of one partial in the workspace
     uint32_t* counters;      // [PA_MAX_CTAS], zero between calls
     float2* part_ml;         // [2 * PA_MAX_CTAS, rows_cap]
@@ -72,8 +87,12 @@ struct PagedAttnParams {
 
 cudaError_t launch_kv_append(const KvAppendParams& p, int f16, int sms, cudaStream_t stream);
 cudaError_t launch_kv_commit(const KvCommitParams& p, cudaStream_t stream);
+cudaError_t launch_kv_pages(const KvPagesParams& p, cudaStream_t stream);
 cudaError_t launch_paged_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                    const PagedAttnParams& p, int D, int f16, int sms, cudaStream_t stream);
+// The same with a cap or slopes, which launch_paged_attention passes on.
+cudaError_t launch_paged_attention_scored(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                          const PagedAttnParams& p, int D, int f16, int sms, cudaStream_t stream);
 
 // The library's record of a failed CUDA call on this host thread, and the
 // check that the current device is one it was built for (api.cu).

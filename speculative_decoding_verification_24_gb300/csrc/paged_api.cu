@@ -217,9 +217,12 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     if (items * (std::ceil((double)c.max_pages * c.page_size / sv::PA_TILE) + sv::PA_ITEM_COST) > 2147483647.0) return SV_ERR_SHAPE;
     if (!std::isfinite(a->scale) || !(a->scale > 0.0f) || !std::isfinite(a->scale * 1.4426950408889634f)) return SV_ERR_CONFIG;
     if (a->flags & ~SV_ARG_TEST_WAIT_TIMEOUT) return SV_ERR_CONFIG;
+    if (a->score_cap != 0.0f && (!(a->score_cap >= 0x1p-10f && a->score_cap <= 4096.0f) ||
+                                 !std::isfinite(a->scale * 2.8853900817779268f / a->score_cap)))
+        return SV_ERR_CONFIG;
     if ((st = check_tree(a->tree_parents, a->N)) != SV_OK) return st;
     if (!aligned(a->cu_new, 4) || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->out_lse, 4) ||
-        !aligned(a->status_word, 4) || !aligned(a->workspace, 256))
+        !aligned(a->status_word, 4) || !aligned(a->workspace, 256) || !aligned(a->bias_slopes, 4))
         return SV_ERR_ALIGN;
     if (!stride_ok(a->q_token_stride) || !stride_ok(a->q_head_stride) || !stride_ok(a->out_token_stride) ||
         !stride_ok(a->out_head_stride))
@@ -247,6 +250,9 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     p.TT = TT;
     while (p.box_shift < 7 && c.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
     p.c = a->scale * 1.4426950408889634f;
+    p.cap_c = a->score_cap * 1.4426950408889634f;
+    p.cap_two = a->score_cap != 0.0f ? a->scale * 2.8853900817779268f / a->score_cap : 0.0f;
+    p.slopes = a->bias_slopes;
     p.rows_cap = piece_rows(a->T, G);
     char* ws = static_cast<char*>(a->workspace);
     p.counters = reinterpret_cast<uint32_t*>(ws);
@@ -286,6 +292,43 @@ extern "C" sv_status spec_kv_commit(const sv_kv_cache* cache, const int32_t* n_a
     return e == cudaSuccess ? SV_OK : fail_cuda(e);
 }
 
+extern "C" sv_status spec_kv_pages(const sv_kv_pages_args* a) {
+    if (!a) return SV_ERR_NULL;
+    if (!a->page_table || !a->held || !a->free_pages || !a->n_free || !a->ctx_lens || !a->cu_new) return SV_ERR_NULL;
+    if (a->B < 1 || a->B > sv::KP_MAX_SEQUENCES || a->max_pages < 1 || a->n_pages < 1 || a->n_pages == INT32_MAX || a->page_size < 8 ||
+        a->page_size > 65536 || a->page_size % 8 != 0 || a->T < 0 || a->page_table_stride < a->max_pages ||
+        a->page_table_stride >= (int64_t(1) << 38))
+        return SV_ERR_SHAPE;
+    // as in the cache's other calls: slots of one sequence, and pages of all, are int32
+    if ((int64_t)a->max_pages * a->page_size > INT32_MAX - 1024 || (int64_t)a->max_pages * a->B > INT32_MAX) return SV_ERR_SHAPE;
+    if (!aligned(a->page_table, 4) || !aligned(a->held, 4) || !aligned(a->free_pages, 4) || !aligned(a->n_free, 4) ||
+        !aligned(a->ctx_lens, 4) || !aligned(a->cu_new, 4) || !aligned(a->slots, 8) || !aligned(a->positions, 4) ||
+        !aligned(a->status_word, 4))
+        return SV_ERR_ALIGN;
+    int sms = 0;
+    const sv_status st = check_device(&sms);
+    if (st != SV_OK) return st;
+    sv::KvPagesParams p = {};
+    p.table = a->page_table;
+    p.table_stride = a->page_table_stride;
+    p.held = a->held;
+    p.free_pages = a->free_pages;
+    p.n_free = a->n_free;
+    p.ctx = a->ctx_lens;
+    p.cu = a->cu_new;
+    p.max_pages = a->max_pages;
+    p.page_size = a->page_size;
+    p.n_pages = a->n_pages;
+    p.B = a->B;
+    p.T = a->T;
+    p.slots = a->slots;
+    p.positions = a->positions;
+    p.status = a->status_word;
+    const cudaError_t e = sv::launch_kv_pages(p, (cudaStream_t)a->stream);
+    return e == cudaSuccess ? SV_OK : fail_cuda(e);
+}
+
+extern "C" size_t sv_kv_pages_args_size(void) { return sizeof(sv_kv_pages_args); }
 extern "C" size_t sv_kv_cache_size(void) { return sizeof(sv_kv_cache); }
 extern "C" size_t sv_kv_append_args_size(void) { return sizeof(sv_kv_append_args); }
 extern "C" size_t sv_paged_attention_args_size(void) { return sizeof(sv_paged_attention_args); }

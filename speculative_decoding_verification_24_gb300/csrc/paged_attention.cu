@@ -315,7 +315,7 @@ __device__ __forceinline__ void softmax_barrier() {
 // Otherwise the points below a line are counted by Euclid's algorithm on (a, m),
 // the axes changing places at each step, the usual way for such sums (Graham,
 // Knuth and Patashnik, Concrete Mathematics, section 3.5, treats them).
-__device__ __noinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+static __device__ __noinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
     const auto pairs_below = [](uint32_t x) { return (uint32_t)((uint64_t)x * (x - 1) / 2); };
     uint32_t m = PA_TILE, ans = n * (b / m) + pairs_below(n) * (a / m);
     a %= m;
@@ -1178,8 +1178,48 @@ __device__ __forceinline__ void join_few(const PagedAttnParams& P, const RowPlac
     if (P.lse && at.valid) P.lse[(size_t)at.token * P.Hq + at.head] = lse_of(M, L);
 }
 
+// Scores of models that change them before the softmax, in the units of its
+// exponent (log2): with MOD & PA_CAP the score s = scale q . k becomes cap
+// tanh(s / cap), with MOD & PA_BIAS slope (position of the key - position of the
+// row) is added. r holds q . k of the keys key0 on.
+constexpr int PA_CAP = 1, PA_BIAS = 2;
+
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// tanh(x) = 1 - 2 / (1 + e^2x): off by 2^-22 or so of 1, at any x.
+template <int MOD>
+__device__ __forceinline__ void change_scores(uint32_t (&r)[PA_TILE], const PagedAttnParams& P, float slope, int far0) {
+    const f32x2 cc = pack2(P.c, P.c), slopes = pack2(slope, slope), two = pack2(P.cap_two, P.cap_two);
+    const f32x2 cap = pack2(P.cap_c, P.cap_c), minus = pack2(-2.0f * P.cap_c, -2.0f * P.cap_c), one = pack2(1.0f, 1.0f);
+    const float f0 = (float)far0;
+    f32x2 far = pack2(f0, f0 + 1.0f);
+    const f32x2 step = pack2(2.0f, 2.0f);
+#pragma unroll
+    for (int k = 0; k < PA_TILE; k += 2) {
+        f32x2 x = pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+        if constexpr ((MOD & PA_CAP) != 0) {
+            float a, b;
+            unpack2(add2(ex2x2(mul2(x, two)), one), a, b);
+            x = fma2(pack2(rcp(a), rcp(b)), minus, cap);
+        }
+        if constexpr ((MOD & PA_BIAS) != 0) {
+            const f32x2 b = mul2(slopes, far);
+            x = (MOD & PA_CAP) != 0 ? add2(x, b) : fma2(x, cc, b);
+            far = add2(far, step);
+        }
+        float a, b;
+        unpack2(x, a, b);
+        r[k] = __float_as_uint(a);
+        r[k + 1] = __float_as_uint(b);
+    }
+}
+
 // Warps 0-3 (w = 0) and 4-7 (w = 1): softmax and output.
-template <int D, bool F16>
+template <int D, bool F16, int MOD>
 __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared& sh, int w,
                                              char* q_smem, char* ring, uint32_t tmem_base) {
     using S = PaShape<D>;
@@ -1201,9 +1241,17 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
         int seen = at.valid ? at.token - c.s.q0 + c.s.ctx + 1 : 0;
         int seen_by_all = c.s.ctx + tok_first + 1;
         uint32_t set = 0;
+        // (bias) this row's position, and how far node `lane`'s is from its slot's
+        int row_pos = seen - 1;
+        float node_far = 0.0f, slope = 0.0f;
+        if constexpr ((MOD & PA_BIAS) != 0) slope = at.valid ? P.slopes[at.head] * 1.4426950408889634f : 0.0f;
         if (P.ch.parents) {
             const uint32_t sets = tree_sets(P.ch, c.b, c.s.n, lane);
             set = __shfl_sync(0xFFFFFFFFu, sets, at.valid ? at.token - c.s.q0 : 0);
+            if constexpr ((MOD & PA_BIAS) != 0) {
+                node_far = (float)(__popc(sets) - 1 - lane);
+                row_pos = c.s.ctx + max(__popc(set) - 1, 0);
+            }
             if (!at.valid) set = 0;
             // a node with a bad chain of parents sees nothing
             seen = set ? c.s.ctx : 0;
@@ -1242,6 +1290,19 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
             if (warp_on) {
                 uint32_t r[PA_TILE];
                 tmem_ld(tmem_s, r);
+                if constexpr (MOD != 0) {
+                    change_scores<MOD>(r, P, slope, key0 - row_pos);
+                    if constexpr ((MOD & PA_BIAS) != 0) {
+                        if (P.ch.parents && key0 + PA_TILE > c.s.ctx) {
+#pragma unroll
+                            for (int k = 0; k < PA_TILE; ++k) {
+                                const int node = key0 + k - c.s.ctx;
+                                const float more = __shfl_sync(0xFFFFFFFFu, node_far, node & 31);
+                                if (node >= 0 && node < KV_MAX_TREE) r[k] = __float_as_uint(fmaf(slope, more, __uint_as_float(r[k])));
+                            }
+                        }
+                    }
+                }
                 if (key0 + PA_TILE > seen_by_all) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -1264,7 +1325,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                     for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(r[k + 2 * j]), __uint_as_float(r[k + 2 * j + 1]));
                 }
                 const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const float top = F16 ? fmaf(most, P.c, -PA_F16_BELOW) : most * P.c;
+                const float top = MOD != 0 ? (F16 ? most - PA_F16_BELOW : most) : F16 ? fmaf(most, P.c, -PA_F16_BELOW) : most * P.c;
                 if (done == 0) {
                     m = top;
                 } else {
@@ -1295,7 +1356,8 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const int at2 = 32 * q + 2 * k;
-                        const f32x2 e = ex2x2(fma2(pack2(__uint_as_float(r[at2]), __uint_as_float(r[at2 + 1])), cc, mm));
+                        const f32x2 x = pack2(__uint_as_float(r[at2]), __uint_as_float(r[at2 + 1]));
+                        const f32x2 e = ex2x2(MOD != 0 ? add2(x, mm) : fma2(x, cc, mm));
                         sum = at2 == 0 ? e : add2(sum, e);
                         float a, b;
                         unpack2(e, a, b);
@@ -1438,7 +1500,7 @@ __device__ __forceinline__ void clear_bad_rows(const PagedAttnParams& P, int D) 
     }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int MOD>
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams P) {
@@ -1500,7 +1562,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // 256 x 216 + 128 x 72 is the same sum.
         if (warp < 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
-            softmax_rows<D, F16>(P, sh, warp >> 2, q_smem, ring, tmem);
+            softmax_rows<D, F16, MOD>(P, sh, warp >> 2, q_smem, ring, tmem);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
             if (warp == 8 || warp == 10) {
@@ -1534,10 +1596,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     if (threadIdx.x == 0 && sh.err) raise_flag(P.ch.status, SV_FLAG_TIMEOUT);
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int MOD>
 static cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p,
                           int grid, cudaStream_t stream) {
-    auto kernel = paged_attention_kernel<D, F16>;
+    auto kernel = paged_attention_kernel<D, F16, MOD>;
     static std::atomic<int> attr_done[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1561,12 +1623,28 @@ static cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, cons
     return cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_k, tm_v, p);
 }
 
-cudaError_t launch_paged_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                   const PagedAttnParams& p, int D, int f16, int sms, cudaStream_t stream) {
+template <int MOD>
+static cudaError_t launch_mod(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p,
+                              int D, int f16, int sms, cudaStream_t stream) {
     const int grid = sms < PA_MAX_CTAS ? sms : PA_MAX_CTAS;
     if (D == 128)
-        return f16 ? launch<128, true>(tm_q, tm_k, tm_v, p, grid, stream) : launch<128, false>(tm_q, tm_k, tm_v, p, grid, stream);
-    return f16 ? launch<64, true>(tm_q, tm_k, tm_v, p, grid, stream) : launch<64, false>(tm_q, tm_k, tm_v, p, grid, stream);
+        return f16 ? launch<128, true, MOD>(tm_q, tm_k, tm_v, p, grid, stream) : launch<128, false, MOD>(tm_q, tm_k, tm_v, p, grid, stream);
+    return f16 ? launch<64, true, MOD>(tm_q, tm_k, tm_v, p, grid, stream) : launch<64, false, MOD>(tm_q, tm_k, tm_v, p, grid, stream);
 }
+
+#ifdef PA_SCORED
+cudaError_t launch_paged_attention_scored(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                          const PagedAttnParams& p, int D, int f16, int sms, cudaStream_t stream) {
+    if (!p.slopes) return launch_mod<PA_CAP>(tm_q, tm_k, tm_v, p, D, f16, sms, stream);
+    if (p.cap_c == 0.0f) return launch_mod<PA_BIAS>(tm_q, tm_k, tm_v, p, D, f16, sms, stream);
+    return launch_mod<PA_CAP | PA_BIAS>(tm_q, tm_k, tm_v, p, D, f16, sms, stream);
+}
+#else
+cudaError_t launch_paged_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                   const PagedAttnParams& p, int D, int f16, int sms, cudaStream_t stream) {
+    if (p.slopes || p.cap_c != 0.0f) return launch_paged_attention_scored(tm_q, tm_k, tm_v, p, D, f16, sms, stream);
+    return launch_mod<0>(tm_q, tm_k, tm_v, p, D, f16, sms, stream);
+}
+#endif
 
 }  // namespace sv

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.cut_reference import cut_row, draw
+from cut_reference import cut_row, draw
 
 pytestmark = pytest.mark.gpu
 
