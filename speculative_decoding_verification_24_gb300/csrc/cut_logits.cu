@@ -15,18 +15,24 @@
 // fp32 a sum of 150,000 weights is off by 1e-6, as much as flat rows' edges lie
 // apart.
 //
-// One cluster of CTAs per row; a row lies in their shared memory, read from HBM
-// once. Steps, of which a row takes those that its settings need:
-//   1. the maximum, and a bound on the k-th largest from the largest of each
-//      warp's (or lane group's) part: k parts' maxima lie at or above it;
-//   2. the sum of all weights, for top-p without top-k;
-//   3. what lies at or above the bound goes to a list in the first CTA, which
-//      ranks it by comparing all pairs and applies the cuts there;
-//   4. where that is more than the list takes, the place is found by histograms:
-//      2048 bins over the places that are possible, the bin in which the count
-//      or the weight is reached becomes the next range, until it fits the list;
-//   5. the draw, over the list or over the rows' parts by their sums, or the
-//      row's output.
+// A row goes to one CTA, or, where rows are few, to a cluster of up to 8. It is
+// read from HBM once, and of every 16 bytes the largest logit's key (16 bits) is
+// kept in shared memory: whatever looks for large elements afterwards reads those
+// keys, and from L2 only the pieces that hold some. Steps, of which a row takes
+// those that its settings need:
+//   1. the maximum and the pieces' keys;
+//   2. top-k: a bound on the k-th largest element (k pieces' maxima lie at or
+//      above it, by ranking the warps' maxima or a histogram of the pieces'); what
+//      lies at or above it goes to the first CTA's list, which sorts it and
+//      applies all cuts there;
+//   3. top-p alone: the sum of all weights, and a histogram of log weights which
+//      says nearly where p of it is reached; then the exact sum above that
+//      region, whose elements go to the list, where the place is found;
+//   4. where a list overflows (thousands of equal logits, k in the thousands) the
+//      place is found by exact histograms over shrinking ranges of places;
+//   5. the draw, over the sorted list or over the warps' parts by their sums and
+//      then in one of them; or the row's output: pieces whose key lies below the
+//      cut are written as -inf without another look.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -45,8 +51,9 @@ constexpr int CL_THREADS = 512;
 constexpr int CL_WARPS = CL_THREADS / 32;
 constexpr int CL_MAX_CS = 8;
 constexpr int CL_BINS = 2048;
-constexpr int CL_LIST = 1024;
-constexpr int CL_ROUNDS = 5;  // of 11 bits each; a place has 50
+constexpr int CL_LIST = 2048;
+constexpr int CL_HITS = 2048;  // pieces of one CTA that gather() reads in one step
+constexpr int CL_ROUNDS = 5;   // of 11 bits each; a place has 50
 constexpr int CL_INDEX_BITS = 18;
 constexpr uint32_t CL_INDEX_MASK = (1u << CL_INDEX_BITS) - 1;
 constexpr int CL_EXP_BITS = 8;
@@ -83,41 +90,14 @@ constexpr ExpTable make_exp_table() {
 }
 __device__ const ExpTable g_exp_table = make_exp_table();
 
-// What one row's cluster shares; every CTA has its own copy, written by all.
-struct CutShared {
-    ExpEntry exp[CL_EXP];
-    // histogram; after its rounds the first CTA's list: places in mass, weights in list_w
-    u64 mass[CL_BINS];
-    union {
-        uint32_t count[CL_BINS];
-        u64 list_w[CL_LIST];
-    };
-    float warp_max[CL_MAX_CS * CL_WARPS];
-    float group_min[CL_MAX_CS * CL_WARPS];
-    u64 cta_mass[2][CL_MAX_CS];      // sums over the cluster's CTAs, two in turn
-    uint32_t cta_count[2][CL_MAX_CS];
-    u64 warp_mass[CL_WARPS];
-    uint32_t warp_count[CL_WARPS];
-    u64 seg_mass[CL_MAX_CS];
-    uint32_t seg_count[CL_MAX_CS];
-    // the bin found by a round, or the place found in the list
-    u64 found_mass, found_place;
-    uint32_t found_bin, found_above, found_count;
-    uint32_t list_n;
-    u64 block_mass;
-    float bound;
-};
-
 struct RowScale {
     float top;       // the row's maximum
     float ch, cl;    // 256 log2(e) / T in two floats
 };
 
-__device__ __forceinline__ float elem_of(uint32_t w, int half) { return half ? bf16_hi(w) : bf16_lo(w); }
-
 // Order of floats as unsigned integers; -0 counts as 0.
 __device__ __forceinline__ uint32_t key32(float z) {
-    const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));
+    const uint32_t u = __float_as_uint(z), b = u == 0x80000000u ? 0u : u;
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_key32(uint32_t k) {
@@ -130,11 +110,24 @@ __device__ __forceinline__ float key_value(uint32_t k) { return from_key32(BF16 
 // A place in the row's order. A padding element has key 0 (a negative NaN),
 // which no place that is kept has.
 __device__ __forceinline__ u64 place_of(uint32_t key, int index) {
-    return (u64)key << CL_INDEX_BITS | (CL_INDEX_MASK - (uint32_t)index);
+    return (u64)key << CL_INDEX_BITS | ((CL_INDEX_MASK - (uint32_t)index) & CL_INDEX_MASK);
 }
 constexpr u64 CL_LOWEST = 1ull << CL_INDEX_BITS;  // at or below every real element's place
 __device__ __forceinline__ int place_index(u64 p) { return (int)(CL_INDEX_MASK - ((uint32_t)p & CL_INDEX_MASK)); }
 __device__ __forceinline__ uint32_t place_key(u64 p) { return (uint32_t)(p >> CL_INDEX_BITS); }
+
+constexpr float CL_L1 = 2.7076061740622863e-3f;  // ln 2 / 256
+constexpr float CL_L2 = 3.6655655969053526e-6f;  // its square / 2
+constexpr float CL_L3 = 3.3083027270131e-9f;     // its cube / 6
+// 2^(n / 256) (1 + e), n as the low bits of a float that 1.5 * 2^23 was added to.
+__device__ __forceinline__ u64 weight_of(uint32_t t_bits, float e, const ExpEntry* table) {
+    const ExpEntry en = table[t_bits & (CL_EXP - 1)];  // (the magic number's low bits are 0)
+    const int tail = __float2int_rn(__fmul_rn(en.f, e));  // below 2^30.5
+    const u64 q = en.q + (u64)((long long)tail * 32);
+    const uint32_t sh = (0x4B400000u + CL_EXP - 1 - t_bits) >> CL_EXP_BITS;  // ceil(-n / 256)
+    const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
+    return __uint_as_float(t_bits) > 12582912.0f - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
+}
 
 // exp((z - top) / T) in units of 2^-44. With d = z - top in two floats, exactly,
 // y = 256 d log2(e) / T = n + x, n whole and |x| <= 1/2: 2^(n / 256) comes from the
@@ -148,34 +141,57 @@ __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry
     const float t = __fmaf_rn(dh, s.ch, MAGIC);
     const float n = __fsub_rn(t, MAGIC);
     const float x = __fadd_rn(__fmaf_rn(dh, s.ch, -n), __fmaf_rn(dh, s.cl, __fmul_rn(dl, s.ch)));
-    constexpr float L1 = 2.7076061740622863e-3f;   // ln 2 / 256
-    constexpr float L2 = 3.6655655969053526e-6f;   // its square / 2
-    constexpr float L3 = 3.3083027270131e-9f;      // its cube / 6
-    const float e = __fmul_rn(x, __fmaf_rn(x, __fmaf_rn(x, L3, L2), L1));
-    const int ni = __float_as_int(t) - 0x4B400000;
-    const ExpEntry en = table[ni & (CL_EXP - 1)];
-    const int tail = __float2int_rn(__fmul_rn(en.f, e));  // below 2^30.5
-    const u64 q = en.q + (u64)((long long)tail * 32);
-    const int sh = -(ni >> CL_EXP_BITS);
-    const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
-    return t > MAGIC - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
+    const float e = __fmul_rn(x, __fmaf_rn(x, __fmaf_rn(x, CL_L3, CL_L2), CL_L1));
+    return weight_of(__float_as_uint(t), e, table);
 }
 
-// The elements of one CTA's part of a row, in 16-byte pieces of which a warp has
-// a run; lane l has its pieces l, l + 32, ...
-template <bool BF16>
-struct Part {
-    static constexpr int E = BF16 ? 8 : 4;
-    const uint4* data;   // shared memory
-    int v0, v1;          // this warp's pieces of the part
-    int first;           // index in the row of the part's first element (negative: padding)
-    __device__ __forceinline__ int index(int v) const { return first + v * E; }
+
+// Two of them at once: the same arithmetic, the exponents' part in packed
+// instructions.
+__device__ __forceinline__ void weight_pair(float z0, float z1, const RowScale& s, const ExpEntry* table, u64& w0, u64& w1) {
+    const f32x2 z = pack2(z0, z1), top = pack2(s.top, s.top), minus = pack2(-1.0f, -1.0f), ch = pack2(s.ch, s.ch), cl = pack2(s.cl, s.cl);
+    const f32x2 magic = pack2(12582912.0f, 12582912.0f);
+    const f32x2 dh = fma2(top, minus, z);
+    const f32x2 bb = fma2(z, minus, dh);
+    const f32x2 dl = fma2(add2(top, bb), minus, fma2(fma2(bb, minus, dh), minus, z));
+    const f32x2 t = fma2(dh, ch, magic);
+    const f32x2 x = add2(fma2(dh, ch, fma2(t, minus, magic)), fma2(dh, cl, mul2(dl, ch)));
+    const f32x2 e = mul2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1)));
+    float t0, t1, e0, e1;
+    unpack2(t, t0, t1);
+    unpack2(e, e0, e1);
+    w0 = weight_of(__float_as_uint(t0), e0, table);
+    w1 = weight_of(__float_as_uint(t1), e1, table);
+}
+
+// What one row's cluster shares; every CTA has its own copy.
+struct CutShared {
+    ExpEntry exp[CL_EXP];
+    u64 list[CL_LIST];               // the first CTA's: places, sorted later; or the exact histogram's weights
+    union {
+        uint32_t count[CL_BINS];     // histogram
+        uint32_t hits[CL_HITS];      // pieces to read
+    };
+    u64 part_mass[CL_MAX_CS * CL_WARPS];  // weights of every warp's part, in the first CTA
+    float warp_max[CL_MAX_CS * CL_WARPS];
+    float lane_min[CL_MAX_CS * CL_WARPS];
+    u64 cta_mass[CL_MAX_CS];
+    u64 warp_mass[CL_WARPS];
+    uint32_t warp_count[CL_WARPS];
+    float warp_value[CL_WARPS];
+    u64 seg_mass[CL_MAX_CS];
+    uint32_t seg_count[CL_MAX_CS];
+    // what a search has found, told to every CTA
+    u64 found_mass, found_place, draw_at;
+    uint32_t found_bin, found_above, found_count, draw_warp;
+    uint32_t list_n, hits_n, kept;
+    float bound;
 };
 
 template <bool BF16>
 __device__ __forceinline__ float piece_elem(const uint4& x, int e) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    return BF16 ? elem_of(w[e >> 1], e & 1) : __uint_as_float(w[e]);
+    return BF16 ? (e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1])) : __uint_as_float(w[e]);
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -183,120 +199,325 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
+template <class N>
+__device__ __forceinline__ N warp_scan(N v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const u64 t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        const N t = __shfl_up_sync(0xFFFFFFFFu, v, o);
         if (lane >= o) v += t;
     }
     return v;
 }
 
-// Sum of weights and number of elements at or above `cut`, per warp into
-// sh.warp_mass / warp_count, and over the cluster.
+// One CTA's part of a row, in 16-byte pieces of which a warp has a run; lane l
+// has its pieces l, l + 32, ...
 template <bool BF16>
-__device__ __forceinline__ void sum_kept(const Part<BF16>& part, CutShared& sh, const RowScale& s, u64 cut, int lane, int warp,
-                                         bool weights, cg::cluster_group& cluster, int CS, int rank, int slot, u64& mass, uint32_t& count) {
-    u64 m = 0;
-    uint32_t n = 0;
-    const uint32_t cut_key = place_key(cut);
-    for (int v = part.v0 + lane; v < part.v1; v += 32) {
-        const uint4 x = part.data[v];
-        const int i0 = part.index(v);
+struct Row {
+    static constexpr int E = BF16 ? 8 : 4;
+    static constexpr int ES = BF16 ? 2 : 4;
+    const char* src;       // the row's first element
+    int V, first;          // index in the row of the part's first element (negative: padding)
+    int n_vecs, v0, v1;    // pieces of the part, this warp's
+    int slice, run;        // pieces per CTA and per warp
+    uint16_t* keys;        // shared memory: a piece's largest key, upper 16 bits
+    CutShared* sh;
+    RowScale s;
+    int CS, rank, lane, warp;
+
+    __device__ __forceinline__ int index(int v) const { return first + v * E; }
+    __device__ __forceinline__ bool partial(int v) const { return index(v) < 0 || index(v) + E > V; }
+    // A piece; where the row fills it in part, `pad` (an element's bits) beside it.
+    __device__ __forceinline__ uint4 load(int v, uint32_t pad) const {
+        const int i0 = index(v);
+        uint4 x;
+        if (!partial(v)) {
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                         : "l"(src + (int64_t)i0 * ES)
+                         : "memory");
+            return x;
+        }
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < Part<BF16>::E; ++e) {
-            const float z = piece_elem<BF16>(x, e);
-            const uint32_t key = key_of<BF16>(z);
-            if (key > cut_key || (key == cut_key && place_of(key, i0 + e) >= cut)) {
-                ++n;
-                if (weights) m += weight(z, s, sh.exp);
+        for (int e = 0; e < E; ++e) {
+            uint32_t b = pad;
+            if (i0 + e >= 0 && i0 + e < V)
+                b = BF16 ? *reinterpret_cast<const uint16_t*>(src + (int64_t)(i0 + e) * 2) : *reinterpret_cast<const uint32_t*>(src + (int64_t)(i0 + e) * 4);
+            if (BF16) w[e / 2] |= b << (16 * (e % 2));
+            else w[e] = b;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // padding that has no place in the order (a negative NaN, key 0)
+    static constexpr uint32_t NOBODY = BF16 ? 0xFFFFu : 0xFFFFFFFFu;
+    static constexpr uint32_t MINUS_INF = BF16 ? 0xFF80u : 0xFF800000u;
+
+    // Every thread of the row's CTAs has got here, and what they wrote is seen.
+    __device__ __forceinline__ void sync() const {
+        if (CS == 1) __syncthreads();
+        else cg::this_cluster().sync();
+    }
+    template <class X>
+    __device__ __forceinline__ X* of(X* mine, int cta) const { return CS == 1 ? mine : cg::this_cluster().map_shared_rank(mine, cta); }
+    template <class F>
+    __device__ __forceinline__ void each_cta(F&& f) const {
+        for (int c = 0; c < CS; ++c) f(of(sh, c));
+    }
+
+    // f(x, v) for this lane's pieces whose key is at least that of `lo`; the next
+    // one is on its way meanwhile.
+    template <class F>
+    __device__ __forceinline__ void each_piece(u64 lo, F&& f) const {
+        const uint32_t lo16 = lo16_of(lo);
+        int v = v0 + lane;
+        const auto next = [&](int at) {
+            while (at < v1 && keys[at] < lo16) at += 32;
+            return at;
+        };
+        v = next(v);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (v < v1) x = load(v, NOBODY);
+        while (v < v1) {
+            const int n = next(v + 32);
+            uint4 y = x;
+            if (n < v1) y = load(n, NOBODY);
+            f(x, v);
+            x = y;
+            v = n;
+        }
+    }
+    static __device__ __forceinline__ uint32_t lo16_of(u64 place) { return BF16 ? place_key(place) : place_key(place) >> 16; }
+};
+
+// Appends to the first CTA's list; what does not fit is counted only.
+__device__ __forceinline__ void append(CutShared* head, u64 place) {
+    const uint32_t at = atomicAdd(&head->list_n, 1u);
+    if (at < CL_LIST) head->list[at] = place;
+}
+
+// The places in [lo, hi] of all parts, to the list: the CTA collects its pieces
+// that hold some, then its threads read one each. Returns how many there are.
+template <bool BF16>
+__device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    CutShared* head = row.of(&sh, 0);
+    const uint32_t lo16 = R::lo16_of(lo);
+    const auto look = [&](int v) {
+        const uint4 x = row.load(v, R::NOBODY);
+        const int i0 = row.index(v);
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            const u64 p = place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e);
+            if (p >= lo && p <= hi) append(head, p);
+        }
+    };
+    // 8 keys at a time; the keys behind the part's last are 0
+    const uint4* keys = reinterpret_cast<const uint4*>(row.keys);
+    for (int g = threadIdx.x; g * 8 < row.n_vecs; g += CL_THREADS) {
+        const uint4 k8 = keys[g];
+        const uint32_t w[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (((w[i / 2] >> (16 * (i % 2))) & 0xFFFFu) < lo16) continue;
+            const int v = g * 8 + i;
+            if (v >= row.n_vecs) continue;
+            const uint32_t at = atomicAdd(&sh.hits_n, 1u);
+            if (at < CL_HITS) sh.hits[at] = (uint32_t)v;
+        }
+    }
+    __syncthreads();
+    if (sh.hits_n <= CL_HITS) {
+        for (int i = threadIdx.x; i < (int)sh.hits_n; i += CL_THREADS) look((int)sh.hits[i]);
+    } else {
+        for (int v = row.v0 + row.lane; v < row.v1; v += 32)
+            if (row.keys[v] >= lo16) look(v);
+    }
+    row.sync();
+    const uint32_t n = head->list_n;
+    if (threadIdx.x == 0) sh.hits_n = 0;
+    return n;
+}
+
+// Sorts the first n entries of the list, descending, by this CTA: few by counting
+// what is larger (4 lanes per entry), more by a bitonic network in shared memory,
+// whose steps over up to 64 neighbours stay within a warp.
+__device__ __noinline__ void sort_list(u64* list, int n) {
+    const int tid = threadIdx.x;
+    if (n <= CL_THREADS / 4) {
+        const int i = tid >> 2;
+        u64 mine = 0;
+        int before = 0;
+        if (i < n) {
+            mine = list[i];
+            for (int j = tid & 3; j < n; j += 4) before += list[j] > mine;
+        }
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
+        __syncthreads();
+        if (i < n && (tid & 3) == 0) list[before] = mine;
+        __syncthreads();
+        return;
+    }
+    int size = 256;
+    while (size < n) size <<= 1;
+    for (int i = n + tid; i < size; i += CL_THREADS) list[i] = 0;
+    for (int block = 2; block <= size; block <<= 1) {
+        for (int stride = block >> 1; stride > 0; stride >>= 1) {
+            if (stride >= 32 || stride == block >> 1) __syncthreads();
+            else __syncwarp();
+            for (int p = tid; p < size / 2; p += CL_THREADS) {
+                const int a = 2 * p - (p & (stride - 1)), b = a + stride;
+                const u64 x = list[a], y = list[b];
+                const bool down = (a & block) == 0;
+                if ((x < y) == down) {
+                    list[a] = y;
+                    list[b] = x;
+                }
             }
         }
     }
-    m = warp_sum(m);
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (lane == 0) {
-        sh.warp_mass[warp] = m;
-        sh.warp_count[warp] = n;
-    }
     __syncthreads();
-    if (warp == 0) {
-        u64 a = warp_sum(lane < CL_WARPS ? sh.warp_mass[lane] : 0);
-        uint32_t c = __reduce_add_sync(0xFFFFFFFFu, lane < CL_WARPS ? sh.warp_count[lane] : 0);
-        if (lane < CS) {
-            *cluster.map_shared_rank(&sh.cta_mass[slot][rank], lane) = a;
-            *cluster.map_shared_rank(&sh.cta_count[slot][rank], lane) = c;
-        }
-    }
-    cluster.sync();
-    mass = 0;
-    count = 0;
-    for (int c = 0; c < CS; ++c) {
-        mass += sh.cta_mass[slot][c];
-        count += sh.cta_count[slot][c];
-    }
 }
 
-// Appends the places in [lo, hi] of all parts to the first CTA's list. What does
-// not fit is counted only. The list's places lie where the histogram was.
-template <bool BF16>
-__device__ __forceinline__ uint32_t gather(const Part<BF16>& part, CutShared& sh, u64 lo, u64 hi, int lane, cg::cluster_group& cluster) {
-    CutShared* head = cluster.map_shared_rank(&sh, 0);
-    const uint32_t lo_key = place_key(lo);
-    for (int v = part.v0 + lane; v < part.v1; v += 32) {
-        const uint4 x = part.data[v];
-        const int i0 = part.index(v);
+// Inclusive sums over the CTA's threads.
+template <class N>
+__device__ __forceinline__ N block_scan(N v, N* warp_sums, int lane, int warp, N& total) {
+    v = warp_scan(v, lane);
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    total = 0;
 #pragma unroll
-        for (int e = 0; e < Part<BF16>::E; ++e) {
-            const uint32_t key = key_of<BF16>(piece_elem<BF16>(x, e));
-            if (key < lo_key) continue;
-            const u64 p = place_of(key, i0 + e);
-            if (p < lo || p > hi) continue;
-            const uint32_t at = atomicAdd(&head->list_n, 1u);
-            if (at < CL_LIST) head->mass[at] = p;
-        }
+    for (int w = 0; w < CL_WARPS; ++w) {
+        const N t = warp_sums[w];
+        if (w < warp) v += t;
+        total += t;
     }
-    cluster.sync();
-    return head->list_n;
+    return v;
 }
 
-// One round of the search in [lo, hi]: the bin in which the count `k` (by_mass
-// false) or the weight `goal` is reached from above, given what lies above hi.
-// The range becomes that bin.
+// The first bin, from 0 on, in which the sum over the bins of all CTAs reaches
+// `goal`, told to every CTA as found_bin (the last one if none does). A bin's value
+// is its count, or count / 4096 times 2^(-decay * bin). found_count: the count
+// of it and its two neighbours.
+template <bool BF16>
+__device__ __forceinline__ void find_bin(const Row<BF16>& row, float goal, float decay, float unit) {
+    CutShared& sh = *row.sh;
+    row.sync();
+    if (row.rank == 0) {
+        static_assert(CL_BINS == 4 * CL_THREADS, "four bins per thread");
+        const int tid = threadIdx.x;
+        if (tid == 0) sh.found_bin = CL_BINS - 1;
+        uint32_t n[4] = {0, 0, 0, 0};
+        for (int c = 0; c < row.CS; ++c) {
+            const uint4 k = reinterpret_cast<const uint4*>(row.of(&sh, c)->count)[tid];
+            n[0] += k.x, n[1] += k.y, n[2] += k.z, n[3] += k.w;
+        }
+        if (row.CS > 1) reinterpret_cast<uint4*>(sh.list)[tid] = make_uint4(n[0], n[1], n[2], n[3]);
+        float v[4], sum = 0.0f, total;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = (float)n[i] * unit * (decay == 0.0f ? 1.0f : ex2(-decay * (float)(4 * tid + i)));
+            sum += v[i];
+        }
+        float before = block_scan(sum, sh.warp_value, row.lane, row.warp, total) - sum;
+        if (before < goal && before + sum >= goal) {
+            int b = 4 * tid + 3;
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                float upto = before;
+                for (int q = 0; q <= i; ++q) upto += v[q];
+                if (upto >= goal) b = 4 * tid + i;
+            }
+            atomicMin(&sh.found_bin, (uint32_t)b);  // (sums of floats need not ascend to the last bit)
+        }
+        __syncthreads();
+        if (tid < row.CS) {
+            const uint32_t b = sh.found_bin;
+            const uint32_t* all = row.CS > 1 ? reinterpret_cast<const uint32_t*>(sh.list) : sh.count;
+            const uint32_t near = all[b] + (b > 0 ? all[b - 1] : 0) + (b + 1 < CL_BINS ? all[b + 1] : 0);
+            CutShared* o = row.of(&sh, tid);
+            o->found_bin = b;
+            o->found_count = near;
+        }
+    }
+    row.sync();
+}
+
+template <bool BF16>
+__device__ __forceinline__ void clear_bins(const Row<BF16>& row) {
+    reinterpret_cast<uint4*>(row.sh->count)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+}
+
+// Sums of the weights at or above `cut`, this warp's into the first CTA's
+// part_mass and the total to every thread.
+template <bool BF16>
+__device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    u64 m = 0;
+    row.each_piece(cut, [&](const uint4& x, int v) {
+        const int i0 = row.index(v);
+#pragma unroll
+        for (int e = 0; e < R::E; e += 2) {
+            const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
+            const bool in0 = place_of(key_of<BF16>(z0), i0 + e) >= cut, in1 = place_of(key_of<BF16>(z1), i0 + e + 1) >= cut;
+            u64 w0, w1;
+            weight_pair(z0, z1, row.s, sh.exp, w0, w1);
+            m += (in0 ? w0 : 0) + (in1 ? w1 : 0);
+        }
+    });
+    m = warp_sum(m);
+    if (row.lane == 0) row.of(&sh, 0)->part_mass[row.rank * CL_WARPS + row.warp] = m;
+    row.sync();
+    u64 total = 0;
+    const u64* parts = row.of(&sh, 0)->part_mass;
+    for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) total += parts[w];
+    return warp_sum(total);
+}
+
+// One round of the exact search in [lo, hi]: the bin in which the count `k`
+// (BY_MASS false) or the weight `goal` is reached from above, given what lies
+// above hi. The range becomes that bin.
 template <bool BF16, bool BY_MASS>
-__device__ __forceinline__ uint32_t narrow(const Part<BF16>& part, CutShared& sh, const RowScale& s, u64& lo, u64& hi, uint32_t& above,
-                                           u64& mass_above, uint32_t k, double goal, int lane, int warp, cg::cluster_group& cluster,
-                                           int CS, int rank) {
-    const int tid = threadIdx.x;
+__device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& hi, uint32_t& above, u64& mass_above, uint32_t k, double goal) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    u64* mass = sh.list;
+    const int tid = threadIdx.x, lane = row.lane, warp = row.warp, CS = row.CS;
     const u64 width = hi - lo;  // one less than the places
     const int bits = 64 - __clzll((long long)width);
     const int shift = width == 0 ? 0 : max(0, bits - 11);
     for (int i = tid; i < CL_BINS; i += CL_THREADS) {
         sh.count[i] = 0;
-        if (BY_MASS) sh.mass[i] = 0;
+        mass[i] = 0;
     }
-    __syncthreads();
-    const uint32_t lo_key = place_key(lo);
-    for (int v = part.v0 + lane; v < part.v1; v += 32) {
-        const uint4 x = part.data[v];
-        const int i0 = part.index(v);
-#pragma unroll
-        for (int e = 0; e < Part<BF16>::E; ++e) {
+    if (tid == 0) {
+        sh.found_bin = 0;
+        sh.found_above = above;
+        sh.found_mass = mass_above;
+        sh.found_count = 0;
+    }
+    row.sync();
+    row.each_piece(lo, [&](const uint4& x, int v) {
+        const int i0 = row.index(v);
+#pragma unroll 1
+        for (int e = 0; e < R::E; ++e) {
             const float z = piece_elem<BF16>(x, e);
-            const uint32_t key = key_of<BF16>(z);
-            if (key < lo_key) continue;
-            const u64 p = place_of(key, i0 + e);
+            const u64 p = place_of(key_of<BF16>(z), i0 + e);
             if (p < lo || p > hi) continue;
             const int bin = (int)((p - lo) >> shift);
             atomicAdd(&sh.count[bin], 1u);
-            if (BY_MASS) atomicAdd(&sh.mass[bin], weight(z, s, sh.exp));
+            if (BY_MASS) atomicAdd(&mass[bin], weight(z, row.s, sh.exp));
         }
-    }
-    cluster.sync();
+    });
+    row.sync();
     // A CTA adds up its share of the bins over all CTAs; a thread has `per`
     // neighbouring ones.
     const int seg = CL_BINS / CS, per = max(1, seg / CL_THREADS);
-    const int b0 = rank * seg + tid * per;
+    const int b0 = row.rank * seg + tid * per;
     const bool on = tid * per < seg;
     uint32_t c_of[4] = {0, 0, 0, 0}, c_sum = 0;  // seg / 512 <= 4
     u64 m_of[4] = {0, 0, 0, 0}, m_sum = 0;
@@ -305,136 +526,112 @@ __device__ __forceinline__ uint32_t narrow(const Part<BF16>& part, CutShared& sh
         for (int i = 0; i < 4; ++i) {
             if (i >= per) break;
             for (int c = 0; c < CS; ++c) {
-                const CutShared* o = cluster.map_shared_rank(&sh, c);
+                const CutShared* o = row.of(&sh, c);
                 c_of[i] += o->count[b0 + i];
-                if (BY_MASS) m_of[i] += o->mass[b0 + i];
+                if (BY_MASS) m_of[i] += o->list[b0 + i];
             }
             c_sum += c_of[i];
             m_sum += m_of[i];
         }
     }
-    // inclusive sums from this thread's bins upwards within the share
-    uint32_t c_in = c_sum;
-    u64 m_in = m_sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t ct = __shfl_down_sync(0xFFFFFFFFu, c_in, o);
-        const u64 mt = BY_MASS ? __shfl_down_sync(0xFFFFFFFFu, m_in, o) : 0;
-        if (lane + o < 32) {
-            c_in += ct;
-            m_in += mt;
-        }
-    }
-    if (lane == 0) {
-        sh.warp_count[warp] = c_in;
-        sh.warp_mass[warp] = m_in;
-    }
-    __syncthreads();
-    for (int w = warp + 1; w < CL_WARPS; ++w) {
-        c_in += sh.warp_count[w];
-        m_in += sh.warp_mass[w];
-    }
+    // inclusive sums from the share's first bin on, turned into those from above
+    uint32_t c_total;
+    u64 m_total;
+    const uint32_t c_in = block_scan(c_sum, sh.warp_count, lane, warp, c_total);
+    const u64 m_in = block_scan(m_sum, sh.warp_mass, lane, warp, m_total);
     if (tid == 0) {
-        for (int c = 0; c < CS; ++c) {
-            *cluster.map_shared_rank(&sh.seg_count[rank], c) = c_in;
-            *cluster.map_shared_rank(&sh.seg_mass[rank], c) = m_in;
-        }
+        row.each_cta([&](CutShared* o) {
+            o->seg_count[row.rank] = c_total;
+            o->seg_mass[row.rank] = m_total;
+        });
     }
-    cluster.sync();
-    uint32_t c_up = above;
-    u64 m_up = mass_above;
-    for (int c = rank + 1; c < CS; ++c) {
-        c_up += sh.seg_count[c];
-        m_up += sh.seg_mass[c];
+    row.sync();
+    uint32_t c = above + c_total - c_in;
+    u64 m = mass_above + m_total - m_in;
+    for (int q = row.rank + 1; q < CS; ++q) {
+        c += sh.seg_count[q];
+        m += sh.seg_mass[q];
     }
     if (on) {
-        // what lies above this thread's bins
-        uint32_t c = c_up + c_in - c_sum;
-        u64 m = m_up + m_in - m_sum;
+        // c and m: what lies above the bin
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
             if (i >= per) continue;
             const bool reached = BY_MASS ? (double)(m + m_of[i]) >= goal : c + c_of[i] >= k;
             const bool before = BY_MASS ? (c != 0 && (double)m >= goal) : c >= k;
             if (c_of[i] != 0 && reached && !before) {
-                for (int d = 0; d < CS; ++d) {
-                    CutShared* o = cluster.map_shared_rank(&sh, d);
+                row.each_cta([&](CutShared* o) {
                     o->found_bin = (uint32_t)(b0 + i);
                     o->found_above = c;
                     o->found_mass = m;
                     o->found_count = c_of[i];
-                }
+                });
             }
             c += c_of[i];
             m += m_of[i];
         }
     }
-    cluster.sync();
+    row.sync();
     above = sh.found_above;
     mass_above = sh.found_mass;
-    const u64 bin = sh.found_bin;
-    const u64 new_lo = lo + (bin << shift);
+    const uint32_t n = sh.found_count;
+    const u64 new_lo = lo + ((u64)sh.found_bin << shift);
     hi = min(hi, new_lo + ((1ull << shift) - 1));
     lo = new_lo;
-    return sh.found_count;
+    row.sync();  // everyone has read what was found
+    return n;
 }
 
-// The place of the last element that a cut keeps: the search narrows [lo, hi]
-// until what is left fits the list, and the first CTA picks it there.
-template <bool BF16, bool BY_MASS>
-__device__ __noinline__ u64 find_cut(const Part<BF16>& part, CutShared& sh, const RowScale& s, u64 lo, u64 hi, uint32_t k, double goal,
-                                     int lane, int warp, int CS, int rank, uint32_t& kept) {
-    cg::cluster_group cluster = cg::this_cluster();
-    uint32_t above = 0, left = CL_LIST + 1;
-    u64 mass_above = 0;
-    for (int round = 0; round < CL_ROUNDS && left > CL_LIST; ++round)
-        left = narrow<BF16, BY_MASS>(part, sh, s, lo, hi, above, mass_above, k, goal, lane, warp, cluster, CS, rank);
-    if (threadIdx.x == 0) {
-        sh.list_n = 0;
-        sh.found_place = lo;
+// In the sorted list of n places below `above` others of weight mass_above: the
+// first one with which the count or the weight is reached, or 0. This CTA's
+// threads; list_w: scratch for nothing but the scan.
+template <bool BF16>
+__device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool by_mass, uint32_t above, u64 mass_above, uint32_t k, double goal) {
+    CutShared& sh = *row.sh;
+    const int tid = threadIdx.x;
+    if (!by_mass) {
+        const int at = (int)k - 1 - (int)above;
+        return at >= 0 && at < n ? sh.list[at] : 0;
     }
-    cluster.sync();  // (also: every CTA has read the histograms, on which the list goes)
-    const uint32_t n = min(gather<BF16>(part, sh, lo, hi, lane, cluster), (uint32_t)CL_LIST);
-    if (rank == 0) {
-        if (BY_MASS) {
-            for (int i = threadIdx.x; i < (int)n; i += CL_THREADS) sh.list_w[i] = weight(key_value<BF16>(place_key(sh.mass[i])), s, sh.exp);
-            __syncthreads();
-        }
-        for (int i = threadIdx.x; i < (int)n; i += CL_THREADS) {
-            const u64 mine = sh.mass[i];
-            uint32_t c = above;
-            u64 m = mass_above;
-            for (int j = 0; j < (int)n; ++j) {
-                if (sh.mass[j] > mine) {
-                    ++c;
-                    if (BY_MASS) m += sh.list_w[j];
-                }
-            }
-            const bool reached = BY_MASS ? (double)(m + sh.list_w[i]) >= goal : c + 1 == k;
-            const bool before = BY_MASS ? (c != 0 && (double)m >= goal) : false;
-            if (reached && !before) {
-                for (int d = 0; d < CS; ++d) {
-                    CutShared* o = cluster.map_shared_rank(&sh, d);
-                    o->found_place = mine;
-                    o->found_count = c + 1;
-                }
-            }
-        }
+    if (above != 0 && (double)mass_above >= goal) return 0;
+    if (tid == 0) sh.found_place = 0;
+    u64 carry = mass_above;
+    for (int base = 0; base < n; base += CL_THREADS) {
+        const int i = base + tid;
+        const u64 p = i < n ? sh.list[i] : 0, w = i < n ? weight(key_value<BF16>(place_key(p)), row.s, sh.exp) : 0;
+        u64 total;
+        const u64 incl = carry + block_scan(w, sh.warp_mass, row.lane, row.warp, total);
+        const u64 before = incl - w;
+        const bool first = above == 0 && i == 0;
+        if (i < n && (double)incl >= goal && (first || (double)before < goal)) sh.found_place = p;
+        carry += total;
     }
-    cluster.sync();
-    kept = sh.found_count;
+    __syncthreads();
     return sh.found_place;
 }
 
-__device__ __forceinline__ u64 block_sum(u64 v, CutShared& sh, int lane, int warp) {
-    v = warp_sum(v);
-    __syncthreads();
-    if (lane == 0) sh.warp_mass[warp] = v;
-    __syncthreads();
-    u64 t = 0;
-#pragma unroll
-    for (int w = 0; w < CL_WARPS; ++w) t += sh.warp_mass[w];
-    return t;
+// 4. The place of the last element that a cut keeps, exactly, in [lo, hi]: the
+// range narrows until what is left fits the list, where it is picked.
+template <bool BF16, bool BY_MASS>
+__device__ __noinline__ u64 find_cut(const Row<BF16>& row, u64 lo, u64 hi, uint32_t k, double goal) {
+    CutShared& sh = *row.sh;
+    uint32_t above = 0, left = CL_LIST + 1;
+    u64 mass_above = 0;
+    for (int round = 0; round < CL_ROUNDS && left > CL_LIST; ++round) left = narrow<BF16, BY_MASS>(row, lo, hi, above, mass_above, k, goal);
+    if (threadIdx.x == 0) sh.list_n = 0;
+    row.sync();
+    const int n = (int)min(gather(row, lo, hi), (uint32_t)CL_LIST);
+    if (row.rank == 0) {
+        sort_list(sh.list, n);
+        u64 place = reach_in_list(row, n, BY_MASS, above, mass_above, k, goal);
+        place = place ? place : lo;
+        __syncthreads();
+        if (threadIdx.x == 0) row.each_cta([&](CutShared* o) { o->found_place = place; });
+    }
+    row.sync();
+    const u64 place = sh.found_place;
+    row.sync();  // everyone has read it
+    return place;
 }
 
 // The largest whole number below or at u of `total`, below total.
@@ -450,58 +647,279 @@ __device__ __forceinline__ void put_token(const CutParams& P, int64_t row, int i
         P.logprobs[row] = (float)(((double)z - (double)s.top) * inv_t - log((double)total * (1.0 / (double)(1ull << CL_UNIT))));
 }
 
+// Draws from the first n of the sorted list, by this CTA.
+template <bool BF16>
+__device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& row, int64_t at_row, int n, double inv_t) {
+    CutShared& sh = *row.sh;
+    const int tid = threadIdx.x;
+    // entries become (index, weight), 18 and 45 bits, and are sorted by index
+    constexpr u64 W = (2ull << CL_UNIT) - 1;
+    for (int i = tid; i < n; i += CL_THREADS) {
+        const u64 p = sh.list[i];
+        sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(key_value<BF16>(place_key(p)), row.s, sh.exp);
+    }
+    __syncthreads();
+    if (n > 1) sort_list(sh.list, n);  // (descending reversed index)
+    u64 total = 0;
+    for (int i = tid; i < n; i += CL_THREADS) total += sh.list[i] & W;
+    u64 all;
+    block_scan(total, sh.warp_mass, row.lane, row.warp, all);
+    const u64 target = draw_target(P.uniforms[at_row], all);
+    u64 carry = 0;
+    for (int base = 0; base < n; base += CL_THREADS) {
+        const int i = base + tid;
+        const u64 e = i < n ? sh.list[i] : 0, w = e & W;
+        u64 sum;
+        const u64 incl = carry + block_scan(w, sh.warp_mass, row.lane, row.warp, sum);
+        if (i < n && incl - w <= target && target < incl) {
+            const int index = (int)(CL_INDEX_MASK - (uint32_t)(e >> (CL_UNIT + 1)));
+            const float z = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row.src)[index] << 16)
+                                 : reinterpret_cast<const float*>(row.src)[index];
+            put_token(P, at_row, index, z, row.s, inv_t, all);
+        }
+        carry += sum;
+    }
+}
+
+// Draws over the warps' parts, whose sums at or above `cut` lie in the first
+// CTA's part_mass: that finds the warp, and the warp the element.
+template <bool BF16>
+__device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& row, int64_t at_row, u64 cut, double inv_t) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    const int lane = row.lane;
+    if (row.rank == 0 && row.warp == 0) {
+        constexpr int N = CL_MAX_CS * CL_WARPS / 32;  // neighbouring parts per lane
+        u64 m[N], sum = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            m[i] = N * lane + i < row.CS * CL_WARPS ? sh.part_mass[N * lane + i] : 0;
+            sum += m[i];
+        }
+        const u64 incl = warp_scan(sum, lane), total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        const u64 target = draw_target(P.uniforms[at_row], total);
+        u64 before = incl - sum;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (before <= target && target < before + m[i]) {
+                row.each_cta([&](CutShared* o) {
+                    o->draw_warp = (uint32_t)(N * lane + i);
+                    o->draw_at = target - before;
+                    o->found_mass = total;
+                });
+            }
+            before += m[i];
+        }
+    }
+    row.sync();
+    if (sh.draw_warp != (uint32_t)(row.rank * CL_WARPS + row.warp)) return;
+    const u64 target = sh.draw_at, total = sh.found_mass;
+    const uint32_t lo16 = R::lo16_of(cut);
+    u64 before = 0;
+    for (int vb = row.v0; vb < row.v1; vb += 32) {
+        const int v = vb + lane;
+        const bool look = v < row.v1 && row.keys[v] >= lo16;
+        if (!__any_sync(0xFFFFFFFFu, look)) continue;
+        u64 mine = 0;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (look) x = row.load(v, R::NOBODY);
+        const auto weight_at = [&](int e) -> u64 {
+            const float z = piece_elem<BF16>(x, e);
+            return look && place_of(key_of<BF16>(z), row.index(v) + e) >= cut ? weight(z, row.s, sh.exp) : 0;
+        };
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) mine += weight_at(e);
+        const u64 incl = warp_scan(mine, lane);
+        u64 at = before + incl - mine;
+        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        if (target >= before) continue;
+        if (at <= target && target < at + mine) {
+#pragma unroll
+            for (int e = 0; e < R::E; ++e) {
+                const u64 w = weight_at(e);
+                if (at <= target && target < at + w) put_token(P, at_row, row.index(v) + e, piece_elem<BF16>(x, e), row.s, inv_t, total);
+                at += w;
+            }
+        }
+        return;
+    }
+}
+
+// 3. Top-p alone. Returns the place of the last kept element and leaves the sums
+// of the warps' parts at or above it in the first CTA's part_mass.
+template <bool BF16>
+__device__ __noinline__ u64 cut_by_mass(const Row<BF16>& row, float top_p, float T, u64 highest) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    const RowScale& s = row.s;
+    const int tid = threadIdx.x;
+    // The last kept element has at least (1 - p) / V of the sum of all weights
+    // (all smaller ones together hold less than 1 - p of it), which is at least 1:
+    // the bins span what can be kept, evenly in log weights.
+    const float span_log = __logf((float)row.V / fmaxf(1.0f - top_p, 1e-9f)) + 0.01f;
+    const float span = span_log * T, to_bin = (float)CL_BINS / span, bin_log = span_log / (float)CL_BINS;
+    clear_bins(row);
+    // all weights, and the histogram: 4096 per element at a bin's upper edge, less
+    // towards its lower one as the weight falls
+    u64 m = 0;
+    row.each_piece(CL_LOWEST, [&](const uint4& x, int) {
+#pragma unroll
+        for (int e = 0; e < R::E; e += 2) {
+            const float z[2] = {piece_elem<BF16>(x, e), piece_elem<BF16>(x, e + 1)};
+            u64 w0, w1;
+            weight_pair(z[0], z[1], s, sh.exp, w0, w1);
+            m += w0 + w1;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float d = __fsub_rn(s.top, z[q]);
+                if (!(d < span)) continue;
+                const float y = __fmul_rn(d, to_bin);
+                const int bin = min((int)y, CL_BINS - 1);
+                atomicAdd(&sh.count[bin], 4096u - (uint32_t)((y - (float)bin) * bin_log * 4096.0f));
+            }
+        }
+    });
+    m = warp_sum(m);
+    if (row.lane == 0) row.of(&sh, 0)->part_mass[row.rank * CL_WARPS + row.warp] = m;
+    row.sync();
+    {
+        const u64* parts = row.of(&sh, 0)->part_mass;
+        u64 t = 0;
+        for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) t += parts[w];
+        m = warp_sum(t);
+    }
+    const double goal = (double)top_p * (double)m;
+    find_bin(row, (float)(goal * (1.0 / (double)(1ull << CL_UNIT))), bin_log * 1.4426950408889634f, 1.0f / 4096.0f);
+    const int bin = (int)sh.found_bin;
+    u64 place = 0;
+    if (sh.found_count < (uint32_t)CL_LIST * 4096u) {
+        // the exact sum above the bin before it, and these three bins to the list
+        const float near_z = __fsub_rn(s.top, (float)(bin + 2) / to_bin * 1.00001f);
+        const u64 lo = max(CL_LOWEST, (u64)key_of<BF16>(near_z - fabsf(near_z) * 1e-6f) << CL_INDEX_BITS);
+        CutShared* head = row.of(&sh, 0);
+        m = 0;
+        uint32_t above = 0;
+        row.each_piece(lo, [&](const uint4& x, int v) {
+            const int i0 = row.index(v);
+#pragma unroll
+            for (int e = 0; e < R::E; e += 2) {
+                const float z[2] = {piece_elem<BF16>(x, e), piece_elem<BF16>(x, e + 1)};
+                bool up[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float d = __fsub_rn(s.top, z[q]);
+                    const int at = d < span ? min((int)__fmul_rn(d, to_bin), CL_BINS - 1) : CL_BINS + 1;
+                    up[q] = at < bin - 1;
+                    if (!up[q] && at <= bin + 1) append(head, place_of(key_of<BF16>(z[q]), i0 + e + q));
+                }
+                above += up[0] + up[1];
+                if (up[0] || up[1]) {
+                    u64 w0, w1;
+                    weight_pair(z[0], z[1], s, sh.exp, w0, w1);
+                    m += (up[0] ? w0 : 0) + (up[1] ? w1 : 0);
+                }
+            }
+        });
+        m = warp_sum(m);
+        above = __reduce_add_sync(0xFFFFFFFFu, above);
+        if (row.lane == 0) {
+            head->part_mass[row.rank * CL_WARPS + row.warp] = m;
+            if (above) atomicAdd(&head->kept, above);
+        }
+        row.sync();
+        if (row.rank == 0) {
+            const int n = (int)sh.list_n;
+            u64 mass_above = 0, place = 0;
+            for (int w = 0; w < row.CS * CL_WARPS; ++w) mass_above += sh.part_mass[w];
+            if (n <= CL_LIST) {
+                sort_list(sh.list, n);
+                place = reach_in_list(row, n, true, sh.kept, mass_above, 0, goal);
+                // what of the list is kept joins its warps' sums
+                if (place) {
+                    const int lead = (int)((reinterpret_cast<uintptr_t>(row.src) & 15) / R::ES);
+                    for (int i = tid; i < n; i += CL_THREADS) {
+                        const u64 p = sh.list[i];
+                        if (p < place) continue;
+                        const int piece = (place_index(p) + lead) / R::E, cta = piece / row.slice, in_cta = piece - cta * row.slice;
+                        atomicAdd(&sh.part_mass[cta * CL_WARPS + in_cta / row.run], weight(key_value<BF16>(place_key(p)), s, sh.exp));
+                    }
+                }
+            }
+            __syncthreads();
+            if (tid == 0) row.each_cta([&](CutShared* o) { o->found_place = place; });
+        }
+        row.sync();
+        place = sh.found_place;
+        row.sync();
+        if (threadIdx.x == 0) sh.list_n = 0;
+    }
+    if (place == 0) {
+        // more equal logits than the list takes, or a border that the histogram missed
+        place = find_cut<BF16, true>(row, CL_LOWEST, highest, 0, goal);
+        sum_above(row, place);
+    }
+    return place;
+}
+
 template <bool BF16, bool DRAW>
 __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_constant__ CutParams P) {
     cluster_arrive_started();
-    cg::cluster_group cluster = cg::this_cluster();
-    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    using R = Row<BF16>;
     extern __shared__ __align__(16) char smem[];
     CutShared& sh = *reinterpret_cast<CutShared*>(smem);
-    uint4* data = reinterpret_cast<uint4*>(smem + sizeof(CutShared));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    using Pt = Part<BF16>;
-    constexpr int ES = BF16 ? 2 : 4;
+    const int tid = threadIdx.x;
+    R row;
+    row.CS = (int)cg::this_cluster().num_blocks();
+    row.rank = (int)cg::this_cluster().block_rank();
+    row.lane = tid & 31;
+    row.warp = tid >> 5;
+    row.sh = &sh;
+    row.keys = reinterpret_cast<uint16_t*>(smem + sizeof(CutShared));
+    row.V = P.V;
+    row.slice = P.slice_vecs;
+    row.run = P.warp_vecs;
+    const int CS = row.CS, rank = row.rank, lane = row.lane, warp = row.warp;
 
-    const int64_t row = blockIdx.x / CS;
-    const int b = (int)(row / P.R), r = (int)(row - (int64_t)b * P.R);
-    const char* src = P.logits + b * P.seq_bytes + r * P.row_bytes;
-    const int lead = (int)(reinterpret_cast<uintptr_t>(src) & 15) / ES;  // elements before the row in its first piece
-    const char* base = src - lead * ES;
-    const int pieces = (lead + P.V + Pt::E - 1) / Pt::E;
-    const int begin = min(rank * P.slice_vecs, pieces), n_vecs = min(P.slice_vecs, pieces - begin);
-    Pt part;
-    part.data = data;
-    part.v0 = min(warp * P.warp_vecs, n_vecs);
-    part.v1 = min(part.v0 + P.warp_vecs, n_vecs);
-    part.first = begin * Pt::E - lead;
-    if (tid == 0) sh.list_n = 0;
+    const int64_t at_row = blockIdx.x / CS;
+    const int b = (int)(at_row / P.R), r = (int)(at_row - (int64_t)b * P.R);
+    row.src = P.logits + b * P.seq_bytes + r * P.row_bytes;
+    const int lead = (int)(reinterpret_cast<uintptr_t>(row.src) & 15) / R::ES;  // elements before the row in its first piece
+    const int pieces = (lead + P.V + R::E - 1) / R::E;
+    const int begin = min(rank * P.slice_vecs, pieces);
+    row.n_vecs = min(P.slice_vecs, pieces - begin);
+    row.v0 = min(warp * P.warp_vecs, row.n_vecs);
+    row.v1 = min(row.v0 + P.warp_vecs, row.n_vecs);
+    row.first = begin * R::E - lead;
+    if (tid == 0) sh.list_n = sh.hits_n = sh.kept = 0;
+    if (tid < CL_EXP) sh.exp[tid] = g_exp_table.e[tid];
+    if (tid < 8) row.keys[(row.n_vecs & ~7) + tid] = 0;  // behind the last key (written below) up to whole 16 bytes
+    __syncthreads();
 
     grid_dependency_wait();
     launch_dependents();
 
-    // 1. This lane's pieces on their way to shared memory; a piece that the row
-    // fills in part goes by elements, with -inf beside them for now.
-    const auto partial = [&](int i0) { return i0 < 0 || i0 + Pt::E > P.V; };
-    for (int v = part.v0 + lane; v < part.v1; v += 32) {
-        const int i0 = part.index(v);
-        if (!partial(i0)) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(data + v)), "l"(base + (int64_t)(begin + v) * 16) : "memory");
-        } else {
+    // 1. The maximum and the pieces' keys.
+    float top = -INFINITY;
+    constexpr int U = 8;
+    for (int v = row.v0 + lane; v < row.v1; v += 32 * U) {
+        uint4 x[U];
 #pragma unroll
-            for (int e = 0; e < Pt::E; ++e) {
-                const bool in = i0 + e >= 0 && i0 + e < P.V;
-                if constexpr (BF16) {
-                    reinterpret_cast<uint16_t*>(data + v)[e] = in ? *reinterpret_cast<const uint16_t*>(src + (int64_t)(i0 + e) * 2) : (uint16_t)0xFF80u;
-                } else {
-                    reinterpret_cast<uint32_t*>(data + v)[e] = in ? *reinterpret_cast<const uint32_t*>(src + (int64_t)(i0 + e) * 4) : 0xFF800000u;
-                }
+        for (int q = 0; q < U; ++q)
+            if (v + 32 * q < row.v1) x[q] = row.load(v + 32 * q, R::MINUS_INF);
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            if (v + 32 * q >= row.v1) continue;
+            float most;
+            if constexpr (BF16) {
+                const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(x[q].x, x[q].y), max_nan_bf16x2(x[q].z, x[q].w));
+                most = max_nan(bf16_lo(m), bf16_hi(m));
+            } else {
+                most = max_nan(max_nan(__uint_as_float(x[q].x), __uint_as_float(x[q].y)), max_nan(__uint_as_float(x[q].z), __uint_as_float(x[q].w)));
             }
+            row.keys[v + 32 * q] = (uint16_t)(key32(most) >> 16);
+            top = max_nan(top, most);
         }
     }
-    if (tid < CL_EXP)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sh.exp[tid])), "l"(&g_exp_table.e[tid]) : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
-
     const float T = P.temperatures ? P.temperatures[b] : P.temperature;
     const int top_k = P.top_ks ? P.top_ks[b] : P.top_k;
     const float top_p = P.top_ps ? P.top_ps[b] : P.top_p, min_p = P.min_ps ? P.min_ps[b] : P.min_p;
@@ -510,76 +928,48 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     const int k = T == 0.0f ? 1 : top_k > 0 && top_k < P.V ? top_k : P.V;
     const double inv_t = T == 0.0f ? 1.0 : 1.0 / (double)T;
 
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    float top = -INFINITY;
-    for (int v = part.v0 + lane; v < part.v1; v += 32) {
-        const uint4 x = data[v];
-        if constexpr (BF16) {
-            const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(x.x, x.y), max_nan_bf16x2(x.z, x.w));
-            top = max_nan(top, max_nan(bf16_lo(m), bf16_hi(m)));
-        } else {
-            top = max_nan(top, max_nan(max_nan(__uint_as_float(x.x), __uint_as_float(x.y)), max_nan(__uint_as_float(x.z), __uint_as_float(x.w))));
-        }
-    }
-    for (int v = part.v0 + lane; v < part.v1; v += 32) {  // padding leaves the order
-        const int i0 = part.index(v);
-        if (!partial(i0)) continue;
-        for (int e = 0; e < Pt::E; ++e) {
-            if (i0 + e >= 0 && i0 + e < P.V) continue;
-            if constexpr (BF16) reinterpret_cast<uint16_t*>(data + v)[e] = 0xFFFFu;
-            else reinterpret_cast<uint32_t*>(data + v)[e] = 0xFFFFFFFFu;
-        }
-    }
-    // groups of 32 or fewer lanes, at least k of them where there are as many lanes
-    const int warps = CS * CL_WARPS;
-    int group = 32;
-    while (group > 1 && warps * (32 / group) < k) group >>= 1;
-    float gmin = top;
-    float wmax = top;
+    float wmax = top, least = top > -INFINITY ? top : INFINITY;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        if (o == group) gmin = wmax;
         wmax = max_nan(wmax, __shfl_xor_sync(0xFFFFFFFFu, wmax, o));
-    }
-    if (group == 32) gmin = wmax;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) gmin = fminf(gmin, __shfl_xor_sync(0xFFFFFFFFu, gmin, o));
-    cluster_wait_started();
-    if (lane < CS) {
-        cluster.map_shared_rank(sh.warp_max, lane)[rank * CL_WARPS + warp] = wmax;
-        cluster.map_shared_rank(sh.group_min, lane)[rank * CL_WARPS + warp] = gmin;
-    }
-    cluster.sync();
-    RowScale s;
-    s.top = -INFINITY;
-    float least = INFINITY;
-    for (int w = lane; w < warps; w += 32) {
-        s.top = max_nan(s.top, sh.warp_max[w]);
-        least = fminf(least, sh.group_min[w]);
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        s.top = max_nan(s.top, __shfl_xor_sync(0xFFFFFFFFu, s.top, o));
         least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
     }
+    cluster_wait_started();
+    if (lane < CS) {
+        row.of(sh.warp_max, lane)[rank * CL_WARPS + warp] = wmax;
+        row.of(sh.lane_min, lane)[rank * CL_WARPS + warp] = least;
+    }
+    row.sync();
+    const int warps = CS * CL_WARPS;
+    row.s.top = -INFINITY;
+    least = INFINITY;
+    for (int w = lane; w < warps; w += 32) {
+        row.s.top = max_nan(row.s.top, sh.warp_max[w]);
+        least = fminf(least, sh.lane_min[w]);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        row.s.top = max_nan(row.s.top, __shfl_xor_sync(0xFFFFFFFFu, row.s.top, o));
+        least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+    }
+    const RowScale& s = row.s;
     const bool row_ok = s.top < INFINITY && s.top > -INFINITY;
-    const int64_t out_row = row;
     u64 cut = CL_LOWEST;  // what is kept lies at or above it
-    uint32_t kept = 0;
     if (!row_ok || !settings_ok) {
         if (rank == 0 && tid == 0) {
             raise_flag(P.status, (row_ok ? 0u : (uint32_t)SV_FLAG_BAD_ROW) | (settings_ok ? 0u : (uint32_t)SV_FLAG_BAD_SETTING));
             if constexpr (DRAW) {
-                P.tokens[out_row] = -1;
-                if (P.logprobs) P.logprobs[out_row] = __int_as_float(0x7fc00000);
+                P.tokens[at_row] = -1;
+                if (P.logprobs) P.logprobs[at_row] = __int_as_float(0x7fc00000);
+            } else {
+                if (P.n_kept) P.n_kept[at_row] = -1;
             }
         }
         if constexpr (DRAW) return;
-        if (!DRAW && rank == 0 && tid == 0 && P.n_kept) P.n_kept[out_row] = -1;
     } else {
         const double c = 1.4426950408889634 * CL_EXP * inv_t;
-        s.ch = (float)c;
-        s.cl = (float)(c - (double)s.ch);
+        row.s.ch = (float)c;
+        row.s.cl = (float)(c - (double)s.ch);
         const u64 highest = (u64)key_of<BF16>(s.top) << CL_INDEX_BITS | CL_INDEX_MASK;
         // min-p: z >= max + T ln(min_p)
         if (min_p > 0.0f && T != 0.0f) {
@@ -589,9 +979,9 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             cut = max(cut, (u64)key << CL_INDEX_BITS);
         }
         const bool by_k = k < P.V, by_p = T != 0.0f && top_p < 1.0f;
-        bool listed = false;   // the first CTA's list holds what may be kept
+        bool summed = false;  // part_mass holds the sums at or above the cut
         if (by_k) {
-            // 3. the list, if it takes everything at or above the bound
+            // 2. a bound on the k-th largest
             u64 bound = CL_LOWEST;
             if (k <= warps) {
                 // the k-th largest of the warps' maxima
@@ -605,151 +995,95 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                     if (before == k - 1) sh.bound = mine;
                 }
                 __syncthreads();
-                least = sh.bound;
+                bound = max(bound, (u64)key_of<BF16>(sh.bound) << CL_INDEX_BITS);
+            } else if (least < s.top) {
+                // that of the pieces', by a histogram between the lanes' smallest
+                // maximum and the row's
+                const float to_bin = (float)(CL_BINS - 1) / __fsub_rn(s.top, least);
+                if (to_bin < INFINITY) {
+                    clear_bins(row);
+                    const uint4* keys = reinterpret_cast<const uint4*>(row.keys);
+                    const uint32_t lo16 = key32(least) >> 16;
+                    for (int g = tid; g * 8 < row.n_vecs; g += CL_THREADS) {
+                        const uint4 k8 = keys[g];
+                        const uint32_t w[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t key = (w[i / 2] >> (16 * (i % 2))) & 0xFFFFu;
+                            if (key < lo16 || g * 8 + i >= row.n_vecs) continue;
+                            const float y = __fmul_rn(__fsub_rn(s.top, from_key32(key << 16 | (BF16 && !(key >> 15) ? 0xFFFFu : 0u))), to_bin);
+                            atomicAdd(&sh.count[max(0, min((int)y, CL_BINS - 1))], 1u);
+                        }
+                    }
+                    find_bin(row, (float)k, 0.0f, 1.0f);
+                    if (sh.found_bin < CL_BINS - 1) {
+                        const float z = __fsub_rn(s.top, (float)(sh.found_bin + 1) / to_bin * 1.0001f);
+                        bound = max(bound, (u64)key_of<BF16>(z - fabsf(z) * 1e-6f) << CL_INDEX_BITS);
+                    }
+                }
             }
-            if (k <= warps * 32) bound = max(bound, (u64)key_of<BF16>(least) << CL_INDEX_BITS);
             // (what min-p drops counts too: it is among the k)
-            const uint32_t n = gather<BF16>(part, sh, bound, highest, lane, cluster);
-            listed = n <= CL_LIST;
+            uint32_t n = gather(row, bound, highest);
+            bool listed = n <= CL_LIST;
             if (!listed) {
-                uint32_t n_k;
-                const u64 cut_k = find_cut<BF16, false>(part, sh, s, bound, highest, (uint32_t)k, 0.0, lane, warp, CS, rank, n_k);
+                row.sync();  // everyone has read the list's length
+                const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0.0);
                 if (k <= CL_LIST) {
-                    if (tid == 0) sh.list_n = 0;  // (every CTA has read it)
-                    cluster.sync();
-                    gather<BF16>(part, sh, cut_k, highest, lane, cluster);
+                    if (tid == 0) sh.list_n = 0;
+                    row.sync();
+                    n = gather(row, cut_k, highest);
                     listed = true;
                 } else {
                     if (by_p) {
-                        u64 mass;
-                        uint32_t n_all;
-                        sum_kept<BF16>(part, sh, s, cut_k, lane, warp, true, cluster, CS, rank, 0, mass, n_all);
-                        uint32_t n_p;
-                        cut = max(cut, find_cut<BF16, true>(part, sh, s, cut_k, highest, 0, (double)top_p * (double)mass, lane, warp, CS, rank, n_p));
+                        const u64 mass = sum_above(row, cut_k);
+                        row.sync();
+                        cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, (double)top_p * (double)mass));
                     }
                     cut = max(cut, cut_k);
                 }
             }
-        } else if (by_p) {
-            u64 mass;
-            uint32_t n_all;
-            sum_kept<BF16>(part, sh, s, CL_LOWEST, lane, warp, true, cluster, CS, rank, 0, mass, n_all);
-            // weights below (1 - p) / V of the sum cannot be among the kept:
-            // all of them together are less than what may be left out
-            const double share = (1.0 - (double)top_p) * (double)mass / ((double)P.V * (double)(1ull << CL_UNIT));
-            const float z = __double2float_rd((double)s.top + (double)(T == 0.0f ? 1.0f : T) * (log(share) * 1.000001 - 0.001));
-            const u64 lo = max(CL_LOWEST, (u64)key_of<BF16>(z) << CL_INDEX_BITS);
-            uint32_t n_p;
-            cut = max(cut, find_cut<BF16, true>(part, sh, s, min(lo, highest), highest, 0, (double)top_p * (double)mass, lane, warp, CS, rank, n_p));
-        }
-        if (listed) {
-            // The cuts, in the list: an element's rank and the weights before it.
-            cluster.sync();  // every CTA has read the list's length
-            if (rank == 0) {
-                const int n = (int)min(sh.list_n, (uint32_t)CL_LIST);
-                for (int i = tid; i < n; i += CL_THREADS) sh.list_w[i] = weight(key_value<BF16>(place_key(sh.mass[i])), s, sh.exp);
-                __syncthreads();
-                uint32_t before[CL_LIST / CL_THREADS];
-                u64 mass_before[CL_LIST / CL_THREADS];
-                u64 of_k = 0;
-#pragma unroll
-                for (int q = 0; q < CL_LIST / CL_THREADS; ++q) {
-                    const int i = tid + q * CL_THREADS;
-                    before[q] = 0;
-                    mass_before[q] = 0;
-                    if (i >= n) continue;
-                    const u64 mine = sh.mass[i];
-                    for (int j = 0; j < n; ++j) {
-                        if (sh.mass[j] > mine) {
-                            ++before[q];
-                            mass_before[q] += sh.list_w[j];
-                        }
+            if (listed) {
+                // The cuts, in the list.
+                row.sync();  // everyone has read its length
+                if (rank == 0) {
+                    const int all = min((int)n, CL_LIST);
+                    sort_list(sh.list, all);
+                    const int of_k = min(all, k);
+                    u64 last = of_k > 0 ? sh.list[of_k - 1] : 0;
+                    if (by_p) {
+                        u64 m = 0, total;
+                        for (int i = tid; i < of_k; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), s, sh.exp);
+                        block_scan(m, sh.warp_mass, lane, warp, total);
+                        last = max(last, reach_in_list(row, of_k, true, 0, 0, 0, (double)top_p * (double)total));
                     }
-                    if (before[q] < (uint32_t)k) of_k += sh.list_w[i];
-                }
-                of_k = block_sum(of_k, sh, lane, warp);
-                const double goal = (double)top_p * (double)of_k;
-                u64 lowest = ~0ull;
-                bool keep[CL_LIST / CL_THREADS];
-#pragma unroll
-                for (int q = 0; q < CL_LIST / CL_THREADS; ++q) {
-                    const int i = tid + q * CL_THREADS;
-                    keep[q] = i < n && before[q] < (uint32_t)k && sh.mass[i] >= cut &&
-                              (!by_p || before[q] == 0 || (double)mass_before[q] < goal);
-                    if (keep[q]) lowest = min(lowest, sh.mass[i]);
-                }
-                // the last kept place
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) lowest = min(lowest, __shfl_xor_sync(0xFFFFFFFFu, lowest, o));
-                __syncthreads();
-                if (lane == 0) sh.warp_mass[warp] = lowest;
-                __syncthreads();
-                for (int w = 0; w < CL_WARPS; ++w) lowest = min(lowest, sh.warp_mass[w]);
-                if constexpr (DRAW) {
-                    u64 total = 0;
-#pragma unroll
-                    for (int q = 0; q < CL_LIST / CL_THREADS; ++q)
-                        if (keep[q]) total += sh.list_w[tid + q * CL_THREADS];
-                    total = block_sum(total, sh, lane, warp);
-                    const u64 target = draw_target(P.uniforms[out_row], total);
-#pragma unroll
-                    for (int q = 0; q < CL_LIST / CL_THREADS; ++q) {
-                        if (!keep[q]) continue;
-                        const int i = tid + q * CL_THREADS;
-                        const u64 mine = sh.mass[i];
-                        const int index = place_index(mine);
-                        u64 m = 0;
-                        for (int j = 0; j < n; ++j)
-                            if (sh.mass[j] >= lowest && place_index(sh.mass[j]) < index) m += sh.list_w[j];
-                        if (m <= target && target < m + sh.list_w[i])
-                            put_token(P, out_row, index, key_value<BF16>(place_key(mine)), s, inv_t, total);
+                    last = max(last, cut);
+                    if constexpr (DRAW) {
+                        // how many of the sorted places are kept
+                        int kept = 0;
+                        for (int i = tid; i < of_k; i += CL_THREADS) kept += sh.list[i] >= last;
+                        uint32_t total;
+                        block_scan((uint32_t)kept, sh.warp_count, lane, warp, total);
+                        draw_list(P, row, at_row, (int)total, inv_t);
+                    } else {
+                        __syncthreads();
+                        if (tid == 0) row.each_cta([&](CutShared* o) { o->found_place = last; });
                     }
-                } else if (tid < CS) {
-                    *cluster.map_shared_rank(&sh.found_place, tid) = lowest;
                 }
+                if constexpr (DRAW) return;
+                row.sync();
+                cut = sh.found_place;
             }
-            if constexpr (DRAW) return;
-            cluster.sync();
-            cut = sh.found_place;
+        } else if (by_p) {
+            const u64 cut_p = cut_by_mass(row, top_p, T, highest);
+            summed = cut_p >= cut;
+            cut = max(cut, cut_p);
         }
         if constexpr (DRAW) {
-            // 5. the draw over the parts: their sums, then the warps', then the elements
-            u64 total;
-            uint32_t n_all;
-            sum_kept<BF16>(part, sh, s, cut, lane, warp, true, cluster, CS, rank, 1, total, n_all);
-            u64 target = draw_target(P.uniforms[out_row], total);
-            u64 before = 0;
-            for (int c2 = 0; c2 < rank; ++c2) before += sh.cta_mass[1][c2];
-            if (before > target || target >= before + sh.cta_mass[1][rank]) return;
-            for (int w = 0; w < warp; ++w) before += sh.warp_mass[w];
-            if (before > target || target >= before + sh.warp_mass[warp]) return;
-            const uint32_t cut_key = place_key(cut);
-            for (int v0 = part.v0; v0 < part.v1; v0 += 32) {
-                const int v = v0 + lane;
-                u64 w_of[Pt::E], mine = 0;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (v < part.v1) x = data[v];
-#pragma unroll
-                for (int e = 0; e < Pt::E; ++e) {
-                    const float z = piece_elem<BF16>(x, e);
-                    const uint32_t key = key_of<BF16>(z);
-                    const bool in = v < part.v1 && (key > cut_key || (key == cut_key && place_of(key, part.index(v) + e) >= cut));
-                    w_of[e] = in ? weight(z, s, sh.exp) : 0;
-                    mine += w_of[e];
-                }
-                const u64 incl = warp_scan(mine, lane);
-                u64 at = before + incl - mine;
-                before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-                if (target >= before) continue;
-                if (at <= target && target < at + mine) {
-#pragma unroll
-                    for (int e = 0; e < Pt::E; ++e) {
-                        if (at <= target && target < at + w_of[e]) put_token(P, out_row, part.index(v) + e, piece_elem<BF16>(x, e), s, inv_t, total);
-                        at += w_of[e];
-                    }
-                }
-                return;
+            if (!summed) {
+                row.sync();
+                sum_above(row, cut);
             }
+            draw_parts(P, row, at_row, cut, inv_t);
             return;
         }
     }
@@ -757,36 +1091,34 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         // 5. the row's output
         const bool valid = row_ok && settings_ok;
         char* out = P.out + b * P.out_seq_bytes + r * P.out_row_bytes;
-        const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (uintptr_t)(lead * ES);
-        const uint32_t cut_key = valid ? place_key(cut) : 1u;
-        if (!valid) cut = CL_LOWEST;
-        for (int v = part.v0 + lane; v < part.v1; v += 32) {
-            uint4 x = data[v];
-            const int i0 = part.index(v);
-            uint32_t keep = 0;
+        const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (uintptr_t)(lead * R::ES);
+        const uint32_t lo16 = valid ? R::lo16_of(cut) : 0;
+        constexpr uint32_t NONE = BF16 ? 0xFF80FF80u : 0xFF800000u;
+        uint32_t kept = 0;
+        for (int v = row.v0 + lane; v < row.v1; v += 32) {
+            const int i0 = row.index(v);
+            uint4 x = make_uint4(NONE, NONE, NONE, NONE);
+            if (!valid || row.keys[v] >= lo16) {
+                x = row.load(v, R::NOBODY);
+                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+                if (valid) {
 #pragma unroll
-            for (int e = 0; e < Pt::E; ++e) {
-                const uint32_t key = key_of<BF16>(piece_elem<BF16>(x, e));
-                if (!valid || key > cut_key || (key == cut_key && place_of(key, i0 + e) >= cut)) keep |= 1u << e;
+                    for (int e = 0; e < R::E; ++e) {
+                        if (place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e) >= cut) {
+                            ++kept;
+                        } else {
+                            if constexpr (BF16) w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | 0xFF800000u : (w[e / 2] & 0xFFFF0000u) | 0xFF80u;
+                            else w[e] = 0xFF800000u;
+                        }
+                    }
+                }
             }
-            const bool whole = !partial(i0);
-            if (!whole) {  // padding is nobody's
-                for (int e = 0; e < Pt::E; ++e)
-                    if (i0 + e < 0 || i0 + e >= P.V) keep &= ~(1u << e);
-            }
-            kept += __popc(keep);
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-            for (int e = 0; e < Pt::E; ++e) {
-                if (keep >> e & 1u) continue;
-                if constexpr (BF16) w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | 0xFF800000u : (w[e / 2] & 0xFFFF0000u) | 0xFF80u;
-                else w[e] = 0xFF800000u;
-            }
-            if (whole && same) {
-                *reinterpret_cast<uint4*>(out + (int64_t)i0 * ES) = x;
+            if (same && !row.partial(v)) {
+                *reinterpret_cast<uint4*>(out + (int64_t)i0 * R::ES) = x;
             } else {
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < Pt::E; ++e) {
+                for (int e = 0; e < R::E; ++e) {
                     if (i0 + e < 0 || i0 + e >= P.V) continue;
                     if constexpr (BF16) reinterpret_cast<uint16_t*>(out)[i0 + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
                     else reinterpret_cast<uint32_t*>(out)[i0 + e] = w[e];
@@ -795,20 +1127,17 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         }
         if (P.n_kept && valid) {
             kept = __reduce_add_sync(0xFFFFFFFFu, kept);
-            __syncthreads();
-            if (lane == 0) sh.warp_count[warp] = kept;
-            __syncthreads();
-            if (tid == 0) {
-                uint32_t n = 0;
-                for (int w = 0; w < CL_WARPS; ++w) n += sh.warp_count[w];
-                *cluster.map_shared_rank(&sh.cta_count[1][rank], 0) = n;
+            row.sync();
+            if (lane == 0) row.of(&sh, 0)->part_mass[rank * CL_WARPS + warp] = kept;
+            row.sync();
+            if (rank == 0 && warp == 0) {
+                u64 n = 0;
+                for (int w = lane; w < warps; w += 32) n += sh.part_mass[w];
+                n = warp_sum(n);
+                if (lane == 0) P.n_kept[at_row] = (int32_t)n;
             }
-            cluster.sync();
-            if (rank == 0 && tid == 0) {
-                uint32_t n = 0;
-                for (int c = 0; c < CS; ++c) n += sh.cta_count[1][c];
-                P.n_kept[out_row] = (int32_t)n;
-            }
+        } else {
+            row.sync();  // no CTA ends while another may look into its memory
         }
     }
 }
@@ -816,9 +1145,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // Launch.
 // ---------------------------------------------------------------------------
-// Shared memory per CTA up to which two are resident per SM.
-constexpr int CL_TWO = 112 * 1024;
-constexpr int CL_ONE = 226 * 1024;
+constexpr int CL_ONE = 226 * 1024;  // shared memory of a CTA at most
 
 template <bool BF16, bool DRAW>
 static cudaError_t launch(CutParams p, int sms, cudaStream_t stream) {
@@ -836,14 +1163,13 @@ static cudaError_t launch(CutParams p, int sms, cudaStream_t stream) {
     constexpr int E = BF16 ? 8 : 4;
     const int64_t rows = (int64_t)p.B * p.R;
     const int vecs = (p.V + E - 1) / E + 1;  // (a row may begin inside a piece)
-    const auto smem_of = [&](int cs) { return (int)sizeof(CutShared) + (vecs + cs - 1) / cs * 16; };
+    // Few rows are spread over as many CTAs as two per SM are, down to 4 pieces
+    // per thread.
     int cs = 1;
-    while (cs < CL_MAX_CS && smem_of(cs) > CL_TWO) cs *= 2;
-    // few rows are spread over more SMs, down to 4 pieces per thread
-    while (cs < CL_MAX_CS && rows * cs * 2 <= sms && vecs / cs > 4 * CL_THREADS) cs *= 2;
+    while (cs < CL_MAX_CS && rows * cs <= sms && vecs / cs > 4 * CL_THREADS) cs *= 2;
     p.slice_vecs = (vecs + cs - 1) / cs;
     p.warp_vecs = (p.slice_vecs + CL_WARPS - 1) / CL_WARPS;
-    const int smem = smem_of(cs);
+    const int smem = (int)sizeof(CutShared) + (p.slice_vecs + 15) / 8 * 16;
     if (smem > CL_ONE || rows * cs > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
