@@ -37,6 +37,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cstddef>
 
 #include "cut.h"
 #include "paged_device.cuh"
@@ -52,6 +53,7 @@ constexpr int CL_WARPS = CL_THREADS / 32;
 constexpr int CL_MAX_CS = 8;
 constexpr int CL_BINS = 2048;
 constexpr int CL_LIST = 2048;
+constexpr uint32_t CL_NEAR = 150;  // elements on either side of where a histogram finds a border
 constexpr int CL_HITS = 2048;  // pieces of one CTA that gather() reads in one step
 constexpr int CL_ROUNDS = 5;   // of 11 bits each; a place has 50
 constexpr int CL_INDEX_BITS = 18;
@@ -61,12 +63,11 @@ constexpr int CL_EXP = 1 << CL_EXP_BITS;  // entries of the table of 2^(i / 256)
 constexpr int CL_UNIT = 44;               // weights are in units of 2^-44
 static_assert((1 << CL_INDEX_BITS) == CUT_MAX_V, "an index per place");
 
-// 2^(i / 256), in weight units and as a float in units of 2^-39.
-struct alignas(16) ExpEntry {
-    u64 q;
-    float f;
-    float unused;
+// 2^(i / 256) as the sum of two floats.
+struct alignas(8) ExpEntry {
+    float hi, lo;
 };
+constexpr int CL_COPIES = 4;  // of the table, side by side, for whole rows: lane l reads copy l % 4
 struct ExpTable {
     ExpEntry e[CL_EXP];
 };
@@ -82,9 +83,8 @@ constexpr ExpTable make_exp_table() {
     ExpTable t = {};
     for (int i = 0; i < CL_EXP; ++i) {
         const double v = exp_series(0.69314718055994530942 * i / CL_EXP);
-        t.e[i].q = (u64)(v * (double)(1ull << CL_UNIT) + 0.5);
-        t.e[i].f = (float)(v * (double)(1ull << 39));
-        t.e[i].unused = 0.0f;
+        t.e[i].hi = (float)v;
+        t.e[i].lo = (float)(v - (double)(float)v);
     }
     return t;
 }
@@ -93,6 +93,7 @@ __device__ const ExpTable g_exp_table = make_exp_table();
 struct RowScale {
     float top;       // the row's maximum
     float ch, cl;    // 256 log2(e) / T in two floats
+    float low;       // a logit of weight 2^-100; NaN where the row's maximum has no room for one
 };
 
 // Order of floats as unsigned integers; -0 counts as 0.
@@ -119,20 +120,12 @@ __device__ __forceinline__ uint32_t place_key(u64 p) { return (uint32_t)(p >> CL
 constexpr float CL_L1 = 2.7076061740622863e-3f;  // ln 2 / 256
 constexpr float CL_L2 = 3.6655655969053526e-6f;  // its square / 2
 constexpr float CL_L3 = 3.3083027270131e-9f;     // its cube / 6
-// 2^(n / 256) (1 + e), n as the low bits of a float that 1.5 * 2^23 was added to.
-__device__ __forceinline__ u64 weight_of(uint32_t t_bits, float e, const ExpEntry* table) {
-    const ExpEntry en = table[t_bits & (CL_EXP - 1)];  // (the magic number's low bits are 0)
-    const int tail = __float2int_rn(__fmul_rn(en.f, e));  // below 2^30.5
-    const u64 q = en.q + (u64)((long long)tail * 32);
-    const uint32_t sh = (0x4B400000u + CL_EXP - 1 - t_bits) >> CL_EXP_BITS;  // ceil(-n / 256)
-    const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
-    return __uint_as_float(t_bits) > 12582912.0f - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
-}
 
 // exp((z - top) / T) in units of 2^-44. With d = z - top in two floats, exactly,
 // y = 256 d log2(e) / T = n + x, n whole and |x| <= 1/2: 2^(n / 256) comes from the
 // table and a shift, and 2^(x / 256) - 1, below 2^-9, from three terms of its
-// series. x is off by 2^-26 and the series by 2^-24 of itself: 2^-33 of w.
+// series. x is off by 2^-26 and the series by 2^-24 of itself: 2^-33 of w. The
+// weight of the maximum is 2^44 exactly.
 __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry* table) {
     const float dh = __fsub_rn(z, s.top);
     const float bb = __fsub_rn(dh, z);
@@ -142,31 +135,59 @@ __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry
     const float n = __fsub_rn(t, MAGIC);
     const float x = __fadd_rn(__fmaf_rn(dh, s.ch, -n), __fmaf_rn(dh, s.cl, __fmul_rn(dl, s.ch)));
     const float e = __fmul_rn(x, __fmaf_rn(x, __fmaf_rn(x, CL_L3, CL_L2), CL_L1));
-    return weight_of(__float_as_uint(t), e, table);
+    const uint32_t tb = __float_as_uint(t);
+    const ExpEntry en = table[tb & (CL_EXP - 1)];  // (the magic number's low bits are 0)
+    const int tail = __float2int_rn(__fmul_rn(__fmaf_rn(en.hi, e, en.lo), 0x1p39f));  // below 2^31
+    const u64 q = ((u64)((__float_as_uint(en.hi) & 0x7FFFFFu) | 0x800000u) << (CL_UNIT - 23)) + (u64)((long long)tail * 32);
+    const uint32_t sh = (0x4B400000u + CL_EXP - 1 - tb) >> CL_EXP_BITS;  // ceil(-n / 256)
+    const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
+    return t > MAGIC - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
 }
 
-
-// Two of them at once: the same arithmetic, the exponents' part in packed
-// instructions.
-__device__ __forceinline__ void weight_pair(float z0, float z1, const RowScale& s, const ExpEntry* table, u64& w0, u64& w1) {
-    const f32x2 z = pack2(z0, z1), top = pack2(s.top, s.top), minus = pack2(-1.0f, -1.0f), ch = pack2(s.ch, s.ch), cl = pack2(s.cl, s.cl);
-    const f32x2 magic = pack2(12582912.0f, 12582912.0f);
-    const f32x2 dh = fma2(top, minus, z);
-    const f32x2 bb = fma2(z, minus, dh);
-    const f32x2 dl = fma2(add2(top, bb), minus, fma2(fma2(bb, minus, dh), minus, z));
-    const f32x2 t = fma2(dh, ch, magic);
-    const f32x2 x = add2(fma2(dh, ch, fma2(t, minus, magic)), fma2(dh, cl, mul2(dl, ch)));
-    const f32x2 e = mul2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1)));
-    float t0, t1, e0, e1;
-    unpack2(t, t0, t1);
-    unpack2(e, e0, e1);
-    w0 = weight_of(__float_as_uint(t0), e0, table);
-    w1 = weight_of(__float_as_uint(t1), e1, table);
-}
+// Adds up weights in floats, two elements at a time in packed instructions, for
+// the passes over whole rows (the integers' shifts cost twice as much: 57
+// instructions per element against 27). w = (hi + (lo + hi e)) 2^-k; the sum s of
+// the first parts begins at 1, so that s >= any of them and (s' - s) - a is the
+// rounding error of s' = s + a exactly; c takes those and the second parts. s + c
+// is right to 2^-34 of the sum or so, beside the weights' own error.
+struct WeightSum {
+    f32x2 s, c;
+    __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)) {}
+    // z0, z1 >= r.low
+    __device__ __forceinline__ void add(float z0, float z1, const RowScale& r, const ExpEntry* table) {
+        const f32x2 z = pack2(z0, z1), top = pack2(r.top, r.top), minus = pack2(-1.0f, -1.0f), ch = pack2(r.ch, r.ch), cl = pack2(r.cl, r.cl);
+        const f32x2 magic = pack2(12582912.0f, 12582912.0f);
+        const f32x2 dh = fma2(top, minus, z);
+        const f32x2 bb = fma2(z, minus, dh);
+        const f32x2 dl = fma2(add2(top, bb), minus, fma2(fma2(bb, minus, dh), minus, z));
+        const f32x2 t = fma2(dh, ch, magic);
+        const f32x2 x = add2(fma2(dh, ch, fma2(t, minus, magic)), fma2(dh, cl, mul2(dl, ch)));
+        const f32x2 e = mul2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1)));
+        float t0, t1;
+        unpack2(t, t0, t1);
+        const uint32_t b0 = __float_as_uint(t0), b1 = __float_as_uint(t1);
+        const ExpEntry p = table[(b0 & (CL_EXP - 1)) * CL_COPIES], q = table[(b1 & (CL_EXP - 1)) * CL_COPIES];
+        // 2^floor(n / 256): the magic number's upper bits leave the word
+        const auto scale = [](uint32_t b) { return __uint_as_float((b & ~(uint32_t)(CL_EXP - 1)) * (1u << (23 - CL_EXP_BITS)) + 0x3F800000u); };
+        const f32x2 pow = pack2(scale(b0), scale(b1)), hi = pack2(p.hi, q.hi);
+        const f32x2 a = mul2(hi, pow), rest = mul2(fma2(hi, e, pack2(p.lo, q.lo)), pow);
+        const f32x2 sum = add2(s, a);
+        c = add2(c, add2(fma2(fma2(s, minus, sum), minus, a), rest));
+        s = sum;
+    }
+    __device__ __forceinline__ u64 total() const {
+        float s0, s1, c0, c1;
+        unpack2(s, s0, s1);
+        unpack2(c, c0, c1);
+        const double v = ((double)s0 - 1.0) + ((double)s1 - 1.0) + ((double)c0 + (double)c1);
+        return v > 0.0 ? (u64)__double2ll_rn(v * (double)(1ull << CL_UNIT)) : 0ull;
+    }
+};
 
 // What one row's cluster shares; every CTA has its own copy.
-struct CutShared {
+struct alignas(16) CutShared {
     ExpEntry exp[CL_EXP];
+    ExpEntry copies[CL_EXP * CL_COPIES];  // of it, where a row's weights are summed
     u64 list[CL_LIST];               // the first CTA's: places, sorted later; or the exact histogram's weights
     union {
         uint32_t count[CL_BINS];     // histogram
@@ -183,10 +204,16 @@ struct CutShared {
     uint32_t seg_count[CL_MAX_CS];
     // what a search has found, told to every CTA
     u64 found_mass, found_place, draw_at;
-    uint32_t found_bin, found_above, found_count, draw_warp;
-    uint32_t list_n, hits_n, kept;
+    uint32_t found_bin, found_from, found_to, found_above, found_count, draw_warp;
+    uint32_t list_n, hits_n;
     float bound;
+    int first, firsts[CL_MAX_CS];
+    // of the row's settings (formed by one thread: the units for doubles are few)
+    double inv_t;
+    float ch, cl, low_by, min_hi, min_lo;
 };
+// (read and cleared 16 bytes at a time, like the pieces' keys behind the struct)
+static_assert(sizeof(CutShared) % 16 == 0 && offsetof(CutShared, list) % 16 == 0 && offsetof(CutShared, count) % 16 == 0, "alignment");
 
 template <bool BF16>
 __device__ __forceinline__ float piece_elem(const uint4& x, int e) {
@@ -209,6 +236,22 @@ __device__ __forceinline__ N warp_scan(N v, int lane) {
     return v;
 }
 
+// A piece that the row src[0..V) fills in part, from index i0 on, `pad` (an
+// element's bits) beside it.
+template <bool BF16>
+__device__ __noinline__ uint4 load_part(const char* src, int V, int i0, uint32_t pad) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < (BF16 ? 8 : 4); ++e) {
+        uint32_t b = pad;
+        if (i0 + e >= 0 && i0 + e < V)
+            b = BF16 ? *reinterpret_cast<const uint16_t*>(src + (int64_t)(i0 + e) * 2) : *reinterpret_cast<const uint32_t*>(src + (int64_t)(i0 + e) * 4);
+        if (BF16) w[e / 2] |= b << (16 * (e % 2));
+        else w[e] = b;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // One CTA's part of a row, in 16-byte pieces of which a warp has a run; lane l
 // has its pieces l, l + 32, ...
 template <bool BF16>
@@ -224,30 +267,20 @@ struct Row {
     RowScale s;
     int CS, rank, lane, warp;
 
+    const uint4* base;     // the part's pieces in memory
+    int full0, full1;      // those that lie in the row as a whole
+
     __device__ __forceinline__ int index(int v) const { return first + v * E; }
-    __device__ __forceinline__ bool partial(int v) const { return index(v) < 0 || index(v) + E > V; }
-    // A piece; where the row fills it in part, `pad` (an element's bits) beside it.
-    __device__ __forceinline__ uint4 load(int v, uint32_t pad) const {
-        const int i0 = index(v);
+    __device__ __forceinline__ bool partial(int v) const { return v < full0 || v >= full1; }
+    __device__ __forceinline__ uint4 load_whole(int v) const {
         uint4 x;
-        if (!partial(v)) {
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                         : "l"(src + (int64_t)i0 * ES)
-                         : "memory");
-            return x;
-        }
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            uint32_t b = pad;
-            if (i0 + e >= 0 && i0 + e < V)
-                b = BF16 ? *reinterpret_cast<const uint16_t*>(src + (int64_t)(i0 + e) * 2) : *reinterpret_cast<const uint32_t*>(src + (int64_t)(i0 + e) * 4);
-            if (BF16) w[e / 2] |= b << (16 * (e % 2));
-            else w[e] = b;
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "l"(base + v)
+                     : "memory");
+        return x;
     }
+    __device__ __forceinline__ uint4 load(int v) const { return partial(v) ? load_part<BF16>(src, V, index(v), NOBODY) : load_whole(v); }
     // padding that has no place in the order (a negative NaN, key 0)
     static constexpr uint32_t NOBODY = BF16 ? 0xFFFFu : 0xFFFFFFFFu;
     static constexpr uint32_t MINUS_INF = BF16 ? 0xFF80u : 0xFF800000u;
@@ -256,6 +289,13 @@ struct Row {
     __device__ __forceinline__ void sync() const {
         if (CS == 1) __syncthreads();
         else cg::this_cluster().sync();
+    }
+    // The same in two halves: what comes between does not wait for the others.
+    __device__ __forceinline__ void arrive() const {
+        if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
+    __device__ __forceinline__ void wait() const {
+        if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     template <class X>
     __device__ __forceinline__ X* of(X* mine, int cta) const { return CS == 1 ? mine : cg::this_cluster().map_shared_rank(mine, cta); }
@@ -276,17 +316,36 @@ struct Row {
         };
         v = next(v);
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (v < v1) x = load(v, NOBODY);
+        if (v < v1) x = load(v);
         while (v < v1) {
             const int n = next(v + 32);
             uint4 y = x;
-            if (n < v1) y = load(n, NOBODY);
+            if (n < v1) y = load(n);
             f(x, v);
             x = y;
             v = n;
         }
     }
-    static __device__ __forceinline__ uint32_t lo16_of(u64 place) { return BF16 ? place_key(place) : place_key(place) >> 16; }
+    // What a piece's key is compared with. (The pieces' keys are of the bits as they
+    // are: -0 has the one below that of 0.)
+    static __device__ __forceinline__ uint32_t lo16_of(u64 place) {
+        const uint32_t k = BF16 ? place_key(place) : place_key(place) >> 16;
+        return k == 0x8000u ? 0x7FFFu : k;
+    }
+    // The key of a piece, and its maximum taken into `most` (of two halves in bf16).
+    static __device__ __forceinline__ uint16_t piece_key(const uint4& x, uint32_t& most) {
+        uint32_t m, b;
+        if constexpr (BF16) {
+            m = max_nan_bf16x2(max_nan_bf16x2(x.x, x.y), max_nan_bf16x2(x.z, x.w));
+            most = max_nan_bf16x2(most, m);
+            b = max_nan_bf16x2(m, m >> 16) << 16;
+        } else {
+            m = __float_as_uint(max_nan(max_nan(__uint_as_float(x.x), __uint_as_float(x.y)), max_nan(__uint_as_float(x.z), __uint_as_float(x.w))));
+            most = __float_as_uint(max_nan(__uint_as_float(most), __uint_as_float(m)));
+            b = m;
+        }
+        return (uint16_t)((b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) >> 16);
+    }
 };
 
 // Appends to the first CTA's list; what does not fit is counted only.
@@ -295,23 +354,12 @@ __device__ __forceinline__ void append(CutShared* head, u64 place) {
     if (at < CL_LIST) head->list[at] = place;
 }
 
-// The places in [lo, hi] of all parts, to the list: the CTA collects its pieces
-// that hold some, then its threads read one each. Returns how many there are.
-template <bool BF16>
-__device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi) {
-    using R = Row<BF16>;
+// f(piece) for this CTA's pieces that hold places from `lo` on: it collects them,
+// then its threads take one each.
+template <bool BF16, class F>
+__device__ __forceinline__ void each_hit(const Row<BF16>& row, u64 lo, F&& f) {
     CutShared& sh = *row.sh;
-    CutShared* head = row.of(&sh, 0);
-    const uint32_t lo16 = R::lo16_of(lo);
-    const auto look = [&](int v) {
-        const uint4 x = row.load(v, R::NOBODY);
-        const int i0 = row.index(v);
-#pragma unroll
-        for (int e = 0; e < R::E; ++e) {
-            const u64 p = place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e);
-            if (p >= lo && p <= hi) append(head, p);
-        }
-    };
+    const uint32_t lo16 = Row<BF16>::lo16_of(lo);
     // 8 keys at a time; the keys behind the part's last are 0
     const uint4* keys = reinterpret_cast<const uint4*>(row.keys);
     for (int g = threadIdx.x; g * 8 < row.n_vecs; g += CL_THREADS) {
@@ -328,15 +376,53 @@ __device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi)
     }
     __syncthreads();
     if (sh.hits_n <= CL_HITS) {
-        for (int i = threadIdx.x; i < (int)sh.hits_n; i += CL_THREADS) look((int)sh.hits[i]);
+        for (int i = threadIdx.x; i < (int)sh.hits_n; i += CL_THREADS) f((int)sh.hits[i]);
     } else {
         for (int v = row.v0 + row.lane; v < row.v1; v += 32)
-            if (row.keys[v] >= lo16) look(v);
+            if (row.keys[v] >= lo16) f(v);
     }
+}
+
+// The places in [lo, hi] of all parts, to the list. Returns how many there are.
+template <bool BF16>
+__device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    CutShared* head = row.of(&sh, 0);
+    each_hit(row, lo, [&](int v) {
+        const uint4 x = row.load(v);
+        const int i0 = row.index(v);
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            const u64 p = place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e);
+            if (p >= lo && p <= hi) append(head, p);
+        }
+    });
     row.sync();
     const uint32_t n = head->list_n;
     if (threadIdx.x == 0) sh.hits_n = 0;
     return n;
+}
+
+// The first index of the row's largest element, whose key is lo's.
+template <bool BF16>
+__device__ __forceinline__ int first_largest(const Row<BF16>& row, u64 lo) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    each_hit(row, lo, [&](int v) {
+        const uint4 x = row.load(v);
+        int first = INT32_MAX;
+#pragma unroll
+        for (int e = R::E - 1; e >= 0; --e)
+            if (key_of<BF16>(piece_elem<BF16>(x, e)) == place_key(lo)) first = row.index(v) + e;
+        atomicMin(&sh.first, first);
+    });
+    __syncthreads();
+    if (threadIdx.x < row.CS) row.of(sh.firsts, threadIdx.x)[row.rank] = sh.first;
+    row.sync();
+    int first = INT32_MAX;
+    for (int c = 0; c < row.CS; ++c) first = min(first, sh.firsts[c]);
+    return first;
 }
 
 // Sorts the first n entries of the list, descending, by this CTA: few by counting
@@ -398,30 +484,37 @@ __device__ __forceinline__ N block_scan(N v, N* warp_sums, int lane, int warp, N
 }
 
 // The first bin, from 0 on, in which the sum over the bins of all CTAs reaches
-// `goal`, told to every CTA as found_bin (the last one if none does). A bin's value
-// is its count, or count / 4096 times 2^(-decay * bin). found_count: the count
-// of it and its two neighbours.
+// `goal` (the last one if none does), told to every CTA as found_bin. A bin's value
+// is its count, or with `decay` count / CL_SHARE times 2^(-decay * bin). With `near`
+// also the bins around it, found_from to found_to, that hold up to `near` elements
+// on either side and one bin at least.
+constexpr uint32_t CL_SHARE = 8192;  // counts per element where bins hold weights
 template <bool BF16>
-__device__ __forceinline__ void find_bin(const Row<BF16>& row, float goal, float decay, float unit) {
+__device__ __forceinline__ void find_bin(const Row<BF16>& row, float goal, float decay, uint32_t near) {
     CutShared& sh = *row.sh;
     row.sync();
     if (row.rank == 0) {
         static_assert(CL_BINS == 4 * CL_THREADS, "four bins per thread");
         const int tid = threadIdx.x;
-        if (tid == 0) sh.found_bin = CL_BINS - 1;
+        if (tid == 0) {
+            sh.found_bin = sh.found_from = CL_BINS - 1;
+            sh.found_to = 0;
+        }
         uint32_t n[4] = {0, 0, 0, 0};
         for (int c = 0; c < row.CS; ++c) {
             const uint4 k = reinterpret_cast<const uint4*>(row.of(&sh, c)->count)[tid];
             n[0] += k.x, n[1] += k.y, n[2] += k.z, n[3] += k.w;
         }
-        if (row.CS > 1) reinterpret_cast<uint4*>(sh.list)[tid] = make_uint4(n[0], n[1], n[2], n[3]);
+        const float unit = decay == 0.0f ? 1.0f : 1.0f / (float)CL_SHARE;
         float v[4], sum = 0.0f, total;
+        uint32_t number = 0, all;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = (float)n[i] * unit * (decay == 0.0f ? 1.0f : ex2(-decay * (float)(4 * tid + i)));
             sum += v[i];
+            number += n[i];
         }
-        float before = block_scan(sum, sh.warp_value, row.lane, row.warp, total) - sum;
+        const float before = block_scan(sum, sh.warp_value, row.lane, row.warp, total) - sum;
         if (before < goal && before + sum >= goal) {
             int b = 4 * tid + 3;
 #pragma unroll
@@ -432,14 +525,32 @@ __device__ __forceinline__ void find_bin(const Row<BF16>& row, float goal, float
             }
             atomicMin(&sh.found_bin, (uint32_t)b);  // (sums of floats need not ascend to the last bit)
         }
+        if (near) {
+            const uint32_t upto = block_scan(number, sh.warp_count, row.lane, row.warp, all);
+            const uint32_t bin = sh.found_bin;
+            if ((bin >> 2) == (uint32_t)tid) {
+                uint32_t c = upto - number;
+                for (uint32_t i = 0; i < (bin & 3); ++i) c += n[i];
+                sh.found_above = c;  // (counts before the bin, and with it)
+                sh.found_count = c + n[bin & 3];
+            }
+            __syncthreads();
+            const uint32_t first = sh.found_above, past = sh.found_count;
+            uint32_t c = upto - number;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at = 4 * tid + i;
+                if (at <= bin && (first - c <= near * CL_SHARE || at + 1 >= bin)) atomicMin(&sh.found_from, at);
+                c += n[i];
+                if (at >= bin && (c - past <= near * CL_SHARE || at <= bin + 1)) atomicMax(&sh.found_to, at);
+            }
+        }
         __syncthreads();
-        if (tid < row.CS) {
-            const uint32_t b = sh.found_bin;
-            const uint32_t* all = row.CS > 1 ? reinterpret_cast<const uint32_t*>(sh.list) : sh.count;
-            const uint32_t near = all[b] + (b > 0 ? all[b - 1] : 0) + (b + 1 < CL_BINS ? all[b + 1] : 0);
+        if (tid > 0 && tid < row.CS) {
             CutShared* o = row.of(&sh, tid);
-            o->found_bin = b;
-            o->found_count = near;
+            o->found_bin = sh.found_bin;
+            o->found_from = sh.found_from;
+            o->found_to = sh.found_to;
         }
     }
     row.sync();
@@ -451,24 +562,61 @@ __device__ __forceinline__ void clear_bins(const Row<BF16>& row) {
     __syncthreads();
 }
 
-// Sums of the weights at or above `cut`, this warp's into the first CTA's
-// part_mass and the total to every thread.
+// This lane's copy of the table, all of them written first.
 template <bool BF16>
-__device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
+__device__ __forceinline__ const ExpEntry* copy_table(const Row<BF16>& row) {
+    CutShared& sh = *row.sh;
+    __syncthreads();
+    for (int i = threadIdx.x; i < CL_EXP * CL_COPIES; i += CL_THREADS) sh.copies[i] = sh.exp[i / CL_COPIES];
+    __syncthreads();
+    return sh.copies + (threadIdx.x & (CL_COPIES - 1));
+}
+
+// Sums of the weights at or above `cut`, this warp's into the first CTA's
+// part_mass and the total to every thread. others(x, v): what else is to be done
+// with each piece.
+template <bool BF16, class F>
+__device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut, F&& others) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     u64 m = 0;
-    row.each_piece(cut, [&](const uint4& x, int v) {
-        const int i0 = row.index(v);
+    const ExpEntry* copy = copy_table(row);
+    if (row.s.low == row.s.low) {
+        // At or above the cut is z >= its logit before its index and z > it behind.
+        const float z_cut = key_value<BF16>(place_key(cut)), z_from = fmaxf(z_cut, row.s.low);
+        const int i_cut = place_index(cut);
+        const float z_over = cut == CL_LOWEST ? z_from : fmaxf(key_value<BF16>(place_key(cut) + 1), row.s.low);
+        WeightSum sum;
+        row.each_piece(cut, [&](const uint4& x, int v) {
+            const int i0 = row.index(v);
+            if (i0 <= i_cut && i_cut < i0 + R::E - 1) {  // the one piece that the index divides
 #pragma unroll
-        for (int e = 0; e < R::E; e += 2) {
-            const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
-            const bool in0 = place_of(key_of<BF16>(z0), i0 + e) >= cut, in1 = place_of(key_of<BF16>(z1), i0 + e + 1) >= cut;
-            u64 w0, w1;
-            weight_pair(z0, z1, row.s, sh.exp, w0, w1);
-            m += (in0 ? w0 : 0) + (in1 ? w1 : 0);
-        }
-    });
+                for (int e = 0; e < R::E; ++e) {
+                    const float z = piece_elem<BF16>(x, e);
+                    if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s, row.sh->exp);
+                }
+            } else {
+                const float from = i0 + R::E - 1 <= i_cut ? z_from : z_over;
+#pragma unroll
+                for (int e = 0; e < R::E; e += 2) {
+                    const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
+                    sum.add(z0 >= from ? z0 : row.s.low, z1 >= from ? z1 : row.s.low, row.s, copy);
+                }
+            }
+            others(x, v);
+        });
+        m += sum.total();
+    } else {
+        row.each_piece(cut, [&](const uint4& x, int v) {
+            const int i0 = row.index(v);
+#pragma unroll 1
+            for (int e = 0; e < R::E; ++e) {
+                const float z = piece_elem<BF16>(x, e);
+                if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s, row.sh->exp);
+            }
+            others(x, v);
+        });
+    }
     m = warp_sum(m);
     if (row.lane == 0) row.of(&sh, 0)->part_mass[row.rank * CL_WARPS + row.warp] = m;
     row.sync();
@@ -510,7 +658,7 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
             if (p < lo || p > hi) continue;
             const int bin = (int)((p - lo) >> shift);
             atomicAdd(&sh.count[bin], 1u);
-            if (BY_MASS) atomicAdd(&mass[bin], weight(z, row.s, sh.exp));
+            if (BY_MASS) atomicAdd(&mass[bin], weight(z, row.s, row.sh->exp));
         }
     });
     row.sync();
@@ -598,7 +746,7 @@ __device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool b
     u64 carry = mass_above;
     for (int base = 0; base < n; base += CL_THREADS) {
         const int i = base + tid;
-        const u64 p = i < n ? sh.list[i] : 0, w = i < n ? weight(key_value<BF16>(place_key(p)), row.s, sh.exp) : 0;
+        const u64 p = i < n ? sh.list[i] : 0, w = i < n ? weight(key_value<BF16>(place_key(p)), row.s, row.sh->exp) : 0;
         u64 total;
         const u64 incl = carry + block_scan(w, sh.warp_mass, row.lane, row.warp, total);
         const u64 before = incl - w;
@@ -613,7 +761,7 @@ __device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool b
 // 4. The place of the last element that a cut keeps, exactly, in [lo, hi]: the
 // range narrows until what is left fits the list, where it is picked.
 template <bool BF16, bool BY_MASS>
-__device__ __noinline__ u64 find_cut(const Row<BF16>& row, u64 lo, u64 hi, uint32_t k, double goal) {
+__device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32_t k, double goal) {
     CutShared& sh = *row.sh;
     uint32_t above = 0, left = CL_LIST + 1;
     u64 mass_above = 0;
@@ -641,22 +789,34 @@ __device__ __forceinline__ u64 draw_target(float u, u64 total) {
     return t < total ? t : total - 1;
 }
 
-__device__ __forceinline__ void put_token(const CutParams& P, int64_t row, int index, float z, const RowScale& s, double inv_t, u64 total) {
+// ln(total / 2^44) for total of 2^44 or more: total = 2^(k + i / 256) (1 + d) with
+// the table's factor, and ln(1 + d) by its series, d < 2^-8; to about 2^-36.
+__device__ __forceinline__ double log_total(u64 total, const ExpEntry* table) {
+    const int k = 63 - __clzll((long long)total);
+    const double m = (double)total * __longlong_as_double((long long)(1023 - k) << 52);  // [1, 2)
+    const int i = min((int)(log2f((float)m) * (float)CL_EXP), CL_EXP - 1);
+    // 2^(-i / 256) = 2^((256 - i) / 256) / 2
+    const ExpEntry e = table[(CL_EXP - i) & (CL_EXP - 1)];
+    const double d = m * (((double)e.hi + (double)e.lo) * (i == 0 ? 1.0 : 0.5)) - 1.0;
+    const float f = (float)d, tail = f * f * (f * (1.0f / 3.0f) - 0.5f - f * f * 0.25f);
+    return ((double)(k - CL_UNIT) + (double)i * (1.0 / CL_EXP)) * 0.69314718055994530942 + (d + (double)tail);
+}
+
+__device__ __forceinline__ void put_token(const CutParams& P, int64_t row, int index, float z, const CutShared& sh, float top, u64 total) {
     P.tokens[row] = index;
-    if (P.logprobs)
-        P.logprobs[row] = (float)(((double)z - (double)s.top) * inv_t - log((double)total * (1.0 / (double)(1ull << CL_UNIT))));
+    if (P.logprobs) P.logprobs[row] = (float)(((double)z - (double)top) * sh.inv_t - log_total(total, sh.exp));
 }
 
 // Draws from the first n of the sorted list, by this CTA.
 template <bool BF16>
-__device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& row, int64_t at_row, int n, double inv_t) {
+__device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& row, int64_t at_row, float u, int n) {
     CutShared& sh = *row.sh;
     const int tid = threadIdx.x;
     // entries become (index, weight), 18 and 45 bits, and are sorted by index
     constexpr u64 W = (2ull << CL_UNIT) - 1;
     for (int i = tid; i < n; i += CL_THREADS) {
         const u64 p = sh.list[i];
-        sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(key_value<BF16>(place_key(p)), row.s, sh.exp);
+        sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(key_value<BF16>(place_key(p)), row.s, row.sh->exp);
     }
     __syncthreads();
     if (n > 1) sort_list(sh.list, n);  // (descending reversed index)
@@ -664,7 +824,7 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
     for (int i = tid; i < n; i += CL_THREADS) total += sh.list[i] & W;
     u64 all;
     block_scan(total, sh.warp_mass, row.lane, row.warp, all);
-    const u64 target = draw_target(P.uniforms[at_row], all);
+    const u64 target = draw_target(u, all);
     u64 carry = 0;
     for (int base = 0; base < n; base += CL_THREADS) {
         const int i = base + tid;
@@ -675,7 +835,7 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
             const int index = (int)(CL_INDEX_MASK - (uint32_t)(e >> (CL_UNIT + 1)));
             const float z = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row.src)[index] << 16)
                                  : reinterpret_cast<const float*>(row.src)[index];
-            put_token(P, at_row, index, z, row.s, inv_t, all);
+            put_token(P, at_row, index, z, sh, row.s.top, all);
         }
         carry += sum;
     }
@@ -684,7 +844,7 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
 // Draws over the warps' parts, whose sums at or above `cut` lie in the first
 // CTA's part_mass: that finds the warp, and the warp the element.
 template <bool BF16>
-__device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& row, int64_t at_row, u64 cut, double inv_t) {
+__device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& row, int64_t at_row, float u, u64 cut) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     const int lane = row.lane;
@@ -697,7 +857,7 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
             sum += m[i];
         }
         const u64 incl = warp_scan(sum, lane), total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-        const u64 target = draw_target(P.uniforms[at_row], total);
+        const u64 target = draw_target(u, total);
         u64 before = incl - sum;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -712,43 +872,41 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
         }
     }
     row.sync();
-    if (sh.draw_warp != (uint32_t)(row.rank * CL_WARPS + row.warp)) return;
+    // The part's pieces, a run of neighbours for each thread of its CTA.
+    const int part = (int)sh.draw_warp - row.rank * CL_WARPS;
+    if (part < 0 || part >= CL_WARPS) return;
     const u64 target = sh.draw_at, total = sh.found_mass;
     const uint32_t lo16 = R::lo16_of(cut);
-    u64 before = 0;
-    for (int vb = row.v0; vb < row.v1; vb += 32) {
-        const int v = vb + lane;
-        const bool look = v < row.v1 && row.keys[v] >= lo16;
-        if (!__any_sync(0xFFFFFFFFu, look)) continue;
-        u64 mine = 0;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (look) x = row.load(v, R::NOBODY);
-        const auto weight_at = [&](int e) -> u64 {
-            const float z = piece_elem<BF16>(x, e);
-            return look && place_of(key_of<BF16>(z), row.index(v) + e) >= cut ? weight(z, row.s, sh.exp) : 0;
-        };
-#pragma unroll
-        for (int e = 0; e < R::E; ++e) mine += weight_at(e);
-        const u64 incl = warp_scan(mine, lane);
-        u64 at = before + incl - mine;
-        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-        if (target >= before) continue;
-        if (at <= target && target < at + mine) {
+    const int p0 = min(part * row.run, row.n_vecs), p1 = min(p0 + row.run, row.n_vecs);
+    const int per = (row.run + CL_THREADS - 1) / CL_THREADS, v0 = min(p0 + (int)threadIdx.x * per, p1), v1 = min(v0 + per, p1);
+    const auto each_weight = [&](auto&& f) {
+        for (int v = v0; v < v1; ++v) {
+            if (row.keys[v] < lo16) continue;
+            const uint4 x = row.load(v);
 #pragma unroll
             for (int e = 0; e < R::E; ++e) {
-                const u64 w = weight_at(e);
-                if (at <= target && target < at + w) put_token(P, at_row, row.index(v) + e, piece_elem<BF16>(x, e), row.s, inv_t, total);
-                at += w;
+                const float z = piece_elem<BF16>(x, e);
+                if (place_of(key_of<BF16>(z), row.index(v) + e) >= cut) f(weight(z, row.s, sh.exp), row.index(v) + e, z);
             }
         }
-        return;
+    };
+    u64 mine = 0, all;
+    each_weight([&](u64 w, int, float) { mine += w; });
+    const u64 incl = block_scan(mine, sh.warp_mass, lane, row.warp, all);
+    const u64 goal = target < all ? target : all - 1;  // (the part's sum in floats may be a little more than this one)
+    u64 at = incl - mine;
+    if (at <= goal && goal < incl) {
+        each_weight([&](u64 w, int index, float z) {
+            if (at <= goal && goal < at + w) put_token(P, at_row, index, z, sh, row.s.top, total);
+            at += w;
+        });
     }
 }
 
 // 3. Top-p alone. Returns the place of the last kept element and leaves the sums
 // of the warps' parts at or above it in the first CTA's part_mass.
 template <bool BF16>
-__device__ __noinline__ u64 cut_by_mass(const Row<BF16>& row, float top_p, float T, u64 highest) {
+__device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float T, u64 highest) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     const RowScale& s = row.s;
@@ -759,73 +917,57 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16>& row, float top_p, float
     const float span_log = __logf((float)row.V / fmaxf(1.0f - top_p, 1e-9f)) + 0.01f;
     const float span = span_log * T, to_bin = (float)CL_BINS / span, bin_log = span_log / (float)CL_BINS;
     clear_bins(row);
-    // all weights, and the histogram: 4096 per element at a bin's upper edge, less
-    // towards its lower one as the weight falls
-    u64 m = 0;
-    row.each_piece(CL_LOWEST, [&](const uint4& x, int) {
+    // All weights, and the histogram: CL_SHARE per element at a bin's upper edge, less
+    // towards its lower one as the weight falls. A logit's bin and its place in it
+    // come from the low bits of a float that 2^23 was added to.
+    const float fine = 128.0f * to_bin, shifted = __fmaf_rn(s.top, fine, 8388608.0f), last = 8388608.0f + 128.0f * CL_BINS - 1.0f;
+    const uint32_t fall = (uint32_t)(bin_log * (float)CL_SHARE * 2.0f + 0.5f);
+    const bool flat = !(fabsf(s.top * fine) < 4194304.0f);  // (then shifted has no room)
+    const u64 m = sum_above(row, CL_LOWEST, [&](const uint4& x, int) {
 #pragma unroll
-        for (int e = 0; e < R::E; e += 2) {
-            const float z[2] = {piece_elem<BF16>(x, e), piece_elem<BF16>(x, e + 1)};
-            u64 w0, w1;
-            weight_pair(z[0], z[1], s, sh.exp, w0, w1);
-            m += w0 + w1;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float d = __fsub_rn(s.top, z[q]);
-                if (!(d < span)) continue;
-                const float y = __fmul_rn(d, to_bin);
-                const int bin = min((int)y, CL_BINS - 1);
-                atomicAdd(&sh.count[bin], 4096u - (uint32_t)((y - (float)bin) * bin_log * 4096.0f));
-            }
+        for (int e = 0; e < R::E; ++e) {
+            const float z = piece_elem<BF16>(x, e);
+            const float y = flat ? __fmaf_rn(__fsub_rn(s.top, z), fine, 8388608.0f) : __fmaf_rn(-z, fine, shifted);
+            if (!(y <= last)) continue;
+            const uint32_t at = __float_as_uint(fmaxf(y, 8388608.0f)) & 0x7FFFFFu;
+            atomicAdd(&sh.count[at >> 7], CL_SHARE - (((at & 127u) * fall + 128u) >> 8));
         }
     });
-    m = warp_sum(m);
-    if (row.lane == 0) row.of(&sh, 0)->part_mass[row.rank * CL_WARPS + row.warp] = m;
-    row.sync();
-    {
-        const u64* parts = row.of(&sh, 0)->part_mass;
-        u64 t = 0;
-        for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) t += parts[w];
-        m = warp_sum(t);
-    }
     const double goal = (double)top_p * (double)m;
-    find_bin(row, (float)(goal * (1.0 / (double)(1ull << CL_UNIT))), bin_log * 1.4426950408889634f, 1.0f / 4096.0f);
-    const int bin = (int)sh.found_bin;
+    find_bin(row, (float)(goal * (1.0 / (double)(1ull << CL_UNIT))), bin_log * 1.4426950408889634f, CL_NEAR);
+    const int bin0 = (int)sh.found_from, bin1 = (int)sh.found_to;
     u64 place = 0;
-    if (sh.found_count < (uint32_t)CL_LIST * 4096u) {
-        // the exact sum above the bin before it, and these three bins to the list
-        const float near_z = __fsub_rn(s.top, (float)(bin + 2) / to_bin * 1.00001f);
-        const u64 lo = max(CL_LOWEST, (u64)key_of<BF16>(near_z - fabsf(near_z) * 1e-6f) << CL_INDEX_BITS);
+    bool any_above = false;
+    {
+        // the sum above the first of these bins, and what lies in them to the list
+        const float z_hi = bin0 > 0 ? __fsub_rn(s.top, (float)bin0 / to_bin) : INFINITY;
+        const float z_lo = key_value<BF16>(key_of<BF16>(__fsub_rn(s.top, (float)(bin1 + 1) / to_bin)));
+        const u64 over = bin0 > 0 ? (u64)(key_of<BF16>(z_hi) + 1) << CL_INDEX_BITS : ~0ull;  // above z_hi
+        const u64 lo = max(CL_LOWEST, (u64)key_of<BF16>(z_lo) << CL_INDEX_BITS);
         CutShared* head = row.of(&sh, 0);
-        m = 0;
-        uint32_t above = 0;
+        any_above = over <= highest;
+        const ExpEntry* copy = sh.copies + (tid & (CL_COPIES - 1));
+        WeightSum sum;
+        u64 exact = 0;
+        const bool fast = s.low == s.low;
+        const float from = bin0 > 0 ? fmaxf(key_value<BF16>(key_of<BF16>(z_hi) + 1), fast ? s.low : -INFINITY) : INFINITY;
         row.each_piece(lo, [&](const uint4& x, int v) {
             const int i0 = row.index(v);
 #pragma unroll
             for (int e = 0; e < R::E; e += 2) {
                 const float z[2] = {piece_elem<BF16>(x, e), piece_elem<BF16>(x, e + 1)};
-                bool up[2];
+                const bool up0 = z[0] >= from, up1 = z[1] >= from;
+                if (up0 || up1) {
+                    if (fast) sum.add(up0 ? z[0] : s.low, up1 ? z[1] : s.low, s, copy);
+                    else exact += (up0 ? weight(z[0], s, sh.exp) : 0) + (up1 ? weight(z[1], s, sh.exp) : 0);
+                }
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float d = __fsub_rn(s.top, z[q]);
-                    const int at = d < span ? min((int)__fmul_rn(d, to_bin), CL_BINS - 1) : CL_BINS + 1;
-                    up[q] = at < bin - 1;
-                    if (!up[q] && at <= bin + 1) append(head, place_of(key_of<BF16>(z[q]), i0 + e + q));
-                }
-                above += up[0] + up[1];
-                if (up[0] || up[1]) {
-                    u64 w0, w1;
-                    weight_pair(z[0], z[1], s, sh.exp, w0, w1);
-                    m += (up[0] ? w0 : 0) + (up[1] ? w1 : 0);
-                }
+                for (int q = 0; q < 2; ++q)
+                    if (z[q] >= z_lo && z[q] < from) append(head, place_of(key_of<BF16>(z[q]), i0 + e + q));
             }
         });
-        m = warp_sum(m);
-        above = __reduce_add_sync(0xFFFFFFFFu, above);
-        if (row.lane == 0) {
-            head->part_mass[row.rank * CL_WARPS + row.warp] = m;
-            if (above) atomicAdd(&head->kept, above);
-        }
+        const u64 mine = warp_sum(exact + sum.total());
+        if (row.lane == 0) head->part_mass[row.rank * CL_WARPS + row.warp] = mine;
         row.sync();
         if (row.rank == 0) {
             const int n = (int)sh.list_n;
@@ -833,7 +975,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16>& row, float top_p, float
             for (int w = 0; w < row.CS * CL_WARPS; ++w) mass_above += sh.part_mass[w];
             if (n <= CL_LIST) {
                 sort_list(sh.list, n);
-                place = reach_in_list(row, n, true, sh.kept, mass_above, 0, goal);
+                place = reach_in_list(row, n, true, any_above, mass_above, 0, goal);
                 // what of the list is kept joins its warps' sums
                 if (place) {
                     const int lead = (int)((reinterpret_cast<uintptr_t>(row.src) & 15) / R::ES);
@@ -841,7 +983,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16>& row, float top_p, float
                         const u64 p = sh.list[i];
                         if (p < place) continue;
                         const int piece = (place_index(p) + lead) / R::E, cta = piece / row.slice, in_cta = piece - cta * row.slice;
-                        atomicAdd(&sh.part_mass[cta * CL_WARPS + in_cta / row.run], weight(key_value<BF16>(place_key(p)), s, sh.exp));
+                        atomicAdd(&sh.part_mass[cta * CL_WARPS + in_cta / row.run], weight(key_value<BF16>(place_key(p)), s, row.sh->exp));
                     }
                 }
             }
@@ -856,7 +998,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16>& row, float top_p, float
     if (place == 0) {
         // more equal logits than the list takes, or a border that the histogram missed
         place = find_cut<BF16, true>(row, CL_LOWEST, highest, 0, goal);
-        sum_above(row, place);
+        sum_above(row, place, [](const uint4&, int) {});
     }
     return place;
 }
@@ -890,7 +1032,13 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     row.v0 = min(warp * P.warp_vecs, row.n_vecs);
     row.v1 = min(row.v0 + P.warp_vecs, row.n_vecs);
     row.first = begin * R::E - lead;
-    if (tid == 0) sh.list_n = sh.hits_n = sh.kept = 0;
+    row.base = reinterpret_cast<const uint4*>(row.src - lead * R::ES) + begin;
+    row.full0 = row.first < 0 ? 1 : 0;
+    row.full1 = row.first + row.n_vecs * R::E > P.V ? row.n_vecs - 1 : row.n_vecs;
+    if (tid == 0) {
+        sh.list_n = sh.hits_n = 0;
+        sh.first = INT32_MAX;
+    }
     if (tid < CL_EXP) sh.exp[tid] = g_exp_table.e[tid];
     if (tid < 8) row.keys[(row.n_vecs & ~7) + tid] = 0;  // behind the last key (written below) up to whole 16 bytes
     __syncthreads();
@@ -898,36 +1046,56 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     grid_dependency_wait();
     launch_dependents();
 
-    // 1. The maximum and the pieces' keys.
-    float top = -INFINITY;
-    constexpr int U = 8;
-    for (int v = row.v0 + lane; v < row.v1; v += 32 * U) {
-        uint4 x[U];
-#pragma unroll
-        for (int q = 0; q < U; ++q)
-            if (v + 32 * q < row.v1) x[q] = row.load(v + 32 * q, R::MINUS_INF);
-#pragma unroll
-        for (int q = 0; q < U; ++q) {
-            if (v + 32 * q >= row.v1) continue;
-            float most;
-            if constexpr (BF16) {
-                const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(x[q].x, x[q].y), max_nan_bf16x2(x[q].z, x[q].w));
-                most = max_nan(bf16_lo(m), bf16_hi(m));
-            } else {
-                most = max_nan(max_nan(__uint_as_float(x[q].x), __uint_as_float(x[q].y)), max_nan(__uint_as_float(x[q].z), __uint_as_float(x[q].w)));
-            }
-            row.keys[v + 32 * q] = (uint16_t)(key32(most) >> 16);
-            top = max_nan(top, most);
-        }
-    }
     const float T = P.temperatures ? P.temperatures[b] : P.temperature;
     const int top_k = P.top_ks ? P.top_ks[b] : P.top_k;
     const float top_p = P.top_ps ? P.top_ps[b] : P.top_p, min_p = P.min_ps ? P.min_ps[b] : P.min_p;
     const bool settings_ok = (T == 0.0f || (T >= 0x1p-64f && T <= 0x1p64f)) && top_k >= 0 && top_p >= 0.0f && top_p <= 1.0f &&
                              min_p >= 0.0f && min_p <= 1.0f;
     const int k = T == 0.0f ? 1 : top_k > 0 && top_k < P.V ? top_k : P.V;
-    const double inv_t = T == 0.0f ? 1.0 : 1.0 / (double)T;
+    const float u = DRAW ? P.uniforms[at_row] : 0.0f;
+    if (tid == CL_THREADS - 1) {
+        const double inv_t = T == 0.0f ? 1.0 : 1.0 / (double)T, c = 1.4426950408889634 * CL_EXP * inv_t;
+        sh.inv_t = inv_t;
+        sh.ch = (float)c;
+        sh.cl = (float)(c - (double)sh.ch);
+        sh.low_by = (float)(100.0 * CL_EXP / 1.4426950408889634 / CL_EXP) * (T == 0.0f ? 1.0f : T);
+        const double d = min_p > 0.0f && T != 0.0f ? (double)T * log((double)min_p) : 0.0;
+        sh.min_hi = (float)d;
+        sh.min_lo = (float)(d - (double)sh.min_hi);
+    }
 
+    // 1. The maximum and the pieces' keys.
+    float top;
+    {
+        constexpr int U = 8;
+        uint32_t most = BF16 ? 0xFF80FF80u : 0xFF800000u;
+        int v = row.v0 + lane;
+        const int end = min(row.v1, row.full1);
+        if (v < row.full0 && v < row.v1) {
+            row.keys[v] = R::piece_key(load_part<BF16>(row.src, P.V, row.index(v), R::MINUS_INF), most);
+            v += 32;
+        }
+        for (; v + 32 * (U - 1) < end; v += 32 * U) {
+            uint4 x[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) x[q] = row.load_whole(v + 32 * q);
+#pragma unroll
+            for (int q = 0; q < U; ++q) row.keys[v + 32 * q] = R::piece_key(x[q], most);
+        }
+        {
+            uint4 x[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (v + 32 * q < end) x[q] = row.load_whole(v + 32 * q);
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (v + 32 * q < end) row.keys[v + 32 * q] = R::piece_key(x[q], most);
+        }
+        const int last = row.v1 - 1;
+        if (last >= max(row.full1, row.v0) && last >= row.full0 && ((last - row.v0) & 31) == lane)
+            row.keys[last] = R::piece_key(load_part<BF16>(row.src, P.V, row.index(last), R::MINUS_INF), most);
+        top = BF16 ? max_nan(bf16_lo(most), bf16_hi(most)) : __uint_as_float(most);
+    }
     float wmax = top, least = top > -INFINITY ? top : INFINITY;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -967,20 +1135,34 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         }
         if constexpr (DRAW) return;
     } else {
-        const double c = 1.4426950408889634 * CL_EXP * inv_t;
-        row.s.ch = (float)c;
-        row.s.cl = (float)(c - (double)s.ch);
+        row.s.ch = sh.ch;
+        row.s.cl = sh.cl;
+        row.s.low = fabsf(s.top * s.ch) < 0x1p21f ? s.top - sh.low_by : __int_as_float(0x7fc00000);
         const u64 highest = (u64)key_of<BF16>(s.top) << CL_INDEX_BITS | CL_INDEX_MASK;
         // min-p: z >= max + T ln(min_p)
         if (min_p > 0.0f && T != 0.0f) {
-            const float z = __double2float_ru((double)s.top + (double)T * log((double)min_p));
+            // the smallest float that is not below the sum of three
+            const ff sum = two_sum(s.top, sh.min_hi);
+            const float rest = __fadd_rn(sum.lo, sh.min_lo);
+            const float z = rest > 0.0f ? from_key32(key32(sum.hi) + 1) : sum.hi;
             // bf16 keys of negative values end in ones, those of others in zeros
             const uint32_t kz = key32(z), key = !BF16 ? kz : (kz >> 31) ? (uint32_t)(((u64)kz + 0xFFFFu) >> 16) : kz >> 16;
             cut = max(cut, (u64)key << CL_INDEX_BITS);
         }
         const bool by_k = k < P.V, by_p = T != 0.0f && top_p < 1.0f;
         bool summed = false;  // part_mass holds the sums at or above the cut
-        if (by_k) {
+        if (k == 1) {
+            // the first of the largest
+            const int first = first_largest(row, highest & ~(u64)CL_INDEX_MASK);
+            if constexpr (DRAW) {
+                if (rank == 0 && tid == 0) {
+                    P.tokens[at_row] = first;
+                    if (P.logprobs) P.logprobs[at_row] = 0.0f;
+                }
+                return;
+            }
+            cut = place_of(place_key(highest), first);
+        } else if (by_k) {
             // 2. a bound on the k-th largest
             u64 bound = CL_LOWEST;
             if (k <= warps) {
@@ -1015,7 +1197,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                             atomicAdd(&sh.count[max(0, min((int)y, CL_BINS - 1))], 1u);
                         }
                     }
-                    find_bin(row, (float)k, 0.0f, 1.0f);
+                    find_bin(row, (float)k, 0.0f, 0);
                     if (sh.found_bin < CL_BINS - 1) {
                         const float z = __fsub_rn(s.top, (float)(sh.found_bin + 1) / to_bin * 1.0001f);
                         bound = max(bound, (u64)key_of<BF16>(z - fabsf(z) * 1e-6f) << CL_INDEX_BITS);
@@ -1035,7 +1217,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                     listed = true;
                 } else {
                     if (by_p) {
-                        const u64 mass = sum_above(row, cut_k);
+                        const u64 mass = sum_above(row, cut_k, [](const uint4&, int) {});
                         row.sync();
                         cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, (double)top_p * (double)mass));
                     }
@@ -1043,8 +1225,10 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                 }
             }
             if (listed) {
-                // The cuts, in the list.
-                row.sync();  // everyone has read its length
+                // The cuts, in the list, whose length the others have read when they
+                // have arrived here.
+                row.arrive();
+                if (CS == 1) __syncthreads();
                 if (rank == 0) {
                     const int all = min((int)n, CL_LIST);
                     sort_list(sh.list, all);
@@ -1052,7 +1236,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                     u64 last = of_k > 0 ? sh.list[of_k - 1] : 0;
                     if (by_p) {
                         u64 m = 0, total;
-                        for (int i = tid; i < of_k; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), s, sh.exp);
+                        for (int i = tid; i < of_k; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), s, row.sh->exp);
                         block_scan(m, sh.warp_mass, lane, warp, total);
                         last = max(last, reach_in_list(row, of_k, true, 0, 0, 0, (double)top_p * (double)total));
                     }
@@ -1063,12 +1247,13 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                         for (int i = tid; i < of_k; i += CL_THREADS) kept += sh.list[i] >= last;
                         uint32_t total;
                         block_scan((uint32_t)kept, sh.warp_count, lane, warp, total);
-                        draw_list(P, row, at_row, (int)total, inv_t);
+                        draw_list(P, row, at_row, u, (int)total);
                     } else {
                         __syncthreads();
                         if (tid == 0) row.each_cta([&](CutShared* o) { o->found_place = last; });
                     }
                 }
+                row.wait();
                 if constexpr (DRAW) return;
                 row.sync();
                 cut = sh.found_place;
@@ -1081,9 +1266,9 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         if constexpr (DRAW) {
             if (!summed) {
                 row.sync();
-                sum_above(row, cut);
+                sum_above(row, cut, [](const uint4&, int) {});
             }
-            draw_parts(P, row, at_row, cut, inv_t);
+            draw_parts(P, row, at_row, u, cut);
             return;
         }
     }
@@ -1099,7 +1284,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             const int i0 = row.index(v);
             uint4 x = make_uint4(NONE, NONE, NONE, NONE);
             if (!valid || row.keys[v] >= lo16) {
-                x = row.load(v, R::NOBODY);
+                x = row.load(v);
                 uint32_t* w = reinterpret_cast<uint32_t*>(&x);
                 if (valid) {
 #pragma unroll
