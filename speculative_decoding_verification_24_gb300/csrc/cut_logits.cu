@@ -53,6 +53,7 @@ constexpr int CL_WARPS = CL_THREADS / 32;
 constexpr int CL_MAX_CS = 8;
 constexpr int CL_BINS = 2048;
 constexpr int CL_LIST = 2048;
+constexpr int CL_GROUPS = 256;
 constexpr uint32_t CL_NEAR = 150;  // elements on either side of where a histogram finds a border
 constexpr int CL_HITS = 2048;  // pieces of one CTA that gather() reads in one step
 constexpr int CL_ROUNDS = 5;   // of 11 bits each; a place has 50
@@ -94,6 +95,7 @@ struct RowScale {
     float top;       // the row's maximum
     float ch, cl;    // 256 log2(e) / T in two floats
     float low;       // a logit of weight 2^-100; NaN where the row's maximum has no room for one
+    float shift, frac;  // for WeightSum, where there is room
 };
 
 // Order of floats as unsigned integers; -0 counts as 0.
@@ -145,42 +147,52 @@ __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry
 }
 
 // Adds up weights in floats, two elements at a time in packed instructions, for
-// the passes over whole rows (the integers' shifts cost twice as much: 57
-// instructions per element against 27). w = (hi + (lo + hi e)) 2^-k; the sum s of
-// the first parts begins at 1, so that s >= any of them and (s' - s) - a is the
-// rounding error of s' = s + a exactly; c takes those and the second parts. s + c
-// is right to 2^-34 of the sum or so, beside the weights' own error.
+// the passes over whole rows (shifting integers took twice as long). Here y = z c -
+// top c, formed at once: r.shift is the magic number less the whole part of top c
+// and r.frac the rest, so that t's low bits are n again; the maximum's own weight
+// is made 1 exactly, which keeps ties exact. w = (hi + (lo + hi e)) 2^-k; the sum
+// s of the first parts begins at 1, so that s >= any of them and a - (s' - s) is
+// the rounding error of s' = s + a exactly; c takes those and the second parts.
+// s + c is right to 2^-33 of the sum or so, like the weights.
 struct WeightSum {
     f32x2 s, c;
     __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)) {}
-    // z0, z1 >= r.low
-    __device__ __forceinline__ void add(float z0, float z1, const RowScale& r, const ExpEntry* table) {
-        const f32x2 z = pack2(z0, z1), top = pack2(r.top, r.top), minus = pack2(-1.0f, -1.0f), ch = pack2(r.ch, r.ch), cl = pack2(r.cl, r.cl);
-        const f32x2 magic = pack2(12582912.0f, 12582912.0f);
-        const f32x2 dh = fma2(top, minus, z);
-        const f32x2 bb = fma2(z, minus, dh);
-        const f32x2 dl = fma2(add2(top, bb), minus, fma2(fma2(bb, minus, dh), minus, z));
-        const f32x2 t = fma2(dh, ch, magic);
-        const f32x2 x = add2(fma2(dh, ch, fma2(t, minus, magic)), fma2(dh, cl, mul2(dl, ch)));
-        const f32x2 e = mul2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1)));
-        float t0, t1;
+    // The two parts of a pair's weights; z0, z1 >= r.low.
+    static __device__ __forceinline__ void pair(float z0, float z1, const RowScale& r, const ExpEntry* table, f32x2& a, f32x2& rest) {
+        const f32x2 z = pack2(z0, z1), minus = pack2(-1.0f, -1.0f), ch = pack2(r.ch, r.ch), shift = pack2(r.shift, r.shift);
+        const f32x2 t = fma2(z, ch, shift);
+        f32x2 x = add2(fma2(z, ch, fma2(t, minus, shift)), fma2(z, pack2(r.cl, r.cl), pack2(-r.frac, -r.frac)));
+        float x0, x1, t0, t1, e0, e1;
+        unpack2(x, x0, x1);
+        x = pack2(z0 == r.top ? 0.0f : x0, z1 == r.top ? 0.0f : x1);
+        unpack2(mul2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1))), e0, e1);
         unpack2(t, t0, t1);
         const uint32_t b0 = __float_as_uint(t0), b1 = __float_as_uint(t1);
         const ExpEntry p = table[(b0 & (CL_EXP - 1)) * CL_COPIES], q = table[(b1 & (CL_EXP - 1)) * CL_COPIES];
         // 2^floor(n / 256): the magic number's upper bits leave the word
         const auto scale = [](uint32_t b) { return __uint_as_float((b & ~(uint32_t)(CL_EXP - 1)) * (1u << (23 - CL_EXP_BITS)) + 0x3F800000u); };
-        const f32x2 pow = pack2(scale(b0), scale(b1)), hi = pack2(p.hi, q.hi);
-        const f32x2 a = mul2(hi, pow), rest = mul2(fma2(hi, e, pack2(p.lo, q.lo)), pow);
-        const f32x2 sum = add2(s, a);
+        const float pow0 = scale(b0), pow1 = scale(b1);
+        a = pack2(__fmul_rn(p.hi, pow0), __fmul_rn(q.hi, pow1));
+        rest = pack2(__fmul_rn(__fmaf_rn(p.hi, e0, p.lo), pow0), __fmul_rn(__fmaf_rn(q.hi, e1, q.lo), pow1));
+    }
+    __device__ __forceinline__ void add(f32x2 a, f32x2 rest) {
+        const f32x2 minus = pack2(-1.0f, -1.0f), sum = add2(s, a);
         c = add2(c, add2(fma2(fma2(s, minus, sum), minus, a), rest));
         s = sum;
+    }
+    __device__ __forceinline__ void add(float z0, float z1, const RowScale& r, const ExpEntry* table) {
+        f32x2 a, rest;
+        pair(z0, z1, r, table, a, rest);
+        add(a, rest);
     }
     __device__ __forceinline__ u64 total() const {
         float s0, s1, c0, c1;
         unpack2(s, s0, s1);
         unpack2(c, c0, c1);
-        const double v = ((double)s0 - 1.0) + ((double)s1 - 1.0) + ((double)c0 + (double)c1);
-        return v > 0.0 ? (u64)__double2ll_rn(v * (double)(1ull << CL_UNIT)) : 0ull;
+        // (differences from 1 are exact, and a double's units are few)
+        const ff sum = two_sum(__fsub_rn(s0, 1.0f), __fsub_rn(s1, 1.0f));
+        const long long v = __float2ll_rn(sum.hi * 0x1p44f) + __float2ll_rn(__fadd_rn(sum.lo, __fadd_rn(c0, c1)) * 0x1p44f);
+        return v > 0 ? (u64)v : 0ull;
     }
 };
 
@@ -194,7 +206,8 @@ struct alignas(16) CutShared {
         uint32_t hits[CL_HITS];      // pieces to read
     };
     u64 part_mass[CL_MAX_CS * CL_WARPS];  // weights of every warp's part, in the first CTA
-    float warp_max[CL_MAX_CS * CL_WARPS];
+    u64 part_all[CL_MAX_CS * CL_WARPS];
+    float group_max[CL_GROUPS];  // of lanes, whose pieces' maxima they are
     float lane_min[CL_MAX_CS * CL_WARPS];
     u64 cta_mass[CL_MAX_CS];
     u64 warp_mass[CL_WARPS];
@@ -203,7 +216,7 @@ struct alignas(16) CutShared {
     u64 seg_mass[CL_MAX_CS];
     uint32_t seg_count[CL_MAX_CS];
     // what a search has found, told to every CTA
-    u64 found_mass, found_place, draw_at;
+    u64 found_mass, found_place, draw_at, goal;
     uint32_t found_bin, found_from, found_to, found_above, found_count, draw_warp;
     uint32_t list_n, hits_n;
     float bound;
@@ -213,7 +226,7 @@ struct alignas(16) CutShared {
     float ch, cl, low_by, min_hi, min_lo;
 };
 // (read and cleared 16 bytes at a time, like the pieces' keys behind the struct)
-static_assert(sizeof(CutShared) % 16 == 0 && offsetof(CutShared, list) % 16 == 0 && offsetof(CutShared, count) % 16 == 0, "alignment");
+static_assert(sizeof(CutShared) % 16 == 0 && offsetof(CutShared, list) % 16 == 0 && offsetof(CutShared, count) % 16 == 0 && offsetof(CutShared, group_max) % 16 == 0, "alignment");
 
 template <bool BF16>
 __device__ __forceinline__ float piece_elem(const uint4& x, int e) {
@@ -355,11 +368,14 @@ __device__ __forceinline__ void append(CutShared* head, u64 place) {
 }
 
 // f(piece) for this CTA's pieces that hold places from `lo` on: it collects them,
-// then its threads take one each.
+// then its threads take one each. Too many to collect: each lane its own, four loads
+// at a time.
 template <bool BF16, class F>
 __device__ __forceinline__ void each_hit(const Row<BF16>& row, u64 lo, F&& f) {
     CutShared& sh = *row.sh;
     const uint32_t lo16 = Row<BF16>::lo16_of(lo);
+    if (threadIdx.x == 0) sh.hits_n = 0;
+    __syncthreads();
     // 8 keys at a time; the keys behind the part's last are 0
     const uint4* keys = reinterpret_cast<const uint4*>(row.keys);
     for (int g = threadIdx.x; g * 8 < row.n_vecs; g += CL_THREADS) {
@@ -376,10 +392,21 @@ __device__ __forceinline__ void each_hit(const Row<BF16>& row, u64 lo, F&& f) {
     }
     __syncthreads();
     if (sh.hits_n <= CL_HITS) {
-        for (int i = threadIdx.x; i < (int)sh.hits_n; i += CL_THREADS) f((int)sh.hits[i]);
+        for (int i = threadIdx.x; i < (int)sh.hits_n; i += CL_THREADS) f((int)sh.hits[i], row.load((int)sh.hits[i]));
     } else {
-        for (int v = row.v0 + row.lane; v < row.v1; v += 32)
-            if (row.keys[v] >= lo16) f(v);
+        constexpr int U = 4;
+        for (int v = row.v0 + row.lane; v < row.v1; v += 32 * U) {
+            uint4 x[U];
+            bool on[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                on[q] = v + 32 * q < row.v1 && row.keys[v + 32 * q] >= lo16;
+                if (on[q]) x[q] = row.load(v + 32 * q);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (on[q]) f(v + 32 * q, x[q]);
+        }
     }
 }
 
@@ -389,8 +416,7 @@ __device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi)
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     CutShared* head = row.of(&sh, 0);
-    each_hit(row, lo, [&](int v) {
-        const uint4 x = row.load(v);
+    each_hit(row, lo, [&](int v, const uint4& x) {
         const int i0 = row.index(v);
 #pragma unroll
         for (int e = 0; e < R::E; ++e) {
@@ -399,9 +425,7 @@ __device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi)
         }
     });
     row.sync();
-    const uint32_t n = head->list_n;
-    if (threadIdx.x == 0) sh.hits_n = 0;
-    return n;
+    return head->list_n;
 }
 
 // The first index of the row's largest element, whose key is lo's.
@@ -409,8 +433,7 @@ template <bool BF16>
 __device__ __forceinline__ int first_largest(const Row<BF16>& row, u64 lo) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
-    each_hit(row, lo, [&](int v) {
-        const uint4 x = row.load(v);
+    each_hit(row, lo, [&](int v, const uint4& x) {
         int first = INT32_MAX;
 #pragma unroll
         for (int e = R::E - 1; e >= 0; --e)
@@ -423,47 +446,6 @@ __device__ __forceinline__ int first_largest(const Row<BF16>& row, u64 lo) {
     int first = INT32_MAX;
     for (int c = 0; c < row.CS; ++c) first = min(first, sh.firsts[c]);
     return first;
-}
-
-// Sorts the first n entries of the list, descending, by this CTA: few by counting
-// what is larger (4 lanes per entry), more by a bitonic network in shared memory,
-// whose steps over up to 64 neighbours stay within a warp.
-__device__ __noinline__ void sort_list(u64* list, int n) {
-    const int tid = threadIdx.x;
-    if (n <= CL_THREADS / 4) {
-        const int i = tid >> 2;
-        u64 mine = 0;
-        int before = 0;
-        if (i < n) {
-            mine = list[i];
-            for (int j = tid & 3; j < n; j += 4) before += list[j] > mine;
-        }
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
-        __syncthreads();
-        if (i < n && (tid & 3) == 0) list[before] = mine;
-        __syncthreads();
-        return;
-    }
-    int size = 256;
-    while (size < n) size <<= 1;
-    for (int i = n + tid; i < size; i += CL_THREADS) list[i] = 0;
-    for (int block = 2; block <= size; block <<= 1) {
-        for (int stride = block >> 1; stride > 0; stride >>= 1) {
-            if (stride >= 32 || stride == block >> 1) __syncthreads();
-            else __syncwarp();
-            for (int p = tid; p < size / 2; p += CL_THREADS) {
-                const int a = 2 * p - (p & (stride - 1)), b = a + stride;
-                const u64 x = list[a], y = list[b];
-                const bool down = (a & block) == 0;
-                if ((x < y) == down) {
-                    list[a] = y;
-                    list[b] = x;
-                }
-            }
-        }
-    }
-    __syncthreads();
 }
 
 // Inclusive sums over the CTA's threads.
@@ -481,6 +463,93 @@ __device__ __forceinline__ N block_scan(N v, N* warp_sums, int lane, int warp, N
         total += t;
     }
     return v;
+}
+
+// Sorts the first n entries of the list, descending, by this CTA; they lie in [lo,
+// hi]. Few: by counting what is larger, 4 lanes per entry. More: into 1024 buckets
+// of equal width, and within a bucket by counting. Where that leaves many in a
+// bucket (equal logits, say): by a bitonic network in shared memory, whose steps
+// over up to 64 neighbours stay within a warp. (1060 entries: 2 us by buckets,
+// 10 by the network.)
+__device__ __noinline__ void sort_list(CutShared& sh, int n, u64 lo, u64 hi) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    u64* list = sh.list;
+    if (n <= CL_THREADS / 4) {
+        const int i = tid >> 2;
+        u64 mine = 0;
+        int before = 0;
+        if (i < n) {
+            mine = list[i];
+            for (int j = tid & 3; j < n; j += 4) before += list[j] > mine;
+        }
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
+        __syncthreads();
+        if (i < n && (tid & 3) == 0) list[before] = mine;
+        __syncthreads();
+        return;
+    }
+    constexpr int PER = CL_LIST / CL_THREADS, BUCKETS = 2 * CL_THREADS, MOST = 64;
+    const int shift = max(0, 54 - __clzll((long long)(hi - lo)));
+    const auto bucket = [&](u64 x) { return BUCKETS - 1 - (int)min((max(x, lo) - lo) >> shift, (u64)(BUCKETS - 1)); };
+    uint2* counts = reinterpret_cast<uint2*>(sh.count);
+    counts[tid] = make_uint2(0, 0);
+    __syncthreads();
+    u64 x[PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int i = tid + q * CL_THREADS;
+        if (i >= n) continue;
+        x[q] = list[i];
+        atomicAdd(&sh.count[bucket(x[q])], 1u);
+    }
+    __syncthreads();
+    const uint2 mine = counts[tid];
+    uint32_t all;
+    const uint32_t before = block_scan(mine.x + mine.y, sh.warp_count, lane, warp, all) - mine.x - mine.y;
+    if (!__syncthreads_or(mine.x > MOST || mine.y > MOST)) {
+        counts[tid] = make_uint2(before, before + mine.x);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (tid + q * CL_THREADS < n) list[atomicAdd(&sh.count[bucket(x[q])], 1u)] = x[q];
+        __syncthreads();
+        // a bucket's count is now where it ends
+        uint32_t to[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            if (tid + q * CL_THREADS >= n) continue;
+            const int b = bucket(x[q]);
+            const uint32_t first = b > 0 ? sh.count[b - 1] : 0;
+            to[q] = first;
+            for (uint32_t j = first; j < sh.count[b]; ++j) to[q] += list[j] > x[q];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (tid + q * CL_THREADS < n) list[to[q]] = x[q];
+        __syncthreads();
+        return;
+    }
+    int size = 256;
+    while (size < n) size <<= 1;
+    for (int i = n + tid; i < size; i += CL_THREADS) list[i] = 0;
+    for (int block = 2; block <= size; block <<= 1) {
+        for (int stride = block >> 1; stride > 0; stride >>= 1) {
+            if (stride >= 32 || stride == block >> 1) __syncthreads();
+            else __syncwarp();
+            for (int p = tid; p < size / 2; p += CL_THREADS) {
+                const int a = 2 * p - (p & (stride - 1)), b = a + stride;
+                const u64 y = list[a], z = list[b];
+                const bool down = (a & block) == 0;
+                if ((y < z) == down) {
+                    list[a] = z;
+                    list[b] = y;
+                }
+            }
+        }
+    }
+    __syncthreads();
 }
 
 // The first bin, from 0 on, in which the sum over the bins of all CTAs reaches
@@ -573,10 +642,9 @@ __device__ __forceinline__ const ExpEntry* copy_table(const Row<BF16>& row) {
 }
 
 // Sums of the weights at or above `cut`, this warp's into the first CTA's
-// part_mass and the total to every thread. others(x, v): what else is to be done
-// with each piece.
-template <bool BF16, class F>
-__device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut, F&& others) {
+// part_mass and the total to every thread.
+template <bool BF16>
+__device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     u64 m = 0;
@@ -603,7 +671,6 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut, F&& othe
                     sum.add(z0 >= from ? z0 : row.s.low, z1 >= from ? z1 : row.s.low, row.s, copy);
                 }
             }
-            others(x, v);
         });
         m += sum.total();
     } else {
@@ -614,7 +681,6 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut, F&& othe
                 const float z = piece_elem<BF16>(x, e);
                 if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s, row.sh->exp);
             }
-            others(x, v);
         });
     }
     m = warp_sum(m);
@@ -630,7 +696,7 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut, F&& othe
 // (BY_MASS false) or the weight `goal` is reached from above, given what lies
 // above hi. The range becomes that bin.
 template <bool BF16, bool BY_MASS>
-__device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& hi, uint32_t& above, u64& mass_above, uint32_t k, double goal) {
+__device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& hi, uint32_t& above, u64& mass_above, uint32_t k, u64 goal) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     u64* mass = sh.list;
@@ -705,8 +771,8 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
             if (i >= per) continue;
-            const bool reached = BY_MASS ? (double)(m + m_of[i]) >= goal : c + c_of[i] >= k;
-            const bool before = BY_MASS ? (c != 0 && (double)m >= goal) : c >= k;
+            const bool reached = BY_MASS ? m + m_of[i] >= goal : c + c_of[i] >= k;
+            const bool before = BY_MASS ? (c != 0 && m >= goal) : c >= k;
             if (c_of[i] != 0 && reached && !before) {
                 row.each_cta([&](CutShared* o) {
                     o->found_bin = (uint32_t)(b0 + i);
@@ -730,18 +796,22 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
     return n;
 }
 
-// In the sorted list of n places below `above` others of weight mass_above: the
-// first one with which the count or the weight is reached, or 0. This CTA's
-// threads; list_w: scratch for nothing but the scan.
+// The fewest units that are p of `total`, to every thread of the CTA.
+__device__ __forceinline__ u64 goal_of(CutShared& sh, float p, u64 total) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.goal = (u64)ceil((double)p * (double)total);
+    __syncthreads();
+    return sh.goal;
+}
+
+// In the sorted list of n places, below others (if `any`) of weight mass_above: the
+// one with which the weight is reached, or 0. A goal known to lie from `goal` to
+// goal_hi only has to be reached by the same place throughout. This CTA's threads.
 template <bool BF16>
-__device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool by_mass, uint32_t above, u64 mass_above, uint32_t k, double goal) {
+__device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool any, u64 mass_above, u64 goal, u64 goal_hi) {
     CutShared& sh = *row.sh;
     const int tid = threadIdx.x;
-    if (!by_mass) {
-        const int at = (int)k - 1 - (int)above;
-        return at >= 0 && at < n ? sh.list[at] : 0;
-    }
-    if (above != 0 && (double)mass_above >= goal) return 0;
+    if (any && mass_above >= goal) return 0;
     if (tid == 0) sh.found_place = 0;
     u64 carry = mass_above;
     for (int base = 0; base < n; base += CL_THREADS) {
@@ -749,19 +819,35 @@ __device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool b
         const u64 p = i < n ? sh.list[i] : 0, w = i < n ? weight(key_value<BF16>(place_key(p)), row.s, row.sh->exp) : 0;
         u64 total;
         const u64 incl = carry + block_scan(w, sh.warp_mass, row.lane, row.warp, total);
-        const u64 before = incl - w;
-        const bool first = above == 0 && i == 0;
-        if (i < n && (double)incl >= goal && (first || (double)before < goal)) sh.found_place = p;
+        const bool first = !any && i == 0;
+        if (i < n && incl >= goal_hi && (first || incl - w < goal)) sh.found_place = p;
         carry += total;
     }
     __syncthreads();
     return sh.found_place;
 }
 
+// The groups' n-th largest maximum, from 0 on.
+__device__ __forceinline__ float nth_group(CutShared& sh, int groups, int n) {
+    const int tid = threadIdx.x;
+    if (tid < groups) {
+        const float mine = sh.group_max[tid];
+        int before = 0;
+        for (int w = 0; w < groups; w += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(sh.group_max + w);
+            before += (o.x > mine || (o.x == mine && w < tid)) + (o.y > mine || (o.y == mine && w + 1 < tid)) +
+                      (o.z > mine || (o.z == mine && w + 2 < tid)) + (o.w > mine || (o.w == mine && w + 3 < tid));
+        }
+        if (before == n) sh.bound = mine;
+    }
+    __syncthreads();
+    return sh.bound;
+}
+
 // 4. The place of the last element that a cut keeps, exactly, in [lo, hi]: the
 // range narrows until what is left fits the list, where it is picked.
 template <bool BF16, bool BY_MASS>
-__device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32_t k, double goal) {
+__device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32_t k, u64 goal) {
     CutShared& sh = *row.sh;
     uint32_t above = 0, left = CL_LIST + 1;
     u64 mass_above = 0;
@@ -770,8 +856,14 @@ __device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32
     row.sync();
     const int n = (int)min(gather(row, lo, hi), (uint32_t)CL_LIST);
     if (row.rank == 0) {
-        sort_list(sh.list, n);
-        u64 place = reach_in_list(row, n, BY_MASS, above, mass_above, k, goal);
+        sort_list(sh, n, lo, hi);
+        u64 place = 0;
+        if constexpr (BY_MASS) {
+            place = reach_in_list(row, n, above != 0, mass_above, goal, goal);
+        } else {
+            const int at = (int)k - 1 - (int)above;
+            place = at >= 0 && at < n ? sh.list[at] : 0;
+        }
         place = place ? place : lo;
         __syncthreads();
         if (threadIdx.x == 0) row.each_cta([&](CutShared* o) { o->found_place = place; });
@@ -819,12 +911,14 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
         sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(key_value<BF16>(place_key(p)), row.s, row.sh->exp);
     }
     __syncthreads();
-    if (n > 1) sort_list(sh.list, n);  // (descending reversed index)
+    if (n > 1) sort_list(sh, n, 0, ~0ull >> 1);  // (descending reversed index)
     u64 total = 0;
     for (int i = tid; i < n; i += CL_THREADS) total += sh.list[i] & W;
     u64 all;
     block_scan(total, sh.warp_mass, row.lane, row.warp, all);
-    const u64 target = draw_target(u, all);
+    if (tid == 0) sh.goal = draw_target(u, all);
+    __syncthreads();
+    const u64 target = sh.goal;
     u64 carry = 0;
     for (int base = 0; base < n; base += CL_THREADS) {
         const int i = base + tid;
@@ -906,7 +1000,7 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
 // 3. Top-p alone. Returns the place of the last kept element and leaves the sums
 // of the warps' parts at or above it in the first CTA's part_mass.
 template <bool BF16>
-__device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float T, u64 highest) {
+__device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float T, u64 highest, float about) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     const RowScale& s = row.s;
@@ -917,13 +1011,14 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     const float span_log = __logf((float)row.V / fmaxf(1.0f - top_p, 1e-9f)) + 0.01f;
     const float span = span_log * T, to_bin = (float)CL_BINS / span, bin_log = span_log / (float)CL_BINS;
     clear_bins(row);
-    // All weights, and the histogram: CL_SHARE per element at a bin's upper edge, less
-    // towards its lower one as the weight falls. A logit's bin and its place in it
-    // come from the low bits of a float that 2^23 was added to.
+    // The histogram: CL_SHARE per element at a bin's upper edge, less towards its
+    // lower one as the weight falls. A logit's bin and its place in it come from the
+    // low bits of a float that 2^23 was added to.
     const float fine = 128.0f * to_bin, shifted = __fmaf_rn(s.top, fine, 8388608.0f), last = 8388608.0f + 128.0f * CL_BINS - 1.0f;
     const uint32_t fall = (uint32_t)(bin_log * (float)CL_SHARE * 2.0f + 0.5f);
     const bool flat = !(fabsf(s.top * fine) < 4194304.0f);  // (then shifted has no room)
-    const u64 m = sum_above(row, CL_LOWEST, [&](const uint4& x, int) {
+    const float least = __fsub_rn(s.top, span * 1.0001f);
+    row.each_piece(max(CL_LOWEST, (u64)key_of<BF16>(least) << CL_INDEX_BITS), [&](const uint4& x, int) {
 #pragma unroll
         for (int e = 0; e < R::E; ++e) {
             const float z = piece_elem<BF16>(x, e);
@@ -933,49 +1028,78 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
             atomicAdd(&sh.count[at >> 7], CL_SHARE - (((at & 127u) * fall + 128u) >> 8));
         }
     });
-    const double goal = (double)top_p * (double)m;
-    find_bin(row, (float)(goal * (1.0 / (double)(1ull << CL_UNIT))), bin_log * 1.4426950408889634f, CL_NEAR);
+    find_bin(row, about * top_p * 0x1p-44f, bin_log * 1.4426950408889634f, CL_NEAR);
     const int bin0 = (int)sh.found_from, bin1 = (int)sh.found_to;
     u64 place = 0;
     bool any_above = false;
+    u64 goal;
     {
-        // the sum above the first of these bins, and what lies in them to the list
+        // the sum of all weights and of those above the first of these bins, exactly,
+        // and what lies in them to the list
         const float z_hi = bin0 > 0 ? __fsub_rn(s.top, (float)bin0 / to_bin) : INFINITY;
         const float z_lo = key_value<BF16>(key_of<BF16>(__fsub_rn(s.top, (float)(bin1 + 1) / to_bin)));
         const u64 over = bin0 > 0 ? (u64)(key_of<BF16>(z_hi) + 1) << CL_INDEX_BITS : ~0ull;  // above z_hi
         const u64 lo = max(CL_LOWEST, (u64)key_of<BF16>(z_lo) << CL_INDEX_BITS);
         CutShared* head = row.of(&sh, 0);
         any_above = over <= highest;
-        const ExpEntry* copy = sh.copies + (tid & (CL_COPIES - 1));
-        WeightSum sum;
-        u64 exact = 0;
+        const ExpEntry* copy = copy_table(row);
         const bool fast = s.low == s.low;
         const float from = bin0 > 0 ? fmaxf(key_value<BF16>(key_of<BF16>(z_hi) + 1), fast ? s.low : -INFINITY) : INFINITY;
-        row.each_piece(lo, [&](const uint4& x, int v) {
-            const int i0 = row.index(v);
+        u64 all = 0, above = 0;
+        const auto to_list = [&](float z, int i) {
+            if (z >= z_lo && z < from) append(head, place_of(key_of<BF16>(z), i));
+        };
+        if (fast) {
+            WeightSum sum, upper;
+            row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
+                const int i0 = row.index(v);
 #pragma unroll
-            for (int e = 0; e < R::E; e += 2) {
-                const float z[2] = {piece_elem<BF16>(x, e), piece_elem<BF16>(x, e + 1)};
-                const bool up0 = z[0] >= from, up1 = z[1] >= from;
-                if (up0 || up1) {
-                    if (fast) sum.add(up0 ? z[0] : s.low, up1 ? z[1] : s.low, s, copy);
-                    else exact += (up0 ? weight(z[0], s, sh.exp) : 0) + (up1 ? weight(z[1], s, sh.exp) : 0);
+                for (int e = 0; e < R::E; e += 2) {
+                    const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
+                    f32x2 a, rest;
+                    WeightSum::pair(z0 >= s.low ? z0 : s.low, z1 >= s.low ? z1 : s.low, s, copy, a, rest);
+                    sum.add(a, rest);
+                    float a0, a1, r0, r1;
+                    unpack2(a, a0, a1);
+                    unpack2(rest, r0, r1);
+                    const bool up0 = z0 >= from, up1 = z1 >= from;
+                    upper.add(pack2(up0 ? a0 : 0.0f, up1 ? a1 : 0.0f), pack2(up0 ? r0 : 0.0f, up1 ? r1 : 0.0f));
+                    to_list(z0, i0 + e);
+                    to_list(z1, i0 + e + 1);
                 }
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (z[q] >= z_lo && z[q] < from) append(head, place_of(key_of<BF16>(z[q]), i0 + e + q));
-            }
-        });
-        const u64 mine = warp_sum(exact + sum.total());
-        if (row.lane == 0) head->part_mass[row.rank * CL_WARPS + row.warp] = mine;
+            });
+            all = sum.total();
+            above = upper.total();
+        } else {
+            row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
+                const int i0 = row.index(v);
+#pragma unroll 1
+                for (int e = 0; e < R::E; ++e) {
+                    const float z = piece_elem<BF16>(x, e);
+                    const u64 w = weight(z, s, sh.exp);
+                    all += w;
+                    above += z >= from ? w : 0;
+                    to_list(z, i0 + e);
+                }
+            });
+        }
+        all = warp_sum(all);
+        above = warp_sum(above);
+        if (row.lane == 0) {
+            head->part_mass[row.rank * CL_WARPS + row.warp] = above;
+            head->part_all[row.rank * CL_WARPS + row.warp] = all;
+        }
         row.sync();
+        all = 0;
+        for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) all += head->part_all[w];
+        goal = goal_of(sh, top_p, warp_sum(all));
         if (row.rank == 0) {
             const int n = (int)sh.list_n;
             u64 mass_above = 0, place = 0;
             for (int w = 0; w < row.CS * CL_WARPS; ++w) mass_above += sh.part_mass[w];
             if (n <= CL_LIST) {
-                sort_list(sh.list, n);
-                place = reach_in_list(row, n, true, any_above, mass_above, 0, goal);
+                sort_list(sh, n, lo, highest);
+                place = reach_in_list(row, n, any_above, mass_above, goal, goal);
                 // what of the list is kept joins its warps' sums
                 if (place) {
                     const int lead = (int)((reinterpret_cast<uintptr_t>(row.src) & 15) / R::ES);
@@ -998,7 +1122,91 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     if (place == 0) {
         // more equal logits than the list takes, or a border that the histogram missed
         place = find_cut<BF16, true>(row, CL_LOWEST, highest, 0, goal);
-        sum_above(row, place, [](const uint4&, int) {});
+        sum_above(row, place);
+    }
+    return place;
+}
+
+// 3a. Top-p alone, first try: a few hundred of the row's largest go to the list with
+// their exact weights, the others' are summed in fp32, to 2^-15 of their sum (an
+// exponent is off by 2^-23 of itself, at most 2^-17 for weights that matter, a
+// thread's sums of at most 132 terms by 2^-17). Where the place is the same whatever that error, it is
+// found: so for rows whose mass lies with few tokens, in one cheap pass instead of
+// the exact ones. Else 0, and the list is empty. about: the sum of all weights in
+// their unit.
+template <bool BF16>
+__device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int groups, u64 highest, float& about) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    const float edge = nth_group(sh, groups, groups * 3 / 4);
+    // (what is -inf has no weight)
+    const u64 lo = (u64)max(key_of<BF16>(edge), key_of<BF16>(-INFINITY) + 1) << CL_INDEX_BITS;
+    const float c = row.s.ch * (1.0f / (float)CL_EXP), top = row.s.top;
+    const uint32_t lo16 = R::lo16_of(lo);
+    f32x2 sum = pack2(0.0f, 0.0f), large = sum;
+    const f32x2 cc = pack2(c, c), minus_top = pack2(-top, -top);
+    row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
+        const bool some = row.keys[v] >= lo16 || row.partial(v);  // (padding is not below the edge either)
+        f32x2 part = pack2(0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < R::E; e += 2) {
+            const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
+            const f32x2 w = ex2x2(mul2(add2(pack2(z0, z1), minus_top), cc));
+            if (some) {
+                float w0, w1;
+                unpack2(w, w0, w1);
+                part = add2(part, pack2(z0 < edge ? w0 : 0.0f, z1 < edge ? w1 : 0.0f));
+                large = add2(large, pack2(z0 >= edge ? w0 : 0.0f, z1 >= edge ? w1 : 0.0f));
+            } else {
+                part = add2(part, w);
+            }
+        }
+        sum = add2(sum, part);
+    });
+    float s0, s1, l0, l1;
+    unpack2(sum, s0, s1);
+    unpack2(large, l0, l1);
+    u64 others = warp_sum((u64)__float2ll_rn((s0 + s1) * 0x1p44f)), listed = warp_sum((u64)__float2ll_rn((l0 + l1) * 0x1p44f));
+    if (row.lane < row.CS) {
+        CutShared* o = row.of(&sh, row.lane);
+        o->part_mass[row.rank * CL_WARPS + row.warp] = others;
+        o->part_all[row.rank * CL_WARPS + row.warp] = listed;
+    }
+    row.sync();
+    others = listed = 0;
+    for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) {
+        others += sh.part_mass[w];
+        listed += sh.part_all[w];
+    }
+    others = warp_sum(others);
+    listed = warp_sum(listed);
+    about = (float)(others + listed);
+    if ((float)listed < about * top_p) return 0;  // (what is near is left to the exact passes)
+    const uint32_t n = gather(row, lo, highest);
+    row.arrive();
+    if (row.CS == 1) __syncthreads();
+    if (row.rank == 0) {
+        u64 place = 0;
+        if (n <= CL_LIST) {
+            sort_list(sh, (int)n, lo, highest);
+            u64 m = 0;
+            for (int i = threadIdx.x; i < (int)n; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), row.s, sh.exp);
+            block_scan(m, sh.warp_mass, row.lane, row.warp, listed);
+            // (2^18: the units to which the warps' sums were rounded, and more)
+            const u64 error = (others >> 15) + (1ull << 18);
+            const u64 goal = goal_of(sh, top_p, listed + others - min(others, error)), goal_hi = goal_of(sh, top_p, listed + others + error);
+            place = reach_in_list(row, (int)n, false, 0, goal, goal_hi);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) row.each_cta([&](CutShared* o) { o->found_place = place; });
+    }
+    row.wait();
+    row.sync();
+    const u64 place = sh.found_place;
+    if (place == 0) {
+        row.sync();  // everyone has read it
+        if (threadIdx.x == 0) sh.list_n = 0;
+        __syncthreads();
     }
     return place;
 }
@@ -1036,7 +1244,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     row.full0 = row.first < 0 ? 1 : 0;
     row.full1 = row.first + row.n_vecs * R::E > P.V ? row.n_vecs - 1 : row.n_vecs;
     if (tid == 0) {
-        sh.list_n = sh.hits_n = 0;
+        sh.list_n = 0;
         sh.first = INT32_MAX;
     }
     if (tid < CL_EXP) sh.exp[tid] = g_exp_table.e[tid];
@@ -1096,25 +1304,28 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             row.keys[last] = R::piece_key(load_part<BF16>(row.src, P.V, row.index(last), R::MINUS_INF), most);
         top = BF16 ? max_nan(bf16_lo(most), bf16_hi(most)) : __uint_as_float(most);
     }
-    float wmax = top, least = top > -INFINITY ? top : INFINITY;
+    // The maxima of groups of lanes: so many that enough lie above what is looked for
+    // and the smallest part of a row is between (a quarter more groups than k, all
+    // that there is room for in top-p's first try).
+    const int warps = CS * CL_WARPS, wanted = k == 1 ? 1 : k < P.V ? (k < CL_GROUPS ? k + k / 4 : CL_GROUPS) : CL_GROUPS;
+    int per_warp = 1;
+    while (warps * per_warp < wanted && warps * per_warp < CL_GROUPS) per_warp *= 2;
+    const int groups = warps * per_warp, width = 32 / per_warp;
+    float least = top > -INFINITY ? top : INFINITY, group = top;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        wmax = max_nan(wmax, __shfl_xor_sync(0xFFFFFFFFu, wmax, o));
+        if (o < width) group = max_nan(group, __shfl_xor_sync(0xFFFFFFFFu, group, o));
         least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
     }
     cluster_wait_started();
-    if (lane < CS) {
-        row.of(sh.warp_max, lane)[rank * CL_WARPS + warp] = wmax;
-        row.of(sh.lane_min, lane)[rank * CL_WARPS + warp] = least;
-    }
+    if (lane < CS) row.of(sh.lane_min, lane)[rank * CL_WARPS + warp] = least;
+    if (lane % width == 0)
+        for (int c = 0; c < CS; ++c) row.of(sh.group_max, c)[(rank * CL_WARPS + warp) * per_warp + lane / width] = group;
     row.sync();
-    const int warps = CS * CL_WARPS;
     row.s.top = -INFINITY;
     least = INFINITY;
-    for (int w = lane; w < warps; w += 32) {
-        row.s.top = max_nan(row.s.top, sh.warp_max[w]);
-        least = fminf(least, sh.lane_min[w]);
-    }
+    for (int w = lane; w < groups; w += 32) row.s.top = max_nan(row.s.top, sh.group_max[w]);
+    for (int w = lane; w < warps; w += 32) least = fminf(least, sh.lane_min[w]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         row.s.top = max_nan(row.s.top, __shfl_xor_sync(0xFFFFFFFFu, row.s.top, o));
@@ -1138,6 +1349,11 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         row.s.ch = sh.ch;
         row.s.cl = sh.cl;
         row.s.low = fabsf(s.top * s.ch) < 0x1p21f ? s.top - sh.low_by : __int_as_float(0x7fc00000);
+        {
+            const float y = __fmul_rn(s.top, s.ch), whole = rintf(y);
+            row.s.shift = 12582912.0f - whole;
+            row.s.frac = __fadd_rn(__fsub_rn(y, whole), __fmaf_rn(s.top, s.cl, __fmaf_rn(s.top, s.ch, -y)));
+        }
         const u64 highest = (u64)key_of<BF16>(s.top) << CL_INDEX_BITS | CL_INDEX_MASK;
         // min-p: z >= max + T ln(min_p)
         if (min_p > 0.0f && T != 0.0f) {
@@ -1165,19 +1381,8 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         } else if (by_k) {
             // 2. a bound on the k-th largest
             u64 bound = CL_LOWEST;
-            if (k <= warps) {
-                // the k-th largest of the warps' maxima
-                if (tid < warps) {
-                    const float mine = sh.warp_max[tid];
-                    int before = 0;
-                    for (int w = 0; w < warps; ++w) {
-                        const float other = sh.warp_max[w];
-                        before += other > mine || (other == mine && w < tid);
-                    }
-                    if (before == k - 1) sh.bound = mine;
-                }
-                __syncthreads();
-                bound = max(bound, (u64)key_of<BF16>(sh.bound) << CL_INDEX_BITS);
+            if (k <= groups) {
+                bound = max(bound, (u64)key_of<BF16>(nth_group(sh, groups, k - 1)) << CL_INDEX_BITS);
             } else if (least < s.top) {
                 // that of the pieces', by a histogram between the lanes' smallest
                 // maximum and the row's
@@ -1209,7 +1414,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             bool listed = n <= CL_LIST;
             if (!listed) {
                 row.sync();  // everyone has read the list's length
-                const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0.0);
+                const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0);
                 if (k <= CL_LIST) {
                     if (tid == 0) sh.list_n = 0;
                     row.sync();
@@ -1217,9 +1422,9 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                     listed = true;
                 } else {
                     if (by_p) {
-                        const u64 mass = sum_above(row, cut_k, [](const uint4&, int) {});
+                        const u64 mass = sum_above(row, cut_k);
                         row.sync();
-                        cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, (double)top_p * (double)mass));
+                        cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, goal_of(sh, top_p, mass)));
                     }
                     cut = max(cut, cut_k);
                 }
@@ -1231,14 +1436,15 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                 if (CS == 1) __syncthreads();
                 if (rank == 0) {
                     const int all = min((int)n, CL_LIST);
-                    sort_list(sh.list, all);
+                    sort_list(sh, all, bound, highest);
                     const int of_k = min(all, k);
                     u64 last = of_k > 0 ? sh.list[of_k - 1] : 0;
                     if (by_p) {
                         u64 m = 0, total;
                         for (int i = tid; i < of_k; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), s, row.sh->exp);
                         block_scan(m, sh.warp_mass, lane, warp, total);
-                        last = max(last, reach_in_list(row, of_k, true, 0, 0, 0, (double)top_p * (double)total));
+                        const u64 goal = goal_of(sh, top_p, total);
+                        last = max(last, reach_in_list(row, of_k, false, 0, goal, goal));
                     }
                     last = max(last, cut);
                     if constexpr (DRAW) {
@@ -1259,14 +1465,29 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                 cut = sh.found_place;
             }
         } else if (by_p) {
-            const u64 cut_p = cut_by_mass(row, top_p, T, highest);
-            summed = cut_p >= cut;
-            cut = max(cut, cut_p);
+            float about;  // the sum of all weights, nearly
+            u64 cut_p = cut_near_top(row, top_p, groups, highest, about);
+            if (cut_p) {
+                cut = max(cut, cut_p);
+                if constexpr (DRAW) {
+                    if (rank == 0) {
+                        uint32_t kept = 0, total;
+                        for (int i = tid; i < (int)sh.list_n; i += CL_THREADS) kept += sh.list[i] >= cut;
+                        block_scan(kept, sh.warp_count, lane, warp, total);
+                        draw_list(P, row, at_row, u, (int)total);
+                    }
+                    return;
+                }
+            } else {
+                cut_p = cut_by_mass(row, top_p, T, highest, about);
+                summed = cut_p >= cut;
+                cut = max(cut, cut_p);
+            }
         }
         if constexpr (DRAW) {
             if (!summed) {
                 row.sync();
-                sum_above(row, cut, [](const uint4&, int) {});
+                sum_above(row, cut);
             }
             draw_parts(P, row, at_row, u, cut);
             return;
@@ -1277,38 +1498,42 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         const bool valid = row_ok && settings_ok;
         char* out = P.out + b * P.out_seq_bytes + r * P.out_row_bytes;
         const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (uintptr_t)(lead * R::ES);
-        const uint32_t lo16 = valid ? R::lo16_of(cut) : 0;
         constexpr uint32_t NONE = BF16 ? 0xFF80FF80u : 0xFF800000u;
         uint32_t kept = 0;
-        for (int v = row.v0 + lane; v < row.v1; v += 32) {
+        const auto put = [&](int v, const uint4& x) {
             const int i0 = row.index(v);
-            uint4 x = make_uint4(NONE, NONE, NONE, NONE);
-            if (!valid || row.keys[v] >= lo16) {
-                x = row.load(v);
-                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-                if (valid) {
-#pragma unroll
-                    for (int e = 0; e < R::E; ++e) {
-                        if (place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e) >= cut) {
-                            ++kept;
-                        } else {
-                            if constexpr (BF16) w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | 0xFF800000u : (w[e / 2] & 0xFFFF0000u) | 0xFF80u;
-                            else w[e] = 0xFF800000u;
-                        }
-                    }
-                }
-            }
             if (same && !row.partial(v)) {
                 *reinterpret_cast<uint4*>(out + (int64_t)i0 * R::ES) = x;
-            } else {
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                return;
+            }
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < R::E; ++e) {
+                if (i0 + e < 0 || i0 + e >= P.V) continue;
+                if constexpr (BF16) reinterpret_cast<uint16_t*>(out)[i0 + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+                else reinterpret_cast<uint32_t*>(out)[i0 + e] = w[e];
+            }
+        };
+        if (!valid) {
+            for (int v = row.v0 + lane; v < row.v1; v += 32) put(v, row.load(v));
+        } else {
+            const uint32_t lo16 = R::lo16_of(cut);
+            for (int v = row.v0 + lane; v < row.v1; v += 32)
+                if (row.keys[v] < lo16) put(v, make_uint4(NONE, NONE, NONE, NONE));
+            each_hit(row, cut, [&](int v, uint4 x) {
+                const int i0 = row.index(v);
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < R::E; ++e) {
-                    if (i0 + e < 0 || i0 + e >= P.V) continue;
-                    if constexpr (BF16) reinterpret_cast<uint16_t*>(out)[i0 + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
-                    else reinterpret_cast<uint32_t*>(out)[i0 + e] = w[e];
+                    if (place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e) >= cut) {
+                        ++kept;
+                    } else {
+                        if constexpr (BF16) w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | 0xFF800000u : (w[e / 2] & 0xFFFF0000u) | 0xFF80u;
+                        else w[e] = 0xFF800000u;
+                    }
                 }
-            }
+                put(v, make_uint4(w[0], w[1], w[2], w[3]));
+            });
         }
         if (P.n_kept && valid) {
             kept = __reduce_add_sync(0xFFFFFFFFu, kept);
