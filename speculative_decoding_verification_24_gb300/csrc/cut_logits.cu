@@ -220,7 +220,16 @@ struct alignas(16) CutShared {
     uint32_t found_bin, found_from, found_to, found_above, found_count, draw_warp;
     uint32_t list_n, hits_n;
     float bound;
-    int first, firsts[CL_MAX_CS];
+    int first_largest, firsts[CL_MAX_CS];
+    // This CTA's part of the row. (Here and not in every thread's registers: 64 are
+    // what two CTAs per SM leave a thread, and the sums' loops need them.)
+    const char* src;       // the row's first element
+    const uint4* base;     // the part's pieces in memory
+    int V, first;          // index in the row of the part's first element (negative: padding)
+    int n_vecs, slice, run;  // pieces of the part; per CTA and per warp
+    int full0, full1;      // those that lie in the row as a whole
+    int CS, rank;
+    RowScale s;
     // of the row's settings (formed by one thread: the units for doubles are few)
     double inv_t;
     float ch, cl, low_by, min_hi, min_lo;
@@ -271,50 +280,51 @@ template <bool BF16>
 struct Row {
     static constexpr int E = BF16 ? 8 : 4;
     static constexpr int ES = BF16 ? 2 : 4;
-    const char* src;       // the row's first element
-    int V, first;          // index in the row of the part's first element (negative: padding)
-    int n_vecs, v0, v1;    // pieces of the part, this warp's
-    int slice, run;        // pieces per CTA and per warp
-    uint16_t* keys;        // shared memory: a piece's largest key, upper 16 bits
     CutShared* sh;
-    RowScale s;
-    int CS, rank, lane, warp;
+    int lane, warp;
 
-    const uint4* base;     // the part's pieces in memory
-    int full0, full1;      // those that lie in the row as a whole
-
-    __device__ __forceinline__ int index(int v) const { return first + v * E; }
-    __device__ __forceinline__ bool partial(int v) const { return v < full0 || v >= full1; }
-    __device__ __forceinline__ uint4 load_whole(int v) const {
+    __device__ __forceinline__ int CS() const { return sh->CS; }
+    __device__ __forceinline__ int rank() const { return sh->rank; }
+    __device__ __forceinline__ int n_vecs() const { return sh->n_vecs; }
+    __device__ __forceinline__ int v0() const { return min(warp * sh->run, sh->n_vecs); }
+    __device__ __forceinline__ int v1() const { return min((warp + 1) * sh->run, sh->n_vecs); }
+    __device__ __forceinline__ const RowScale& s() const { return sh->s; }
+    // shared memory: a piece's largest key, upper 16 bits
+    __device__ __forceinline__ uint16_t* keys() const { return reinterpret_cast<uint16_t*>(sh + 1); }
+    __device__ __forceinline__ int index(int v) const { return sh->first + v * E; }
+    __device__ __forceinline__ bool partial(int v) const { return v < sh->full0 || v >= sh->full1; }
+    static __device__ __forceinline__ uint4 load_whole(const uint4* at) {
         uint4 x;
         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "l"(base + v)
+                     : "l"(at)
                      : "memory");
         return x;
     }
-    __device__ __forceinline__ uint4 load(int v) const { return partial(v) ? load_part<BF16>(src, V, index(v), NOBODY) : load_whole(v); }
+    __device__ __forceinline__ uint4 load(int v) const {
+        return partial(v) ? load_part<BF16>(sh->src, sh->V, index(v), NOBODY) : load_whole(sh->base + v);
+    }
     // padding that has no place in the order (a negative NaN, key 0)
     static constexpr uint32_t NOBODY = BF16 ? 0xFFFFu : 0xFFFFFFFFu;
     static constexpr uint32_t MINUS_INF = BF16 ? 0xFF80u : 0xFF800000u;
 
     // Every thread of the row's CTAs has got here, and what they wrote is seen.
     __device__ __forceinline__ void sync() const {
-        if (CS == 1) __syncthreads();
+        if (CS() == 1) __syncthreads();
         else cg::this_cluster().sync();
     }
     // The same in two halves: what comes between does not wait for the others.
     __device__ __forceinline__ void arrive() const {
-        if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (CS() > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
     __device__ __forceinline__ void wait() const {
-        if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (CS() > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     template <class X>
-    __device__ __forceinline__ X* of(X* mine, int cta) const { return CS == 1 ? mine : cg::this_cluster().map_shared_rank(mine, cta); }
+    __device__ __forceinline__ X* of(X* mine, int cta) const { return CS() == 1 ? mine : cg::this_cluster().map_shared_rank(mine, cta); }
     template <class F>
     __device__ __forceinline__ void each_cta(F&& f) const {
-        for (int c = 0; c < CS; ++c) f(of(sh, c));
+        for (int c = 0; c < CS(); ++c) f(of(sh, c));
     }
 
     // f(x, v) for this lane's pieces whose key is at least that of `lo`; the next
@@ -322,21 +332,45 @@ struct Row {
     template <class F>
     __device__ __forceinline__ void each_piece(u64 lo, F&& f) const {
         const uint32_t lo16 = lo16_of(lo);
-        int v = v0 + lane;
+        const uint16_t* k = keys();
+        const uint4* from = sh->base;
+        const int end = v1(), whole0 = sh->full0, whole1 = sh->full1;
         const auto next = [&](int at) {
-            while (at < v1 && keys[at] < lo16) at += 32;
+            while (at < end && k[at] < lo16) at += 32;
             return at;
         };
-        v = next(v);
+        const auto get = [&](int v) { return v < whole0 || v >= whole1 ? load_part<BF16>(sh->src, sh->V, index(v), NOBODY) : load_whole(from + v); };
+        int v = next(v0() + lane);
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (v < v1) x = load(v);
-        while (v < v1) {
+        if (v < end) x = get(v);
+        while (v < end) {
             const int n = next(v + 32);
             uint4 y = x;
-            if (n < v1) y = load(n);
+            if (n < end) y = get(n);
             f(x, v);
             x = y;
             v = n;
+        }
+    }
+    // The same for passes that do little with a piece: U loads at a time. (One ahead,
+    // as above, left them waiting for L2: 64 flat rows' top-p 88 us, 70 so.)
+    template <class F>
+    __device__ __forceinline__ void each_piece_quick(u64 lo, F&& f) const {
+        constexpr int U = 8;
+        const uint32_t lo16 = lo16_of(lo);
+        const uint16_t* k = keys();
+        const int end = v1();
+        for (int v = v0() + lane; v < end; v += 32 * U) {
+            uint4 x[U];
+            bool on[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                on[q] = v + 32 * q < end && k[v + 32 * q] >= lo16;
+                if (on[q]) x[q] = load(v + 32 * q);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (on[q]) f(x[q], v + 32 * q);
         }
     }
     // What a piece's key is compared with. (The pieces' keys are of the bits as they
@@ -377,15 +411,15 @@ __device__ __forceinline__ void each_hit(const Row<BF16>& row, u64 lo, F&& f) {
     if (threadIdx.x == 0) sh.hits_n = 0;
     __syncthreads();
     // 8 keys at a time; the keys behind the part's last are 0
-    const uint4* keys = reinterpret_cast<const uint4*>(row.keys);
-    for (int g = threadIdx.x; g * 8 < row.n_vecs; g += CL_THREADS) {
+    const uint4* keys = reinterpret_cast<const uint4*>(row.keys());
+    for (int g = threadIdx.x; g * 8 < row.n_vecs(); g += CL_THREADS) {
         const uint4 k8 = keys[g];
         const uint32_t w[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (((w[i / 2] >> (16 * (i % 2))) & 0xFFFFu) < lo16) continue;
             const int v = g * 8 + i;
-            if (v >= row.n_vecs) continue;
+            if (v >= row.n_vecs()) continue;
             const uint32_t at = atomicAdd(&sh.hits_n, 1u);
             if (at < CL_HITS) sh.hits[at] = (uint32_t)v;
         }
@@ -395,12 +429,12 @@ __device__ __forceinline__ void each_hit(const Row<BF16>& row, u64 lo, F&& f) {
         for (int i = threadIdx.x; i < (int)sh.hits_n; i += CL_THREADS) f((int)sh.hits[i], row.load((int)sh.hits[i]));
     } else {
         constexpr int U = 4;
-        for (int v = row.v0 + row.lane; v < row.v1; v += 32 * U) {
+        for (int v = row.v0() + row.lane; v < row.v1(); v += 32 * U) {
             uint4 x[U];
             bool on[U];
 #pragma unroll
             for (int q = 0; q < U; ++q) {
-                on[q] = v + 32 * q < row.v1 && row.keys[v + 32 * q] >= lo16;
+                on[q] = v + 32 * q < row.v1() && row.keys()[v + 32 * q] >= lo16;
                 if (on[q]) x[q] = row.load(v + 32 * q);
             }
 #pragma unroll
@@ -438,13 +472,13 @@ __device__ __forceinline__ int first_largest(const Row<BF16>& row, u64 lo) {
 #pragma unroll
         for (int e = R::E - 1; e >= 0; --e)
             if (key_of<BF16>(piece_elem<BF16>(x, e)) == place_key(lo)) first = row.index(v) + e;
-        atomicMin(&sh.first, first);
+        atomicMin(&sh.first_largest, first);
     });
     __syncthreads();
-    if (threadIdx.x < row.CS) row.of(sh.firsts, threadIdx.x)[row.rank] = sh.first;
+    if (threadIdx.x < row.CS()) row.of(sh.firsts, threadIdx.x)[row.rank()] = sh.first_largest;
     row.sync();
     int first = INT32_MAX;
-    for (int c = 0; c < row.CS; ++c) first = min(first, sh.firsts[c]);
+    for (int c = 0; c < row.CS(); ++c) first = min(first, sh.firsts[c]);
     return first;
 }
 
@@ -562,7 +596,7 @@ template <bool BF16>
 __device__ __forceinline__ void find_bin(const Row<BF16>& row, float goal, float decay, uint32_t near) {
     CutShared& sh = *row.sh;
     row.sync();
-    if (row.rank == 0) {
+    if (row.rank() == 0) {
         static_assert(CL_BINS == 4 * CL_THREADS, "four bins per thread");
         const int tid = threadIdx.x;
         if (tid == 0) {
@@ -570,7 +604,7 @@ __device__ __forceinline__ void find_bin(const Row<BF16>& row, float goal, float
             sh.found_to = 0;
         }
         uint32_t n[4] = {0, 0, 0, 0};
-        for (int c = 0; c < row.CS; ++c) {
+        for (int c = 0; c < row.CS(); ++c) {
             const uint4 k = reinterpret_cast<const uint4*>(row.of(&sh, c)->count)[tid];
             n[0] += k.x, n[1] += k.y, n[2] += k.z, n[3] += k.w;
         }
@@ -615,7 +649,7 @@ __device__ __forceinline__ void find_bin(const Row<BF16>& row, float goal, float
             }
         }
         __syncthreads();
-        if (tid > 0 && tid < row.CS) {
+        if (tid > 0 && tid < row.CS()) {
             CutShared* o = row.of(&sh, tid);
             o->found_bin = sh.found_bin;
             o->found_from = sh.found_from;
@@ -649,11 +683,11 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
     CutShared& sh = *row.sh;
     u64 m = 0;
     const ExpEntry* copy = copy_table(row);
-    if (row.s.low == row.s.low) {
+    if (row.s().low == row.s().low) {
         // At or above the cut is z >= its logit before its index and z > it behind.
-        const float z_cut = key_value<BF16>(place_key(cut)), z_from = fmaxf(z_cut, row.s.low);
+        const float z_cut = key_value<BF16>(place_key(cut)), z_from = fmaxf(z_cut, row.s().low);
         const int i_cut = place_index(cut);
-        const float z_over = cut == CL_LOWEST ? z_from : fmaxf(key_value<BF16>(place_key(cut) + 1), row.s.low);
+        const float z_over = cut == CL_LOWEST ? z_from : fmaxf(key_value<BF16>(place_key(cut) + 1), row.s().low);
         WeightSum sum;
         row.each_piece(cut, [&](const uint4& x, int v) {
             const int i0 = row.index(v);
@@ -661,14 +695,14 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
 #pragma unroll
                 for (int e = 0; e < R::E; ++e) {
                     const float z = piece_elem<BF16>(x, e);
-                    if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s, row.sh->exp);
+                    if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s(), row.sh->exp);
                 }
             } else {
                 const float from = i0 + R::E - 1 <= i_cut ? z_from : z_over;
 #pragma unroll
                 for (int e = 0; e < R::E; e += 2) {
                     const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
-                    sum.add(z0 >= from ? z0 : row.s.low, z1 >= from ? z1 : row.s.low, row.s, copy);
+                    sum.add(z0 >= from ? z0 : row.s().low, z1 >= from ? z1 : row.s().low, row.s(), copy);
                 }
             }
         });
@@ -679,16 +713,16 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
 #pragma unroll 1
             for (int e = 0; e < R::E; ++e) {
                 const float z = piece_elem<BF16>(x, e);
-                if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s, row.sh->exp);
+                if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s(), row.sh->exp);
             }
         });
     }
     m = warp_sum(m);
-    if (row.lane == 0) row.of(&sh, 0)->part_mass[row.rank * CL_WARPS + row.warp] = m;
+    if (row.lane == 0) row.of(&sh, 0)->part_mass[row.rank() * CL_WARPS + row.warp] = m;
     row.sync();
     u64 total = 0;
     const u64* parts = row.of(&sh, 0)->part_mass;
-    for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) total += parts[w];
+    for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) total += parts[w];
     return warp_sum(total);
 }
 
@@ -700,7 +734,7 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     u64* mass = sh.list;
-    const int tid = threadIdx.x, lane = row.lane, warp = row.warp, CS = row.CS;
+    const int tid = threadIdx.x, lane = row.lane, warp = row.warp, CS = row.CS();
     const u64 width = hi - lo;  // one less than the places
     const int bits = 64 - __clzll((long long)width);
     const int shift = width == 0 ? 0 : max(0, bits - 11);
@@ -724,14 +758,14 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
             if (p < lo || p > hi) continue;
             const int bin = (int)((p - lo) >> shift);
             atomicAdd(&sh.count[bin], 1u);
-            if (BY_MASS) atomicAdd(&mass[bin], weight(z, row.s, row.sh->exp));
+            if (BY_MASS) atomicAdd(&mass[bin], weight(z, row.s(), row.sh->exp));
         }
     });
     row.sync();
     // A CTA adds up its share of the bins over all CTAs; a thread has `per`
     // neighbouring ones.
     const int seg = CL_BINS / CS, per = max(1, seg / CL_THREADS);
-    const int b0 = row.rank * seg + tid * per;
+    const int b0 = row.rank() * seg + tid * per;
     const bool on = tid * per < seg;
     uint32_t c_of[4] = {0, 0, 0, 0}, c_sum = 0;  // seg / 512 <= 4
     u64 m_of[4] = {0, 0, 0, 0}, m_sum = 0;
@@ -755,14 +789,14 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
     const u64 m_in = block_scan(m_sum, sh.warp_mass, lane, warp, m_total);
     if (tid == 0) {
         row.each_cta([&](CutShared* o) {
-            o->seg_count[row.rank] = c_total;
-            o->seg_mass[row.rank] = m_total;
+            o->seg_count[row.rank()] = c_total;
+            o->seg_mass[row.rank()] = m_total;
         });
     }
     row.sync();
     uint32_t c = above + c_total - c_in;
     u64 m = mass_above + m_total - m_in;
-    for (int q = row.rank + 1; q < CS; ++q) {
+    for (int q = row.rank() + 1; q < CS; ++q) {
         c += sh.seg_count[q];
         m += sh.seg_mass[q];
     }
@@ -816,7 +850,7 @@ __device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool a
     u64 carry = mass_above;
     for (int base = 0; base < n; base += CL_THREADS) {
         const int i = base + tid;
-        const u64 p = i < n ? sh.list[i] : 0, w = i < n ? weight(key_value<BF16>(place_key(p)), row.s, row.sh->exp) : 0;
+        const u64 p = i < n ? sh.list[i] : 0, w = i < n ? weight(key_value<BF16>(place_key(p)), row.s(), row.sh->exp) : 0;
         u64 total;
         const u64 incl = carry + block_scan(w, sh.warp_mass, row.lane, row.warp, total);
         const bool first = !any && i == 0;
@@ -855,7 +889,7 @@ __device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32
     if (threadIdx.x == 0) sh.list_n = 0;
     row.sync();
     const int n = (int)min(gather(row, lo, hi), (uint32_t)CL_LIST);
-    if (row.rank == 0) {
+    if (row.rank() == 0) {
         sort_list(sh, n, lo, hi);
         u64 place = 0;
         if constexpr (BY_MASS) {
@@ -908,7 +942,7 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
     constexpr u64 W = (2ull << CL_UNIT) - 1;
     for (int i = tid; i < n; i += CL_THREADS) {
         const u64 p = sh.list[i];
-        sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(key_value<BF16>(place_key(p)), row.s, row.sh->exp);
+        sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(key_value<BF16>(place_key(p)), row.s(), row.sh->exp);
     }
     __syncthreads();
     if (n > 1) sort_list(sh, n, 0, ~0ull >> 1);  // (descending reversed index)
@@ -927,9 +961,9 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
         const u64 incl = carry + block_scan(w, sh.warp_mass, row.lane, row.warp, sum);
         if (i < n && incl - w <= target && target < incl) {
             const int index = (int)(CL_INDEX_MASK - (uint32_t)(e >> (CL_UNIT + 1)));
-            const float z = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row.src)[index] << 16)
-                                 : reinterpret_cast<const float*>(row.src)[index];
-            put_token(P, at_row, index, z, sh, row.s.top, all);
+            const float z = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row.sh->src)[index] << 16)
+                                 : reinterpret_cast<const float*>(row.sh->src)[index];
+            put_token(P, at_row, index, z, sh, row.s().top, all);
         }
         carry += sum;
     }
@@ -942,12 +976,12 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     const int lane = row.lane;
-    if (row.rank == 0 && row.warp == 0) {
+    if (row.rank() == 0 && row.warp == 0) {
         constexpr int N = CL_MAX_CS * CL_WARPS / 32;  // neighbouring parts per lane
         u64 m[N], sum = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            m[i] = N * lane + i < row.CS * CL_WARPS ? sh.part_mass[N * lane + i] : 0;
+            m[i] = N * lane + i < row.CS() * CL_WARPS ? sh.part_mass[N * lane + i] : 0;
             sum += m[i];
         }
         const u64 incl = warp_scan(sum, lane), total = __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -967,20 +1001,20 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
     }
     row.sync();
     // The part's pieces, a run of neighbours for each thread of its CTA.
-    const int part = (int)sh.draw_warp - row.rank * CL_WARPS;
+    const int part = (int)sh.draw_warp - row.rank() * CL_WARPS;
     if (part < 0 || part >= CL_WARPS) return;
     const u64 target = sh.draw_at, total = sh.found_mass;
     const uint32_t lo16 = R::lo16_of(cut);
-    const int p0 = min(part * row.run, row.n_vecs), p1 = min(p0 + row.run, row.n_vecs);
-    const int per = (row.run + CL_THREADS - 1) / CL_THREADS, v0 = min(p0 + (int)threadIdx.x * per, p1), v1 = min(v0 + per, p1);
+    const int p0 = min(part * row.sh->run, row.n_vecs()), p1 = min(p0 + row.sh->run, row.n_vecs());
+    const int per = (row.sh->run + CL_THREADS - 1) / CL_THREADS, v0 = min(p0 + (int)threadIdx.x * per, p1), v1 = min(v0 + per, p1);
     const auto each_weight = [&](auto&& f) {
         for (int v = v0; v < v1; ++v) {
-            if (row.keys[v] < lo16) continue;
+            if (row.keys()[v] < lo16) continue;
             const uint4 x = row.load(v);
 #pragma unroll
             for (int e = 0; e < R::E; ++e) {
                 const float z = piece_elem<BF16>(x, e);
-                if (place_of(key_of<BF16>(z), row.index(v) + e) >= cut) f(weight(z, row.s, sh.exp), row.index(v) + e, z);
+                if (place_of(key_of<BF16>(z), row.index(v) + e) >= cut) f(weight(z, row.s(), sh.exp), row.index(v) + e, z);
             }
         }
     };
@@ -991,7 +1025,7 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
     u64 at = incl - mine;
     if (at <= goal && goal < incl) {
         each_weight([&](u64 w, int index, float z) {
-            if (at <= goal && goal < at + w) put_token(P, at_row, index, z, sh, row.s.top, total);
+            if (at <= goal && goal < at + w) put_token(P, at_row, index, z, sh, row.s().top, total);
             at += w;
         });
     }
@@ -1003,12 +1037,12 @@ template <bool BF16>
 __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float T, u64 highest, float about) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
-    const RowScale& s = row.s;
+    const RowScale& s = row.s();
     const int tid = threadIdx.x;
     // The last kept element has at least (1 - p) / V of the sum of all weights
     // (all smaller ones together hold less than 1 - p of it), which is at least 1:
     // the bins span what can be kept, evenly in log weights.
-    const float span_log = __logf((float)row.V / fmaxf(1.0f - top_p, 1e-9f)) + 0.01f;
+    const float span_log = __logf((float)row.sh->V / fmaxf(1.0f - top_p, 1e-9f)) + 0.01f;
     const float span = span_log * T, to_bin = (float)CL_BINS / span, bin_log = span_log / (float)CL_BINS;
     clear_bins(row);
     // The histogram: CL_SHARE per element at a bin's upper edge, less towards its
@@ -1018,7 +1052,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     const uint32_t fall = (uint32_t)(bin_log * (float)CL_SHARE * 2.0f + 0.5f);
     const bool flat = !(fabsf(s.top * fine) < 4194304.0f);  // (then shifted has no room)
     const float least = __fsub_rn(s.top, span * 1.0001f);
-    row.each_piece(max(CL_LOWEST, (u64)key_of<BF16>(least) << CL_INDEX_BITS), [&](const uint4& x, int) {
+    row.each_piece_quick(max(CL_LOWEST, (u64)key_of<BF16>(least) << CL_INDEX_BITS), [&](const uint4& x, int) {
 #pragma unroll
         for (int e = 0; e < R::E; ++e) {
             const float z = piece_elem<BF16>(x, e);
@@ -1086,28 +1120,28 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         all = warp_sum(all);
         above = warp_sum(above);
         if (row.lane == 0) {
-            head->part_mass[row.rank * CL_WARPS + row.warp] = above;
-            head->part_all[row.rank * CL_WARPS + row.warp] = all;
+            head->part_mass[row.rank() * CL_WARPS + row.warp] = above;
+            head->part_all[row.rank() * CL_WARPS + row.warp] = all;
         }
         row.sync();
         all = 0;
-        for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) all += head->part_all[w];
+        for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) all += head->part_all[w];
         goal = goal_of(sh, top_p, warp_sum(all));
-        if (row.rank == 0) {
+        if (row.rank() == 0) {
             const int n = (int)sh.list_n;
             u64 mass_above = 0, place = 0;
-            for (int w = 0; w < row.CS * CL_WARPS; ++w) mass_above += sh.part_mass[w];
+            for (int w = 0; w < row.CS() * CL_WARPS; ++w) mass_above += sh.part_mass[w];
             if (n <= CL_LIST) {
                 sort_list(sh, n, lo, highest);
                 place = reach_in_list(row, n, any_above, mass_above, goal, goal);
                 // what of the list is kept joins its warps' sums
                 if (place) {
-                    const int lead = (int)((reinterpret_cast<uintptr_t>(row.src) & 15) / R::ES);
+                    const int lead = (int)((reinterpret_cast<uintptr_t>(row.sh->src) & 15) / R::ES);
                     for (int i = tid; i < n; i += CL_THREADS) {
                         const u64 p = sh.list[i];
                         if (p < place) continue;
-                        const int piece = (place_index(p) + lead) / R::E, cta = piece / row.slice, in_cta = piece - cta * row.slice;
-                        atomicAdd(&sh.part_mass[cta * CL_WARPS + in_cta / row.run], weight(key_value<BF16>(place_key(p)), s, row.sh->exp));
+                        const int piece = (place_index(p) + lead) / R::E, cta = piece / row.sh->slice, in_cta = piece - cta * row.sh->slice;
+                        atomicAdd(&sh.part_mass[cta * CL_WARPS + in_cta / row.sh->run], weight(key_value<BF16>(place_key(p)), s, row.sh->exp));
                     }
                 }
             }
@@ -1141,12 +1175,12 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
     const float edge = nth_group(sh, groups, groups * 3 / 4);
     // (what is -inf has no weight)
     const u64 lo = (u64)max(key_of<BF16>(edge), key_of<BF16>(-INFINITY) + 1) << CL_INDEX_BITS;
-    const float c = row.s.ch * (1.0f / (float)CL_EXP), top = row.s.top;
+    const float c = row.s().ch * (1.0f / (float)CL_EXP), top = row.s().top;
     const uint32_t lo16 = R::lo16_of(lo);
     f32x2 sum = pack2(0.0f, 0.0f), large = sum;
     const f32x2 cc = pack2(c, c), minus_top = pack2(-top, -top);
-    row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
-        const bool some = row.keys[v] >= lo16 || row.partial(v);  // (padding is not below the edge either)
+    row.each_piece_quick(CL_LOWEST, [&](const uint4& x, int v) {
+        const bool some = row.keys()[v] >= lo16 || row.partial(v);  // (padding is not below the edge either)
         f32x2 part = pack2(0.0f, 0.0f);
 #pragma unroll
         for (int e = 0; e < R::E; e += 2) {
@@ -1167,14 +1201,14 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
     unpack2(sum, s0, s1);
     unpack2(large, l0, l1);
     u64 others = warp_sum((u64)__float2ll_rn((s0 + s1) * 0x1p44f)), listed = warp_sum((u64)__float2ll_rn((l0 + l1) * 0x1p44f));
-    if (row.lane < row.CS) {
+    if (row.lane < row.CS()) {
         CutShared* o = row.of(&sh, row.lane);
-        o->part_mass[row.rank * CL_WARPS + row.warp] = others;
-        o->part_all[row.rank * CL_WARPS + row.warp] = listed;
+        o->part_mass[row.rank() * CL_WARPS + row.warp] = others;
+        o->part_all[row.rank() * CL_WARPS + row.warp] = listed;
     }
     row.sync();
     others = listed = 0;
-    for (int w = row.lane; w < row.CS * CL_WARPS; w += 32) {
+    for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) {
         others += sh.part_mass[w];
         listed += sh.part_all[w];
     }
@@ -1184,13 +1218,13 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
     if ((float)listed < about * top_p) return 0;  // (what is near is left to the exact passes)
     const uint32_t n = gather(row, lo, highest);
     row.arrive();
-    if (row.CS == 1) __syncthreads();
-    if (row.rank == 0) {
+    if (row.CS() == 1) __syncthreads();
+    if (row.rank() == 0) {
         u64 place = 0;
         if (n <= CL_LIST) {
             sort_list(sh, (int)n, lo, highest);
             u64 m = 0;
-            for (int i = threadIdx.x; i < (int)n; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), row.s, sh.exp);
+            for (int i = threadIdx.x; i < (int)n; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), row.s(), sh.exp);
             block_scan(m, sh.warp_mass, row.lane, row.warp, listed);
             // (2^18: the units to which the warps' sums were rounded, and more)
             const u64 error = (others >> 15) + (1ull << 18);
@@ -1219,37 +1253,37 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     CutShared& sh = *reinterpret_cast<CutShared*>(smem);
     const int tid = threadIdx.x;
     R row;
-    row.CS = (int)cg::this_cluster().num_blocks();
-    row.rank = (int)cg::this_cluster().block_rank();
     row.lane = tid & 31;
     row.warp = tid >> 5;
     row.sh = &sh;
-    row.keys = reinterpret_cast<uint16_t*>(smem + sizeof(CutShared));
-    row.V = P.V;
-    row.slice = P.slice_vecs;
-    row.run = P.warp_vecs;
-    const int CS = row.CS, rank = row.rank, lane = row.lane, warp = row.warp;
+    const int CS = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank(), lane = row.lane, warp = row.warp;
 
     const int64_t at_row = blockIdx.x / CS;
     const int b = (int)(at_row / P.R), r = (int)(at_row - (int64_t)b * P.R);
-    row.src = P.logits + b * P.seq_bytes + r * P.row_bytes;
-    const int lead = (int)(reinterpret_cast<uintptr_t>(row.src) & 15) / R::ES;  // elements before the row in its first piece
-    const int pieces = (lead + P.V + R::E - 1) / R::E;
-    const int begin = min(rank * P.slice_vecs, pieces);
-    row.n_vecs = min(P.slice_vecs, pieces - begin);
-    row.v0 = min(warp * P.warp_vecs, row.n_vecs);
-    row.v1 = min(row.v0 + P.warp_vecs, row.n_vecs);
-    row.first = begin * R::E - lead;
-    row.base = reinterpret_cast<const uint4*>(row.src - lead * R::ES) + begin;
-    row.full0 = row.first < 0 ? 1 : 0;
-    row.full1 = row.first + row.n_vecs * R::E > P.V ? row.n_vecs - 1 : row.n_vecs;
+    const char* src = P.logits + b * P.seq_bytes + r * P.row_bytes;
+    const int lead = (int)(reinterpret_cast<uintptr_t>(src) & 15) / R::ES;  // elements before the row in its first piece
+    if (tid == 0) {
+        const int pieces = (lead + P.V + R::E - 1) / R::E, begin = min(rank * P.slice_vecs, pieces);
+        sh.src = src;
+        sh.base = reinterpret_cast<const uint4*>(src - lead * R::ES) + begin;
+        sh.V = P.V;
+        sh.first = begin * R::E - lead;
+        sh.n_vecs = min(P.slice_vecs, pieces - begin);
+        sh.slice = P.slice_vecs;
+        sh.run = P.warp_vecs;
+        sh.full0 = sh.first < 0 ? 1 : 0;
+        sh.full1 = sh.first + sh.n_vecs * R::E > P.V ? sh.n_vecs - 1 : sh.n_vecs;
+        sh.CS = CS;
+        sh.rank = rank;
+    }
     if (tid == 0) {
         sh.list_n = 0;
-        sh.first = INT32_MAX;
+        sh.first_largest = INT32_MAX;
     }
     if (tid < CL_EXP) sh.exp[tid] = g_exp_table.e[tid];
-    if (tid < 8) row.keys[(row.n_vecs & ~7) + tid] = 0;  // behind the last key (written below) up to whole 16 bytes
     __syncthreads();
+    // behind the last key up to whole 16 bytes
+    if (tid < (-row.n_vecs() & 7)) row.keys()[row.n_vecs() + tid] = 0;
 
     grid_dependency_wait();
     launch_dependents();
@@ -1277,31 +1311,31 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     {
         constexpr int U = 8;
         uint32_t most = BF16 ? 0xFF80FF80u : 0xFF800000u;
-        int v = row.v0 + lane;
-        const int end = min(row.v1, row.full1);
-        if (v < row.full0 && v < row.v1) {
-            row.keys[v] = R::piece_key(load_part<BF16>(row.src, P.V, row.index(v), R::MINUS_INF), most);
+        int v = row.v0() + lane;
+        const int end = min(row.v1(), row.sh->full1);
+        if (v < row.sh->full0 && v < row.v1()) {
+            row.keys()[v] = R::piece_key(load_part<BF16>(row.sh->src, P.V, row.index(v), R::MINUS_INF), most);
             v += 32;
         }
         for (; v + 32 * (U - 1) < end; v += 32 * U) {
             uint4 x[U];
 #pragma unroll
-            for (int q = 0; q < U; ++q) x[q] = row.load_whole(v + 32 * q);
+            for (int q = 0; q < U; ++q) x[q] = R::load_whole(sh.base + v + 32 * q);
 #pragma unroll
-            for (int q = 0; q < U; ++q) row.keys[v + 32 * q] = R::piece_key(x[q], most);
+            for (int q = 0; q < U; ++q) row.keys()[v + 32 * q] = R::piece_key(x[q], most);
         }
         {
             uint4 x[U];
 #pragma unroll
             for (int q = 0; q < U; ++q)
-                if (v + 32 * q < end) x[q] = row.load_whole(v + 32 * q);
+                if (v + 32 * q < end) x[q] = R::load_whole(sh.base + v + 32 * q);
 #pragma unroll
             for (int q = 0; q < U; ++q)
-                if (v + 32 * q < end) row.keys[v + 32 * q] = R::piece_key(x[q], most);
+                if (v + 32 * q < end) row.keys()[v + 32 * q] = R::piece_key(x[q], most);
         }
-        const int last = row.v1 - 1;
-        if (last >= max(row.full1, row.v0) && last >= row.full0 && ((last - row.v0) & 31) == lane)
-            row.keys[last] = R::piece_key(load_part<BF16>(row.src, P.V, row.index(last), R::MINUS_INF), most);
+        const int last = row.v1() - 1;
+        if (last >= max(row.sh->full1, row.v0()) && last >= row.sh->full0 && ((last - row.v0()) & 31) == lane)
+            row.keys()[last] = R::piece_key(load_part<BF16>(row.sh->src, P.V, row.index(last), R::MINUS_INF), most);
         top = BF16 ? max_nan(bf16_lo(most), bf16_hi(most)) : __uint_as_float(most);
     }
     // The maxima of groups of lanes: so many that enough lie above what is looked for
@@ -1322,17 +1356,16 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     if (lane % width == 0)
         for (int c = 0; c < CS; ++c) row.of(sh.group_max, c)[(rank * CL_WARPS + warp) * per_warp + lane / width] = group;
     row.sync();
-    row.s.top = -INFINITY;
+    float row_top = -INFINITY;
     least = INFINITY;
-    for (int w = lane; w < groups; w += 32) row.s.top = max_nan(row.s.top, sh.group_max[w]);
+    for (int w = lane; w < groups; w += 32) row_top = max_nan(row_top, sh.group_max[w]);
     for (int w = lane; w < warps; w += 32) least = fminf(least, sh.lane_min[w]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        row.s.top = max_nan(row.s.top, __shfl_xor_sync(0xFFFFFFFFu, row.s.top, o));
+        row_top = max_nan(row_top, __shfl_xor_sync(0xFFFFFFFFu, row_top, o));
         least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
     }
-    const RowScale& s = row.s;
-    const bool row_ok = s.top < INFINITY && s.top > -INFINITY;
+    const bool row_ok = row_top < INFINITY && row_top > -INFINITY;
     u64 cut = CL_LOWEST;  // what is kept lies at or above it
     if (!row_ok || !settings_ok) {
         if (rank == 0 && tid == 0) {
@@ -1346,14 +1379,17 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         }
         if constexpr (DRAW) return;
     } else {
-        row.s.ch = sh.ch;
-        row.s.cl = sh.cl;
-        row.s.low = fabsf(s.top * s.ch) < 0x1p21f ? s.top - sh.low_by : __int_as_float(0x7fc00000);
-        {
-            const float y = __fmul_rn(s.top, s.ch), whole = rintf(y);
-            row.s.shift = 12582912.0f - whole;
-            row.s.frac = __fadd_rn(__fsub_rn(y, whole), __fmaf_rn(s.top, s.cl, __fmaf_rn(s.top, s.ch, -y)));
+        const RowScale& s = sh.s;
+        if (tid == 0) {
+            const float ch = sh.ch, y = __fmul_rn(row_top, ch), whole = rintf(y);
+            sh.s.top = row_top;
+            sh.s.ch = ch;
+            sh.s.cl = sh.cl;
+            sh.s.low = fabsf(y) < 0x1p21f ? row_top - sh.low_by : __int_as_float(0x7fc00000);
+            sh.s.shift = 12582912.0f - whole;
+            sh.s.frac = __fadd_rn(__fsub_rn(y, whole), __fmaf_rn(row_top, sh.cl, __fmaf_rn(row_top, ch, -y)));
         }
+        __syncthreads();
         const u64 highest = (u64)key_of<BF16>(s.top) << CL_INDEX_BITS | CL_INDEX_MASK;
         // min-p: z >= max + T ln(min_p)
         if (min_p > 0.0f && T != 0.0f) {
@@ -1389,15 +1425,15 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                 const float to_bin = (float)(CL_BINS - 1) / __fsub_rn(s.top, least);
                 if (to_bin < INFINITY) {
                     clear_bins(row);
-                    const uint4* keys = reinterpret_cast<const uint4*>(row.keys);
+                    const uint4* keys = reinterpret_cast<const uint4*>(row.keys());
                     const uint32_t lo16 = key32(least) >> 16;
-                    for (int g = tid; g * 8 < row.n_vecs; g += CL_THREADS) {
+                    for (int g = tid; g * 8 < row.n_vecs(); g += CL_THREADS) {
                         const uint4 k8 = keys[g];
                         const uint32_t w[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint32_t key = (w[i / 2] >> (16 * (i % 2))) & 0xFFFFu;
-                            if (key < lo16 || g * 8 + i >= row.n_vecs) continue;
+                            if (key < lo16 || g * 8 + i >= row.n_vecs()) continue;
                             const float y = __fmul_rn(__fsub_rn(s.top, from_key32(key << 16 | (BF16 && !(key >> 15) ? 0xFFFFu : 0u))), to_bin);
                             atomicAdd(&sh.count[max(0, min((int)y, CL_BINS - 1))], 1u);
                         }
@@ -1515,11 +1551,11 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             }
         };
         if (!valid) {
-            for (int v = row.v0 + lane; v < row.v1; v += 32) put(v, row.load(v));
+            for (int v = row.v0() + lane; v < row.v1(); v += 32) put(v, row.load(v));
         } else {
             const uint32_t lo16 = R::lo16_of(cut);
-            for (int v = row.v0 + lane; v < row.v1; v += 32)
-                if (row.keys[v] < lo16) put(v, make_uint4(NONE, NONE, NONE, NONE));
+            for (int v = row.v0() + lane; v < row.v1(); v += 32)
+                if (row.keys()[v] < lo16) put(v, make_uint4(NONE, NONE, NONE, NONE));
             each_hit(row, cut, [&](int v, uint4 x) {
                 const int i0 = row.index(v);
                 uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -1555,6 +1591,9 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // Launch.
 // ---------------------------------------------------------------------------
+#ifndef CL_F
+#define CL_F 4
+#endif
 constexpr int CL_ONE = 226 * 1024;  // shared memory of a CTA at most
 
 template <bool BF16, bool DRAW>
@@ -1573,10 +1612,12 @@ static cudaError_t launch(CutParams p, int sms, cudaStream_t stream) {
     constexpr int E = BF16 ? 8 : 4;
     const int64_t rows = (int64_t)p.B * p.R;
     const int vecs = (p.V + E - 1) / E + 1;  // (a row may begin inside a piece)
-    // Few rows are spread over as many CTAs as two per SM are, down to 4 pieces
-    // per thread.
+    // Few rows are spread over several CTAs each, down to 4 pieces per thread: where
+    // a row may need its weights summed, a lone CTA's row would keep all others
+    // waiting at the end, so up to 4 CTAs each until there are 8 per SM's two places;
+    const bool sums = !(!p.temperatures && p.temperature == 0.0f) && !(!p.top_ks && p.top_k > 0 && p.top_k <= CL_LIST);
     int cs = 1;
-    while (cs < CL_MAX_CS && rows * cs <= sms && vecs / cs > 4 * CL_THREADS) cs *= 2;
+    while (cs < CL_MAX_CS && rows * cs <= (cs < 4 ? (int64_t)sms * (sums ? CL_F : 1) : sms / 2) && vecs / cs > 4 * CL_THREADS) cs *= 2;
     p.slice_vecs = (vecs + cs - 1) / cs;
     p.warp_vecs = (p.slice_vecs + CL_WARPS - 1) / CL_WARPS;
     const int smem = (int)sizeof(CutShared) + (p.slice_vecs + 15) / 8 * 16;
