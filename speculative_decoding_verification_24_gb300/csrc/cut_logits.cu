@@ -218,7 +218,7 @@ struct alignas(16) CutShared {
     // what a search has found, told to every CTA
     u64 found_mass, found_place, draw_at, goal;
     uint32_t found_bin, found_from, found_to, found_above, found_count, draw_warp;
-    uint32_t list_n, hits_n;
+    uint32_t list_n, hits_n, counts[CL_MAX_CS];
     float bound;
     int first_largest, firsts[CL_MAX_CS];
     // This CTA's part of the row. (Here and not in every thread's registers: 64 are
@@ -313,13 +313,6 @@ struct Row {
         if (CS() == 1) __syncthreads();
         else cg::this_cluster().sync();
     }
-    // The same in two halves: what comes between does not wait for the others.
-    __device__ __forceinline__ void arrive() const {
-        if (CS() > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    }
-    __device__ __forceinline__ void wait() const {
-        if (CS() > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    }
     template <class X>
     __device__ __forceinline__ X* of(X* mine, int cta) const { return CS() == 1 ? mine : cg::this_cluster().map_shared_rank(mine, cta); }
     template <class F>
@@ -395,10 +388,37 @@ struct Row {
     }
 };
 
-// Appends to the first CTA's list; what does not fit is counted only.
-__device__ __forceinline__ void append(CutShared* head, u64 place) {
-    const uint32_t at = atomicAdd(&head->list_n, 1u);
-    if (at < CL_LIST) head->list[at] = place;
+// The list. Every CTA appends to its own (atomics on another CTA's memory took a
+// microsecond each) after begin_list, collect brings them to the first CTA's and
+// returns how many there are: with more than CL_LIST nothing is moved. What does
+// not fit is counted only.
+__device__ __forceinline__ void begin_list(CutShared& sh) {
+    if (threadIdx.x == 0) sh.list_n = 0;
+    __syncthreads();
+}
+__device__ __forceinline__ void append(CutShared& sh, u64 place) {
+    const uint32_t at = atomicAdd(&sh.list_n, 1u);
+    if (at < CL_LIST) sh.list[at] = place;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t collect(const Row<BF16>& row) {
+    CutShared& sh = *row.sh;
+    __syncthreads();
+    uint32_t n = sh.list_n;
+    if (row.CS() == 1) return n;
+    if (threadIdx.x < row.CS()) row.of(sh.counts, threadIdx.x)[row.rank()] = n;
+    row.sync();
+    uint32_t before = 0, all = 0;
+    for (int c = 0; c < row.CS(); ++c) {
+        if (c < row.rank()) before += sh.counts[c];
+        all += sh.counts[c];
+    }
+    if (all <= CL_LIST && row.rank() > 0) {
+        CutShared* head = row.of(&sh, 0);
+        for (uint32_t i = threadIdx.x; i < n; i += CL_THREADS) head->list[before + i] = sh.list[i];
+    }
+    row.sync();
+    return all;
 }
 
 // f(piece) for this CTA's pieces that hold places from `lo` on: it collects them,
@@ -449,17 +469,16 @@ template <bool BF16>
 __device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
-    CutShared* head = row.of(&sh, 0);
+    begin_list(sh);
     each_hit(row, lo, [&](int v, const uint4& x) {
         const int i0 = row.index(v);
 #pragma unroll
         for (int e = 0; e < R::E; ++e) {
             const u64 p = place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e);
-            if (p >= lo && p <= hi) append(head, p);
+            if (p >= lo && p <= hi) append(sh, p);
         }
     });
-    row.sync();
-    return head->list_n;
+    return collect(row);
 }
 
 // The first index of the row's largest element, whose key is lo's.
@@ -886,8 +905,6 @@ __device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32
     uint32_t above = 0, left = CL_LIST + 1;
     u64 mass_above = 0;
     for (int round = 0; round < CL_ROUNDS && left > CL_LIST; ++round) left = narrow<BF16, BY_MASS>(row, lo, hi, above, mass_above, k, goal);
-    if (threadIdx.x == 0) sh.list_n = 0;
-    row.sync();
     const int n = (int)min(gather(row, lo, hi), (uint32_t)CL_LIST);
     if (row.rank() == 0) {
         sort_list(sh, n, lo, hi);
@@ -1076,12 +1093,13 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         const u64 lo = max(CL_LOWEST, (u64)key_of<BF16>(z_lo) << CL_INDEX_BITS);
         CutShared* head = row.of(&sh, 0);
         any_above = over <= highest;
+        begin_list(sh);
         const ExpEntry* copy = copy_table(row);
         const bool fast = s.low == s.low;
         const float from = bin0 > 0 ? fmaxf(key_value<BF16>(key_of<BF16>(z_hi) + 1), fast ? s.low : -INFINITY) : INFINITY;
         u64 all = 0, above = 0;
         const auto to_list = [&](float z, int i) {
-            if (z >= z_lo && z < from) append(head, place_of(key_of<BF16>(z), i));
+            if (z >= z_lo && z < from) append(sh, place_of(key_of<BF16>(z), i));
         };
         if (fast) {
             WeightSum sum, upper;
@@ -1123,14 +1141,15 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
             head->part_mass[row.rank() * CL_WARPS + row.warp] = above;
             head->part_all[row.rank() * CL_WARPS + row.warp] = all;
         }
-        row.sync();
+        const int n = (int)collect(row);
+        if (row.CS() == 1) __syncthreads();
         all = 0;
         for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) all += head->part_all[w];
         goal = goal_of(sh, top_p, warp_sum(all));
         if (row.rank() == 0) {
-            const int n = (int)sh.list_n;
             u64 mass_above = 0, place = 0;
-            for (int w = 0; w < row.CS() * CL_WARPS; ++w) mass_above += sh.part_mass[w];
+            for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) mass_above += sh.part_mass[w];
+            mass_above = warp_sum(mass_above);
             if (n <= CL_LIST) {
                 sort_list(sh, n, lo, highest);
                 place = reach_in_list(row, n, any_above, mass_above, goal, goal);
@@ -1151,7 +1170,6 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         row.sync();
         place = sh.found_place;
         row.sync();
-        if (threadIdx.x == 0) sh.list_n = 0;
     }
     if (place == 0) {
         // more equal logits than the list takes, or a border that the histogram missed
@@ -1169,7 +1187,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
 // the exact ones. Else 0, and the list is empty. about: the sum of all weights in
 // their unit.
 template <bool BF16>
-__device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int groups, u64 highest, float& about) {
+__device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int groups, u64 highest, float& about, uint32_t& n) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     const float edge = nth_group(sh, groups, groups * 3 / 4);
@@ -1216,9 +1234,7 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
     listed = warp_sum(listed);
     about = (float)(others + listed);
     if ((float)listed < about * top_p) return 0;  // (what is near is left to the exact passes)
-    const uint32_t n = gather(row, lo, highest);
-    row.arrive();
-    if (row.CS() == 1) __syncthreads();
+    n = gather(row, lo, highest);
     if (row.rank() == 0) {
         u64 place = 0;
         if (n <= CL_LIST) {
@@ -1234,14 +1250,9 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
         __syncthreads();
         if (threadIdx.x == 0) row.each_cta([&](CutShared* o) { o->found_place = place; });
     }
-    row.wait();
     row.sync();
     const u64 place = sh.found_place;
-    if (place == 0) {
-        row.sync();  // everyone has read it
-        if (threadIdx.x == 0) sh.list_n = 0;
-        __syncthreads();
-    }
+    if (place == 0) row.sync();  // everyone has read it
     return place;
 }
 
@@ -1277,7 +1288,6 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         sh.rank = rank;
     }
     if (tid == 0) {
-        sh.list_n = 0;
         sh.first_largest = INT32_MAX;
     }
     if (tid < CL_EXP) sh.exp[tid] = g_exp_table.e[tid];
@@ -1449,11 +1459,8 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             uint32_t n = gather(row, bound, highest);
             bool listed = n <= CL_LIST;
             if (!listed) {
-                row.sync();  // everyone has read the list's length
                 const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0);
                 if (k <= CL_LIST) {
-                    if (tid == 0) sh.list_n = 0;
-                    row.sync();
                     n = gather(row, cut_k, highest);
                     listed = true;
                 } else {
@@ -1466,10 +1473,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                 }
             }
             if (listed) {
-                // The cuts, in the list, whose length the others have read when they
-                // have arrived here.
-                row.arrive();
-                if (CS == 1) __syncthreads();
+                // The cuts, in the list.
                 if (rank == 0) {
                     const int all = min((int)n, CL_LIST);
                     sort_list(sh, all, bound, highest);
@@ -1495,20 +1499,20 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                         if (tid == 0) row.each_cta([&](CutShared* o) { o->found_place = last; });
                     }
                 }
-                row.wait();
                 if constexpr (DRAW) return;
                 row.sync();
                 cut = sh.found_place;
             }
         } else if (by_p) {
             float about;  // the sum of all weights, nearly
-            u64 cut_p = cut_near_top(row, top_p, groups, highest, about);
+            uint32_t listed_n;
+            u64 cut_p = cut_near_top(row, top_p, groups, highest, about, listed_n);
             if (cut_p) {
                 cut = max(cut, cut_p);
                 if constexpr (DRAW) {
                     if (rank == 0) {
                         uint32_t kept = 0, total;
-                        for (int i = tid; i < (int)sh.list_n; i += CL_THREADS) kept += sh.list[i] >= cut;
+                        for (int i = tid; i < (int)listed_n; i += CL_THREADS) kept += sh.list[i] >= cut;
                         block_scan(kept, sh.warp_count, lane, warp, total);
                         draw_list(P, row, at_row, u, (int)total);
                     }
