@@ -880,19 +880,21 @@ __device__ __forceinline__ u64 reach_in_list(const Row<BF16>& row, int n, bool a
     return sh.found_place;
 }
 
-// The groups' n-th largest maximum, from 0 on.
+// The groups' n-th largest maximum, from 0 on: each is compared with all others, by
+// as many lanes as there are for it.
 __device__ __forceinline__ float nth_group(CutShared& sh, int groups, int n) {
-    const int tid = threadIdx.x;
-    if (tid < groups) {
-        const float mine = sh.group_max[tid];
-        int before = 0;
-        for (int w = 0; w < groups; w += 4) {
+    const int lanes = min(CL_THREADS / groups, 32), i = (int)threadIdx.x / lanes, from = (int)threadIdx.x % lanes;
+    const float mine = i < groups ? sh.group_max[i] : 0.0f;
+    int before = 0;
+    if (i < groups) {
+        for (int w = 4 * from; w < groups; w += 4 * lanes) {
             const float4 o = *reinterpret_cast<const float4*>(sh.group_max + w);
-            before += (o.x > mine || (o.x == mine && w < tid)) + (o.y > mine || (o.y == mine && w + 1 < tid)) +
-                      (o.z > mine || (o.z == mine && w + 2 < tid)) + (o.w > mine || (o.w == mine && w + 3 < tid));
+            before += (o.x > mine || (o.x == mine && w < i)) + (o.y > mine || (o.y == mine && w + 1 < i)) +
+                      (o.z > mine || (o.z == mine && w + 2 < i)) + (o.w > mine || (o.w == mine && w + 3 < i));
         }
-        if (before == n) sh.bound = mine;
     }
+    for (int o = 1; o < lanes; o <<= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    if (i < groups && before == n) sh.bound = mine;
     __syncthreads();
     return sh.bound;
 }
@@ -1151,7 +1153,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
             for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) mass_above += sh.part_mass[w];
             mass_above = warp_sum(mass_above);
             if (n <= CL_LIST) {
-                sort_list(sh, n, lo, highest);
+                sort_list(sh, n, lo, min(highest, over - 1));
                 place = reach_in_list(row, n, any_above, mass_above, goal, goal);
                 // what of the list is kept joins its warps' sums
                 if (place) {
@@ -1351,7 +1353,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     // The maxima of groups of lanes: so many that enough lie above what is looked for
     // and the smallest part of a row is between (a quarter more groups than k, all
     // that there is room for in top-p's first try).
-    const int warps = CS * CL_WARPS, wanted = k == 1 ? 1 : k < P.V ? (k < CL_GROUPS ? k + k / 4 : CL_GROUPS) : CL_GROUPS;
+    const int warps = CS * CL_WARPS, wanted = k == 1 ? 1 : k < P.V ? (k < CL_GROUPS ? k + k / 4 : CL_GROUPS) : CL_GROUPS / 2;
     int per_warp = 1;
     while (warps * per_warp < wanted && warps * per_warp < CL_GROUPS) per_warp *= 2;
     const int groups = warps * per_warp, width = 32 / per_warp;
