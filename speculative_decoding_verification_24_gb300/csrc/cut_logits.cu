@@ -1597,9 +1597,6 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // Launch.
 // ---------------------------------------------------------------------------
-#ifndef CL_F
-#define CL_F 4
-#endif
 constexpr int CL_ONE = 226 * 1024;  // shared memory of a CTA at most
 
 template <bool BF16, bool DRAW>
@@ -1618,12 +1615,15 @@ static cudaError_t launch(CutParams p, int sms, cudaStream_t stream) {
     constexpr int E = BF16 ? 8 : 4;
     const int64_t rows = (int64_t)p.B * p.R;
     const int vecs = (p.V + E - 1) / E + 1;  // (a row may begin inside a piece)
-    // Few rows are spread over several CTAs each, down to 4 pieces per thread: where
-    // a row may need its weights summed, a lone CTA's row would keep all others
-    // waiting at the end, so up to 4 CTAs each until there are 8 per SM's two places;
+    // Few rows are spread over several CTAs each, down to 4 pieces per thread: as
+    // many as fill two per SM. Where a row may need its weights summed, a lone CTA's
+    // row would keep all others waiting, so up to 4 CTAs per row while that makes no
+    // more than 8 per SM (192 rows of 128256 fp32 with mixed settings: 214 us with
+    // one CTA, 145 with two, 125 with four; the largest of 256 rows of 151936 bf16
+    // alone: 16 us with one, 31 with four).
     const bool sums = !(!p.temperatures && p.temperature == 0.0f) && !(!p.top_ks && p.top_k > 0 && p.top_k <= CL_LIST);
     int cs = 1;
-    while (cs < CL_MAX_CS && rows * cs <= (cs < 4 ? (int64_t)sms * (sums ? CL_F : 1) : sms / 2) && vecs / cs > 4 * CL_THREADS) cs *= 2;
+    while (cs < CL_MAX_CS && rows * cs <= (cs < 4 ? (int64_t)sms * (sums ? 4 : 1) : sms / 2) && vecs / cs > 4 * CL_THREADS) cs *= 2;
     p.slice_vecs = (vecs + cs - 1) / cs;
     p.warp_vecs = (p.slice_vecs + CL_WARPS - 1) / CL_WARPS;
     const int smem = (int)sizeof(CutShared) + (p.slice_vecs + 15) / 8 * 16;

@@ -76,7 +76,7 @@ struct PagedAttnParams {
     int q_box;               // tokens of one copy of queries, a divisor of TT
     int box_shift;           // log2 of the rows of one copy (page_size's power of two, at most 128)
     float c;                 // scale * log2(e)
-    float cap_c, cap_two;    // cap * log2(e), or 0 without a cap; 2 scale * log2(e) / cap
+    float cap_c, cap_in;     // cap * log2(e), or 0 without a cap; scale / cap
     const float* slopes;     // [Hq] or nullptr
     int rows_cap;            // rows of one partial in the workspace
     uint32_t* counters;      // [PA_MAX_CTAS], zero between calls

@@ -251,7 +251,7 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     while (p.box_shift < 7 && c.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
     p.c = a->scale * 1.4426950408889634f;
     p.cap_c = a->score_cap * 1.4426950408889634f;
-    p.cap_two = a->score_cap != 0.0f ? a->scale * 2.8853900817779268f / a->score_cap : 0.0f;
+    p.cap_in = a->score_cap != 0.0f ? a->scale / a->score_cap : 0.0f;
     p.slopes = a->bias_slopes;
     p.rows_cap = piece_rows(a->T, G);
     char* ws = static_cast<char*>(a->workspace);
