@@ -97,34 +97,28 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv_pages_kernel(const __grid_co
     const int top = torn ? 0 : n_free + run.x;
     if ((bad || torn) && rank == 0 && tid == 0) raise_flag(P.status, SV_FLAG_BAD_LENGTH);
 
-    // Sequences go round the cluster's CTAs, a warp looks at 32 of one CTA's.
-    const auto each = [&](auto&& f) {
-        for (int first = warp * 32; first * CS < P.B; first += KP_THREADS) {
-            const int b = (first + lane) * CS + rank;
-            KpSequence s = {0, -1, 0, 0};
-            int give = 0, want = 0;
-            if (b < P.B) {
-                s = seq[b];
-                give = seq[b + 1].push - s.push;
-                want = seq[b + 1].pop - s.pop;
+    // The pages that move are numbered by sequence and place, and go round the
+    // cluster's threads; f(b, i): the i-th of sequence b's. (With a warp per sequence
+    // a few sequences that want hundreds of pages kept one warp busy: 30 us.)
+    const auto each_page = [&](int KpSequence::*first, int count, auto&& f) {
+        for (int x = rank * KP_THREADS + tid; x < count; x += CS * KP_THREADS) {
+            int b = 0, end = P.B;  // first[b] <= x < first[end]
+            while (end - b > 1) {
+                const int mid = (b + end) >> 1;
+                if (seq[mid].*first <= x) b = mid;
+                else end = mid;
             }
-            f(b, s, give, want);
+            f(b, x - seq[b].*first);
         }
     };
     if (!torn) {
-        each([&](int b, const KpSequence& s, int give, int) {
-            for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, give > 0); todo; todo &= todo - 1) {
-                const int l = __ffs(todo) - 1;
-                const int n = __shfl_sync(0xFFFFFFFFu, give, l), at = n_free + __shfl_sync(0xFFFFFFFFu, s.push, l);
-                const int from = __shfl_sync(0xFFFFFFFFu, s.held, l) - n;
-                int32_t* row = P.table + (int64_t)__shfl_sync(0xFFFFFFFFu, b, l) * P.table_stride + from;
-                for (int i = lane; i < n; i += 32) {
-                    const int page = row[i];
-                    if (page < 0 || page >= P.n_pages) raise_flag(P.status, SV_FLAG_BAD_PAGE);
-                    P.free_pages[at + i] = page;
-                    row[i] = -1;
-                }
-            }
+        each_page(&KpSequence::push, run.x, [&](int b, int i) {
+            const int give = seq[b + 1].push - seq[b].push;
+            int32_t* entry = P.table + (int64_t)b * P.table_stride + seq[b].held - give + i;
+            const int page = *entry;
+            if (page < 0 || page >= P.n_pages) raise_flag(P.status, SV_FLAG_BAD_PAGE);
+            P.free_pages[n_free + seq[b].push + i] = page;
+            *entry = -1;
         });
     }
     cluster_wait_started();
@@ -138,23 +132,27 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv_pages_kernel(const __grid_co
         return page;
     };
     if (!torn) {
+        each_page(&KpSequence::pop, min(run.y, top), [&](int b, int i) {
+            if (seq[b + 1].pop > top) return;  // not enough for all of its own: it gets none
+            P.table[(int64_t)b * P.table_stride + seq[b].held + i] = popped(seq[b].pop + i);
+        });
         int most = 0;
         bool none = false;
-        each([&](int b, const KpSequence& s, int give, int want) {
-            const bool granted = want > 0 && want <= top - s.pop;
+        for (int b = tid; b < P.B; b += KP_THREADS) {
+            const KpSequence s = seq[b], after = seq[b + 1];
+            const int give = after.push - s.push, want = after.pop - s.pop;
+            const bool granted = want > 0 && after.pop <= top;
             none |= want > 0 && !granted;
-            if (granted) most = max(most, s.pop + want);
-            if (give > 0 || granted) P.held[b] = s.held - give + want;
-            for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, granted); todo; todo &= todo - 1) {
-                const int l = __ffs(todo) - 1;
-                const int n = __shfl_sync(0xFFFFFFFFu, want, l), at = __shfl_sync(0xFFFFFFFFu, s.pop, l);
-                int32_t* row = P.table + (int64_t)__shfl_sync(0xFFFFFFFFu, b, l) * P.table_stride + __shfl_sync(0xFFFFFFFFu, s.held, l);
-                for (int i = lane; i < n; i += 32) row[i] = popped(at + i);
-            }
-        });
-        if (none) raise_flag(P.status, SV_FLAG_NO_PAGES);
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        if (lane == 0 && most > 0) atomicMax(cluster.map_shared_rank(&taken, 0), most);
+            if (granted) most = max(most, after.pop);
+            if (b % CS == rank && (give > 0 || granted)) P.held[b] = s.held - give + want;
+        }
+        if (rank == 0) {
+            if (none) raise_flag(P.status, SV_FLAG_NO_PAGES);
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            if (lane == 0 && most > 0) atomicMax(&taken, most);
+            __syncthreads();
+            if (tid == 0) *P.n_free = top - taken;
+        }
     }
     if (P.slots || P.positions) {
         // a warp has a run of rows; a lane searches its first row's sequence and
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv_pages_kernel(const __grid_co
                     if (j < s.held) {
                         page = P.table[(int64_t)b * P.table_stride + j];
                         if (page < 0 || page >= P.n_pages) raise_flag(P.status, SV_FLAG_BAD_PAGE);
-                    } else if (seq[b + 1].pop - s.pop <= top - s.pop) {
+                    } else if (seq[b + 1].pop <= top) {
                         page = popped(s.pop + j - s.held);
                     }
                     if (page >= 0 && page < P.n_pages) slot = (int64_t)page * P.page_size + in_page;
@@ -196,8 +194,6 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv_pages_kernel(const __grid_co
             if (P.positions) P.positions[t] = pos;
         }
     }
-    cluster.sync();  // `taken` is complete
-    if (rank == 0 && tid == 0 && !torn) *P.n_free = top - taken;
 }
 
 cudaError_t launch_kv_pages(const KvPagesParams& p, cudaStream_t stream) {
