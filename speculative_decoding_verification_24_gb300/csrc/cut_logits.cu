@@ -400,6 +400,13 @@ __device__ __forceinline__ void append(CutShared& sh, u64 place) {
     const uint32_t at = atomicAdd(&sh.list_n, 1u);
     if (at < CL_LIST) sh.list[at] = place;
 }
+// Places for this lane's `mine` entries of a counted array, the warp's by one atomic.
+__device__ __forceinline__ uint32_t take_places(uint32_t* n, uint32_t mine, int lane) {
+    const uint32_t incl = warp_scan(mine, lane);
+    uint32_t first = 0;
+    if (lane == 31 && incl) first = atomicAdd(n, incl);
+    return __shfl_sync(0xFFFFFFFFu, first, 31) + incl - mine;
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t collect(const Row<BF16>& row) {
     CutShared& sh = *row.sh;
@@ -421,7 +428,8 @@ __device__ __forceinline__ uint32_t collect(const Row<BF16>& row) {
     return all;
 }
 
-// f(piece) for this CTA's pieces that hold places from `lo` on: it collects them,
+// f(v, piece, on) for this CTA's pieces that hold places from `lo` on, by whole
+// warps, a lane without a piece not `on`: the CTA collects them,
 // then its threads take one each. Too many to collect: each lane its own, four loads
 // at a time.
 template <bool BF16, class F>
@@ -432,34 +440,44 @@ __device__ __forceinline__ void each_hit(const Row<BF16>& row, u64 lo, F&& f) {
     __syncthreads();
     // 8 keys at a time; the keys behind the part's last are 0
     const uint4* keys = reinterpret_cast<const uint4*>(row.keys());
-    for (int g = threadIdx.x; g * 8 < row.n_vecs(); g += CL_THREADS) {
-        const uint4 k8 = keys[g];
-        const uint32_t w[4] = {k8.x, k8.y, k8.z, k8.w};
+    const int n_vecs = row.n_vecs();
+    for (int g0 = row.warp * 32; g0 * 8 < n_vecs; g0 += CL_THREADS) {
+        const int g = g0 + row.lane;
+        uint32_t hit = 0;
+        if (g * 8 < n_vecs) {
+            const uint4 k8 = keys[g];
+            const uint32_t w[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (((w[i / 2] >> (16 * (i % 2))) & 0xFFFFu) < lo16) continue;
-            const int v = g * 8 + i;
-            if (v >= row.n_vecs()) continue;
-            const uint32_t at = atomicAdd(&sh.hits_n, 1u);
-            if (at < CL_HITS) sh.hits[at] = (uint32_t)v;
+            for (int i = 0; i < 8; ++i)
+                if (((w[i / 2] >> (16 * (i % 2))) & 0xFFFFu) >= lo16 && g * 8 + i < n_vecs) hit |= 1u << i;
         }
+        if (!__any_sync(0xFFFFFFFFu, hit != 0)) continue;
+        for (uint32_t at = take_places(&sh.hits_n, __popc(hit), row.lane); hit; hit &= hit - 1, ++at)
+            if (at < CL_HITS) sh.hits[at] = (uint32_t)(g * 8 + __ffs(hit) - 1);
     }
     __syncthreads();
     if (sh.hits_n <= CL_HITS) {
-        for (int i = threadIdx.x; i < (int)sh.hits_n; i += CL_THREADS) f((int)sh.hits[i], row.load((int)sh.hits[i]));
+        const int n = (int)sh.hits_n;
+        for (int i0 = row.warp * 32; i0 < n; i0 += CL_THREADS) {
+            const bool on = i0 + row.lane < n;
+            const int v = on ? (int)sh.hits[i0 + row.lane] : 0;
+            f(v, on ? row.load(v) : make_uint4(0, 0, 0, 0), on);
+        }
     } else {
         constexpr int U = 4;
-        for (int v = row.v0() + row.lane; v < row.v1(); v += 32 * U) {
+        const int end = row.v1();
+        for (int v0 = row.v0(); v0 < end; v0 += 32 * U) {
             uint4 x[U];
             bool on[U];
 #pragma unroll
             for (int q = 0; q < U; ++q) {
-                on[q] = v + 32 * q < row.v1() && row.keys()[v + 32 * q] >= lo16;
-                if (on[q]) x[q] = row.load(v + 32 * q);
+                const int v = v0 + row.lane + 32 * q;
+                on[q] = v < end && row.keys()[v] >= lo16;
+                x[q] = on[q] ? row.load(v) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int q = 0; q < U; ++q)
-                if (on[q]) f(v + 32 * q, x[q]);
+                if (__any_sync(0xFFFFFFFFu, on[q])) f(v0 + row.lane + 32 * q, x[q], on[q]);
         }
     }
 }
@@ -470,12 +488,20 @@ __device__ __forceinline__ uint32_t gather(const Row<BF16>& row, u64 lo, u64 hi)
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     begin_list(sh);
-    each_hit(row, lo, [&](int v, const uint4& x) {
+    each_hit(row, lo, [&](int v, const uint4& x, bool on) {
         const int i0 = row.index(v);
+        uint32_t in = 0;
 #pragma unroll
         for (int e = 0; e < R::E; ++e) {
             const u64 p = place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e);
-            if (p >= lo && p <= hi) append(sh, p);
+            if (on && p >= lo && p <= hi) in |= 1u << e;
+        }
+        uint32_t at = take_places(&sh.list_n, __popc(in), row.lane);
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+            if (!(in >> e & 1u)) continue;
+            if (at < CL_LIST) sh.list[at] = place_of(key_of<BF16>(piece_elem<BF16>(x, e)), i0 + e);
+            ++at;
         }
     });
     return collect(row);
@@ -486,12 +512,12 @@ template <bool BF16>
 __device__ __forceinline__ int first_largest(const Row<BF16>& row, u64 lo) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
-    each_hit(row, lo, [&](int v, const uint4& x) {
+    each_hit(row, lo, [&](int v, const uint4& x, bool on) {
         int first = INT32_MAX;
 #pragma unroll
         for (int e = R::E - 1; e >= 0; --e)
             if (key_of<BF16>(piece_elem<BF16>(x, e)) == place_key(lo)) first = row.index(v) + e;
-        atomicMin(&sh.first_largest, first);
+        if (on) atomicMin(&sh.first_largest, first);
     });
     __syncthreads();
     if (threadIdx.x < row.CS()) row.of(sh.firsts, threadIdx.x)[row.rank()] = sh.first_largest;
@@ -1562,7 +1588,8 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             const uint32_t lo16 = R::lo16_of(cut);
             for (int v = row.v0() + lane; v < row.v1(); v += 32)
                 if (row.keys()[v] < lo16) put(v, make_uint4(NONE, NONE, NONE, NONE));
-            each_hit(row, cut, [&](int v, uint4 x) {
+            each_hit(row, cut, [&](int v, const uint4& x, bool on) {
+                if (!on) return;
                 const int i0 = row.index(v);
                 uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
