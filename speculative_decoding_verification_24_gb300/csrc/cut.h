@@ -30,6 +30,7 @@ struct CutParams {
     uint32_t* status;        // or nullptr
     int slice_vecs;          // 16-byte pieces of a row per CTA at most
     int warp_vecs;           // of these per warp
+    int longest_first;       // the rows' order
 };
 
 cudaError_t launch_cut_logits(CutParams p, int dtype, bool draw, int sms, cudaStream_t stream);

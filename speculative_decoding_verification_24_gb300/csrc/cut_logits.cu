@@ -220,7 +220,7 @@ struct alignas(16) CutShared {
     uint32_t found_bin, found_from, found_to, found_above, found_count, draw_warp;
     uint32_t list_n, hits_n, counts[CL_MAX_CS];
     float bound;
-    int first_largest, firsts[CL_MAX_CS];
+    int first_largest, firsts[CL_MAX_CS], sequence;
     // This CTA's part of the row. (Here and not in every thread's registers: 64 are
     // what two CTAs per SM leave a thread, and the sums' loops need them.)
     const char* src;       // the row's first element
@@ -1284,6 +1284,34 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
     return place;
 }
 
+// The n-th sequence when those whose rows may need all their weights summed come
+// first: top-p without a short top-k.
+constexpr int CL_ORDERED = 4 * CL_THREADS;  // sequences at most
+__device__ __forceinline__ int longest_first(const CutParams& P, CutShared& sh, int n, int lane, int warp) {
+    constexpr int PER = CL_ORDERED / CL_THREADS;
+    const int first = PER * threadIdx.x;
+    uint32_t slow = 0, all;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int i = first + q;
+        if (i >= P.B) continue;
+        const float T = P.temperatures ? P.temperatures[i] : P.temperature, p = P.top_ps ? P.top_ps[i] : P.top_p;
+        const int k = P.top_ks ? P.top_ks[i] : P.top_k;
+        if (T != 0.0f && p < 1.0f && (k <= 0 || k >= P.V || k > CL_LIST)) slow |= 1u << q;
+    }
+    const uint32_t mine = __popc(slow);
+    int before = (int)(block_scan(mine, sh.warp_count, lane, warp, all) - mine);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int i = first + q;
+        const bool s = slow >> q & 1u;
+        if (i < P.B && n == (s ? before : (int)all + i - before)) sh.sequence = i;
+        before += s;
+    }
+    __syncthreads();
+    return sh.sequence;
+}
+
 template <bool BF16, bool DRAW>
 __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_constant__ CutParams P) {
     cluster_arrive_started();
@@ -1297,8 +1325,16 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     row.sh = &sh;
     const int CS = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank(), lane = row.lane, warp = row.warp;
 
-    const int64_t at_row = blockIdx.x / CS;
-    const int b = (int)(at_row / P.R), r = (int)(at_row - (int64_t)b * P.R);
+    if (tid < CL_EXP) sh.exp[tid] = g_exp_table.e[tid];
+    grid_dependency_wait();
+    launch_dependents();
+
+    // Which row. Where there are more than run at once, those that take longest come
+    // first, lest one begins when the others are done.
+    int b = blockIdx.x / CS / P.R;
+    const int r = blockIdx.x / CS - b * P.R;
+    if (P.longest_first) b = longest_first(P, sh, b, lane, warp);
+    const int64_t at_row = (int64_t)b * P.R + r;
     const char* src = P.logits + b * P.seq_bytes + r * P.row_bytes;
     const int lead = (int)(reinterpret_cast<uintptr_t>(src) & 15) / R::ES;  // elements before the row in its first piece
     if (tid == 0) {
@@ -1315,16 +1351,10 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         sh.CS = CS;
         sh.rank = rank;
     }
-    if (tid == 0) {
-        sh.first_largest = INT32_MAX;
-    }
-    if (tid < CL_EXP) sh.exp[tid] = g_exp_table.e[tid];
+    if (tid == 0) sh.first_largest = INT32_MAX;
     __syncthreads();
     // behind the last key up to whole 16 bytes
     if (tid < (-row.n_vecs() & 7)) row.keys()[row.n_vecs() + tid] = 0;
-
-    grid_dependency_wait();
-    launch_dependents();
 
     const float T = P.temperatures ? P.temperatures[b] : P.temperature;
     const int top_k = P.top_ks ? P.top_ks[b] : P.top_k;
@@ -1655,6 +1685,7 @@ static cudaError_t launch(CutParams p, int sms, cudaStream_t stream) {
     p.warp_vecs = (p.slice_vecs + CL_WARPS - 1) / CL_WARPS;
     const int smem = (int)sizeof(CutShared) + (p.slice_vecs + 15) / 8 * 16;
     if (smem > CL_ONE || rows * cs > INT32_MAX) return cudaErrorInvalidValue;
+    p.longest_first = (p.temperatures || p.top_ks || p.top_ps) && p.B <= CL_ORDERED && rows * cs > 2 * sms;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)(rows * cs), 1, 1);
