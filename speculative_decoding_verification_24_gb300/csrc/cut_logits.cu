@@ -1374,6 +1374,17 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         sh.min_lo = (float)(d - (double)sh.min_hi);
     }
 
+    // A row that nothing cuts is written as it is read.
+    char* out = nullptr;
+    bool same = false, through = false;
+    uint4* copy_to = nullptr;
+    if constexpr (!DRAW) {
+        out = P.out + b * P.out_seq_bytes + r * P.out_row_bytes;
+        same = (reinterpret_cast<uintptr_t>(out) & 15) == (uintptr_t)(lead * R::ES);
+        through = same && k >= P.V && top_p >= 1.0f && min_p == 0.0f;
+        if (through && out != src) copy_to = reinterpret_cast<uint4*>(out + (int64_t)sh.first * R::ES);
+    }
+
     // 1. The maximum and the pieces' keys.
     float top;
     {
@@ -1391,6 +1402,10 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             for (int q = 0; q < U; ++q) x[q] = R::load_whole(sh.base + v + 32 * q);
 #pragma unroll
             for (int q = 0; q < U; ++q) row.keys()[v + 32 * q] = R::piece_key(x[q], most);
+            if (!DRAW && copy_to) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) __stcs(copy_to + v + 32 * q, x[q]);
+            }
         }
         {
             uint4 x[U];
@@ -1400,6 +1415,11 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
 #pragma unroll
             for (int q = 0; q < U; ++q)
                 if (v + 32 * q < end) row.keys()[v + 32 * q] = R::piece_key(x[q], most);
+            if (!DRAW && copy_to) {
+#pragma unroll
+                for (int q = 0; q < U; ++q)
+                    if (v + 32 * q < end) __stcs(copy_to + v + 32 * q, x[q]);
+            }
         }
         const int last = row.v1() - 1;
         if (last >= max(row.sh->full1, row.v0()) && last >= row.sh->full0 && ((last - row.v0()) & 31) == lane)
@@ -1594,14 +1614,12 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     if constexpr (!DRAW) {
         // 5. the row's output
         const bool valid = row_ok && settings_ok;
-        char* out = P.out + b * P.out_seq_bytes + r * P.out_row_bytes;
-        const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (uintptr_t)(lead * R::ES);
         constexpr uint32_t NONE = BF16 ? 0xFF80FF80u : 0xFF800000u;
         uint32_t kept = 0;
         const auto put = [&](int v, const uint4& x) {
             const int i0 = row.index(v);
             if (same && !row.partial(v)) {
-                *reinterpret_cast<uint4*>(out + (int64_t)i0 * R::ES) = x;
+                __stcs(reinterpret_cast<uint4*>(out + (int64_t)i0 * R::ES), x);  // (not read again: 2304 rows 243 us without, 229 so)
                 return;
             }
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -1612,8 +1630,10 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                 else reinterpret_cast<uint32_t*>(out)[i0 + e] = w[e];
             }
         };
-        if (!valid) {
-            for (int v = row.v0() + lane; v < row.v1(); v += 32) put(v, row.load(v));
+        if (!valid || through) {
+            for (int v = row.v0() + lane; v < row.v1(); v += 32)
+                if (!through || row.partial(v)) put(v, row.load(v));
+            if (valid && rank == 0 && tid == 0) kept = P.V;
         } else {
             const uint32_t lo16 = R::lo16_of(cut);
             for (int v = row.v0() + lane; v < row.v1(); v += 32)
