@@ -1063,9 +1063,24 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
             }
         }
     };
+    if (threadIdx.x == 0) sh.first_largest = -1;  // (free by now: the part's last element that can be drawn)
     u64 mine = 0, all;
-    each_weight([&](u64 w, int, float) { mine += w; });
+    int last = -1;
+    each_weight([&](u64 w, int index, float z) {
+        mine += w;
+        if (z > -INFINITY) last = index;
+    });
     const u64 incl = block_scan(mine, sh.warp_mass, lane, row.warp, all);
+    if (all == 0) {
+        // weights of less than half a unit each, whose sum in floats is some units
+        if (last >= 0) atomicMax(&sh.first_largest, last);
+        __syncthreads();
+        if (last >= 0 && last == sh.first_largest)
+            each_weight([&](u64, int index, float z) {
+                if (index == last) put_token(P, at_row, index, z, sh, row.s().top, total);
+            });
+        return;
+    }
     const u64 goal = target < all ? target : all - 1;  // (the part's sum in floats may be a little more than this one)
     u64 at = incl - mine;
     if (at <= goal && goal < incl) {

@@ -162,6 +162,24 @@ def test_uniforms_at_and_past_the_ends():
     check(z, u, dict(top_k=7))
 
 
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
+def test_the_end_of_a_row_whose_weights_hardly_count(dtype):
+    """u of 1 and next to it where the last tokens' weights are below any unit but
+    their sum is not: a token that can be drawn comes out all the same."""
+    sv = api()
+    for V, far in ((20000, 34.0), (150000, 36.0), (20000, 60.0), (3000, 800.0)):
+        z = torch.full((4, V), -far).to(dtype)
+        z[:, 5] = 0.0
+        z[1, V // 2:] = -math.inf
+        u = torch.tensor([1.0, 1.0, 1.0 - 2.0 ** -24, 2.0]).cuda()
+        lp = torch.empty(4, device="cuda")
+        for kw in (dict(), dict(top_p=0.99999), dict(top_k=2500)):
+            tokens = sv.spec_sample(z.cuda(), u, **kw, out_logprobs=lp).tolist()
+            for i, t in enumerate(tokens):
+                assert 0 <= t < V and z[i, t] > -math.inf, (V, far, kw, i)
+            assert tokens[2] == 5
+
+
 def test_settings_per_sequence_and_out_of_range():
     B, R, V = 14, 3, 900
     z = rows_of(B * R, V, F32, 2)
