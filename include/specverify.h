@@ -613,8 +613,8 @@ size_t sv_paged_attention_args_size(void);
  *   min_p  keeps those with w_j >= min_p, that is at least min_p times as likely
  *          as the first (0: all).
  * A row keeps what all three keep, always its first. T = 0 keeps the first
- * alone. w and their sums are held to about 2^-33 of each w in integers of 64
- * bits; results do not depend on timing.
+ * alone. Sums of w are held to about 1e-11 of themselves (integers of 64 bits, and
+ * pairs of floats); results do not depend on timing.
  *
  * Rows with a NaN, with +inf or without a finite logit (SV_FLAG_BAD_ROW) and
  * rows with a setting that is out of range (SV_FLAG_BAD_SETTING) give token -1

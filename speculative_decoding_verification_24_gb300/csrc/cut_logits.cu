@@ -7,13 +7,14 @@
 // (key of its logit, reversed index) as one integer that grows towards the
 // row's top. Places are unique, so ties need no care of their own.
 //
-// Weights w_j = exp((z_j - max) / T) are whole numbers in units of 2^-44, right
-// to about 2^-33 of themselves (weight()). Whole numbers add up to the same sum
-// in any order, so results do not depend on how a row is split over threads and
-// CTAs or on the order of atomics, and a token is the one that the definition
-// gives unless its u lies within about 1e-11 of an edge between two tokens. In
-// fp32 a sum of 150,000 weights is off by 1e-6, as much as flat rows' edges lie
-// apart.
+// Weights w_j = exp((z_j - max) / T) are whole numbers in units of 2^-44 (weight())
+// wherever a place is decided. Whole numbers add up to the same sum in any order,
+// whatever the order of atomics. Sums over whole rows are formed in floats with
+// their rounding errors kept (WeightSum) and then made whole numbers: right to 1e-11
+// or so, in an order that the row's split over threads alone gives. So a call's
+// results do not depend on timing, and a token is the one that the definition gives
+// unless its u lies within about 1e-11 of an edge between two tokens. In plain fp32
+// a sum of 150,000 weights is off by 1e-6, as much as flat rows' edges lie apart.
 //
 // A row goes to one CTA, or, where rows are few, to a cluster of up to 8. It is
 // read from HBM once, and of every 16 bytes the largest logit's key (16 bits) is
@@ -25,8 +26,9 @@
 //      above it, by ranking the warps' maxima or a histogram of the pieces'); what
 //      lies at or above it goes to the first CTA's list, which sorts it and
 //      applies all cuts there;
-//   3. top-p alone: the sum of all weights, and a histogram of log weights which
-//      says nearly where p of it is reached; then the exact sum above that
+//   3. top-p alone: the list gets a few hundred of the row's largest, and the sum of
+//      all weights in fp32 often shows already where among them p of it is reached.
+//      Else a histogram of log weights says nearly where; then the sum above that
 //      region, whose elements go to the list, where the place is found;
 //   4. where a list overflows (thousands of equal logits, k in the thousands) the
 //      place is found by exact histograms over shrinking ranges of places;
@@ -95,7 +97,7 @@ struct RowScale {
     float top;       // the row's maximum
     float ch, cl;    // 256 log2(e) / T in two floats
     float low;       // a logit of weight 2^-100; NaN where the row's maximum has no room for one
-    float shift, frac;  // for WeightSum, where there is room
+    float shift, frac, rest;  // for WeightSum, where there is room
 };
 
 // Order of floats as unsigned integers; -0 counts as 0.
@@ -120,27 +122,32 @@ __device__ __forceinline__ int place_index(u64 p) { return (int)(CL_INDEX_MASK -
 __device__ __forceinline__ uint32_t place_key(u64 p) { return (uint32_t)(p >> CL_INDEX_BITS); }
 
 constexpr float CL_L1 = 2.7076061740622863e-3f;  // ln 2 / 256
+constexpr float CL_L1_LOW = (float)(0.69314718055994530942 / 256.0 - (double)2.7076061740622863e-3f);  // what that drops
 constexpr float CL_L2 = 3.6655655969053526e-6f;  // its square / 2
 constexpr float CL_L3 = 3.3083027270131e-9f;     // its cube / 6
 
-// exp((z - top) / T) in units of 2^-44. With d = z - top in two floats, exactly,
-// y = 256 d log2(e) / T = n + x, n whole and |x| <= 1/2: 2^(n / 256) comes from the
-// table and a shift, and 2^(x / 256) - 1, below 2^-9, from three terms of its
-// series. x is off by 2^-26 and the series by 2^-24 of itself: 2^-33 of w. The
-// weight of the maximum is 2^44 exactly.
+// exp((z - top) / T) in units of 2^-44, for the few elements that decide: those of a
+// list, of a draw's last part, of a pass that is made again. With d = z - top in two
+// floats, exactly, y = 256 d log2(e) / T = n + r + x, n whole, |r| <= 1/2 and x its
+// rounding errors: 2^(n / 256) = hi + lo comes from the table and a shift, and with u
+// = (r + x) ln 2 / 256 in two floats e^u - 1 from its series. Right to 2^-43 of
+// itself and the unit; the maximum's is 2^44 exactly.
 __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry* table) {
     const float dh = __fsub_rn(z, s.top);
     const float bb = __fsub_rn(dh, z);
     const float dl = __fsub_rn(__fsub_rn(z, __fsub_rn(dh, bb)), __fadd_rn(s.top, bb));
     constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23: adding it rounds to whole numbers
     const float t = __fmaf_rn(dh, s.ch, MAGIC);
-    const float n = __fsub_rn(t, MAGIC);
-    const float x = __fadd_rn(__fmaf_rn(dh, s.ch, -n), __fmaf_rn(dh, s.cl, __fmul_rn(dl, s.ch)));
-    const float e = __fmul_rn(x, __fmaf_rn(x, __fmaf_rn(x, CL_L3, CL_L2), CL_L1));
+    const float p = __fmul_rn(dh, s.ch), r = __fsub_rn(p, __fsub_rn(t, MAGIC));
+    const float x = __fmaf_rn(dl, s.ch, __fmaf_rn(dh, s.cl, __fmaf_rn(dh, s.ch, -p)));
+    const float uh = __fmul_rn(r, CL_L1), ul = __fmaf_rn(x, CL_L1, __fmaf_rn(r, CL_L1_LOW, __fmaf_rn(r, CL_L1, -uh)));
+    const float el = __fmaf_rn(__fmul_rn(uh, uh), __fmaf_rn(uh, __fmaf_rn(uh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), ul);
     const uint32_t tb = __float_as_uint(t);
     const ExpEntry en = table[tb & (CL_EXP - 1)];  // (the magic number's low bits are 0)
-    const int tail = __float2int_rn(__fmul_rn(__fmaf_rn(en.hi, e, en.lo), 0x1p39f));  // below 2^31
-    const u64 q = ((u64)((__float_as_uint(en.hi) & 0x7FFFFFu) | 0x800000u) << (CL_UNIT - 23)) + (u64)((long long)tail * 32);
+    const float second = __fmul_rn(en.hi, uh);
+    const float third = __fadd_rn(__fmaf_rn(en.hi, el, __fmaf_rn(en.lo, uh, en.lo)), __fmaf_rn(en.hi, uh, -second));
+    const u64 q = ((u64)((__float_as_uint(en.hi) & 0x7FFFFFu) | 0x800000u) << (CL_UNIT - 23)) +
+                  (u64)(__float2ll_rn(__fmul_rn(second, 0x1p44f)) + __float2int_rn(__fmul_rn(third, 0x1p44f)));
     const uint32_t sh = (0x4B400000u + CL_EXP - 1 - tb) >> CL_EXP_BITS;  // ceil(-n / 256)
     const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
     return t > MAGIC - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
@@ -149,11 +156,13 @@ __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry
 // Adds up weights in floats, two elements at a time in packed instructions, for
 // the passes over whole rows (shifting integers took twice as long). Here y = z c -
 // top c, formed at once: r.shift is the magic number less the whole part of top c
-// and r.frac the rest, so that t's low bits are n again; the maximum's own weight
-// is made 1 exactly, which keeps ties exact. w = (hi + (lo + hi e)) 2^-k; the sum
+// and r.frac the rest, so that t's low bits are n again. What r.frac's rounding
+// dropped would move all weights alike, by 2^-34 of themselves; it is added to e,
+// whose own rounding takes it up on average: a row's sum is right to about 2^-37.
+// The maximum's own weight is made 1 exactly, which keeps ties exact. w = (hi + (lo + hi e)) 2^-k; the sum
 // s of the first parts begins at 1, so that s >= any of them and a - (s' - s) is
 // the rounding error of s' = s + a exactly; c takes those and the second parts.
-// s + c is right to 2^-33 of the sum or so, like the weights.
+// The sum is used only where an error of 2^-33 of it changes nothing.
 struct WeightSum {
     f32x2 s, c;
     __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)) {}
@@ -161,12 +170,12 @@ struct WeightSum {
     static __device__ __forceinline__ void pair(float z0, float z1, const RowScale& r, const ExpEntry* table, f32x2& a, f32x2& rest) {
         const f32x2 z = pack2(z0, z1), minus = pack2(-1.0f, -1.0f), ch = pack2(r.ch, r.ch), shift = pack2(r.shift, r.shift);
         const f32x2 t = fma2(z, ch, shift);
-        f32x2 x = add2(fma2(z, ch, fma2(t, minus, shift)), fma2(z, pack2(r.cl, r.cl), pack2(-r.frac, -r.frac)));
-        float x0, x1, t0, t1, e0, e1;
-        unpack2(x, x0, x1);
-        x = pack2(z0 == r.top ? 0.0f : x0, z1 == r.top ? 0.0f : x1);
-        unpack2(mul2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1))), e0, e1);
+        const f32x2 x = add2(fma2(z, ch, fma2(t, minus, shift)), fma2(z, pack2(r.cl, r.cl), pack2(-r.frac, -r.frac)));
+        float t0, t1, e0, e1;
+        unpack2(fma2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1)), pack2(r.rest, r.rest)), e0, e1);
         unpack2(t, t0, t1);
+        e0 = z0 == r.top ? 0.0f : e0;
+        e1 = z1 == r.top ? 0.0f : e1;
         const uint32_t b0 = __float_as_uint(t0), b1 = __float_as_uint(t1);
         const ExpEntry p = table[(b0 & (CL_EXP - 1)) * CL_COPIES], q = table[(b1 & (CL_EXP - 1)) * CL_COPIES];
         // 2^floor(n / 256): the magic number's upper bits leave the word
@@ -346,7 +355,7 @@ struct Row {
         }
     }
     // The same for passes that do little with a piece: U loads at a time. (One ahead,
-    // as above, left them waiting for L2: 64 flat rows' top-p 88 us, 70 so.)
+    // as above, leaves them waiting for L2.)
     template <class F>
     __device__ __forceinline__ void each_piece_quick(u64 lo, F&& f) const {
         constexpr int U = 8;
@@ -548,8 +557,7 @@ __device__ __forceinline__ N block_scan(N v, N* warp_sums, int lane, int warp, N
 // hi]. Few: by counting what is larger, 4 lanes per entry. More: into 1024 buckets
 // of equal width, and within a bucket by counting. Where that leaves many in a
 // bucket (equal logits, say): by a bitonic network in shared memory, whose steps
-// over up to 64 neighbours stay within a warp. (1060 entries: 2 us by buckets,
-// 10 by the network.)
+// over up to 64 neighbours stay within a warp.
 __device__ __noinline__ void sort_list(CutShared& sh, int n, u64 lo, u64 hi) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     u64* list = sh.list;
@@ -1127,9 +1135,13 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     u64 place = 0;
     bool any_above = false;
     u64 goal;
-    {
-        // the sum of all weights and of those above the first of these bins, exactly,
-        // and what lies in them to the list
+    // The sum of all weights and of those above the first of these bins, and what
+    // lies in them to the list. Where the goal comes so near to a border that the
+    // sums in floats may err (one row in thousands), or the list does not hold it,
+    // once more with every weight formed by weight(). (Of 460,800 rows of all settings
+    // one then keeps another token than 64-bit arithmetic does, at a sum 1e-12 from the
+    // goal; it costs the others the check, 250 -> 263 us for 256 flat rows of 151936.)
+    for (bool precise = !(s.low == s.low);; precise = true) {
         const float z_hi = bin0 > 0 ? __fsub_rn(s.top, (float)bin0 / to_bin) : INFINITY;
         const float z_lo = key_value<BF16>(key_of<BF16>(__fsub_rn(s.top, (float)(bin1 + 1) / to_bin)));
         const u64 over = bin0 > 0 ? (u64)(key_of<BF16>(z_hi) + 1) << CL_INDEX_BITS : ~0ull;  // above z_hi
@@ -1138,13 +1150,12 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         any_above = over <= highest;
         begin_list(sh);
         const ExpEntry* copy = copy_table(row);
-        const bool fast = s.low == s.low;
-        const float from = bin0 > 0 ? fmaxf(key_value<BF16>(key_of<BF16>(z_hi) + 1), fast ? s.low : -INFINITY) : INFINITY;
+        const float from = bin0 > 0 ? fmaxf(key_value<BF16>(key_of<BF16>(z_hi) + 1), precise ? -INFINITY : s.low) : INFINITY;
         u64 all = 0, above = 0;
         const auto to_list = [&](float z, int i) {
             if (z >= z_lo && z < from) append(sh, place_of(key_of<BF16>(z), i));
         };
-        if (fast) {
+        if (!precise) {
             WeightSum sum, upper;
             row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
                 const int i0 = row.index(v);
@@ -1188,14 +1199,16 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         if (row.CS() == 1) __syncthreads();
         all = 0;
         for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) all += head->part_all[w];
-        goal = goal_of(sh, top_p, warp_sum(all));
+        all = warp_sum(all);
+        goal = goal_of(sh, top_p, all);
         if (row.rank() == 0) {
             u64 mass_above = 0, place = 0;
             for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) mass_above += sh.part_mass[w];
             mass_above = warp_sum(mass_above);
             if (n <= CL_LIST) {
                 sort_list(sh, n, lo, min(highest, over - 1));
-                place = reach_in_list(row, n, any_above, mass_above, goal, goal);
+                const u64 unsure = precise ? 0 : all >> 33;
+                place = reach_in_list(row, n, any_above, mass_above, goal - min(goal, unsure), goal + unsure);
                 // what of the list is kept joins its warps' sums
                 if (place) {
                     const int lead = (int)((reinterpret_cast<uintptr_t>(row.sh->src) & 15) / R::ES);
@@ -1213,6 +1226,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         row.sync();
         place = sh.found_place;
         row.sync();
+        if (place || precise) break;
     }
     if (place == 0) {
         // more equal logits than the list takes, or a border that the histogram missed
@@ -1490,7 +1504,9 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             sh.s.cl = sh.cl;
             sh.s.low = fabsf(y) < 0x1p21f ? row_top - sh.low_by : __int_as_float(0x7fc00000);
             sh.s.shift = 12582912.0f - whole;
-            sh.s.frac = __fadd_rn(__fsub_rn(y, whole), __fmaf_rn(row_top, sh.cl, __fmaf_rn(row_top, ch, -y)));
+            const float a = __fsub_rn(y, whole), low = __fmaf_rn(row_top, sh.cl, __fmaf_rn(row_top, ch, -y)), frac = __fadd_rn(a, low);
+            sh.s.frac = frac;
+            sh.s.rest = -__fadd_rn(__fsub_rn(a, frac), low) * CL_L1;
         }
         __syncthreads();
         const u64 highest = (u64)key_of<BF16>(s.top) << CL_INDEX_BITS | CL_INDEX_MASK;
