@@ -491,7 +491,8 @@ typedef struct {
     uint32_t flags;              /* SV_ARG_TEST_WAIT_TIMEOUT or 0                 */
     sv_stream_t stream;
     float score_cap;             /* 0: none; else 2^-10..4096: scores become cap *
-                                    tanh(scale q . k / cap)                       */
+                                    tanh(scale q . k / cap); scale / cap from
+                                    2^-60 to 2^60                                 */
     const float* bias_slopes;    /* [Hq] float (device), finite, or NULL: slope_h *
                                     (the key's position - the token's) is added to
                                     the score, after the cap. A slot's position is

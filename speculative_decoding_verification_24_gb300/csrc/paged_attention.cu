@@ -1201,8 +1201,10 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // error, 2^-21.7, fitted to tanh(x) / x on [0, 0.7]): 7 operations of the FMA units,
 // which bound it. Else tanh(x) = 1 - 2 / (1 + e^2x), off by 2^-22 or so of 1, at any
 // x: 3 of those and 2 of the units that exponentials take. A warp's tile takes the
-// first if all its scores are near. (2048 tokens over 8192, 209 us uncapped: 343 us
-// with the first, 377 with the second alone.)
+// first if all its rows see all its keys and all their scores are near: scores that
+// a row does not see, and rows that no token has, are what the memory held before,
+// and results would change with it. (2048 tokens over 8192, 209 us uncapped:
+// 328 us with the first, 397 with the second alone.)
 constexpr float PA_CAP_NEAR = 0.7f;
 struct Cap {
     f32x2 in2, k0, k1, k2, k3, k4;  // (scale / cap)^2; the polynomial's coefficients times scale log2(e)
@@ -1214,7 +1216,6 @@ struct Cap {
         k3 = both(-0.0508362352848053f * P.c), k4 = both(0.01377371046692133f * P.c);
         c = both(P.cap_c), two = both(2.8853900817779268f * P.cap_in), minus = both(-2.0f * P.cap_c);
     }
-    // (-inf, a masked score, stays that: the leading coefficient is positive)
     __device__ __forceinline__ f32x2 near(f32x2 r, f32x2 add) const {
         const f32x2 s = mul2(mul2(r, in2), r);
         return fma2(r, fma2(s, fma2(s, fma2(s, fma2(s, k4, k3), k2), k1), k0), add);
@@ -1226,18 +1227,18 @@ struct Cap {
     }
 };
 
-__device__ __forceinline__ bool cap_near(const uint32_t (&r)[PA_TILE], const PagedAttnParams& P) {
+__device__ __forceinline__ bool cap_near(const uint32_t (&r)[PA_TILE], const PagedAttnParams& P, bool valid) {
     float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < PA_TILE; k += 8)
 #pragma unroll
         for (int j = 0; j < 4; ++j) top[j] = max3_abs(top[j], __uint_as_float(r[k + 2 * j]), __uint_as_float(r[k + 2 * j + 1]));
-    return !__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.cap_in > PA_CAP_NEAR);
+    return !__any_sync(0xFFFFFFFFu, valid && fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.cap_in > PA_CAP_NEAR);
 }
 
 // A tile's scores, changed.
 template <int MOD>
-__device__ __forceinline__ void change_scores(uint32_t (&r)[PA_TILE], const PagedAttnParams& P, float slope, int far0) {
+__device__ __forceinline__ void change_scores(uint32_t (&r)[PA_TILE], const PagedAttnParams& P, float slope, int far0, bool near) {
     const f32x2 cc = pack2(P.c, P.c), slopes = pack2(slope, slope), step = pack2(2.0f, 2.0f), zero = pack2(0.0f, 0.0f);
     const float f0 = (float)far0;
     f32x2 far = pack2(f0, f0 + 1.0f);
@@ -1257,7 +1258,7 @@ __device__ __forceinline__ void change_scores(uint32_t (&r)[PA_TILE], const Page
     };
     if constexpr ((MOD & PA_CAP) != 0) {
         const Cap cap(P);
-        if (cap_near(r, P)) each([&](f32x2 x, f32x2 bias) { return cap.near(x, bias); });
+        if (MOD != PA_CAP && near) each([&](f32x2 x, f32x2 bias) { return cap.near(x, bias); });
         else each([&](f32x2 x, f32x2 bias) { return cap.any(x, bias); });
     } else {
         each([&](f32x2 x, f32x2 bias) { return fma2(x, cc, bias); });
@@ -1338,10 +1339,11 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                 tmem_ld(tmem_s, r);
                 // A cap alone keeps the order, so scores near 0 are changed only where
                 // they become weights.
-                bool late = false;
-                if constexpr (MOD == PA_CAP) late = cap_near(r, P);
+                bool near = false;
+                if constexpr ((MOD & PA_CAP) != 0) near = key0 + PA_TILE <= seen_by_all && cap_near(r, P, at.valid);
+                const bool late = MOD == PA_CAP && near;
                 if constexpr (MOD != 0) {
-                    if (!late) change_scores<MOD>(r, P, slope, key0 - row_pos);
+                    if (!late) change_scores<MOD>(r, P, slope, key0 - row_pos, near);
                     if constexpr ((MOD & PA_BIAS) != 0) {
                         if (P.ch.parents && key0 + PA_TILE > c.s.ctx) {
 #pragma unroll
@@ -1430,7 +1432,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                 };
                 if constexpr (MOD == PA_CAP) {
                     // (two copies of the loop: one with a branch for 32 scores at a
-                    // time took 363 us where these take 343)
+                    // time took 6 % longer)
                     const Cap cap(P);
                     if (late) weights([&](f32x2 x) { return cap.near(x, mm); });
                     else weights([&](f32x2 x) { return add2(x, mm); });

@@ -304,3 +304,30 @@ def test_drafts_drawn_cut_and_verified(dtype):
     for b in range(B):
         for i in range(n[b] + 1):
             assert cut_t[b, i, tokens[b][i]].item() > -math.inf
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes_and_settings(seed):
+    """Rows of any length and spread, as they lie in a padded buffer, with settings
+    per sequence or one for all."""
+    g = torch.Generator().manual_seed(100 + seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))  # noqa: E731
+    B, R = pick(1, 6), pick(1, 4)
+    V = int(2 ** (1 + 16 * torch.rand(1, generator=g).item()))
+    V, dtype = max(2, V), (BF16, F32)[seed % 2]
+    z = (torch.randn(B * R, V, generator=g) * 10.0 ** (torch.rand(B * R, 1, generator=g) * 2 - 1)).to(dtype)
+    row, seq = V + pick(0, 9), 0
+    seq = R * row + pick(0, 9)
+    flat = torch.full((B * seq + 16,), math.nan, dtype=dtype, device="cuda")
+    placed = torch.as_strided(flat, (B, R, V), (seq, row, 1), pick(0, 8))
+    placed.copy_(z.view(B, R, V))
+    any_of = lambda *x: x[pick(0, len(x) - 1)]  # noqa: E731
+    make = dict(temperature=lambda: any_of(0.0, 0.2, 0.7, 1.0, 3.0), top_k=lambda: any_of(0, 1, 5, 50, 700, V, V - 1),
+                top_p=lambda: any_of(0.0, 0.3, 0.9, 0.99, 1.0, 1.0), min_p=lambda: any_of(0.0, 0.0, 0.02, 0.5))
+    settings = {}
+    for name, one in make.items():
+        if pick(0, 1):
+            settings[name] = torch.tensor([one() for _ in range(B)], dtype=torch.int32 if name == "top_k" else F32)
+        else:
+            settings[name] = one()
+    assert check(z, torch.rand(B * R, generator=g), settings, R=R, placed=placed) <= 1

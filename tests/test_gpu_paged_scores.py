@@ -255,3 +255,46 @@ def test_values_that_are_not_finite():
     assert torch.isfinite(out[:10]).all() and torch.equal(out[:10], want[:10])
     assert (out[10:, :4, 5] == float("inf")).all()
     assert torch.equal(out[10:, 4:], want[10:, 4:])
+
+
+@pytest.mark.parametrize("power", (-60, 60))
+def test_the_smallest_and_largest_scale_of_a_cap(power):
+    """At 2^-60 all keys that a token sees count alike; at 2^60 scores are the cap,
+    minus it or 0. Masked and unread entries stay out of both."""
+    c = Case([(300, 3), (0, 40), (128, 1)], cap=4.0, seed=15)
+    c.scale = 4.0 * 2.0 ** power
+    g = torch.Generator().manual_seed(16)
+    c.q = torch.randint(-1, 2, c.q.shape, generator=g).to(BF16).cuda()
+    fill = torch.randint(-1, 2, c.k.shape, generator=g).to(BF16).cuda()
+    c.k = torch.where(torch.isnan(c.k), c.k, fill)  # products are whole numbers, of up to 128: exact
+    out = c.run()
+    for b, (ctx, n) in enumerate(c.seqs):
+        k, v = (entries(x, c.table, b, range(ctx + n), c.page) for x in (c.k, c.v))
+        for i in range(n):
+            t, seen = int(c.cu[b]) + i, ctx + i + 1
+            s = torch.einsum("hgd,shd->hgs", c.q[t].cpu().double().view(2, 4, 128), k[:seen].double())
+            w = torch.softmax(4.0 * torch.sign(s) if power > 0 else torch.zeros_like(s), -1)
+            ref = torch.einsum("hgs,shd->hgd", w, v[:seen].double()).reshape(8, 128)
+            size = torch.einsum("hgs,shd->hgd", w, v[:seen].double().abs()).reshape(8, 128)
+            # weights and output are rounded by half a step each; scores are off by 2^-21 of the cap
+            assert ((out[t].cpu().double() - ref).abs() <= 1.01 * (2.0 ** -8 + 2.0 ** -17) * size + 2.0 ** -8 * ref.abs()).all()
+
+
+@pytest.mark.parametrize("name", list(KINDS))
+@pytest.mark.parametrize("D", [64, 128])
+def test_results_do_not_depend_on_what_ran_before(name, D):
+    """Scores that no row sees are what the memory held: large ones of another
+    call, or none. Neither they nor the entries behind the last token count."""
+    c = Case([(5, 1), (100, 5), (300, 2), (0, 40), (700, 1)], D=D, seed=17, dirty=False, q_scale=0.3, **kind(name, 8))
+    other = Case([(900, 130)] * 8, D=D, seed=18, q_scale=300.0, **kind(name, 8))
+    first, lse = c.run(), c.lse
+    rows = torch.arange(c.k.shape[0] * c.page, device="cuda").view(-1, c.page)
+    used = torch.zeros_like(rows, dtype=torch.bool)
+    for b, (ctx, n) in enumerate(c.seqs):
+        at = torch.arange(ctx + n)
+        used[torch.from_numpy(c.table)[b, at // c.page].long().cuda(), (at % c.page).cuda()] = True
+    for junk in (0.0, 1e4, float("nan"), None):
+        other.run()
+        if junk is not None:
+            c.k.masked_fill_(~used[:, :, None, None], junk)
+        assert torch.equal(c.run(), first) and torch.equal(c.lse, lse)

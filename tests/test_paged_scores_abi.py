@@ -17,3 +17,11 @@ from test_paged_abi import ALIGN, CONFIG, FAKE, attention_args
 def test_refused(changes, code):
     build()
     assert binding.library().spec_paged_attention(ctypes.byref(attention_args(**changes))) == code
+
+
+@pytest.mark.parametrize("scale,cap", [(2.0 ** -61, 1.0), (2.0 ** 61, 1.0), (2.0 ** -50, 4096.0), (2.0 ** 52, 2.0 ** -10)])
+def test_a_scale_too_far_from_the_cap(scale, cap):
+    """Neither it nor its square is to be 0 or infinite."""
+    build()
+    call = binding.library().spec_paged_attention
+    assert call(ctypes.byref(attention_args(score_cap=cap, scale=scale))) == CONFIG
