@@ -217,7 +217,7 @@ extern "C" sv_status spec_paged_attention(const sv_paged_attention_args* a) {
     if (items * (std::ceil((double)c.max_pages * c.page_size / sv::PA_TILE) + sv::PA_ITEM_COST) > 2147483647.0) return SV_ERR_SHAPE;
     if (!std::isfinite(a->scale) || !(a->scale > 0.0f) || !std::isfinite(a->scale * 1.4426950408889634f)) return SV_ERR_CONFIG;
     if (a->flags & ~SV_ARG_TEST_WAIT_TIMEOUT) return SV_ERR_CONFIG;
-    // (the kernel squares scale / cap)
+    // (the kernel squares scale / cap and multiplies it with masked scores, -inf: neither 0 nor inf)
     if (a->score_cap != 0.0f && (!(a->score_cap >= 0x1p-10f && a->score_cap <= 4096.0f) ||
                                  !(a->scale / a->score_cap >= 0x1p-60f && a->scale / a->score_cap <= 0x1p60f)))
         return SV_ERR_CONFIG;

@@ -1201,10 +1201,10 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // error, 2^-21.7, fitted to tanh(x) / x on [0, 0.7]): 7 operations of the FMA units,
 // which bound it. Else tanh(x) = 1 - 2 / (1 + e^2x), off by 2^-22 or so of 1, at any
 // x: 3 of those and 2 of the units that exponentials take. A warp's tile takes the
-// first if all its rows see all its keys and all their scores are near: scores that
-// a row does not see, and rows that no token has, are what the memory held before,
-// and results would change with it. (2048 tokens over 8192, 209 us uncapped:
-// 328 us with the first, 397 with the second alone.)
+// first if all its scores are near and of tokens: keys behind the last and rows that
+// no token has are what the memory held before, and results would change with it.
+// (2048 tokens over 8192, 209 us uncapped: 322 us with the first, 390 with the
+// second alone.)
 constexpr float PA_CAP_NEAR = 0.7f;
 struct Cap {
     f32x2 in2, k0, k1, k2, k3, k4;  // (scale / cap)^2; the polynomial's coefficients times scale log2(e)
@@ -1216,6 +1216,7 @@ struct Cap {
         k3 = both(-0.0508362352848053f * P.c), k4 = both(0.01377371046692133f * P.c);
         c = both(P.cap_c), two = both(2.8853900817779268f * P.cap_in), minus = both(-2.0f * P.cap_c);
     }
+    // (-inf, a masked score, stays that: the leading coefficient is positive)
     __device__ __forceinline__ f32x2 near(f32x2 r, f32x2 add) const {
         const f32x2 s = mul2(mul2(r, in2), r);
         return fma2(r, fma2(s, fma2(s, fma2(s, fma2(s, k4, k3), k2), k1), k0), add);
@@ -1227,13 +1228,21 @@ struct Cap {
     }
 };
 
-__device__ __forceinline__ bool cap_near(const uint32_t (&r)[PA_TILE], const PagedAttnParams& P, bool valid) {
+// Whether the first n scores are near in all of a warp's rows (a row that no token
+// has: cap_in 0).
+__device__ __forceinline__ bool cap_near(const uint32_t (&r)[PA_TILE], const PagedAttnParams& P, float cap_in, int n) {
     float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n >= PA_TILE) {
 #pragma unroll
-    for (int k = 0; k < PA_TILE; k += 8)
+        for (int k = 0; k < PA_TILE; k += 8)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top[j] = max3_abs(top[j], __uint_as_float(r[k + 2 * j]), __uint_as_float(r[k + 2 * j + 1]));
-    return !__any_sync(0xFFFFFFFFu, valid && fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.cap_in > PA_CAP_NEAR);
+            for (int j = 0; j < 4; ++j) top[j] = max3_abs(top[j], __uint_as_float(r[k + 2 * j]), __uint_as_float(r[k + 2 * j + 1]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < PA_TILE; ++k)
+            if (k < n) top[k % 4] = fmaxf(top[k % 4], fabsf(__uint_as_float(r[k])));
+    }
+    return !__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cap_in > PA_CAP_NEAR);
 }
 
 // A tile's scores, changed.
@@ -1340,7 +1349,7 @@ __device__ __forceinline__ void softmax_rows(const PagedAttnParams& P, PaShared&
                 // A cap alone keeps the order, so scores near 0 are changed only where
                 // they become weights.
                 bool near = false;
-                if constexpr ((MOD & PA_CAP) != 0) near = key0 + PA_TILE <= seen_by_all && cap_near(r, P, at.valid);
+                if constexpr ((MOD & PA_CAP) != 0) near = cap_near(r, P, at.valid ? P.cap_in : 0.0f, key_end - key0);
                 const bool late = MOD == PA_CAP && near;
                 if constexpr (MOD != 0) {
                     if (!late) change_scores<MOD>(r, P, slope, key0 - row_pos, near);
