@@ -159,10 +159,11 @@ __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry
 // and r.frac the rest, so that t's low bits are n again. What r.frac's rounding
 // dropped would move all weights alike, by 2^-34 of themselves; it is added to e,
 // whose own rounding takes it up on average: a row's sum is right to about 2^-37.
-// The maximum's own weight is made 1 exactly, which keeps ties exact. w = (hi + (lo + hi e)) 2^-k; the sum
-// s of the first parts begins at 1, so that s >= any of them and a - (s' - s) is
-// the rounding error of s' = s + a exactly; c takes those and the second parts.
-// The sum is used only where an error of 2^-33 of it changes nothing.
+// The maximum's own weight is made 1 exactly, which keeps ties exact. w = (hi + (lo
+// + hi e)) 2^-k; the sum s of the first parts begins at 1, so that s >= any of them
+// and a - (s' - s) is the rounding error of s' = s + a exactly; c takes those and
+// the second parts. Where top-p's goal comes within 2^-33 of a border the sum
+// decides nothing (cut_by_mass).
 struct WeightSum {
     f32x2 s, c;
     __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)) {}
@@ -244,7 +245,8 @@ struct alignas(16) CutShared {
     float ch, cl, low_by, min_hi, min_lo;
 };
 // (read and cleared 16 bytes at a time, like the pieces' keys behind the struct)
-static_assert(sizeof(CutShared) % 16 == 0 && offsetof(CutShared, list) % 16 == 0 && offsetof(CutShared, count) % 16 == 0 && offsetof(CutShared, group_max) % 16 == 0, "alignment");
+static_assert(sizeof(CutShared) % 16 == 0 && offsetof(CutShared, list) % 16 == 0 && offsetof(CutShared, count) % 16 == 0 &&
+                  offsetof(CutShared, group_max) % 16 == 0, "alignment");
 
 template <bool BF16>
 __device__ __forceinline__ float piece_elem(const uint4& x, int e) {
