@@ -1548,7 +1548,9 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     } else {
         const RowScale& s = sh.s;
         if (tid == 0) {
-            const float ch = sh.ch, y = __fmul_rn(row_top, ch), whole = rintf(y);
+            // (rounded as WeightSum rounds it: from y, next to a half, the maximum's own
+            // exponent came out as 1 / 256)
+            const float ch = sh.ch, y = __fmul_rn(row_top, ch), whole = __fsub_rn(__fmaf_rn(row_top, ch, 12582912.0f), 12582912.0f);
             sh.s.top = row_top;
             sh.s.ch = ch;
             sh.s.cl = sh.cl;

@@ -331,3 +331,11 @@ def test_random_shapes_and_settings(seed):
         else:
             settings[name] = one()
     assert check(z, torch.rand(B * R, generator=g), settings, R=R, placed=placed) <= 1
+
+
+@pytest.mark.parametrize("offset", (3.0, 12.0, 100.0))
+def test_the_largest_weight_is_one_wherever_the_maximum_lies(offset):
+    """256 log2(e) max / T next to halves of whole numbers too."""
+    g = torch.Generator().manual_seed(int(offset))
+    z = torch.randn(6000, 16, generator=g) + offset * (0.5 + torch.rand(6000, 1, generator=g))
+    assert check(z, torch.rand(6000, generator=g), dict()) <= 1
