@@ -43,12 +43,11 @@
 
 #include "cut.h"
 #include "paged_device.cuh"
+#include "cut_weights.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace sv {
-
-typedef unsigned long long u64;
 
 constexpr int CL_THREADS = 512;
 constexpr int CL_WARPS = CL_THREADS / 32;
@@ -61,44 +60,9 @@ constexpr int CL_HITS = 2048;  // pieces of one CTA that gather() reads in one s
 constexpr int CL_ROUNDS = 5;   // of 11 bits each; a place has 50
 constexpr int CL_INDEX_BITS = 18;
 constexpr uint32_t CL_INDEX_MASK = (1u << CL_INDEX_BITS) - 1;
-constexpr int CL_EXP_BITS = 8;
-constexpr int CL_EXP = 1 << CL_EXP_BITS;  // entries of the table of 2^(i / 256)
-constexpr int CL_UNIT = 44;               // weights are in units of 2^-44
 static_assert((1 << CL_INDEX_BITS) == CUT_MAX_V, "an index per place");
 
-// 2^(i / 256) as the sum of two floats.
-struct alignas(8) ExpEntry {
-    float hi, lo;
-};
-constexpr int CL_COPIES = 4;  // of the table, side by side, for whole rows: lane l reads copy l % 4
-struct ExpTable {
-    ExpEntry e[CL_EXP];
-};
-constexpr double exp_series(double x) {
-    double sum = 1.0, term = 1.0;
-    for (int i = 1; i < 30; ++i) {
-        term *= x / i;
-        sum += term;
-    }
-    return sum;
-}
-constexpr ExpTable make_exp_table() {
-    ExpTable t = {};
-    for (int i = 0; i < CL_EXP; ++i) {
-        const double v = exp_series(0.69314718055994530942 * i / CL_EXP);
-        t.e[i].hi = (float)v;
-        t.e[i].lo = (float)(v - (double)(float)v);
-    }
-    return t;
-}
 __device__ const ExpTable g_exp_table = make_exp_table();
-
-struct RowScale {
-    float top;       // the row's maximum
-    float ch, cl;    // 256 log2(e) / T in two floats
-    float low;       // a logit of weight 2^-100; NaN where the row's maximum has no room for one
-    float shift, frac, rest;  // for WeightSum, where there is room
-};
 
 // Order of floats as unsigned integers; -0 counts as 0.
 __device__ __forceinline__ uint32_t key32(float z) {
@@ -120,91 +84,6 @@ __device__ __forceinline__ u64 place_of(uint32_t key, int index) {
 constexpr u64 CL_LOWEST = 1ull << CL_INDEX_BITS;  // at or below every real element's place
 __device__ __forceinline__ int place_index(u64 p) { return (int)(CL_INDEX_MASK - ((uint32_t)p & CL_INDEX_MASK)); }
 __device__ __forceinline__ uint32_t place_key(u64 p) { return (uint32_t)(p >> CL_INDEX_BITS); }
-
-constexpr float CL_L1 = 2.7076061740622863e-3f;  // ln 2 / 256
-constexpr float CL_L1_LOW = (float)(0.69314718055994530942 / 256.0 - (double)2.7076061740622863e-3f);  // what that drops
-constexpr float CL_L2 = 3.6655655969053526e-6f;  // its square / 2
-constexpr float CL_L3 = 3.3083027270131e-9f;     // its cube / 6
-
-// exp((z - top) / T) in units of 2^-44, for the few elements that decide: those of a
-// list, of a draw's last part, of a pass that is made again. With d = z - top in two
-// floats, exactly, y = 256 d log2(e) / T = n + r + x, n whole, |r| <= 1/2 and x its
-// rounding errors: 2^(n / 256) = hi + lo comes from the table and a shift, and with u
-// = (r + x) ln 2 / 256 in two floats e^u - 1 from its series. Right to 2^-43 of
-// itself and the unit; the maximum's is 2^44 exactly.
-__device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry* table) {
-    const float dh = __fsub_rn(z, s.top);
-    const float bb = __fsub_rn(dh, z);
-    const float dl = __fsub_rn(__fsub_rn(z, __fsub_rn(dh, bb)), __fadd_rn(s.top, bb));
-    constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23: adding it rounds to whole numbers
-    const float t = __fmaf_rn(dh, s.ch, MAGIC);
-    const float p = __fmul_rn(dh, s.ch), r = __fsub_rn(p, __fsub_rn(t, MAGIC));
-    const float x = __fmaf_rn(dl, s.ch, __fmaf_rn(dh, s.cl, __fmaf_rn(dh, s.ch, -p)));
-    const float uh = __fmul_rn(r, CL_L1), ul = __fmaf_rn(x, CL_L1, __fmaf_rn(r, CL_L1_LOW, __fmaf_rn(r, CL_L1, -uh)));
-    const float el = __fmaf_rn(__fmul_rn(uh, uh), __fmaf_rn(uh, __fmaf_rn(uh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), ul);
-    const uint32_t tb = __float_as_uint(t);
-    const ExpEntry en = table[tb & (CL_EXP - 1)];  // (the magic number's low bits are 0)
-    const float second = __fmul_rn(en.hi, uh);
-    const float third = __fadd_rn(__fmaf_rn(en.hi, el, __fmaf_rn(en.lo, uh, en.lo)), __fmaf_rn(en.hi, uh, -second));
-    const u64 q = ((u64)((__float_as_uint(en.hi) & 0x7FFFFFu) | 0x800000u) << (CL_UNIT - 23)) +
-                  (u64)(__float2ll_rn(__fmul_rn(second, 0x1p44f)) + __float2int_rn(__fmul_rn(third, 0x1p44f)));
-    const uint32_t sh = (0x4B400000u + CL_EXP - 1 - tb) >> CL_EXP_BITS;  // ceil(-n / 256)
-    const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
-    return t > MAGIC - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
-}
-
-// Adds up weights in floats, two elements at a time in packed instructions, for
-// the passes over whole rows (shifting integers took twice as long). Here y = z c -
-// top c, formed at once: r.shift is the magic number less the whole part of top c
-// and r.frac the rest, so that t's low bits are n again. What r.frac's rounding
-// dropped would move all weights alike, by 2^-34 of themselves; it is added to e,
-// whose own rounding takes it up on average: a row's sum is right to about 2^-37.
-// The maximum's own weight is made 1 exactly, which keeps ties exact. w = (hi + (lo
-// + hi e)) 2^-k; the sum s of the first parts begins at 1, so that s >= any of them
-// and a - (s' - s) is the rounding error of s' = s + a exactly; c takes those and
-// the second parts. Where top-p's goal comes within 2^-33 of a border the sum
-// decides nothing (cut_by_mass).
-struct WeightSum {
-    f32x2 s, c;
-    __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)) {}
-    // The two parts of a pair's weights; z0, z1 >= r.low.
-    static __device__ __forceinline__ void pair(float z0, float z1, const RowScale& r, const ExpEntry* table, f32x2& a, f32x2& rest) {
-        const f32x2 z = pack2(z0, z1), minus = pack2(-1.0f, -1.0f), ch = pack2(r.ch, r.ch), shift = pack2(r.shift, r.shift);
-        const f32x2 t = fma2(z, ch, shift);
-        const f32x2 x = add2(fma2(z, ch, fma2(t, minus, shift)), fma2(z, pack2(r.cl, r.cl), pack2(-r.frac, -r.frac)));
-        float t0, t1, e0, e1;
-        unpack2(fma2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1)), pack2(r.rest, r.rest)), e0, e1);
-        unpack2(t, t0, t1);
-        e0 = z0 == r.top ? 0.0f : e0;
-        e1 = z1 == r.top ? 0.0f : e1;
-        const uint32_t b0 = __float_as_uint(t0), b1 = __float_as_uint(t1);
-        const ExpEntry p = table[(b0 & (CL_EXP - 1)) * CL_COPIES], q = table[(b1 & (CL_EXP - 1)) * CL_COPIES];
-        // 2^floor(n / 256): the magic number's upper bits leave the word
-        const auto scale = [](uint32_t b) { return __uint_as_float((b & ~(uint32_t)(CL_EXP - 1)) * (1u << (23 - CL_EXP_BITS)) + 0x3F800000u); };
-        const float pow0 = scale(b0), pow1 = scale(b1);
-        a = pack2(__fmul_rn(p.hi, pow0), __fmul_rn(q.hi, pow1));
-        rest = pack2(__fmul_rn(__fmaf_rn(p.hi, e0, p.lo), pow0), __fmul_rn(__fmaf_rn(q.hi, e1, q.lo), pow1));
-    }
-    __device__ __forceinline__ void add(f32x2 a, f32x2 rest) {
-        const f32x2 minus = pack2(-1.0f, -1.0f), sum = add2(s, a);
-        c = add2(c, add2(fma2(fma2(s, minus, sum), minus, a), rest));
-        s = sum;
-    }
-    __device__ __forceinline__ void add(float z0, float z1, const RowScale& r, const ExpEntry* table) {
-        f32x2 a, rest;
-        pair(z0, z1, r, table, a, rest);
-        add(a, rest);
-    }
-    __device__ __forceinline__ u64 total() const {
-        float s0, s1, c0, c1;
-        unpack2(s, s0, s1);
-        unpack2(c, c0, c1);
-        // (differences from 1 are exact, and a double's units are few)
-        const ff sum = two_sum(__fsub_rn(s0, 1.0f), __fsub_rn(s1, 1.0f));
-        const long long v = __float2ll_rn(sum.hi * 0x1p44f) + __float2ll_rn(__fadd_rn(sum.lo, __fadd_rn(c0, c1)) * 0x1p44f);
-        return v > 0 ? (u64)v : 0ull;
-    }
-};
 
 // What one row's cluster shares; every CTA has its own copy.
 struct alignas(16) CutShared {
@@ -1547,19 +1426,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         if constexpr (DRAW) return;
     } else {
         const RowScale& s = sh.s;
-        if (tid == 0) {
-            // (rounded as WeightSum rounds it: from y, next to a half, the maximum's own
-            // exponent came out as 1 / 256)
-            const float ch = sh.ch, y = __fmul_rn(row_top, ch), whole = __fsub_rn(__fmaf_rn(row_top, ch, 12582912.0f), 12582912.0f);
-            sh.s.top = row_top;
-            sh.s.ch = ch;
-            sh.s.cl = sh.cl;
-            sh.s.low = fabsf(y) < 0x1p21f ? row_top - sh.low_by : __int_as_float(0x7fc00000);
-            sh.s.shift = 12582912.0f - whole;
-            const float a = __fsub_rn(y, whole), low = __fmaf_rn(row_top, sh.cl, __fmaf_rn(row_top, ch, -y)), frac = __fadd_rn(a, low);
-            sh.s.frac = frac;
-            sh.s.rest = -__fadd_rn(__fsub_rn(a, frac), low) * CL_L1;
-        }
+        if (tid == 0) set_scale(sh.s, row_top, sh.ch, sh.cl, sh.low_by);
         __syncthreads();
         const u64 highest = (u64)key_of<BF16>(s.top) << CL_INDEX_BITS | CL_INDEX_MASK;
         // min-p: z >= max + T ln(min_p)

@@ -1,0 +1,150 @@
+// Weights of a row's logits, w = exp((z - max) / T): one by one in whole units
+// (weight), and added up in packed floats (WeightSum). Only roundings, products,
+// sums and shifts, whose results are the same on the host: the tests compile this
+// file there, with these few functions of the device beside it (f32x2 and ff of
+// sv_device.cuh among them), and compare it with 64-bit and longer arithmetic.
+#pragma once
+
+namespace sv {
+
+typedef unsigned long long u64;
+
+constexpr int CL_EXP_BITS = 8;
+constexpr int CL_EXP = 1 << CL_EXP_BITS;  // entries of the table of 2^(i / 256)
+constexpr int CL_UNIT = 44;               // weights are in units of 2^-44
+
+// 2^(i / 256) as the sum of two floats.
+struct alignas(8) ExpEntry {
+    float hi, lo;
+};
+constexpr int CL_COPIES = 4;  // of the table, side by side, for whole rows: lane l reads copy l % 4
+struct ExpTable {
+    ExpEntry e[CL_EXP];
+};
+constexpr double exp_series(double x) {
+    double sum = 1.0, term = 1.0;
+    for (int i = 1; i < 30; ++i) {
+        term *= x / i;
+        sum += term;
+    }
+    return sum;
+}
+constexpr ExpTable make_exp_table() {
+    ExpTable t = {};
+    for (int i = 0; i < CL_EXP; ++i) {
+        const double v = exp_series(0.69314718055994530942 * i / CL_EXP);
+        t.e[i].hi = (float)v;
+        t.e[i].lo = (float)(v - (double)(float)v);
+    }
+    return t;
+}
+constexpr float CL_L1 = 2.7076061740622863e-3f;  // ln 2 / 256
+constexpr float CL_L1_LOW = (float)(0.69314718055994530942 / 256.0 - (double)2.7076061740622863e-3f);  // what that drops
+constexpr float CL_L2 = 3.6655655969053526e-6f;  // its square / 2
+constexpr float CL_L3 = 3.3083027270131e-9f;     // its cube / 6
+
+struct RowScale {
+    float top;       // the row's maximum
+    float ch, cl;    // 256 log2(e) / T in two floats
+    float low;       // a logit of weight 2^-100; NaN where the row's maximum has no room for one
+    float shift, frac, rest;  // for WeightSum, where there is room
+};
+
+// What a row's maximum decides; low_by: how far below it a weight is 2^-100.
+__device__ __forceinline__ void set_scale(RowScale& s, float top, float ch, float cl, float low_by) {
+    // (rounded as WeightSum rounds it: from y, next to a half, the maximum's own
+    // exponent came out as 1 / 256)
+    const float y = __fmul_rn(top, ch), whole = __fsub_rn(__fmaf_rn(top, ch, 12582912.0f), 12582912.0f);
+    s.top = top;
+    s.ch = ch;
+    s.cl = cl;
+    s.low = fabsf(y) < 0x1p21f ? top - low_by : __uint_as_float(0x7fc00000u);
+    s.shift = 12582912.0f - whole;
+    const float a = __fsub_rn(y, whole), low = __fmaf_rn(top, cl, __fmaf_rn(top, ch, -y)), frac = __fadd_rn(a, low);
+    s.frac = frac;
+    s.rest = -__fadd_rn(__fsub_rn(a, frac), low) * CL_L1;
+}
+
+// exp((z - top) / T) in units of 2^-44, for the few elements that decide: those of a
+// list, of a draw's last part, of a pass that is made again. With d = z - top in two
+// floats, exactly, y = 256 d log2(e) / T = n + r + x, n whole, |r| <= 1/2 and x its
+// rounding errors: 2^(n / 256) = hi + lo comes from the table and a shift, and with u
+// = (r + x) ln 2 / 256 = uh + ul in two floats e^u - 1 = uh + el from its series, el
+// with every term that uh and ul have in common. Right to 2^-40 of itself and two
+// units; the maximum's is 2^44 exactly.
+__device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry* table) {
+    const float dh = __fsub_rn(z, s.top);
+    const float bb = __fsub_rn(dh, z);
+    const float dl = __fsub_rn(__fsub_rn(z, __fsub_rn(dh, bb)), __fadd_rn(s.top, bb));
+    constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23: adding it rounds to whole numbers
+    const float t = __fmaf_rn(dh, s.ch, MAGIC);
+    const float p = __fmul_rn(dh, s.ch), r = __fsub_rn(p, __fsub_rn(t, MAGIC));
+    const float x = __fmaf_rn(dl, s.ch, __fmaf_rn(dh, s.cl, __fmaf_rn(dh, s.ch, -p)));
+    const float uh = __fmul_rn(r, CL_L1), ul = __fmaf_rn(x, CL_L1, __fmaf_rn(r, CL_L1_LOW, __fmaf_rn(r, CL_L1, -uh)));
+    const float el = __fmaf_rn(__fmul_rn(uh, uh), __fmaf_rn(uh, __fmaf_rn(uh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f),
+                               __fmaf_rn(__fmaf_rn(ul, 0.5f, uh), ul, ul));
+    const uint32_t tb = __float_as_uint(t);
+    const ExpEntry en = table[tb & (CL_EXP - 1)];  // (the magic number's low bits are 0)
+    const float second = __fmul_rn(en.hi, uh);
+    const float third = __fadd_rn(__fmaf_rn(en.hi, el, __fmaf_rn(en.lo, uh, en.lo)), __fmaf_rn(en.hi, uh, -second));
+    const u64 q = ((u64)((__float_as_uint(en.hi) & 0x7FFFFFu) | 0x800000u) << (CL_UNIT - 23)) +
+                  (u64)(__float2ll_rn(__fmul_rn(second, 0x1p44f)) + __float2int_rn(__fmul_rn(third, 0x1p44f)));
+    const uint32_t sh = (0x4B400000u + CL_EXP - 1 - tb) >> CL_EXP_BITS;  // ceil(-n / 256)
+    const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
+    return t > MAGIC - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
+}
+
+// Adds up weights in floats, two elements at a time in packed instructions, for
+// the passes over whole rows (shifting integers took twice as long). Here y = z c -
+// top c, formed at once: r.shift is the magic number less the whole part of top c
+// and r.frac the rest, so that t's low bits are n again. What r.frac's rounding
+// dropped would move all weights alike, by 2^-34 of themselves; it is added to e,
+// whose own rounding takes it up on average: a row's sum is right to about 2^-37.
+// The maximum's own weight is made 1 exactly, which keeps ties exact. w = (hi + (lo
+// + hi e)) 2^-k; the sum s of the first parts begins at 1, so that s >= any of them
+// and a - (s' - s) is the rounding error of s' = s + a exactly; c takes those and
+// the second parts. Where top-p's goal comes within 2^-33 of a border the sum
+// decides nothing (cut_by_mass).
+struct WeightSum {
+    f32x2 s, c;
+    __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)) {}
+    // The two parts of a pair's weights; z0, z1 >= r.low.
+    static __device__ __forceinline__ void pair(float z0, float z1, const RowScale& r, const ExpEntry* table, f32x2& a, f32x2& rest) {
+        const f32x2 z = pack2(z0, z1), minus = pack2(-1.0f, -1.0f), ch = pack2(r.ch, r.ch), shift = pack2(r.shift, r.shift);
+        const f32x2 t = fma2(z, ch, shift);
+        const f32x2 x = add2(fma2(z, ch, fma2(t, minus, shift)), fma2(z, pack2(r.cl, r.cl), pack2(-r.frac, -r.frac)));
+        float t0, t1, e0, e1;
+        unpack2(fma2(x, fma2(x, fma2(x, pack2(CL_L3, CL_L3), pack2(CL_L2, CL_L2)), pack2(CL_L1, CL_L1)), pack2(r.rest, r.rest)), e0, e1);
+        unpack2(t, t0, t1);
+        e0 = z0 == r.top ? 0.0f : e0;
+        e1 = z1 == r.top ? 0.0f : e1;
+        const uint32_t b0 = __float_as_uint(t0), b1 = __float_as_uint(t1);
+        const ExpEntry p = table[(b0 & (CL_EXP - 1)) * CL_COPIES], q = table[(b1 & (CL_EXP - 1)) * CL_COPIES];
+        // 2^floor(n / 256): the magic number's upper bits leave the word
+        const auto scale = [](uint32_t b) { return __uint_as_float((b & ~(uint32_t)(CL_EXP - 1)) * (1u << (23 - CL_EXP_BITS)) + 0x3F800000u); };
+        const float pow0 = scale(b0), pow1 = scale(b1);
+        a = pack2(__fmul_rn(p.hi, pow0), __fmul_rn(q.hi, pow1));
+        rest = pack2(__fmul_rn(__fmaf_rn(p.hi, e0, p.lo), pow0), __fmul_rn(__fmaf_rn(q.hi, e1, q.lo), pow1));
+    }
+    __device__ __forceinline__ void add(f32x2 a, f32x2 rest) {
+        const f32x2 minus = pack2(-1.0f, -1.0f), sum = add2(s, a);
+        c = add2(c, add2(fma2(fma2(s, minus, sum), minus, a), rest));
+        s = sum;
+    }
+    __device__ __forceinline__ void add(float z0, float z1, const RowScale& r, const ExpEntry* table) {
+        f32x2 a, rest;
+        pair(z0, z1, r, table, a, rest);
+        add(a, rest);
+    }
+    __device__ __forceinline__ u64 total() const {
+        float s0, s1, c0, c1;
+        unpack2(s, s0, s1);
+        unpack2(c, c0, c1);
+        // (differences from 1 are exact, and a double's units are few)
+        const ff sum = two_sum(__fsub_rn(s0, 1.0f), __fsub_rn(s1, 1.0f));
+        const long long v = __float2ll_rn(sum.hi * 0x1p44f) + __float2ll_rn(__fadd_rn(sum.lo, __fadd_rn(c0, c1)) * 0x1p44f);
+        return v > 0 ? (u64)v : 0ull;
+    }
+};
+
+}  // namespace sv
