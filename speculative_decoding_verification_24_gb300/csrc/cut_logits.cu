@@ -7,8 +7,8 @@
 // (key of its logit, reversed index) as one integer that grows towards the
 // row's top. Places are unique, so ties need no care of their own.
 //
-// Weights w_j = exp((z_j - max) / T) are whole numbers in units of 2^-44 (weight())
-// wherever a place is decided. Whole numbers add up to the same sum in any order,
+// Weights w_j = exp((z_j - max) / T) are whole numbers (weight()) wherever a place is
+// decided, in the finest unit that the row's sum leaves room for. Whole numbers add up to the same sum in any order,
 // whatever the order of atomics. Sums over whole rows are formed in floats with
 // their rounding errors kept (WeightSum) and then made whole numbers: right to 1e-11
 // or so, in an order that the row's split over threads alone gives. So a call's
@@ -640,7 +640,7 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
                 }
             }
         });
-        m += sum.total();
+        m += sum.total(row.s().unit);
     } else {
         row.each_piece(cut, [&](const uint4& x, int v) {
             const int i0 = row.index(v);
@@ -864,9 +864,9 @@ __device__ __forceinline__ u64 draw_target(float u, u64 total) {
     return t < total ? t : total - 1;
 }
 
-// ln(total / 2^44) for total of 2^44 or more: total = 2^(k + i / 256) (1 + d) with
+// ln(total / 2^unit) for a total of one or more: total = 2^(k + i / 256) (1 + d) with
 // the table's factor, and ln(1 + d) by its series, d < 2^-8; to about 2^-36.
-__device__ __forceinline__ double log_total(u64 total, const ExpEntry* table) {
+__device__ __forceinline__ double log_total(u64 total, int unit, const ExpEntry* table) {
     const int k = 63 - __clzll((long long)total);
     const double m = (double)total * __longlong_as_double((long long)(1023 - k) << 52);  // [1, 2)
     const int i = min((int)(log2f((float)m) * (float)CL_EXP), CL_EXP - 1);
@@ -874,7 +874,7 @@ __device__ __forceinline__ double log_total(u64 total, const ExpEntry* table) {
     const ExpEntry e = table[(CL_EXP - i) & (CL_EXP - 1)];
     const double d = m * (((double)e.hi + (double)e.lo) * (i == 0 ? 1.0 : 0.5)) - 1.0;
     const float f = (float)d, tail = f * f * (f * (1.0f / 3.0f) - 0.5f - f * f * 0.25f);
-    return ((double)(k - CL_UNIT) + (double)i * (1.0 / CL_EXP)) * 0.69314718055994530942 + (d + (double)tail);
+    return ((double)(k - unit) + (double)i * (1.0 / CL_EXP)) * 0.69314718055994530942 + (d + (double)tail);
 }
 
 __device__ __forceinline__ void put_token(const CutParams& P, int64_t row, int index, float z, const CutShared& sh, float top, double log_sum) {
@@ -887,18 +887,19 @@ template <bool BF16>
 __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& row, int64_t at_row, float u, int n) {
     CutShared& sh = *row.sh;
     const int tid = threadIdx.x;
-    // entries become (index, weight), 18 and 45 bits, and are sorted by index
-    constexpr u64 W = (2ull << CL_UNIT) - 1;
     if (n <= CL_THREADS / 4) {
         // Few: 4 lanes per entry add up those before it in the order of indices, and
         // all; the sum's logarithm is formed meanwhile. (A row of 32,000, top-k 50 and
-        // top-p: 12.9 us with a sort and two scans, 10.2 so.)
+        // top-p: 12.9 us with a sort and two scans, 10.2 so.) Entries become (reversed
+        // index, weight), 18 and 45 bits: 128 halves of that unit are 2^-38.
+        constexpr int UNIT = 44;
+        constexpr u64 W = (2ull << UNIT) - 1;
         const int i = tid >> 2;
         float z = 0.0f;
         if (i < n && (tid & 3) == 0) {
             const u64 p = sh.list[i];
             z = key_value<BF16>(place_key(p));
-            sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(z, row.s(), row.sh->exp);
+            sh.list[i] = (p & CL_INDEX_MASK) << (UNIT + 1) | weight(z, row.s(), row.sh->exp, UNIT, none_of(UNIT));
         }
         __syncthreads();
         const u64 mine = i < n ? sh.list[i] : 0;
@@ -915,38 +916,37 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
             before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
             all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
         }
-        if (tid == 3 && P.logprobs) sh.log_sum = log_total(all, sh.exp);
+        if (tid == 3 && P.logprobs) sh.log_sum = log_total(all, UNIT, sh.exp);
         __syncthreads();
         if (i < n && (tid & 3) == 0) {
             const u64 target = draw_target(u, all);
             if (before <= target && target < before + (mine & W))
-                put_token(P, at_row, (int)(CL_INDEX_MASK - (uint32_t)(mine >> (CL_UNIT + 1))), z, sh, row.s().top, sh.log_sum);
+                put_token(P, at_row, (int)(CL_INDEX_MASK - (uint32_t)(mine >> (UNIT + 1))), z, sh, row.s().top, sh.log_sum);
         }
         return;
     }
+    // entries become (reversed index, key) and are sorted by index
     for (int i = tid; i < n; i += CL_THREADS) {
         const u64 p = sh.list[i];
-        sh.list[i] = (p & CL_INDEX_MASK) << (CL_UNIT + 1) | weight(key_value<BF16>(place_key(p)), row.s(), row.sh->exp);
+        sh.list[i] = (p & CL_INDEX_MASK) << 32 | place_key(p);
     }
     __syncthreads();
-    sort_list(sh, n, 0, ~0ull >> 1);  // (descending reversed index)
+    sort_list(sh, n, 0, (1ull << (CL_INDEX_BITS + 32)) - 1);  // (descending reversed index)
+    const auto weight_of = [&](u64 e) { return weight(key_value<BF16>((uint32_t)e), row.s(), row.sh->exp); };
     u64 total = 0;
-    for (int i = tid; i < n; i += CL_THREADS) total += sh.list[i] & W;
+    for (int i = tid; i < n; i += CL_THREADS) total += weight_of(sh.list[i]);
     u64 all;
     block_scan(total, sh.warp_mass, row.lane, row.warp, all);
     const u64 target = draw_target(u, all);
     u64 carry = 0;
     for (int base = 0; base < n; base += CL_THREADS) {
         const int i = base + tid;
-        const u64 e = i < n ? sh.list[i] : 0, w = e & W;
+        const u64 e = i < n ? sh.list[i] : 0, w = i < n ? weight_of(e) : 0;
         u64 sum;
         const u64 incl = carry + block_scan(w, sh.warp_mass, row.lane, row.warp, sum);
-        if (i < n && incl - w <= target && target < incl) {
-            const int index = (int)(CL_INDEX_MASK - (uint32_t)(e >> (CL_UNIT + 1)));
-            const float z = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row.sh->src)[index] << 16)
-                                 : reinterpret_cast<const float*>(row.sh->src)[index];
-            put_token(P, at_row, index, z, sh, row.s().top, log_total(all, sh.exp));
-        }
+        if (i < n && incl - w <= target && target < incl)
+            put_token(P, at_row, (int)(CL_INDEX_MASK - (uint32_t)(e >> 32)), key_value<BF16>((uint32_t)e), sh, row.s().top,
+                      log_total(all, row.s().unit, sh.exp));
         carry += sum;
     }
 }
@@ -1014,7 +1014,7 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
         __syncthreads();
         if (last >= 0 && last == sh.first_largest)
             each_weight([&](u64, int index, float z) {
-                if (index == last) put_token(P, at_row, index, z, sh, row.s().top, log_total(total, sh.exp));
+                if (index == last) put_token(P, at_row, index, z, sh, row.s().top, log_total(total, row.s().unit, sh.exp));
             });
         return;
     }
@@ -1022,7 +1022,7 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
     u64 at = incl - mine;
     if (at <= goal && goal < incl) {
         each_weight([&](u64 w, int index, float z) {
-            if (at <= goal && goal < at + w) put_token(P, at_row, index, z, sh, row.s().top, log_total(total, sh.exp));
+            if (at <= goal && goal < at + w) put_token(P, at_row, index, z, sh, row.s().top, log_total(total, row.s().unit, sh.exp));
             at += w;
         });
     }
@@ -1103,8 +1103,8 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
                     to_list(z1, i0 + e + 1);
                 }
             });
-            all = sum.total();
-            above = upper.total();
+            all = sum.total(s.unit);
+            above = upper.total(s.unit);
         } else {
             row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
                 const int i0 = row.index(v);
@@ -1171,7 +1171,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
 // thread's sums of at most 132 terms by 2^-17). Where the place is the same whatever that error, it is
 // found: so for rows whose mass lies with few tokens, in one cheap pass instead of
 // the exact ones. Else 0, and the list is empty. about: the sum of all weights in
-// their unit.
+// units of 2^-44; from here on it gives the row's unit.
 template <bool BF16>
 __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int groups, u64 highest, float& about, uint32_t& n) {
     using R = Row<BF16>;
@@ -1219,6 +1219,9 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
     others = warp_sum(others);
     listed = warp_sum(listed);
     about = (float)(others + listed);
+    // (the sum is right to 2^-15)
+    if (threadIdx.x == 0) set_unit(sh.s, unit_of(about * 0x1.0008p-44f));
+    __syncthreads();
     if ((float)listed < about * top_p) return 0;  // (what is near is left to the exact passes)
     n = gather(row, lo, highest);
     if (row.rank() == 0) {
@@ -1229,7 +1232,9 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
             for (int i = threadIdx.x; i < (int)n; i += CL_THREADS) m += weight(key_value<BF16>(place_key(sh.list[i])), row.s(), sh.exp);
             block_scan(m, sh.warp_mass, row.lane, row.warp, listed);
             // (2^18: the units to which the warps' sums were rounded, and more)
-            const u64 error = (others >> 15) + (1ull << 18);
+            const int up = row.s().unit - 44;
+            const u64 error = ((others >> 15) + (1ull << 18)) << up;
+            others <<= up;
             const u64 goal = goal_of(top_p, listed + others - min(others, error)), goal_hi = goal_of(top_p, listed + others + error);
             place = reach_in_list(row, (int)n, false, 0, goal, goal_hi);
         }
@@ -1426,7 +1431,10 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
         if constexpr (DRAW) return;
     } else {
         const RowScale& s = sh.s;
-        if (tid == 0) set_scale(sh.s, row_top, sh.ch, sh.cl, sh.low_by);
+        if (tid == 0) {
+            set_scale(sh.s, row_top, sh.ch, sh.cl, sh.low_by);
+            set_unit(sh.s, unit_of((float)k));  // (the sum is not above that)
+        }
         __syncthreads();
         const u64 highest = (u64)key_of<BF16>(s.top) << CL_INDEX_BITS | CL_INDEX_MASK;
         // min-p: z >= max + T ln(min_p)

@@ -11,7 +11,8 @@ typedef unsigned long long u64;
 
 constexpr int CL_EXP_BITS = 8;
 constexpr int CL_EXP = 1 << CL_EXP_BITS;  // entries of the table of 2^(i / 256)
-constexpr int CL_UNIT = 44;               // weights are in units of 2^-44
+constexpr int CL_FRACTION = 44;           // bits behind the point of a weight's mantissa in [1, 2)
+constexpr float CL_MAGIC = 12582912.0f;   // 1.5 * 2^23: adding it rounds to whole numbers
 
 // 2^(i / 256) as the sum of two floats.
 struct alignas(8) ExpEntry {
@@ -48,37 +49,53 @@ struct RowScale {
     float ch, cl;    // 256 log2(e) / T in two floats
     float low;       // a logit of weight 2^-100; NaN where the row's maximum has no room for one
     float shift, frac, rest;  // for WeightSum, where there is room
+    int unit;        // weights are whole numbers in units of 2^-unit
+    float none;      // what an exponent has to lie above, 2 more than the unit's
 };
+
+// The finest unit in which weights of this sum (at least 1/2) stay below 2^63. Equal
+// weights are all rounded the same way, so that the unit's half counts as often as
+// there are tokens: V 2^-62 of the sum or less. (In units of 2^-44 throughout, as many
+// as 262144 largest weights leave room for, 262143 logits 28 below the largest were
+// off by 1.3 %, their sum by 2e-9 of the row's.)
+__device__ __forceinline__ int unit_of(float sum) {
+    const int e = (int)(__float_as_uint(sum) >> 23) - 127;
+    return e < 0 ? 62 : 62 - e;
+}
+__device__ __forceinline__ float none_of(int unit) { return CL_MAGIC - (float)((unit + 2) * CL_EXP); }
+__device__ __forceinline__ void set_unit(RowScale& s, int unit) {
+    s.unit = unit;
+    s.none = none_of(unit);
+}
 
 // What a row's maximum decides; low_by: how far below it a weight is 2^-100.
 __device__ __forceinline__ void set_scale(RowScale& s, float top, float ch, float cl, float low_by) {
     // (rounded as WeightSum rounds it: from y, next to a half, the maximum's own
     // exponent came out as 1 / 256)
-    const float y = __fmul_rn(top, ch), whole = __fsub_rn(__fmaf_rn(top, ch, 12582912.0f), 12582912.0f);
+    const float y = __fmul_rn(top, ch), whole = __fsub_rn(__fmaf_rn(top, ch, CL_MAGIC), CL_MAGIC);
     s.top = top;
     s.ch = ch;
     s.cl = cl;
     s.low = fabsf(y) < 0x1p21f ? top - low_by : __uint_as_float(0x7fc00000u);
-    s.shift = 12582912.0f - whole;
+    s.shift = CL_MAGIC - whole;
     const float a = __fsub_rn(y, whole), low = __fmaf_rn(top, cl, __fmaf_rn(top, ch, -y)), frac = __fadd_rn(a, low);
     s.frac = frac;
     s.rest = -__fadd_rn(__fsub_rn(a, frac), low) * CL_L1;
 }
 
-// exp((z - top) / T) in units of 2^-44, for the few elements that decide: those of a
+// exp((z - top) / T) in units of 2^-unit, for the few elements that decide: those of a
 // list, of a draw's last part, of a pass that is made again. With d = z - top in two
 // floats, exactly, y = 256 d log2(e) / T = n + r + x, n whole, |r| <= 1/2 and x its
 // rounding errors: 2^(n / 256) = hi + lo comes from the table and a shift, and with u
 // = (r + x) ln 2 / 256 = uh + ul in two floats e^u - 1 = uh + el from its series, el
-// with every term that uh and ul have in common. Right to 2^-40 of itself and two
-// units; the maximum's is 2^44 exactly.
-__device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry* table) {
+// with every term that uh and ul have in common. Right to 2^-40 of itself and half a
+// unit; the maximum's is 2^unit exactly.
+__device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry* table, int unit, float none) {
     const float dh = __fsub_rn(z, s.top);
     const float bb = __fsub_rn(dh, z);
     const float dl = __fsub_rn(__fsub_rn(z, __fsub_rn(dh, bb)), __fadd_rn(s.top, bb));
-    constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23: adding it rounds to whole numbers
-    const float t = __fmaf_rn(dh, s.ch, MAGIC);
-    const float p = __fmul_rn(dh, s.ch), r = __fsub_rn(p, __fsub_rn(t, MAGIC));
+    const float t = __fmaf_rn(dh, s.ch, CL_MAGIC);
+    const float p = __fmul_rn(dh, s.ch), r = __fsub_rn(p, __fsub_rn(t, CL_MAGIC));
     const float x = __fmaf_rn(dl, s.ch, __fmaf_rn(dh, s.cl, __fmaf_rn(dh, s.ch, -p)));
     const float uh = __fmul_rn(r, CL_L1), ul = __fmaf_rn(x, CL_L1, __fmaf_rn(r, CL_L1_LOW, __fmaf_rn(r, CL_L1, -uh)));
     const float el = __fmaf_rn(__fmul_rn(uh, uh), __fmaf_rn(uh, __fmaf_rn(uh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f),
@@ -87,12 +104,14 @@ __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry
     const ExpEntry en = table[tb & (CL_EXP - 1)];  // (the magic number's low bits are 0)
     const float second = __fmul_rn(en.hi, uh);
     const float third = __fadd_rn(__fmaf_rn(en.hi, el, __fmaf_rn(en.lo, uh, en.lo)), __fmaf_rn(en.hi, uh, -second));
-    const u64 q = ((u64)((__float_as_uint(en.hi) & 0x7FFFFFu) | 0x800000u) << (CL_UNIT - 23)) +
+    const u64 q = ((u64)((__float_as_uint(en.hi) & 0x7FFFFFu) | 0x800000u) << (CL_FRACTION - 23)) +
                   (u64)(__float2ll_rn(__fmul_rn(second, 0x1p44f)) + __float2int_rn(__fmul_rn(third, 0x1p44f)));
-    const uint32_t sh = (0x4B400000u + CL_EXP - 1 - tb) >> CL_EXP_BITS;  // ceil(-n / 256)
-    const u64 w = (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63);
-    return t > MAGIC - 46.0f * CL_EXP ? w : 0ull;  // (and where d is -inf)
+    const int k = (int)((0x4B400000u + CL_EXP - 1 - tb) >> CL_EXP_BITS);  // ceil(-n / 256)
+    const int sh = k + CL_FRACTION - unit;                               // at most 46
+    const u64 w = sh >= 0 ? (q + ((1ull << (sh & 63)) >> 1)) >> (sh & 63) : q << (-sh & 63);
+    return t > none ? w : 0ull;  // (and where d is -inf)
 }
+__device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry* table) { return weight(z, s, table, s.unit, s.none); }
 
 // Adds up weights in floats, two elements at a time in packed instructions, for
 // the passes over whole rows (shifting integers took twice as long). Here y = z c -
@@ -136,13 +155,14 @@ struct WeightSum {
         pair(z0, z1, r, table, a, rest);
         add(a, rest);
     }
-    __device__ __forceinline__ u64 total() const {
+    __device__ __forceinline__ u64 total(int unit) const {
         float s0, s1, c0, c1;
         unpack2(s, s0, s1);
         unpack2(c, c0, c1);
         // (differences from 1 are exact, and a double's units are few)
         const ff sum = two_sum(__fsub_rn(s0, 1.0f), __fsub_rn(s1, 1.0f));
-        const long long v = __float2ll_rn(sum.hi * 0x1p44f) + __float2ll_rn(__fadd_rn(sum.lo, __fadd_rn(c0, c1)) * 0x1p44f);
+        const float units = __uint_as_float((uint32_t)(127 + unit) << 23);
+        const long long v = __float2ll_rn(sum.hi * units) + __float2ll_rn(__fadd_rn(sum.lo, __fadd_rn(c0, c1)) * units);
         return v > 0 ? (u64)v : 0ull;
     }
 };

@@ -53,13 +53,19 @@ static sv::RowScale scale(float top, float T) {
     const double c = 1.4426950408889634 * sv::CL_EXP * (1.0 / (double)T);
     sv::RowScale s;
     sv::set_scale(s, top, (float)c, (float)(c - (double)(float)c), (float)(100.0 / 1.4426950408889634) * T);
+    sv::set_unit(s, 44);
     return s;
 }
 
-extern "C" int cut_unit() { return sv::CL_UNIT; }
+extern "C" int cut_unit() { return 44; }
+extern "C" int cut_unit_of(float sum) { return sv::unit_of(sum); }
 
 // Each logit's weight in units.
 extern "C" void cut_weights(const float* z, int n, float top, float T, unsigned long long* out) {
     const sv::RowScale s = scale(top, T);
     for (int i = 0; i < n; ++i) out[i] = sv::weight(z[i], s, table.e);
+}
+extern "C" void cut_weights_in(const float* z, int n, float top, float T, int unit, unsigned long long* out) {
+    const sv::RowScale s = scale(top, T);
+    for (int i = 0; i < n; ++i) out[i] = sv::weight(z[i], s, table.e, unit, sv::none_of(unit));
 }

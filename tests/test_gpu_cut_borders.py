@@ -1,0 +1,83 @@
+"""Cuts and draws whose goal lies next to a border: within 1e-11 of the sum, as the
+interface says, they are those of the definition (cut_borders.py)."""
+import numpy as np
+import pytest
+import torch
+
+from cut_borders import Row
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def api():
+    import speculative_decoding_verification_24_gb300 as sv
+    return sv
+
+
+def cuts(z, ps, **kw):
+    """What is kept of the row z [V] for each top-p: masks [len(ps), V]."""
+    ps = torch.as_tensor(np.asarray(ps, np.float32)).cuda()
+    flags, n = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(len(ps), dtype=torch.int32, device="cuda")
+    out = api().spec_truncate_logits(z.cuda().expand(len(ps), -1), top_p=ps, out_n_kept=n, status_word=flags,
+                                     out=torch.empty(len(ps), len(z), dtype=z.dtype, device="cuda"), **kw)
+    kept = (out > float("-inf")).cpu().numpy()
+    assert flags.item() == 0 and n.tolist() == kept.sum(1).tolist()
+    return kept
+
+
+def draws(z, us, **kw):
+    us = torch.as_tensor(np.asarray(us, np.float32)).cuda()
+    return api().spec_sample(z.cuda().expand(len(us), -1), us, **kw).tolist()
+
+
+FAR = pytest.mark.parametrize("V,far,ps", [
+    (200000, 25.0, (0.999999,)), (262144, 28.0, (1 - 2.0 ** -23,)), (250000, 22.5, (0.99998, 0.99999)), (262144, 22.0, (0.99995, 0.9999)),
+    (3000, 24.0, (1 - 2.0 ** -23, 1 - 2.0 ** -24)), (40000, 20.0, (0.99999, 0.9999999)),
+])
+
+
+def far_below(V, far, dtype):
+    z = torch.full((V,), -far).to(dtype)
+    z[V // 3] = 0.0
+    return z
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
+@FAR
+def test_many_equal_logits_far_below_the_first(dtype, V, far, ps):
+    z = far_below(V, far, dtype)
+    for k in (0, 1500):
+        row = Row(z.double().numpy(), k=k)
+        for p, kept in zip(ps, cuts(z, ps, top_k=k)):
+            row.check_count(row.count_of(kept), p)
+
+
+def usual(V, dtype, sigma, seed):
+    z = (torch.randn(V, generator=torch.Generator().manual_seed(seed)) * sigma).to(dtype)
+    if seed % 2:
+        z[seed % V] = z.float().max() + 3 * sigma  # a few tokens hold most
+        z[(7 * seed) % V] = z.float().max() - sigma
+    return z
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
+def test_short_lists_next_to_a_border(dtype):
+    """top-k of up to 2048: sums in a list."""
+    checked = 0
+    for seed, V, sigma, k in ((1, 5000, 2.0, 50), (2, 32000, 2.0, 128), (3, 32000, 1.0, 129), (4, 5000, 0.3, 1500), (6, 32000, 0.2, 2048),
+                              (8, 151936, 0.5, 2000), (10, 151936, 0.3, 1024)):
+        z = usual(V, dtype, sigma, seed)
+        row = Row(z.double().numpy(), 0.9, k)
+        ps = row.near_cuts(40, most=2e-9)
+        if len(ps):
+            for p, kept in zip(ps, cuts(z, ps, temperature=0.9, top_k=k)):
+                row.check_count(row.count_of(kept), p)
+                checked += 1
+        us = row.near_draws(40, most=2e-9)
+        if len(us):
+            for u, token in zip(us, draws(z, us, temperature=0.9, top_k=k)):
+                row.check_token(token, u)
+                checked += 1
+    assert checked > 20
