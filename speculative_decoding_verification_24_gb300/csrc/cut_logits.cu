@@ -636,8 +636,9 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
 #pragma unroll
                 for (int e = 0; e < R::E; e += 2) {
                     const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
-                    sum.add(z0 >= from ? z0 : row.s().low, z1 >= from ? z1 : row.s().low, row.s(), copy);
+                    sum.add(z0 >= from ? z0 : row.s().low, z1 >= from ? z1 : row.s().low, row.s(), copy, e == 0);
                 }
+                sum.end_piece();
             }
         });
         m += sum.total(row.s().unit);
@@ -1066,10 +1067,8 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     u64 goal;
     // The sum of all weights and of those above the first of these bins, and what
     // lies in them to the list. Where the goal comes so near to a border that the
-    // sums in floats may err (one row in thousands), or the list does not hold it,
-    // once more with every weight formed by weight(). (Of 460,800 rows of all settings
-    // one then keeps another token than 64-bit arithmetic does, at a sum 1e-12 from the
-    // goal; it costs the others the check, 250 -> 263 us for 256 flat rows of 151936.)
+    // sums in floats may err (a flat row in a thousand or two), or the list does not hold it,
+    // once more with every weight formed by weight().
     for (bool precise = !(s.low == s.low);; precise = true) {
         const float z_hi = bin0 > 0 ? __fsub_rn(s.top, (float)bin0 / to_bin) : INFINITY;
         const float z_lo = key_value<BF16>(key_of<BF16>(__fsub_rn(s.top, (float)(bin1 + 1) / to_bin)));
@@ -1093,15 +1092,17 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
                     const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
                     f32x2 a, rest;
                     WeightSum::pair(z0 >= s.low ? z0 : s.low, z1 >= s.low ? z1 : s.low, s, copy, a, rest);
-                    sum.add(a, rest);
+                    sum.add(a, rest, e == 0);
                     float a0, a1, r0, r1;
                     unpack2(a, a0, a1);
                     unpack2(rest, r0, r1);
                     const bool up0 = z0 >= from, up1 = z1 >= from;
-                    upper.add(pack2(up0 ? a0 : 0.0f, up1 ? a1 : 0.0f), pack2(up0 ? r0 : 0.0f, up1 ? r1 : 0.0f));
+                    upper.add(pack2(up0 ? a0 : 0.0f, up1 ? a1 : 0.0f), pack2(up0 ? r0 : 0.0f, up1 ? r1 : 0.0f), e == 0);
                     to_list(z0, i0 + e);
                     to_list(z1, i0 + e + 1);
                 }
+                sum.end_piece();
+                upper.end_piece();
             });
             all = sum.total(s.unit);
             above = upper.total(s.unit);
@@ -1136,7 +1137,10 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
             mass_above = warp_sum(mass_above);
             if (n <= CL_LIST) {
                 sort_list(sh, n, lo, min(highest, over - 1));
-                const u64 unsure = precise ? 0 : all >> 33;
+                // (of the weights' own errors those above count 1 - p, the others p)
+                const float fa = (float)all, fm = (float)mass_above;
+                const u64 unsure = precise ? 0 : (u64)(CL_PAIR_ERROR * (top_p * (fa - fm) + (1.0f - top_p) * fm) +
+                                                       sum_error(top_p * fa + fm, sh.V, s.unit));
                 place = reach_in_list(row, n, any_above, mass_above, goal - min(goal, unsure), goal + unsure);
                 // what of the list is kept joins its warps' sums
                 if (place) {

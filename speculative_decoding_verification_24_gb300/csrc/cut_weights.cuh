@@ -118,15 +118,24 @@ __device__ __forceinline__ u64 weight(float z, const RowScale& s, const ExpEntry
 // top c, formed at once: r.shift is the magic number less the whole part of top c
 // and r.frac the rest, so that t's low bits are n again. What r.frac's rounding
 // dropped would move all weights alike, by 2^-34 of themselves; it is added to e,
-// whose own rounding takes it up on average: a row's sum is right to about 2^-37.
-// The maximum's own weight is made 1 exactly, which keeps ties exact. w = (hi + (lo
-// + hi e)) 2^-k; the sum s of the first parts begins at 1, so that s >= any of them
-// and a - (s' - s) is the rounding error of s' = s + a exactly; c takes those and
-// the second parts. Where top-p's goal comes within 2^-33 of a border the sum
-// decides nothing (cut_by_mass).
+// whose own rounding takes it up on average. The maximum's own weight is made 1
+// exactly, which keeps ties exact. w = (hi + (lo + hi e)) 2^-k; the sum s of the first
+// parts begins at 1, so that s >= any of them and a - (s' - s) is the rounding error of
+// s' = s + a exactly. A piece's errors and second parts are added up and go to c,
+// whose own errors go to d.
+//
+// What that leaves. A weight: |x| <= 1.2 is rounded three times (2^-26, 2^-25, 2^-24,
+// times ln 2 / 256), its polynomial twice (2^-33 each), ln 2 / 256 once (2^-33.3),
+// hi e + lo once (2^-32.3 of hi): CL_PAIR_ERROR of itself. A piece's sum: 4 additions
+// at most that a second part (2^-8.2 of its weight) meets, 2^-24 each: CL_ADD_ERROR.
+// First parts too small for s go to c whole, rounded like the others: 4 2^-24 of V
+// weights of at most 2^-24 of what s is, 1 and the thread's own (sum_error). Over the
+// thousands of weights of a usual row these cancel, to about 2^-37 of the sum; where a
+// decision comes nearer than the bound it is made with weight() (cut_by_mass).
+constexpr float CL_PAIR_ERROR = 0x1p-30f, CL_ADD_ERROR = 0x1.8p-31f;
 struct WeightSum {
-    f32x2 s, c;
-    __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)) {}
+    f32x2 s, c, d, part;
+    __device__ __forceinline__ WeightSum() : s(pack2(1.0f, 1.0f)), c(pack2(0.0f, 0.0f)), d(c), part(c) {}
     // The two parts of a pair's weights; z0, z1 >= r.low.
     static __device__ __forceinline__ void pair(float z0, float z1, const RowScale& r, const ExpEntry* table, f32x2& a, f32x2& rest) {
         const f32x2 z = pack2(z0, z1), minus = pack2(-1.0f, -1.0f), ch = pack2(r.ch, r.ch), shift = pack2(r.shift, r.shift);
@@ -145,26 +154,44 @@ struct WeightSum {
         a = pack2(__fmul_rn(p.hi, pow0), __fmul_rn(q.hi, pow1));
         rest = pack2(__fmul_rn(__fmaf_rn(p.hi, e0, p.lo), pow0), __fmul_rn(__fmaf_rn(q.hi, e1, q.lo), pow1));
     }
-    __device__ __forceinline__ void add(f32x2 a, f32x2 rest) {
-        const f32x2 minus = pack2(-1.0f, -1.0f), sum = add2(s, a);
-        c = add2(c, add2(fma2(fma2(s, minus, sum), minus, a), rest));
+    // One pair of a piece, whose last one is followed by end_piece().
+    __device__ __forceinline__ void add(f32x2 a, f32x2 rest, bool first) {
+        const f32x2 minus = pack2(-1.0f, -1.0f), sum = add2(s, a), q = add2(fma2(fma2(s, minus, sum), minus, a), rest);
+        part = first ? q : add2(part, q);
         s = sum;
     }
-    __device__ __forceinline__ void add(float z0, float z1, const RowScale& r, const ExpEntry* table) {
+    __device__ __forceinline__ void end_piece() {
+        // (Knuth's two-sum: either may be the larger one)
+        const f32x2 minus = pack2(-1.0f, -1.0f), sum = add2(c, part), of_part = fma2(c, minus, sum), of_c = fma2(of_part, minus, sum);
+        d = add2(d, add2(fma2(of_c, minus, c), fma2(of_part, minus, part)));
+        c = sum;
+    }
+    __device__ __forceinline__ void add(float z0, float z1, const RowScale& r, const ExpEntry* table, bool first) {
         f32x2 a, rest;
         pair(z0, z1, r, table, a, rest);
-        add(a, rest);
+        add(a, rest, first);
     }
     __device__ __forceinline__ u64 total(int unit) const {
-        float s0, s1, c0, c1;
+        float s0, s1, c0, c1, d0, d1;
         unpack2(s, s0, s1);
         unpack2(c, c0, c1);
+        unpack2(d, d0, d1);
         // (differences from 1 are exact, and a double's units are few)
-        const ff sum = two_sum(__fsub_rn(s0, 1.0f), __fsub_rn(s1, 1.0f));
+        const ff sum = two_sum(__fsub_rn(s0, 1.0f), __fsub_rn(s1, 1.0f)), more = two_sum(c0, c1);
         const float units = __uint_as_float((uint32_t)(127 + unit) << 23);
-        const long long v = __float2ll_rn(sum.hi * units) + __float2ll_rn(__fadd_rn(sum.lo, __fadd_rn(c0, c1)) * units);
+        const long long v = __float2ll_rn(sum.hi * units) + __float2ll_rn(more.hi * units) +
+                            __float2ll_rn(__fadd_rn(__fadd_rn(sum.lo, more.lo), __fadd_rn(d0, d1)) * units);
         return v > 0 ? (u64)v : 0ull;
     }
 };
+
+// What two sums in units of 2^-unit, or one sum and a part of it, and their
+// difference may be off by together, beside CL_PAIR_ERROR of each weight: `sum` is
+// both added up. (Behind it: a unit and a half for each of 8 CTAs' threads, half a one
+// for each of a list's entries or a part's elements.)
+__device__ __forceinline__ float sum_error(float sum, int V, int unit) {
+    const float one = __uint_as_float((uint32_t)(127 + unit) << 23);
+    return sum * CL_ADD_ERROR + (float)V * 0x1p-45f * (one + sum * (1.0f / 512.0f)) + 32768.0f;
+}
 
 }  // namespace sv

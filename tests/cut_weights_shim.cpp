@@ -69,3 +69,23 @@ extern "C" void cut_weights_in(const float* z, int n, float top, float T, int un
     const sv::RowScale s = scale(top, T);
     for (int i = 0; i < n; ++i) out[i] = sv::weight(z[i], s, table.e, unit, sv::none_of(unit));
 }
+
+// The sum of one thread's logits in floats, in units of 2^-unit: pieces of `per`
+// elements, an even number of them; below `low` a logit counts as that.
+extern "C" unsigned long long cut_sum(const float* z, int n, float top, float T, int per, int unit) {
+    static sv::ExpEntry copies[sv::CL_EXP * sv::CL_COPIES];
+    for (int i = 0; i < sv::CL_EXP * sv::CL_COPIES; ++i) copies[i] = table.e[i / sv::CL_COPIES];
+    const sv::RowScale s = scale(top, T);
+    sv::WeightSum sum;
+    for (int i = 0; i + per <= n; i += per) {
+        for (int e = 0; e < per; e += 2) {
+            const float a = z[i + e], b = z[i + e + 1];
+            sum.add(a >= s.low ? a : s.low, b >= s.low ? b : s.low, s, copies, e == 0);
+        }
+        sum.end_piece();
+    }
+    return sum.total(unit);
+}
+
+extern "C" float cut_pair_error() { return sv::CL_PAIR_ERROR; }
+extern "C" float cut_sum_error(float sum, int V, int unit) { return sv::sum_error(sum, V, unit); }

@@ -81,3 +81,54 @@ def test_the_unit_leaves_room_for_the_sum(shim):
         assert unit == 62 or np.float64(np.float32(sum_)) * 2.0 ** unit >= 2.0 ** 62
     # what the kernel adds up beforehand is right to 2^-15, and taken as 2^-13 more
     assert shim.cut_unit_of(2.0 ** 18 * (1 + 2.0 ** -13)) == 44
+
+
+def sums(shim, z, top, T, per, unit):
+    """Rows [threads, n] of one thread's logits each: their sums in floats."""
+    shim.cut_sum.restype = ctypes.c_uint64
+    return [shim.cut_sum(at(r), len(r), ctypes.c_float(top), ctypes.c_float(T), per, unit) for r in map(f32, z)]
+
+
+def check_sums(shim, z, top, T, per):
+    """Every thread's sum against the weights' own errors and the sums'."""
+    shim.cut_pair_error.restype = shim.cut_sum_error.restype = ctypes.c_float
+    shim.cut_sum_error.argtypes = [ctypes.c_float, ctypes.c_int, ctypes.c_int]
+    want = exact(f32(z).reshape(-1), top, T).reshape(np.shape(z)).sum(1)
+    unit = shim.cut_unit_of(ctypes.c_float(float(want.max()) + 1.0))
+    got = np.array(sums(shim, z, top, T, per, unit), np.uint64).astype(np.longdouble) * np.longdouble(2.0) ** -unit
+    # (the constant behind sum_error is for all threads of 8 CTAs: 1.5 units each here)
+    bound = [shim.cut_pair_error() * float(x) + (shim.cut_sum_error(float(x) * 2.0 ** unit, z.shape[1], unit) - 32768 + 2) * 2.0 ** -unit
+             for x in want]
+    off = np.abs(got - want).astype(np.float64)
+    assert (off <= bound).all(), float((off / bound).max())
+    return float((off / want.astype(np.float64)).max())
+
+
+@pytest.mark.parametrize("per", (4, 8))
+def test_sums_in_floats_keep_their_bound(shim, per):
+    rng = np.random.default_rng(3)
+    for T, offset in ((1.0, 0.0), (0.7, 8.0), (1.3, -40.0), (0.05, 30.0), (2.0, 1000.0)):
+        top = np.float32(offset)
+        for n in (8, 64, 512):
+            for sigma in (0.1, 1.0, 4.0, 12.0):
+                z = np.minimum(f32(offset - np.abs(rng.normal(size=(40, n)) * sigma * T)), top)
+                check_sums(shim, z, top, T, per)
+
+
+@pytest.mark.parametrize("per", (4, 8))
+def test_sums_in_floats_of_few_and_of_equal_weights(shim, per):
+    """A single weight's error counts whole, and equal ones' errors all the same way:
+    of weights too small for the first sum, too."""
+    rng = np.random.default_rng(4)
+    worst = 0.0
+    for T, offset in ((1.0, 0.0), (0.7, 7.3), (1.3, -90.0), (0.9, 400.0)):
+        top = np.float32(offset)
+        z = f32(np.full((20000, 8), offset - 200.0 * T))
+        z[:, 3] = np.minimum(f32(offset - rng.uniform(0, 3, 20000) * T), top)
+        worst = max(worst, check_sums(shim, z, top, T, per))
+        for below in (0.37, 3.0, 9.0, 15.9, 16.6, 17.3, 22.0, 28.0):
+            for first in (0.0, 5.0):
+                z = f32(np.full((20, 512), offset - below * T) - rng.uniform(0, 0.01, (20, 1)) * T)
+                z[:, 7] = offset - first * T
+                check_sums(shim, np.minimum(z, top), top, T, per)
+    assert worst > 2.0 ** -33  # as single weights are off by

@@ -63,6 +63,32 @@ def usual(V, dtype, sigma, seed):
 
 
 @pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
+@pytest.mark.parametrize("V,sigma,T", ((5000, 3.0, 0.8), (5000, 0.5, 1.0), (32000, 1.0, 1.3), (151936, 1.0, 1.0), (151936, 1.5, 1.0), (262144, 0.3, 1.0)))
+def test_cuts_next_to_a_border(dtype, V, sigma, T):
+    checked = 0
+    for seed in (2, 3, 4):
+        z = usual(V, dtype, sigma, seed)
+        for k in (0, 3000, V - V // 5):
+            if k and k >= V:
+                continue
+            row = Row(z.double().numpy(), T, k)
+            ps = row.near_cuts(48)
+            checked += len(ps)
+            if not len(ps):
+                continue
+            kept = cuts(z, ps, temperature=T, top_k=k)
+            for p, x in zip(ps, kept):
+                row.check_count(row.count_of(x), p)
+            # and a draw of what is kept, next to an edge of it
+            n = row.count_of(kept[0])
+            us = row.near_draws(4, n=n)
+            if len(us):
+                for u, token in zip(us, draws(z, us, temperature=T, top_k=k, top_p=float(ps[0]))):
+                    row.check_token(token, u, n)
+    assert checked > 30
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
 def test_short_lists_next_to_a_border(dtype):
     """top-k of up to 2048: sums in a list."""
     checked = 0
@@ -81,3 +107,16 @@ def test_short_lists_next_to_a_border(dtype):
                 row.check_token(token, u)
                 checked += 1
     assert checked > 20
+
+
+@pytest.mark.parametrize("offset", (2.0 ** 15, -2.0 ** 15))
+def test_a_maximum_without_room_for_float_sums(offset):
+    """256 log2(e) max / T above 2^21: every weight is formed in whole units."""
+    z = usual(50000, F32, 2.0, 2) + offset
+    row = Row(z.double().numpy())
+    us, ps = row.near_draws(40), row.near_cuts(40)
+    for u, token in zip(us, draws(z, us)):
+        row.check_token(token, u)
+    for p, kept in zip(ps, cuts(z, ps)):
+        row.check_count(row.count_of(kept), p)
+    assert len(us) + len(ps) > 20
