@@ -661,11 +661,46 @@ __device__ __forceinline__ u64 sum_above(const Row<BF16>& row, u64 cut) {
     return warp_sum(total);
 }
 
+// The row's unit from then on, its sum being `total` in the present one (to 2^-27).
+template <bool BF16>
+__device__ __forceinline__ void refine_unit(const Row<BF16>& row, u64 total) {
+    CutShared& sh = *row.sh;
+    __syncthreads();  // everyone has used the present one
+    if (threadIdx.x == 0) set_unit(sh.s, unit_of((float)total * 0x1.0008p0f * __uint_as_float((uint32_t)(127 - sh.s.unit) << 23)));
+    __syncthreads();
+}
+
+// The whole part of u total, 0 <= u <= 1, and whether there is more: by whole
+// numbers, in every thread (one thread's doubles kept the others waiting).
+__device__ __forceinline__ u64 share_of(float u, u64 total, bool& more) {
+    const uint32_t b = __float_as_uint(u) & 0x7FFFFFFFu, exponent = max(b >> 23, 1u);
+    const u64 m = b >> 23 ? (b & 0x7FFFFFu) | 0x800000u : b;  // u = m 2^-shift
+    const int shift = 150 - (int)exponent;                    // 23 to 149
+    const u64 low = m * total, high = __umul64hi(m, total);   // (below 2^22)
+    if (shift < 64) {
+        more = (low << (64 - shift)) != 0;
+        return high << (64 - shift) | low >> shift;
+    }
+    const int rest = shift - 64;
+    more = low != 0 || (rest < 32 ? (uint32_t)high << 1 << (31 - rest) : (uint32_t)high) != 0;
+    return rest < 32 ? high >> rest : 0;
+}
+
+// The fewest units that are p of `total`.
+__device__ __forceinline__ u64 goal_of(float p, u64 total) {
+    bool more;
+    const u64 goal = share_of(p, total, more);
+    return goal + more;
+}
+
 // One round of the exact search in [lo, hi]: the bin in which the count `k`
 // (BY_MASS false) or the weight `goal` is reached from above, given what lies
-// above hi. The range becomes that bin.
+// above hi. The range becomes that bin. A goal of GOAL_OF_ALL becomes p of all weights
+// in the range: a share of the same whole numbers that are searched.
+constexpr u64 GOAL_OF_ALL = ~0ull;
 template <bool BF16, bool BY_MASS>
-__device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& hi, uint32_t& above, u64& mass_above, uint32_t k, u64 goal) {
+__device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& hi, uint32_t& above, u64& mass_above, uint32_t k, u64& goal,
+                                           float p) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     u64* mass = sh.list;
@@ -689,9 +724,9 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
 #pragma unroll 1
         for (int e = 0; e < R::E; ++e) {
             const float z = piece_elem<BF16>(x, e);
-            const u64 p = place_of(key_of<BF16>(z), i0 + e);
-            if (p < lo || p > hi) continue;
-            const int bin = (int)((p - lo) >> shift);
+            const u64 place = place_of(key_of<BF16>(z), i0 + e);
+            if (place < lo || place > hi) continue;
+            const int bin = (int)((place - lo) >> shift);
             atomicAdd(&sh.count[bin], 1u);
             if (BY_MASS) atomicAdd(&mass[bin], weight(z, row.s(), row.sh->exp));
         }
@@ -729,6 +764,11 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
         });
     }
     row.sync();
+    if (BY_MASS && goal == GOAL_OF_ALL) {
+        u64 all = 0;
+        for (int q = 0; q < CS; ++q) all += sh.seg_mass[q];
+        goal = goal_of(p, all);
+    }
     uint32_t c = above + c_total - c_in;
     u64 m = mass_above + m_total - m_in;
     for (int q = row.rank() + 1; q < CS; ++q) {
@@ -763,29 +803,6 @@ __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& h
     lo = new_lo;
     row.sync();  // everyone has read what was found
     return n;
-}
-
-// The whole part of u total, 0 <= u <= 1, and whether there is more: by whole
-// numbers, in every thread (one thread's doubles kept the others waiting).
-__device__ __forceinline__ u64 share_of(float u, u64 total, bool& more) {
-    const uint32_t b = __float_as_uint(u) & 0x7FFFFFFFu, exponent = max(b >> 23, 1u);
-    const u64 m = b >> 23 ? (b & 0x7FFFFFu) | 0x800000u : b;  // u = m 2^-shift
-    const int shift = 150 - (int)exponent;                    // 23 to 149
-    const u64 low = m * total, high = __umul64hi(m, total);   // (below 2^22)
-    if (shift < 64) {
-        more = (low << (64 - shift)) != 0;
-        return high << (64 - shift) | low >> shift;
-    }
-    const int rest = shift - 64;
-    more = low != 0 || (rest < 32 ? (uint32_t)high << 1 << (31 - rest) : (uint32_t)high) != 0;
-    return rest < 32 ? high >> rest : 0;
-}
-
-// The fewest units that are p of `total`.
-__device__ __forceinline__ u64 goal_of(float p, u64 total) {
-    bool more;
-    const u64 goal = share_of(p, total, more);
-    return goal + more;
 }
 
 // In the sorted list of n places, below others (if `any`) of weight mass_above: the
@@ -831,13 +848,14 @@ __device__ __forceinline__ float nth_group(CutShared& sh, int groups, int n) {
 }
 
 // 4. The place of the last element that a cut keeps, exactly, in [lo, hi]: the
-// range narrows until what is left fits the list, where it is picked.
+// range narrows until what is left fits the list, where it is picked. (goal, p: as
+// above)
 template <bool BF16, bool BY_MASS>
-__device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32_t k, u64 goal) {
+__device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32_t k, u64 goal, float p) {
     CutShared& sh = *row.sh;
     uint32_t above = 0, left = CL_LIST + 1;
     u64 mass_above = 0;
-    for (int round = 0; round < CL_ROUNDS && left > CL_LIST; ++round) left = narrow<BF16, BY_MASS>(row, lo, hi, above, mass_above, k, goal);
+    for (int round = 0; round < CL_ROUNDS && left > CL_LIST; ++round) left = narrow<BF16, BY_MASS>(row, lo, hi, above, mass_above, k, goal, p);
     const int n = (int)min(gather(row, lo, hi), (uint32_t)CL_LIST);
     if (row.rank() == 0) {
         sort_list(sh, n, lo, hi);
@@ -1163,7 +1181,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     }
     if (place == 0) {
         // more equal logits than the list takes, or a border that the histogram missed
-        place = find_cut<BF16, true>(row, CL_LOWEST, highest, 0, goal);
+        place = find_cut<BF16, true>(row, CL_LOWEST, highest, 0, goal, top_p);
         sum_above(row, place);
     }
     return place;
@@ -1499,15 +1517,16 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             uint32_t n = gather(row, bound, highest);
             bool listed = n <= CL_LIST;
             if (!listed) {
-                const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0);
+                const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0, 0.0f);
                 if (k <= CL_LIST) {
                     n = gather(row, cut_k, highest);
                     listed = true;
                 } else {
                     if (by_p) {
-                        const u64 mass = sum_above(row, cut_k);
+                        // (the sum in floats gives the unit alone)
+                        refine_unit(row, sum_above(row, cut_k));
                         row.sync();
-                        cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, goal_of(top_p, mass)));
+                        cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, GOAL_OF_ALL, top_p));
                     }
                     cut = max(cut, cut_k);
                 }

@@ -54,6 +54,16 @@ def test_many_equal_logits_far_below_the_first(dtype, V, far, ps):
             row.check_count(row.count_of(kept), p)
 
 
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
+@FAR
+def test_many_equal_logits_below_a_large_top_k(dtype, V, far, ps):
+    z = far_below(V, far, dtype)
+    for k in (2500, V - 7):
+        row = Row(z.double().numpy(), k=k)
+        for p, kept in zip(ps, cuts(z, ps, top_k=k)):
+            row.check_count(row.count_of(kept), p)
+
+
 def usual(V, dtype, sigma, seed):
     z = (torch.randn(V, generator=torch.Generator().manual_seed(seed)) * sigma).to(dtype)
     if seed % 2:
