@@ -29,7 +29,6 @@ struct CutParams {
     int32_t* n_kept;         // [B, R] or nullptr
     uint32_t* status;        // or nullptr
     int slice_vecs;          // 16-byte pieces of a row per CTA at most
-    int warp_vecs;           // of these per warp
     int longest_first;       // the rows' order
 };
 

@@ -105,8 +105,8 @@ struct alignas(16) CutShared {
     u64 seg_mass[CL_MAX_CS];
     uint32_t seg_count[CL_MAX_CS];
     // what a search has found, told to every CTA
-    u64 found_mass, found_place, draw_at;
-    uint32_t found_bin, found_from, found_to, found_above, found_count, draw_warp;
+    u64 found_mass, found_place, draw_at, draw_before;
+    uint32_t found_bin, found_from, found_to, found_above, found_count, draw_warp, drawn;
     uint32_t list_n, hits_n, counts[CL_MAX_CS];
     float bound;
     int first_largest, firsts[CL_MAX_CS], sequence;
@@ -277,6 +277,24 @@ struct Row {
         return (uint16_t)((b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) >> 16);
     }
 };
+
+// A CTA's part of the row at sh.src: `slice` pieces from piece `begin` on, of CS parts.
+template <bool BF16>
+__device__ __forceinline__ void set_part(CutShared& sh, int lead, int V, int begin, int slice, int CS, int rank) {
+    using R = Row<BF16>;
+    const int pieces = (lead + V + R::E - 1) / R::E;
+    begin = min(begin, pieces);
+    sh.base = reinterpret_cast<const uint4*>(sh.src - lead * R::ES) + begin;
+    sh.V = V;
+    sh.first = begin * R::E - lead;
+    sh.n_vecs = min(slice, pieces - begin);
+    sh.slice = slice;
+    sh.run = (slice + CL_WARPS - 1) / CL_WARPS;
+    sh.full0 = sh.first < 0 ? 1 : 0;
+    sh.full1 = sh.first + sh.n_vecs * R::E > V ? sh.n_vecs - 1 : sh.n_vecs;
+    sh.CS = CS;
+    sh.rank = rank;
+}
 
 // The list. Every CTA appends to its own (atomics on another CTA's memory took a
 // microsecond each) after begin_list, collect brings them to the first CTA's and
@@ -971,9 +989,13 @@ __device__ __forceinline__ void draw_list(const CutParams& P, const Row<BF16>& r
 }
 
 // Draws over the warps' parts, whose sums at or above `cut` lie in the first
-// CTA's part_mass: that finds the warp, and the warp the element.
+// CTA's part_mass: that finds the warp, and its CTA the element, by weight(). Where
+// the sums are in floats (not `precise`) and the target comes as near to the element's
+// edges as they may be off by, nothing is drawn, and that CTA gets false: a row in some
+// thousands, whose sums it then forms anew (the others have ended: with a barrier that
+// kept them 256 rows under min-p took 63 us, not 54).
 template <bool BF16>
-__device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& row, int64_t at_row, float u, u64 cut) {
+__device__ __forceinline__ bool draw_parts(const CutParams& P, const Row<BF16>& row, int64_t at_row, float u, u64 cut, bool precise) {
     using R = Row<BF16>;
     CutShared& sh = *row.sh;
     const int lane = row.lane;
@@ -993,6 +1015,7 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
             if (before <= target && target < before + m[i]) {
                 row.each_cta([&](CutShared* o) {
                     o->draw_warp = (uint32_t)(N * lane + i);
+                    o->draw_before = before;
                     o->draw_at = target - before;
                     o->found_mass = total;
                 });
@@ -1000,17 +1023,18 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
             before += m[i];
         }
     }
+    if (threadIdx.x == 0) sh.drawn = 0;
     row.sync();
     // The part's pieces, a run of neighbours for each thread of its CTA.
     const int part = (int)sh.draw_warp - row.rank() * CL_WARPS;
-    if (part < 0 || part >= CL_WARPS) return;
-    const u64 target = sh.draw_at, total = sh.found_mass;
+    if (part < 0 || part >= CL_WARPS) return true;
+    const u64 target = sh.draw_at, total = sh.found_mass, before = sh.draw_before;
     const uint32_t lo16 = R::lo16_of(cut);
     const int p0 = min(part * row.sh->run, row.n_vecs()), p1 = min(p0 + row.sh->run, row.n_vecs());
     const int per = (row.sh->run + CL_THREADS - 1) / CL_THREADS, v0 = min(p0 + (int)threadIdx.x * per, p1), v1 = min(v0 + per, p1);
     const auto each_weight = [&](auto&& f) {
         for (int v = v0; v < v1; ++v) {
-            if (row.keys()[v] < lo16) continue;
+            if (!precise && row.keys()[v] < lo16) continue;
             const uint4 x = row.load(v);
 #pragma unroll
             for (int e = 0; e < R::E; ++e) {
@@ -1019,32 +1043,56 @@ __device__ __forceinline__ void draw_parts(const CutParams& P, const Row<BF16>& 
             }
         }
     };
-    if (threadIdx.x == 0) sh.first_largest = -1;  // (free by now: the part's last element that can be drawn)
     u64 mine = 0, all;
-    int last = -1;
-    each_weight([&](u64 w, int index, float z) {
-        mine += w;
-        if (z > -INFINITY) last = index;
-    });
-    const u64 incl = block_scan(mine, sh.warp_mass, lane, row.warp, all);
-    if (all == 0) {
-        // weights of less than half a unit each, whose sum in floats is some units
-        if (last >= 0) atomicMax(&sh.first_largest, last);
-        __syncthreads();
-        if (last >= 0 && last == sh.first_largest)
-            each_weight([&](u64, int index, float z) {
-                if (index == last) put_token(P, at_row, index, z, sh, row.s().top, log_total(total, row.s().unit, sh.exp));
-            });
-        return;
-    }
-    const u64 goal = target < all ? target : all - 1;  // (the part's sum in floats may be a little more than this one)
-    u64 at = incl - mine;
-    if (at <= goal && goal < incl) {
+    each_weight([&](u64 w, int, float) { mine += w; });
+    u64 at = block_scan(mine, sh.warp_mass, lane, row.warp, all) - mine;
+    if (at <= target && target < at + mine) {
+        u64 slack = 0;
+        if (!precise) {
+            // (of the weights' own errors those before the part count 1 - u, the others u)
+            const float ft = (float)total, fb = (float)before, share = __saturatef(u);
+            slack = (u64)(CL_PAIR_ERROR * (share * (ft - fb) + (1.0f - share) * fb) + sum_error(share * ft + fb, sh.V, row.s().unit));
+            if (!(row.s().low == row.s().low)) slack += (u64)sh.V;  // (weight()'s halves of a unit)
+        }
         each_weight([&](u64 w, int index, float z) {
-            if (at <= goal && goal < at + w) put_token(P, at_row, index, z, sh, row.s().top, log_total(total, row.s().unit, sh.exp));
+            if (at <= target && target < at + w && (target - at >= slack || before + at == 0) && at + w - target > slack) {
+                put_token(P, at_row, index, z, sh, row.s().top, log_total(total, row.s().unit, sh.exp));
+                sh.drawn = 1;
+            }
             at += w;
         });
     }
+    __syncthreads();
+    return sh.drawn != 0;
+}
+
+// After a draw that came too near to an edge: the CTA that looked for the element takes
+// the whole row for its part, the unit from its sum, and forms the warps' parts' sums
+// by weight(). (It has no keys of most of these pieces.)
+template <bool BF16>
+__device__ __noinline__ void sum_alone(const Row<BF16> row, u64 cut) {
+    using R = Row<BF16>;
+    CutShared& sh = *row.sh;
+    refine_unit(row, sh.found_mass);
+    if (threadIdx.x == 0) {
+        const int lead = (int)(reinterpret_cast<uintptr_t>(sh.src) & 15) / R::ES;
+        set_part<BF16>(sh, lead, sh.V, 0, (lead + sh.V + R::E - 1) / R::E, 1, 0);
+    }
+    __syncthreads();
+    u64 m = 0;
+    const int end = row.v1();
+    for (int v = row.v0() + row.lane; v < end; v += 32) {
+        const uint4 x = row.load(v);
+        const int i0 = row.index(v);
+#pragma unroll 1
+        for (int e = 0; e < R::E; ++e) {
+            const float z = piece_elem<BF16>(x, e);
+            if (place_of(key_of<BF16>(z), i0 + e) >= cut) m += weight(z, row.s(), sh.exp);
+        }
+    }
+    m = warp_sum(m);
+    if (row.lane == 0) sh.part_mass[row.warp] = m;
+    __syncthreads();
 }
 
 // 3. Top-p alone. Returns the place of the last kept element and leaves the sums
@@ -1323,18 +1371,8 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     const char* src = P.logits + b * P.seq_bytes + r * P.row_bytes;
     const int lead = (int)(reinterpret_cast<uintptr_t>(src) & 15) / R::ES;  // elements before the row in its first piece
     if (tid == 0) {
-        const int pieces = (lead + P.V + R::E - 1) / R::E, begin = min(rank * P.slice_vecs, pieces);
         sh.src = src;
-        sh.base = reinterpret_cast<const uint4*>(src - lead * R::ES) + begin;
-        sh.V = P.V;
-        sh.first = begin * R::E - lead;
-        sh.n_vecs = min(P.slice_vecs, pieces - begin);
-        sh.slice = P.slice_vecs;
-        sh.run = P.warp_vecs;
-        sh.full0 = sh.first < 0 ? 1 : 0;
-        sh.full1 = sh.first + sh.n_vecs * R::E > P.V ? sh.n_vecs - 1 : sh.n_vecs;
-        sh.CS = CS;
-        sh.rank = rank;
+        set_part<BF16>(sh, lead, P.V, rank * P.slice_vecs, P.slice_vecs, CS, rank);
     }
     if (tid == 0) sh.first_largest = INT32_MAX;
     __syncthreads();
@@ -1595,7 +1633,9 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                 row.sync();
                 sum_above(row, cut);
             }
-            draw_parts(P, row, at_row, u, cut);
+            if (draw_parts(P, row, at_row, u, cut, false)) return;
+            sum_alone(row, cut);
+            draw_parts(P, row, at_row, u, cut, true);
             return;
         }
     }
@@ -1690,7 +1730,6 @@ static cudaError_t launch(CutParams p, int sms, cudaStream_t stream) {
     int cs = 1;
     while (cs < CL_MAX_CS && rows * cs <= (cs < 4 ? (int64_t)sms * (sums ? 4 : 1) : sms / 2) && vecs / cs > 4 * CL_THREADS) cs *= 2;
     p.slice_vecs = (vecs + cs - 1) / cs;
-    p.warp_vecs = (p.slice_vecs + CL_WARPS - 1) / CL_WARPS;
     const int smem = (int)sizeof(CutShared) + (p.slice_vecs + 15) / 8 * 16;
     if (smem > CL_ONE || rows * cs > INT32_MAX) return cudaErrorInvalidValue;
     p.longest_first = (p.temperatures || p.top_ks || p.top_ps) && p.B <= CL_ORDERED && rows * cs > 2 * sms;

@@ -56,6 +56,19 @@ def test_many_equal_logits_far_below_the_first(dtype, V, far, ps):
 
 @pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
 @FAR
+def test_draws_from_many_equal_logits_far_below_the_first(dtype, V, far, ps):
+    """Of all, of a list and of more than a list takes."""
+    z = far_below(V, far, dtype)
+    us = (0.5, 1 - 2.0 ** -24, 1 - 2.0 ** -22, 0.999999, 0.99999, 0.3)
+    for k in (0, 1500, 2500, V - 7):
+        if k < V:
+            row = Row(z.double().numpy(), k=k)
+            for u, token in zip(us, draws(z, us, top_k=k)):
+                row.check_token(token, u)
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
+@FAR
 def test_many_equal_logits_below_a_large_top_k(dtype, V, far, ps):
     z = far_below(V, far, dtype)
     for k in (2500, V - 7):
@@ -70,6 +83,29 @@ def usual(V, dtype, sigma, seed):
         z[seed % V] = z.float().max() + 3 * sigma  # a few tokens hold most
         z[(7 * seed) % V] = z.float().max() - sigma
     return z
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
+@pytest.mark.parametrize("V,sigma,T", ((2000, 3.0, 1.0), (5000, 3.0, 0.8), (5000, 1.0, 1.0), (32000, 2.0, 1.3), (151936, 1.5, 1.0), (151936, 3.0, 0.7)))
+def test_draws_next_to_an_edge(dtype, V, sigma, T):
+    checked = 0
+    for seed in (1, 2, 3, 4):
+        z = usual(V, dtype, sigma, seed)
+        row = Row(z.double().numpy(), T)
+        us = row.near_draws(64)
+        checked += len(us)
+        if len(us):
+            for x, token in zip(us, draws(z, us, temperature=T)):
+                row.check_token(token, x)
+        # of what a large top-k leaves
+        k = V - V // 5
+        row = Row(z.double().numpy(), T, k)
+        us = row.near_draws(32)
+        checked += len(us)
+        if len(us):
+            for x, token in zip(us, draws(z, us, temperature=T, top_k=k)):
+                row.check_token(token, x)
+    assert checked > 50
 
 
 @pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "fp32"))
@@ -130,3 +166,25 @@ def test_a_maximum_without_room_for_float_sums(offset):
     for p, kept in zip(ps, cuts(z, ps)):
         row.check_count(row.count_of(kept), p)
     assert len(us) + len(ps) > 20
+
+
+@pytest.mark.parametrize("offset,T", ((0.0, 1.0), (7.3, 0.7), (-90.0, 1.3), (400.0, 0.9)))
+def test_draws_next_to_an_edge_of_few_tokens(offset, T):
+    """Rows of 5 tokens, two of which hold most: the error of a single weight counts
+    whole. Of a million such rows those where some u lies next to an edge."""
+    g = torch.Generator().manual_seed(int(abs(offset)))
+    z = torch.randn(1_000_000, 5, generator=g) - 4.0
+    z[:, 1] = 0.0
+    z[:, 3] = -torch.rand(len(z), generator=g) * 3.0
+    z = z * T + offset
+    zd = z.double().numpy()
+    w = np.exp((zd - zd.max(1, keepdims=True)) / np.float64(np.float32(T)))
+    sums = w.cumsum(1)
+    edges = sums[:, 1] / sums[:, -1]  # (right to 1e-15)
+    u = edges.astype(np.float32)
+    gap = u.astype(np.float64) - edges
+    rows = np.nonzero((np.abs(gap) > 1.2e-11) & (np.abs(gap) < 2e-10))[0]
+    assert len(rows) > 2000
+    tokens = api().spec_sample(z[rows].cuda(), torch.from_numpy(u[rows]).cuda(), temperature=T).cpu().numpy()
+    # below the edge it is the token before it, else one behind it
+    assert np.array_equal(tokens <= 1, gap[rows] < 0), f"{int(((tokens <= 1) != (gap[rows] < 0)).sum())} of {len(rows)}"
