@@ -1133,7 +1133,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     u64 goal;
     // The sum of all weights and of those above the first of these bins, and what
     // lies in them to the list. Where the goal comes so near to a border that the
-    // sums in floats may err (a flat row in a thousand or two), or the list does not hold it,
+    // sums in floats may err (a flat row in thousands), or the list does not hold it,
     // once more with every weight formed by weight().
     for (bool precise = !(s.low == s.low);; precise = true) {
         const float z_hi = bin0 > 0 ? __fsub_rn(s.top, (float)bin0 / to_bin) : INFINITY;
@@ -1150,7 +1150,8 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
             if (z >= z_lo && z < from) append(sh, place_of(key_of<BF16>(z), i));
         };
         if (!precise) {
-            WeightSum sum, upper;
+            WeightSum upper, lower;
+            const f32x2 minus = pack2(-1.0f, -1.0f);
             row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
                 const int i0 = row.index(v);
 #pragma unroll
@@ -1158,20 +1159,21 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
                     const float z0 = piece_elem<BF16>(x, e), z1 = piece_elem<BF16>(x, e + 1);
                     f32x2 a, rest;
                     WeightSum::pair(z0 >= s.low ? z0 : s.low, z1 >= s.low ? z1 : s.low, s, copy, a, rest);
-                    sum.add(a, rest, e == 0);
                     float a0, a1, r0, r1;
                     unpack2(a, a0, a1);
                     unpack2(rest, r0, r1);
                     const bool up0 = z0 >= from, up1 = z1 >= from;
-                    upper.add(pack2(up0 ? a0 : 0.0f, up1 ? a1 : 0.0f), pack2(up0 ? r0 : 0.0f, up1 ? r1 : 0.0f), e == 0);
+                    const f32x2 a_up = pack2(up0 ? a0 : 0.0f, up1 ? a1 : 0.0f), rest_up = pack2(up0 ? r0 : 0.0f, up1 ? r1 : 0.0f);
+                    upper.add(a_up, rest_up, e == 0);
+                    lower.add(fma2(a_up, minus, a), fma2(rest_up, minus, rest), e == 0);
                     to_list(z0, i0 + e);
                     to_list(z1, i0 + e + 1);
                 }
-                sum.end_piece();
                 upper.end_piece();
+                lower.end_piece();
             });
-            all = sum.total(s.unit);
             above = upper.total(s.unit);
+            all = above + lower.total(s.unit);
         } else {
             row.each_piece(CL_LOWEST, [&](const uint4& x, int v) {
                 const int i0 = row.index(v);
@@ -1203,10 +1205,9 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
             mass_above = warp_sum(mass_above);
             if (n <= CL_LIST) {
                 sort_list(sh, n, lo, min(highest, over - 1));
-                // (of the weights' own errors those above count 1 - p, the others p)
-                const float fa = (float)all, fm = (float)mass_above;
-                const u64 unsure = precise ? 0 : (u64)(CL_PAIR_ERROR * (top_p * (fa - fm) + (1.0f - top_p) * fm) +
-                                                       sum_error(top_p * fa + fm, sh.V, s.unit));
+                // (p of all less what is above: errors above count 1 - p, the others' p)
+                const float off = top_p * (float)(all - mass_above) + (1.0f - top_p) * (float)mass_above;
+                const u64 unsure = precise ? 0 : (u64)(CL_PAIR_ERROR * off + sum_error(off, sh.V, s.unit));
                 place = reach_in_list(row, n, any_above, mass_above, goal - min(goal, unsure), goal + unsure);
                 // what of the list is kept joins its warps' sums
                 if (place) {

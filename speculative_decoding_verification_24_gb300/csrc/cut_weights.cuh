@@ -185,10 +185,10 @@ struct WeightSum {
     }
 };
 
-// What two sums in units of 2^-unit, or one sum and a part of it, and their
-// difference may be off by together, beside CL_PAIR_ERROR of each weight: `sum` is
-// both added up. (Behind it: a unit and a half for each of 8 CTAs' threads, half a one
-// for each of a list's entries or a part's elements.)
+// What a sum of sums in units of 2^-unit may be off by, beside CL_PAIR_ERROR of each
+// weight: `sum` is them added up, each times what it counts. (Behind it: a unit and a
+// half for each of 8 CTAs' threads and two sums, half a one for each of a list's
+// entries or a part's elements.)
 __device__ __forceinline__ float sum_error(float sum, int V, int unit) {
     const float one = __uint_as_float((uint32_t)(127 + unit) << 23);
     return sum * CL_ADD_ERROR + (float)V * 0x1p-45f * (one + sum * (1.0f / 512.0f)) + 32768.0f;
