@@ -1319,8 +1319,11 @@ __device__ __noinline__ u64 cut_near_top(const Row<BF16> row, float top_p, int g
 }
 
 // The n-th sequence when those whose rows may need all their weights summed come
-// first: top-p without a short top-k.
+// first: top-p without a short top-k, or a draw from a row that no top-k cuts short.
+// (256 rows of 151936 bf16, drawn with no cut or top-k 50 by sequence: 70 us with top-p's
+// alone first, 62 so; 700 of 128256 fp32: 159, 120.)
 constexpr int CL_ORDERED = 4 * CL_THREADS;  // sequences at most
+template <bool DRAW>
 __device__ __forceinline__ int longest_first(const CutParams& P, CutShared& sh, int n, int lane, int warp) {
     constexpr int PER = CL_ORDERED / CL_THREADS;
     const int first = PER * threadIdx.x;
@@ -1331,7 +1334,7 @@ __device__ __forceinline__ int longest_first(const CutParams& P, CutShared& sh, 
         if (i >= P.B) continue;
         const float T = P.temperatures ? P.temperatures[i] : P.temperature, p = P.top_ps ? P.top_ps[i] : P.top_p;
         const int k = P.top_ks ? P.top_ks[i] : P.top_k;
-        if (T != 0.0f && p < 1.0f && (k <= 0 || k >= P.V || k > CL_LIST)) slow |= 1u << q;
+        if (T != 0.0f && (DRAW || p < 1.0f) && (k <= 0 || k >= P.V || k > CL_LIST)) slow |= 1u << q;
     }
     const uint32_t mine = __popc(slow);
     int before = (int)(block_scan(mine, sh.warp_count, lane, warp, all) - mine);
@@ -1367,7 +1370,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
     // first, lest one begins when the others are done.
     int b = blockIdx.x / CS / P.R;
     const int r = blockIdx.x / CS - b * P.R;
-    if (P.longest_first) b = longest_first(P, sh, b, lane, warp);
+    if (P.longest_first) b = longest_first<DRAW>(P, sh, b, lane, warp);
     const int64_t at_row = (int64_t)b * P.R + r;
     const char* src = P.logits + b * P.seq_bytes + r * P.row_bytes;
     const int lead = (int)(reinterpret_cast<uintptr_t>(src) & 15) / R::ES;  // elements before the row in its first piece
