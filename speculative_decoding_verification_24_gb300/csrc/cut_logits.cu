@@ -98,7 +98,6 @@ struct alignas(16) CutShared {
     u64 part_all[CL_MAX_CS * CL_WARPS];
     float group_max[CL_GROUPS];  // of lanes, whose pieces' maxima they are
     float lane_min[CL_MAX_CS * CL_WARPS];
-    u64 cta_mass[CL_MAX_CS];
     u64 warp_mass[CL_WARPS];
     uint32_t warp_count[CL_WARPS];
     float warp_value[CL_WARPS];
