@@ -163,7 +163,7 @@ def step_tree(model, text, lens, K=4):
 def step_sample(model, drafter, text, lens, uniforms, seed, K=4, **settings):
     """K tokens drawn from the drafter, one after another, and verified. uniforms
     [K, B] draw the drafts, seed the verify step's. settings: temperature, top_k,
-    top_p, min_p. The drafter's cache takes the last draft too, so that whatever is
+    top_p, min_p, each a number or one per sequence ([B]). The drafter's cache takes the last draft too, so that whatever is
     kept is in it."""
     B, dev = model.B, model.device
     one = torch.arange(B + 1, dtype=torch.int32, device=dev)
@@ -179,7 +179,10 @@ def step_sample(model, drafter, text, lens, uniforms, seed, K=4, **settings):
     hidden = model.forward(torch.cat([last_tokens(text, lens), drafts], dim=1).view(-1), one * (K + 1))
     target = spec_lmhead_logits(hidden, model.head).view(B, K + 1, -1)
     spec_truncate_logits(target, **settings, out=target)
-    out, n = spec_verify(target, torch.stack(rows, dim=1), drafts, settings.get("temperature", 1.0) or 1.0, "sample", seed)
+    temperature = settings.get("temperature", 1.0)
+    if not torch.is_tensor(temperature):
+        temperature = temperature or 1.0  # (a row cut at 0 has one token, likely at any temperature)
+    out, n = spec_verify(target, torch.stack(rows, dim=1), drafts, temperature, "sample", seed)
     model.commit(text, lens, out, n)
     drafter.ctx = torch.minimum(before + 1 + n, lens - 1)
     return n, target

@@ -99,8 +99,8 @@ typedef enum {
                                       that access instead                          */
     SV_FLAG_BAD_PAGE = 512u,       /* a page table entry outside [0, n_pages) where
                                       a token's page was needed                    */
-    SV_FLAG_BAD_SETTING = 1024u,   /* a row's temperature, top_k, top_p or min_p is
-                                      out of range                                 */
+    SV_FLAG_BAD_SETTING = 1024u,   /* a row's or sequence's temperature, or a row's
+                                      top_k, top_p or min_p is out of range        */
     SV_FLAG_NO_PAGES = 2048u       /* too few free pages for every sequence's tokens */
 } sv_device_flag;
 
@@ -183,6 +183,14 @@ typedef struct {
                                     a batch of at least 19 sequences when such a
                                     plan fills about two CTAs per SM and
                                     cluster_size is 0                              */
+    const float* temperatures;   /* [B] float (device) or NULL: each sample
+                                    sequence's own T, in the place of temperature,
+                                    which is then not looked at: as temperature,
+                                    else the sequence is invalid
+                                    (SV_FLAG_BAD_SETTING); 0 verifies it greedily,
+                                    which is what T towards 0 comes to. Such a call
+                                    takes one cluster per sequence
+                                    (seqs_per_cluster above 1: SV_ERR_CONFIG)      */
 } sv_verify_args;
 
 /* sv_verify_args.flags: the inputs of this call are not written by the work
@@ -649,7 +657,8 @@ typedef struct {
 sv_status spec_sample(const sv_logits_cut* cut, const float* uniforms, int32_t* out_tokens, float* out_logprobs);
 
 /* Writes the rows with -inf in the place of what is cut; what is kept is copied
- * (the temperature is not applied to it).
+ * (the temperature is not applied to it: sv_verify_args.temperature and
+ * temperatures are).
  *   out [B, R, V] of the logits' dtype (device), strides in elements >= 0; may be
  *     the logits (same address and strides), else must not overlap them.
  *   out_n_kept [B, R] int32 (device) or NULL: how many are kept, -inf logits

@@ -87,6 +87,7 @@ class sv_verify_args(ctypes.Structure):
         ("draft_lens", ctypes.c_void_p),
         ("out_draw_edges", ctypes.c_void_p),
         ("seqs_per_cluster", ctypes.c_int),
+        ("temperatures", ctypes.c_void_p),
     ]
 
 
@@ -371,7 +372,12 @@ def _empty(shape, dtype, device, stream, zero=False):
 
 def spec_verify(target_logits, draft_logits, draft_tokens, temperature=1.0, mode="sample", seed=0,
                 out_tokens=None, out_n_accepted=None, stream=None):
-    """Verify a batch: returns (out_tokens [B, K+1] int32, out_n_accepted [B] int32)."""
+    """Verify a batch: returns (out_tokens [B, K+1] int32, out_n_accepted [B]
+    int32). temperature: a number, or one per sequence ([B] float32)."""
+    if isinstance(temperature, torch.Tensor):
+        out = spec_verify_ex(target_logits, draft_logits, draft_tokens, temperature, mode, seed, out_tokens=out_tokens,
+                             out_n_accepted=out_n_accepted, stream=stream)
+        return out["tokens"], out["n_accepted"]
     B, K1, V = target_logits.shape
     K = K1 - 1
     dev = target_logits.device
@@ -396,6 +402,8 @@ def spec_verify_ex(target_logits, draft_logits, draft_tokens, temperature=1.0, m
                    out_draw_edges=None, lib=None, seqs_per_cluster=0, plan_only=False):
     """Verify with per-sequence modes ([B] int32 tensor, or 'greedy'/'sample'
     for all), explicit Philox sequence ids and optional debug outputs.
+    temperature: a number, or one per sequence ([B] float32, 0 for a sequence
+    that is verified greedily).
     debug=True allocates out_p_target, out_p_draft, out_residual_mass,
     out_draw_edges and status_word. overlap_previous=True sets SV_ARG_OVERLAP_PREVIOUS (the
     inputs are not written by the work just before this call on the stream).
@@ -432,7 +440,16 @@ def spec_verify_ex(target_logits, draft_logits, draft_tokens, temperature=1.0, m
     a.draft_tokens = _ptr(draft_tokens)
     a.B, a.K, a.V = B, K, V
     a.dtype = _dtype_code(target_logits)
-    a.temperature = float(temperature)
+    if isinstance(temperature, torch.Tensor):
+        if temperature.dtype is not torch.float32:
+            raise TypeError(f"temperature must be float32, got {temperature.dtype}")
+        if temperature.shape != (B,):
+            raise ValueError(f"temperature must be a number or [{B}], one per sequence, got {list(temperature.shape)}")
+        if temperature.device != dev:
+            raise ValueError("temperature must live on the logits' CUDA device")
+        a.temperatures = _ptr(temperature)
+    else:
+        a.temperature = float(temperature)
     if isinstance(modes, torch.Tensor):
         a.mode = SV_SAMPLE
         a.modes = _ptr(modes)

@@ -85,7 +85,7 @@ static sv_status verify_impl(const sv_verify_args* a, sv_dtype dtype_t, sv_dtype
     if (!a->modes && a->mode == SV_SAMPLE && !a->draft_logits) return SV_ERR_NULL;
     const bool may_sample = a->modes != nullptr || a->mode == SV_SAMPLE;
     double c = 1.0;
-    if (may_sample) {
+    if (may_sample && !a->temperatures) {
         const double T = (double)a->temperature;
         if (!std::isfinite(T) || !(T > 0.0)) return SV_ERR_TEMPERATURE;
         c = 1.4426950408889634 / T;  // log2(e) / T
@@ -95,7 +95,7 @@ static sv_status verify_impl(const sv_verify_args* a, sv_dtype dtype_t, sv_dtype
     if (!aligned(a->target_logits, es_t) || (a->draft_logits && !aligned(a->draft_logits, es_d)) ||
         !aligned(a->draft_tokens, 4) || !aligned(a->out_tokens, 4) || !aligned(a->out_n_accepted, 4) ||
         (a->modes && !aligned(a->modes, 4)) || (a->seq_ids && !aligned(a->seq_ids, 8)) ||
-        (a->draft_lens && !aligned(a->draft_lens, 4)) ||
+        (a->draft_lens && !aligned(a->draft_lens, 4)) || (a->temperatures && !aligned(a->temperatures, 4)) ||
         (a->out_p_target && !aligned(a->out_p_target, 4)) ||
         (a->out_p_draft && !aligned(a->out_p_draft, 4)) ||
         (a->out_residual_mass && !aligned(a->out_residual_mass, 4)) ||
@@ -130,8 +130,9 @@ static sv_status verify_impl(const sv_verify_args* a, sv_dtype dtype_t, sv_dtype
     cs = usable;
 
     // Several sequences per cluster (plain calls): asked for, or automatic
-    // when it spreads a large batch evenly over the SMs.
-    const bool plain = !target_parts && !(a->flags & SV_ARG_OVERLAP_PREVIOUS);
+    // when it spreads a large batch evenly over the SMs. (A cluster's sequences
+    // share one temperature.)
+    const bool plain = !target_parts && !(a->flags & SV_ARG_OVERLAP_PREVIOUS) && !(may_sample && a->temperatures);
     if (a->seqs_per_cluster < 0 || a->seqs_per_cluster > 8 || (a->seqs_per_cluster > 1 && !plain))
         return SV_ERR_CONFIG;
     int n_cl = 0, gcs = 0;
@@ -166,6 +167,7 @@ static sv_status verify_impl(const sv_verify_args* a, sv_dtype dtype_t, sv_dtype
     p.V = a->V;
     p.mode = (int)a->mode;
     p.c = (float)c;
+    p.temperatures = may_sample ? a->temperatures : nullptr;
     p.seed = a->seed;
     p.out_tokens = a->out_tokens;
     p.out_n_accepted = a->out_n_accepted;

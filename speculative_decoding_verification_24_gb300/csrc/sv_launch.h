@@ -18,6 +18,7 @@ struct VerifyParams {
     int B, K, V;
     int mode;                  // used when modes == nullptr
     float c;                   // log2(e) / temperature
+    const float* temperatures; // [B] or nullptr: each sample sequence's own
     uint64_t seed;
     int32_t* out_tokens;       // [B, K+1]
     int32_t* out_n_accepted;   // [B]

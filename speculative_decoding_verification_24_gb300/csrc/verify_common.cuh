@@ -53,6 +53,7 @@ static __device__ __noinline__ bool dbg_load_ok(const VerifyParams& p, const voi
                     dbg_within(a, bytes, p.draft, B * (K1 - 1) * V * (size_t)p.es_d) ||
                     dbg_within(a, bytes, p.tokens, B * K1 * 4) ||  // [B, K]; [B, K+1] for trees
                     dbg_within(a, bytes, p.modes, B * 4) || dbg_within(a, bytes, p.draft_lens, B * 4) ||
+                    dbg_within(a, bytes, p.temperatures, B * 4) ||
                     dbg_within(a, bytes, p.seq_ids, B * 8) || dbg_within(a, bytes, p.tree_parents, B * K1 * 4) ||
                     dbg_within(a, bytes, p.target_parts, (size_t)p.part_tiles * (size_t)p.part_M * 8) ||
                     dbg_within(a, bytes, p.draft_parts, (size_t)p.part_tiles * B * (K1 - 1) * 8);

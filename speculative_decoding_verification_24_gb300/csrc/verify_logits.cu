@@ -69,6 +69,7 @@ struct SeqShared {
     int cstar;
     int total_chunks;
     int seq_b;                          // the sequence this cluster verifies
+    float own_c;                        // its log2(e) / T; 0: T is 0, negative: T cannot be used
     uint64_t never;                     // a barrier nothing completes (failure-path tests)
     // the final search in the CTA holding the draw
     int found, step_lp[P2_SLOTS / 32], step_hit[P2_SLOTS / 32];
@@ -365,12 +366,12 @@ __global__ void __launch_bounds__(NTHREADS, 2) verify_logits_kernel(VerifyParams
     // start while the work ahead of it on the stream is finishing. A plain
     // call (no overlap flag, not the LM-head path) reads no input before that
     // work has completed: it waits here when its prologue reads inputs
-    // (per-sequence modes or draft counts), otherwise just before its first
+    // (per-sequence modes, draft counts or temperatures), otherwise just before its first
     // input read, once the input-free prologue has run. (Without the launch
     // attribute the wait returns at once.)
     const bool fused = p.target_parts != nullptr;
     const bool plain = !p.overlap_previous && !fused;
-    const bool prologue_reads = p.modes != nullptr || p.draft_lens != nullptr;
+    const bool prologue_reads = p.modes != nullptr || p.draft_lens != nullptr || p.temperatures != nullptr;
     if (plain && prologue_reads) grid_dependency_wait();
     // Cluster c verifies sequence c, or, with per-sequence modes, the c-th of
     // the order (sample sequences, then the others, each in index order): the
@@ -404,7 +405,16 @@ __global__ void __launch_bounds__(NTHREADS, 2) verify_logits_kernel(VerifyParams
                 left -= cnt;
             }
         }
-        if (lane == 0) sh.seq_b = seq;
+        if (lane == 0) {
+            sh.seq_b = seq;
+            if constexpr (CAN_SAMPLE && CAN_GREEDY) {
+                // (one thread's division in doubles, as the host forms the call's c)
+                if (p.temperatures) {
+                    const float T = ld_in(p, p.temperatures + seq, -1.0f);
+                    sh.own_c = T > 0.0f && T < INFINITY ? (float)(1.4426950408889634 / (double)T) : T == 0.0f ? 0.0f : -1.0f;
+                }
+            }
+        }
     }
     __syncthreads();
     const int b = sh.seq_b;
@@ -415,16 +425,24 @@ __global__ void __launch_bounds__(NTHREADS, 2) verify_logits_kernel(VerifyParams
     // With overlap, the whole call may run alongside the work ahead of it,
     // and each thread that stores to global memory first waits for that work
     // to complete, just before its stores.
-    const int mode = p.modes ? ld_in(p, p.modes + b, -1) : p.mode;
+    int mode = p.modes ? ld_in(p, p.modes + b, -1) : p.mode;
+    float c = p.c;
+    bool setting_ok = true;
+    if constexpr (CAN_SAMPLE && CAN_GREEDY) {
+        if (p.temperatures && mode == 1) {
+            c = sh.own_c;
+            setting_ok = c >= 0.0f && c < INFINITY;
+            if (c == 0.0f) mode = 0;
+        }
+    }
     // Kb: the drafts this sequence verifies (continuous batching), 0..K
     const int Kb = p.draft_lens ? ld_in(p, p.draft_lens + b, -1) : K;
     const bool len_ok = Kb >= 0 && Kb <= K;
-    const bool mode_ok = (mode == 0 || mode == 1) && !(mode == 1 && drf == nullptr) && len_ok;
+    const bool mode_ok = (mode == 0 || mode == 1) && !(mode == 1 && drf == nullptr) && len_ok && setting_ok;
     const bool sample = CAN_SAMPLE && (!CAN_GREEDY || mode == 1) && mode_ok;
     // which partials this launch merges (a constant unless the set is mixed)
     const bool use_soft = !CAN_GREEDY || (CAN_SAMPLE && sample);
     const int nrows = mode_ok ? (sample ? 2 * Kb + 1 : Kb + 1) : 0;
-    const float c = p.c;
 
     if (tid == 0) {
         for (int s = 0; s < NSTAGE; ++s) mbar_init(&sh.full[s], 1);
@@ -694,6 +712,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) verify_logits_kernel(VerifyParams
                 st_out(p, p.out_draw_edges + (2 * (size_t)b + lane), __int_as_float(0x7fc00000));
             if (lane == 0 && p.status_word && invalid)
                 atomicOr(p.status_word, !len_ok        ? (unsigned)SV_FLAG_BAD_LENGTH
+                                        : !setting_ok  ? (unsigned)SV_FLAG_BAD_SETTING
                                         : !mode_ok     ? (unsigned)SV_FLAG_BAD_MODE
                                         : any_bad_token ? (unsigned)SV_FLAG_BAD_TOKEN
                                                         : (unsigned)SV_FLAG_BAD_ROW);
@@ -1198,11 +1217,12 @@ static cudaError_t launch_ms(const VerifyParams& p, int cs, cudaStream_t stream)
 }
 
 // The mode set a launch needs: trees and all-greedy batches run the greedy
-// kernel, all-sample batches the sample kernel, per-sequence modes both.
+// kernel, all-sample batches the sample kernel, per-sequence modes or
+// temperatures (of which 0 is greedy) both.
 template <typename TT, typename TD>
 static cudaError_t launch_typed(const VerifyParams& p, int cs, cudaStream_t stream) {
     if (p.tree_parents || (!p.modes && p.mode == SV_GREEDY)) return launch_ms<TT, TD, MS_GREEDY>(p, cs, stream);
-    if (!p.modes && p.mode == SV_SAMPLE) return launch_ms<TT, TD, MS_SAMPLE>(p, cs, stream);
+    if (!p.modes && !p.temperatures && p.mode == SV_SAMPLE) return launch_ms<TT, TD, MS_SAMPLE>(p, cs, stream);
     return launch_ms<TT, TD, MS_MIXED>(p, cs, stream);
 }
 
