@@ -712,8 +712,8 @@ __device__ __forceinline__ u64 goal_of(float p, u64 total) {
 
 // One round of the exact search in [lo, hi]: the bin in which the count `k`
 // (BY_MASS false) or the weight `goal` is reached from above, given what lies
-// above hi. The range becomes that bin. A goal of GOAL_OF_ALL becomes p of all weights
-// in the range: a share of the same whole numbers that are searched.
+// above hi. The range becomes that bin. The first round's GOAL_OF_ALL becomes p of all
+// weights in the range: a share of the same whole numbers that are searched.
 constexpr u64 GOAL_OF_ALL = ~0ull;
 template <bool BF16, bool BY_MASS>
 __device__ __forceinline__ uint32_t narrow(const Row<BF16>& row, u64& lo, u64& hi, uint32_t& above, u64& mass_above, uint32_t k, u64& goal,
@@ -864,14 +864,14 @@ __device__ __forceinline__ float nth_group(CutShared& sh, int groups, int n) {
     return sh.bound;
 }
 
-// 4. The place of the last element that a cut keeps, exactly, in [lo, hi]: the
-// range narrows until what is left fits the list, where it is picked. (goal, p: as
-// above)
+// 4. The place of the last element that a cut keeps, exactly, in [lo, hi], the k-th or
+// (BY_MASS) the one with which p of all weights there is reached: the range narrows
+// until what is left fits the list, where it is picked.
 template <bool BF16, bool BY_MASS>
-__device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32_t k, u64 goal, float p) {
+__device__ __noinline__ u64 find_cut(const Row<BF16> row, u64 lo, u64 hi, uint32_t k, float p) {
     CutShared& sh = *row.sh;
     uint32_t above = 0, left = CL_LIST + 1;
-    u64 mass_above = 0;
+    u64 mass_above = 0, goal = GOAL_OF_ALL;
     for (int round = 0; round < CL_ROUNDS && left > CL_LIST; ++round) left = narrow<BF16, BY_MASS>(row, lo, hi, above, mass_above, k, goal, p);
     const int n = (int)min(gather(row, lo, hi), (uint32_t)CL_LIST);
     if (row.rank() == 0) {
@@ -1129,11 +1129,10 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
     const int bin0 = (int)sh.found_from, bin1 = (int)sh.found_to;
     u64 place = 0;
     bool any_above = false;
-    u64 goal;
     // The sum of all weights and of those above the first of these bins, and what
     // lies in them to the list. Where the goal comes so near to a border that the
-    // sums in floats may err (a flat row in thousands), or the list does not hold it,
-    // once more with every weight formed by weight().
+    // sums in floats may err (a flat row in thousands), or is not in the list, once more
+    // with every weight formed by weight().
     for (bool precise = !(s.low == s.low);; precise = true) {
         const float z_hi = bin0 > 0 ? __fsub_rn(s.top, (float)bin0 / to_bin) : INFINITY;
         const float z_lo = key_value<BF16>(key_of<BF16>(__fsub_rn(s.top, (float)(bin1 + 1) / to_bin)));
@@ -1197,7 +1196,7 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         all = 0;
         for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) all += head->part_all[w];
         all = warp_sum(all);
-        goal = goal_of(top_p, all);
+        const u64 goal = goal_of(top_p, all);
         if (row.rank() == 0) {
             u64 mass_above = 0, place = 0;
             for (int w = row.lane; w < row.CS() * CL_WARPS; w += 32) mass_above += sh.part_mass[w];
@@ -1225,11 +1224,11 @@ __device__ __noinline__ u64 cut_by_mass(const Row<BF16> row, float top_p, float 
         row.sync();
         place = sh.found_place;
         row.sync();
-        if (place || precise) break;
+        if (place || precise || n > CL_LIST) break;
     }
     if (place == 0) {
         // more equal logits than the list takes, or a border that the histogram missed
-        place = find_cut<BF16, true>(row, CL_LOWEST, highest, 0, goal, top_p);
+        place = find_cut<BF16, true>(row, CL_LOWEST, highest, 0, top_p);
         sum_above(row, place);
     }
     return place;
@@ -1558,7 +1557,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
             uint32_t n = gather(row, bound, highest);
             bool listed = n <= CL_LIST;
             if (!listed) {
-                const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0, 0.0f);
+                const u64 cut_k = find_cut<BF16, false>(row, bound, highest, (uint32_t)k, 0.0f);
                 if (k <= CL_LIST) {
                     n = gather(row, cut_k, highest);
                     listed = true;
@@ -1567,7 +1566,7 @@ __global__ void __launch_bounds__(CL_THREADS, 2) cut_logits_kernel(const __grid_
                         // (the sum in floats gives the unit alone)
                         refine_unit(row, sum_above(row, cut_k));
                         row.sync();
-                        cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, GOAL_OF_ALL, top_p));
+                        cut = max(cut, find_cut<BF16, true>(row, cut_k, highest, 0, top_p));
                     }
                     cut = max(cut, cut_k);
                 }
