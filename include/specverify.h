@@ -501,10 +501,12 @@ typedef struct {
     float score_cap;             /* 0: none; else 2^-10..4096: scores become cap *
                                     tanh(scale q . k / cap); scale / cap from
                                     2^-60 to 2^60                                 */
-    const float* bias_slopes;    /* [Hq] float (device), finite, or NULL: slope_h *
-                                    (the key's position - the token's) is added to
-                                    the score, after the cap. A slot's position is
-                                    its number, a tree node's ctx + its depth     */
+    const float* bias_slopes;    /* [Hq] float (device), or NULL: slope_h * (the
+                                    key's position - the token's) is added to the
+                                    score, after the cap; it and its product with the
+                                    longest distance are to stay below 2^127. A
+                                    slot's position is its number, a tree node's ctx
+                                    + its depth                                   */
 } sv_paged_attention_args;
 
 /* Bytes of workspace of a call with T packed rows: SV_PAGED_WORKSPACE_HEAD
@@ -585,7 +587,8 @@ typedef struct {
  * Where too few are left, the first sequence that asks for more than there are
  * and all later ones that ask get none (SV_FLAG_NO_PAGES): they keep what they
  * have, held says so, and their tokens beyond it have slot -1.
- * What lies in the stack from n_free on has no meaning.
+ * What lies in the stack from n_free on has no meaning. A page has one owner: one that
+ * several tables name comes back as often as it is given back.
  *   SV_FLAG_BAD_LENGTH: a sequence with a negative context, more tokens than its
  *     table has room for or a held outside [0, max_pages] is left out (it keeps
  *     its pages; its rows' slots and positions are -1). Where cu_new does not
@@ -622,8 +625,9 @@ size_t sv_paged_attention_args_size(void);
  *   min_p  keeps those with w_j >= min_p, that is at least min_p times as likely
  *          as the first (0: all).
  * A row keeps what all three keep, always its first. T = 0 keeps the first
- * alone. Sums of w are held to about 1e-11 of themselves (integers of 64 bits, and
- * pairs of floats); results do not depend on timing.
+ * alone. What top_p keeps is decided by sums of w that are right to 1e-11 of
+ * themselves, whatever the row: one whose top_p lies closer to a border than that may
+ * keep a token more or less. Results do not depend on timing.
  *
  * Rows with a NaN, with +inf or without a finite logit (SV_FLAG_BAD_ROW) and
  * rows with a setting that is out of range (SV_FLAG_BAD_SETTING) give token -1
@@ -648,12 +652,12 @@ typedef struct {
 
 /* Draws one token per row: the smallest index whose cumulative w over what is
  * kept, in the order of indices, exceeds u times their sum.
- *   uniforms [B, R] float (device): the u, in [0, 1); others are taken as the
- *     nearest one, NaN as 0.
+ *   uniforms [B, R] float (device): the u, in [0, 1); below 0 and NaN count as 0, 1
+ *     and above as next to 1: the last token with a weight that counts.
  *   out_tokens [B, R] int32 (device).
  *   out_logprobs [B, R] float (device) or NULL: natural log of the token's
  *     probability among what is kept.
- * An u within about 1e-11 of the edge between two tokens may give the other. */
+ * A u within 1e-11 of the edge between two tokens may give the other. */
 sv_status spec_sample(const sv_logits_cut* cut, const float* uniforms, int32_t* out_tokens, float* out_logprobs);
 
 /* Writes the rows with -inf in the place of what is cut; what is kept is copied

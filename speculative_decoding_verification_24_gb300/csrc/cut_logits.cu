@@ -8,13 +8,15 @@
 // row's top. Places are unique, so ties need no care of their own.
 //
 // Weights w_j = exp((z_j - max) / T) are whole numbers (weight()) wherever a place is
-// decided, in the finest unit that the row's sum leaves room for. Whole numbers add up to the same sum in any order,
-// whatever the order of atomics. Sums over whole rows are formed in floats with
-// their rounding errors kept (WeightSum) and then made whole numbers: right to 1e-11
-// or so, in an order that the row's split over threads alone gives. So a call's
-// results do not depend on timing, and a token is the one that the definition gives
-// unless its u lies within about 1e-11 of an edge between two tokens. In plain fp32
-// a sum of 150,000 weights is off by 1e-6, as much as flat rows' edges lie apart.
+// decided, in the finest unit that the row's sum leaves room for: right to 2^-40 of
+// themselves. Whole numbers add up to the same sum in any order, whatever the order of
+// atomics. Sums over whole rows are first formed in floats with their rounding errors
+// kept (WeightSum), in an order that the row's split over threads alone gives, and
+// decide where what they may be off by leaves no doubt; a row in thousands is summed
+// once more in whole numbers. So a call's results do not depend on timing, and a token
+// is the one that the definition gives unless its u lies within 1e-11 of an edge
+// between two tokens. In plain fp32 a sum of 150,000 weights is off by 1e-6, as much as
+// flat rows' edges lie apart.
 //
 // A row goes to one CTA, or, where rows are few, to a cluster of up to 8. It is
 // read from HBM once, and of every 16 bytes the largest logit's key (16 bits) is
@@ -33,7 +35,7 @@
 //   4. where a list overflows (thousands of equal logits, k in the thousands) the
 //      place is found by exact histograms over shrinking ranges of places;
 //   5. the draw, over the sorted list or over the warps' parts by their sums and
-//      then in one of them; or the row's output: pieces whose key lies below the
+//      then in one of them, once more by exact sums next to an edge; or the row's output: pieces whose key lies below the
 //      cut are written as -inf without another look.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

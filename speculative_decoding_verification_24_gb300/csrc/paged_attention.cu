@@ -1198,7 +1198,7 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 
 // cap tanh(s / cap) + add, of q . k, in the exponent's units. Near 0, |s / cap| <=
 // PA_CAP_NEAR, tanh(x) is x times a polynomial in x^2 (minimax for the relative
-// error, 2^-21.7, fitted to tanh(x) / x on [0, 0.7]): 7 operations of the FMA units,
+// error, 2^-21.6, fitted to tanh(x) / x on [0, 0.7]): 7 operations of the FMA units,
 // which bound it. Else tanh(x) = 1 - 2 / (1 + e^2x), off by 2^-22 or so of 1, at any
 // x: 3 of those and 2 of the units that exponentials take. A warp's tile takes the
 // first if all its scores are near and of tokens: keys behind the last and rows that
