@@ -625,9 +625,8 @@ size_t sv_paged_attention_args_size(void);
  *   min_p  keeps those with w_j >= min_p, that is at least min_p times as likely
  *          as the first (0: all).
  * A row keeps what all three keep, always its first. T = 0 keeps the first
- * alone. What top_p keeps is decided by sums of w that are right to 1e-11 of
- * themselves, whatever the row: one whose top_p lies closer to a border than that may
- * keep a token more or less. Results do not depend on timing.
+ * alone. What top_p keeps is what some top_p within 1e-11 of the given one keeps by
+ * exact sums, whatever the row. Results do not depend on timing.
  *
  * Rows with a NaN, with +inf or without a finite logit (SV_FLAG_BAD_ROW) and
  * rows with a setting that is out of range (SV_FLAG_BAD_SETTING) give token -1
@@ -657,7 +656,7 @@ typedef struct {
  *   out_tokens [B, R] int32 (device).
  *   out_logprobs [B, R] float (device) or NULL: natural log of the token's
  *     probability among what is kept.
- * A u within 1e-11 of the edge between two tokens may give the other. */
+ * The token is that of some u within 1e-11 of the given one, by exact sums. */
 sv_status spec_sample(const sv_logits_cut* cut, const float* uniforms, int32_t* out_tokens, float* out_logprobs);
 
 /* Writes the rows with -inf in the place of what is cut; what is kept is copied

@@ -35,8 +35,9 @@
 //   4. where a list overflows (thousands of equal logits, k in the thousands) the
 //      place is found by exact histograms over shrinking ranges of places;
 //   5. the draw, over the sorted list or over the warps' parts by their sums and
-//      then in one of them, once more by exact sums next to an edge; or the row's output: pieces whose key lies below the
-//      cut are written as -inf without another look.
+//      then in one of them, once more by exact sums next to an edge; or the row's
+//      output: pieces whose key lies below the cut are written as -inf without another
+//      look.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
